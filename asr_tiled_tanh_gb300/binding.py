@@ -25,13 +25,16 @@ RNNT_F32, RNNT_BF16, RNNT_BF16_E4M3 = 0, 1, 2
 DTYPES = {"f32": RNNT_F32, "bf16": RNNT_BF16, "bf16-e4m3": RNNT_BF16_E4M3}
 RNNT_TILED, RNNT_UNTILED = 0, 1
 
-# Every function include/rnnt.h and include/rnnt_profile.h declare (the test
-# hooks of include/rnnt_testing.h are called by their own tests).
+# Every function include/rnnt.h, include/rnnt_ops.h and include/rnnt_profile.h
+# declare (the test hooks of include/rnnt_testing.h are called by their own tests).
 EXPORTS = ("rnnt_saved_bytes", "rnnt_saved_layout", "rnnt_workspace_bytes",
            "rnnt_graph_capturable", "rnnt_tile_cells_for_budget", "rnnt_fwd", "rnnt_bwd",
            "rnnt_bwd_ex", "rnnt_fwd_bwd", "rnnt_fwd_noalloc",
            "rnnt_device_status",
-           "rnnt_status_string", "rnnt_profile_start", "rnnt_profile_stop", "rnnt_profile_entry")
+           "rnnt_status_string", "rnnt_profile_start", "rnnt_profile_stop", "rnnt_profile_entry",
+           "rnnt_ops_status", "rnnt_embed_workspace_bytes", "rnnt_embed_fwd", "rnnt_embed_bwd",
+           "rnnt_norm_saved_bytes", "rnnt_norm_workspace_bytes", "rnnt_norm_fwd",
+           "rnnt_norm_bwd", "rnnt_orth_workspace_bytes", "rnnt_orth")
 
 
 class RnntError(RuntimeError):
@@ -126,6 +129,17 @@ def load(build_if_missing: bool = False):
     lib.rnnt_testing_gemm_timeout.restype = ctypes.c_int
     lib.rnnt_testing_gemm_timeout.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int, P, P, P,
                                               P, ctypes.c_ulonglong, P]
+    # the operators of include/rnnt_ops.h (dims structs by pointer: see ops.py)
+    for name, args in (("rnnt_embed_fwd", [P] * 7), ("rnnt_embed_bwd", [P] * 6 + [S, P, P]),
+                       ("rnnt_norm_fwd", [P] * 8 + [S, P, P]),
+                       ("rnnt_norm_bwd", [P] * 11 + [S, P, P]), ("rnnt_orth", [P] * 4 + [S, P, P]),
+                       ("rnnt_ops_status", [P, P, ctypes.POINTER(ctypes.c_int32)])):
+        getattr(lib, name).restype = ctypes.c_int
+        getattr(lib, name).argtypes = args
+    for name in ("rnnt_embed_workspace_bytes", "rnnt_norm_saved_bytes",
+                 "rnnt_norm_workspace_bytes", "rnnt_orth_workspace_bytes"):
+        getattr(lib, name).restype = S
+        getattr(lib, name).argtypes = [P]
     _lib = lib
     return lib
 

@@ -1,0 +1,44 @@
+// ops.h -- shared pieces of the operators of include/rnnt_ops.h (internal).
+#pragma once
+#include <cstdio>
+#include <cstdlib>
+
+#include "../../include/rnnt_ops.h"
+#include "kernels.h"
+#include "profile.h"
+
+namespace rnnt {
+
+inline bool op_dtype(int d) { return d == RNNT_F32 || d == RNNT_BF16; }
+inline int op_size(int d) { return d == RNNT_F32 ? 4 : 2; }
+inline bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+#define OPS_CHECK(expr)                                                                  \
+  do {                                                                                   \
+    cudaError_t e_ = (expr);                                                             \
+    if (e_ != cudaSuccess) {                                                             \
+      if (getenv("RNNT_VERBOSE"))                                                        \
+        fprintf(stderr, "rnnt: %s -> %s (%s:%d)\n", #expr, cudaGetErrorString(e_),       \
+                __FILE__, __LINE__);                                                     \
+      return RNNT_ERR_CUDA;                                                              \
+    }                                                                                    \
+  } while (0)
+
+// Launch with an optional profiling bracket (see include/rnnt_profile.h).
+#define OPS_LAUNCH(name, expr)          \
+  do {                                  \
+    rnnt::ProfScope ps_(name, st);      \
+    OPS_CHECK(expr);                    \
+  } while (0)
+
+__device__ __forceinline__ void report(int32_t* status, int code) {
+  if (status) atomicOr(status, status_bit(code));
+}
+
+template <typename T> __device__ __forceinline__ T from_f(float x);
+template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+
+}  // namespace rnnt

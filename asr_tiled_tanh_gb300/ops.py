@@ -1,0 +1,227 @@
+"""Python binding of include/rnnt_ops.h: the operators around the loss.
+
+    LabelEmbedding   hL from the labels, and the table's gradient from dhL
+    FrameNorm        hA from the encoder's frames (group norm + activation, channels last,
+                     ragged lengths), and the frames' gradient from dhA
+    Orthogonalizer   the orthogonalised update of a weight matrix (Newton-Schulz products)
+
+Argument checks and marshalling only; each class owns the workspace, saved state and status
+word of one problem size, as ``Rnnt`` does for the loss.  A call works on the current stream
+unless one is given, writes into the tensor it is handed or into a new one, and returns it.
+Calls of one object share its buffers and must not overlap on the GPU: use one object per
+stream.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from .binding import RNNT_BF16, RNNT_F32, RnntError, _check, _stream, load
+
+_DTYPES = {"f32": (RNNT_F32, torch.float32), "bf16": (RNNT_BF16, torch.bfloat16)}
+_ACTS = {"none": 0, "silu": 1, "relu": 2}
+
+
+class RnntEmbedDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("U1", ctypes.c_int), ("V", ctypes.c_int),
+                ("D", ctypes.c_int), ("blank", ctypes.c_int), ("sos", ctypes.c_int),
+                ("table_dtype", ctypes.c_int), ("row_dtype", ctypes.c_int),
+                ("scale", ctypes.c_float), ("ld_table", ctypes.c_longlong),
+                ("ld_rows", ctypes.c_longlong)]
+
+
+class RnntNormDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("C", ctypes.c_int),
+                ("G", ctypes.c_int), ("act", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("eps", ctypes.c_float), ("x_frame", ctypes.c_longlong),
+                ("x_batch", ctypes.c_longlong), ("y_frame", ctypes.c_longlong),
+                ("y_batch", ctypes.c_longlong)]
+
+
+class RnntOrthDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int), ("cols", ctypes.c_int), ("batch", ctypes.c_int),
+                ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("steps", ctypes.c_int),
+                ("eps", ctypes.c_float), ("in_ld", ctypes.c_longlong),
+                ("in_batch", ctypes.c_longlong), ("out_ld", ctypes.c_longlong),
+                ("out_batch", ctypes.c_longlong)]
+
+
+def _dtype(name):
+    try:
+        return _DTYPES[name]
+    except KeyError:
+        raise ValueError(f"dtype {name!r}: one of {sorted(_DTYPES)}") from None
+
+
+def _ptr(t, name, dtype, shape, strides):
+    """Data pointer of a CUDA tensor that has exactly this type and layout."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor of {dtype} {tuple(shape)} is needed, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.stride() != strides:
+        # (the stride of a dimension of length 1 is never used)
+        if any(n > 1 and a != b for n, a, b in zip(shape, t.stride(), strides)):
+            raise ValueError(f"{name}: strides {strides} are needed, got {t.stride()}")
+    return t.data_ptr()
+
+
+class _Op:
+    """Status word and workspace of one problem size."""
+
+    def __init__(self, ws_bytes, what, device):
+        if ws_bytes == 0:
+            raise RnntError(1, what)
+        self.device = device
+        self.ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+        self.ws_bytes = ws_bytes
+        self.status_word = torch.zeros(1, dtype=torch.int32, device=device)
+        self._args = (self.ws.data_ptr(), ws_bytes, self.status_word.data_ptr())
+
+    def status(self, stream=None):
+        """(status code, raw word) of every call so far; synchronizes the stream."""
+        w = ctypes.c_int32(0)
+        code = load().rnnt_ops_status(self.status_word.data_ptr(), _stream(stream),
+                                      ctypes.byref(w))
+        return code, int(w.value)
+
+
+class LabelEmbedding(_Op):
+    """hL[b,u] = scale * E[id(b,u)] for u <= U_len[b], else 0 (id(b,0) = blank with sos).
+
+    B, U1, V, D: samples, label positions, labels, width.  dtype: of the table; out_dtype: of
+    the rows and of their gradient.  ld_table, ld_rows: row strides in elements (0: D).
+    """
+
+    def __init__(self, B, U1, V, D, dtype="bf16", out_dtype="bf16", scale=1.0, sos=True, blank=0,
+                 ld_table=0, ld_rows=0, device="cuda"):
+        tcode, self._tt = _dtype(dtype)
+        rcode, self._rt = _dtype(out_dtype)
+        self.dims = RnntEmbedDims(B, U1, V, D, blank, int(sos), tcode, rcode, scale, ld_table,
+                                  ld_rows)
+        self._d = ctypes.byref(self.dims)
+        lib = load()
+        super().__init__(lib.rnnt_embed_workspace_bytes(self._d), "LabelEmbedding(dims)", device)
+        self._fwd, self._bwd = lib.rnnt_embed_fwd, lib.rnnt_embed_bwd
+        lt, lr = ld_table or D, ld_rows or D
+        self._ids = ((B, U1), (U1, 1))
+        self._len = ((B,), (1,))
+        self._table = ((V, D), (lt, 1))
+        self._rows = ((B, U1, D), (U1 * lr, lr, 1))
+
+    def _in(self, ids, U_len):
+        return (_ptr(ids, "ids", torch.int32, *self._ids),
+                None if U_len is None else _ptr(U_len, "U_len", torch.int32, *self._len))
+
+    def fwd(self, table, ids, U_len=None, out=None, stream=None):
+        """The rows [B,U1,D] of ids [B,U1] int32; U_len [B] int32 or None (every row)."""
+        if out is None:
+            shape, strides = self._rows
+            out = torch.empty_strided(shape, strides, dtype=self._rt, device=self.device)
+        i, u = self._in(ids, U_len)
+        _check(self._fwd(self._d, i, u, _ptr(table, "table", self._tt, *self._table),
+                         _ptr(out, "out", self._rt, *self._rows), self._args[2],
+                         _stream(stream)), "rnnt_embed_fwd")
+        return out
+
+    def bwd(self, dout, ids, U_len=None, dtable=None, stream=None):
+        """The table's gradient [V,D] fp32 from the rows' gradient."""
+        if dtable is None:
+            shape, strides = self._table
+            dtable = torch.empty_strided(shape, strides, dtype=torch.float32, device=self.device)
+        i, u = self._in(ids, U_len)
+        _check(self._bwd(self._d, i, u, _ptr(dout, "dout", self._rt, *self._rows),
+                         _ptr(dtable, "dtable", torch.float32, *self._table), *self._args,
+                         _stream(stream)), "rnnt_embed_bwd")
+        return dtable
+
+
+class FrameNorm(_Op):
+    """y = act(gamma * xh + beta), xh the group norm of x [B,T,C] over the frames t < T_len[b].
+
+    x_strides, y_strides: (batch, frame) strides in elements of x and dx, and of y and dy
+    (None: dense).  fwd keeps the statistics that bwd reads.
+    """
+
+    def __init__(self, B, T, C, G, act="silu", dtype="bf16", eps=1e-5, x_strides=None,
+                 y_strides=None, device="cuda"):
+        code, self._t = _dtype(dtype)
+        if act not in _ACTS:
+            raise ValueError(f"act {act!r}: one of {sorted(_ACTS)}")
+        xs, ys = x_strides or (T * C, C), y_strides or (T * C, C)
+        self.dims = RnntNormDims(B, T, C, G, _ACTS[act], code, eps, xs[1], xs[0], ys[1], ys[0])
+        self._d = ctypes.byref(self.dims)
+        lib = load()
+        super().__init__(lib.rnnt_norm_workspace_bytes(self._d), "FrameNorm(dims)", device)
+        self.saved = torch.empty(lib.rnnt_norm_saved_bytes(self._d), dtype=torch.uint8,
+                                 device=device)
+        self._saved = self.saved.data_ptr()
+        self._fwd, self._bwd = lib.rnnt_norm_fwd, lib.rnnt_norm_bwd
+        self._x = ((B, T, C), (xs[0], xs[1], 1))
+        self._y = ((B, T, C), (ys[0], ys[1], 1))
+        self._c = ((C,), (1,))
+        self._len = ((B,), (1,))
+
+    def _params(self, gamma, beta, T_len):
+        f = torch.float32
+        return (None if gamma is None else _ptr(gamma, "gamma", f, *self._c),
+                None if beta is None else _ptr(beta, "beta", f, *self._c),
+                None if T_len is None else _ptr(T_len, "T_len", torch.int32, *self._len))
+
+    def fwd(self, x, gamma=None, beta=None, T_len=None, y=None, stream=None):
+        """y [B,T,C]; gamma, beta [C] fp32 or None; T_len [B] int32 or None (every frame)."""
+        if y is None:
+            y = torch.empty_strided(*self._y, dtype=self._t, device=self.device)
+        _check(self._fwd(self._d, _ptr(x, "x", self._t, *self._x),
+                         *self._params(gamma, beta, T_len), _ptr(y, "y", self._t, *self._y),
+                         self._saved, *self._args, _stream(stream)), "rnnt_norm_fwd")
+        return y
+
+    def bwd(self, x, dy, gamma=None, beta=None, T_len=None, dx=None, dgamma=None, dbeta=None,
+            stream=None):
+        """(dx, dgamma, dbeta) for the x and T_len of the last fwd."""
+        if dx is None:
+            dx = torch.empty_strided(*self._x, dtype=self._t, device=self.device)
+        if dgamma is None:
+            dgamma = torch.empty(self.dims.C, dtype=torch.float32, device=self.device)
+        if dbeta is None:
+            dbeta = torch.empty(self.dims.C, dtype=torch.float32, device=self.device)
+        _check(self._bwd(self._d, _ptr(x, "x", self._t, *self._x),
+                         _ptr(dy, "dy", self._t, *self._y), *self._params(gamma, beta, T_len),
+                         self._saved, _ptr(dx, "dx", self._t, *self._x),
+                         _ptr(dgamma, "dgamma", torch.float32, *self._c),
+                         _ptr(dbeta, "dbeta", torch.float32, *self._c), *self._args,
+                         _stream(stream)), "rnnt_norm_bwd")
+        return dx, dgamma, dbeta
+
+
+class Orthogonalizer(_Op):
+    """O = the Newton-Schulz iterate of G / |G|_F after `steps` steps (see include/rnnt_ops.h).
+
+    G [batch,rows,cols], or [rows,cols] with batch = 1.  in_strides, out_strides: (batch, row)
+    strides in elements (None: dense).
+    """
+
+    def __init__(self, rows, cols, batch=1, dtype="f32", out_dtype="bf16", steps=5, eps=1e-7,
+                 in_strides=None, out_strides=None, device="cuda"):
+        icode, self._it = _dtype(dtype)
+        ocode, self._ot = _dtype(out_dtype)
+        i, o = in_strides or (rows * cols, cols), out_strides or (rows * cols, cols)
+        self.dims = RnntOrthDims(rows, cols, batch, icode, ocode, steps, eps, i[1], i[0], o[1],
+                                 o[0])
+        self._d = ctypes.byref(self.dims)
+        lib = load()
+        super().__init__(lib.rnnt_orth_workspace_bytes(self._d), "Orthogonalizer(dims)", device)
+        self._run = lib.rnnt_orth
+        self._in = ((batch, rows, cols), (i[0], i[1], 1))
+        self._out = ((batch, rows, cols), (o[0], o[1], 1))
+
+    def run(self, G, out=None, stream=None):
+        flat = G.dim() == 2
+        if out is None:
+            out = torch.empty_strided(*self._out, dtype=self._ot, device=self.device)
+            out = out[0] if flat and self.dims.batch == 1 else out
+        _check(self._run(self._d, _ptr(G[None] if flat else G, "G", self._it, *self._in),
+                         _ptr(out[None] if out.dim() == 2 else out, "out", self._ot, *self._out),
+                         *self._args, _stream(stream)), "rnnt_orth")
+        return out
