@@ -1,5 +1,5 @@
 // k_embed.cu -- the prediction network's label embedding (include/rnnt_ops.h).
-#include <algorithm>
+#include <atomic>
 
 #include "ops.h"
 #include "ptx.cuh"
@@ -39,41 +39,88 @@ __device__ __forceinline__ int label_of(const EmbedArgs& a, int n) {
 
 // ---- rows -------------------------------------------------------------------
 // hL row n = scale * E[label].  Bound by its stores (a row is written once, the
-// table's rows come from L2): a block holds as many rows as fit its threads, a
-// thread owns VEC consecutive columns of K rows, whose loads are in flight
-// together.  VEC = 8 needs 16-byte aligned rows; others take one column.
+// table's rows come from L2).  A lane owns VEC consecutive columns: eight on
+// 16-byte aligned rows, else two or one.
+//
+// A lane's VEC elements as they are loaded (the registers that loads in flight
+// hold), and widened.
+template <int BYTES> struct RawWord;
+template <> struct RawWord<2> { using type = unsigned short; };
+template <> struct RawWord<4> { using type = unsigned int; };
+template <> struct RawWord<8> { using type = uint2; };
+template <> struct RawWord<16> { using type = uint4; };
+
 template <int VEC, typename T>
-__device__ __forceinline__ void load_vec(const T* p, float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    v[0] = to_f<T>(*p);
-  } else if constexpr (sizeof(T) == 4) {
+struct Raw {
+  static constexpr int BYTES = VEC * sizeof(T), WORDS = BYTES > 16 ? BYTES / 16 : 1;
+  using W = typename RawWord<(BYTES > 16 ? 16 : BYTES)>::type;
+  W w[WORDS];
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < VEC; i += 4) {
-      const float4 q = __ldg((const float4*)(p + i));
-      v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+    for (int i = 0; i < WORDS; ++i) w[i] = W{};
+  }
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = __ldg((const W*)p + i);
+  }
+  __device__ __forceinline__ void widen(float (&v)[VEC]) const {
+    if constexpr (sizeof(T) == 4) {
+      const uint32_t* u = (const uint32_t*)w;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = __uint_as_float(u[i]);
+    } else if constexpr (VEC == 1) {
+      v[0] = __uint_as_float((uint32_t)w[0] << 16);
+    } else {
+      const uint32_t* u = (const uint32_t*)w;
+#pragma unroll
+      for (int i = 0; i < VEC / 2; ++i) {
+        v[2 * i] = ptx::bf16lo(u[i]);
+        v[2 * i + 1] = ptx::bf16hi(u[i]);
+      }
     }
-  } else if constexpr (VEC == 4) {
-    const uint2 q = __ldg((const uint2*)p);
-    v[0] = ptx::bf16lo(q.x); v[1] = ptx::bf16hi(q.x);
-    v[2] = ptx::bf16lo(q.y); v[3] = ptx::bf16hi(q.y);
+  }
+};
+
+template <int VEC>
+__device__ __forceinline__ void scale_vec(float (&v)[VEC], float s) {
+  if constexpr (VEC == 1) {
+    v[0] *= s;
   } else {
-    const uint4 q = __ldg((const uint4*)p);
-    v[0] = ptx::bf16lo(q.x); v[1] = ptx::bf16hi(q.x);
-    v[2] = ptx::bf16lo(q.y); v[3] = ptx::bf16hi(q.y);
-    v[4] = ptx::bf16lo(q.z); v[5] = ptx::bf16hi(q.z);
-    v[6] = ptx::bf16lo(q.w); v[7] = ptx::bf16hi(q.w);
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) {
+      const float2 x = __fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(s, s));
+      v[i] = x.x;
+      v[i + 1] = x.y;
+    }
   }
 }
+template <int VEC>
+__device__ __forceinline__ void add_vec(float (&a)[VEC], const float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    a[0] += v[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) {
+      const float2 x = __fadd2_rn(make_float2(a[i], a[i + 1]), make_float2(v[i], v[i + 1]));
+      a[i] = x.x;
+      a[i + 1] = x.y;
+    }
+  }
+}
+
 template <int VEC, typename T>
 __device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
   if constexpr (VEC == 1) {
     *p = from_f<T>(v[0]);
+  } else if constexpr (VEC == 2 && sizeof(T) == 4) {
+    *(float2*)p = make_float2(v[0], v[1]);
+  } else if constexpr (VEC == 2) {
+    *(uint32_t*)p = ptx::pack_bf16x2(v[0], v[1]);
   } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int i = 0; i < VEC; i += 4)
       *(float4*)(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
   } else {
-    static_assert(VEC == 8, "bf16 stores are 16 bytes");
     *(uint4*)p = make_uint4(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]),
                             ptx::pack_bf16x2(v[4], v[5]), ptx::pack_bf16x2(v[6], v[7]));
   }
@@ -81,115 +128,211 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
 
 constexpr int ROWS_THREADS = 256;
 
+// A warp writes K steps of 32 / (1 << lg) rows, 1 << lg lanes to a row.  Each
+// lane looks one row's label up; the rows take theirs by shuffle.
 template <int VEC, int K, typename TE, typename TR>
 __global__ void __launch_bounds__(ROWS_THREADS)
-k_embed_rows(EmbedArgs a, const TE* __restrict__ table, TR* __restrict__ rows) {
-  const int vpr = a.D / VEC;                     // vectors per row
-  const int tpr = min(vpr, ROWS_THREADS);        // threads per row
-  const int rpb = ROWS_THREADS / tpr;            // rows per pass of the block
-  const int r = threadIdx.x / tpr, c0 = threadIdx.x - r * tpr;
-  if (r >= rpb) return;
+k_embed_rows(EmbedArgs a, int lg, const TE* __restrict__ table, TR* __restrict__ rows) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int vpr = a.D / VEC, per = 32 >> lg;
+  const long long n0 = ((long long)blockIdx.x * (ROWS_THREADS / 32) + warp) * (K * per);
   const int N = a.B * a.U1;
-  const long long n0 = (long long)blockIdx.x * rpb * K + r;
+  const int left = (int)max(0LL, min((long long)(K * per), N - n0));
+  const int mine = lane < left ? label_of(a, (int)n0 + lane) : -1;
+  const int sub = lane >> lg, c0 = lane & ((1 << lg) - 1);
   int lab[K];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const long long n = n0 + (long long)k * rpb;
-    lab[k] = n < N ? label_of(a, (int)n) : -1;
-  }
-  for (int c = c0; c < vpr; c += tpr) {
-    float v[K][VEC];
+  for (int k = 0; k < K; ++k) lab[k] = __shfl_sync(0xffffffffu, mine, k * per + sub);
+  TR* out = rows + (n0 + sub) * a.ld_rows;
+  for (int c = c0; c < vpr; c += 1 << lg) {
+    Raw<VEC, TE> raw[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (lab[k] >= 0) {
-        load_vec<VEC, TE>(table + lab[k] * a.ld_table + c * VEC, v[k]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[k][i] = 0.f;
-      }
+      if (lab[k] >= 0) raw[k].load(table + lab[k] * a.ld_table + c * VEC);
+      else raw[k].zero();
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const long long n = n0 + (long long)k * rpb;
-      if (n < N) {
-        if (lab[k] >= 0) {  // (0 exactly where there is no label, whatever the scale)
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) v[k][i] *= a.scale;
-        }
-        store_vec<VEC, TR>(rows + n * a.ld_rows + c * VEC, v[k]);
-      }
+      if (k * per + sub >= left) break;
+      float v[VEC];
+      raw[k].widen(v);
+      scale_vec<VEC>(v, a.scale);
+      store_vec<VEC, TR>(out + (long long)(k * per) * a.ld_rows + c * VEC, v);
     }
   }
 }
 
 template <int VEC, typename TE, typename TR>
 cudaError_t launch_rows_v(const EmbedArgs& a, const TE* table, TR* rows, cudaStream_t st) {
-  const int vpr = a.D / VEC, rpb = ROWS_THREADS / std::min(vpr, ROWS_THREADS);
-  const long long N = (long long)a.B * a.U1;
-  // four rows a thread once every SM has several blocks of them; below, one,
-  // so that a few rows still spread over the SMs
-  if (N >= 32LL * num_sms() * rpb)
-    k_embed_rows<VEC, 4><<<(unsigned)cdiv(N, 4 * rpb), ROWS_THREADS, 0, st>>>(a, table, rows);
+  const int vpr = a.D / VEC;
+  const int lg = vpr > 16 ? 5 : vpr > 8 ? 4 : 3, per = 32 >> lg;
+  const long long N = (long long)a.B * a.U1, warps = ROWS_THREADS / 32;
+  // eight loads in flight per lane once that still gives every SM its warps;
+  // below, one, so that a few rows spread over the SMs
+  if (N >= 64LL * num_sms() * per)
+    k_embed_rows<VEC, 8>
+        <<<(unsigned)cdiv(N, 8 * per * warps), ROWS_THREADS, 0, st>>>(a, lg, table, rows);
   else
-    k_embed_rows<VEC, 1><<<(unsigned)cdiv(N, rpb), ROWS_THREADS, 0, st>>>(a, table, rows);
+    k_embed_rows<VEC, 1>
+        <<<(unsigned)cdiv(N, per * warps), ROWS_THREADS, 0, st>>>(a, lg, table, rows);
   return cudaGetLastError();
+}
+
+// Widest vector (8, 2 or 1 elements) that every row of these tensors allows.
+int vec_of(int D, long long ld_a, const void* pa, int size_a, long long ld_b, const void* pb,
+           int size_b) {
+  for (int v = 8; v > 1; v = v == 8 ? 2 : 1) {
+    const int aa = v * size_a < 16 ? v * size_a : 16, ab = v * size_b < 16 ? v * size_b : 16;
+    if (D % v == 0 && ld_a % v == 0 && ld_b % v == 0 && aligned_to(pa, aa) && aligned_to(pb, ab))
+      return v;
+  }
+  return 1;
 }
 
 template <typename TE, typename TR>
 cudaError_t launch_rows(const EmbedArgs& a, const void* table, void* rows, cudaStream_t st) {
-  const bool v8 = a.D % 8 == 0 && a.ld_table % 8 == 0 && a.ld_rows % 8 == 0 &&
-                  aligned_to(table, 16) && aligned_to(rows, 16);
-  return v8 ? launch_rows_v<8>(a, (const TE*)table, (TR*)rows, st)
-            : launch_rows_v<1>(a, (const TE*)table, (TR*)rows, st);
+  const int v = vec_of(a.D, a.ld_table, table, sizeof(TE), a.ld_rows, rows, sizeof(TR));
+  if (v == 8) return launch_rows_v<8>(a, (const TE*)table, (TR*)rows, st);
+  if (v == 2) return launch_rows_v<2>(a, (const TE*)table, (TR*)rows, st);
+  return launch_rows_v<1>(a, (const TE*)table, (TR*)rows, st);
 }
 
 // ---- the table's gradient -----------------------------------------------------
-// dE[v] = scale * sum of the dhL rows whose label is v.  The rows' labels are
-// sorted (stably: rows of one label keep their order), so that every label is
-// a run of the sorted list, and the list is cut into chunks of equal length:
-// the work does not depend on how the labels repeat.  A run inside one chunk
-// is summed in registers and stored; a run that crosses chunks leaves one
-// partial row in each, and the partial rows form the next level's (much
-// shorter) sorted list.  No atomics on values: the order of every sum follows
-// from the labels alone.  Rows without a label carry the label V and sort last.
+// dE[v] = scale * sum of the dhL rows whose label is v.  The rows are listed
+// by label (stably: rows of one label keep their order), so that every label
+// is a run of the list, and the list is cut into chunks of equal length: the
+// work does not depend on how the labels repeat.  A run inside one chunk is
+// summed in registers and stored; one that crosses chunks leaves a partial row
+// in each, and a second kernel adds those.  No atomics on values: the order of
+// every sum follows from the labels alone.  Rows without a label carry the
+// label V.
 
-// Stable sort of few rows by counting: a warp finds row i's place as the number
-// of rows with a smaller label plus the earlier ones with the same label.  N^2
-// comparisons, but one launch; at 4096 rows as long as the radix passes.
-constexpr int RANK_MAX = 4096;
-constexpr int SORT_THREADS = 1024;
+constexpr int SORT_THREADS = 1024, SORT_WARPS = SORT_THREADS / 32;
+
+// The list of few rows, by label ranges: block c owns labels [c r, (c+1) r) and
+// reads every row's label.  First it counts its own labels per warp segment and
+// the rows of smaller labels, which gives every label's place; then each warp
+// walks its segment in order and lists the rows.  One launch, about 4 us, where
+// the radix sort below takes three (13 us); every block reads all labels, so
+// beyond GROUP_MAX_ROWS the radix sort is the shorter (at 103,424 rows 16 us
+// against 23).
+//
+// Table rows that no label names are cleared here and in the two kernels of
+// the sums, a share each (ClearShare): the stores of a large table take longer
+// than the rest and drain under it.
+constexpr int GROUP_MAX_ROWS = 4096, GROUP_MAX_RANGE = 384;
+
+struct ClearShare {
+  int range;                // labels per group
+  int j0, j1;               // this kernel's share of each group's labels
+  const uint8_t* present;   // [V], NULL: nothing to clear
+};
+
+// Clear the share's rows of group g, one row per warp at a time.
+__device__ __forceinline__ void clear_rows(const ClearShare& s, int g, int V, int D,
+                                           float* dtable, long long ld, int v4) {
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  for (int j = s.j0 + (threadIdx.x >> 5); j < s.j1; j += warps) {
+    const int v = g * s.range + j;
+    if (v >= V || s.present[v]) continue;
+    float* row = dtable + v * ld;
+    if (v4) {
+      for (int d = 4 * lane; d < D; d += 128) *(float4*)(row + d) = make_float4(0, 0, 0, 0);
+    } else {
+      for (int d = lane; d < D; d += 32) row[d] = 0.f;
+    }
+  }
+}
 
 __global__ void __launch_bounds__(SORT_THREADS)
-k_embed_rank(EmbedArgs a, int32_t* __restrict__ skey, int32_t* __restrict__ sidx) {
-  __shared__ __align__(16) int32_t key[RANK_MAX];
-  const int N = a.B * a.U1, N4 = (N + 127) / 128 * 128;
-  for (int n = threadIdx.x; n < N4; n += SORT_THREADS) {
-    const int v = n < N ? label_of(a, n) : a.V;
+k_embed_group(EmbedArgs a, ClearShare cs, int32_t* __restrict__ lkey, int32_t* __restrict__ lidx,
+              int32_t* __restrict__ live, uint8_t* present, float* __restrict__ dtable, int v4) {
+  extern __shared__ __align__(16) int32_t sm[];  // [SORT_WARPS][range] counters, [range] totals
+  __shared__ __align__(16) int32_t key[GROUP_MAX_ROWS];
+  __shared__ int wsum[SORT_WARPS], base_s;
+  const int range = cs.range;
+  int32_t* cnt = sm;
+  int32_t* total = sm + SORT_WARPS * range;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int N = a.B * a.U1, NP = (N + 127) / 128 * 128;
+  const int v0 = blockIdx.x * range, r = min(range, a.V - v0);
+  for (int i = tid; i < SORT_WARPS * range; i += SORT_THREADS) cnt[i] = 0;
+  for (int n = tid; n < NP; n += SORT_THREADS) {
+    const int v = n < N ? label_of(a, n) : -1;
     key[n] = v < 0 ? a.V : v;
   }
   __syncthreads();
   ptx::griddep_launch();
-  const int lane = threadIdx.x & 31;
-  const int i = blockIdx.x * (SORT_THREADS / 32) + (threadIdx.x >> 5);
-  if (i >= N) return;
-  const int k = key[i];
+  const int seg = (int)cdiv(NP / 128, SORT_WARPS) * 128;
+  const int n0 = min(NP, warp * seg), n1 = min(NP, n0 + seg);
+  int32_t* mycnt = cnt + warp * range;
   int below = 0;
-  for (int j = 4 * lane; j < N4; j += 128) {
-    const int4 q = *(const int4*)(key + j);
-    below += q.x < k + (j < i);
-    below += q.y < k + (j + 1 < i);
-    below += q.z < k + (j + 2 < i);
-    below += q.w < k + (j + 3 < i);
+  for (int n = n0 + 4 * lane; n < n1; n += 128) {
+    const int4 q = *(const int4*)(key + n);
+    const int k[4] = {q.x - v0, q.y - v0, q.z - v0, q.w - v0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      below += k[i] < 0;
+      if ((unsigned)k[i] < (unsigned)r) atomicAdd(mycnt + k[i], 1);
+    }
   }
   below = __reduce_add_sync(0xffffffffu, below);
-  if (lane == 0) {
-    skey[below] = k;
-    sidx[below] = i;
+  if (lane == 0) wsum[warp] = below;
+  __syncthreads();
+  // places: of a label among the smaller ones, of a warp's rows in their label
+  if (warp == 0) {
+    const int x = __reduce_add_sync(0xffffffffu, wsum[lane]);
+    if (lane == 0) base_s = x;
+  }
+  for (int j = tid; j < r; j += SORT_THREADS) {
+    int run = 0;
+#pragma unroll 8
+    for (int w = 0; w < SORT_WARPS; ++w) {
+      const int c = cnt[w * range + j];
+      cnt[w * range + j] = run;
+      run += c;
+    }
+    total[j] = run;
+    present[v0 + j] = run != 0;
+  }
+  __syncthreads();
+  clear_rows(cs, blockIdx.x, a.V, a.D, dtable, a.ld_table, v4);
+  if (warp == 0) {
+    int run = base_s;
+    for (int j0 = 0; j0 < r; j0 += 32) {
+      const int v = j0 + lane < r ? total[j0 + lane] : 0;
+      int x = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (j0 + lane < r) total[j0 + lane] = run + x - v;
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0 && v0 + r == a.V) *live = run;
+  }
+  __syncthreads();
+  for (int n = n0; n < n1; n += 32) {
+    const int k = key[n + lane] - v0;
+    const bool in = (unsigned)k < (unsigned)r;
+    if (!__any_sync(0xffffffffu, in)) continue;
+    const unsigned peers = __match_any_sync(0xffffffffu, in ? k : -1);
+    const int rank = __popc(peers & ((1u << lane) - 1));
+    if (in) {
+      const int pos = total[k] + mycnt[k] + rank;
+      lkey[pos] = k + v0;
+      lidx[pos] = n + lane;
+    }
+    __syncwarp();
+    if (in && rank == 0) mycnt[k] += __popc(peers);
+    __syncwarp();
   }
 }
 
-// Radix sort, least significant digit first, for more rows.  Block c owns the
-// c-th range of `per` list entries.  k_embed_hist counts the first digit per
+// The list by a radix sort, least significant digit first, for more rows or
+// labels than that (rows without a label come last).  Block c owns the c-th
+// range of `per` list entries.  k_embed_hist counts the first digit per
 // block; every scatter pass moves its entries and counts the next digit at
 // their destination (integer atomics: the counts do not depend on order).
 struct SortArgs {
@@ -230,7 +373,7 @@ k_embed_hist(EmbedArgs a, SortArgs s, int32_t* __restrict__ key, int32_t* __rest
 }
 
 __global__ void __launch_bounds__(SORT_THREADS) k_embed_scatter(SortArgs s) {
-  constexpr int WARPS = SORT_THREADS / 32;
+  constexpr int WARPS = SORT_WARPS;
   __shared__ uint16_t wcnt[WARPS][MAX_DIGITS];
   __shared__ int base[MAX_DIGITS];
   __shared__ int parts[SORT_THREADS], before[SORT_THREADS];
@@ -313,62 +456,71 @@ __global__ void __launch_bounds__(SORT_THREADS) k_embed_scatter(SortArgs s) {
   }
 }
 
-// One level of the sums.  A block owns WARPS * 32 list entries and 32 * VEC
-// columns; a warp sums 32 entries, eight rows' loads in flight, and its first
-// and last run meet the other warps' in shared memory (slots 2w and 2w + 1).
-// Bound by reading the rows: each is read once, 512 bytes of it per warp.
+// ---- sums -----------------------------------------------------------------
+// A block owns SUM_WARPS * E list entries and 32 * VEC columns; a warp sums E
+// entries, FLY rows' loads in flight, and its first and last run meet the
+// other warps' in shared memory (slots 2w and 2w + 1).  Bound by reading the
+// rows, each once.  E = 32 amortises a warp's start; few rows take E = 8, one
+// round of loads, so that more warps share them.
 struct SumArgs {
   int n, V, D;
+  const int32_t* live;  // list length on the device (NULL: n)
   const int32_t* key;
-  const int32_t* idx;   // row of src, -1: nothing to add (its key still counts)
+  const int32_t* idx;
   long long ld_src;
   float scale;
   float* dtable;
   long long ld_table;
-  int chunks;           // blocks past them store zeros into labels that do not occur
-  int32_t* pkey;        // next level's list (2 per chunk); unused at the last level
-  int32_t* pidx;
-  float* part;
+  int chunks;           // blocks past them clear table rows that no label names
+  ClearShare clear;     // (listed by label ranges; else looked up in the list)
+  int v4;
+  float* part;          // partial rows: chunk c's head at 2c, its tail at 2c + 1
   long long ldp;
 };
 
-// Sum of a run, as it leaves a warp or block: alone (its label is complete), or
-// one piece of a run that continues to the left (head slot) or right only (tail).
-enum { RUN_WHOLE, RUN_HEAD, RUN_TAIL };
-__device__ __forceinline__ int run_kind(bool left, bool right) {
-  return left ? RUN_HEAD : right ? RUN_TAIL : RUN_WHOLE;
-}
+constexpr int SUM_WARPS = 8;
 
-template <int WARPS, int VEC, typename TS>
-__global__ void __launch_bounds__(WARPS * 32)
+template <int E, int VEC, typename TS>
+__global__ void __launch_bounds__(SUM_WARPS * 32, 4)
 k_embed_sum(SumArgs a, const TS* __restrict__ src) {
+  constexpr int WARPS = SUM_WARPS;
+  constexpr int FLY = VEC * sizeof(TS) > 16 ? 4 : 8;  // (four blocks an SM: 64 registers)
   __shared__ float sv[2 * WARPS][32 * VEC];
   __shared__ int skey[2 * WARPS], sused[2 * WARPS];
+  struct alignas(16) Entry { long long off; int key, pad; };
+  __shared__ Entry ent[WARPS][E];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = (blockIdx.y * 32 + lane) * VEC;
   const bool col_ok = col < a.D;
   ptx::griddep_wait();
   ptx::griddep_launch();
+  const int n = a.live ? *a.live : a.n;
   if ((int)blockIdx.x >= a.chunks) {
-    // labels that do not occur: eight a warp, looked up in the sorted list
+    if (blockIdx.y) return;
+    if (a.clear.present) {
+      clear_rows(a.clear, blockIdx.x - a.chunks, a.V, a.D, a.dtable, a.ld_table, a.v4);
+      return;
+    }
+    // eight labels a warp, looked up in the list
     const long long v0 = ((long long)(blockIdx.x - a.chunks) * WARPS + warp) * 8;
     const long long v = v0 + lane;
     bool absent = false;
     if (lane < 8 && v < a.V) {
-      int lo = 0, hi = a.n;  // first entry with a key >= v
+      int lo = 0, hi = n;  // first entry with a key >= v
       while (lo < hi) {
         const int mid = (int)(((long long)lo + hi) >> 1);
         if (a.key[mid] < v) lo = mid + 1;
         else hi = mid;
       }
-      absent = lo == a.n || a.key[lo] != (int)v;
+      absent = lo == n || a.key[lo] != (int)v;
     }
     unsigned m = __ballot_sync(0xffffffffu, absent);
     const float z[VEC] = {};
     while (m) {
       const int r = __ffs(m) - 1;
       m &= m - 1;
-      if (col_ok) store_vec<VEC, float>(a.dtable + (v0 + r) * a.ld_table + col, z);
+      for (int d = lane * VEC; d < a.D; d += 32 * VEC)
+        store_vec<VEC, float>(a.dtable + (v0 + r) * a.ld_table + d, z);
     }
     return;
   }
@@ -376,15 +528,23 @@ k_embed_sum(SumArgs a, const TS* __restrict__ src) {
     if (!col_ok) return;
     float o[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) o[i] = a.scale * acc[i];
+    for (int i = 0; i < VEC; ++i) o[i] = acc[i];
+    scale_vec<VEC>(o, a.scale);
     store_vec<VEC, float>(a.dtable + v * a.ld_table + col, o);
   };
-  const long long e0 = ((long long)blockIdx.x * WARPS + warp) * 32;
-  const int cnt = (int)max(0LL, min(32LL, a.n - e0));
-  const int mykey = lane < cnt ? a.key[e0 + lane] : a.V;
-  const int myidx = lane < cnt ? a.idx[e0 + lane] : -1;
-  const int prev = cnt > 0 && e0 > 0 ? a.key[e0 - 1] : -1;
-  const int next = e0 + 32 < a.n ? a.key[e0 + 32] : -1;
+  const long long b0 = (long long)blockIdx.x * WARPS * E, b1 = b0 + WARPS * E;
+  if (b0 >= n) return;
+  const long long e0 = b0 + warp * E;
+  const int here = (int)max(0LL, min((long long)E, n - e0));
+  const int mykey = lane < here ? a.key[e0 + lane] : a.V;
+  const long long myrow = lane < here ? a.idx[e0 + lane] : 0;
+  const int prev = here > 0 && e0 > 0 ? a.key[e0 - 1] : -1;
+  const int next = e0 + E < n ? a.key[e0 + E] : -1;
+  const int bprev = b0 > 0 ? a.key[b0 - 1] : -1;
+  const int bnext = b1 < n ? a.key[b1] : -1;
+  // rows without a label (V) are last: they are no entries
+  const int cnt = __popc(__ballot_sync(0xffffffffu, mykey != a.V));
+  if (lane < E) ent[warp][lane] = Entry{myrow * a.ld_src, mykey, 0};
   if (lane < 2) {
     skey[2 * warp + lane] = a.V;
     sused[2 * warp + lane] = 0;
@@ -392,18 +552,17 @@ k_embed_sum(SumArgs a, const TS* __restrict__ src) {
   __syncwarp();
   float acc[VEC] = {};
   int cur = __shfl_sync(0xffffffffu, mykey, 0);
-  bool first = true;  // the run that holds entry 0
+  bool first = true;  // the run that holds the segment's first entry
   auto flush = [&](bool last) {
     if (cur == a.V) return;
     const bool left = first && prev == cur, right = last && next == cur;
-    const int kind = run_kind(left, right);
-    if (kind == RUN_WHOLE) {
+    if (!left && !right) {
       store_row(cur, acc);
       return;
     }
-    const int slot = 2 * warp + (kind == RUN_TAIL);
+    const int slot = 2 * warp + !left;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) sv[slot][lane * VEC + i] = acc[i];
+    for (int i = 0; i < VEC; ++i) sv[slot][i * 32 + lane] = acc[i];
     if (lane == 0) {
       skey[slot] = cur;
       sused[slot] = 1;
@@ -412,64 +571,53 @@ k_embed_sum(SumArgs a, const TS* __restrict__ src) {
       if (left && right) skey[slot + 1] = cur;
     }
   };
+  const TS* mycol = src + (col_ok ? col : 0);
 #pragma unroll 1
-  for (int j0 = 0; j0 < cnt; j0 += 8) {
-    float x[8][VEC];
+  for (int j0 = 0; j0 < cnt; j0 += FLY) {
+    Raw<VEC, TS> raw[FLY];
+    int key[FLY];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int k = __shfl_sync(0xffffffffu, mykey, j0 + j);
-      const int r = __shfl_sync(0xffffffffu, myidx, j0 + j);
-      if (k != a.V && r >= 0 && col_ok) {
-        load_vec<VEC, TS>(src + r * a.ld_src + col, x[j]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) x[j][i] = 0.f;
-      }
+    for (int j = 0; j < FLY; ++j) {
+      // (past the last entry: the last one again, not added)
+      const Entry e = ent[warp][min(j0 + j, cnt - 1)];
+      key[j] = e.key;
+      raw[j].load(mycol + e.off);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int k = __shfl_sync(0xffffffffu, mykey, j0 + j);
-      if (k != cur) {
+    for (int j = 0; j < FLY; ++j) {
+      if (j0 + j >= cnt) break;
+      if (key[j] != cur) {
         flush(false);
-        cur = k;
+        cur = key[j];
         first = false;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) acc[i] = x[j][i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) acc[i] += x[j][i];
+        for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
       }
+      float x[VEC];
+      raw[j].widen(x);
+      add_vec<VEC>(acc, x);
     }
   }
   flush(true);
   __syncthreads();
   if (warp != 0) return;
   // the warps' pieces, in order
-  const long long b0 = (long long)blockIdx.x * WARPS * 32;
-  const int bprev = b0 > 0 ? a.key[b0 - 1] : -1;
-  const int bnext = b0 + WARPS * 32 < a.n ? a.key[b0 + WARPS * 32] : -1;
-  int hk[2] = {a.V, a.V}, hu[2] = {-1, -1};
-  cur = skey[0];
+  const int slotkey = lane < 2 * WARPS ? skey[lane] : a.V;
+  if (!__any_sync(0xffffffffu, slotkey != a.V)) return;
+  const int slotused = lane < 2 * WARPS ? sused[lane] : 0;
+  cur = __shfl_sync(0xffffffffu, slotkey, 0);
   first = true;
 #pragma unroll
   for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
   auto flush_block = [&](bool last) {
     if (cur == a.V) return;
     const bool left = first && bprev == cur, right = last && bnext == cur;
-    const int kind = run_kind(left, right);
-    if (kind == RUN_WHOLE) {
-      store_row(cur, acc);
-      return;
-    }
-    const int t = kind == RUN_TAIL;
-    const int slot = 2 * blockIdx.x + t;
-    if (col_ok) store_vec<VEC, float>(a.part + slot * a.ldp + col, acc);
-    hk[t] = cur;
-    hu[t] = slot;
-    if (left && right) hk[1] = cur;
+    if (!left && !right) store_row(cur, acc);
+    else if (col_ok) store_vec<VEC, float>(a.part + (2LL * blockIdx.x + !left) * a.ldp + col, acc);
   };
+#pragma unroll
   for (int s = 0; s < 2 * WARPS; ++s) {
-    const int k = skey[s];
+    const int k = __shfl_sync(0xffffffffu, slotkey, s);
     if (k != cur) {
       flush_block(false);
       cur = k;
@@ -477,23 +625,81 @@ k_embed_sum(SumArgs a, const TS* __restrict__ src) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
     }
-    if (sused[s]) {
+    if (__shfl_sync(0xffffffffu, slotused, s)) {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) acc[i] += sv[s][lane * VEC + i];
+      for (int i = 0; i < VEC; ++i) acc[i] += sv[s][i * 32 + lane];
     }
   }
   flush_block(true);
-  if (a.pkey && blockIdx.y == 0 && lane < 2) {
-    a.pkey[2 * blockIdx.x + lane] = lane ? hk[1] : hk[0];
-    a.pidx[2 * blockIdx.x + lane] = lane ? hu[1] : hu[0];
+}
+
+// Runs that cross chunks: the block of the chunk in which such a run begins
+// finds the chunk in which it ends and adds its pieces, a contiguous share per
+// warp, then the warps' sums in order.
+template <int E, int VEC>
+__global__ void __launch_bounds__(SUM_WARPS * 32) k_embed_join(SumArgs a) {
+  constexpr int CHUNK = SUM_WARPS * E;
+  __shared__ float sv[SUM_WARPS][32 * VEC];
+  __shared__ int end_s;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = (blockIdx.y * 32 + lane) * VEC;
+  const int c = blockIdx.x;
+  ptx::griddep_wait();
+  if (c >= a.chunks - 1) {
+    if (blockIdx.y == 0)
+      clear_rows(a.clear, c - max(0, a.chunks - 1), a.V, a.D, a.dtable, a.ld_table, a.v4);
+    return;
   }
+  const int n = a.live ? *a.live : a.n;
+  const long long e0 = (long long)c * CHUNK, e1 = e0 + CHUNK;
+  if (e1 >= n) return;
+  const int k = a.key[e1 - 1];
+  if (k == a.V || a.key[e1] != k) return;
+  if (e0 > 0 && a.key[e0 - 1] == k) return;  // it began earlier
+  // last chunk of the run: the first after c whose next entry is another label
+  if (threadIdx.x == 0) end_s = 0x7fffffff;
+  __syncthreads();
+  int last = 0;
+  for (int d = c + 1;; d += SUM_WARPS * 32) {
+    const long long e = ((long long)d + threadIdx.x + 1) * CHUNK;
+    if (e >= n || a.key[e] != k) atomicMin(&end_s, d + threadIdx.x);
+    __syncthreads();
+    last = end_s;
+    __syncthreads();
+    if (last != 0x7fffffff) break;
+  }
+  const int pieces = last - c + 1, share = (pieces + SUM_WARPS - 1) / SUM_WARPS;
+  const int p0 = warp * share, p1 = min(pieces, p0 + share);
+  float acc[VEC] = {};
+  if (col < a.D) {
+#pragma unroll 4
+    for (int p = p0; p < p1; ++p) {  // piece 0 is chunk c's tail, the others are heads
+      Raw<VEC, float> raw;
+      raw.load(a.part + (2LL * (c + p) + (p == 0)) * a.ldp + col);
+      float x[VEC];
+      raw.widen(x);
+      add_vec<VEC>(acc, x);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) sv[warp][i * 32 + lane] = acc[i];
+  __syncthreads();
+  if (warp != 0 || col >= a.D) return;
+  const int busy = (pieces + share - 1) / share;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    float s = acc[i];
+    for (int w = 1; w < busy; ++w) s += sv[w][i * 32 + lane];
+    acc[i] = a.scale * s;
+  }
+  store_vec<VEC, float>(a.dtable + k * a.ld_table + col, acc);
 }
 
 bool embed_args(const rnnt_embed_dims* d, EmbedArgs* a) {
   if (!d || d->B < 0 || d->U1 < 1 || d->V < 1 || d->D < 1) return false;
   if ((long long)d->B * d->U1 > (1LL << 30)) return false;
   if (d->sos && (d->blank < 0 || d->blank >= d->V)) return false;
-  if (!op_dtype(d->table_dtype) || !op_dtype(d->row_dtype)) return false;
+  if (!op_dtype(d->table_dtype) || !op_dtype(d->row_dtype) || !isfinite(d->scale)) return false;
   if ((d->ld_table && d->ld_table < d->D) || (d->ld_rows && d->ld_rows < d->D)) return false;
   a->B = d->B; a->U1 = d->U1; a->V = d->V; a->D = d->D;
   a->blank = d->blank; a->sos = d->sos != 0; a->scale = d->scale;
@@ -502,16 +708,16 @@ bool embed_args(const rnnt_embed_dims* d, EmbedArgs* a) {
   return true;
 }
 
-// Workspace and levels of a gradient call.
+// Workspace and launches of a gradient call.
 struct EmbedPlan {
-  int N, blocks, per, passes, bits;  // blocks 0: sorted by counting
-  int levels;
-  long long n[8], chunks[8];         // list length and chunks of every level
+  int N;
+  int range, groups;                 // listed by label ranges (groups 0: by the radix sort)
+  int blocks, per, passes, bits;
+  int entries;                       // list entries per warp of the sums
+  int chunks;
   int ldp;
-  size_t w_key[2], w_idx[2], w_hist, hist_each, w_pkey[8], w_pidx[8], w_part[8], total;
+  size_t w_key[2], w_idx[2], w_live, w_present, w_hist, hist_each, w_part, total;
 };
-
-constexpr int SUM_WARPS0 = 8, SUM_WARPS1 = 32;
 
 EmbedPlan embed_plan(const EmbedArgs& a) {
   EmbedPlan p{};
@@ -522,7 +728,13 @@ EmbedPlan embed_plan(const EmbedArgs& a) {
     p.w_key[i] = put(4 * (size_t)p.N);
     p.w_idx[i] = put(4 * (size_t)p.N);
   }
-  if (p.N > RANK_MAX) {
+  p.w_live = put(4);
+  // (152: the SMs; the layout may not depend on the device that runs it)
+  p.range = (int)cdiv(a.V, 152);
+  if (p.N > 0 && p.N <= GROUP_MAX_ROWS && p.range <= GROUP_MAX_RANGE) {
+    p.groups = (int)cdiv(a.V, p.range);
+    p.w_present = put((size_t)a.V);
+  } else {
     int bits = 1;
     while ((1LL << bits) <= a.V) ++bits;  // labels 0 to V
     p.passes = (int)cdiv(bits, MAX_DIGIT_BITS);
@@ -530,50 +742,80 @@ EmbedPlan embed_plan(const EmbedArgs& a) {
     // at most one block per SM, whole tiles of SORT_THREADS entries each (every
     // block reads all blocks' counts, so more blocks would read more)
     const long long tiles = cdiv(p.N, SORT_THREADS);
-    p.per = (int)cdiv(tiles, std::min<long long>(tiles, 152)) * SORT_THREADS;
-    p.blocks = (int)cdiv(p.N, p.per);
+    p.per = (int)cdiv(tiles, tiles < 152 ? (tiles ? tiles : 1) : 152) * SORT_THREADS;
+    p.blocks = p.N ? (int)cdiv(p.N, p.per) : 0;
     p.hist_each = (size_t)p.blocks << p.bits;
     p.w_hist = put(4 * p.hist_each * p.passes);
   }
-  p.ldp = (int)cdiv(a.D, 4) * 4;
-  long long n = p.N;
-  for (int l = 0;; ++l) {
-    p.n[l] = n;
-    p.chunks[l] = cdiv(n, 32 * (l ? SUM_WARPS1 : SUM_WARPS0));
-    p.levels = l + 1;
-    if (p.chunks[l] <= 1) break;
-    const size_t slots = 2 * (size_t)p.chunks[l];
-    p.w_pkey[l] = put(4 * slots);
-    p.w_pidx[l] = put(4 * slots);
-    p.w_part[l] = put(4 * slots * p.ldp);
-    n = (long long)slots;
-  }
-  p.total = o ? o : ALIGN;
+  // one round of loads a warp until that fills the SMs' warps several times
+  p.entries = p.N <= 16384 ? 8 : 32;
+  p.chunks = (int)cdiv(p.N, SUM_WARPS * p.entries);
+  p.ldp = (int)cdiv(a.D, 8) * 8;
+  p.w_part = put(8 * (size_t)p.chunks * p.ldp);
+  p.total = o;
   return p;
 }
 
 // A launch that may start its set-up under the previous kernel's tail (the
 // kernels wait with griddep_wait before they read).
 template <typename... KA, typename... A>
-cudaError_t launch_dep(void (*k)(KA...), dim3 grid, int threads, cudaStream_t st, A... args) {
+cudaError_t launch_dep(void (*k)(KA...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                       A... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
-template <int WARPS, typename TS>
-cudaError_t launch_sum(const SumArgs& s, const void* src, unsigned blocks, bool v4,
-                       cudaStream_t st) {
-  const dim3 grid(blocks, (unsigned)cdiv(s.D, v4 ? 128 : 32));
-  return v4 ? launch_dep(k_embed_sum<WARPS, 4, TS>, grid, WARPS * 32, st, s, (const TS*)src)
-            : launch_dep(k_embed_sum<WARPS, 1, TS>, grid, WARPS * 32, st, s, (const TS*)src);
+cudaError_t launch_group(const EmbedArgs& a, const EmbedPlan& p, const ClearShare& cs,
+                         int32_t* lkey, int32_t* lidx, int32_t* live, float* dtable, int v4,
+                         cudaStream_t st) {
+  const size_t smem = 4 * (size_t)(SORT_WARPS + 1) * p.range;
+  static std::atomic<bool> opted_in[kDeviceSlots];
+  std::atomic<bool>& opted = opted_in[device_slot()];
+  if (!opted.load()) {
+    const cudaError_t e = cudaFuncSetAttribute(k_embed_group,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               4 * (SORT_WARPS + 1) * GROUP_MAX_RANGE);
+    if (e != cudaSuccess) return e;
+    opted.store(true);
+  }
+  k_embed_group<<<p.groups, SORT_THREADS, smem, st>>>(a, cs, lkey, lidx, live,
+                                                      (uint8_t*)cs.present, dtable, v4);
+  return cudaGetLastError();
+}
+
+template <int E, int VEC, typename TS>
+cudaError_t launch_sums_v(SumArgs s, const void* src, int clear, ClearShare last,
+                          cudaStream_t st) {
+  const unsigned cols = (unsigned)cdiv(s.D, 32 * VEC);
+  const cudaError_t e = launch_dep(k_embed_sum<E, VEC, TS>, dim3(s.chunks + clear, cols),
+                                   SUM_WARPS * 32, 0, st, s, (const TS*)src);
+  if (e != cudaSuccess) return e;
+  s.clear = last;
+  const int join = (s.chunks > 1 ? s.chunks - 1 : 0) + (last.present ? clear : 0);
+  if (!join) return cudaSuccess;
+  return launch_dep(k_embed_join<E, VEC>, dim3(join, cols), SUM_WARPS * 32, 0, st, s);
+}
+
+template <typename TS>
+cudaError_t launch_sums(const SumArgs& s, const void* src, int clear, const ClearShare& last,
+                        int entries, int vec, cudaStream_t st) {
+  if (entries == 8) {
+    if (vec == 8) return launch_sums_v<8, 8, TS>(s, src, clear, last, st);
+    if (vec == 2) return launch_sums_v<8, 2, TS>(s, src, clear, last, st);
+    return launch_sums_v<8, 1, TS>(s, src, clear, last, st);
+  }
+  if (vec == 8) return launch_sums_v<32, 8, TS>(s, src, clear, last, st);
+  if (vec == 2) return launch_sums_v<32, 2, TS>(s, src, clear, last, st);
+  return launch_sums_v<32, 1, TS>(s, src, clear, last, st);
 }
 
 }  // namespace
@@ -641,14 +883,17 @@ rnnt_status rnnt_embed_bwd(const rnnt_embed_dims* dims, const int32_t* ids, cons
   const EmbedPlan p = embed_plan(a);
   char* w = (char*)ws;
   auto at = [&](size_t off) { return (int32_t*)(w + off); };
-  int out = 0;  // which of the two list buffers holds the sorted list
-  if (p.N > 0 && !p.blocks) {
-    ProfScope ps("embed_sort", st);
-    k_embed_rank<<<(unsigned)cdiv(p.N, SORT_THREADS / 32), SORT_THREADS, 0, st>>>(
-        a, at(p.w_key[0]), at(p.w_idx[0]));
-    OPS_CHECK(cudaGetLastError());
+  int out = 0;  // which of the two list buffers holds the list
+  const int v4 = a.D % 4 == 0 && a.ld_table % 4 == 0 && aligned_to(dtable, 16);
+  ClearShare cs{};
+  if (p.groups) {
+    cs.range = p.range;
+    cs.j1 = p.range * 3 / 8;
+    cs.present = (const uint8_t*)(w + p.w_present);
+    OPS_LAUNCH("embed_list", launch_group(a, p, cs, at(p.w_key[0]), at(p.w_idx[0]), at(p.w_live),
+                                          dtable, v4, st));
   } else if (p.N > 0) {
-    ProfScope ps("embed_sort", st);
+    ProfScope ps("embed_list", st);
     ps.set_kernels(1 + p.passes);
     SortArgs s{};
     s.N = p.N; s.per = p.per; s.blocks = p.blocks; s.bits = p.bits;
@@ -668,38 +913,36 @@ rnnt_status rnnt_embed_bwd(const rnnt_embed_dims* dims, const int32_t* ids, cons
       s.next_bits = k + 1 < p.passes ? p.bits : 0;
       s.hist = hist + k * p.hist_each;
       s.hist_next = hist + (k + 1) * p.hist_each;
-      OPS_CHECK(launch_dep(k_embed_scatter, dim3(p.blocks), SORT_THREADS, st, s));
+      OPS_CHECK(launch_dep(k_embed_scatter, dim3(p.blocks), SORT_THREADS, 0, st, s));
     }
   }
   ProfScope ps("embed_grad", st);
-  ps.set_kernels(p.levels);
-  const bool v4 = a.D % 4 == 0 && a.ld_table % 4 == 0 && a.ld_rows % 4 == 0 &&
-                  aligned_to(dtable, 16) && aligned_to(drows, 4 * op_size(dims->row_dtype));
-  for (int l = 0; l < p.levels; ++l) {
-    SumArgs s{};
-    s.n = (int)p.n[l]; s.V = a.V; s.D = a.D;
-    s.key = at(l ? p.w_pkey[l - 1] : p.w_key[out]);
-    s.idx = at(l ? p.w_pidx[l - 1] : p.w_idx[out]);
-    s.ld_src = l ? p.ldp : a.ld_rows;
-    s.scale = a.scale;
-    s.dtable = dtable; s.ld_table = a.ld_table;
-    s.chunks = (int)p.chunks[l];
-    s.ldp = p.ldp;
-    if (l + 1 < p.levels) {
-      s.pkey = at(p.w_pkey[l]);
-      s.pidx = at(p.w_pidx[l]);
-      s.part = (float*)(w + p.w_part[l]);
-    }
-    if (l) {
-      OPS_CHECK((launch_sum<SUM_WARPS1, float>(s, w + p.w_part[l - 1], (unsigned)s.chunks, v4, st)));
-      continue;
-    }
-    const unsigned blocks = (unsigned)(s.chunks + cdiv(a.V, 8 * SUM_WARPS0));
-    if (dims->row_dtype == RNNT_F32)
-      OPS_CHECK((launch_sum<SUM_WARPS0, float>(s, drows, blocks, v4, st)));
-    else
-      OPS_CHECK((launch_sum<SUM_WARPS0, __nv_bfloat16>(s, drows, blocks, v4, st)));
+  ps.set_kernels(p.chunks < 2 && !p.groups ? 1 : 2);
+  SumArgs s{};
+  s.n = p.N; s.V = a.V; s.D = a.D;
+  s.live = p.groups ? at(p.w_live) : nullptr;
+  s.key = at(p.w_key[out]);
+  s.idx = at(p.w_idx[out]);
+  s.ld_src = a.ld_rows;
+  s.scale = a.scale;
+  s.dtable = dtable; s.ld_table = a.ld_table;
+  s.chunks = p.chunks;
+  s.part = (float*)(w + p.w_part);
+  s.ldp = p.ldp;
+  s.v4 = v4;
+  ClearShare last{};
+  int clear = (int)cdiv(a.V, 8 * SUM_WARPS);
+  if (p.groups) {
+    clear = p.groups;
+    last = s.clear = cs;
+    s.clear.j0 = cs.j1;
+    s.clear.j1 = last.j0 = p.range * 3 / 4;
+    last.j1 = p.range;
   }
+  const int vec = vec_of(a.D, a.ld_table, dtable, 4, a.ld_rows, drows, op_size(dims->row_dtype));
+  OPS_CHECK(dims->row_dtype == RNNT_F32
+                ? launch_sums<float>(s, drows, clear, last, p.entries, vec, st)
+                : launch_sums<__nv_bfloat16>(s, drows, clear, last, p.entries, vec, st));
   return RNNT_OK;
 }
 

@@ -29,7 +29,8 @@ ORTH = dict(rows=8, cols=16, batch=1, in_dtype=0, out_dtype=1, steps=5, eps=1e-7
 
 @pytest.mark.parametrize("bad", [dict(B=-1), dict(U1=0), dict(V=0), dict(D=0), dict(blank=7),
                                  dict(blank=-1), dict(table_dtype=2), dict(row_dtype=3),
-                                 dict(ld_table=15), dict(ld_rows=-1), dict(B=1 << 20, U1=1 << 11)])
+                                 dict(ld_table=15), dict(ld_rows=-1), dict(B=1 << 20, U1=1 << 11),
+                                 dict(scale=float("inf")), dict(scale=float("nan"))])
 def test_embed_dims(lib, bad):
     d = RnntEmbedDims(**{**EMBED, **bad})
     assert lib.rnnt_embed_workspace_bytes(ctypes.byref(d)) == 0
