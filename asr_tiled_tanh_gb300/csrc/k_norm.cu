@@ -8,8 +8,24 @@
 namespace rnnt {
 namespace {
 
+// Division of 0 <= n < 2^31 by a fixed d (round-up reciprocal): a multiply-high,
+// an add and a shift in place of the twenty instructions of a 32-bit division.
+struct FastDiv {
+  uint32_t d, mul, shift;
+};
+FastDiv fast_div(uint32_t d) {
+  FastDiv f{d, 0, 0};
+  while ((1ull << f.shift) < d) ++f.shift;
+  f.mul = (uint32_t)(((1ull << 32) * ((1ull << f.shift) - d)) / d + 1);
+  return f;
+}
+__device__ __forceinline__ int operator/(int n, const FastDiv& f) {
+  return (int)((__umulhi((uint32_t)n, f.mul) + (uint32_t)n) >> f.shift);
+}
+
 struct NormArgs {
   int B, T, C, G, cg, act;
+  FastDiv cg_div;
   float eps;
   long long xf, xb, yf, yb;
   const float* gamma;
@@ -129,7 +145,8 @@ struct Slab {
   int per_max;       // frames a block may own
   int cbv;           // vectors of a column block (all VEC-wide columns of W, at most NT)
   int pow2;          // cbv is a power of two <= 32: columns meet by shuffles first
-  int ch_bytes;      // scratch bytes per reduced quantity
+  int scratch;       // scratch bytes per reduced quantity
+  FastDiv per_sample_div, S_div, cbv_div;
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -153,29 +170,31 @@ __device__ __forceinline__ float peer_f32(const float* p, int rank) {
 }
 
 // Sums over the block's frames of NA quantities per channel, for the channels
-// of the current column block: afterwards scr[q * n + c], n = cbv * VEC.
+// of the current column block: afterwards res[q * n + c], n = cbv * VEC, where
+// res is returned (behind the NA * rows * n partial sums).
 template <int NA, int VEC>
-__device__ __forceinline__ void reduce_channels(const Slab& sl, float2 (&acc)[NA][kPairs(VEC)],
-                                                float* scr, int col, int rg, bool active) {
+__device__ __forceinline__ const float* reduce_channels(const Slab& sl,
+                                                        float2 (&acc)[NA][kPairs(VEC)],
+                                                        float* scr, int col, int rg, bool active) {
   const int n = sl.cbv * VEC, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rows = sl.pow2 ? NWARPS : NT / sl.cbv;
+  const int rows = sl.pow2 ? NWARPS : NT / sl.cbv_div;
   if (sl.pow2) {
+    for (int o = sl.cbv; o < 32; o <<= 1) {
 #pragma unroll
-    for (int q = 0; q < NA; ++q)
+      for (int q = 0; q < NA; ++q)
 #pragma unroll
-      for (int i = 0; i < kPairs(VEC); ++i)
-        for (int o = sl.cbv; o < 32; o <<= 1) {
+        for (int i = 0; i < kPairs(VEC); ++i) {
           acc[q][i].x += __shfl_xor_sync(0xffffffffu, acc[q][i].x, o);
-          acc[q][i].y += __shfl_xor_sync(0xffffffffu, acc[q][i].y, o);
+          if (VEC > 1) acc[q][i].y += __shfl_xor_sync(0xffffffffu, acc[q][i].y, o);
         }
+    }
     rg = warp;
     active = lane < sl.cbv;
   }
-  __syncthreads();  // the scratch's last readers are done
   if (active) {
 #pragma unroll
     for (int q = 0; q < NA; ++q) {
-      float* d = scr + ((size_t)q * rows + rg) * n + col * VEC;
+      float* d = scr + (q * rows + rg) * n + col * VEC;
 #pragma unroll
       for (int i = 0; i < kPairs(VEC); ++i) {
         d[2 * i] = acc[q][i].x;
@@ -184,27 +203,17 @@ __device__ __forceinline__ void reduce_channels(const Slab& sl, float2 (&acc)[NA
     }
   }
   __syncthreads();
-  float tot[NA][4];  // n <= 4 NT
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int c = threadIdx.x + k * NT;
-#pragma unroll
-    for (int q = 0; q < NA; ++q) {
-      float s = 0.f;
-      if (c < n)
-        for (int r = 0; r < rows; ++r) s += scr[((size_t)q * rows + r) * n + c];
-      tot[q][k] = s;
-    }
+  float* res = scr + NA * rows * n;
+  for (int c = threadIdx.x; c < NA * n; c += NT) {
+    const int q = NA > 1 && c >= n;
+    const float* d = scr + q * (rows - 1) * n + c;
+    float t = 0.f;
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r) t += d[r * n];
+    res[c] = t;
   }
   __syncthreads();
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int c = threadIdx.x + k * NT;
-    if (c < n)
-#pragma unroll
-      for (int q = 0; q < NA; ++q) scr[(size_t)q * n + c] = tot[q][k];
-  }
-  __syncthreads();
+  return res;
 }
 
 // gs[q][g] += sum over the group's channels of the column block of w(c) scr[q][c]
@@ -264,18 +273,17 @@ struct Where {
 template <int VEC>
 __device__ __forceinline__ Where<VEC> where(const NormArgs& a, const Slab& sl) {
   Where<VEC> w;
-  const int per_sample = a.G / sl.kk;
-  const int slab = blockIdx.x / sl.S;
+  const int slab = (int)blockIdx.x / sl.S_div;
   w.rank = blockIdx.x - slab * sl.S;
-  w.b = slab / per_sample;
-  w.c0 = (slab - w.b * per_sample) * sl.W;
+  w.b = slab / sl.per_sample_div;
+  w.c0 = (slab - w.b * (int)sl.per_sample_div.d) * sl.W;
   w.tb = frames_of(a, w.b);
-  const int per = (w.tb + sl.S - 1) / sl.S;
+  const int per = (w.tb + sl.S - 1) / sl.S_div;
   w.t0 = min(w.tb, w.rank * per);
   w.rows = min(w.tb, w.t0 + per) - w.t0;
-  w.rg = threadIdx.x / sl.cbv;
+  w.rg = (int)threadIdx.x / sl.cbv_div;
   w.v = threadIdx.x - w.rg * sl.cbv;
-  w.step = NT / sl.cbv;
+  w.step = NT / sl.cbv_div;
   w.active = w.rg < w.step;
   return w;
 }
@@ -284,23 +292,36 @@ __device__ __forceinline__ Where<VEC> where(const NormArgs& a, const Slab& sl) {
 template <int VEC, typename T>
 __device__ __forceinline__ void zero_tail(const NormArgs& a, const Slab& sl, const Where<VEC>& w,
                                           T* out, long long ld) {
-  const int left = a.T - w.tb, per = (left + sl.S - 1) / sl.S;
+  const int left = a.T - w.tb, per = (left + sl.S - 1) / sl.S_div;
   const int z0 = w.tb + min(left, w.rank * per), z1 = w.tb + min(left, (w.rank + 1) * per);
   if (!w.active) return;
   const Ch<VEC> z{};
   for (int cb = 0; cb < sl.W; cb += sl.cbv * VEC) {
     const int c = cb + w.v * VEC;
     if (c >= sl.W) continue;
-    for (int t = z0 + w.rg; t < z1; t += w.step) store_ch<VEC, T>(out + t * ld + c, z);
+    T* p = out + (long long)(z0 + w.rg) * ld + c;
+    const long long inc = w.step * ld;
+#pragma unroll 4
+    for (int t = z0 + w.rg; t < z1; t += w.step, p += inc) store_ch<VEC, T>(p, z);
   }
 }
 
+// Frames of the calling thread's column: rg, rg + step, ...
+template <int VEC>
+__device__ __forceinline__ int rows_of(const Where<VEC>& w) {
+  return w.active && w.rg < w.rows ? (w.rows - 1 - w.rg) / w.step + 1 : 0;
+}
+
+// Row steps: within shared memory 32 bits do.
+template <int RES> struct StepType { using type = long long; };
+template <> struct StepType<1> { using type = int; };
+
 template <typename T, int VEC, int ACT, int RES>
-__global__ void __launch_bounds__(NT, RES ? 3 : 4)
+__global__ void __launch_bounds__(NT, 3)
 k_norm_fwd(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) {
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float gs[1][MAX_KK];
-  __shared__ float mean_s[MAX_KK], m2_s[MAX_KK], n_s;  // read by the cluster's other blocks
+  // (gs[1], mean_s and n_s are read by the cluster's other blocks)
+  __shared__ float gs[2][MAX_KK], mean_s[MAX_KK], n_s;
   __shared__ float mean_t[MAX_KK], rstd_t[MAX_KK];
   T* tile = (T*)smem;
   float* scr = (float*)(smem + (RES ? align_up((size_t)sl.per_max * sl.W * sizeof(T), 16) : 0));
@@ -309,58 +330,78 @@ k_norm_fwd(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) {
   T* ys = y + w.b * a.yb + w.c0;
   if (RES) copy_share(tile, xs + (long long)w.t0 * a.xf, a.xf, w.rows, sl.W);
   zero_tail<VEC, T>(a, sl, w, ys, a.yf);
+  using Step = typename StepType<RES>::type;
   const T* src = RES ? tile : xs + (long long)w.t0 * a.xf;
-  const long long ld = RES ? sl.W : a.xf;
-  const int nb = sl.cbv * VEC;
+  const Step ld = RES ? sl.W : a.xf, inc = ld * w.step;
+  const int nb = sl.cbv * VEC, cnt = rows_of(w);
   const float n = (float)w.rows * a.cg;
-  if (threadIdx.x < sl.kk) gs[0][threadIdx.x] = 0.f;
+  if (threadIdx.x < sl.kk) gs[0][threadIdx.x] = gs[1][threadIdx.x] = 0.f;
   if (RES) copy_wait();
   __syncthreads();
-  // the block's own mean per group, then the squares about it
+  // One pass over the data: every thread sums its own frames of a channel and
+  // their squares about the first of them (its few frames lose no digits to
+  // that, wherever the mean is).  Then the block's mean, and the squares about
+  // that: q - s^2 / k about the thread's mean, plus k (its mean - mean)^2.
+  float2 fsum[kPairs(VEC)], fsq[kPairs(VEC)];
 #pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
+  for (int half = 0; half < 2; ++half) {
 #pragma unroll 1
     for (int cb = 0; cb < sl.W; cb += nb) {
       const int c = cb + w.v * VEC;
-      const bool on = w.active && c < sl.W;
+      const bool on = w.active && c < sl.W && cnt > 0;
       float2 acc[1][kPairs(VEC)] = {};
-      if (on) {
-        if (pass == 0) {
-#pragma unroll 4
-          for (int r = w.rg; r < w.rows; r += w.step) {
-            const Ch<VEC> q = load_ch<VEC, T>(src + r * ld + c);
+      // (a slab of one column block keeps its sums; wider ones read again)
+      if (on && (half == 0 || nb < sl.W)) {
+        const T* p = src + w.rg * ld + c;
+        const Ch<VEC> first = load_ch<VEC, T>(p);
+        float2 m[kPairs(VEC)], s0[kPairs(VEC)] = {}, q0[kPairs(VEC)] = {};
 #pragma unroll
-            for (int i = 0; i < kPairs(VEC); ++i) acc[0][i] = __fadd2_rn(acc[0][i], q.v[i]);
+        for (int i = 0; i < kPairs(VEC); ++i)
+          m[i] = make_float2(-first.v[i].x, -first.v[i].y);
+#pragma unroll 4
+        for (int k = 0; k < cnt; ++k, p += inc) {
+          const Ch<VEC> q = load_ch<VEC, T>(p);
+#pragma unroll
+          for (int i = 0; i < kPairs(VEC); ++i) {
+            const float2 d = __fadd2_rn(q.v[i], m[i]);
+            s0[i] = __fadd2_rn(s0[i], d);
+            q0[i] = __ffma2_rn(d, d, q0[i]);
           }
-        } else {
-          float2 m[kPairs(VEC)];
+        }
+        const float k = (float)cnt, rk = 1.f / k;
 #pragma unroll
-          for (int i = 0; i < kPairs(VEC); ++i)
-            m[i] = make_float2(-mean_s[(c + 2 * i) / a.cg],
-                               VEC > 1 ? -mean_s[(c + 2 * i + 1) / a.cg] : 0.f);
-#pragma unroll 4
-          for (int r = w.rg; r < w.rows; r += w.step) {
-            const Ch<VEC> q = load_ch<VEC, T>(src + r * ld + c);
+        for (int i = 0; i < kPairs(VEC); ++i) {
+          const float2 mk = __fmul2_rn(s0[i], make_float2(rk, rk));
+          fsum[i] = __fadd2_rn(mk, first.v[i]);
+          fsq[i] = __ffma2_rn(make_float2(-s0[i].x, -s0[i].y), mk, q0[i]);
+        }
+      }
+      if (on) {
+        const float2 k = make_float2((float)cnt, (float)cnt);
 #pragma unroll
-            for (int i = 0; i < kPairs(VEC); ++i) {
-              const float2 d = __fadd2_rn(q.v[i], m[i]);
-              acc[0][i] = __ffma2_rn(d, d, acc[0][i]);
-            }
+        for (int i = 0; i < kPairs(VEC); ++i) {
+          if (half == 0) {
+            acc[0][i] = __fmul2_rn(k, fsum[i]);
+          } else {
+            const int ca = c + 2 * i, cz = VEC > 1 ? ca + 1 : ca;
+            const float2 d = __fadd2_rn(fsum[i], make_float2(-mean_s[ca / a.cg_div],
+                                                             -mean_s[cz / a.cg_div]));
+            acc[0][i] = __ffma2_rn(__fmul2_rn(d, d), k, fsq[i]);
           }
         }
       }
-      reduce_channels<1, VEC>(sl, acc, scr, w.v, w.rg, on);
-      reduce_groups<1, VEC>(sl, a.cg, cb, scr, gs, [](int) { return 1.f; });
+      const float* res =
+          reduce_channels<1, VEC>(sl, acc, scr, w.v, w.rg, w.active && c < sl.W);
+      reduce_groups<1, VEC>(sl, a.cg, cb, res, gs + half, [](int) { return 1.f; });
     }
     __syncthreads();
-    for (int g = threadIdx.x; g < sl.kk; g += NT) {
-      if (pass == 0) mean_s[g] = w.rows ? gs[0][g] / n : 0.f;
-      else m2_s[g] = gs[0][g];
-      gs[0][g] = 0.f;
+    if (half == 0) {
+      for (int g = threadIdx.x; g < sl.kk; g += NT) mean_s[g] = w.rows ? gs[0][g] / n : 0.f;
+      if (threadIdx.x == 0) n_s = n;
+      __syncthreads();
     }
-    if (threadIdx.x == 0) n_s = n;
-    __syncthreads();
   }
+  const float* m2_s = gs[1];
   // the blocks' (n, mean, M2) joined in order
   if (sl.S > 1) {
     cluster_arrive();
@@ -390,24 +431,29 @@ k_norm_fwd(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) {
   for (int cb = 0; cb < sl.W; cb += nb) {
     const int c = cb + w.v * VEC;
     if (!w.active || c >= sl.W) continue;
+    if (cnt == 0) continue;
     float2 m[kPairs(VEC)], s[kPairs(VEC)], be[kPairs(VEC)];
 #pragma unroll
     for (int i = 0; i < kPairs(VEC); ++i) {
       float2 rs, ga;
       const int ca = c + 2 * i, cz = VEC > 1 ? ca + 1 : ca;
-      m[i] = make_float2(-mean_t[ca / a.cg], -mean_t[cz / a.cg]);
-      rs = make_float2(rstd_t[ca / a.cg], rstd_t[cz / a.cg]);
+      const int gx = ca / a.cg_div, gz = cz / a.cg_div;
+      m[i] = make_float2(-mean_t[gx], -mean_t[gz]);
+      rs = make_float2(rstd_t[gx], rstd_t[gz]);
       ga = a.gamma ? make_float2(a.gamma[w.c0 + ca], a.gamma[w.c0 + cz]) : make_float2(1.f, 1.f);
       be[i] = a.beta ? make_float2(a.beta[w.c0 + ca], a.beta[w.c0 + cz]) : make_float2(0.f, 0.f);
       s[i] = __fmul2_rn(rs, ga);
     }
+    const T* p = src + w.rg * ld + c;
+    T* o = yt + w.rg * a.yf + c;
+    const long long oinc = w.step * a.yf;
 #pragma unroll 4
-    for (int r = w.rg; r < w.rows; r += w.step) {
-      Ch<VEC> q = load_ch<VEC, T>(src + r * ld + c);
+    for (int k = 0; k < cnt; ++k, p += inc, o += oinc) {
+      Ch<VEC> q = load_ch<VEC, T>(p);
 #pragma unroll
       for (int i = 0; i < kPairs(VEC); ++i)
         q.v[i] = act2<ACT, T>(__ffma2_rn(__fadd2_rn(q.v[i], m[i]), s[i], be[i]));
-      store_ch<VEC, T>(yt + r * a.yf + c, q);
+      store_ch<VEC, T>(o, q);
     }
   }
   __syncwarp();
@@ -436,8 +482,10 @@ k_norm_bwd(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict__ d
   zero_tail<VEC, T>(a, sl, w, os, a.xf);
   os += (long long)w.t0 * a.xf;
   const T *sx = RES ? tx : xs, *sd = RES ? td : ds;
-  const long long lx = RES ? sl.W : a.xf, ldy = RES ? sl.W : a.yf;
-  const int nb = sl.cbv * VEC;
+  using Step = typename StepType<RES>::type;
+  const Step lx = RES ? sl.W : a.xf, ldy = RES ? sl.W : a.yf;
+  const Step xinc = lx * w.step, dinc = ldy * w.step;
+  const int nb = sl.cbv * VEC, cnt = rows_of(w);
   const float2* stats = a.stats + (long long)w.b * a.G + w.c0 / a.cg;
   for (int g = threadIdx.x; g < sl.kk; g += NT) gs[0][g] = gs[1][g] = 0.f;
   if (RES) copy_wait();
@@ -453,7 +501,7 @@ k_norm_bwd(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict__ d
 #pragma unroll
         for (int i = 0; i < kPairs(VEC); ++i) {
           const int ca = c + 2 * i, cz = VEC > 1 ? ca + 1 : ca;
-          const float2 p = stats[ca / a.cg], q = stats[cz / a.cg];
+          const float2 p = stats[ca / a.cg_div], q = stats[cz / a.cg_div];
           m[i] = make_float2(-p.x, -q.x);
           rs[i] = make_float2(p.y, q.y);
           ga[i] = a.gamma ? make_float2(a.gamma[w.c0 + ca], a.gamma[w.c0 + cz])
@@ -465,10 +513,10 @@ k_norm_bwd(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict__ d
       if (pass == 0) {
         float2 acc[2][kPairs(VEC)] = {};
         if (on) {
+          const T *px = sx + w.rg * lx + c, *pd = sd + w.rg * ldy + c;
 #pragma unroll 2
-          for (int r = w.rg; r < w.rows; r += w.step) {
-            const Ch<VEC> q = load_ch<VEC, T>(sx + r * lx + c);
-            const Ch<VEC> d = load_ch<VEC, T>(sd + r * ldy + c);
+          for (int k = 0; k < cnt; ++k, px += xinc, pd += dinc) {
+            const Ch<VEC> q = load_ch<VEC, T>(px), d = load_ch<VEC, T>(pd);
 #pragma unroll
             for (int i = 0; i < kPairs(VEC); ++i) {
               const float2 xh = __fmul2_rn(__fadd2_rn(q.v[i], m[i]), rs[i]);
@@ -478,25 +526,27 @@ k_norm_bwd(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict__ d
             }
           }
         }
-        reduce_channels<2, VEC>(sl, acc, scr, w.v, w.rg, on);
+        const float* res = reduce_channels<2, VEC>(sl, acc, scr, w.v, w.rg, on);
         for (int k = threadIdx.x; k < nb && cb + k < sl.W; k += NT)
           part[((long long)w.b * sl.S + w.rank) * a.C + w.c0 + cb + k] =
-              make_float2(scr[k], scr[nb + k]);
-        reduce_groups<2, VEC>(sl, a.cg, cb, scr, gs, [&](int ch) {
+              make_float2(res[k], res[nb + k]);
+        reduce_groups<2, VEC>(sl, a.cg, cb, res, gs, [&](int ch) {
           return a.gamma ? a.gamma[w.c0 + ch] : 1.f;
         });
       } else if (on) {
         float2 k1[kPairs(VEC)], k2[kPairs(VEC)];
 #pragma unroll
         for (int i = 0; i < kPairs(VEC); ++i) {
-          const int ga_ = (c + 2 * i) / a.cg, gz = (VEC > 1 ? c + 2 * i + 1 : c + 2 * i) / a.cg;
-          k1[i] = make_float2(-m1_t[ga_], -m1_t[gz]);
-          k2[i] = make_float2(-m2_t[ga_], -m2_t[gz]);
+          const int ca = c + 2 * i, gx = ca / a.cg_div, gz = (VEC > 1 ? ca + 1 : ca) / a.cg_div;
+          k1[i] = make_float2(-m1_t[gx], -m1_t[gz]);
+          k2[i] = make_float2(-m2_t[gx], -m2_t[gz]);
         }
+        const T *px = sx + w.rg * lx + c, *pd = sd + w.rg * ldy + c;
+        T* po = os + w.rg * a.xf + c;
+        const long long oinc = w.step * a.xf;
 #pragma unroll 2
-        for (int r = w.rg; r < w.rows; r += w.step) {
-          const Ch<VEC> q = load_ch<VEC, T>(sx + r * lx + c);
-          const Ch<VEC> d = load_ch<VEC, T>(sd + r * ldy + c);
+        for (int k = 0; k < cnt; ++k, px += xinc, pd += dinc, po += oinc) {
+          const Ch<VEC> q = load_ch<VEC, T>(px), d = load_ch<VEC, T>(pd);
           Ch<VEC> o;
 #pragma unroll
           for (int i = 0; i < kPairs(VEC); ++i) {
@@ -504,7 +554,7 @@ k_norm_bwd(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict__ d
             const float2 g = dact2<ACT, T>(d.v[i], __ffma2_rn(xh, ga[i], be[i]));
             o.v[i] = __fmul2_rn(rs[i], __ffma2_rn(xh, k2[i], __ffma2_rn(g, ga[i], k1[i])));
           }
-          store_ch<VEC, T>(os + r * a.xf + c, o);
+          store_ch<VEC, T>(po, o);
         }
       }
     }
@@ -579,6 +629,7 @@ bool norm_args(const rnnt_norm_dims* d, NormArgs* a) {
   if (!(d->eps >= 0.f)) return false;
   a->B = d->B; a->T = d->T; a->C = d->C; a->G = d->G; a->cg = d->C / d->G;
   a->act = d->act; a->eps = d->eps;
+  a->cg_div = fast_div(a->cg);
   a->xf = d->x_frame ? d->x_frame : d->C;
   a->xb = d->x_batch ? d->x_batch : d->T * a->xf;
   a->yf = d->y_frame ? d->y_frame : d->C;
@@ -645,10 +696,13 @@ NormCut norm_cut(const NormArgs& a, int e, int tiles, bool aligned) {
   s.cbv = vr < NT ? vr : NT;
   s.pow2 = s.cbv <= 32 && (s.cbv & (s.cbv - 1)) == 0;
   const int rows = s.pow2 ? NWARPS : NT / s.cbv;
-  s.ch_bytes = 4 * rows * s.cbv * n.vec;
+  s.scratch = 4 * (rows + 1) * s.cbv * n.vec;
+  s.per_sample_div = fast_div(a.G / kk);
+  s.S_div = fast_div(s.S);
+  s.cbv_div = fast_div(s.cbv);
   const size_t tile = align_up((size_t)s.per_max * s.W * e, 16) * tiles;
   n.res = n.vec == 4 && tile <= SHARE_MAX;
-  n.smem = (n.res ? tile : 0) + (size_t)s.ch_bytes * tiles;
+  n.smem = (n.res ? tile : 0) + (size_t)s.scratch * tiles;
   return n;
 }
 
