@@ -1,5 +1,6 @@
 // k_norm.cu -- group norm with an activation over encoder frames, channels
 // last (include/rnnt_ops.h).
+#include <algorithm>
 #include <atomic>
 
 #include "ops.h"
@@ -46,11 +47,9 @@ __device__ __forceinline__ int frames_of(const NormArgs& a, int b) {
 }
 
 // ---- activation -------------------------------------------------------------
-// sigmoid of two values.  fp32: to fp32's own accuracy.  bf16: ex2 and one
-// reciprocal for the pair, 1 / (p q) times q and p (three special-function
-// operations instead of four, which is what bounds the bf16 kernels next to
-// their memory traffic); the exponent is capped at 60 so that p q stays finite
-// (sigmoid below 2^-60 is taken as that).
+// sigmoid of two values.  fp32: to fp32's own accuracy.  bf16: ex2 and the
+// reciprocal of the special-function unit (relative error about 2^-22; a large
+// negative u gives 1 / inf = 0).
 template <typename T>
 __device__ __forceinline__ float2 sigmoid2(float2 u) {
   if constexpr (sizeof(T) == 4) {
@@ -58,12 +57,11 @@ __device__ __forceinline__ float2 sigmoid2(float2 u) {
   } else {
     const float kL = -1.4426950408889634f;
     const float2 t = __fmul2_rn(u, make_float2(kL, kL));
-    const float2 pq = __fadd2_rn(make_float2(ptx::ex2(fminf(t.x, 60.f)),
-                                             ptx::ex2(fminf(t.y, 60.f))),
-                                 make_float2(1.f, 1.f));
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(pq.x * pq.y));
-    return __fmul2_rn(make_float2(pq.y, pq.x), make_float2(r, r));
+    const float2 p = __fadd2_rn(make_float2(ptx::ex2(t.x), ptx::ex2(t.y)), make_float2(1.f, 1.f));
+    float2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(p.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(p.y));
+    return r;
   }
 }
 
@@ -91,12 +89,12 @@ __device__ __forceinline__ float2 dact2(float2 dy, float2 u) {
 }
 
 // ---- vectors ------------------------------------------------------------------
-// A thread's VEC (4 or 1) consecutive channels of a frame, as pairs of fp32.
+// A thread's VEC (8, 4 or 1) consecutive channels of a frame, as pairs of fp32.
+constexpr int kPairs(int vec) { return vec == 1 ? 1 : vec / 2; }
 template <int VEC>
 struct Ch {
-  float2 v[VEC == 4 ? 2 : 1];
+  float2 v[kPairs(VEC)];
 };
-constexpr int kPairs(int vec) { return vec == 4 ? 2 : 1; }
 
 template <int VEC, typename T>
 __device__ __forceinline__ Ch<VEC> load_ch(const T* p) {
@@ -107,10 +105,16 @@ __device__ __forceinline__ Ch<VEC> load_ch(const T* p) {
     const float4 q = *(const float4*)p;
     c.v[0] = make_float2(q.x, q.y);
     c.v[1] = make_float2(q.z, q.w);
-  } else {
+  } else if constexpr (VEC == 4) {
     const uint2 q = *(const uint2*)p;
     c.v[0] = make_float2(ptx::bf16lo(q.x), ptx::bf16hi(q.x));
     c.v[1] = make_float2(ptx::bf16lo(q.y), ptx::bf16hi(q.y));
+  } else {
+    const uint4 q = *(const uint4*)p;
+    c.v[0] = make_float2(ptx::bf16lo(q.x), ptx::bf16hi(q.x));
+    c.v[1] = make_float2(ptx::bf16lo(q.y), ptx::bf16hi(q.y));
+    c.v[2] = make_float2(ptx::bf16lo(q.z), ptx::bf16hi(q.z));
+    c.v[3] = make_float2(ptx::bf16lo(q.w), ptx::bf16hi(q.w));
   }
   return c;
 }
@@ -120,31 +124,58 @@ __device__ __forceinline__ void store_ch(T* p, const Ch<VEC>& c) {
     *p = from_f<T>(c.v[0].x);
   } else if constexpr (sizeof(T) == 4) {
     *(float4*)p = make_float4(c.v[0].x, c.v[0].y, c.v[1].x, c.v[1].y);
-  } else {
+  } else if constexpr (VEC == 4) {
     *(uint2*)p = make_uint2(ptx::pack_bf16x2(c.v[0].x, c.v[0].y),
                             ptx::pack_bf16x2(c.v[1].x, c.v[1].y));
+  } else {
+    *(uint4*)p = make_uint4(ptx::pack_bf16x2(c.v[0].x, c.v[0].y),
+                            ptx::pack_bf16x2(c.v[1].x, c.v[1].y),
+                            ptx::pack_bf16x2(c.v[2].x, c.v[2].y),
+                            ptx::pack_bf16x2(c.v[3].x, c.v[3].y));
+  }
+}
+
+// fp32 parameters of a thread's channels (NULL: all `other`).
+template <int VEC>
+__device__ __forceinline__ void load_param(float2 (&v)[kPairs(VEC)], const float* p, float other,
+                                           bool al16) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < kPairs(VEC); ++i) v[i] = make_float2(other, other);
+  } else if (VEC > 1 && al16) {
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) {
+      const float4 q = __ldg((const float4*)p + i);
+      v[2 * i] = make_float2(q.x, q.y);
+      v[2 * i + 1] = make_float2(q.z, q.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPairs(VEC); ++i)
+      v[i] = make_float2(__ldg(p + 2 * i), VEC > 1 ? __ldg(p + 2 * i + 1) : other);
   }
 }
 
 // ---- slabs ----------------------------------------------------------------------
 // A slab is one sample's frames of kk whole groups (W = kk C/G channels, at
 // least 64 bytes of a frame where the groups allow).  A cluster of S blocks
-// owns it, a contiguous share of its frames each; RES blocks copy their share
-// into shared memory once and make every pass over it there, so that x (and
-// dy) are read once from DRAM and y (dx) written once, which is the kernels'
-// bound.  Shares are kept to 72 KB so that three blocks share an SM: one
-// computes while the others' copies are in flight.  Slabs that eight blocks
-// cannot hold, and rows that are not 16-byte aligned, are read from global
-// memory in every pass (RES = 0).
-constexpr int NT = 256, NWARPS = NT / 32;
+// owns it, a contiguous share of its frames each.  The resident kernels
+// (k_norm_*_res) copy their share into shared memory once and make every pass
+// over it there, so that x (and dy) are read once from DRAM and y (dx) written
+// once, which is the kernels' bound; slabs that eight blocks cannot hold, and
+// rows that are not 16-byte aligned, are read from global memory in every pass
+// (k_norm_*_stream).
+constexpr int NT = 128, NWARPS = NT / 32;
 constexpr int MAX_KK = 128;
-constexpr int SHARE = 72 * 1024, SHARE_MAX = 208 * 1024;
+constexpr int SHARE = 64 * 1024, SHARE_MAX = 200 * 1024;
 
 struct Slab {
   int kk, W, S;      // groups and channels per slab, blocks per slab
   int per_max;       // frames a block may own
+  int slots;         // 16-byte vectors a thread of a resident kernel may own
   int cbv;           // vectors of a column block (all VEC-wide columns of W, at most NT)
   int pow2;          // cbv is a power of two <= 32: columns meet by shuffles first
+  int nslabs;
   int scratch;       // scratch bytes per reduced quantity
   FastDiv per_sample_div, S_div, cbv_div;
 };
@@ -236,34 +267,6 @@ __device__ __forceinline__ void reduce_groups(const Slab& sl, int cg, int cb, co
   }
 }
 
-// The block's frames of a slab, copied to shared memory as dense rows of W.
-template <typename T>
-__device__ __forceinline__ void copy_share(T* dst, const T* src, long long ld, int rows, int W) {
-  const int cpr = W * (int)sizeof(T) / 16;  // 16-byte pieces of a row
-  const int per = NT / cpr;                 // rows per step of the block (cpr <= NT)
-  if (per > 0) {
-    const int r0 = threadIdx.x / cpr, c = threadIdx.x - r0 * cpr;
-    if (r0 >= per) return;
-    const char* g = (const char*)(src + r0 * ld) + 16 * c;
-    uint32_t d = ptx::smem_u32(dst) + (uint32_t)(r0 * cpr + c) * 16;
-    for (int r = r0; r < rows; r += per) {
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(g) : "memory");
-      g += (long long)per * ld * sizeof(T);
-      d += (uint32_t)(per * cpr) * 16;
-    }
-  } else {
-    for (int i = threadIdx.x; i < rows * cpr; i += NT) {
-      const int r = i / cpr, c = i - r * cpr;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst) + 16 * i),
-                   "l"((const char*)(src + r * ld) + 16 * c)
-                   : "memory");
-    }
-  }
-}
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
-}
-
 // The block's slab, frames and column.
 template <int VEC>
 struct Where {
@@ -271,10 +274,9 @@ struct Where {
   bool active;
 };
 template <int VEC>
-__device__ __forceinline__ Where<VEC> where(const NormArgs& a, const Slab& sl) {
+__device__ __forceinline__ Where<VEC> where(const NormArgs& a, const Slab& sl, int slab, int rank) {
   Where<VEC> w;
-  const int slab = (int)blockIdx.x / sl.S_div;
-  w.rank = blockIdx.x - slab * sl.S;
+  w.rank = rank;
   w.b = slab / sl.per_sample_div;
   w.c0 = (slab - w.b * (int)sl.per_sample_div.d) * sl.W;
   w.tb = frames_of(a, w.b);
@@ -312,105 +314,15 @@ __device__ __forceinline__ int rows_of(const Where<VEC>& w) {
   return w.active && w.rg < w.rows ? (w.rows - 1 - w.rg) / w.step + 1 : 0;
 }
 
-// Row steps: within shared memory 32 bits do.
-template <int RES> struct StepType { using type = long long; };
-template <> struct StepType<1> { using type = int; };
-
-template <typename T, int VEC, int ACT, int RES>
-__global__ void __launch_bounds__(NT, 3)
-k_norm_fwd(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  // (gs[1], mean_s and n_s are read by the cluster's other blocks)
-  __shared__ float gs[2][MAX_KK], mean_s[MAX_KK], n_s;
-  __shared__ float mean_t[MAX_KK], rstd_t[MAX_KK];
-  T* tile = (T*)smem;
-  float* scr = (float*)(smem + (RES ? align_up((size_t)sl.per_max * sl.W * sizeof(T), 16) : 0));
-  const Where<VEC> w = where<VEC>(a, sl);
-  const T* xs = x + w.b * a.xb + w.c0;
-  T* ys = y + w.b * a.yb + w.c0;
-  if (RES) copy_share(tile, xs + (long long)w.t0 * a.xf, a.xf, w.rows, sl.W);
-  zero_tail<VEC, T>(a, sl, w, ys, a.yf);
-  using Step = typename StepType<RES>::type;
-  const T* src = RES ? tile : xs + (long long)w.t0 * a.xf;
-  const Step ld = RES ? sl.W : a.xf, inc = ld * w.step;
-  const int nb = sl.cbv * VEC, cnt = rows_of(w);
-  const float n = (float)w.rows * a.cg;
-  if (threadIdx.x < sl.kk) gs[0][threadIdx.x] = gs[1][threadIdx.x] = 0.f;
-  if (RES) copy_wait();
-  __syncthreads();
-  // One pass over the data: every thread sums its own frames of a channel and
-  // their squares about the first of them (its few frames lose no digits to
-  // that, wherever the mean is).  Then the block's mean, and the squares about
-  // that: q - s^2 / k about the thread's mean, plus k (its mean - mean)^2.
-  float2 fsum[kPairs(VEC)], fsq[kPairs(VEC)];
-#pragma unroll 1
-  for (int half = 0; half < 2; ++half) {
-#pragma unroll 1
-    for (int cb = 0; cb < sl.W; cb += nb) {
-      const int c = cb + w.v * VEC;
-      const bool on = w.active && c < sl.W && cnt > 0;
-      float2 acc[1][kPairs(VEC)] = {};
-      // (a slab of one column block keeps its sums; wider ones read again)
-      if (on && (half == 0 || nb < sl.W)) {
-        const T* p = src + w.rg * ld + c;
-        const Ch<VEC> first = load_ch<VEC, T>(p);
-        float2 m[kPairs(VEC)], s0[kPairs(VEC)] = {}, q0[kPairs(VEC)] = {};
-#pragma unroll
-        for (int i = 0; i < kPairs(VEC); ++i)
-          m[i] = make_float2(-first.v[i].x, -first.v[i].y);
-#pragma unroll 4
-        for (int k = 0; k < cnt; ++k, p += inc) {
-          const Ch<VEC> q = load_ch<VEC, T>(p);
-#pragma unroll
-          for (int i = 0; i < kPairs(VEC); ++i) {
-            const float2 d = __fadd2_rn(q.v[i], m[i]);
-            s0[i] = __fadd2_rn(s0[i], d);
-            q0[i] = __ffma2_rn(d, d, q0[i]);
-          }
-        }
-        const float k = (float)cnt, rk = 1.f / k;
-#pragma unroll
-        for (int i = 0; i < kPairs(VEC); ++i) {
-          const float2 mk = __fmul2_rn(s0[i], make_float2(rk, rk));
-          fsum[i] = __fadd2_rn(mk, first.v[i]);
-          fsq[i] = __ffma2_rn(make_float2(-s0[i].x, -s0[i].y), mk, q0[i]);
-        }
-      }
-      if (on) {
-        const float2 k = make_float2((float)cnt, (float)cnt);
-#pragma unroll
-        for (int i = 0; i < kPairs(VEC); ++i) {
-          if (half == 0) {
-            acc[0][i] = __fmul2_rn(k, fsum[i]);
-          } else {
-            const int ca = c + 2 * i, cz = VEC > 1 ? ca + 1 : ca;
-            const float2 d = __fadd2_rn(fsum[i], make_float2(-mean_s[ca / a.cg_div],
-                                                             -mean_s[cz / a.cg_div]));
-            acc[0][i] = __ffma2_rn(__fmul2_rn(d, d), k, fsq[i]);
-          }
-        }
-      }
-      const float* res =
-          reduce_channels<1, VEC>(sl, acc, scr, w.v, w.rg, w.active && c < sl.W);
-      reduce_groups<1, VEC>(sl, a.cg, cb, res, gs + half, [](int) { return 1.f; });
-    }
-    __syncthreads();
-    if (half == 0) {
-      for (int g = threadIdx.x; g < sl.kk; g += NT) mean_s[g] = w.rows ? gs[0][g] / n : 0.f;
-      if (threadIdx.x == 0) n_s = n;
-      __syncthreads();
-    }
-  }
-  const float* m2_s = gs[1];
-  // the blocks' (n, mean, M2) joined in order
-  if (sl.S > 1) {
-    cluster_arrive();
-    cluster_wait();
-  }
+// The blocks' (n, mean, M2) of a slab, joined in order; st: the cluster's
+// [group] (mean, M2) and n at the same shared addresses of every block.
+__device__ __forceinline__ void join_stats(const NormArgs& a, const Slab& sl, int b, int c0,
+                                           int rank, const float* mean_s, const float* m2_s,
+                                           const float* n_s, float* mean_t, float* rstd_t) {
   for (int g = threadIdx.x; g < sl.kk; g += NT) {
     float nt = 0.f, mt = 0.f, st = 0.f;
     for (int k = 0; k < sl.S; ++k) {
-      const float nk = sl.S > 1 ? peer_f32(&n_s, k) : n_s;
+      const float nk = sl.S > 1 ? peer_f32(n_s, k) : *n_s;
       if (nk == 0.f) continue;
       const float mk = sl.S > 1 ? peer_f32(&mean_s[g], k) : mean_s[g];
       const float sk = sl.S > 1 ? peer_f32(&m2_s[g], k) : m2_s[g];
@@ -422,27 +334,125 @@ k_norm_fwd(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) {
     const float rstd = nt > 0.f ? 1.f / sqrtf(st / nt + a.eps) : 0.f;
     mean_t[g] = mt;
     rstd_t[g] = rstd;
-    if (w.rank == 0) a.stats[(long long)w.b * a.G + w.c0 / a.cg + g] = make_float2(mt, rstd);
+    if (rank == 0) a.stats[(long long)b * a.G + c0 / a.cg_div + g] = make_float2(mt, rstd);
   }
+}
+
+// Sums and squares of a thread's frames of its channels about the first of
+// them (its few frames lose no digits to that, wherever the mean is), then the
+// thread's mean and its squares about that: q - s^2 / k.
+template <int VEC>
+struct Partial {
+  float2 first[kPairs(VEC)], s[kPairs(VEC)], q[kPairs(VEC)];
+  __device__ __forceinline__ void begin(const Ch<VEC>& c) {
+#pragma unroll
+    for (int i = 0; i < kPairs(VEC); ++i) {
+      first[i] = make_float2(-c.v[i].x, -c.v[i].y);
+      s[i] = q[i] = make_float2(0.f, 0.f);
+    }
+  }
+  __device__ __forceinline__ void add(const Ch<VEC>& c) {
+#pragma unroll
+    for (int i = 0; i < kPairs(VEC); ++i) {
+      const float2 d = __fadd2_rn(c.v[i], first[i]);
+      s[i] = __fadd2_rn(s[i], d);
+      q[i] = __ffma2_rn(d, d, q[i]);
+    }
+  }
+  // s: the thread's mean, q: squares about it
+  __device__ __forceinline__ void end(int cnt) {
+    const float rk = __frcp_rn((float)cnt);
+#pragma unroll
+    for (int i = 0; i < kPairs(VEC); ++i) {
+      const float2 mk = __fmul2_rn(s[i], make_float2(rk, rk));
+      q[i] = __ffma2_rn(make_float2(-s[i].x, -s[i].y), mk, q[i]);
+      s[i] = __fadd2_rn(mk, make_float2(-first[i].x, -first[i].y));
+    }
+  }
+  // half 0: the sum; half 1: the squares about the groups' means
+  __device__ __forceinline__ void out(float2 (&acc)[1][kPairs(VEC)], int half, int cnt, int c,
+                                      const float* mean_s, const FastDiv& cg) const {
+    const float2 k = make_float2((float)cnt, (float)cnt);
+#pragma unroll
+    for (int i = 0; i < kPairs(VEC); ++i) {
+      if (half == 0) {
+        acc[0][i] = __fmul2_rn(k, s[i]);
+      } else {
+        const int ca = c + 2 * i, cz = VEC > 1 ? ca + 1 : ca;
+        const float2 d = __fadd2_rn(s[i], make_float2(-mean_s[ca / cg], -mean_s[cz / cg]));
+        acc[0][i] = __ffma2_rn(__fmul2_rn(d, d), k, q[i]);
+      }
+    }
+  }
+};
+
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(NT, 5)
+k_norm_fwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  // (gs[1], mean_s and n_s are read by the cluster's other blocks)
+  __shared__ float gs[2][MAX_KK], mean_s[MAX_KK], n_s;
+  __shared__ float mean_t[MAX_KK], rstd_t[MAX_KK];
+  float* scr = (float*)smem;
+  const int slab = (int)blockIdx.x / sl.S_div;
+  const Where<VEC> w = where<VEC>(a, sl, slab, blockIdx.x - slab * sl.S);
+  const T* src = x + w.b * a.xb + w.c0 + (long long)w.t0 * a.xf;
+  T* ys = y + w.b * a.yb + w.c0;
+  zero_tail<VEC, T>(a, sl, w, ys, a.yf);
+  const long long ld = a.xf, inc = ld * w.step;
+  const int nb = sl.cbv * VEC, cnt = rows_of(w);
+  const float n = (float)w.rows * a.cg;
+  for (int g = threadIdx.x; g < sl.kk; g += NT) gs[0][g] = gs[1][g] = 0.f;
+  __syncthreads();
+  Partial<VEC> st;
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {
+#pragma unroll 1
+    for (int cb = 0; cb < sl.W; cb += nb) {
+      const int c = cb + w.v * VEC;
+      const bool in = w.active && c < sl.W;
+      float2 acc[1][kPairs(VEC)] = {};
+      if (in && cnt > 0) {
+        if (half == 0 || nb < sl.W) {  // (one column block keeps its sums; more read again)
+          const T* p = src + w.rg * ld + c;
+          st.begin(load_ch<VEC, T>(p));
+#pragma unroll 4
+          for (int k = 0; k < cnt; ++k, p += inc) st.add(load_ch<VEC, T>(p));
+          st.end(cnt);
+        }
+        st.out(acc, half, cnt, c, mean_s, a.cg_div);
+      }
+      const float* res = reduce_channels<1, VEC>(sl, acc, scr, w.v, w.rg, in);
+      reduce_groups<1, VEC>(sl, a.cg, cb, res, gs + half, [](int) { return 1.f; });
+    }
+    __syncthreads();
+    if (half == 0) {
+      for (int g = threadIdx.x; g < sl.kk; g += NT) mean_s[g] = w.rows ? gs[0][g] / n : 0.f;
+      if (threadIdx.x == 0) n_s = n;
+      __syncthreads();
+    }
+  }
+  if (sl.S > 1) {
+    cluster_arrive();
+    cluster_wait();
+  }
+  join_stats(a, sl, w.b, w.c0, w.rank, mean_s, gs[1], &n_s, mean_t, rstd_t);
   __syncthreads();
   if (sl.S > 1) cluster_arrive();  // (waited for at the end: peers may still read)
   T* yt = ys + (long long)w.t0 * a.yf;
 #pragma unroll 1
   for (int cb = 0; cb < sl.W; cb += nb) {
     const int c = cb + w.v * VEC;
-    if (!w.active || c >= sl.W) continue;
-    if (cnt == 0) continue;
+    if (cnt == 0 || c >= sl.W) continue;
     float2 m[kPairs(VEC)], s[kPairs(VEC)], be[kPairs(VEC)];
+    load_param<VEC>(s, a.gamma ? a.gamma + w.c0 + c : nullptr, 1.f, false);
+    load_param<VEC>(be, a.beta ? a.beta + w.c0 + c : nullptr, 0.f, false);
 #pragma unroll
     for (int i = 0; i < kPairs(VEC); ++i) {
-      float2 rs, ga;
       const int ca = c + 2 * i, cz = VEC > 1 ? ca + 1 : ca;
       const int gx = ca / a.cg_div, gz = cz / a.cg_div;
       m[i] = make_float2(-mean_t[gx], -mean_t[gz]);
-      rs = make_float2(rstd_t[gx], rstd_t[gz]);
-      ga = a.gamma ? make_float2(a.gamma[w.c0 + ca], a.gamma[w.c0 + cz]) : make_float2(1.f, 1.f);
-      be[i] = a.beta ? make_float2(a.beta[w.c0 + ca], a.beta[w.c0 + cz]) : make_float2(0.f, 0.f);
-      s[i] = __fmul2_rn(rs, ga);
+      s[i] = __fmul2_rn(make_float2(rstd_t[gx], rstd_t[gz]), s[i]);
     }
     const T* p = src + w.rg * ld + c;
     T* o = yt + w.rg * a.yf + c;
@@ -460,102 +470,131 @@ k_norm_fwd(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) {
   if (sl.S > 1) cluster_wait();
 }
 
+// Per-channel constants of the backward and its two uses of a frame:
+// g = dy act'(u) with xh, and dx.
+template <typename T, int VEC, int ACT>
+struct Back {
+  float2 m[kPairs(VEC)], rs[kPairs(VEC)], ga[kPairs(VEC)], be[kPairs(VEC)];
+  __device__ __forceinline__ void stats(const float2* st, int c, const FastDiv& cg) {
+#pragma unroll
+    for (int i = 0; i < kPairs(VEC); ++i) {
+      const int ca = c + 2 * i, cz = VEC > 1 ? ca + 1 : ca;
+      const float2 p = st[ca / cg], q = st[cz / cg];
+      m[i] = make_float2(-p.x, -q.x);
+      rs[i] = make_float2(p.y, q.y);
+    }
+  }
+  __device__ __forceinline__ void g_of(int i, float2 x, float2 dy, float2& xh, float2& g) const {
+    xh = __fmul2_rn(__fadd2_rn(x, m[i]), rs[i]);
+    g = dact2<ACT, T>(dy, __ffma2_rn(xh, ga[i], be[i]));
+  }
+  __device__ __forceinline__ void sums(const Ch<VEC>& x, const Ch<VEC>& dy,
+                                       float2 (&acc)[2][kPairs(VEC)]) const {
+#pragma unroll
+    for (int i = 0; i < kPairs(VEC); ++i) {
+      float2 xh, g;
+      g_of(i, x.v[i], dy.v[i], xh, g);
+      acc[0][i] = __ffma2_rn(g, xh, acc[0][i]);
+      acc[1][i] = __fadd2_rn(acc[1][i], g);
+    }
+  }
+  __device__ __forceinline__ Ch<VEC> dx(const Ch<VEC>& x, const Ch<VEC>& dy,
+                                        const float2 (&k1)[kPairs(VEC)],
+                                        const float2 (&k2)[kPairs(VEC)]) const {
+    Ch<VEC> o;
+#pragma unroll
+    for (int i = 0; i < kPairs(VEC); ++i) {
+      float2 xh, g;
+      g_of(i, x.v[i], dy.v[i], xh, g);
+      o.v[i] = __fmul2_rn(rs[i], __ffma2_rn(xh, k2[i], __ffma2_rn(g, ga[i], k1[i])));
+    }
+    return o;
+  }
+};
+
+// Minus the means of gamma g and gamma g xh for a thread's channels.
+template <int VEC>
+__device__ __forceinline__ void means_of(const float* m1_t, const float* m2_t, int c,
+                                         const FastDiv& cg, float2 (&k1)[kPairs(VEC)],
+                                         float2 (&k2)[kPairs(VEC)]) {
+#pragma unroll
+  for (int i = 0; i < kPairs(VEC); ++i) {
+    const int ca = c + 2 * i, gx = ca / cg, gz = (VEC > 1 ? ca + 1 : ca) / cg;
+    k1[i] = make_float2(-m1_t[gx], -m1_t[gz]);
+    k2[i] = make_float2(-m2_t[gx], -m2_t[gz]);
+  }
+}
+
+// m1, m2 of the slab's groups from the blocks' sums gs[2][MAX_KK], in order.
+__device__ __forceinline__ void join_means(const NormArgs& a, const Slab& sl, int tb,
+                                           const float (*gs)[MAX_KK], float* m1_t, float* m2_t) {
+  const float n = (float)tb * a.cg;
+  for (int g = threadIdx.x; g < sl.kk; g += NT) {
+    float s2 = 0.f, s1 = 0.f;
+    for (int k = 0; k < sl.S; ++k) {
+      s2 += sl.S > 1 ? peer_f32(&gs[0][g], k) : gs[0][g];
+      s1 += sl.S > 1 ? peer_f32(&gs[1][g], k) : gs[1][g];
+    }
+    m1_t[g] = n > 0.f ? s1 / n : 0.f;
+    m2_t[g] = n > 0.f ? s2 / n : 0.f;
+  }
+}
+
 // part: per slab block and channel (sum g xh, sum g), [B][S][C].
-template <typename T, int VEC, int ACT, int RES>
-__global__ void __launch_bounds__(NT, RES ? 3 : 2)
-k_norm_bwd(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict__ dy,
-           T* __restrict__ dx, float2* __restrict__ part) {
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(NT, 5)
+k_norm_bwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict__ dy,
+                  T* __restrict__ dx, float2* __restrict__ part) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float gs[2][MAX_KK];  // read by the cluster's other blocks
   __shared__ float m1_t[MAX_KK], m2_t[MAX_KK];
-  const size_t tb = RES ? align_up((size_t)sl.per_max * sl.W * sizeof(T), 16) : 0;
-  T *tx = (T*)smem, *td = (T*)(smem + tb);
-  float* scr = (float*)(smem + 2 * tb);
-  const Where<VEC> w = where<VEC>(a, sl);
+  float* scr = (float*)smem;
+  const int slab = (int)blockIdx.x / sl.S_div;
+  const Where<VEC> w = where<VEC>(a, sl, slab, blockIdx.x - slab * sl.S);
   const T* xs = x + w.b * a.xb + w.c0 + (long long)w.t0 * a.xf;
   const T* ds = dy + w.b * a.yb + w.c0 + (long long)w.t0 * a.yf;
   T* os = dx + w.b * a.xb + w.c0;
-  if (RES) {
-    copy_share(tx, xs, a.xf, w.rows, sl.W);
-    copy_share(td, ds, a.yf, w.rows, sl.W);
-  }
   zero_tail<VEC, T>(a, sl, w, os, a.xf);
   os += (long long)w.t0 * a.xf;
-  const T *sx = RES ? tx : xs, *sd = RES ? td : ds;
-  using Step = typename StepType<RES>::type;
-  const Step lx = RES ? sl.W : a.xf, ldy = RES ? sl.W : a.yf;
-  const Step xinc = lx * w.step, dinc = ldy * w.step;
+  const long long xinc = a.xf * w.step, dinc = a.yf * w.step;
   const int nb = sl.cbv * VEC, cnt = rows_of(w);
-  const float2* stats = a.stats + (long long)w.b * a.G + w.c0 / a.cg;
+  const float2* stats = a.stats + (long long)w.b * a.G + w.c0 / a.cg_div;
   for (int g = threadIdx.x; g < sl.kk; g += NT) gs[0][g] = gs[1][g] = 0.f;
-  if (RES) copy_wait();
   __syncthreads();
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
     for (int cb = 0; cb < sl.W; cb += nb) {
       const int c = cb + w.v * VEC;
-      const bool on = w.active && c < sl.W;
-      float2 m[kPairs(VEC)], rs[kPairs(VEC)], ga[kPairs(VEC)], be[kPairs(VEC)];
-      if (on) {
-#pragma unroll
-        for (int i = 0; i < kPairs(VEC); ++i) {
-          const int ca = c + 2 * i, cz = VEC > 1 ? ca + 1 : ca;
-          const float2 p = stats[ca / a.cg_div], q = stats[cz / a.cg_div];
-          m[i] = make_float2(-p.x, -q.x);
-          rs[i] = make_float2(p.y, q.y);
-          ga[i] = a.gamma ? make_float2(a.gamma[w.c0 + ca], a.gamma[w.c0 + cz])
-                          : make_float2(1.f, 1.f);
-          be[i] = a.beta ? make_float2(a.beta[w.c0 + ca], a.beta[w.c0 + cz])
-                         : make_float2(0.f, 0.f);
-        }
+      const bool in = w.active && c < sl.W;
+      Back<T, VEC, ACT> bk;
+      if (in) {
+        bk.stats(stats, c, a.cg_div);
+        load_param<VEC>(bk.ga, a.gamma ? a.gamma + w.c0 + c : nullptr, 1.f, false);
+        load_param<VEC>(bk.be, a.beta ? a.beta + w.c0 + c : nullptr, 0.f, false);
       }
+      const T *px = xs + w.rg * a.xf + c, *pd = ds + w.rg * a.yf + c;
       if (pass == 0) {
         float2 acc[2][kPairs(VEC)] = {};
-        if (on) {
-          const T *px = sx + w.rg * lx + c, *pd = sd + w.rg * ldy + c;
+        if (in) {
 #pragma unroll 2
-          for (int k = 0; k < cnt; ++k, px += xinc, pd += dinc) {
-            const Ch<VEC> q = load_ch<VEC, T>(px), d = load_ch<VEC, T>(pd);
-#pragma unroll
-            for (int i = 0; i < kPairs(VEC); ++i) {
-              const float2 xh = __fmul2_rn(__fadd2_rn(q.v[i], m[i]), rs[i]);
-              const float2 g = dact2<ACT, T>(d.v[i], __ffma2_rn(xh, ga[i], be[i]));
-              acc[0][i] = __ffma2_rn(g, xh, acc[0][i]);
-              acc[1][i] = __fadd2_rn(acc[1][i], g);
-            }
-          }
+          for (int k = 0; k < cnt; ++k, px += xinc, pd += dinc)
+            bk.sums(load_ch<VEC, T>(px), load_ch<VEC, T>(pd), acc);
         }
-        const float* res = reduce_channels<2, VEC>(sl, acc, scr, w.v, w.rg, on);
+        const float* res = reduce_channels<2, VEC>(sl, acc, scr, w.v, w.rg, in);
         for (int k = threadIdx.x; k < nb && cb + k < sl.W; k += NT)
           part[((long long)w.b * sl.S + w.rank) * a.C + w.c0 + cb + k] =
               make_float2(res[k], res[nb + k]);
         reduce_groups<2, VEC>(sl, a.cg, cb, res, gs, [&](int ch) {
           return a.gamma ? a.gamma[w.c0 + ch] : 1.f;
         });
-      } else if (on) {
+      } else if (in) {
         float2 k1[kPairs(VEC)], k2[kPairs(VEC)];
-#pragma unroll
-        for (int i = 0; i < kPairs(VEC); ++i) {
-          const int ca = c + 2 * i, gx = ca / a.cg_div, gz = (VEC > 1 ? ca + 1 : ca) / a.cg_div;
-          k1[i] = make_float2(-m1_t[gx], -m1_t[gz]);
-          k2[i] = make_float2(-m2_t[gx], -m2_t[gz]);
-        }
-        const T *px = sx + w.rg * lx + c, *pd = sd + w.rg * ldy + c;
+        means_of<VEC>(m1_t, m2_t, c, a.cg_div, k1, k2);
         T* po = os + w.rg * a.xf + c;
-        const long long oinc = w.step * a.xf;
 #pragma unroll 2
-        for (int k = 0; k < cnt; ++k, px += xinc, pd += dinc, po += oinc) {
-          const Ch<VEC> q = load_ch<VEC, T>(px), d = load_ch<VEC, T>(pd);
-          Ch<VEC> o;
-#pragma unroll
-          for (int i = 0; i < kPairs(VEC); ++i) {
-            const float2 xh = __fmul2_rn(__fadd2_rn(q.v[i], m[i]), rs[i]);
-            const float2 g = dact2<ACT, T>(d.v[i], __ffma2_rn(xh, ga[i], be[i]));
-            o.v[i] = __fmul2_rn(rs[i], __ffma2_rn(xh, k2[i], __ffma2_rn(g, ga[i], k1[i])));
-          }
-          store_ch<VEC, T>(po, o);
-        }
+        for (int k = 0; k < cnt; ++k, px += xinc, pd += dinc, po += xinc)
+          store_ch<VEC, T>(po, bk.dx(load_ch<VEC, T>(px), load_ch<VEC, T>(pd), k1, k2));
       }
     }
     if (pass) break;
@@ -564,21 +603,281 @@ k_norm_bwd(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict__ d
       cluster_arrive();
       cluster_wait();
     }
-    const float n = (float)w.tb * a.cg;
-    for (int g = threadIdx.x; g < sl.kk; g += NT) {
-      float s2 = 0.f, s1 = 0.f;
-      for (int k = 0; k < sl.S; ++k) {
-        s2 += sl.S > 1 ? peer_f32(&gs[0][g], k) : gs[0][g];
-        s1 += sl.S > 1 ? peer_f32(&gs[1][g], k) : gs[1][g];
-      }
-      m1_t[g] = n > 0.f ? s1 / n : 0.f;
-      m2_t[g] = n > 0.f ? s2 / n : 0.f;
-    }
+    join_means(a, sl, w.tb, gs, m1_t, m2_t);
     __syncthreads();
     if (sl.S > 1) cluster_arrive();  // (waited for at the end: peers may still read)
   }
   __syncwarp();
   if (sl.S > 1) cluster_wait();
+}
+
+// ---- resident kernels -------------------------------------------------------------
+// A block walks slabs.  A thread owns one 16-byte column of its block's share,
+// every step-th frame, and is the only reader of its shared-memory slots: it
+// waits for its own copies alone, and as soon as the last pass has read a slot
+// it copies the next slab's frame into it.  So the loads of the next slab run
+// under the last pass of this one, with no barrier between them, and the blocks
+// of an SM (three at the 64 KB share) overlap one's reductions with another's
+// passes.
+template <typename T>
+constexpr int kVec16 = 16 / (int)sizeof(T);
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+constexpr int SLOT = NT * 16;  // bytes from one of a thread's slots to its next
+
+template <typename T, int ACT>
+__global__ void __launch_bounds__(NT, 4)
+k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) {
+  constexpr int VEC = kVec16<T>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  // (read by the cluster's other blocks: one set per parity of the slab count,
+  // so that one barrier a slab keeps writers off what peers still read)
+  __shared__ float mean_s[2][MAX_KK], m2_s[2][MAX_KK], n_s[2];
+  __shared__ float gs[1][MAX_KK], mean_t[MAX_KK], rstd_t[MAX_KK];
+  float* scr = (float*)(smem + (size_t)sl.slots * SLOT);
+  const unsigned char* mine = smem + threadIdx.x * 16;
+  const uint32_t mine_a = ptx::smem_u32(mine);
+  const int first = (int)blockIdx.x / sl.S_div, rank = blockIdx.x - first * sl.S;
+  const int stride = (int)gridDim.x / sl.S_div;
+  const bool al16 = (((uintptr_t)a.gamma | (uintptr_t)a.beta) & 15) == 0;
+  Where<VEC> w = where<VEC>(a, sl, first, rank);
+  const int c = w.v * VEC;
+  int cnt = rows_of(w);
+  const long long xinc = a.xf * w.step, yinc = a.yf * w.step;
+  {
+    const T* p = x + w.b * a.xb + w.c0 + (long long)(w.t0 + w.rg) * a.xf + c;
+    for (int k = 0; k < cnt; ++k, p += xinc) copy16(mine_a + k * SLOT, p);
+    copy_commit();
+    copy_commit();
+  }
+  int ready = cnt;  // slots of the first of the two copy groups
+  int par = 0;
+#pragma unroll 1
+  for (int slab = first; slab < sl.nslabs; slab += stride, par ^= 1) {
+    const bool more = slab + stride < sl.nslabs;
+    Where<VEC> nx = w;
+    int ncnt = 0;
+    if (more) {
+      nx = where<VEC>(a, sl, slab + stride, rank);
+      ncnt = rows_of(nx);
+    }
+    T* ys = y + w.b * a.yb + w.c0;
+    float2 s[kPairs(VEC)], be[kPairs(VEC)], m[kPairs(VEC)];
+    if (w.active) {
+      load_param<VEC>(s, a.gamma ? a.gamma + w.c0 + c : nullptr, 1.f, al16);
+      load_param<VEC>(be, a.beta ? a.beta + w.c0 + c : nullptr, 0.f, al16);
+    }
+    zero_tail<VEC, T>(a, sl, w, ys, a.yf);
+    const float n = (float)w.rows * a.cg;
+    Partial<VEC> st;
+    copy_wait<1>();
+    if (cnt > 0) {
+      if (ready == 0) copy_wait<0>();
+      st.begin(load_ch<VEC, T>((const T*)mine));
+#pragma unroll 4
+      for (int k = 0; k < ready; ++k) st.add(load_ch<VEC, T>((const T*)(mine + k * SLOT)));
+      copy_wait<0>();
+#pragma unroll 4
+      for (int k = ready; k < cnt; ++k) st.add(load_ch<VEC, T>((const T*)(mine + k * SLOT)));
+      st.end(cnt);
+    }
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      float2 acc[1][kPairs(VEC)] = {};
+      if (cnt > 0) st.out(acc, half, cnt, c, mean_s[par], a.cg_div);
+      for (int g = threadIdx.x; g < sl.kk; g += NT) gs[0][g] = 0.f;
+      const float* res = reduce_channels<1, VEC>(sl, acc, scr, w.v, w.rg, w.active);
+      reduce_groups<1, VEC>(sl, a.cg, 0, res, gs, [](int) { return 1.f; });
+      __syncthreads();
+      for (int g = threadIdx.x; g < sl.kk; g += NT) {
+        if (half == 0) mean_s[par][g] = w.rows ? gs[0][g] / n : 0.f;
+        else m2_s[par][g] = gs[0][g];
+      }
+      if (threadIdx.x == 0) n_s[par] = n;
+      __syncthreads();
+    }
+    if (sl.S > 1) {
+      cluster_arrive();
+      cluster_wait();
+    }
+    join_stats(a, sl, w.b, w.c0, rank, mean_s[par], m2_s[par], &n_s[par], mean_t, rstd_t);
+    __syncthreads();
+    // last pass: write y, copy the next slab into the slots it has read
+    if (w.active) {
+#pragma unroll
+      for (int i = 0; i < kPairs(VEC); ++i) {
+        const int ca = c + 2 * i, gx = ca / a.cg_div, gz = (ca + 1) / a.cg_div;
+        m[i] = make_float2(-mean_t[gx], -mean_t[gz]);
+        s[i] = __fmul2_rn(make_float2(rstd_t[gx], rstd_t[gz]), s[i]);
+      }
+    }
+    T* o = ys + (long long)(w.t0 + w.rg) * a.yf + c;
+    const T* p = x + nx.b * a.xb + nx.c0 + (long long)(nx.t0 + nx.rg) * a.xf + c;
+    const int both = min(cnt, ncnt), head = both / 2;
+    auto apply = [&](int k) {
+      Ch<VEC> q = load_ch<VEC, T>((const T*)(mine + k * SLOT));
+#pragma unroll
+      for (int i = 0; i < kPairs(VEC); ++i)
+        q.v[i] = act2<ACT, T>(__ffma2_rn(__fadd2_rn(q.v[i], m[i]), s[i], be[i]));
+      store_ch<VEC, T>(o, q);
+      o += yinc;
+    };
+    auto fetch = [&](int k) {
+      copy16(mine_a + k * SLOT, p);
+      p += xinc;
+    };
+    int k = 0;
+#pragma unroll 2
+    for (; k < head; ++k) {
+      apply(k);
+      fetch(k);
+    }
+    copy_commit();
+#pragma unroll 2
+    for (; k < both; ++k) {
+      apply(k);
+      fetch(k);
+    }
+    for (int j = k; j < ncnt; ++j) fetch(j);
+    copy_commit();
+#pragma unroll 2
+    for (int j = k; j < cnt; ++j) apply(j);
+    w = nx;
+    cnt = ncnt;
+    ready = head;
+  }
+  __syncwarp();
+  if (sl.S > 1) {  // peers may still read this block's statistics
+    cluster_arrive();
+    cluster_wait();
+  }
+}
+
+template <typename T, int ACT>
+__global__ void __launch_bounds__(NT, 4)
+k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict__ dy,
+               T* __restrict__ dx, float2* __restrict__ part) {
+  constexpr int VEC = kVec16<T>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float gs[2][2][MAX_KK];  // by parity; read by the cluster's other blocks
+  __shared__ float m1_t[MAX_KK], m2_t[MAX_KK];
+  const int half_bytes = sl.slots * SLOT;
+  float* scr = (float*)(smem + 2 * (size_t)half_bytes);
+  const unsigned char* mine = smem + threadIdx.x * 16;
+  const uint32_t mine_a = ptx::smem_u32(mine);
+  const int first = (int)blockIdx.x / sl.S_div, rank = blockIdx.x - first * sl.S;
+  const int stride = (int)gridDim.x / sl.S_div;
+  const bool al16 = (((uintptr_t)a.gamma | (uintptr_t)a.beta) & 15) == 0;
+  Where<VEC> w = where<VEC>(a, sl, first, rank);
+  const int c = w.v * VEC;
+  int cnt = rows_of(w);
+  const long long xinc = a.xf * w.step, dinc = a.yf * w.step;
+  {
+    const T* p = x + w.b * a.xb + w.c0 + (long long)(w.t0 + w.rg) * a.xf + c;
+    const T* d = dy + w.b * a.yb + w.c0 + (long long)(w.t0 + w.rg) * a.yf + c;
+    for (int k = 0; k < cnt; ++k, p += xinc, d += dinc) {
+      copy16(mine_a + k * SLOT, p);
+      copy16(mine_a + half_bytes + k * SLOT, d);
+    }
+    copy_commit();
+    copy_commit();
+  }
+  int ready = cnt, par = 0;
+#pragma unroll 1
+  for (int slab = first; slab < sl.nslabs; slab += stride, par ^= 1) {
+    const bool more = slab + stride < sl.nslabs;
+    Where<VEC> nx = w;
+    int ncnt = 0;
+    if (more) {
+      nx = where<VEC>(a, sl, slab + stride, rank);
+      ncnt = rows_of(nx);
+    }
+    T* os = dx + w.b * a.xb + w.c0;
+    Back<T, VEC, ACT> bk;
+    if (w.active) {
+      bk.stats(a.stats + (long long)w.b * a.G + w.c0 / a.cg_div, c, a.cg_div);
+      load_param<VEC>(bk.ga, a.gamma ? a.gamma + w.c0 + c : nullptr, 1.f, al16);
+      load_param<VEC>(bk.be, a.beta ? a.beta + w.c0 + c : nullptr, 0.f, al16);
+    }
+    zero_tail<VEC, T>(a, sl, w, os, a.xf);
+    float2 acc[2][kPairs(VEC)] = {};
+    auto sums = [&](int k) {
+      bk.sums(load_ch<VEC, T>((const T*)(mine + k * SLOT)),
+              load_ch<VEC, T>((const T*)(mine + half_bytes + k * SLOT)), acc);
+    };
+    copy_wait<1>();
+#pragma unroll 2
+    for (int k = 0; k < ready; ++k) sums(k);
+    copy_wait<0>();
+#pragma unroll 2
+    for (int k = ready; k < cnt; ++k) sums(k);
+    for (int g = threadIdx.x; g < sl.kk; g += NT) gs[par][0][g] = gs[par][1][g] = 0.f;
+    const float* res = reduce_channels<2, VEC>(sl, acc, scr, w.v, w.rg, w.active);
+    for (int k = threadIdx.x; k < sl.W; k += NT)
+      part[((long long)w.b * sl.S + rank) * a.C + w.c0 + k] = make_float2(res[k], res[sl.W + k]);
+    reduce_groups<2, VEC>(sl, a.cg, 0, res, gs[par], [&](int ch) {
+      return a.gamma ? a.gamma[w.c0 + ch] : 1.f;
+    });
+    __syncthreads();
+    if (sl.S > 1) {
+      cluster_arrive();
+      cluster_wait();
+    }
+    join_means(a, sl, w.tb, gs[par], m1_t, m2_t);
+    __syncthreads();
+    float2 k1[kPairs(VEC)], k2[kPairs(VEC)];
+    if (w.active) means_of<VEC>(m1_t, m2_t, c, a.cg_div, k1, k2);
+    T* o = os + (long long)(w.t0 + w.rg) * a.xf + c;
+    const T* p = x + nx.b * a.xb + nx.c0 + (long long)(nx.t0 + nx.rg) * a.xf + c;
+    const T* d = dy + nx.b * a.yb + nx.c0 + (long long)(nx.t0 + nx.rg) * a.yf + c;
+    const int both = min(cnt, ncnt), head = both / 2;
+    auto apply = [&](int k) {
+      store_ch<VEC, T>(o, bk.dx(load_ch<VEC, T>((const T*)(mine + k * SLOT)),
+                                load_ch<VEC, T>((const T*)(mine + half_bytes + k * SLOT)), k1,
+                                k2));
+      o += xinc;
+    };
+    auto fetch = [&](int k) {
+      copy16(mine_a + k * SLOT, p);
+      copy16(mine_a + half_bytes + k * SLOT, d);
+      p += xinc;
+      d += dinc;
+    };
+    int k = 0;
+#pragma unroll 1
+    for (; k < head; ++k) {
+      apply(k);
+      fetch(k);
+    }
+    copy_commit();
+#pragma unroll 1
+    for (; k < both; ++k) {
+      apply(k);
+      fetch(k);
+    }
+    for (int j = k; j < ncnt; ++j) fetch(j);
+    copy_commit();
+#pragma unroll 1
+    for (int j = k; j < cnt; ++j) apply(j);
+    w = nx;
+    cnt = ncnt;
+    ready = head;
+  }
+  __syncwarp();
+  if (sl.S > 1) {  // peers may still read this block's sums
+    cluster_arrive();
+    cluster_wait();
+  }
 }
 
 // dgamma, dbeta: the column sums of part [rows][C], 32 channels a cluster, a
@@ -659,15 +958,16 @@ rnnt_status norm_check(const rnnt_norm_dims* d, NormArgs* a, const void* x, cons
 struct NormCut {
   Slab sl;
   int vec, res;
+  int grid;
   size_t smem;
 };
 
 NormCut norm_cut(const NormArgs& a, int e, int tiles, bool aligned) {
   NormCut n{};
-  n.vec = 0;
   // the fewest whole groups that make 64-byte pieces of a frame (16-byte
   // aligned ones); short of that, 32 channels of any alignment
   int kk = 0;
+  n.vec = 1;
   if (aligned)
     for (int k = 1; k <= a.G && k <= MAX_KK; ++k)
       if (a.G % k == 0 && (long long)k * a.cg * e % 16 == 0) {
@@ -675,23 +975,29 @@ NormCut norm_cut(const NormArgs& a, int e, int tiles, bool aligned) {
         n.vec = 4;
         if (k * a.cg * e >= 64) break;
       }
-  if (!kk) {
-    n.vec = 1;
+  if (!kk)
     for (int k = 1; k <= a.G && k <= MAX_KK; ++k)
       if (a.G % k == 0) {
         kk = k;
         if (k * a.cg >= 32) break;
       }
-  }
   Slab& s = n.sl;
   s.kk = kk;
   s.W = kk * a.cg;
-  const long long frame = (long long)s.W * e * tiles, slabs = (long long)a.B * (a.G / kk);
+  s.nslabs = a.B * (a.G / kk);
+  const long long frame = (long long)s.W * e * tiles;
   s.S = 1;
   while (s.S < 8 && cdiv(a.T, s.S) * frame > SHARE) s.S *= 2;
   // few slabs: shares of at least 64 frames, until there are two blocks an SM
-  while (s.S < 8 && slabs * s.S < 2 * 152 && a.T >= 128 * s.S) s.S *= 2;
+  while (s.S < 8 && (long long)s.nslabs * s.S < 2 * 152 && a.T >= 128 * s.S) s.S *= 2;
   s.per_max = (int)cdiv(a.T, s.S);
+  // resident: a thread per 16-byte column, slots within the block's share
+  const int cols16 = s.W * e / 16;
+  if (n.vec == 4 && cols16 <= NT) {
+    s.slots = (int)cdiv(s.per_max, NT / cols16);
+    n.res = (size_t)s.slots * SLOT * tiles <= SHARE_MAX;
+  }
+  if (n.res) n.vec = 16 / e;
   const int vr = s.W / n.vec;
   s.cbv = vr < NT ? vr : NT;
   s.pow2 = s.cbv <= 32 && (s.cbv & (s.cbv - 1)) == 0;
@@ -700,9 +1006,12 @@ NormCut norm_cut(const NormArgs& a, int e, int tiles, bool aligned) {
   s.per_sample_div = fast_div(a.G / kk);
   s.S_div = fast_div(s.S);
   s.cbv_div = fast_div(s.cbv);
-  const size_t tile = align_up((size_t)s.per_max * s.W * e, 16) * tiles;
-  n.res = n.vec == 4 && tile <= SHARE_MAX;
-  n.smem = (n.res ? tile : 0) + (size_t)s.scratch * tiles;
+  n.smem = (n.res ? (size_t)s.slots * SLOT * tiles : 0) + (size_t)s.scratch * tiles;
+  n.grid = s.nslabs * s.S;
+  if (n.res) {  // as many blocks as the SMs hold (228 KB each, at most 4 by registers)
+    const int per_sm = (int)std::min<size_t>(4, (228 * 1024) / (n.smem + 4 * 1024));
+    n.grid = std::min(s.nslabs, std::max(1, per_sm * num_sms() / s.S)) * s.S;
+  }
   return n;
 }
 
@@ -730,32 +1039,35 @@ cudaError_t opt_in(K k, std::atomic<bool>* done) {
   std::atomic<bool>& d = done[device_slot()];
   if (d.load()) return cudaSuccess;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             SHARE_MAX + 16 * 1024);
+                                             SHARE_MAX + 20 * 1024);
   if (e == cudaSuccess) d.store(true);
   return e;
 }
 
-template <typename T, int VEC, int ACT, int RES>
-cudaError_t norm_launch(const NormArgs& a, const NormCut& n, const void* x, const void* dy,
+// dy NULL: the forward kernel, else the backward.
+template <typename T, typename KF, typename KB>
+cudaError_t norm_launch(KF kf, KB kb, std::atomic<bool>* fdone, std::atomic<bool>* bdone,
+                        const NormArgs& a, const NormCut& n, const void* x, const void* dy,
                         void* out, float2* part, cudaStream_t st) {
-  static std::atomic<bool> f[kDeviceSlots], b[kDeviceSlots];
-  const unsigned grid = (unsigned)((long long)a.B * (a.G / n.sl.kk) * n.sl.S);
-  cudaError_t e = dy ? opt_in(k_norm_bwd<T, VEC, ACT, RES>, b)
-                     : opt_in(k_norm_fwd<T, VEC, ACT, RES>, f);
+  const cudaError_t e = dy ? opt_in(kb, bdone) : opt_in(kf, fdone);
   if (e != cudaSuccess) return e;
-  if (dy)
-    return launch_cluster(k_norm_bwd<T, VEC, ACT, RES>, grid, n.sl.S, n.smem, st, a, n.sl,
-                          (const T*)x, (const T*)dy, (T*)out, part);
-  return launch_cluster(k_norm_fwd<T, VEC, ACT, RES>, grid, n.sl.S, n.smem, st, a, n.sl,
-                        (const T*)x, (T*)out);
+  return dy ? launch_cluster(kb, n.grid, n.sl.S, n.smem, st, a, n.sl, (const T*)x, (const T*)dy,
+                             (T*)out, part)
+            : launch_cluster(kf, n.grid, n.sl.S, n.smem, st, a, n.sl, (const T*)x, (T*)out);
 }
 
 template <typename T, int ACT>
 cudaError_t norm_launch_cut(const NormArgs& a, const NormCut& n, const void* x, const void* dy,
                             void* out, float2* part, cudaStream_t st) {
-  if (n.res) return norm_launch<T, 4, ACT, 1>(a, n, x, dy, out, part, st);
-  if (n.vec == 4) return norm_launch<T, 4, ACT, 0>(a, n, x, dy, out, part, st);
-  return norm_launch<T, 1, ACT, 0>(a, n, x, dy, out, part, st);
+  static std::atomic<bool> done[6][kDeviceSlots];
+  if (n.res)
+    return norm_launch<T>(k_norm_fwd_res<T, ACT>, k_norm_bwd_res<T, ACT>, done[0], done[1], a, n,
+                          x, dy, out, part, st);
+  if (n.vec == 4)
+    return norm_launch<T>(k_norm_fwd_stream<T, 4, ACT>, k_norm_bwd_stream<T, 4, ACT>, done[2],
+                          done[3], a, n, x, dy, out, part, st);
+  return norm_launch<T>(k_norm_fwd_stream<T, 1, ACT>, k_norm_bwd_stream<T, 1, ACT>, done[4],
+                        done[5], a, n, x, dy, out, part, st);
 }
 
 // dy NULL: forward, x -> out = y; else backward, (x, dy) -> out = dx and part.
