@@ -2,6 +2,7 @@
 // last (include/rnnt_ops.h).
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "ops.h"
 #include "ptx.cuh"
@@ -36,9 +37,10 @@ struct NormArgs {
   int32_t* status;
 };
 
-__device__ __forceinline__ int frames_of(const NormArgs& a, int b) {
-  if (!a.T_len) return a.T;
-  const int t = __ldg(a.T_len + b);
+__device__ __forceinline__ int length_of(const NormArgs& a, int b) {
+  return a.T_len ? __ldg(a.T_len + b) : a.T;
+}
+__device__ __forceinline__ int frames_of(const NormArgs& a, int t) {
   if (t < 0 || t > a.T) {
     report(a.status, RNNT_ERR_LENGTH_RANGE);
     return 0;
@@ -176,6 +178,9 @@ struct Slab {
   int cbv;           // vectors of a column block (all VEC-wide columns of W, at most NT)
   int pow2;          // cbv is a power of two <= 32: columns meet by shuffles first
   int nslabs;
+  int uni;           // a thread's channels are of one group (and pow2): GroupSum applies
+  int lanes;         // lane bits that share a group (uni)
+  int keep;          // a block's slabs have the same channels
   int scratch;       // scratch bytes per reduced quantity
   FastDiv per_sample_div, S_div, cbv_div;
 };
@@ -274,12 +279,13 @@ struct Where {
   bool active;
 };
 template <int VEC>
-__device__ __forceinline__ Where<VEC> where(const NormArgs& a, const Slab& sl, int slab, int rank) {
+__device__ __forceinline__ Where<VEC> where(const NormArgs& a, const Slab& sl, int slab, int rank,
+                                            int length) {
   Where<VEC> w;
   w.rank = rank;
   w.b = slab / sl.per_sample_div;
   w.c0 = (slab - w.b * (int)sl.per_sample_div.d) * sl.W;
-  w.tb = frames_of(a, w.b);
+  w.tb = frames_of(a, length);
   const int per = (w.tb + sl.S - 1) / sl.S_div;
   w.t0 = min(w.tb, w.rank * per);
   w.rows = min(w.tb, w.t0 + per) - w.t0;
@@ -395,7 +401,8 @@ k_norm_fwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ 
   __shared__ float mean_t[MAX_KK], rstd_t[MAX_KK];
   float* scr = (float*)smem;
   const int slab = (int)blockIdx.x / sl.S_div;
-  const Where<VEC> w = where<VEC>(a, sl, slab, blockIdx.x - slab * sl.S);
+  const Where<VEC> w = where<VEC>(a, sl, slab, blockIdx.x - slab * sl.S,
+                                  length_of(a, slab / sl.per_sample_div));
   const T* src = x + w.b * a.xb + w.c0 + (long long)w.t0 * a.xf;
   T* ys = y + w.b * a.yb + w.c0;
   zero_tail<VEC, T>(a, sl, w, ys, a.yf);
@@ -550,7 +557,8 @@ k_norm_bwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restr
   __shared__ float m1_t[MAX_KK], m2_t[MAX_KK];
   float* scr = (float*)smem;
   const int slab = (int)blockIdx.x / sl.S_div;
-  const Where<VEC> w = where<VEC>(a, sl, slab, blockIdx.x - slab * sl.S);
+  const Where<VEC> w = where<VEC>(a, sl, slab, blockIdx.x - slab * sl.S,
+                                  length_of(a, slab / sl.per_sample_div));
   const T* xs = x + w.b * a.xb + w.c0 + (long long)w.t0 * a.xf;
   const T* ds = dy + w.b * a.yb + w.c0 + (long long)w.t0 * a.yf;
   T* os = dx + w.b * a.xb + w.c0;
@@ -611,6 +619,21 @@ k_norm_bwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restr
   if (sl.S > 1) cluster_wait();
 }
 
+// Sum of one value per thread over the block's threads of the same group, for
+// slabs whose threads hold channels of one group each: shuffles over the lane
+// bits in sl.lanes, then the warps' sums from buf[group][warp] in order.
+__device__ __forceinline__ float group_lanes(float v, int lanes) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+    if (lanes & o) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float group_warps(const float (*buf)[NWARPS], int g) {
+  static_assert(NWARPS == 4, "one 16-byte read");
+  const float4 q = *(const float4*)buf[g];
+  return ((q.x + q.y) + q.z) + q.w;
+}
+
 // ---- resident kernels -------------------------------------------------------------
 // A block walks slabs.  A thread owns one 16-byte column of its block's share,
 // every step-th frame, and is the only reader of its shared-memory slots: it
@@ -635,23 +658,61 @@ __device__ __forceinline__ void copy_wait() {
 
 constexpr int SLOT = NT * 16;  // bytes from one of a thread's slots to its next
 
-template <typename T, int ACT>
-__global__ void __launch_bounds__(NT, 4)
+// The last pass over `cnt` slots, with the next slab's `ncnt` frames copied into
+// the slots behind it, in two copy groups.  Returns the slots of the first.
+// (Two frames at a time: the copies order memory, so a frame's loads would not
+// start before the one ahead has stored.)
+template <typename A, typename F>
+__device__ __forceinline__ int turn_over(int cnt, int ncnt, A apply, F fetch) {
+  using Two = std::integral_constant<int, 2>;
+  using One = std::integral_constant<int, 1>;
+  const int both = min(cnt, ncnt) & ~1, head = (both / 2) & ~1;
+  int k = 0;
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {
+    const int end = part ? both : head;
+#pragma unroll 1
+    for (; k < end; k += 2) {
+      apply(k, Two{});
+      fetch(k);
+      fetch(k + 1);
+    }
+    if (part == 0) copy_commit();
+  }
+  // what only one of the two slabs has; a frame is copied in once its slot is read
+  const int done = k;
+#pragma unroll 1
+  for (; k + 2 <= cnt; k += 2) apply(k, Two{});
+  if (k < cnt) apply(k, One{});
+  for (k = done; k < ncnt; ++k) fetch(k);
+  copy_commit();
+  return head;
+}
+
+// Length of the block's slab after next, asked for one slab ahead of its use.
+__device__ __forceinline__ int length_ahead(const NormArgs& a, const Slab& sl, int slab) {
+  return slab < sl.nslabs ? length_of(a, slab / sl.per_sample_div) : 0;
+}
+
+template <typename T, int ACT, int UNI>
+__global__ void __launch_bounds__(NT, 3)
 k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) {
-  constexpr int VEC = kVec16<T>;
+  constexpr int VEC = kVec16<T>, NP = kPairs(VEC);
   extern __shared__ __align__(16) unsigned char smem[];
   // (read by the cluster's other blocks: one set per parity of the slab count,
   // so that one barrier a slab keeps writers off what peers still read)
   __shared__ float mean_s[2][MAX_KK], m2_s[2][MAX_KK], n_s[2];
   __shared__ float gs[1][MAX_KK], mean_t[MAX_KK], rstd_t[MAX_KK];
+  __shared__ __align__(16) float buf[2][UNI ? 32 : 1][NWARPS];
   float* scr = (float*)(smem + (size_t)sl.slots * SLOT);
   const unsigned char* mine = smem + threadIdx.x * 16;
   const uint32_t mine_a = ptx::smem_u32(mine);
   const int first = (int)blockIdx.x / sl.S_div, rank = blockIdx.x - first * sl.S;
-  const int stride = (int)gridDim.x / sl.S_div;
+  const int stride = (int)gridDim.x / sl.S_div, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool al16 = (((uintptr_t)a.gamma | (uintptr_t)a.beta) & 15) == 0;
-  Where<VEC> w = where<VEC>(a, sl, first, rank);
-  const int c = w.v * VEC;
+  Where<VEC> w = where<VEC>(a, sl, first, rank, length_of(a, first / sl.per_sample_div));
+  int ahead = length_ahead(a, sl, first + stride);
+  const int c = w.v * VEC, myg = c / a.cg_div;
   int cnt = rows_of(w);
   const long long xinc = a.xf * w.step, yinc = a.yf * w.step;
   {
@@ -668,11 +729,12 @@ k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) 
     Where<VEC> nx = w;
     int ncnt = 0;
     if (more) {
-      nx = where<VEC>(a, sl, slab + stride, rank);
+      nx = where<VEC>(a, sl, slab + stride, rank, ahead);
       ncnt = rows_of(nx);
     }
+    ahead = length_ahead(a, sl, slab + 2 * stride);
     T* ys = y + w.b * a.yb + w.c0;
-    float2 s[kPairs(VEC)], be[kPairs(VEC)], m[kPairs(VEC)];
+    float2 s[NP], be[NP], m[NP];
     if (w.active) {
       load_param<VEC>(s, a.gamma ? a.gamma + w.c0 + c : nullptr, 1.f, al16);
       load_param<VEC>(be, a.beta ? a.beta + w.c0 + c : nullptr, 0.f, al16);
@@ -691,70 +753,125 @@ k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) 
       for (int k = ready; k < cnt; ++k) st.add(load_ch<VEC, T>((const T*)(mine + k * SLOT)));
       st.end(cnt);
     }
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      float2 acc[1][kPairs(VEC)] = {};
-      if (cnt > 0) st.out(acc, half, cnt, c, mean_s[par], a.cg_div);
-      for (int g = threadIdx.x; g < sl.kk; g += NT) gs[0][g] = 0.f;
-      const float* res = reduce_channels<1, VEC>(sl, acc, scr, w.v, w.rg, w.active);
-      reduce_groups<1, VEC>(sl, a.cg, 0, res, gs, [](int) { return 1.f; });
-      __syncthreads();
-      for (int g = threadIdx.x; g < sl.kk; g += NT) {
-        if (half == 0) mean_s[par][g] = w.rows ? gs[0][g] / n : 0.f;
-        else m2_s[par][g] = gs[0][g];
-      }
-      if (threadIdx.x == 0) n_s[par] = n;
-      __syncthreads();
-    }
-    if (sl.S > 1) {
-      cluster_arrive();
-      cluster_wait();
-    }
-    join_stats(a, sl, w.b, w.c0, rank, mean_s[par], m2_s[par], &n_s[par], mean_t, rstd_t);
-    __syncthreads();
-    // last pass: write y, copy the next slab into the slots it has read
-    if (w.active) {
+    if constexpr (UNI) {
+      // the thread's (count, mean, squares about it) over its channels; then
+      // the block's mean, then the squares about that
+      float tn = 0.f, tm = 0.f, tq = 0.f;
+      if (cnt > 0) {
+        float2 ms = st.s[0], qs = st.q[0];
 #pragma unroll
-      for (int i = 0; i < kPairs(VEC); ++i) {
-        const int ca = c + 2 * i, gx = ca / a.cg_div, gz = (ca + 1) / a.cg_div;
-        m[i] = make_float2(-mean_t[gx], -mean_t[gz]);
-        s[i] = __fmul2_rn(make_float2(rstd_t[gx], rstd_t[gz]), s[i]);
+        for (int i = 1; i < NP; ++i) {
+          ms = __fadd2_rn(ms, st.s[i]);
+          qs = __fadd2_rn(qs, st.q[i]);
+        }
+        tm = (ms.x + ms.y) * (1.f / VEC);
+        float2 ds = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const float2 d = __fadd2_rn(st.s[i], make_float2(-tm, -tm));
+          ds = __ffma2_rn(d, d, ds);
+        }
+        tq = fmaf(ds.x + ds.y, (float)cnt, qs.x + qs.y);
+        tn = (float)(cnt * VEC);
+      }
+      const float rn = __frcp_rn(fmaxf(n, 1.f));
+      const bool leader = (lane & sl.lanes) == 0;
+      float v = group_lanes(tn * tm, sl.lanes);
+      if (leader) buf[0][myg][warp] = v;
+      __syncthreads();
+      float mean = group_warps(buf[0], myg) * rn;
+      const float d = tm - mean;
+      v = group_lanes(fmaf(tn * d, d, tq), sl.lanes);
+      if (leader) buf[1][myg][warp] = v;
+      __syncthreads();
+      float m2 = group_warps(buf[1], myg), all = n;
+      if (sl.S > 1) {
+        if (leader && warp == 0) {
+          mean_s[par][myg] = mean;
+          m2_s[par][myg] = m2;
+        }
+        if (threadIdx.x == 0) n_s[par] = n;
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        float mt = 0.f, sq = 0.f;
+        all = 0.f;
+        for (int k = 0; k < sl.S; ++k) {
+          const float nk = peer_f32(&n_s[par], k), mk = peer_f32(&mean_s[par][myg], k),
+                      sk = peer_f32(&m2_s[par][myg], k);
+          if (nk == 0.f) continue;
+          const float dk = mk - mt, f = __fdividef(nk, all + nk);
+          mt = fmaf(dk, f, mt);
+          sq += fmaf(dk * dk, all * f, sk);
+          all += nk;
+        }
+        mean = mt;
+        m2 = sq;
+      }
+      const float rstd =
+          all > 0.f ? rsqrtf(fmaf(m2, __frcp_rn(fmaxf(all, 1.f)), a.eps)) : 0.f;
+      if (rank == 0 && warp == 0 && leader)
+        a.stats[(long long)w.b * a.G + w.c0 / a.cg_div + myg] = make_float2(all > 0.f ? mean : 0.f, rstd);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        m[i] = make_float2(-mean, -mean);
+        s[i] = __fmul2_rn(make_float2(rstd, rstd), s[i]);
+      }
+    } else {
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        float2 acc[1][NP] = {};
+        if (cnt > 0) st.out(acc, half, cnt, c, mean_s[par], a.cg_div);
+        for (int g = threadIdx.x; g < sl.kk; g += NT) gs[0][g] = 0.f;
+        const float* res = reduce_channels<1, VEC>(sl, acc, scr, w.v, w.rg, w.active);
+        reduce_groups<1, VEC>(sl, a.cg, 0, res, gs, [](int) { return 1.f; });
+        __syncthreads();
+        for (int g = threadIdx.x; g < sl.kk; g += NT) {
+          if (half == 0) mean_s[par][g] = w.rows ? gs[0][g] / n : 0.f;
+          else m2_s[par][g] = gs[0][g];
+        }
+        if (threadIdx.x == 0) n_s[par] = n;
+        __syncthreads();
+      }
+      if (sl.S > 1) {
+        cluster_arrive();
+        cluster_wait();
+      }
+      join_stats(a, sl, w.b, w.c0, rank, mean_s[par], m2_s[par], &n_s[par], mean_t, rstd_t);
+      __syncthreads();
+      if (w.active) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const int ca = c + 2 * i, gx = ca / a.cg_div, gz = (ca + 1) / a.cg_div;
+          m[i] = make_float2(-mean_t[gx], -mean_t[gz]);
+          s[i] = __fmul2_rn(make_float2(rstd_t[gx], rstd_t[gz]), s[i]);
+        }
       }
     }
+    // last pass: write y, copy the next slab into the slots it has read
     T* o = ys + (long long)(w.t0 + w.rg) * a.yf + c;
     const T* p = x + nx.b * a.xb + nx.c0 + (long long)(nx.t0 + nx.rg) * a.xf + c;
-    const int both = min(cnt, ncnt), head = both / 2;
-    auto apply = [&](int k) {
-      Ch<VEC> q = load_ch<VEC, T>((const T*)(mine + k * SLOT));
+    auto apply = [&](int k, auto frames) {
+      constexpr int U = decltype(frames)::value;
+      Ch<VEC> q[U];
 #pragma unroll
-      for (int i = 0; i < kPairs(VEC); ++i)
-        q.v[i] = act2<ACT, T>(__ffma2_rn(__fadd2_rn(q.v[i], m[i]), s[i], be[i]));
-      store_ch<VEC, T>(o, q);
-      o += yinc;
+      for (int u = 0; u < U; ++u) q[u] = load_ch<VEC, T>((const T*)(mine + (k + u) * SLOT));
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+          q[u].v[i] = act2<ACT, T>(__ffma2_rn(__fadd2_rn(q[u].v[i], m[i]), s[i], be[i]));
+        store_ch<VEC, T>(o, q[u]);
+        o += yinc;
+      }
     };
     auto fetch = [&](int k) {
       copy16(mine_a + k * SLOT, p);
       p += xinc;
     };
-    int k = 0;
-#pragma unroll 2
-    for (; k < head; ++k) {
-      apply(k);
-      fetch(k);
-    }
-    copy_commit();
-#pragma unroll 2
-    for (; k < both; ++k) {
-      apply(k);
-      fetch(k);
-    }
-    for (int j = k; j < ncnt; ++j) fetch(j);
-    copy_commit();
-#pragma unroll 2
-    for (int j = k; j < cnt; ++j) apply(j);
+    ready = turn_over(cnt, ncnt, apply, fetch);
     w = nx;
     cnt = ncnt;
-    ready = head;
   }
   __syncwarp();
   if (sl.S > 1) {  // peers may still read this block's statistics
@@ -763,23 +880,26 @@ k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) 
   }
 }
 
-template <typename T, int ACT>
-__global__ void __launch_bounds__(NT, 4)
+// part: sums per block (keep) or per sample, block and channel of (g xh, g).
+template <typename T, int ACT, int UNI>
+__global__ void __launch_bounds__(NT, 3)
 k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict__ dy,
                T* __restrict__ dx, float2* __restrict__ part) {
-  constexpr int VEC = kVec16<T>;
+  constexpr int VEC = kVec16<T>, NP = kPairs(VEC);
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float gs[2][2][MAX_KK];  // by parity; read by the cluster's other blocks
   __shared__ float m1_t[MAX_KK], m2_t[MAX_KK];
+  __shared__ __align__(16) float buf[2][2][UNI ? 32 : 1][NWARPS];
   const int half_bytes = sl.slots * SLOT;
   float* scr = (float*)(smem + 2 * (size_t)half_bytes);
   const unsigned char* mine = smem + threadIdx.x * 16;
   const uint32_t mine_a = ptx::smem_u32(mine);
   const int first = (int)blockIdx.x / sl.S_div, rank = blockIdx.x - first * sl.S;
-  const int stride = (int)gridDim.x / sl.S_div;
+  const int stride = (int)gridDim.x / sl.S_div, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool al16 = (((uintptr_t)a.gamma | (uintptr_t)a.beta) & 15) == 0;
-  Where<VEC> w = where<VEC>(a, sl, first, rank);
-  const int c = w.v * VEC;
+  Where<VEC> w = where<VEC>(a, sl, first, rank, length_of(a, first / sl.per_sample_div));
+  int ahead = length_ahead(a, sl, first + stride);
+  const int c = w.v * VEC, myg = c / a.cg_div;
   int cnt = rows_of(w);
   const long long xinc = a.xf * w.step, dinc = a.yf * w.step;
   {
@@ -793,15 +913,17 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
     copy_commit();
   }
   int ready = cnt, par = 0;
+  float2 tot[2][NP] = {};  // sums of all the block's slabs with these channels
 #pragma unroll 1
   for (int slab = first; slab < sl.nslabs; slab += stride, par ^= 1) {
     const bool more = slab + stride < sl.nslabs;
     Where<VEC> nx = w;
     int ncnt = 0;
     if (more) {
-      nx = where<VEC>(a, sl, slab + stride, rank);
+      nx = where<VEC>(a, sl, slab + stride, rank, ahead);
       ncnt = rows_of(nx);
     }
+    ahead = length_ahead(a, sl, slab + 2 * stride);
     T* os = dx + w.b * a.xb + w.c0;
     Back<T, VEC, ACT> bk;
     if (w.active) {
@@ -810,7 +932,7 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
       load_param<VEC>(bk.be, a.beta ? a.beta + w.c0 + c : nullptr, 0.f, al16);
     }
     zero_tail<VEC, T>(a, sl, w, os, a.xf);
-    float2 acc[2][kPairs(VEC)] = {};
+    float2 acc[2][NP] = {};
     auto sums = [&](int k) {
       bk.sums(load_ch<VEC, T>((const T*)(mine + k * SLOT)),
               load_ch<VEC, T>((const T*)(mine + half_bytes + k * SLOT)), acc);
@@ -821,31 +943,83 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
     copy_wait<0>();
 #pragma unroll 2
     for (int k = ready; k < cnt; ++k) sums(k);
-    for (int g = threadIdx.x; g < sl.kk; g += NT) gs[par][0][g] = gs[par][1][g] = 0.f;
-    const float* res = reduce_channels<2, VEC>(sl, acc, scr, w.v, w.rg, w.active);
-    for (int k = threadIdx.x; k < sl.W; k += NT)
-      part[((long long)w.b * sl.S + rank) * a.C + w.c0 + k] = make_float2(res[k], res[sl.W + k]);
-    reduce_groups<2, VEC>(sl, a.cg, 0, res, gs[par], [&](int ch) {
-      return a.gamma ? a.gamma[w.c0 + ch] : 1.f;
-    });
-    __syncthreads();
-    if (sl.S > 1) {
-      cluster_arrive();
-      cluster_wait();
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      tot[0][i] = __fadd2_rn(tot[0][i], acc[0][i]);
+      tot[1][i] = __fadd2_rn(tot[1][i], acc[1][i]);
     }
-    join_means(a, sl, w.tb, gs[par], m1_t, m2_t);
-    __syncthreads();
-    float2 k1[kPairs(VEC)], k2[kPairs(VEC)];
-    if (w.active) means_of<VEC>(m1_t, m2_t, c, a.cg_div, k1, k2);
+    float2 k1[NP], k2[NP];
+    if constexpr (UNI) {
+      float2 s1 = make_float2(0.f, 0.f), s2 = s1;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        s2 = __ffma2_rn(bk.ga[i], acc[0][i], s2);
+        s1 = __ffma2_rn(bk.ga[i], acc[1][i], s1);
+      }
+      const bool leader = (lane & sl.lanes) == 0;
+      const float v2 = group_lanes(s2.x + s2.y, sl.lanes);
+      const float v1 = group_lanes(s1.x + s1.y, sl.lanes);
+      if (leader) {
+        buf[par][0][myg][warp] = v2;
+        buf[par][1][myg][warp] = v1;
+      }
+      __syncthreads();
+      float g2 = group_warps(buf[par][0], myg), g1 = group_warps(buf[par][1], myg);
+      if (sl.S > 1) {
+        if (leader && warp == 0) {
+          gs[par][0][myg] = g2;
+          gs[par][1][myg] = g1;
+        }
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        g2 = g1 = 0.f;
+        for (int k = 0; k < sl.S; ++k) {
+          g2 += peer_f32(&gs[par][0][myg], k);
+          g1 += peer_f32(&gs[par][1][myg], k);
+        }
+      }
+      const float rn = __frcp_rn(fmaxf((float)w.tb * a.cg, 1.f));
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        k1[i] = make_float2(-g1 * rn, -g1 * rn);
+        k2[i] = make_float2(-g2 * rn, -g2 * rn);
+      }
+    } else {
+      for (int g = threadIdx.x; g < sl.kk; g += NT) gs[par][0][g] = gs[par][1][g] = 0.f;
+      const float* res = reduce_channels<2, VEC>(sl, acc, scr, w.v, w.rg, w.active);
+      reduce_groups<2, VEC>(sl, a.cg, 0, res, gs[par], [&](int ch) {
+        return a.gamma ? a.gamma[w.c0 + ch] : 1.f;
+      });
+      __syncthreads();
+      if (sl.S > 1) {
+        cluster_arrive();
+        cluster_wait();
+      }
+      join_means(a, sl, w.tb, gs[par], m1_t, m2_t);
+      __syncthreads();
+      if (w.active) means_of<VEC>(m1_t, m2_t, c, a.cg_div, k1, k2);
+    }
+    if (!sl.keep || !more) {  // these channels' sums leave the block
+      const float* res = reduce_channels<2, VEC>(sl, tot, scr, w.v, w.rg, w.active);
+      const int row = sl.keep ? first / sl.per_sample_div : w.b;
+      for (int k = threadIdx.x; k < sl.W; k += NT)
+        part[((long long)row * sl.S + rank) * a.C + w.c0 + k] = make_float2(res[k], res[sl.W + k]);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) tot[0][i] = tot[1][i] = make_float2(0.f, 0.f);
+    }
     T* o = os + (long long)(w.t0 + w.rg) * a.xf + c;
     const T* p = x + nx.b * a.xb + nx.c0 + (long long)(nx.t0 + nx.rg) * a.xf + c;
     const T* d = dy + nx.b * a.yb + nx.c0 + (long long)(nx.t0 + nx.rg) * a.yf + c;
-    const int both = min(cnt, ncnt), head = both / 2;
-    auto apply = [&](int k) {
-      store_ch<VEC, T>(o, bk.dx(load_ch<VEC, T>((const T*)(mine + k * SLOT)),
-                                load_ch<VEC, T>((const T*)(mine + half_bytes + k * SLOT)), k1,
-                                k2));
-      o += xinc;
+    auto apply = [&](int k, auto frames) {
+      constexpr int U = decltype(frames)::value;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        store_ch<VEC, T>(o, bk.dx(load_ch<VEC, T>((const T*)(mine + (k + u) * SLOT)),
+                                  load_ch<VEC, T>((const T*)(mine + half_bytes + (k + u) * SLOT)),
+                                  k1, k2));
+        o += xinc;
+      }
     };
     auto fetch = [&](int k) {
       copy16(mine_a + k * SLOT, p);
@@ -853,25 +1027,9 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
       p += xinc;
       d += dinc;
     };
-    int k = 0;
-#pragma unroll 1
-    for (; k < head; ++k) {
-      apply(k);
-      fetch(k);
-    }
-    copy_commit();
-#pragma unroll 1
-    for (; k < both; ++k) {
-      apply(k);
-      fetch(k);
-    }
-    for (int j = k; j < ncnt; ++j) fetch(j);
-    copy_commit();
-#pragma unroll 1
-    for (int j = k; j < cnt; ++j) apply(j);
+    ready = turn_over(cnt, ncnt, apply, fetch);
     w = nx;
     cnt = ncnt;
-    ready = head;
   }
   __syncwarp();
   if (sl.S > 1) {  // peers may still read this block's sums
@@ -959,6 +1117,7 @@ struct NormCut {
   Slab sl;
   int vec, res;
   int grid;
+  int rows;  // rows of part
   size_t smem;
 };
 
@@ -1008,9 +1167,22 @@ NormCut norm_cut(const NormArgs& a, int e, int tiles, bool aligned) {
   s.cbv_div = fast_div(s.cbv);
   n.smem = (n.res ? (size_t)s.slots * SLOT * tiles : 0) + (size_t)s.scratch * tiles;
   n.grid = s.nslabs * s.S;
-  if (n.res) {  // as many blocks as the SMs hold (228 KB each, at most 4 by registers)
-    const int per_sm = (int)std::min<size_t>(4, (228 * 1024) / (n.smem + 4 * 1024));
-    n.grid = std::min(s.nslabs, std::max(1, per_sm * num_sms() / s.S)) * s.S;
+  n.rows = a.B * s.S;
+  if (n.res) {
+    // as many blocks as the SMs hold (228 KB each; 3 by the kernels' registers,
+    // more when they take fewer), in steps of a sample's slabs, so that a block
+    // keeps its channels
+    const int per_sample = a.G / kk;
+    const int per_sm = (int)std::min<size_t>(4, (228 * 1024) / (n.smem + 8 * 1024));
+    int clusters = std::min(s.nslabs, std::max(1, per_sm * num_sms() / s.S));
+    s.keep = clusters >= per_sample;
+    if (s.keep) {
+      clusters = clusters / per_sample * per_sample;
+      n.rows = clusters / per_sample * s.S;
+    }
+    n.grid = clusters * s.S;
+    s.uni = s.pow2 && a.cg % n.vec == 0;
+    s.lanes = s.uni ? 31 & ~(s.cbv - a.cg / n.vec) : 0;
   }
   return n;
 }
@@ -1059,10 +1231,13 @@ cudaError_t norm_launch(KF kf, KB kb, std::atomic<bool>* fdone, std::atomic<bool
 template <typename T, int ACT>
 cudaError_t norm_launch_cut(const NormArgs& a, const NormCut& n, const void* x, const void* dy,
                             void* out, float2* part, cudaStream_t st) {
-  static std::atomic<bool> done[6][kDeviceSlots];
+  static std::atomic<bool> done[8][kDeviceSlots];
+  if (n.res && n.sl.uni)
+    return norm_launch<T>(k_norm_fwd_res<T, ACT, 1>, k_norm_bwd_res<T, ACT, 1>, done[6], done[7],
+                          a, n, x, dy, out, part, st);
   if (n.res)
-    return norm_launch<T>(k_norm_fwd_res<T, ACT>, k_norm_bwd_res<T, ACT>, done[0], done[1], a, n,
-                          x, dy, out, part, st);
+    return norm_launch<T>(k_norm_fwd_res<T, ACT, 0>, k_norm_bwd_res<T, ACT, 0>, done[0], done[1],
+                          a, n, x, dy, out, part, st);
   if (n.vec == 4)
     return norm_launch<T>(k_norm_fwd_stream<T, 4, ACT>, k_norm_bwd_stream<T, 4, ACT>, done[2],
                           done[3], a, n, x, dy, out, part, st);
@@ -1143,7 +1318,7 @@ rnnt_status rnnt_norm_bwd(const rnnt_norm_dims* dims, const void* x, const void*
                      : norm_launch_act<__nv_bfloat16>(a, n, x, dy, dx, part, st));
   }
   if (!dgamma && !dbeta) return RNNT_OK;
-  const int rows = a.B * n.sl.S, S = rows > 256 ? 8 : 1;
+  const int rows = n.rows, S = rows > 256 ? 8 : 1;
   OPS_LAUNCH("norm_params", launch_cluster(k_norm_params, (unsigned)cdiv(a.C, 32) * S, S, 0, st,
                                            (const float2*)part, rows, a.C, S, dgamma, dbeta));
   return RNNT_OK;
