@@ -182,7 +182,8 @@ struct Slab {
   int lanes;         // lane bits that share a group (uni)
   int keep;          // a block's slabs have the same channels
   int scratch;       // scratch bytes per reduced quantity
-  FastDiv per_sample_div, S_div, cbv_div;
+  int S_log, step_log;  // S; NT / cbv where cbv is a power of two
+  FastDiv per_sample_div, cbv_div;
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -203,6 +204,13 @@ __device__ __forceinline__ float peer_f32(const float* p, int rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_u32(p)), "r"(rank));
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
   return v;
+}
+
+// write a value to the same shared address of another block of the cluster
+__device__ __forceinline__ void to_peer_f32(float* p, int rank, float v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_u32(p)), "r"(rank));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 
 // Sums over the block's frames of NA quantities per channel, for the channels
@@ -279,20 +287,25 @@ struct Where {
   bool active;
 };
 template <int VEC>
+__device__ __forceinline__ void set_frames(Where<VEC>& w, const NormArgs& a, const Slab& sl,
+                                           int length) {
+  w.tb = frames_of(a, length);
+  const int per = (w.tb + sl.S - 1) >> sl.S_log;
+  w.t0 = min(w.tb, w.rank * per);
+  w.rows = min(w.tb, w.t0 + per) - w.t0;
+}
+template <int VEC>
 __device__ __forceinline__ Where<VEC> where(const NormArgs& a, const Slab& sl, int slab, int rank,
                                             int length) {
   Where<VEC> w;
   w.rank = rank;
   w.b = slab / sl.per_sample_div;
   w.c0 = (slab - w.b * (int)sl.per_sample_div.d) * sl.W;
-  w.tb = frames_of(a, length);
-  const int per = (w.tb + sl.S - 1) / sl.S_div;
-  w.t0 = min(w.tb, w.rank * per);
-  w.rows = min(w.tb, w.t0 + per) - w.t0;
   w.rg = (int)threadIdx.x / sl.cbv_div;
   w.v = threadIdx.x - w.rg * sl.cbv;
   w.step = NT / sl.cbv_div;
   w.active = w.rg < w.step;
+  set_frames(w, a, sl, length);
   return w;
 }
 
@@ -300,7 +313,7 @@ __device__ __forceinline__ Where<VEC> where(const NormArgs& a, const Slab& sl, i
 template <int VEC, typename T>
 __device__ __forceinline__ void zero_tail(const NormArgs& a, const Slab& sl, const Where<VEC>& w,
                                           T* out, long long ld) {
-  const int left = a.T - w.tb, per = (left + sl.S - 1) / sl.S_div;
+  const int left = a.T - w.tb, per = (left + sl.S - 1) >> sl.S_log;
   const int z0 = w.tb + min(left, w.rank * per), z1 = w.tb + min(left, (w.rank + 1) * per);
   if (!w.active) return;
   const Ch<VEC> z{};
@@ -316,8 +329,10 @@ __device__ __forceinline__ void zero_tail(const NormArgs& a, const Slab& sl, con
 
 // Frames of the calling thread's column: rg, rg + step, ...
 template <int VEC>
-__device__ __forceinline__ int rows_of(const Where<VEC>& w) {
-  return w.active && w.rg < w.rows ? (w.rows - 1 - w.rg) / w.step + 1 : 0;
+__device__ __forceinline__ int rows_of(const Where<VEC>& w, const Slab& sl) {
+  if (!w.active || w.rg >= w.rows) return 0;
+  const int last = w.rows - 1 - w.rg;
+  return (sl.pow2 ? last >> sl.step_log : last / w.step) + 1;
 }
 
 // The blocks' (n, mean, M2) of a slab, joined in order; st: the cluster's
@@ -400,14 +415,14 @@ k_norm_fwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ 
   __shared__ float gs[2][MAX_KK], mean_s[MAX_KK], n_s;
   __shared__ float mean_t[MAX_KK], rstd_t[MAX_KK];
   float* scr = (float*)smem;
-  const int slab = (int)blockIdx.x / sl.S_div;
+  const int slab = (int)blockIdx.x >> sl.S_log;
   const Where<VEC> w = where<VEC>(a, sl, slab, blockIdx.x - slab * sl.S,
                                   length_of(a, slab / sl.per_sample_div));
   const T* src = x + w.b * a.xb + w.c0 + (long long)w.t0 * a.xf;
   T* ys = y + w.b * a.yb + w.c0;
   zero_tail<VEC, T>(a, sl, w, ys, a.yf);
   const long long ld = a.xf, inc = ld * w.step;
-  const int nb = sl.cbv * VEC, cnt = rows_of(w);
+  const int nb = sl.cbv * VEC, cnt = rows_of(w, sl);
   const float n = (float)w.rows * a.cg;
   for (int g = threadIdx.x; g < sl.kk; g += NT) gs[0][g] = gs[1][g] = 0.f;
   __syncthreads();
@@ -556,7 +571,7 @@ k_norm_bwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restr
   __shared__ float gs[2][MAX_KK];  // read by the cluster's other blocks
   __shared__ float m1_t[MAX_KK], m2_t[MAX_KK];
   float* scr = (float*)smem;
-  const int slab = (int)blockIdx.x / sl.S_div;
+  const int slab = (int)blockIdx.x >> sl.S_log;
   const Where<VEC> w = where<VEC>(a, sl, slab, blockIdx.x - slab * sl.S,
                                   length_of(a, slab / sl.per_sample_div));
   const T* xs = x + w.b * a.xb + w.c0 + (long long)w.t0 * a.xf;
@@ -565,7 +580,7 @@ k_norm_bwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restr
   zero_tail<VEC, T>(a, sl, w, os, a.xf);
   os += (long long)w.t0 * a.xf;
   const long long xinc = a.xf * w.step, dinc = a.yf * w.step;
-  const int nb = sl.cbv * VEC, cnt = rows_of(w);
+  const int nb = sl.cbv * VEC, cnt = rows_of(w, sl);
   const float2* stats = a.stats + (long long)w.b * a.G + w.c0 / a.cg_div;
   for (int g = threadIdx.x; g < sl.kk; g += NT) gs[0][g] = gs[1][g] = 0.f;
   __syncthreads();
@@ -689,6 +704,18 @@ __device__ __forceinline__ int turn_over(int cnt, int ncnt, A apply, F fetch) {
   return head;
 }
 
+// The block's next slab: the same channels of a later sample (keep), or any.
+template <int VEC>
+__device__ __forceinline__ void next_where(Where<VEC>& w, const NormArgs& a, const Slab& sl,
+                                           int slab, int stride, int length) {
+  if (sl.keep) {
+    w.b += stride / sl.per_sample_div;
+    set_frames(w, a, sl, length);
+  } else {
+    w = where<VEC>(a, sl, slab, w.rank, length);
+  }
+}
+
 // Length of the block's slab after next, asked for one slab ahead of its use.
 __device__ __forceinline__ int length_ahead(const NormArgs& a, const Slab& sl, int slab) {
   return slab < sl.nslabs ? length_of(a, slab / sl.per_sample_div) : 0;
@@ -699,21 +726,23 @@ __global__ void __launch_bounds__(NT, 3)
 k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) {
   constexpr int VEC = kVec16<T>, NP = kPairs(VEC);
   extern __shared__ __align__(16) unsigned char smem[];
-  // (read by the cluster's other blocks: one set per parity of the slab count,
-  // so that one barrier a slab keeps writers off what peers still read)
-  __shared__ float mean_s[2][MAX_KK], m2_s[2][MAX_KK], n_s[2];
-  __shared__ float gs[1][MAX_KK], mean_t[MAX_KK], rstd_t[MAX_KK];
-  __shared__ __align__(16) float buf[2][UNI ? 32 : 1][NWARPS];
+  // (what other blocks of the cluster read or write has a set per parity of the
+  // slab count, so that one barrier a slab keeps writers off what is still read)
+  constexpr int GK = UNI ? 1 : MAX_KK, UK = UNI ? 32 : 1;
+  __shared__ float mean_s[2][GK], m2_s[2][GK], n_s[2];
+  __shared__ float gs[1][MAX_KK], mean_t[GK], rstd_t[GK];
+  __shared__ __align__(16) float buf[2][UK][NWARPS];
+  __shared__ float from[2][8][2][UK];  // (mean, M2) of every block of the cluster
   float* scr = (float*)(smem + (size_t)sl.slots * SLOT);
   const unsigned char* mine = smem + threadIdx.x * 16;
   const uint32_t mine_a = ptx::smem_u32(mine);
-  const int first = (int)blockIdx.x / sl.S_div, rank = blockIdx.x - first * sl.S;
-  const int stride = (int)gridDim.x / sl.S_div, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int first = (int)blockIdx.x >> sl.S_log, rank = blockIdx.x - first * sl.S;
+  const int stride = (int)gridDim.x >> sl.S_log, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool al16 = (((uintptr_t)a.gamma | (uintptr_t)a.beta) & 15) == 0;
   Where<VEC> w = where<VEC>(a, sl, first, rank, length_of(a, first / sl.per_sample_div));
   int ahead = length_ahead(a, sl, first + stride);
   const int c = w.v * VEC, myg = c / a.cg_div;
-  int cnt = rows_of(w);
+  int cnt = rows_of(w, sl);
   const long long xinc = a.xf * w.step, yinc = a.yf * w.step;
   {
     const T* p = x + w.b * a.xb + w.c0 + (long long)(w.t0 + w.rg) * a.xf + c;
@@ -723,24 +752,25 @@ k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) 
   }
   int ready = cnt;  // slots of the first of the two copy groups
   int par = 0;
+  float2 ga[NP], be[NP];
 #pragma unroll 1
   for (int slab = first; slab < sl.nslabs; slab += stride, par ^= 1) {
     const bool more = slab + stride < sl.nslabs;
     Where<VEC> nx = w;
     int ncnt = 0;
     if (more) {
-      nx = where<VEC>(a, sl, slab + stride, rank, ahead);
-      ncnt = rows_of(nx);
+      next_where(nx, a, sl, slab + stride, stride, ahead);
+      ncnt = rows_of(nx, sl);
     }
     ahead = length_ahead(a, sl, slab + 2 * stride);
     T* ys = y + w.b * a.yb + w.c0;
-    float2 s[NP], be[NP], m[NP];
-    if (w.active) {
-      load_param<VEC>(s, a.gamma ? a.gamma + w.c0 + c : nullptr, 1.f, al16);
+    if (w.active && (!sl.keep || slab == first)) {
+      load_param<VEC>(ga, a.gamma ? a.gamma + w.c0 + c : nullptr, 1.f, al16);
       load_param<VEC>(be, a.beta ? a.beta + w.c0 + c : nullptr, 0.f, al16);
     }
     zero_tail<VEC, T>(a, sl, w, ys, a.yf);
     const float n = (float)w.rows * a.cg;
+    float2 s[NP], m[NP];
     Partial<VEC> st;
     copy_wait<1>();
     if (cnt > 0) {
@@ -786,20 +816,21 @@ k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) 
       __syncthreads();
       float m2 = group_warps(buf[1], myg), all = n;
       if (sl.S > 1) {
-        if (leader && warp == 0) {
-          mean_s[par][myg] = mean;
-          m2_s[par][myg] = m2;
-        }
-        if (threadIdx.x == 0) n_s[par] = n;
+        if (leader && warp == 0)
+          for (int k = 0; k < sl.S; ++k) {
+            to_peer_f32(&from[par][rank][0][myg], k, mean);
+            to_peer_f32(&from[par][rank][1][myg], k, m2);
+          }
         __syncwarp();
         cluster_arrive();
         cluster_wait();
+        const int per = (w.tb + sl.S - 1) >> sl.S_log;  // frames of the blocks but the last
         float mt = 0.f, sq = 0.f;
         all = 0.f;
         for (int k = 0; k < sl.S; ++k) {
-          const float nk = peer_f32(&n_s[par], k), mk = peer_f32(&mean_s[par][myg], k),
-                      sk = peer_f32(&m2_s[par][myg], k);
-          if (nk == 0.f) continue;
+          const float nk = (float)(min(w.tb, (k + 1) * per) - min(w.tb, k * per)) * a.cg;
+          const float mk = from[par][k][0][myg], sk = from[par][k][1][myg];
+          if (nk == 0.f) break;
           const float dk = mk - mt, f = __fdividef(nk, all + nk);
           mt = fmaf(dk, f, mt);
           sq += fmaf(dk * dk, all * f, sk);
@@ -815,7 +846,7 @@ k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) 
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         m[i] = make_float2(-mean, -mean);
-        s[i] = __fmul2_rn(make_float2(rstd, rstd), s[i]);
+        s[i] = __fmul2_rn(make_float2(rstd, rstd), ga[i]);
       }
     } else {
 #pragma unroll 1
@@ -844,7 +875,7 @@ k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) 
         for (int i = 0; i < NP; ++i) {
           const int ca = c + 2 * i, gx = ca / a.cg_div, gz = (ca + 1) / a.cg_div;
           m[i] = make_float2(-mean_t[gx], -mean_t[gz]);
-          s[i] = __fmul2_rn(make_float2(rstd_t[gx], rstd_t[gz]), s[i]);
+          s[i] = __fmul2_rn(make_float2(rstd_t[gx], rstd_t[gz]), ga[i]);
         }
       }
     }
@@ -887,20 +918,22 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
                T* __restrict__ dx, float2* __restrict__ part) {
   constexpr int VEC = kVec16<T>, NP = kPairs(VEC);
   extern __shared__ __align__(16) unsigned char smem[];
+  constexpr int GK = UNI ? 1 : MAX_KK, UK = UNI ? 32 : 1;
   __shared__ float gs[2][2][MAX_KK];  // by parity; read by the cluster's other blocks
-  __shared__ float m1_t[MAX_KK], m2_t[MAX_KK];
-  __shared__ __align__(16) float buf[2][2][UNI ? 32 : 1][NWARPS];
+  __shared__ float m1_t[GK], m2_t[GK];
+  __shared__ __align__(16) float buf[2][2][UK][NWARPS];
+  __shared__ float from[2][8][2][UK];  // sums of every block of the cluster
   const int half_bytes = sl.slots * SLOT;
   float* scr = (float*)(smem + 2 * (size_t)half_bytes);
   const unsigned char* mine = smem + threadIdx.x * 16;
   const uint32_t mine_a = ptx::smem_u32(mine);
-  const int first = (int)blockIdx.x / sl.S_div, rank = blockIdx.x - first * sl.S;
-  const int stride = (int)gridDim.x / sl.S_div, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int first = (int)blockIdx.x >> sl.S_log, rank = blockIdx.x - first * sl.S;
+  const int stride = (int)gridDim.x >> sl.S_log, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool al16 = (((uintptr_t)a.gamma | (uintptr_t)a.beta) & 15) == 0;
   Where<VEC> w = where<VEC>(a, sl, first, rank, length_of(a, first / sl.per_sample_div));
   int ahead = length_ahead(a, sl, first + stride);
   const int c = w.v * VEC, myg = c / a.cg_div;
-  int cnt = rows_of(w);
+  int cnt = rows_of(w, sl);
   const long long xinc = a.xf * w.step, dinc = a.yf * w.step;
   {
     const T* p = x + w.b * a.xb + w.c0 + (long long)(w.t0 + w.rg) * a.xf + c;
@@ -913,26 +946,44 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
     copy_commit();
   }
   int ready = cnt, par = 0;
+  Back<T, VEC, ACT> bk;
+  // (a slab's statistics are asked for one slab ahead)
+  auto stats_of = [&](const Where<VEC>& q) {
+    return a.stats[(long long)q.b * a.G + q.c0 / a.cg_div + myg];
+  };
+  float2 stat = UNI ? stats_of(w) : make_float2(0.f, 0.f);
   float2 tot[2][NP] = {};  // sums of all the block's slabs with these channels
 #pragma unroll 1
   for (int slab = first; slab < sl.nslabs; slab += stride, par ^= 1) {
     const bool more = slab + stride < sl.nslabs;
-    Where<VEC> nx = w;
-    int ncnt = 0;
-    if (more) {
-      nx = where<VEC>(a, sl, slab + stride, rank, ahead);
-      ncnt = rows_of(nx);
-    }
-    ahead = length_ahead(a, sl, slab + 2 * stride);
     T* os = dx + w.b * a.xb + w.c0;
-    Back<T, VEC, ACT> bk;
-    if (w.active) {
+    if constexpr (UNI) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        bk.m[i] = make_float2(-stat.x, -stat.x);
+        bk.rs[i] = make_float2(stat.y, stat.y);
+      }
+    } else if (w.active) {
       bk.stats(a.stats + (long long)w.b * a.G + w.c0 / a.cg_div, c, a.cg_div);
+    }
+    if (w.active && (!sl.keep || slab == first)) {
       load_param<VEC>(bk.ga, a.gamma ? a.gamma + w.c0 + c : nullptr, 1.f, al16);
       load_param<VEC>(bk.be, a.beta ? a.beta + w.c0 + c : nullptr, 0.f, al16);
     }
-    zero_tail<VEC, T>(a, sl, w, os, a.xf);
     float2 acc[2][NP] = {};
+    // the next slab, and the zeros past this one's frames: work for the time
+    // that the blocks of a cluster wait for one another
+    Where<VEC> nx = w;
+    int ncnt = 0;
+    auto meanwhile = [&]() {
+      if (more) {
+        next_where(nx, a, sl, slab + stride, stride, ahead);
+        ncnt = rows_of(nx, sl);
+        if (UNI) stat = stats_of(nx);
+      }
+      ahead = length_ahead(a, sl, slab + 2 * stride);
+      zero_tail<VEC, T>(a, sl, w, os, a.xf);
+    };
     auto sums = [&](int k) {
       bk.sums(load_ch<VEC, T>((const T*)(mine + k * SLOT)),
               load_ch<VEC, T>((const T*)(mine + half_bytes + k * SLOT)), acc);
@@ -966,18 +1017,23 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
       __syncthreads();
       float g2 = group_warps(buf[par][0], myg), g1 = group_warps(buf[par][1], myg);
       if (sl.S > 1) {
-        if (leader && warp == 0) {
-          gs[par][0][myg] = g2;
-          gs[par][1][myg] = g1;
-        }
+        if (leader && warp == 0)
+          for (int k = 0; k < sl.S; ++k) {
+            to_peer_f32(&from[par][rank][0][myg], k, g2);
+            to_peer_f32(&from[par][rank][1][myg], k, g1);
+          }
         __syncwarp();
         cluster_arrive();
+        meanwhile();
+        __syncwarp();
         cluster_wait();
         g2 = g1 = 0.f;
         for (int k = 0; k < sl.S; ++k) {
-          g2 += peer_f32(&gs[par][0][myg], k);
-          g1 += peer_f32(&gs[par][1][myg], k);
+          g2 += from[par][k][0][myg];
+          g1 += from[par][k][1][myg];
         }
+      } else {
+        meanwhile();
       }
       const float rn = __frcp_rn(fmaxf((float)w.tb * a.cg, 1.f));
 #pragma unroll
@@ -999,6 +1055,7 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
       join_means(a, sl, w.tb, gs[par], m1_t, m2_t);
       __syncthreads();
       if (w.active) means_of<VEC>(m1_t, m2_t, c, a.cg_div, k1, k2);
+      meanwhile();
     }
     if (!sl.keep || !more) {  // these channels' sums leave the block
       const float* res = reduce_channels<2, VEC>(sl, tot, scr, w.v, w.rg, w.active);
@@ -1163,7 +1220,8 @@ NormCut norm_cut(const NormArgs& a, int e, int tiles, bool aligned) {
   const int rows = s.pow2 ? NWARPS : NT / s.cbv;
   s.scratch = 4 * (rows + 1) * s.cbv * n.vec;
   s.per_sample_div = fast_div(a.G / kk);
-  s.S_div = fast_div(s.S);
+  for (s.S_log = 0; (1 << s.S_log) < s.S;) ++s.S_log;
+  for (s.step_log = 0; (2 << s.step_log) <= NT / s.cbv;) ++s.step_log;
   s.cbv_div = fast_div(s.cbv);
   n.smem = (n.res ? (size_t)s.slots * SLOT * tiles : 0) + (size_t)s.scratch * tiles;
   n.grid = s.nslabs * s.S;
