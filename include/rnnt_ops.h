@@ -124,7 +124,9 @@ rnnt_status rnnt_norm_bwd(const rnnt_norm_dims* dims, const void* x, const void*
  * optimiser; O = X.  The singular values move towards 1 and the singular
  * vectors stay: O is near the closest (semi-)orthogonal matrix to G.  A matrix
  * of zeros gives zeros; a NaN or an infinity gives NaN throughout its matrix.
- * rows * cols <= 2^31 - 1 per matrix.
+ * rows * cols <= 2^31 - 1 per matrix, batch <= 65535.  O must not overlap G.
+ * A wait inside the kernel that gives up sets RNNT_ERR_TIMEOUT; O is then
+ * undefined.
  */
 typedef struct {
   int rows, cols, batch;

@@ -56,7 +56,7 @@ def test_norm_dims(lib, bad):
 @pytest.mark.parametrize("bad", [dict(rows=0), dict(cols=-2), dict(batch=-1), dict(in_dtype=2),
                                  dict(out_dtype=5), dict(steps=0), dict(steps=33), dict(eps=-1e-7),
                                  dict(in_ld=15), dict(out_ld=3), dict(batch=2, out_batch=100),
-                                 dict(rows=1 << 16, cols=1 << 15)])
+                                 dict(rows=1 << 16, cols=1 << 15), dict(batch=1 << 16)])
 def test_orth_dims(lib, bad):
     d = RnntOrthDims(**{**ORTH, **bad})
     assert lib.rnnt_orth_workspace_bytes(ctypes.byref(d)) == 0
