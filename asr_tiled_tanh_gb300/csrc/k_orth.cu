@@ -17,7 +17,7 @@
 // S below 1.5 and those of P below 4 (a singular value never leaves [0, 1.21]).
 // A product takes one term (hi hi) or three (hi hi + hi lo + lo hi, the missing
 // lo lo is below 2^-22):
-//   exact (fp32 results, and small matrices, where it costs nothing): three
+//   exact (fp32 results, and small matrices, where it costs little): three
 //     terms everywhere;
 //   fast (bf16 results): one term in gram and update, whose rounding of 2^-12
 //     per entry averages out over the row; three in poly, the smallest product,
@@ -45,11 +45,11 @@ namespace {
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 
 constexpr int BM = 128, BK = 64;      // tile rows; K per stage: a 128-byte swizzle atom of fp16
-constexpr int BN_MAX = 256;
-constexpr int STAGES = 4;
-constexpr int A_BYTES = BM * BK * 2, STAGE_BYTES = A_BYTES + BN_MAX * BK * 2;
+constexpr int BOX = 64 * 64 * 2;      // bytes of a TMA box
+constexpr int RING = 192 * 1024, MAX_STAGES = 8;
 constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS;
-constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 256;
+constexpr int PITCH = 80, STG = 32 * PITCH;  // an epilogue warp's staging rows of 64 bytes
+constexpr int SMEM = 1024 + RING + EPI_WARPS * STG + 256;
 constexpr uint64_t WAIT_NS = 2000000000ull;  // 2 s per wait, then give up
 constexpr int XE = 14, SE = 14, PE = 13;     // scale exponents of X, S and P
 
@@ -62,16 +62,16 @@ enum { BUF_X0, BUF_X1, BUF_S, BUF_P };
 
 struct OrthArgs {
   int m, n, tall, batch, steps;
-  int terms;            // of gram and update: 3 (exact) or 1 (fast)
+  int exact;            // three terms in gram and update too
   int rows, cols;       // of G, and of X
   long long ldx, ldm;   // row strides of X; of S and P
   __half* X[2][2];
   __half* S[2];
   __half* P[2];
-  float* part;          // gram partial tiles [splits][batch][tiles][128][128]
-  int tiles;            // 128 x 128 tiles on and above the diagonal of S
+  float* part;          // gram partial tiles [splits][batch][tiles][128][bn]
+  int blocks;           // 128 x 128 blocks on and above the diagonal of S
   int splits, kb_split; // gram: K ranges and their length in K blocks
-  int bn;               // update: tile width
+  int bn[3];            // tile width of each product
   int ut_m, ut_n;       // update: tiles
   const void* G;
   int in_f32;
@@ -79,6 +79,7 @@ struct OrthArgs {
   void* O;
   int out_f32;
   long long out_ld, out_batch;
+  int out_vec;          // O takes 16-byte stores
   float eps;
   const double* sums;   // [batch][nb] partial sums of squares
   int nb;
@@ -190,39 +191,45 @@ __device__ __forceinline__ void triangle(int t, int nt, int& i, int& j) {
   j = i + t;
 }
 
-// One product: its tiles and operands.
+// One product: its tiles and operands.  fat: a stage holds hi and lo of both
+// operands, and the two small terms add up in an accumulator of their own (the
+// tensor cores' fp32 sums truncate: small terms added to a large sum would lose
+// digits, and three adds per K step instead of one would truncate it more).
 struct Work {
-  int kind, units, kbs, K, bn, terms, a_mn, b_mn, a_buf, b_buf;
+  int kind, units, kbs, K, bn, fat, a_mn, b_mn, a_buf, b_buf;
+  int stage_bytes, stages;
 };
 struct Unit {
-  int b, m0, n0, kb0, kb1, tile, diag;
+  int b, m0, n0, kb0, kb1, diag;
 };
 
 __device__ __forceinline__ Work work_of(const OrthArgs& a, int kind, int cur) {
   Work w;
   w.kind = kind;
   w.a_mn = w.b_mn = 0;
-  w.bn = 128;
-  w.terms = a.terms;
+  w.bn = kind == GRAM ? a.bn[0] : kind == POLY ? a.bn[1] : a.bn[2];
+  w.fat = a.exact;
+  const int sym = a.batch * a.blocks * (BM / w.bn);
   if (kind == GRAM) {
     w.K = a.n;
     w.a_buf = w.b_buf = cur;
     w.a_mn = w.b_mn = a.tall;
-    w.units = a.batch * a.tiles * a.splits;
+    w.units = sym * a.splits;
   } else if (kind == POLY) {
     w.K = a.m;
     w.a_buf = w.b_buf = BUF_S;
-    w.terms = 3;
-    w.units = a.batch * a.tiles;
+    w.fat = 1;
+    w.units = sym;
   } else {
     w.K = a.m;
-    w.bn = a.bn;
     w.a_buf = a.tall ? cur : BUF_P;
     w.b_buf = a.tall ? BUF_P : cur;
     w.b_mn = !a.tall;
     w.units = a.batch * a.ut_m * a.ut_n;
   }
   w.kbs = (w.K + BK - 1) / BK;
+  w.stage_bytes = (BM + w.bn) * BK * 2 << w.fat;
+  w.stages = min(MAX_STAGES, RING / w.stage_bytes);
   return w;
 }
 
@@ -230,7 +237,6 @@ __device__ __forceinline__ Unit unit_of(const OrthArgs& a, const Work& w, int u)
   Unit q;
   q.kb0 = 0;
   q.kb1 = w.kbs;
-  q.tile = u;
   q.diag = 0;
   if (w.kind == UPDATE) {
     const int n = u % a.ut_n, rest = u / a.ut_n;
@@ -239,18 +245,20 @@ __device__ __forceinline__ Unit unit_of(const OrthArgs& a, const Work& w, int u)
     q.n0 = n * w.bn;
     return q;
   }
+  const int per_block = BM / w.bn, per = a.blocks * per_block;
   int rest = u;
-  if (w.kind == GRAM) {
-    const int per = a.batch * a.tiles, ks = u / per;
-    rest = u - ks * per;
+  if (w.kind == GRAM && a.splits > 1) {
+    const int ks = u / (a.batch * per);
+    rest = u - ks * a.batch * per;
     q.kb0 = ks * a.kb_split;
     q.kb1 = min(w.kbs, q.kb0 + a.kb_split);
   }
-  q.b = rest / a.tiles;
+  q.b = rest / per;
+  rest -= q.b * per;
   int i, j;
-  triangle(rest - q.b * a.tiles, (a.m + BM - 1) / BM, i, j);
+  triangle(rest / per_block, (a.m + BM - 1) / BM, i, j);
   q.m0 = i * BM;
-  q.n0 = j * BM;
+  q.n0 = j * BM + rest % per_block * w.bn;
   q.diag = i == j;
   return q;
 }
@@ -290,156 +298,224 @@ __device__ __forceinline__ bool epi_any(bool v) {
   return r != 0;
 }
 
-// 32 consecutive values of a row as hi and lo planes; nv of them exist.
-__device__ __forceinline__ void store_split(__half* hi, __half* lo, const float (&v)[32], int nv) {
-  if (nv >= 32) {
+// ---- epilogue input and output ------------------------------------------------------
+// A warp's 32 rows x 64 bytes of a row-major matrix, lane = row.  Global
+// accesses take 8 rows x 64 bytes per instruction and pass through the warp's
+// staging rows: one row per lane, 16 bytes of each, would touch 32 lines per
+// instruction (that made the update's epilogue 12 us a tile, three times its
+// products).  rows, bytes: how much of the block exists.
+__device__ __forceinline__ void rows_issue(uint4 (&x)[4], const void* p, long long ld, int rows,
+                                           int bytes) {
+  const int lane = threadIdx.x & 31, piece = (lane & 3) * 16;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint4 h, l;
-      split2(v[8 * i], v[8 * i + 1], h.x, l.x);
-      split2(v[8 * i + 2], v[8 * i + 3], h.y, l.y);
-      split2(v[8 * i + 4], v[8 * i + 5], h.z, l.z);
-      split2(v[8 * i + 6], v[8 * i + 7], h.w, l.w);
-      *(uint4*)(hi + 8 * i) = h;
-      *(uint4*)(lo + 8 * i) = l;
-    }
-    return;
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    x[i] = r < rows && piece < bytes ? *(const uint4*)((const char*)p + r * ld + piece)
+                                     : make_uint4(0, 0, 0, 0);
   }
+}
+__device__ __forceinline__ void rows_finish(unsigned char* stg, const uint4 (&x)[4],
+                                            uint4 (&q)[4]) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    uint32_t h, l;
-    split2(v[2 * i], v[2 * i + 1], h, l);
-    if (2 * i < nv) {
-      ((unsigned short*)hi)[2 * i] = (unsigned short)h;
-      ((unsigned short*)lo)[2 * i] = (unsigned short)l;
-    }
-    if (2 * i + 1 < nv) {
-      ((unsigned short*)hi)[2 * i + 1] = (unsigned short)(h >> 16);
-      ((unsigned short*)lo)[2 * i + 1] = (unsigned short)(l >> 16);
+  for (int i = 0; i < 4; ++i)
+    *(uint4*)(stg + (i * 8 + (lane >> 2)) * PITCH + (lane & 3) * 16) = x[i];
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q[i] = *(const uint4*)(stg + lane * PITCH + i * 16);
+}
+__device__ __forceinline__ void rows_store(unsigned char* stg, const uint4 (&q)[4], void* p,
+                                           long long ld, int rows, int bytes) {
+  const int lane = threadIdx.x & 31, piece = (lane & 3) * 16;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) *(uint4*)(stg + lane * PITCH + i * 16) = q[i];
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    if (r < rows && piece < bytes)
+      *(uint4*)((char*)p + r * ld + piece) = *(const uint4*)(stg + r * PITCH + piece);
+  }
+}
+
+// 32 scaled values as 64 bytes of hi and of lo
+__device__ __forceinline__ void split32(const float (&v)[32], uint4 (&h)[4], uint4 (&l)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    split2(v[8 * i], v[8 * i + 1], h[i].x, l[i].x);
+    split2(v[8 * i + 2], v[8 * i + 3], h[i].y, l[i].y);
+    split2(v[8 * i + 4], v[8 * i + 5], h[i].z, l[i].z);
+    split2(v[8 * i + 6], v[8 * i + 7], h[i].w, l[i].w);
+  }
+}
+__device__ __forceinline__ void add_halves(const uint4 (&q)[4], float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 x = unpack_h2(w[k]);
+      v[8 * i + 2 * k] += x.x;
+      v[8 * i + 2 * k + 1] += x.y;
     }
   }
 }
 
-// The transposed copy: value j goes to row j of the planes, at this lane's
-// column (a warp's lanes are 32 neighbouring columns).
-__device__ __forceinline__ void store_split_t(__half* hi, __half* lo, long long ld,
-                                              const float (&v)[32], int nv) {
+// The transposed copy of a warp's block: value j of every lane goes to row j,
+// at this lane's column (neighbouring lanes, neighbouring columns); nv rows
+// exist, and this lane's column does.
+__device__ __forceinline__ void store_t(__half* p, long long ld, const uint4 (&q)[4], int nv) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    uint32_t h, l;
-    split2(v[2 * i], v[2 * i + 1], h, l);
-    if (2 * i < nv) {
-      ((unsigned short*)hi)[2 * i * ld] = (unsigned short)h;
-      ((unsigned short*)lo)[2 * i * ld] = (unsigned short)l;
-    }
-    if (2 * i + 1 < nv) {
-      ((unsigned short*)hi)[(2 * i + 1) * ld] = (unsigned short)(h >> 16);
-      ((unsigned short*)lo)[(2 * i + 1) * ld] = (unsigned short)(l >> 16);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = 8 * i + 2 * k;
+      if (j < nv) ((unsigned short*)p)[j * ld] = (unsigned short)w[k];
+      if (j + 1 < nv) ((unsigned short*)p)[(j + 1) * ld] = (unsigned short)(w[k] >> 16);
     }
   }
 }
 
-// v[j] = hi + lo (scaled) of 32 consecutive values; 0 past nv.
-__device__ __forceinline__ void load_split(const __half* hi, const __half* lo, float (&v)[32],
-                                           int nv) {
-  if (nv >= 32) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 h = *(const uint4*)(hi + 8 * i), l = *(const uint4*)(lo + 8 * i);
-      const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 x = unpack_h2(hw[k]), y = unpack_h2(lw[k]);
-        v[8 * i + 2 * k] = x.x + y.x;
-        v[8 * i + 2 * k + 1] = x.y + y.y;
-      }
-    }
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 32; ++j)
-    v[j] = j < nv ? __half2float(hi[j]) + __half2float(lo[j]) : 0.f;
+// What the epilogue of a 32 x 32 block needs besides its products: S (poly) or
+// X (update), asked for before the products are done.
+struct Ahead {
+  uint4 hi[4], lo[4];
+};
+
+struct Block {  // a warp's 32 x 32 block of a product
+  int row0, col0, rows, cols;  // rows and columns of it that exist
+};
+__device__ __forceinline__ Block block_of(const OrthArgs& a, const Work& w, const Unit& q, int lrow0,
+                                          int lcol0) {
+  Block k;
+  k.row0 = q.m0 + lrow0;
+  k.col0 = q.n0 + lcol0;
+  k.rows = (w.kind == UPDATE ? a.rows : a.m) - k.row0;
+  k.cols = (w.kind == UPDATE ? a.cols : a.m) - k.col0;
+  return k;
 }
 
-// One 32-column piece of an accumulator row: v holds the products of row
-// `row`, columns col0 .. col0 + 31.
-__device__ __forceinline__ void finish(const OrthArgs& a, const Work& w, const Unit& q, int step,
-                                       int cur, float (&v)[32], int row, int col0, int lrow,
-                                       int lcol) {
+// (Planes' rows are padded to 16 bytes with zeros, which stay zeros: whole
+// 16-byte pieces are read and written.)
+__device__ __forceinline__ int plane_bytes(const Block& k) { return (k.cols + 7) / 8 * 16; }
+
+__device__ __forceinline__ void look_ahead(const OrthArgs& a, const Work& w, const Unit& q, int cur,
+                                           const Block& k, Ahead& h) {
+  if (w.kind == GRAM) return;
+  const __half *hi, *lo;
+  long long ld, at;
   if (w.kind == UPDATE) {
-    const int nv = min(32, a.cols - col0);
-    if (row >= a.rows || nv <= 0) return;
-    const long long at = ((long long)q.b * a.rows + row) * a.ldx + col0;
-    float x[32];
-    load_split(a.X[cur][0] + at, a.X[cur][1] + at, x, nv);
+    hi = a.X[cur][0]; lo = a.X[cur][1]; ld = a.ldx;
+    at = ((long long)q.b * a.rows + k.row0) * ld + k.col0;
+  } else {
+    hi = a.S[0]; lo = a.S[1]; ld = a.ldm;
+    at = ((long long)q.b * a.m + k.row0) * ld + k.col0;
+  }
+  rows_issue(h.hi, hi + at, ld * 2, k.rows, plane_bytes(k));
+  rows_issue(h.lo, lo + at, ld * 2, k.rows, plane_bytes(k));
+}
+
+// v: the products of the block's row `lane`.
+__device__ __forceinline__ void finish(const OrthArgs& a, const Work& w, const Unit& q, int unit,
+                                       int step, int cur, float (&v)[32], const Ahead& ahead,
+                                       const Block& k, int lrow0, int lcol0, unsigned char* stg) {
+  const int lane = threadIdx.x & 31;
+  uint4 h[4], l[4];
+  if (w.kind == GRAM && a.splits > 1) {
+    float* p = a.part + ((long long)unit * BM + lrow0) * w.bn + lcol0;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float* x = v + 16 * half + 4 * i;
+        h[i] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                          __float_as_uint(x[3]));
+      }
+      rows_store(stg, h, p + 16 * half, w.bn * 4, 32, 64);
+    }
+    return;
+  }
+  if (k.rows <= 0 || k.cols <= 0) return;  // (the same for the whole warp)
+  float x[32];
+  if (w.kind != GRAM) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) x[j] = 0.f;
+    rows_finish(stg, ahead.hi, h);
+    add_halves(h, x);
+    rows_finish(stg, ahead.lo, h);
+    add_halves(h, x);
+  }
+  if (w.kind == UPDATE) {
     const float f = kA + shift_of(step);
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = fmaf(f, x[j], v[j] * (1.f / (1 << PE)));
     if (step + 1 < a.steps) {
-      store_split(a.X[cur ^ 1][0] + at, a.X[cur ^ 1][1] + at, v, nv);
+      const long long at = ((long long)q.b * a.rows + k.row0) * a.ldx + k.col0;
+      split32(v, h, l);
+      rows_store(stg, h, a.X[cur ^ 1][0] + at, a.ldx * 2, k.rows, plane_bytes(k));
+      rows_store(stg, l, a.X[cur ^ 1][1] + at, a.ldx * 2, k.rows, plane_bytes(k));
       return;
     }
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] *= 1.f / (1 << XE);
-    const long long o = q.b * a.out_batch + row * a.out_ld + col0;
-    if (a.out_f32) {
-      float* p = (float*)a.O + o;
-      if (nv == 32 && ((uintptr_t)p & 15) == 0) {
+    const long long o = q.b * a.out_batch + k.row0 * a.out_ld + k.col0;
+    if (!a.out_vec) {
+      if (lane >= k.rows) return;
 #pragma unroll
-        for (int j = 0; j < 32; j += 4)
-          *(float4*)(p + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-      } else {
+      for (int j = 0; j < 32; ++j) {
+        if (j >= k.cols) continue;
+        if (a.out_f32) ((float*)a.O)[o + lane * a.out_ld + j] = v[j];
+        else ((__nv_bfloat16*)a.O)[o + lane * a.out_ld + j] = __float2bfloat16_rn(v[j]);
+      }
+    } else if (a.out_f32) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j < nv) p[j] = v[j];
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float* y = v + 16 * half + 4 * i;
+          h[i] = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
+                            __float_as_uint(y[3]));
+        }
+        rows_store(stg, h, (float*)a.O + o + 16 * half, a.out_ld * 4, k.rows,
+                   (k.cols - 16 * half) * 4);
       }
     } else {
-      __nv_bfloat16* p = (__nv_bfloat16*)a.O + o;
-      if (nv == 32 && ((uintptr_t)p & 15) == 0) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 8)
-          *(uint4*)(p + j) = make_uint4(
-              ptx::pack_bf16x2(v[j], v[j + 1]), ptx::pack_bf16x2(v[j + 2], v[j + 3]),
-              ptx::pack_bf16x2(v[j + 4], v[j + 5]), ptx::pack_bf16x2(v[j + 6], v[j + 7]));
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j < nv) p[j] = __float2bfloat16_rn(v[j]);
+      for (int i = 0; i < 4; ++i) {
+        const float* y = v + 8 * i;
+        h[i] = make_uint4(ptx::pack_bf16x2(y[0], y[1]), ptx::pack_bf16x2(y[2], y[3]),
+                          ptx::pack_bf16x2(y[4], y[5]), ptx::pack_bf16x2(y[6], y[7]));
       }
+      rows_store(stg, h, (__nv_bfloat16*)a.O + o, a.out_ld * 2, k.rows, k.cols * 2);
     }
     return;
   }
-  if (w.kind == GRAM && a.splits > 1) {
-    float* p = a.part + (long long)q.tile * (BM * BM) + lrow * BM + lcol;
-#pragma unroll
-    for (int j = 0; j < 32; j += 4)
-      *(float4*)(p + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-    return;
-  }
-  const int nv = min(32, a.m - col0);
-  if (row >= a.m || nv <= 0) return;
-  const long long base = (long long)q.b * a.m * a.ldm, at = base + row * a.ldm + col0;
-  __half *hi = a.S[0], *lo = a.S[1];
+  __half* const* out = a.S;
+  bool lo = true;
   if (w.kind == GRAM) {
     const float f = 1.f / (1 << (2 * XE - SE));
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] *= f;
   } else {
-    float s[32];
-    load_split(a.S[0] + at, a.S[1] + at, s, nv);
     const float fs = kB / (1 << (SE - PE)), fp = kC / (1 << (2 * SE - PE));
     const float d = shift_of(step) * (1 << PE);
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-      v[j] = fmaf(fs, s[j], v[j] * fp) - (row == col0 + j ? d : 0.f);
-    hi = a.P[0];
-    lo = a.P[1];
+      v[j] = fmaf(fs, x[j], v[j] * fp) - (k.row0 + lane == k.col0 + j ? d : 0.f);
+    out = a.P;
+    lo = a.exact;  // (the update's one term takes P's hi alone)
   }
-  store_split(hi + at, lo + at, v, nv);
-  if (!q.diag) {
-    const long long t = base + col0 * a.ldm + row;
-    store_split_t(hi + t, lo + t, a.ldm, v, nv);
-  }
+  split32(v, h, l);
+  const long long base = (long long)q.b * a.m * a.ldm, at = base + k.row0 * a.ldm + k.col0;
+  const long long t = base + k.col0 * a.ldm + k.row0 + lane;
+  rows_store(stg, h, out[0] + at, a.ldm * 2, k.rows, plane_bytes(k));
+  if (!q.diag && lane < k.rows) store_t(out[0] + t, a.ldm, h, k.cols);
+  if (!lo) return;
+  rows_store(stg, l, out[1] + at, a.ldm * 2, k.rows, plane_bytes(k));
+  if (!q.diag && lane < k.rows) store_t(out[1] + t, a.ldm, l, k.cols);
 }
 
 // 1 / (|G|_F + eps) of matrix b, the same in every lane (0 for a matrix of
@@ -451,7 +527,12 @@ __device__ __forceinline__ float inverse_norm(const OrthArgs& a, int b) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (!isfinite(s)) return __int_as_float(0x7fc00000);
-  const float n = (float)sqrt(s) + a.eps;
+  // square root in fp32 of the sum scaled by an even power of two (fp64 square
+  // roots and divisions take microseconds here)
+  const int e = (((int)(__double2hiint(s) >> 20) & 0x7ff) - 1023) & ~1;
+  const float r = s > 0 ? ldexpf(sqrtf((float)(s * __hiloint2double((1023 - e) << 20, 0))), e / 2)
+                        : 0.f;
+  const float n = r + a.eps;
   return n > 0.f ? 1.f / n : 0.f;
 }
 
@@ -501,36 +582,60 @@ __device__ __forceinline__ void convert(const OrthArgs& a, int tid, int nthreads
 }
 
 // S from the gram partial tiles, summed in the order of the K ranges: a warp
-// takes a 32 x 32 piece, lane = column.
+// takes 8 rows x 32 columns, lane = column, four ranges' loads in flight.
 __device__ __forceinline__ void join_gram(const OrthArgs& a, int warp, int nwarps) {
-  const int lane = threadIdx.x & 31, nt = (a.m + BM - 1) / BM;
-  const int items = a.batch * a.tiles * 16;
+  const int lane = threadIdx.x & 31, nt = (a.m + BM - 1) / BM, bn = a.bn[0];
+  const int per_block = BM / bn, per_unit = 16 * (bn / 32);
+  const int units = a.batch * a.blocks * per_block;
   const float f = 1.f / (1 << (2 * XE - SE));
-  for (int it = warp; it < items; it += nwarps) {
-    const int tile = it >> 4, rb = (it >> 2) & 3, cb = it & 3;
-    const int b = tile / a.tiles;
+  const long long step = (long long)units * BM * bn;
+  for (int it = warp; it < units * per_unit; it += nwarps) {
+    const int unit = it / per_unit, piece = it - unit * per_unit;
+    const int rg = piece & 15, cb = piece >> 4;
+    const int b = unit / (a.blocks * per_block), rest = unit - b * a.blocks * per_block;
     int i, j;
-    triangle(tile - b * a.tiles, nt, i, j);
-    const int row0 = i * BM + rb * 32, col = j * BM + cb * 32 + lane;
-    if (row0 >= a.m || j * BM + cb * 32 >= a.m) continue;
-    const float* p = a.part + (long long)tile * (BM * BM) + rb * 32 * BM + cb * 32 + lane;
-    const long long step = (long long)a.batch * a.tiles * (BM * BM);
-    float v[32];
+    triangle(rest / per_block, nt, i, j);
+    const int row0 = i * BM + rg * 8, colb = j * BM + rest % per_block * bn + cb * 32;
+    const int col = colb + lane;
+    if (row0 >= a.m || colb >= a.m) continue;
+    const float* p = a.part + ((long long)unit * BM + rg * 8) * bn + cb * 32 + lane;
+    float v[8] = {};
+    int k = 0;
+    for (; k + 4 <= a.splits; k += 4, p += 4 * step) {
+      float x[4][8];
 #pragma unroll
-    for (int r = 0; r < 32; ++r) v[r] = 0.f;
-    for (int k = 0; k < a.splits; ++k, p += step) {
+      for (int u = 0; u < 4; ++u)
 #pragma unroll
-      for (int r = 0; r < 32; ++r) v[r] += __ldcg(p + r * BM);
+        for (int r = 0; r < 8; ++r) x[u][r] = __ldcg(p + u * step + r * bn);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[r] += x[u][r];
     }
+    for (; k < a.splits; ++k, p += step) {
 #pragma unroll
-    for (int r = 0; r < 32; ++r) v[r] *= f;
-    if (col >= a.m) continue;
-    const int nv = min(32, a.m - row0);
+      for (int r = 0; r < 8; ++r) v[r] += __ldcg(p + r * bn);
+    }
+    if (col >= a.ldm) continue;
+    uint4 h, l;
+    split2(v[0] * f, v[1] * f, h.x, l.x);
+    split2(v[2] * f, v[3] * f, h.y, l.y);
+    split2(v[4] * f, v[5] * f, h.z, l.z);
+    split2(v[6] * f, v[7] * f, h.w, l.w);
     const long long base = (long long)b * a.m * a.ldm;
-    store_split_t(a.S[0] + base + row0 * a.ldm + col, a.S[1] + base + row0 * a.ldm + col, a.ldm, v,
-                  nv);
-    if (i != j)
-      store_split(a.S[0] + base + col * a.ldm + row0, a.S[1] + base + col * a.ldm + row0, v, nv);
+    const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      if (row0 + r >= a.m) break;
+      const long long at = base + (row0 + r) * a.ldm + col;
+      ((unsigned short*)a.S[0])[at] = (unsigned short)(hw[r / 2] >> (16 * (r & 1)));
+      ((unsigned short*)a.S[1])[at] = (unsigned short)(lw[r / 2] >> (16 * (r & 1)));
+    }
+    if (i != j && col < a.m) {  // (the eight rows, past m zeros, are one 16-byte piece)
+      const long long at = base + col * a.ldm + row0;
+      *(uint4*)(a.S[0] + at) = h;
+      *(uint4*)(a.S[1] + at) = l;
+    }
   }
 }
 
@@ -539,9 +644,10 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem =
       (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint64_t* full = (uint64_t*)(smem + STAGES * STAGE_BYTES);
-  uint64_t* empty = full + STAGES;
-  uint64_t* acc_full = empty + STAGES;
+  unsigned char* staging = smem + RING;
+  uint64_t* full = (uint64_t*)(staging + EPI_WARPS * STG);
+  uint64_t* empty = full + MAX_STAGES;
+  uint64_t* acc_full = empty + MAX_STAGES;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* done_bar = acc_empty + 2;
   uint32_t* tmem_holder = (uint32_t*)(done_bar + 1);
@@ -549,7 +655,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < MAX_STAGES; ++s) {
       ptx::mbar_init(&full[s], 1);
       ptx::mbar_init(&empty[s], 1);
     }
@@ -570,15 +676,13 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const int phases_per_step = a.splits > 1 ? 4 : 3;  // gram, (join,) poly, update
-
+  // Every product lays its own stages over the ring, from stage 0 on (the grid
+  // barrier before it says that the ring is idle); `par` has each stage
+  // barrier's parity.
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
     if (ptx::elect_one()) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int issued[STAGES];
-#pragma unroll
-      for (int s = 0; s < STAGES; ++s) issued[s] = -1;
+      uint32_t par = 0, used = 0;
       for (int g = 0; g < 3 * a.steps && !*abort_flag; ++g) {
         const int step = g / 3, kind = g - 3 * step;
         const int ph = 1 + step * phases_per_step + (kind ? kind + phases_per_step - 3 : 0);
@@ -589,82 +693,90 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
           break;
         }
         fence_proxy_async();
+        int stage = 0;
         for (int u = cta; u < w.units && !*abort_flag; u += ctas) {
           const Unit q = unit_of(a, w, u);
-          for (int v = q.kb0 * w.terms; v < q.kb1 * w.terms; ++v) {
-            const int kb = v / w.terms, term = v - kb * w.terms;
-            if (!ptx::mbar_wait(&empty[stage], phase ^ 1, WAIT_NS)) {
+          for (int kb = q.kb0; kb < q.kb1; ++kb) {
+            if (!ptx::mbar_wait(&empty[stage], (par >> stage & 1) ^ 1, WAIT_NS)) {
               give_up(a, abort_flag);
               break;
             }
-            ptx::mbar_arrive_expect_tx(&full[stage], A_BYTES + w.bn * BK * 2);
-            unsigned char* sa = smem + stage * STAGE_BYTES;
-            unsigned char* sb = sa + A_BYTES;
-            const CUtensorMap* ma = &maps.m[w.a_buf][term == 2];
-            const CUtensorMap* mb = &maps.m[w.b_buf][term == 1];
+            ptx::mbar_arrive_expect_tx(&full[stage], w.stage_bytes);
+            unsigned char* d = smem + stage * w.stage_bytes;
             // boxes of 64 x 64: K-major rows (k, row), MN-major rows (row, k)
+            for (int pl = 0; pl <= w.fat; ++pl) {
 #pragma unroll
-            for (int j = 0; j < BM / 64; ++j) {
-              const int r = q.m0 + 64 * j;
-              tma_load_3d(sa + j * 8192, ma, &full[stage], w.a_mn ? r : kb * BK,
-                          w.a_mn ? kb * BK : r, q.b);
+              for (int j = 0; j < BM / 64; ++j, d += BOX) {
+                const int r = q.m0 + 64 * j;
+                tma_load_3d(d, &maps.m[w.a_buf][pl], &full[stage], w.a_mn ? r : kb * BK,
+                            w.a_mn ? kb * BK : r, q.b);
+              }
             }
-            for (int j = 0; j < w.bn / 64; ++j) {
-              const int r = q.n0 + 64 * j;
-              tma_load_3d(sb + j * 8192, mb, &full[stage], w.b_mn ? r : kb * BK,
-                          w.b_mn ? kb * BK : r, q.b);
+            for (int pl = 0; pl <= w.fat; ++pl) {
+              for (int j = 0; j < w.bn / 64; ++j, d += BOX) {
+                const int r = q.n0 + 64 * j;
+                tma_load_3d(d, &maps.m[w.b_buf][pl], &full[stage], w.b_mn ? r : kb * BK,
+                            w.b_mn ? kb * BK : r, q.b);
+              }
             }
-#pragma unroll
-            for (int s = 0; s < STAGES; ++s)
-              if (s == stage) issued[s] = (int)phase;
-            if (++stage == STAGES) { stage = 0; phase ^= 1; }
+            par ^= 1u << stage;
+            used |= 1u << stage;
+            if (++stage == w.stages) stage = 0;
           }
         }
       }
       // every load issued has landed before the block may end
-#pragma unroll
-      for (int s = 0; s < STAGES; ++s)
-        if (issued[s] >= 0 && !ptx::mbar_wait(&full[s], (uint32_t)issued[s], WAIT_NS))
+      for (int s = 0; s < MAX_STAGES; ++s)
+        if (used >> s & 1 && !ptx::mbar_wait(&full[s], (par >> s & 1) ^ 1, WAIT_NS))
           give_up(a, abort_flag);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
     if (ptx::elect_one()) {
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
+      uint32_t par = 0, acc_phase = 0;
+      int acc = 0;
       for (int g = 0; g < 3 * a.steps && !*abort_flag; ++g) {
         const int step = g / 3, kind = g - 3 * step;
         const Work w = work_of(a, kind, step & 1);
         const uint32_t idesc = idesc_f16(w.bn, w.a_mn, w.b_mn);
+        const uint32_t plane_a = BM * BK * 2, plane_b = w.bn * BK * 2;
+        int stage = 0;
         for (int u = cta; u < w.units && !*abort_flag; u += ctas) {
           const Unit q = unit_of(a, w, u);
-          // (a block may wait here while others finish the product before: the
-          // limit is that of its own loads, so this wait allows for theirs)
+          // (these waits allow for the other blocks' products before as well)
           if (!ptx::mbar_wait(&acc_empty[acc], acc_phase ^ 1, 4 * WAIT_NS)) {
             give_up(a, abort_flag);
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t d = tmem + acc * BN_MAX;
+          const uint32_t d = tmem + acc * 256;
           bool ok = true;
-          for (int v = q.kb0 * w.terms; v < q.kb1 * w.terms; ++v) {
-            if (!ptx::mbar_wait(&full[stage], phase, 4 * WAIT_NS)) {
+          for (int kb = q.kb0; kb < q.kb1; ++kb) {
+            if (!ptx::mbar_wait(&full[stage], par >> stage & 1, 4 * WAIT_NS)) {
               give_up(a, abort_flag);
               ok = false;
               break;
             }
             ptx::tc_fence_after();
-            const uint32_t a0 = ptx::smem_u32(smem + stage * STAGE_BYTES), b0 = a0 + A_BYTES;
-            const int ksteps = min(BK / 16, (w.K - v / w.terms * BK + 15) / 16);
+            const uint32_t a0 = ptx::smem_u32(smem + stage * w.stage_bytes);
+            const uint32_t b0 = a0 + (plane_a << w.fat);
+            const int ksteps = min(BK / 16, (w.K - kb * BK + 15) / 16);
             for (int k = 0; k < ksteps; ++k) {
-              const uint64_t ad = w.a_mn ? ptx::sdesc_sw128(a0 + k * 2048, 8192, 1024)
-                                         : ptx::sdesc_sw128(a0 + k * 32, 16, 1024);
-              const uint64_t bd = w.b_mn ? ptx::sdesc_sw128(b0 + k * 2048, 8192, 1024)
-                                         : ptx::sdesc_sw128(b0 + k * 32, 16, 1024);
-              ptx::mma_bf16(d, ad, bd, idesc, v > q.kb0 * w.terms || k > 0);
+              const uint32_t ao = w.a_mn ? k * 2048 : k * 32, bo = w.b_mn ? k * 2048 : k * 32;
+              const uint32_t al = w.a_mn ? 8192 : 16, bl = w.b_mn ? 8192 : 16;
+              const uint64_t ah = ptx::sdesc_sw128(a0 + ao, al, 1024);
+              const uint64_t bh = ptx::sdesc_sw128(b0 + bo, bl, 1024);
+              const uint32_t more = kb > q.kb0 || k > 0;
+              ptx::mma_bf16(d, ah, bh, idesc, more);
+              if (w.fat) {
+                ptx::mma_bf16(d + 128, ah, ptx::sdesc_sw128(b0 + plane_b + bo, bl, 1024), idesc,
+                              more);
+                ptx::mma_bf16(d + 128, ptx::sdesc_sw128(a0 + plane_a + ao, al, 1024), bh, idesc, 1);
+              }
             }
             ptx::mma_commit(&empty[stage]);
-            if (++stage == STAGES) { stage = 0; phase ^= 1; }
+            par ^= 1u << stage;
+            if (++stage == w.stages) stage = 0;
           }
           if (!ok) break;
           ptx::mma_commit(&acc_full[acc]);
@@ -679,15 +791,16 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
     // ---------------------------------------------------------------- epilogue
     const int et = threadIdx.x - 64, ew = et >> 5;
     const int sub = warp & 3, half = ew >> 2;
+    unsigned char* stg = staging + ew * STG;
     int acc = 0;
     uint32_t acc_phase = 0;
     unsigned ph = 0;
-    // all of the block's writes of this phase, then one arrival for the block
+    // One arrival for the block, after all of its writes of this phase (the
+    // barrier orders the other threads' writes before thread 0's release).
     auto arrive = [&]() {
-      fence_proxy_async();
-      __threadfence();
       ptx::named_barrier(1, 32 * EPI_WARPS);
       if (et == 0) {
+        __threadfence();
         asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.counter) : "memory");
       }
       ++ph;
@@ -695,9 +808,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
     auto wait = [&]() {
       const bool late = et == 0 && !grid_wait(a, ph * ctas, abort_flag);
       if (late) give_up(a, abort_flag);
-      const bool ok = !epi_any(late);
-      __threadfence();
-      return ok;
+      return !epi_any(late);
     };
     if (a.in_f32) convert<float>(a, cta * 32 * EPI_WARPS + et, ctas * 32 * EPI_WARPS);
     else convert<__nv_bfloat16>(a, cta * 32 * EPI_WARPS + et, ctas * 32 * EPI_WARPS);
@@ -709,21 +820,39 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
       if (!(ok = wait())) break;
       for (int u = cta; u < w.units && ok; u += ctas) {
         const Unit q = unit_of(a, w, u);
+        Ahead ahead;
+        Block k = block_of(a, w, q, sub * 32, half * 32);
+        look_ahead(a, w, q, step & 1, k, ahead);
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(&acc_full[acc], acc_phase, 4 * WAIT_NS));
         if (!ok) {
           give_up(a, abort_flag);
           break;
         }
         ptx::tc_fence_after();
-        const uint32_t t0 = tmem + acc * BN_MAX + ((uint32_t)(sub * 32) << 16);
-        const int lrow = sub * 32 + lane;
+        const uint32_t t0 = tmem + acc * 256 + ((uint32_t)(sub * 32) << 16);
 #pragma unroll 1
         for (int c = half; c < w.bn / 32; c += 2) {
           float v[32];
           ptx::tmem_ld32(t0 + c * 32, v);
-          ptx::tmem_ld_wait();
-          ptx::reg_fence32(v);
-          finish(a, w, q, step, step & 1, v, q.m0 + lrow, q.n0 + c * 32, lrow, c * 32);
+          if (w.fat) {
+            float x[32];
+            ptx::tmem_ld32(t0 + 128 + c * 32, x);
+            ptx::tmem_ld_wait();
+            ptx::reg_fence32(v);
+            ptx::reg_fence32(x);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] += x[j];
+          } else {
+            ptx::tmem_ld_wait();
+            ptx::reg_fence32(v);
+          }
+          const Ahead now = ahead;
+          const Block kn = k;
+          if (c + 2 < w.bn / 32) {
+            k = block_of(a, w, q, sub * 32, (c + 2) * 32);
+            look_ahead(a, w, q, step & 1, k, ahead);
+          }
+          finish(a, w, q, u, step, step & 1, v, now, kn, sub * 32, c * 32, stg);
           __syncwarp();
         }
         ptx::tc_fence_before();
@@ -807,25 +936,32 @@ bool orth_plan(const rnnt_orth_dims* d, OrthPlan* p) {
   a.ldx = cdiv(a.cols, 8) * 8;
   a.ldm = cdiv(a.m, 8) * 8;
   const long long nt = cdiv(a.m, BM);
-  a.tiles = (int)(nt * (nt + 1) / 2);
+  a.blocks = (int)(nt * (nt + 1) / 2);
   // exact products where the result is fp32; for small matrices they cost
-  // nothing (a product's time is its latency)
-  a.terms = a.out_f32 || a.m <= 256 ? 3 : 1;
-  // gram: K in as many ranges as there are SMs for its tiles, eight K blocks
-  // at least (a range's partial tile costs as much as four)
+  // little (a product's time is its latency)
+  a.exact = a.out_f32 || a.m <= 256;
+  // gram: K in as many ranges as there are SMs for its blocks, eight K blocks
+  // at least (a range's partial tile costs as much as four); without ranges,
+  // and for poly, 64-wide tiles while they fit the SMs once: a product's time
+  // is then a tile's, and half the tile takes half of it
   const int kbs = (int)cdiv(a.n, BK);
-  const long long gu = (long long)a.batch * a.tiles;
+  const long long gu = (long long)a.batch * a.blocks;
   a.splits = (int)std::max<long long>(1, std::min<long long>(kSms / std::max(1LL, gu), kbs / 8));
   a.kb_split = (int)cdiv(kbs, a.splits);
   a.splits = (int)cdiv(kbs, a.kb_split);
-  // update: 256-wide tiles when they fill the SMs
+  a.bn[POLY] = 2 * gu <= kSms ? 64 : 128;
+  a.bn[GRAM] = a.splits == 1 ? a.bn[POLY] : 128;
+  // update: the widest tiles that fill the SMs (exact ones keep a second
+  // accumulator: 128 at most)
   const int un = a.tall ? a.m : a.n, um = a.tall ? a.n : a.m;
   a.ut_m = (int)cdiv(um, BM);
-  a.bn = (long long)a.batch * a.ut_m * cdiv(un, 256) >= kSms ? 256 : 128;
-  a.ut_n = (int)cdiv(un, a.bn);
-  const long long units =
-      std::max(gu * a.splits, (long long)a.batch * a.ut_m * a.ut_n);
-  if ((long long)a.batch * a.ut_m * a.ut_n > 2147483647LL || gu * 16 > 2147483647LL) return false;
+  auto tiles = [&](int bn) { return (long long)a.batch * a.ut_m * cdiv(un, bn); };
+  a.bn[UPDATE] = !a.exact && tiles(256) >= kSms ? 256 : tiles(128) >= kSms ? 128 : 64;
+  a.ut_n = (int)cdiv(un, a.bn[UPDATE]);
+  const long long gram_units = gu * (BM / a.bn[GRAM]) * a.splits;
+  const long long units = std::max(
+      {gram_units, gu * (BM / a.bn[POLY]), (long long)a.batch * a.ut_m * a.ut_n});
+  if (tiles(64) > 2147483647LL || gram_units * 64 > 2147483647LL) return false;
   p->ctas = (int)std::min<long long>(kSms, units);
   a.nb = (int)std::min<long long>(std::max<long long>(1, (long long)a.rows * a.cols / 4096), 256);
   const size_t x = 2 * (size_t)a.batch * a.rows * a.ldx, s = 2 * (size_t)a.batch * a.m * a.ldm;
@@ -835,7 +971,7 @@ bool orth_plan(const rnnt_orth_dims* d, OrthPlan* p) {
     for (int j = 0; j < 2; ++j) p->w_X[i][j] = put(x);
   for (int j = 0; j < 2; ++j) p->w_S[j] = put(s);
   for (int j = 0; j < 2; ++j) p->w_P[j] = put(s);
-  p->w_part = put(a.splits > 1 ? 4 * (size_t)(gu * a.splits) * BM * BM : 0);
+  p->w_part = put(a.splits > 1 ? 4 * (size_t)gram_units * BM * a.bn[GRAM] : 0);
   p->w_sums = put(8 * (size_t)a.batch * a.nb);
   p->w_sync = put(8);
   p->total = o;
@@ -916,6 +1052,9 @@ rnnt_status rnnt_orth(const rnnt_orth_dims* dims, const void* G, void* O, void* 
   a.counter = (unsigned*)(w + p.w_sync);
   a.abort = (int*)(w + p.w_sync) + 1;
   a.G = G; a.O = O; a.status = status;
+  const int per16 = a.out_f32 ? 4 : 8;
+  a.out_vec = aligned_to(O, 16) && a.cols % per16 == 0 && a.out_ld % per16 == 0 &&
+              (a.batch == 1 || a.out_batch % per16 == 0);
   cudaStream_t st = (cudaStream_t)stream;
   ProfScope ps("orth", st);
   ps.set_kernels(2);
