@@ -701,22 +701,26 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
               give_up(a, abort_flag);
               break;
             }
-            ptx::mbar_arrive_expect_tx(&full[stage], w.stage_bytes);
+            // (a block on the diagonal multiplies its rows by themselves: one load)
+            ptx::mbar_arrive_expect_tx(&full[stage],
+                                       q.diag ? BM * BK * 2 << w.fat : w.stage_bytes);
             unsigned char* d = smem + stage * w.stage_bytes;
             // boxes of 64 x 64: K-major rows (k, row), MN-major rows (row, k)
-            for (int pl = 0; pl <= w.fat; ++pl) {
-#pragma unroll
-              for (int j = 0; j < BM / 64; ++j, d += BOX) {
-                const int r = q.m0 + 64 * j;
-                tma_load_3d(d, &maps.m[w.a_buf][pl], &full[stage], w.a_mn ? r : kb * BK,
-                            w.a_mn ? kb * BK : r, q.b);
-              }
+            const int k0 = kb * BK;
+            for (int pl = 0; pl <= w.fat; ++pl, d += 2 * BOX) {
+              const CUtensorMap* m = &maps.m[w.a_buf][pl];
+              tma_load_3d(d, m, &full[stage], w.a_mn ? q.m0 : k0, w.a_mn ? k0 : q.m0, q.b);
+              tma_load_3d(d + BOX, m, &full[stage], w.a_mn ? q.m0 + 64 : k0,
+                          w.a_mn ? k0 : q.m0 + 64, q.b);
             }
-            for (int pl = 0; pl <= w.fat; ++pl) {
-              for (int j = 0; j < w.bn / 64; ++j, d += BOX) {
+            for (int pl = 0; pl <= w.fat && !q.diag; ++pl) {
+              const CUtensorMap* m = &maps.m[w.b_buf][pl];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (64 * j >= w.bn) break;
                 const int r = q.n0 + 64 * j;
-                tma_load_3d(d, &maps.m[w.b_buf][pl], &full[stage], w.b_mn ? r : kb * BK,
-                            w.b_mn ? kb * BK : r, q.b);
+                tma_load_3d(d, m, &full[stage], w.b_mn ? r : k0, w.b_mn ? k0 : r, q.b);
+                d += BOX;
               }
             }
             par ^= 1u << stage;
@@ -739,7 +743,13 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
         const int step = g / 3, kind = g - 3 * step;
         const Work w = work_of(a, kind, step & 1);
         const uint32_t idesc = idesc_f16(w.bn, w.a_mn, w.b_mn);
-        const uint32_t plane_a = BM * BK * 2, plane_b = w.bn * BK * 2;
+        // 16-byte units: planes, one K step of 16 in each layout, and the
+        // descriptors without their address
+        const uint32_t plane_a = BM * BK * 2 / 16, plane_b = w.bn * BK * 2 / 16;
+        const uint32_t step_a = w.a_mn ? 128 : 2, step_b = w.b_mn ? 128 : 2;
+        const uint64_t desc_a = ptx::sdesc_sw128(0, w.a_mn ? 8192 : 16, 1024);
+        const uint64_t desc_b = ptx::sdesc_sw128(0, w.b_mn ? 8192 : 16, 1024);
+        const uint32_t smem_a = ptx::smem_u32(smem);
         int stage = 0;
         for (int u = cta; u < w.units && !*abort_flag; u += ctas) {
           const Unit q = unit_of(a, w, u);
@@ -758,20 +768,30 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
               break;
             }
             ptx::tc_fence_after();
-            const uint32_t a0 = ptx::smem_u32(smem + stage * w.stage_bytes);
-            const uint32_t b0 = a0 + (plane_a << w.fat);
+            // (one thread issues every MMA: descriptors are stepped, not built)
+            const uint64_t sa = (smem_a + stage * w.stage_bytes) >> 4;
+            const uint64_t ah = desc_a + sa, al = ah + plane_a;
+            const uint64_t bh = desc_b + sa + (q.diag ? (q.n0 - q.m0) * (BK * 2 / 16)
+                                                      : plane_a << w.fat);
+            const uint64_t bl = bh + (q.diag ? plane_a : plane_b);
             const int ksteps = min(BK / 16, (w.K - kb * BK + 15) / 16);
-            for (int k = 0; k < ksteps; ++k) {
-              const uint32_t ao = w.a_mn ? k * 2048 : k * 32, bo = w.b_mn ? k * 2048 : k * 32;
-              const uint32_t al = w.a_mn ? 8192 : 16, bl = w.b_mn ? 8192 : 16;
-              const uint64_t ah = ptx::sdesc_sw128(a0 + ao, al, 1024);
-              const uint64_t bh = ptx::sdesc_sw128(b0 + bo, bl, 1024);
-              const uint32_t more = kb > q.kb0 || k > 0;
-              ptx::mma_bf16(d, ah, bh, idesc, more);
-              if (w.fat) {
-                ptx::mma_bf16(d + 128, ah, ptx::sdesc_sw128(b0 + plane_b + bo, bl, 1024), idesc,
-                              more);
-                ptx::mma_bf16(d + 128, ptx::sdesc_sw128(a0 + plane_a + ao, al, 1024), bh, idesc, 1);
+            uint32_t more = kb > q.kb0;
+            if (w.fat) {
+#pragma unroll
+              for (int k = 0; k < BK / 16; ++k) {
+                if (k >= ksteps) break;
+                const uint64_t ka = k * step_a, kb_ = k * step_b;
+                ptx::mma_bf16(d, ah + ka, bh + kb_, idesc, more);
+                ptx::mma_bf16(d + 128, ah + ka, bl + kb_, idesc, more);
+                ptx::mma_bf16(d + 128, al + ka, bh + kb_, idesc, 1);
+                more = 1;
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < BK / 16; ++k) {
+                if (k >= ksteps) break;
+                ptx::mma_bf16(d, ah + k * step_a, bh + k * step_b, idesc, more);
+                more = 1;
               }
             }
             ptx::mma_commit(&empty[stage]);
@@ -951,12 +971,16 @@ bool orth_plan(const rnnt_orth_dims* d, OrthPlan* p) {
   a.splits = (int)cdiv(kbs, a.kb_split);
   a.bn[POLY] = 2 * gu <= kSms ? 64 : 128;
   a.bn[GRAM] = a.splits == 1 ? a.bn[POLY] : 128;
-  // update: the widest tiles that fill the SMs (exact ones keep a second
-  // accumulator: 128 at most)
+  // update: the width whose rounds over the SMs load the fewest operand rows (an
+  // SM takes in about 96 GB/s whatever the stage, which bounds every product
+  // here); exact ones keep a second accumulator: 128 at most
   const int un = a.tall ? a.m : a.n, um = a.tall ? a.n : a.m;
   a.ut_m = (int)cdiv(um, BM);
   auto tiles = [&](int bn) { return (long long)a.batch * a.ut_m * cdiv(un, bn); };
-  a.bn[UPDATE] = !a.exact && tiles(256) >= kSms ? 256 : tiles(128) >= kSms ? 128 : 64;
+  auto rows = [&](int bn) { return cdiv(tiles(bn), kSms) * (BM + bn); };
+  a.bn[UPDATE] = 64;
+  for (int bn = 128; bn <= (a.exact ? 128 : 256); bn *= 2)
+    if (rows(bn) <= rows(a.bn[UPDATE])) a.bn[UPDATE] = bn;
   a.ut_n = (int)cdiv(un, a.bn[UPDATE]);
   const long long gram_units = gu * (BM / a.bn[GRAM]) * a.splits;
   const long long units = std::max(
