@@ -68,7 +68,10 @@ struct OrthArgs {
   __half* X[2][2];
   __half* S[2];
   __half* P[2];
-  float* part;          // gram partial tiles [splits][batch][tiles][128][bn]
+  int thin;             // blocks per matrix of k_orth_thin (0: k_orth)
+  float* part;          // gram partial tiles [splits][batch][tiles][128][bn];
+                        // k_orth_thin: [batch][thin][128][128]
+  float* sum;           // k_orth_thin: their sum [batch][128][128]
   int blocks;           // 128 x 128 blocks on and above the diagonal of S
   int splits, kb_split; // gram: K ranges and their length in K blocks
   int bn[3];            // tile width of each product
@@ -83,7 +86,7 @@ struct OrthArgs {
   float eps;
   const double* sums;   // [batch][nb] partial sums of squares
   int nb;
-  unsigned* counter;    // grid barrier: arrivals so far
+  unsigned* counter;    // grid barriers: arrivals so far (one per matrix; k_orth has one)
   int* abort;
   int32_t* status;
 };
@@ -96,9 +99,9 @@ template <typename T>
 __global__ void __launch_bounds__(256)
 k_orth_sumsq(OrthArgs a, double* sums) {
   __shared__ double part[8];
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
-    *a.counter = 0;
-    *a.abort = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.counter[blockIdx.y] = 0;
+    if (blockIdx.y == 0) *a.abort = 0;
   }
   const T* g = (const T*)a.G + blockIdx.y * a.in_batch;
   const int chunks = (a.cols + 7) / 8;  // of eight columns
@@ -265,11 +268,11 @@ __device__ __forceinline__ Unit unit_of(const OrthArgs& a, const Work& w, int u)
 
 // Wait until `target` blocks have arrived at the grid barrier in all.
 __device__ __forceinline__ bool grid_wait(const OrthArgs& a, unsigned target,
-                                          volatile int* abort_flag) {
+                                          volatile int* abort_flag, int b = 0) {
   uint64_t t0 = 0;
   for (int i = 0;; ++i) {
     unsigned v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a.counter) : "memory");
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a.counter + b) : "memory");
     if (v >= target) return true;
     if ((i & 63) == 63) {
       if (*abort_flag || *(volatile int*)a.abort) return false;
@@ -895,6 +898,319 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
   if (warp == 1) ptx::tmem_dealloc(tmem, 512);
 }
 
+// ---- thin matrices --------------------------------------------------------------------
+// m <= 128: everything stays on chip.  A block keeps 128 columns of X (rows of a
+// tall one, transposed on the way in and out) as hi and lo in shared memory, in
+// the swizzled layout that serves both as the K-major operand of its share of
+// S and as the MN-major operand of its share of P X; S, then P over it, have the
+// same layout.  So a product is three MMA chains and a pass of the 128 x 128
+// accumulator through registers, about 0.7 us, against 4.4 us through global
+// memory and a grid barrier; only the blocks' shares of S meet there, once per
+// step.  All products exact.
+constexpr int THIN_THREADS = 256;
+constexpr int IMG = 128 * 128 * 2;           // bytes of a 128 x 128 plane: two 64-column blocks
+constexpr int THIN_SMEM = 1024 + 4 * IMG + 256;
+
+// byte of (row, col) in a plane, col a multiple of 8
+__device__ __forceinline__ uint32_t img_at(int row, int col) {
+  return (col >> 6) * (IMG / 2) + row * 128 + (((col >> 3 & 7) ^ (row & 7)) << 4);
+}
+
+// v of (row, col0 .. col0 + 31) as hi and lo, to or from the planes at p
+__device__ __forceinline__ void img_store(unsigned char* p, int row, int col0,
+                                          const float (&v)[32]) {
+  uint4 h[4], l[4];
+  split32(v, h, l);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t at = img_at(row, col0 + 8 * i);
+    *(uint4*)(p + at) = h[i];
+    *(uint4*)(p + IMG + at) = l[i];
+  }
+}
+__device__ __forceinline__ void img_load(const unsigned char* p, int row, int col0,
+                                         float (&v)[32]) {
+  uint4 h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t at = img_at(row, col0 + 8 * i);
+    h[i] = *(const uint4*)(p + at);
+    l[i] = *(const uint4*)(p + IMG + at);
+  }
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = 0.f;
+  add_halves(h, v);
+  add_halves(l, v);
+}
+
+// Eight consecutive elements of a row of G, those past nv 0.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int nv, bool vec, float (&v)[8]) {
+  if (vec && nv >= 8) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 x = __ldg((const float4*)p), y = __ldg((const float4*)p + 1);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+      v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+    } else {
+      const uint4 x = __ldg((const uint4*)p);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[2 * k] = ptx::bf16lo(w[k]);
+        v[2 * k + 1] = ptx::bf16hi(w[k]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = k < nv ? to_f<T>(p[k]) : 0.f;
+  }
+}
+
+// The block's columns j0 .. of X into the planes at p (zeros outside).
+template <typename T>
+__device__ __forceinline__ void thin_load(const OrthArgs& a, int b, int j0, unsigned char* p) {
+  const T* g = (const T*)a.G + b * a.in_batch;
+  const bool vec = a.in_ld % 8 == 0 && a.in_batch % 8 == 0 && ((uintptr_t)a.G & 15) == 0;
+  const float f = inverse_norm(a, b) * (1 << XE);
+  for (int t = threadIdx.x; t < 128 * 16; t += THIN_THREADS) {
+    // eight neighbours in memory: columns of a row of X, or (tall) rows of a column
+    const int line = t >> 4, c = (t & 15) * 8;
+    const int lines = a.tall ? a.n - j0 : a.m, left = (a.tall ? a.m : a.n - j0) - c;
+    float v[8] = {};
+    if (line < lines && left > 0)
+      load8<T>(a.tall ? g + (j0 + line) * a.in_ld + c : g + line * a.in_ld + j0 + c, left, vec, v);
+    uint4 h, l;
+    split2(v[0] * f, v[1] * f, h.x, l.x);
+    split2(v[2] * f, v[3] * f, h.y, l.y);
+    split2(v[4] * f, v[5] * f, h.z, l.z);
+    split2(v[6] * f, v[7] * f, h.w, l.w);
+    if (!a.tall) {
+      const uint32_t at = img_at(line, c);
+      *(uint4*)(p + at) = h;
+      *(uint4*)(p + IMG + at) = l;
+    } else {
+      const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t at = img_at(c + k, line & ~7) + (line & 7) * 2;
+        *(unsigned short*)(p + at) = (unsigned short)(hw[k / 2] >> (16 * (k & 1)));
+        *(unsigned short*)(p + IMG + at) = (unsigned short)(lw[k / 2] >> (16 * (k & 1)));
+      }
+    }
+  }
+}
+
+// D += A B^T over `ksteps` steps of 16, three terms: hi hi at d, the small ones
+// at d + 128.  A K-major at pa; B K-major or MN-major (b_mn) at pb.
+__device__ __forceinline__ void thin_mma(uint32_t d, uint32_t pa, uint32_t pb, int b_mn, int n,
+                                         int ksteps) {
+  const uint32_t idesc = idesc_f16(n, 0, b_mn);
+  for (int k = 0; k < ksteps; ++k) {
+    const uint32_t ko = (k >> 2) * (IMG / 2) + (k & 3) * 32;
+    const uint64_t ah = ptx::sdesc_sw128(pa + ko, 16, 1024);
+    const uint64_t al = ptx::sdesc_sw128(pa + IMG + ko, 16, 1024);
+    const uint64_t bh = b_mn ? ptx::sdesc_sw128(pb + k * 2048, IMG / 2, 1024)
+                             : ptx::sdesc_sw128(pb + ko, 16, 1024);
+    const uint64_t bl = b_mn ? ptx::sdesc_sw128(pb + IMG + k * 2048, IMG / 2, 1024)
+                             : ptx::sdesc_sw128(pb + IMG + ko, 16, 1024);
+    ptx::mma_bf16(d, ah, bh, idesc, k > 0);
+    ptx::mma_bf16(d + 128, ah, bl, idesc, k > 0);
+    ptx::mma_bf16(d + 128, al, bh, idesc, 1);
+  }
+}
+
+// The blocks' shares of S, summed: block c of `blocks` adds slice c of all
+// shares [blocks][m][128], in order of the blocks (eight ranges of them, one
+// per warp, when there are many).
+__device__ __forceinline__ void thin_reduce(const float* part, float* sum, int c, int blocks, int m,
+                                            float4 (*tmp)[32]) {
+  const int groups = m * 32, per = (groups + blocks - 1) / blocks;
+  const int g0 = c * per, g1 = min(groups, g0 + per);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float4* p = (const float4*)part;
+  auto add = [](float4& s, const float4& x) {
+    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+  };
+  if (blocks < 16) {
+    for (int g = g0 + threadIdx.x; g < g1; g += THIN_THREADS) {
+      float4 s = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+      for (int k = 0; k < blocks; ++k) add(s, __ldcg(p + (long long)k * 4096 + g));
+      ((float4*)sum)[g] = s;
+    }
+    return;
+  }
+  const int range = (blocks + 7) / 8, k0 = warp * range, k1 = min(blocks, k0 + range);
+  for (int gb = g0; gb < g1; gb += 32) {
+    const int g = gb + lane;
+    float4 s = make_float4(0, 0, 0, 0);
+    if (g < g1) {
+#pragma unroll 8
+      for (int k = k0; k < k1; ++k) add(s, __ldcg(p + (long long)k * 4096 + g));
+    }
+    tmp[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && g < g1) {
+      for (int w = 1; w < 8; ++w) add(s, tmp[w][lane]);
+      ((float4*)sum)[g] = s;
+    }
+    __syncthreads();
+  }
+}
+
+__global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ float4 tmp[8][32];
+  __shared__ __align__(8) uint64_t bar[1];
+  __shared__ uint32_t tmem_holder[1];
+  __shared__ int abort_s;
+  unsigned char* X = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  unsigned char* S = X + 2 * IMG;  // S, then P
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x / a.thin, c = blockIdx.x - b * a.thin;
+  const int j0 = c * 128, nc = min(128, a.n - j0);
+  const int row = (warp & 3) * 32 + lane, cbase = (warp >> 2) * 64;
+  if (tid == 0) {
+    ptx::mbar_init(bar, 1);
+    ptx::fence_mbar_init();
+    abort_s = 0;
+  }
+  if (warp == 0) {
+    ptx::tmem_alloc(tmem_holder, 256);
+    ptx::tmem_relinquish();
+  }
+  if (a.in_f32) thin_load<float>(a, b, j0, X);
+  else thin_load<__nv_bfloat16>(a, b, j0, X);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t xs = ptx::smem_u32(X), ss = ptx::smem_u32(S);
+  const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+  const int mk = (a.m + 15) / 16, nk = (nc + 15) / 16;  // K steps over m and over the columns
+  uint32_t parity = 0;
+  // One product: thread 0 issues it once the block's writes are visible to the
+  // tensor cores; afterwards the accumulator is there for every thread.
+  auto product = [&](uint32_t pa, uint32_t pb, int b_mn, int n, int ksteps) {
+    ptx::fence_proxy_async_smem();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (tid == 0) {
+      thin_mma(tmem, pa, pb, b_mn, n, ksteps);
+      ptx::mma_commit(bar);
+    }
+    __syncwarp();
+    if (!ptx::mbar_wait(bar, parity, WAIT_NS)) report(a.status, RNNT_ERR_TIMEOUT);
+    __syncwarp();
+    parity ^= 1;
+    ptx::tc_fence_after();
+  };
+  auto acc32 = [&](int col0, float (&v)[32]) {
+    float x[32];
+    ptx::tmem_ld32(lanes + col0, v);
+    ptx::tmem_ld32(lanes + 128 + col0, x);
+    ptx::tmem_ld_wait();
+    ptx::reg_fence32(v);
+    ptx::reg_fence32(x);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] += x[j];
+  };
+  unsigned arrivals = 0;
+  auto meet = [&]() {
+    __syncthreads();
+    arrivals += a.thin;
+    if (tid == 0) {
+      __threadfence();
+      asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.counter + b) : "memory");
+      if (!abort_s && !grid_wait(a, arrivals, &abort_s, b)) give_up(a, &abort_s);
+    }
+    __syncthreads();
+  };
+  float* part = a.part + (long long)b * a.thin * 128 * 128;
+  float* sum = a.sum + (long long)b * 128 * 128;
+#pragma unroll 1
+  for (int step = 0; step < a.steps; ++step) {
+    // S
+    product(xs, xs, 0, mk * 16, nk);
+    const float fs = 1.f / (1 << (2 * XE - SE));
+    if (a.thin > 1) {  // (stored by columns: lanes are rows)
+#pragma unroll 1
+      for (int c0 = cbase; c0 < min(cbase + 64, a.m); c0 += 32) {
+        float v[32];
+        acc32(c0, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (c0 + j < a.m) part[((long long)c * 128 + c0 + j) * 128 + row] = v[j];
+      }
+      meet();
+      thin_reduce(part, sum, c, a.thin, a.m, tmp);
+      meet();
+    }
+#pragma unroll 1
+    for (int c0 = cbase; c0 < min(cbase + 64, mk * 16); c0 += 32) {
+      float v[32];
+      if (a.thin > 1) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = c0 + j < a.m ? __ldcg(sum + (c0 + j) * 128 + row) : 0.f;
+      } else {
+        acc32(c0, v);
+      }
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = c0 + j < a.m ? v[j] * fs : 0.f;
+      img_store(S, row, c0, v);
+    }
+    // P, over S
+    product(ss, ss, 0, mk * 16, mk);
+    const float ps = kB / (1 << (SE - PE)), pp = kC / (1 << (2 * SE - PE));
+    const float d = shift_of(step) * (1 << PE);
+#pragma unroll 1
+    for (int c0 = cbase; c0 < min(cbase + 64, mk * 16); c0 += 32) {
+      float v[32], x[32];
+      acc32(c0, v);
+      img_load(S, row, c0, x);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        v[j] = fmaf(ps, x[j], v[j] * pp) - (row == c0 + j ? d : 0.f);
+        if (row >= a.m || c0 + j >= a.m) v[j] = 0.f;
+      }
+      img_store(S, row, c0, v);
+    }
+    // X
+    product(ss, xs, 1, nk * 16, mk);
+    const float f = kA + shift_of(step);
+#pragma unroll 1
+    for (int c0 = cbase; c0 < min(cbase + 64, nk * 16); c0 += 32) {
+      float v[32], x[32];
+      acc32(c0, v);
+      img_load(X, row, c0, x);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        v[j] = fmaf(f, x[j], v[j] * (1.f / (1 << PE)));
+        if (c0 + j >= nc) v[j] = 0.f;
+      }
+      if (step + 1 < a.steps) {
+        img_store(X, row, c0, v);
+        continue;
+      }
+      if (row >= a.m) continue;
+      const long long o = b * a.out_batch;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        if (c0 + j >= nc) continue;
+        const long long at = o + (a.tall ? (j0 + c0 + j) * a.out_ld + row
+                                         : row * a.out_ld + j0 + c0 + j);
+        if (a.out_f32) ((float*)a.O)[at] = v[j] * (1.f / (1 << XE));
+        else ((__nv_bfloat16*)a.O)[at] = __float2bfloat16_rn(v[j] * (1.f / (1 << XE)));
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 0) ptx::tmem_dealloc(tmem, 256);
+}
+
 // ---- host ------------------------------------------------------------------------------
 PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -927,7 +1243,7 @@ bool make_map(CUtensorMap* m, const void* p, long long rows, long long cols, lon
 struct OrthPlan {
   OrthArgs a;
   int ctas;
-  size_t w_X[2][2], w_S[2], w_P[2], w_part, w_sums, w_sync, total;
+  size_t w_X[2][2], w_S[2], w_P[2], w_part, w_sum, w_sums, w_sync, total;
 };
 
 constexpr int kSms = 152;  // (the plan may not depend on the device that runs it)
@@ -988,22 +1304,63 @@ bool orth_plan(const rnnt_orth_dims* d, OrthPlan* p) {
   if (tiles(64) > 2147483647LL || gram_units * 64 > 2147483647LL) return false;
   p->ctas = (int)std::min<long long>(kSms, units);
   a.nb = (int)std::min<long long>(std::max<long long>(1, (long long)a.rows * a.cols / 4096), 256);
-  const size_t x = 2 * (size_t)a.batch * a.rows * a.ldx, s = 2 * (size_t)a.batch * a.m * a.ldm;
+  // thin: a block per 128 columns; more than one per matrix wait for one another
+  // and have to be resident together
+  const long long thin = cdiv(a.n, 128);
+  a.thin = a.m <= 128 && (thin == 1 || thin * a.batch <= kSms) ? (int)thin : 0;
+  const size_t x = a.thin ? 0 : 2 * (size_t)a.batch * a.rows * a.ldx;
+  const size_t s = a.thin ? 0 : 2 * (size_t)a.batch * a.m * a.ldm;
   size_t o = 0;
   auto put = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes); return at; };
   for (int i = 0; i < 2; ++i)
     for (int j = 0; j < 2; ++j) p->w_X[i][j] = put(x);
   for (int j = 0; j < 2; ++j) p->w_S[j] = put(s);
   for (int j = 0; j < 2; ++j) p->w_P[j] = put(s);
-  p->w_part = put(a.splits > 1 ? 4 * (size_t)gram_units * BM * a.bn[GRAM] : 0);
+  p->w_part = put(a.thin > 1 ? 4 * (size_t)a.batch * a.thin * 128 * 128
+                  : !a.thin && a.splits > 1 ? 4 * (size_t)gram_units * BM * a.bn[GRAM] : 0);
+  p->w_sum = put(a.thin > 1 ? 4 * (size_t)a.batch * 128 * 128 : 0);
   p->w_sums = put(8 * (size_t)a.batch * a.nb);
-  p->w_sync = put(8);
+  p->w_sync = put(4 * (size_t)a.batch + 4);
   p->total = o;
   return true;
 }
 
+// Blocks that wait for one another are all resident at once: a cooperative launch.
+template <typename... KA, typename... A>
+cudaError_t launch_resident(void (*k)(KA...), bool together, int grid, int threads, size_t smem,
+                            cudaStream_t st, const A&... args) {
+  static std::atomic<bool> opted_in[kDeviceSlots];  // per kernel (its signature) and device
+  std::atomic<bool>& opted = opted_in[device_slot()];
+  if (!opted.load()) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    opted.store(true);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeCooperative;
+  at[0].val.cooperative = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = together ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
 cudaError_t orth_launch(OrthPlan& p, cudaStream_t st) {
   OrthArgs& a = p.a;
+  double* sums = const_cast<double*>(a.sums);
+  const dim3 grid(a.nb, a.batch);
+  if (a.in_f32) k_orth_sumsq<float><<<grid, 256, 0, st>>>(a, sums);
+  else k_orth_sumsq<__nv_bfloat16><<<grid, 256, 0, st>>>(a, sums);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (a.thin)
+    return launch_resident(k_orth_thin, a.thin > 1, a.thin * a.batch, THIN_THREADS, THIN_SMEM, st,
+                           a);
   OrthMaps maps;
   for (int j = 0; j < 2; ++j) {
     for (int i = 0; i < 2; ++i)
@@ -1013,32 +1370,7 @@ cudaError_t orth_launch(OrthPlan& p, cudaStream_t st) {
         !make_map(&maps.m[BUF_P][j], a.P[j], a.m, a.m, a.ldm, a.batch))
       return cudaErrorInvalidValue;
   }
-  static std::atomic<bool> opted_in[kDeviceSlots];
-  std::atomic<bool>& opted = opted_in[device_slot()];
-  if (!opted.load()) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(k_orth, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-    if (e != cudaSuccess) return e;
-    opted.store(true);
-  }
-  double* sums = const_cast<double*>(a.sums);
-  const dim3 grid(a.nb, a.batch);
-  if (a.in_f32) k_orth_sumsq<float><<<grid, 256, 0, st>>>(a, sums);
-  else k_orth_sumsq<__nv_bfloat16><<<grid, 256, 0, st>>>(a, sums);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // all blocks are resident at once (they wait for one another): cooperative
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeCooperative;
-  at[0].val.cooperative = 1;
-  cfg.gridDim = dim3(std::min(p.ctas, num_sms()));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = SMEM;
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_orth, maps, a);
+  return launch_resident(k_orth, true, std::min(p.ctas, num_sms()), THREADS, SMEM, st, maps, a);
 }
 
 }  // namespace
@@ -1072,9 +1404,10 @@ rnnt_status rnnt_orth(const rnnt_orth_dims* dims, const void* G, void* O, void* 
     a.P[j] = (__half*)(w + p.w_P[j]);
   }
   a.part = (float*)(w + p.w_part);
+  a.sum = (float*)(w + p.w_sum);
   a.sums = (const double*)(w + p.w_sums);
   a.counter = (unsigned*)(w + p.w_sync);
-  a.abort = (int*)(w + p.w_sync) + 1;
+  a.abort = (int*)(w + p.w_sync) + a.batch;
   a.G = G; a.O = O; a.status = status;
   const int per16 = a.out_f32 ? 4 : 8;
   a.out_vec = aligned_to(O, 16) && a.cols % per16 == 0 && a.out_ld % per16 == 0 &&
