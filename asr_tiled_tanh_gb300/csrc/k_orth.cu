@@ -232,7 +232,10 @@ __device__ __forceinline__ Work work_of(const OrthArgs& a, int kind, int cur) {
   }
   w.kbs = (w.K + BK - 1) / BK;
   w.stage_bytes = (BM + w.bn) * BK * 2 << w.fat;
-  w.stages = min(MAX_STAGES, RING / w.stage_bytes);
+  // (the widest tiles' epilogue is the longer part of their product: a fourth
+  // stage would only load ahead of it, against its own accesses: 503 against 478 us
+  // at 16384 x 1024)
+  w.stages = min(w.bn > 128 ? 3 : MAX_STAGES, RING / w.stage_bytes);
   return w;
 }
 
@@ -1312,8 +1315,11 @@ bool orth_plan(const rnnt_orth_dims* d, OrthPlan* p) {
   const size_t s = a.thin ? 0 : 2 * (size_t)a.batch * a.m * a.ldm;
   size_t o = 0;
   auto put = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes); return at; };
+  // (fast products read no lo of X: its only reader is the thread that writes the
+  // new one, so one plane serves both buffers, and X of 16384 x 1024 stays in L2)
   for (int i = 0; i < 2; ++i)
-    for (int j = 0; j < 2; ++j) p->w_X[i][j] = put(x);
+    for (int j = 0; j < 2; ++j)
+      p->w_X[i][j] = i && j && !a.exact ? p->w_X[0][1] : put(x);
   for (int j = 0; j < 2; ++j) p->w_S[j] = put(s);
   for (int j = 0; j < 2; ++j) p->w_P[j] = put(s);
   p->w_part = put(a.thin > 1 ? 4 * (size_t)a.batch * a.thin * 128 * 128
