@@ -91,6 +91,29 @@ struct OrthArgs {
   int32_t* status;
 };
 
+// Eight consecutive elements of a row of G, those past nv 0.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int nv, bool vec, float (&v)[8]) {
+  if (vec && nv >= 8) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 x = __ldg((const float4*)p), y = __ldg((const float4*)p + 1);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+      v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+    } else {
+      const uint4 x = __ldg((const uint4*)p);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[2 * k] = ptx::bf16lo(w[k]);
+        v[2 * k + 1] = ptx::bf16hi(w[k]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = k < nv ? to_f<T>(p[k]) : 0.f;
+  }
+}
+
 // ---- sums of squares ---------------------------------------------------------------
 // Block (i, b) adds the squares of its share of matrix b: eight at a time in
 // fp32, those in fp64, so that neither 1e-18 nor 1e18 leaves the range.  Also
@@ -105,35 +128,29 @@ k_orth_sumsq(OrthArgs a, double* sums) {
   }
   const T* g = (const T*)a.G + blockIdx.y * a.in_batch;
   const int chunks = (a.cols + 7) / 8;  // of eight columns
-  const bool vec = a.cols % 8 == 0 && a.in_ld % 8 == 0 && a.in_batch % 8 == 0 &&
-                   ((uintptr_t)a.G & 15) == 0;
+  const bool vec = a.in_ld % 8 == 0 && a.in_batch % 8 == 0 && ((uintptr_t)a.G & 15) == 0;
   double s = 0;
-  const long long total = (long long)a.rows * chunks;
-  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
-    const int r = (int)(i / chunks), c = (int)(i - (long long)r * chunks) * 8;
-    const T* p = g + r * a.in_ld + c;
-    float q = 0.f;
-    if (vec) {
-      if constexpr (sizeof(T) == 4) {
-        const float4 x = __ldg((const float4*)p), y = __ldg((const float4*)p + 1);
-        q = x.x * x.x + x.y * x.y + x.z * x.z + x.w * x.w + y.x * y.x + y.y * y.y + y.z * y.z +
-            y.w * y.w;
-      } else {
-        const uint4 x = __ldg((const uint4*)p);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  const long long total = (long long)a.rows * chunks, stride = gridDim.x * 256LL;
+  for (long long i0 = blockIdx.x * 256LL + threadIdx.x; i0 < total; i0 += 4 * stride) {
+    float v[4][8];  // four chunks' loads in flight
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float lo = ptx::bf16lo(w[k]), hi = ptx::bf16hi(w[k]);
-          q += lo * lo + hi * hi;
-        }
-      }
-    } else {
-      for (int k = 0; k < 8 && c + k < a.cols; ++k) {
-        const float v = to_f<T>(p[k]);
-        q += v * v;
+    for (int u = 0; u < 4; ++u) {
+      const long long i = i0 + u * stride;
+      const int r = (int)(i / chunks), c = (int)(i - (long long)r * chunks) * 8;
+      if (i < total) {
+        load8<T>(g + r * a.in_ld + c, a.cols - c, vec, v[u]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[u][k] = 0.f;
       }
     }
-    s += (double)q;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float q = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) q = fmaf(v[u][k], v[u][k], q);
+      s += (double)q;
+    }
   }
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
@@ -542,47 +559,39 @@ __device__ __forceinline__ float inverse_norm(const OrthArgs& a, int b) {
   return n > 0.f ? 1.f / n : 0.f;
 }
 
-// X = G / (|G|_F + eps) as hi and lo planes (epilogue warps of all blocks).
+// X = G / (|G|_F + eps) as hi and lo planes (epilogue warps of all blocks), four
+// chunks of eight in flight.
 template <typename T>
 __device__ __forceinline__ void convert(const OrthArgs& a, int tid, int nthreads) {
   const int chunks = (a.cols + 7) / 8;
-  const bool vec = a.cols % 8 == 0 && a.in_ld % 8 == 0 && a.in_batch % 8 == 0 &&
-                   ((uintptr_t)a.G & 15) == 0;
+  const bool vec = a.in_ld % 8 == 0 && a.in_batch % 8 == 0 && ((uintptr_t)a.G & 15) == 0;
   const long long per = (long long)a.rows * chunks;
   for (int b = 0; b < a.batch; ++b) {
     const float f = inverse_norm(a, b) * (1 << XE);
-    for (long long i = tid; i < per; i += nthreads) {
-      const int r = (int)(i / chunks), c = (int)(i - (long long)r * chunks) * 8;
-      const T* p = (const T*)a.G + b * a.in_batch + r * a.in_ld + c;
-      const int nv = min(8, a.cols - c);
-      float v[8];
-      if (vec) {
-        if constexpr (sizeof(T) == 4) {
-          const float4 x = __ldg((const float4*)p), y = __ldg((const float4*)p + 1);
-          v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-          v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-        } else {
-          const uint4 x = __ldg((const uint4*)p);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    for (long long i0 = tid; i0 < per; i0 += 4LL * nthreads) {
+      float v[4][8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            v[2 * k] = ptx::bf16lo(w[k]);
-            v[2 * k + 1] = ptx::bf16hi(w[k]);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = k < nv ? to_f<T>(p[k]) : 0.f;
+      for (int u = 0; u < 4; ++u) {
+        const long long i = i0 + (long long)u * nthreads;
+        const int r = (int)(i / chunks), c = (int)(i - (long long)r * chunks) * 8;
+        if (i < per)
+          load8<T>((const T*)a.G + b * a.in_batch + r * a.in_ld + c, a.cols - c, vec, v[u]);
       }
-      uint4 h, l;
-      split2(v[0] * f, v[1] * f, h.x, l.x);
-      split2(v[2] * f, v[3] * f, h.y, l.y);
-      split2(v[4] * f, v[5] * f, h.z, l.z);
-      split2(v[6] * f, v[7] * f, h.w, l.w);
-      // (columns past the matrix, up to the row stride, hold zeros)
-      const long long at = ((long long)b * a.rows + r) * a.ldx + c;
-      *(uint4*)(a.X[0][0] + at) = h;
-      *(uint4*)(a.X[0][1] + at) = l;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const long long i = i0 + (long long)u * nthreads;
+        if (i >= per) break;
+        const int r = (int)(i / chunks), c = (int)(i - (long long)r * chunks) * 8;
+        uint4 h, l;
+        split2(v[u][0] * f, v[u][1] * f, h.x, l.x);
+        split2(v[u][2] * f, v[u][3] * f, h.y, l.y);
+        split2(v[u][4] * f, v[u][5] * f, h.z, l.z);
+        split2(v[u][6] * f, v[u][7] * f, h.w, l.w);
+        // (columns past the matrix, up to the row stride, hold zeros)
+        const long long at = ((long long)b * a.rows + r) * a.ldx + c;
+        *(uint4*)(a.X[0][0] + at) = h;
+        *(uint4*)(a.X[0][1] + at) = l;
+      }
     }
   }
 }
@@ -946,29 +955,6 @@ __device__ __forceinline__ void img_load(const unsigned char* p, int row, int co
   add_halves(l, v);
 }
 
-// Eight consecutive elements of a row of G, those past nv 0.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int nv, bool vec, float (&v)[8]) {
-  if (vec && nv >= 8) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 x = __ldg((const float4*)p), y = __ldg((const float4*)p + 1);
-      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-      v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-    } else {
-      const uint4 x = __ldg((const uint4*)p);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[2 * k] = ptx::bf16lo(w[k]);
-        v[2 * k + 1] = ptx::bf16hi(w[k]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = k < nv ? to_f<T>(p[k]) : 0.f;
-  }
-}
-
 // The block's columns j0 .. of X into the planes at p (zeros outside).
 template <typename T>
 __device__ __forceinline__ void thin_load(const OrthArgs& a, int b, int j0, unsigned char* p) {
@@ -1306,7 +1292,7 @@ bool orth_plan(const rnnt_orth_dims* d, OrthPlan* p) {
       {gram_units, gu * (BM / a.bn[POLY]), (long long)a.batch * a.ut_m * a.ut_n});
   if (tiles(64) > 2147483647LL || gram_units * 64 > 2147483647LL) return false;
   p->ctas = (int)std::min<long long>(kSms, units);
-  a.nb = (int)std::min<long long>(std::max<long long>(1, (long long)a.rows * a.cols / 4096), 256);
+  a.nb = (int)std::min<long long>(std::max<long long>(1, (long long)a.rows * a.cols / 8192), 1216);
   // thin: a block per 128 columns; more than one per matrix wait for one another
   // and have to be resident together
   const long long thin = cdiv(a.n, 128);
