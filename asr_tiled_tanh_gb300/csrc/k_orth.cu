@@ -47,9 +47,12 @@ constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr int BM = 128, BK = 64;      // tile rows; K per stage: a 128-byte swizzle atom of fp16
 constexpr int BOX = 64 * 64 * 2;      // bytes of a TMA box
 constexpr int RING = 192 * 1024, MAX_STAGES = 8;
-constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS;
+constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS + 32;
 constexpr int PITCH = 80, STG = 32 * PITCH;  // an epilogue warp's staging rows of 64 bytes
 constexpr int SMEM = 1024 + RING + EPI_WARPS * STG + 256;
+// fast update: the ring ends here, and two 128 x 64 blocks of X (hi and lo) follow
+constexpr int XBUF_AT = 144 * 1024, XPLANE = 128 * 128, XBUF = 2 * XPLANE;
+static_assert(XBUF_AT + 2 * XBUF <= RING + EPI_WARPS * STG, "blocks of X lie in the ring and staging");
 constexpr uint64_t WAIT_NS = 2000000000ull;  // 2 s per wait, then give up
 constexpr int XE = 14, SE = 14, PE = 13;     // scale exponents of X, S and P
 
@@ -171,6 +174,13 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uin
       "l"(m), "r"(ptx::smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* src, int x, int y,
+                                             int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(m),
+      "r"(ptx::smem_u32(src)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
 // global writes of this thread become visible to TMA loads ordered after them
 __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async;" ::: "memory");
@@ -217,18 +227,20 @@ __device__ __forceinline__ void triangle(int t, int nt, int& i, int& j) {
 // digits, and three adds per K step instead of one would truncate it more).
 struct Work {
   int kind, units, kbs, K, bn, fat, a_mn, b_mn, a_buf, b_buf;
+  int boxed;  // the epilogue's X comes and goes by TMA (fast update)
   int stage_bytes, stages;
 };
 struct Unit {
   int b, m0, n0, kb0, kb1, diag;
 };
 
+template <int EXACT>
 __device__ __forceinline__ Work work_of(const OrthArgs& a, int kind, int cur) {
   Work w;
   w.kind = kind;
   w.a_mn = w.b_mn = 0;
   w.bn = kind == GRAM ? a.bn[0] : kind == POLY ? a.bn[1] : a.bn[2];
-  w.fat = a.exact;
+  w.fat = EXACT;
   const int sym = a.batch * a.blocks * (BM / w.bn);
   if (kind == GRAM) {
     w.K = a.n;
@@ -249,10 +261,8 @@ __device__ __forceinline__ Work work_of(const OrthArgs& a, int kind, int cur) {
   }
   w.kbs = (w.K + BK - 1) / BK;
   w.stage_bytes = (BM + w.bn) * BK * 2 << w.fat;
-  // (the widest tiles' epilogue is the longer part of their product: a fourth
-  // stage would only load ahead of it, against its own accesses: 503 against 478 us
-  // at 16384 x 1024)
-  w.stages = min(w.bn > 128 ? 3 : MAX_STAGES, RING / w.stage_bytes);
+  w.boxed = !EXACT && kind == UPDATE;
+  w.stages = min(MAX_STAGES, (w.boxed ? XBUF_AT : RING) / w.stage_bytes);
   return w;
 }
 
@@ -442,6 +452,7 @@ __device__ __forceinline__ void look_ahead(const OrthArgs& a, const Work& w, con
 }
 
 // v: the products of the block's row `lane`.
+template <int EXACT>
 __device__ __forceinline__ void finish(const OrthArgs& a, const Work& w, const Unit& q, int unit,
                                        int step, int cur, float (&v)[32], const Ahead& ahead,
                                        const Block& k, int lrow0, int lcol0, unsigned char* stg) {
@@ -471,7 +482,7 @@ __device__ __forceinline__ void finish(const OrthArgs& a, const Work& w, const U
     rows_finish(stg, ahead.lo, h);
     add_halves(h, x);
   }
-  if (w.kind == UPDATE) {
+  if (EXACT && w.kind == UPDATE) {  // (fast: update_box)
     const float f = kA + shift_of(step);
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = fmaf(f, x[j], v[j] * (1.f / (1 << PE)));
@@ -529,7 +540,7 @@ __device__ __forceinline__ void finish(const OrthArgs& a, const Work& w, const U
     for (int j = 0; j < 32; ++j)
       v[j] = fmaf(fs, x[j], v[j] * fp) - (k.row0 + lane == k.col0 + j ? d : 0.f);
     out = a.P;
-    lo = a.exact;  // (the update's one term takes P's hi alone)
+    lo = EXACT;  // (the update's one term takes P's hi alone)
   }
   split32(v, h, l);
   const long long base = (long long)q.b * a.m * a.ldm, at = base + k.row0 * a.ldm + k.col0;
@@ -539,6 +550,67 @@ __device__ __forceinline__ void finish(const OrthArgs& a, const Work& w, const U
   if (!lo) return;
   rows_store(stg, l, out[1] + at, a.ldm * 2, k.rows, plane_bytes(k));
   if (!q.diag && lane < k.rows) store_t(out[1] + t, a.ldm, l, k.cols);
+}
+
+// Blocks of 64 columns of a fast update's tile.
+__device__ __forceinline__ int boxes_of(const OrthArgs& a, const Work& w, const Unit& q) {
+  return min(w.bn / 64, (a.cols - q.n0 + 63) / 64);
+}
+
+// Fast update of 32 columns of the thread's row of an X block in shared memory
+// (128-byte swizzled rows, hi and lo planes): x <- f x + v in place; after the
+// last step the result to O, through the hi plane.
+__device__ __forceinline__ void update_box(const OrthArgs& a, const Unit& q, int step,
+                                           float (&v)[32], unsigned char* p, int row, int col,
+                                           int out_col) {
+  const float f = kA + shift_of(step);
+  uint4 h[4], l[4];
+  const uint32_t r0 = row * 128, sw = row & 7, c0 = col >> 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = *(const uint4*)(p + r0 + (((c0 + i) ^ sw) << 4));
+    l[i] = *(const uint4*)(p + XPLANE + r0 + (((c0 + i) ^ sw) << 4));
+  }
+  float x[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) x[j] = 0.f;
+  add_halves(h, x);
+  add_halves(l, x);
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = fmaf(f, x[j], v[j] * (1.f / (1 << PE)));
+  if (step + 1 < a.steps) {
+    split32(v, h, l);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      *(uint4*)(p + r0 + (((c0 + i) ^ sw) << 4)) = h[i];
+      *(uint4*)(p + XPLANE + r0 + (((c0 + i) ^ sw) << 4)) = l[i];
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] *= 1.f / (1 << XE);
+  __nv_bfloat16* o = (__nv_bfloat16*)a.O + q.b * a.out_batch;
+  const int cols = a.cols - out_col, lane = threadIdx.x & 31;
+  if (!a.out_vec) {
+    if (q.m0 + row >= a.rows) return;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < cols) o[(q.m0 + row) * a.out_ld + out_col + j] = __float2bfloat16_rn(v[j]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *(uint4*)(p + r0 + (((c0 + i) ^ sw) << 4)) = make_uint4(
+        ptx::pack_bf16x2(v[8 * i], v[8 * i + 1]), ptx::pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+        ptx::pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), ptx::pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = (row & ~31) + i * 8 + (lane >> 2), piece = lane & 3;
+    if (q.m0 + r < a.rows && 8 * piece < cols)
+      *(uint4*)(o + (q.m0 + r) * a.out_ld + out_col + 8 * piece) =
+          *(const uint4*)(p + r * 128 + (((c0 + piece) ^ (r & 7)) << 4));
+  }
 }
 
 // 1 / (|G|_F + eps) of matrix b, the same in every lane (0 for a matrix of
@@ -654,6 +726,7 @@ __device__ __forceinline__ void join_gram(const OrthArgs& a, int warp, int nwarp
   }
 }
 
+template <int EXACT>
 __global__ void __launch_bounds__(THREADS, 1)
 k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
   extern __shared__ unsigned char smem_raw[];
@@ -664,7 +737,10 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
   uint64_t* empty = full + MAX_STAGES;
   uint64_t* acc_full = empty + MAX_STAGES;
   uint64_t* acc_empty = acc_full + 2;
-  uint64_t* done_bar = acc_empty + 2;
+  uint64_t* x_full = acc_empty + 2;  // X blocks: loaded, done with, all stored
+  uint64_t* x_done = x_full + 2;
+  uint64_t* x_stored = x_done + 2;
+  uint64_t* done_bar = x_stored + 1;
   uint32_t* tmem_holder = (uint32_t*)(done_bar + 1);
   volatile int* abort_flag = (volatile int*)(tmem_holder + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -677,7 +753,10 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
     for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(&acc_full[s], 1);
       ptx::mbar_init(&acc_empty[s], 32 * EPI_WARPS);
+      ptx::mbar_init(&x_full[s], 1);
+      ptx::mbar_init(&x_done[s], EPI_WARPS);
     }
+    ptx::mbar_init(x_stored, 1);
     ptx::mbar_init(done_bar, 1);
     ptx::fence_mbar_init();
     *abort_flag = 0;
@@ -701,7 +780,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
       for (int g = 0; g < 3 * a.steps && !*abort_flag; ++g) {
         const int step = g / 3, kind = g - 3 * step;
         const int ph = 1 + step * phases_per_step + (kind ? kind + phases_per_step - 3 : 0);
-        const Work w = work_of(a, kind, step & 1);
+        const Work w = work_of<EXACT>(a, kind, step & 1);
         if (cta >= w.units) continue;
         if (!grid_wait(a, (unsigned)ph * ctas, abort_flag)) {
           give_up(a, abort_flag);
@@ -756,7 +835,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
       int acc = 0;
       for (int g = 0; g < 3 * a.steps && !*abort_flag; ++g) {
         const int step = g / 3, kind = g - 3 * step;
-        const Work w = work_of(a, kind, step & 1);
+        const Work w = work_of<EXACT>(a, kind, step & 1);
         const uint32_t idesc = idesc_f16(w.bn, w.a_mn, w.b_mn);
         // 16-byte units: planes, one K step of 16 in each layout, and the
         // descriptors without their address
@@ -791,7 +870,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
             const uint64_t bl = bh + (q.diag ? plane_a : plane_b);
             const int ksteps = min(BK / 16, (w.K - kb * BK + 15) / 16);
             uint32_t more = kb > q.kb0;
-            if (w.fat) {
+            if (EXACT || w.fat) {
 #pragma unroll
               for (int k = 0; k < BK / 16; ++k) {
                 if (k >= ksteps) break;
@@ -822,12 +901,71 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
       ptx::mma_commit(done_bar);
       if (!ptx::mbar_wait(done_bar, 0, WAIT_NS)) give_up(a, abort_flag);
     }
+  } else if (warp == 2 + EPI_WARPS) {
+    // ---------------------------------------------------------------- X blocks
+    // Fast update: loads the 128 x 64 blocks of X (hi and lo) that the epilogue
+    // updates in place, two at a time, and stores them to the other X.
+    if (!EXACT && ptx::elect_one()) {
+      unsigned char* xbuf = smem + XBUF_AT;
+      int n_load = 0, n_done = 0;
+      bool ok = true;
+      for (int step = 0; step < a.steps && ok; ++step) {
+        const int cur = step & 1;
+        const Work w = work_of<EXACT>(a, UPDATE, cur);
+        if (cta >= w.units) continue;
+        if (!grid_wait(a, (unsigned)((step + 1) * phases_per_step) * ctas, abort_flag)) {
+          give_up(a, abort_flag);
+          break;
+        }
+        fence_proxy_async();
+        const bool last = step + 1 == a.steps;
+        // two walks over the same blocks: the loads run two ahead of the stores
+        int lu = cta, lc = 0, su = cta, sc = 0;
+        while (ok && su < w.units) {
+          while (lu < w.units && n_load < n_done + 2) {
+            const Unit q = unit_of(a, w, lu);
+            unsigned char* d = xbuf + (n_load & 1) * XBUF;
+            uint64_t* bar = &x_full[n_load & 1];
+            ptx::mbar_arrive_expect_tx(bar, XBUF);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)  // hi rows 0-63, 64-127, lo rows 0-63, 64-127
+              tma_load_3d(d + j * BOX, &maps.m[cur][j >> 1], bar, q.n0 + 64 * lc,
+                          q.m0 + 64 * (j & 1), q.b);
+            ++n_load;
+            if (++lc == boxes_of(a, w, q)) { lc = 0; lu += ctas; }
+          }
+          const Unit q = unit_of(a, w, su);
+          if (!ptx::mbar_wait(&x_done[n_done & 1], n_done >> 1 & 1, 4 * WAIT_NS)) {
+            give_up(a, abort_flag);
+            ok = false;
+            break;
+          }
+          if (!last) {
+            const unsigned char* d = xbuf + (n_done & 1) * XBUF;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (q.m0 + 64 * (j & 1) < a.rows)
+                tma_store_3d(&maps.m[cur ^ 1][j >> 1], d + j * BOX, q.n0 + 64 * sc,
+                             q.m0 + 64 * (j & 1), q.b);
+            ptx::bulk_commit();
+            ptx::bulk_wait_read();
+          }
+          ++n_done;
+          if (++sc == boxes_of(a, w, q)) { sc = 0; su += ctas; }
+        }
+        ptx::bulk_wait_all();
+        ptx::mbar_arrive(x_stored);
+      }
+      // every load issued has landed before the block may end
+      for (int i = n_done; i < n_load; ++i)
+        if (!ptx::mbar_wait(&x_full[i & 1], i >> 1 & 1, WAIT_NS)) give_up(a, abort_flag);
+    }
   } else {
     // ---------------------------------------------------------------- epilogue
     const int et = threadIdx.x - 64, ew = et >> 5;
     const int sub = warp & 3, half = ew >> 2;
     unsigned char* stg = staging + ew * STG;
-    int acc = 0;
+    int acc = 0, n_box = 0;
     uint32_t acc_phase = 0;
     unsigned ph = 0;
     // One arrival for the block, after all of its writes of this phase (the
@@ -851,13 +989,13 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
     bool ok = true;
     for (int g = 0; g < 3 * a.steps && ok; ++g) {
       const int step = g / 3, kind = g - 3 * step;
-      const Work w = work_of(a, kind, step & 1);
+      const Work w = work_of<EXACT>(a, kind, step & 1);
       if (!(ok = wait())) break;
       for (int u = cta; u < w.units && ok; u += ctas) {
         const Unit q = unit_of(a, w, u);
         Ahead ahead;
         Block k = block_of(a, w, q, sub * 32, half * 32);
-        look_ahead(a, w, q, step & 1, k, ahead);
+        if (!w.boxed) look_ahead(a, w, q, step & 1, k, ahead);
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(&acc_full[acc], acc_phase, 4 * WAIT_NS));
         if (!ok) {
           give_up(a, abort_flag);
@@ -865,11 +1003,37 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
         }
         ptx::tc_fence_after();
         const uint32_t t0 = tmem + acc * 256 + ((uint32_t)(sub * 32) << 16);
+        if (!EXACT && w.boxed) {
+          const int boxes = boxes_of(a, w, q);
+#pragma unroll 1
+          for (int c = 0; c < boxes; ++c, ++n_box) {
+            float v[32];
+            ptx::tmem_ld32(t0 + c * 64 + half * 32, v);
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait(&x_full[n_box & 1], n_box >> 1 & 1,
+                                                        4 * WAIT_NS));
+            ptx::tmem_ld_wait();
+            ptx::reg_fence32(v);
+            if (!ok) {
+              give_up(a, abort_flag);
+              break;
+            }
+            update_box(a, q, step, v, smem + XBUF_AT + (n_box & 1) * XBUF, sub * 32 + lane,
+                       half * 32, q.n0 + c * 64 + half * 32);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&x_done[n_box & 1]);
+          }
+          if (!ok) break;
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&acc_empty[acc]);
+          if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+          continue;
+        }
 #pragma unroll 1
         for (int c = half; c < w.bn / 32; c += 2) {
           float v[32];
           ptx::tmem_ld32(t0 + c * 32, v);
-          if (w.fat) {
+          if (EXACT || w.fat) {
             float x[32];
             ptx::tmem_ld32(t0 + 128 + c * 32, x);
             ptx::tmem_ld_wait();
@@ -887,13 +1051,16 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
             k = block_of(a, w, q, sub * 32, (c + 2) * 32);
             look_ahead(a, w, q, step & 1, k, ahead);
           }
-          finish(a, w, q, u, step, step & 1, v, now, kn, sub * 32, c * 32, stg);
+          finish<EXACT>(a, w, q, u, step, step & 1, v, now, kn, sub * 32, c * 32, stg);
           __syncwarp();
         }
         ptx::tc_fence_before();
         ptx::mbar_arrive(&acc_empty[acc]);
         if (++acc == 2) { acc = 0; acc_phase ^= 1; }
       }
+      // (the X blocks are stored by another warp)
+      if (!EXACT && w.boxed && cta < w.units && ok && et == 0)
+        ok = ptx::mbar_wait(x_stored, step & 1, 4 * WAIT_NS);
       ok = !epi_any(!ok);
       if (!ok) break;
       arrive();
@@ -1318,10 +1485,10 @@ bool orth_plan(const rnnt_orth_dims* d, OrthPlan* p) {
 }
 
 // Blocks that wait for one another are all resident at once: a cooperative launch.
-template <typename... KA, typename... A>
+template <int WHICH, typename... KA, typename... A>
 cudaError_t launch_resident(void (*k)(KA...), bool together, int grid, int threads, size_t smem,
                             cudaStream_t st, const A&... args) {
-  static std::atomic<bool> opted_in[kDeviceSlots];  // per kernel (its signature) and device
+  static std::atomic<bool> opted_in[kDeviceSlots];  // per kernel (WHICH) and device
   std::atomic<bool>& opted = opted_in[device_slot()];
   if (!opted.load()) {
     const cudaError_t e =
@@ -1351,7 +1518,7 @@ cudaError_t orth_launch(OrthPlan& p, cudaStream_t st) {
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (a.thin)
-    return launch_resident(k_orth_thin, a.thin > 1, a.thin * a.batch, THIN_THREADS, THIN_SMEM, st,
+    return launch_resident<2>(k_orth_thin, a.thin > 1, a.thin * a.batch, THIN_THREADS, THIN_SMEM, st,
                            a);
   OrthMaps maps;
   for (int j = 0; j < 2; ++j) {
@@ -1362,7 +1529,9 @@ cudaError_t orth_launch(OrthPlan& p, cudaStream_t st) {
         !make_map(&maps.m[BUF_P][j], a.P[j], a.m, a.m, a.ldm, a.batch))
       return cudaErrorInvalidValue;
   }
-  return launch_resident(k_orth, true, std::min(p.ctas, num_sms()), THREADS, SMEM, st, maps, a);
+  const int blocks = std::min(p.ctas, num_sms());
+  return a.exact ? launch_resident<1>(k_orth<1>, true, blocks, THREADS, SMEM, st, maps, a)
+                 : launch_resident<0>(k_orth<0>, true, blocks, THREADS, SMEM, st, maps, a);
 }
 
 }  // namespace
