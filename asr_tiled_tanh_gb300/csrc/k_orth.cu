@@ -1161,17 +1161,19 @@ __device__ __forceinline__ void thin_load(const OrthArgs& a, int b, int j0, unsi
 __device__ __forceinline__ void thin_mma(uint32_t d, uint32_t pa, uint32_t pb, int b_mn, int n,
                                          int ksteps) {
   const uint32_t idesc = idesc_f16(n, 0, b_mn);
-  for (int k = 0; k < ksteps; ++k) {
-    const uint32_t ko = (k >> 2) * (IMG / 2) + (k & 3) * 32;
-    const uint64_t ah = ptx::sdesc_sw128(pa + ko, 16, 1024);
-    const uint64_t al = ptx::sdesc_sw128(pa + IMG + ko, 16, 1024);
-    const uint64_t bh = b_mn ? ptx::sdesc_sw128(pb + k * 2048, IMG / 2, 1024)
-                             : ptx::sdesc_sw128(pb + ko, 16, 1024);
-    const uint64_t bl = b_mn ? ptx::sdesc_sw128(pb + IMG + k * 2048, IMG / 2, 1024)
-                             : ptx::sdesc_sw128(pb + IMG + ko, 16, 1024);
-    ptx::mma_bf16(d, ah, bh, idesc, k > 0);
-    ptx::mma_bf16(d + 128, ah, bl, idesc, k > 0);
-    ptx::mma_bf16(d + 128, al, bh, idesc, 1);
+  // (one thread issues them: the descriptors are stepped, in 16-byte units)
+  const uint64_t da = ptx::sdesc_sw128(pa, 16, 1024);
+  const uint64_t db = ptx::sdesc_sw128(pb, b_mn ? IMG / 2 : 16, 1024);
+  constexpr uint32_t LO = IMG / 16, BLOCK = IMG / 32;
+  uint32_t more = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (k >= ksteps) break;
+    const uint32_t ko = (k >> 2) * BLOCK + (k & 3) * 2, kb = b_mn ? k * 128 : ko;
+    ptx::mma_bf16(d, da + ko, db + kb, idesc, more);
+    ptx::mma_bf16(d + 128, da + ko, db + kb + LO, idesc, more);
+    ptx::mma_bf16(d + 128, da + ko + LO, db + kb, idesc, 1);
+    more = 1;
   }
 }
 
@@ -1225,7 +1227,8 @@ __global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / a.thin, c = blockIdx.x - b * a.thin;
   const int j0 = c * 128, nc = min(128, a.n - j0);
-  const int row = (warp & 3) * 32 + lane, cbase = (warp >> 2) * 64;
+  // a warp's lanes are 32 rows; it takes every other 32 columns
+  const int row = (warp & 3) * 32 + lane, cbase = (warp >> 2) * 32;
   if (tid == 0) {
     ptx::mbar_init(bar, 1);
     ptx::fence_mbar_init();
@@ -1292,7 +1295,7 @@ __global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a)
     const float fs = 1.f / (1 << (2 * XE - SE));
     if (a.thin > 1) {  // (stored by columns: lanes are rows)
 #pragma unroll 1
-      for (int c0 = cbase; c0 < min(cbase + 64, a.m); c0 += 32) {
+      for (int c0 = cbase; c0 < a.m; c0 += 64) {
         float v[32];
         acc32(c0, v);
 #pragma unroll
@@ -1304,7 +1307,7 @@ __global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a)
       meet();
     }
 #pragma unroll 1
-    for (int c0 = cbase; c0 < min(cbase + 64, mk * 16); c0 += 32) {
+    for (int c0 = cbase; c0 < mk * 16; c0 += 64) {
       float v[32];
       if (a.thin > 1) {
 #pragma unroll
@@ -1321,7 +1324,7 @@ __global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a)
     const float ps = kB / (1 << (SE - PE)), pp = kC / (1 << (2 * SE - PE));
     const float d = shift_of(step) * (1 << PE);
 #pragma unroll 1
-    for (int c0 = cbase; c0 < min(cbase + 64, mk * 16); c0 += 32) {
+    for (int c0 = cbase; c0 < mk * 16; c0 += 64) {
       float v[32], x[32];
       acc32(c0, v);
       img_load(S, row, c0, x);
@@ -1336,7 +1339,7 @@ __global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a)
     product(ss, xs, 1, nk * 16, mk);
     const float f = kA + shift_of(step);
 #pragma unroll 1
-    for (int c0 = cbase; c0 < min(cbase + 64, nk * 16); c0 += 32) {
+    for (int c0 = cbase; c0 < nk * 16; c0 += 64) {
       float v[32], x[32];
       acc32(c0, v);
       img_load(X, row, c0, x);
@@ -1452,7 +1455,7 @@ bool orth_plan(const rnnt_orth_dims* d, OrthPlan* p) {
   auto rows = [&](int bn) { return cdiv(tiles(bn), kSms) * (BM + bn); };
   a.bn[UPDATE] = 64;
   for (int bn = 128; bn <= (a.exact ? 128 : 256); bn *= 2)
-    if (rows(bn) <= rows(a.bn[UPDATE])) a.bn[UPDATE] = bn;
+    if (rows(bn) < rows(a.bn[UPDATE])) a.bn[UPDATE] = bn;
   a.ut_n = (int)cdiv(un, a.bn[UPDATE]);
   const long long gram_units = gu * (BM / a.bn[GRAM]) * a.splits;
   const long long units = std::max(
