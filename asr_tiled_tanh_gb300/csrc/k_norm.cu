@@ -180,6 +180,7 @@ struct Slab {
   int nslabs;
   int uni;           // a thread's channels are of one group (and pow2): GroupSum applies
   int lanes;         // lane bits that share a group (uni)
+  int lg;            // log2 of the lanes that gather a group's sum (not uni)
   int keep;          // a block's slabs have the same channels
   int scratch;       // scratch bytes per reduced quantity
   int S_log, step_log;  // S; NT / cbv where cbv is a power of two
@@ -278,6 +279,37 @@ __device__ __forceinline__ void reduce_groups(const Slab& sl, int cg, int cb, co
       if (lane == 0) gs[q][g] += s[q];
     }
   }
+}
+
+// gs[g] = the sum over the block of the values of group g's channels: v holds one
+// per channel of the thread's column.  sl.lg lanes gather a group's values from
+// the block's, so that all groups are summed at once.
+template <int VEC>
+__device__ __forceinline__ void gather_groups(const Slab& sl, int rows, int cg,
+                                              const FastDiv& cg_div,
+                                              const float2 (&v)[kPairs(VEC)], float* scr,
+                                              float* gs) {
+#pragma unroll
+  for (int i = 0; i < kPairs(VEC); ++i) {
+    scr[2 * i * NT + threadIdx.x] = v[i].x;
+    scr[(2 * i + 1) * NT + threadIdx.x] = v[i].y;
+  }
+  __syncthreads();
+  const int sub = threadIdx.x >> sl.lg, at = threadIdx.x & ((1 << sl.lg) - 1);
+  const int n = min(rows, NT / sl.cbv_div) * cg;  // (row groups that hold frames)
+  for (int g0 = 0; g0 < sl.kk; g0 += NT >> sl.lg) {  // (the same rounds for every thread)
+    const int g = g0 + sub;
+    float s = 0.f;
+    if (g < sl.kk) {
+      for (int k = at; k < n; k += 1 << sl.lg) {
+        const int rg = k / cg_div, c = g * cg + k - rg * cg;
+        s += scr[(c % VEC) * NT + rg * sl.cbv + c / VEC];
+      }
+    }
+    for (int o = 1 << sl.lg >> 1; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (at == 0 && g < sl.kk) gs[g] = s;
+  }
+  __syncthreads();
 }
 
 // The block's slab, frames and column.
@@ -730,7 +762,7 @@ k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) 
   // slab count, so that one barrier a slab keeps writers off what is still read)
   constexpr int GK = UNI ? 1 : MAX_KK, UK = UNI ? 32 : 1;
   __shared__ float mean_s[2][GK], m2_s[2][GK], n_s[2];
-  __shared__ float gs[1][MAX_KK], mean_t[GK], rstd_t[GK];
+  __shared__ float mean_t[GK], rstd_t[GK];
   __shared__ __align__(16) float buf[2][UK][NWARPS];
   __shared__ float from[2][8][2][UK];  // (mean, M2) of every block of the cluster
   float* scr = (float*)(smem + (size_t)sl.slots * SLOT);
@@ -853,16 +885,13 @@ k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) 
       for (int half = 0; half < 2; ++half) {
         float2 acc[1][NP] = {};
         if (cnt > 0) st.out(acc, half, cnt, c, mean_s[par], a.cg_div);
-        for (int g = threadIdx.x; g < sl.kk; g += NT) gs[0][g] = 0.f;
-        const float* res = reduce_channels<1, VEC>(sl, acc, scr, w.v, w.rg, w.active);
-        reduce_groups<1, VEC>(sl, a.cg, 0, res, gs, [](int) { return 1.f; });
-        __syncthreads();
-        for (int g = threadIdx.x; g < sl.kk; g += NT) {
-          if (half == 0) mean_s[par][g] = w.rows ? gs[0][g] / n : 0.f;
-          else m2_s[par][g] = gs[0][g];
+        gather_groups<VEC>(sl, w.rows, a.cg, a.cg_div, acc[0], scr, half ? m2_s[par] : mean_s[par]);
+        if (half == 0) {
+          for (int g = threadIdx.x; g < sl.kk; g += NT)
+            mean_s[par][g] = w.rows ? mean_s[par][g] / n : 0.f;
+          if (threadIdx.x == 0) n_s[par] = n;
+          __syncthreads();
         }
-        if (threadIdx.x == 0) n_s[par] = n;
-        __syncthreads();
       }
       if (sl.S > 1) {
         cluster_arrive();
@@ -1042,12 +1071,16 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
         k2[i] = make_float2(-g2 * rn, -g2 * rn);
       }
     } else {
-      for (int g = threadIdx.x; g < sl.kk; g += NT) gs[par][0][g] = gs[par][1][g] = 0.f;
-      const float* res = reduce_channels<2, VEC>(sl, acc, scr, w.v, w.rg, w.active);
-      reduce_groups<2, VEC>(sl, a.cg, 0, res, gs[par], [&](int ch) {
-        return a.gamma ? a.gamma[w.c0 + ch] : 1.f;
-      });
-      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float2 v[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          v[i] = make_float2(0.f, 0.f);
+          if (w.active) v[i] = __fmul2_rn(bk.ga[i], acc[q][i]);
+        }
+        gather_groups<VEC>(sl, w.rows, a.cg, a.cg_div, v, scr, gs[par][q]);
+      }
       if (sl.S > 1) {
         cluster_arrive();
         cluster_wait();
@@ -1181,15 +1214,22 @@ struct NormCut {
 NormCut norm_cut(const NormArgs& a, int e, int tiles, bool aligned) {
   NormCut n{};
   // the fewest whole groups that make 64-byte pieces of a frame (16-byte
-  // aligned ones); short of that, 32 channels of any alignment
+  // aligned ones) and, while there are more slabs than the SMs take twice, 4 KB
+  // (a slab costs its reductions, whatever its length); short of alignment, 32
+  // channels
+  auto enough = [&](int k) {
+    return (long long)a.T * k * a.cg * e >= 4096 || (long long)a.B * (a.G / k) <= 2 * 3 * 152;
+  };
   int kk = 0;
   n.vec = 1;
   if (aligned)
     for (int k = 1; k <= a.G && k <= MAX_KK; ++k)
       if (a.G % k == 0 && (long long)k * a.cg * e % 16 == 0) {
+        // (groups as long as a thread may hold a 16-byte column of them)
+        if (kk && (long long)k * a.cg * e > 16 * NT) break;
         kk = k;
         n.vec = 4;
-        if (k * a.cg * e >= 64) break;
+        if (k * a.cg * e >= 64 && enough(k)) break;
       }
   if (!kk)
     for (int k = 1; k <= a.G && k <= MAX_KK; ++k)
@@ -1204,8 +1244,10 @@ NormCut norm_cut(const NormArgs& a, int e, int tiles, bool aligned) {
   const long long frame = (long long)s.W * e * tiles;
   s.S = 1;
   while (s.S < 8 && cdiv(a.T, s.S) * frame > SHARE) s.S *= 2;
-  // few slabs: shares of at least 64 frames, until there are two blocks an SM
-  while (s.S < 8 && (long long)s.nslabs * s.S < 2 * 152 && a.T >= 128 * s.S) s.S *= 2;
+  // few slabs: shares of at least 2048 values, until there are two blocks an SM
+  while (s.S < 8 && (long long)s.nslabs * s.S < 2 * 152 &&
+         (long long)a.T / (2 * s.S) * s.W >= 2048 && a.T >= 4 * s.S)
+    s.S *= 2;
   s.per_max = (int)cdiv(a.T, s.S);
   // resident: a thread per 16-byte column, slots within the block's share
   const int cols16 = s.W * e / 16;
@@ -1219,6 +1261,9 @@ NormCut norm_cut(const NormArgs& a, int e, int tiles, bool aligned) {
   s.pow2 = s.cbv <= 32 && (s.cbv & (s.cbv - 1)) == 0;
   const int rows = s.pow2 ? NWARPS : NT / s.cbv;
   s.scratch = 4 * (rows + 1) * s.cbv * n.vec;
+  for (s.lg = 0; s.lg < 5 && (kk << (s.lg + 1)) <= NT;) ++s.lg;
+  // (gather_groups takes a value per thread and channel)
+  if (n.res) s.scratch = std::max(s.scratch, (int)cdiv(4 * NT * n.vec, tiles));
   s.per_sample_div = fast_div(a.G / kk);
   for (s.S_log = 0; (1 << s.S_log) < s.S;) ++s.S_log;
   for (s.step_log = 0; (2 << s.step_log) <= NT / s.cbv;) ++s.step_log;

@@ -195,15 +195,15 @@ class FrameNorm(_Op):
         """(dx, dgamma, dbeta) for the x and T_len of the last fwd."""
         if dx is None:
             dx = torch.empty_strided(*self._x, dtype=self._t, device=self.device)
+        f = torch.float32
         if dgamma is None:
-            dgamma = torch.empty(self.dims.C, dtype=torch.float32, device=self.device)
+            dgamma = torch.empty(self.dims.C, dtype=f, device=self.device)
         if dbeta is None:
-            dbeta = torch.empty(self.dims.C, dtype=torch.float32, device=self.device)
+            dbeta = torch.empty(self.dims.C, dtype=f, device=self.device)
+        pg, pb = (_ptr(dgamma, "dgamma", f, *self._c), _ptr(dbeta, "dbeta", f, *self._c))
         _check(self._bwd(self._d, _ptr(x, "x", self._t, *self._x),
                          _ptr(dy, "dy", self._t, *self._y), *self._params(gamma, beta, T_len),
-                         self._saved, _ptr(dx, "dx", self._t, *self._x),
-                         _ptr(dgamma, "dgamma", torch.float32, *self._c),
-                         _ptr(dbeta, "dbeta", torch.float32, *self._c), *self._args,
+                         self._saved, _ptr(dx, "dx", self._t, *self._x), pg, pb, *self._args,
                          self._stream(stream)), "rnnt_norm_bwd")
         return dx, dgamma, dbeta
 
