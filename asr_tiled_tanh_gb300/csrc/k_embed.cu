@@ -108,6 +108,8 @@ __device__ __forceinline__ void add_vec(float (&a)[VEC], const float (&v)[VEC]) 
   }
 }
 
+// (16-byte stores say that they stream: the rows of a large batch would else
+// push one another's lines out half written, 23 against 19 us for 106 MB)
 template <int VEC, typename T>
 __device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
   if constexpr (VEC == 1) {
@@ -119,14 +121,14 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
   } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int i = 0; i < VEC; i += 4)
-      *(float4*)(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      __stcs((float4*)(p + i), make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
   } else {
-    *(uint4*)p = make_uint4(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]),
-                            ptx::pack_bf16x2(v[4], v[5]), ptx::pack_bf16x2(v[6], v[7]));
+    __stcs((uint4*)p, make_uint4(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]),
+                                 ptx::pack_bf16x2(v[4], v[5]), ptx::pack_bf16x2(v[6], v[7])));
   }
 }
 
-constexpr int ROWS_THREADS = 256;
+constexpr int ROWS_THREADS = 128;
 
 // A warp writes K steps of 32 / (1 << lg) rows, 1 << lg lanes to a row.  Each
 // lane looks one row's label up; the rows take theirs by shuffle.
@@ -167,11 +169,12 @@ cudaError_t launch_rows_v(const EmbedArgs& a, const TE* table, TR* rows, cudaStr
   const int vpr = a.D / VEC;
   const int lg = vpr > 16 ? 5 : vpr > 8 ? 4 : 3, per = 32 >> lg;
   const long long N = (long long)a.B * a.U1, warps = ROWS_THREADS / 32;
-  // eight loads in flight per lane once that still gives every SM its warps;
-  // below, one, so that a few rows spread over the SMs
+  // four loads in flight per lane (eight, 19 us, or blocks of 256, 17.5, were
+  // slower than 17.1 for 1024 x 101 rows of 512) once that still gives every SM
+  // its warps; below, one, so that a few rows spread over the SMs
   if (N >= 64LL * num_sms() * per)
-    k_embed_rows<VEC, 8>
-        <<<(unsigned)cdiv(N, 8 * per * warps), ROWS_THREADS, 0, st>>>(a, lg, table, rows);
+    k_embed_rows<VEC, 4>
+        <<<(unsigned)cdiv(N, 4 * per * warps), ROWS_THREADS, 0, st>>>(a, lg, table, rows);
   else
     k_embed_rows<VEC, 1>
         <<<(unsigned)cdiv(N, per * warps), ROWS_THREADS, 0, st>>>(a, lg, table, rows);
@@ -378,7 +381,12 @@ __global__ void __launch_bounds__(SORT_THREADS) k_embed_scatter(SortArgs s) {
   __shared__ int base[MAX_DIGITS];
   __shared__ int parts[SORT_THREADS], before[SORT_THREADS];
   const int R = 1 << s.bits, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < WARPS * MAX_DIGITS / 2; i += SORT_THREADS) ((uint32_t*)wcnt)[i] = 0;
   ptx::griddep_wait();
+  const int n1 = (int)min((long long)s.N, (long long)(blockIdx.x + 1) * s.per);
+  // (a tile's entries are asked for ahead of what they wait for)
+  int n = blockIdx.x * s.per + tid;
+  int next_key = n < n1 ? s.key_in[n] : 0, next_row = n < n1 && s.idx_in ? s.idx_in[n] : n;
   // where the block's entries of digit d begin: all smaller digits, and the
   // earlier blocks' entries of the same one
   {
@@ -418,15 +426,19 @@ __global__ void __launch_bounds__(SORT_THREADS) k_embed_scatter(SortArgs s) {
     }
   }
   ptx::griddep_launch();
-  const int n1 = (int)min((long long)s.N, (long long)(blockIdx.x + 1) * s.per);
   for (int t0 = blockIdx.x * s.per; t0 < n1; t0 += SORT_THREADS) {
-    const int n = t0 + tid;
     const bool in = n < n1;
-    const int key = in ? s.key_in[n] : 0;
-    const int row = in ? (s.idx_in ? s.idx_in[n] : n) : 0;
+    const int key = next_key, row = next_row;
+    n += SORT_THREADS;
+    if (n < n1) {
+      next_key = s.key_in[n];
+      next_row = s.idx_in ? s.idx_in[n] : n;
+    }
     const int d = in ? (key >> s.shift) & (R - 1) : R;  // (R: no entry)
-    __syncthreads();
-    for (int i = tid; i < WARPS * R; i += SORT_THREADS) wcnt[i >> s.bits][i & (R - 1)] = 0;
+    if (t0 > (int)blockIdx.x * s.per) {
+      __syncthreads();
+      for (int i = tid; i < WARPS * MAX_DIGITS / 2; i += SORT_THREADS) ((uint32_t*)wcnt)[i] = 0;
+    }
     __syncthreads();
     const unsigned peers = __match_any_sync(0xffffffffu, d);
     const int rank = __popc(peers & ((1u << lane) - 1));
