@@ -265,7 +265,8 @@ k_embed_group(EmbedArgs a, ClearShare cs, int32_t* __restrict__ lkey, int32_t* _
     key[n] = v < 0 ? a.V : v;
   }
   __syncthreads();
-  ptx::griddep_launch();
+  // The blocks of the sums are not let in early: waiting on the SMs they take the
+  // room of the clearing blocks (27.3 us against 22.7 for 1296 rows, V 4096).
   const int seg = (int)cdiv(NP / 128, SORT_WARPS) * 128;
   const int n0 = min(NP, warp * seg), n1 = min(NP, n0 + seg);
   int32_t* mycnt = cnt + warp * range;
