@@ -49,22 +49,30 @@ __device__ __forceinline__ int frames_of(const NormArgs& a, int t) {
 }
 
 // ---- activation -------------------------------------------------------------
-// sigmoid of two values.  fp32: to fp32's own accuracy.  bf16: ex2 and the
-// reciprocal of the special-function unit (relative error about 2^-22; a large
-// negative u gives 1 / inf = 0).
+// sigmoid of two values by the special-function unit's ex2 and reciprocal
+// (relative error about 2^-22; a large negative u gives 1 / inf = 0).  fp32 also
+// carries what the product u log2(e) rounds off, or large |u| would lose digits
+// in the exponent; expf and a division, 30 instructions for these 8, held the
+// fp32 kernels to half the bandwidth.
 template <typename T>
 __device__ __forceinline__ float2 sigmoid2(float2 u) {
+  const float kL = -1.4426950408889634f;
+  const float2 t = __fmul2_rn(u, make_float2(kL, kL));
+  float2 e = make_float2(ptx::ex2(t.x), ptx::ex2(t.y));
   if constexpr (sizeof(T) == 4) {
-    return make_float2(1.f / (1.f + expf(-u.x)), 1.f / (1.f + expf(-u.y)));
-  } else {
-    const float kL = -1.4426950408889634f;
-    const float2 t = __fmul2_rn(u, make_float2(kL, kL));
-    const float2 p = __fadd2_rn(make_float2(ptx::ex2(t.x), ptx::ex2(t.y)), make_float2(1.f, 1.f));
-    float2 r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(p.x));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(p.y));
-    return r;
+    // -log2(e) = kL + kLow; 2^(t + f) = 2^t (1 + f ln 2)
+    const float kLow = (float)(-1.4426950408889634 - (double)kL), kLn2 = 0.6931471805599453f;
+    const float2 f = __ffma2_rn(u, make_float2(kLow, kLow),
+                                __ffma2_rn(u, make_float2(kL, kL), make_float2(-t.x, -t.y)));
+    const float2 c = __ffma2_rn(f, make_float2(kLn2, kLn2), make_float2(1.f, 1.f));
+    // (beyond, e is 0 or so large that only 1 or 0 is left, and f may be NaN)
+    e = make_float2(fabsf(t.x) < 126.f ? e.x * c.x : e.x, fabsf(t.y) < 126.f ? e.y * c.y : e.y);
   }
+  const float2 p = __fadd2_rn(e, make_float2(1.f, 1.f));
+  float2 r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(p.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(p.y));
+  return r;
 }
 
 template <int ACT, typename T>
@@ -524,10 +532,16 @@ k_norm_fwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ 
   if (sl.S > 1) cluster_wait();
 }
 
-// Per-channel constants of the backward and its two uses of a frame:
-// g = dy act'(u) with xh, and dx.
+// The backward's two uses of a frame, in d = x - mean and s = rstd gamma:
+//   u = s d + beta,  g = dy act'(u),  sums of g d and g (rstd goes onto the sums),
+//   dx = s g + (k1 + k2 d),  k1 = -rstd m1,  k2 = -rstd^2 m2.
+// The sums become fp32 gradients and take sigmoid2.  dx in bf16 takes the unit's
+// tanh, one operation where sigmoid2 has two: its relative error of 2^-11 moves
+// act' by at most 2^-12 (1 + |u| / 2), where the rounding of dx moves it by 2^-9
+// (1024 x 1000 x 512: 485 us against 509).
 template <typename T, int VEC, int ACT>
 struct Back {
+  static constexpr bool kHalf = ACT == RNNT_ACT_SILU && sizeof(T) == 2;
   float2 m[kPairs(VEC)], rs[kPairs(VEC)], ga[kPairs(VEC)], be[kPairs(VEC)];
   __device__ __forceinline__ void stats(const float2* st, int c, const FastDiv& cg) {
 #pragma unroll
@@ -538,31 +552,72 @@ struct Back {
       rs[i] = make_float2(p.y, q.y);
     }
   }
-  __device__ __forceinline__ void g_of(int i, float2 x, float2 dy, float2& xh, float2& g) const {
-    xh = __fmul2_rn(__fadd2_rn(x, m[i]), rs[i]);
-    g = dact2<ACT, T>(dy, __ffma2_rn(xh, ga[i], be[i]));
-  }
-  __device__ __forceinline__ void sums(const Ch<VEC>& x, const Ch<VEC>& dy,
-                                       float2 (&acc)[2][kPairs(VEC)]) const {
+  struct Sums {
+    float2 m[kPairs(VEC)], s[kPairs(VEC)], be[kPairs(VEC)];
+    __device__ __forceinline__ void add(const Ch<VEC>& x, const Ch<VEC>& dy,
+                                        float2 (&acc)[2][kPairs(VEC)]) const {
+#pragma unroll
+      for (int i = 0; i < kPairs(VEC); ++i) {
+        const float2 d = __fadd2_rn(x.v[i], m[i]);
+        const float2 g = dact2<ACT, T>(dy.v[i], __ffma2_rn(d, s[i], be[i]));
+        acc[0][i] = __ffma2_rn(g, d, acc[0][i]);
+        acc[1][i] = __fadd2_rn(acc[1][i], g);
+      }
+    }
+  };
+  struct Dx {
+    float2 m[kPairs(VEC)], s[kPairs(VEC)], be[kPairs(VEC)], k1[kPairs(VEC)], k2[kPairs(VEC)];
+    __device__ __forceinline__ Ch<VEC> of(const Ch<VEC>& x, const Ch<VEC>& dy) const {
+      Ch<VEC> o;
+#pragma unroll
+      for (int i = 0; i < kPairs(VEC); ++i) {
+        const float2 d = __fadd2_rn(x.v[i], m[i]), u = __ffma2_rn(d, s[i], be[i]);
+        const float2 k = __ffma2_rn(d, k2[i], k1[i]);
+        if constexpr (kHalf) {
+          // s and be are halved: u is h = u / 2, and with t = tanh h
+          // act'(u) = (1 + t + h (1 - t^2)) / 2
+          float2 t;
+          asm("tanh.approx.f32 %0, %1;" : "=f"(t.x) : "f"(u.x));
+          asm("tanh.approx.f32 %0, %1;" : "=f"(t.y) : "f"(u.y));
+          const float2 w = __fmul2_rn(dy.v[i], s[i]);
+          const float2 q = __ffma2_rn(make_float2(-t.x, -t.y), t, make_float2(1.f, 1.f));
+          o.v[i] = __ffma2_rn(w, __ffma2_rn(u, q, t), __fadd2_rn(w, k));
+        } else {
+          o.v[i] = __ffma2_rn(dact2<ACT, T>(dy.v[i], u), s[i], k);
+        }
+      }
+      return o;
+    }
+  };
+  __device__ __forceinline__ Sums sums() const {
+    Sums q;
 #pragma unroll
     for (int i = 0; i < kPairs(VEC); ++i) {
-      float2 xh, g;
-      g_of(i, x.v[i], dy.v[i], xh, g);
-      acc[0][i] = __ffma2_rn(g, xh, acc[0][i]);
-      acc[1][i] = __fadd2_rn(acc[1][i], g);
+      q.m[i] = m[i];
+      q.s[i] = __fmul2_rn(rs[i], ga[i]);
+      q.be[i] = be[i];
     }
+    return q;
   }
-  __device__ __forceinline__ Ch<VEC> dx(const Ch<VEC>& x, const Ch<VEC>& dy,
-                                        const float2 (&k1)[kPairs(VEC)],
-                                        const float2 (&k2)[kPairs(VEC)]) const {
-    Ch<VEC> o;
+  // g (x - mean) to g xh
+  __device__ __forceinline__ void scale(float2 (&acc)[kPairs(VEC)]) const {
+#pragma unroll
+    for (int i = 0; i < kPairs(VEC); ++i) acc[i] = __fmul2_rn(acc[i], rs[i]);
+  }
+  // k1, k2: minus the means of gamma g and gamma g xh
+  __device__ __forceinline__ Dx dx(const float2 (&k1)[kPairs(VEC)],
+                                   const float2 (&k2)[kPairs(VEC)]) const {
+    Dx q;
+    const float2 f = kHalf ? make_float2(0.5f, 0.5f) : make_float2(1.f, 1.f);
 #pragma unroll
     for (int i = 0; i < kPairs(VEC); ++i) {
-      float2 xh, g;
-      g_of(i, x.v[i], dy.v[i], xh, g);
-      o.v[i] = __fmul2_rn(rs[i], __ffma2_rn(xh, k2[i], __ffma2_rn(g, ga[i], k1[i])));
+      q.m[i] = m[i];
+      q.s[i] = __fmul2_rn(f, __fmul2_rn(rs[i], ga[i]));
+      q.be[i] = __fmul2_rn(f, be[i]);
+      q.k1[i] = __fmul2_rn(rs[i], k1[i]);
+      q.k2[i] = __fmul2_rn(__fmul2_rn(rs[i], rs[i]), k2[i]);
     }
-    return o;
+    return q;
   }
 };
 
@@ -632,9 +687,11 @@ k_norm_bwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restr
       if (pass == 0) {
         float2 acc[2][kPairs(VEC)] = {};
         if (in) {
+          const auto sums = bk.sums();
 #pragma unroll 2
           for (int k = 0; k < cnt; ++k, px += xinc, pd += dinc)
-            bk.sums(load_ch<VEC, T>(px), load_ch<VEC, T>(pd), acc);
+            sums.add(load_ch<VEC, T>(px), load_ch<VEC, T>(pd), acc);
+          bk.scale(acc[0]);
         }
         const float* res = reduce_channels<2, VEC>(sl, acc, scr, w.v, w.rg, in);
         for (int k = threadIdx.x; k < nb && cb + k < sl.W; k += NT)
@@ -646,10 +703,11 @@ k_norm_bwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restr
       } else if (in) {
         float2 k1[kPairs(VEC)], k2[kPairs(VEC)];
         means_of<VEC>(m1_t, m2_t, c, a.cg_div, k1, k2);
+        const auto last = bk.dx(k1, k2);
         T* po = os + w.rg * a.xf + c;
 #pragma unroll 2
         for (int k = 0; k < cnt; ++k, px += xinc, pd += dinc, po += xinc)
-          store_ch<VEC, T>(po, bk.dx(load_ch<VEC, T>(px), load_ch<VEC, T>(pd), k1, k2));
+          store_ch<VEC, T>(po, last.of(load_ch<VEC, T>(px), load_ch<VEC, T>(pd)));
       }
     }
     if (pass) break;
@@ -1013,9 +1071,10 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
       ahead = length_ahead(a, sl, slab + 2 * stride);
       zero_tail<VEC, T>(a, sl, w, os, a.xf);
     };
+    const auto pass = bk.sums();
     auto sums = [&](int k) {
-      bk.sums(load_ch<VEC, T>((const T*)(mine + k * SLOT)),
-              load_ch<VEC, T>((const T*)(mine + half_bytes + k * SLOT)), acc);
+      pass.add(load_ch<VEC, T>((const T*)(mine + k * SLOT)),
+               load_ch<VEC, T>((const T*)(mine + half_bytes + k * SLOT)), acc);
     };
     copy_wait<1>();
 #pragma unroll 2
@@ -1023,6 +1082,7 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
     copy_wait<0>();
 #pragma unroll 2
     for (int k = ready; k < cnt; ++k) sums(k);
+    bk.scale(acc[0]);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       tot[0][i] = __fadd2_rn(tot[0][i], acc[0][i]);
@@ -1098,6 +1158,7 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
 #pragma unroll
       for (int i = 0; i < NP; ++i) tot[0][i] = tot[1][i] = make_float2(0.f, 0.f);
     }
+    const auto last = bk.dx(k1, k2);
     T* o = os + (long long)(w.t0 + w.rg) * a.xf + c;
     const T* p = x + nx.b * a.xb + nx.c0 + (long long)(nx.t0 + nx.rg) * a.xf + c;
     const T* d = dy + nx.b * a.yb + nx.c0 + (long long)(nx.t0 + nx.rg) * a.yf + c;
@@ -1105,9 +1166,8 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
       constexpr int U = decltype(frames)::value;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        store_ch<VEC, T>(o, bk.dx(load_ch<VEC, T>((const T*)(mine + (k + u) * SLOT)),
-                                  load_ch<VEC, T>((const T*)(mine + half_bytes + (k + u) * SLOT)),
-                                  k1, k2));
+        store_ch<VEC, T>(o, last.of(load_ch<VEC, T>((const T*)(mine + (k + u) * SLOT)),
+                                    load_ch<VEC, T>((const T*)(mine + half_bytes + (k + u) * SLOT))));
         o += xinc;
       }
     };
@@ -1214,11 +1274,12 @@ struct NormCut {
 NormCut norm_cut(const NormArgs& a, int e, int tiles, bool aligned) {
   NormCut n{};
   // the fewest whole groups that make 64-byte pieces of a frame (16-byte
-  // aligned ones) and, while there are more slabs than the SMs take twice, 4 KB
-  // (a slab costs its reductions, whatever its length); short of alignment, 32
-  // channels
+  // aligned ones) and, while there are more slabs than the SMs take twice, 16 KB:
+  // a slab costs its reductions, whatever its length (250 frames of 512 channels,
+  // 4096 samples: 337 us forward and 546 backward, against 433 and 780 with slabs
+  // of 8 KB upward; from 32 KB upward 352 and 669).  Short of alignment, 32 channels.
   auto enough = [&](int k) {
-    return (long long)a.T * k * a.cg * e >= 4096 || (long long)a.B * (a.G / k) <= 2 * 3 * 152;
+    return (long long)a.T * k * a.cg * e >= 16384 || (long long)a.B * (a.G / k) <= 2 * 3 * 152;
   };
   int kk = 0;
   n.vec = 1;
@@ -1272,40 +1333,76 @@ NormCut norm_cut(const NormArgs& a, int e, int tiles, bool aligned) {
   n.grid = s.nslabs * s.S;
   n.rows = a.B * s.S;
   if (n.res) {
-    // as many blocks as the SMs hold (228 KB each; 3 by the kernels' registers,
-    // more when they take fewer), in steps of a sample's slabs, so that a block
-    // keeps its channels
-    const int per_sample = a.G / kk;
-    const int per_sm = (int)std::min<size_t>(4, (228 * 1024) / (n.smem + 8 * 1024));
-    int clusters = std::min(s.nslabs, std::max(1, per_sm * num_sms() / s.S));
-    s.keep = clusters >= per_sample;
-    if (s.keep) {
-      clusters = clusters / per_sample * per_sample;
-      n.rows = clusters / per_sample * s.S;
-    }
-    n.grid = clusters * s.S;
     s.uni = s.pow2 && a.cg % n.vec == 0;
     s.lanes = s.uni ? 31 & ~(s.cbv - a.cg / n.vec) : 0;
   }
   return n;
 }
 
-// Launch a kernel in clusters of S blocks.
+// The grid of a resident kernel: as many clusters as the card holds at a time,
+// since blocks that walk slabs from the start leave nothing to later ones (512
+// samples of 2000 frames: 690 us backward, against 886 where 112 clusters of 4
+// were launched and 110 fit).  Where it costs at most an eighth of them, a whole
+// number of samples' slabs, so that a block keeps its channels and their sums.
+void norm_grid(const NormArgs& a, NormCut* n, int most) {
+  Slab& s = n->sl;
+  const int per_sample = a.G / s.kk;
+  int clusters = std::min(s.nslabs, most);
+  const int whole = clusters / per_sample * per_sample;
+  s.keep = whole * 8 >= clusters * 7;
+  if (s.keep) {
+    clusters = whole;
+    n->rows = clusters / per_sample * s.S;
+  }
+  n->grid = clusters * s.S;
+}
+
+// A launch in clusters of S blocks.
+struct ClusterLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  ClusterLaunch(unsigned grid, int S, size_t smem, cudaStream_t st) {
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = S;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = S > 1 ? 1 : 0;
+  }
+};
 template <typename... KA, typename... A>
 cudaError_t launch_cluster(void (*k)(KA...), unsigned grid, int S, size_t smem, cudaStream_t st,
                            A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = S;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = S > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k, args...);
+  const ClusterLaunch l(grid, S, smem, st);
+  return cudaLaunchKernelEx(&l.cfg, k, args...);
+}
+
+// Clusters of S blocks that the card holds at a time, asked once for each kernel,
+// device, cluster size and 4 KB of shared memory.
+struct Resident {
+  static constexpr int kStep = 4096, kSteps = (SHARE_MAX + 20 * 1024) / kStep;
+  std::atomic<uint16_t> most[kDeviceSlots][4][kSteps + 1];
+};
+template <typename K>
+cudaError_t most_clusters(K k, Resident* known, const NormCut& n, int* most) {
+  const int step = (int)cdiv((long long)n.smem, Resident::kStep);
+  std::atomic<uint16_t>& m = known->most[device_slot()][n.sl.S_log][step];
+  *most = m.load();
+  if (*most) return cudaSuccess;
+  const ClusterLaunch l(n.sl.S, n.sl.S, (size_t)step * Resident::kStep, nullptr);
+  cudaError_t e;
+  if (n.sl.S > 1) {
+    e = cudaOccupancyMaxActiveClusters(most, k, &l.cfg);
+  } else {
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(most, k, NT, l.cfg.dynamicSmemBytes);
+    *most *= num_sms();
+  }
+  *most = std::min(std::max(1, *most), 65535);
+  if (e == cudaSuccess) m.store((uint16_t)*most);
+  return e;
 }
 
 // Shared memory above 48 KB is asked for once per kernel and device.
@@ -1322,35 +1419,42 @@ cudaError_t opt_in(K k, std::atomic<bool>* done) {
 // dy NULL: the forward kernel, else the backward.
 template <typename T, typename KF, typename KB>
 cudaError_t norm_launch(KF kf, KB kb, std::atomic<bool>* fdone, std::atomic<bool>* bdone,
-                        const NormArgs& a, const NormCut& n, const void* x, const void* dy,
-                        void* out, float2* part, cudaStream_t st) {
-  const cudaError_t e = dy ? opt_in(kb, bdone) : opt_in(kf, fdone);
+                        Resident* known, const NormArgs& a, NormCut* n, const void* x,
+                        const void* dy, void* out, float2* part, cudaStream_t st) {
+  cudaError_t e = dy ? opt_in(kb, bdone) : opt_in(kf, fdone);
   if (e != cudaSuccess) return e;
-  return dy ? launch_cluster(kb, n.grid, n.sl.S, n.smem, st, a, n.sl, (const T*)x, (const T*)dy,
-                             (T*)out, part)
-            : launch_cluster(kf, n.grid, n.sl.S, n.smem, st, a, n.sl, (const T*)x, (T*)out);
+  if (known) {
+    int most = 0;
+    e = dy ? most_clusters(kb, known + 1, *n, &most) : most_clusters(kf, known, *n, &most);
+    if (e != cudaSuccess) return e;
+    norm_grid(a, n, most);
+  }
+  return dy ? launch_cluster(kb, n->grid, n->sl.S, n->smem, st, a, n->sl, (const T*)x,
+                             (const T*)dy, (T*)out, part)
+            : launch_cluster(kf, n->grid, n->sl.S, n->smem, st, a, n->sl, (const T*)x, (T*)out);
 }
 
 template <typename T, int ACT>
-cudaError_t norm_launch_cut(const NormArgs& a, const NormCut& n, const void* x, const void* dy,
+cudaError_t norm_launch_cut(const NormArgs& a, NormCut* n, const void* x, const void* dy,
                             void* out, float2* part, cudaStream_t st) {
   static std::atomic<bool> done[8][kDeviceSlots];
-  if (n.res && n.sl.uni)
+  static Resident known[4];
+  if (n->res && n->sl.uni)
     return norm_launch<T>(k_norm_fwd_res<T, ACT, 1>, k_norm_bwd_res<T, ACT, 1>, done[6], done[7],
-                          a, n, x, dy, out, part, st);
-  if (n.res)
+                          known, a, n, x, dy, out, part, st);
+  if (n->res)
     return norm_launch<T>(k_norm_fwd_res<T, ACT, 0>, k_norm_bwd_res<T, ACT, 0>, done[0], done[1],
-                          a, n, x, dy, out, part, st);
-  if (n.vec == 4)
+                          known + 2, a, n, x, dy, out, part, st);
+  if (n->vec == 4)
     return norm_launch<T>(k_norm_fwd_stream<T, 4, ACT>, k_norm_bwd_stream<T, 4, ACT>, done[2],
-                          done[3], a, n, x, dy, out, part, st);
+                          done[3], nullptr, a, n, x, dy, out, part, st);
   return norm_launch<T>(k_norm_fwd_stream<T, 1, ACT>, k_norm_bwd_stream<T, 1, ACT>, done[4],
-                        done[5], a, n, x, dy, out, part, st);
+                        done[5], nullptr, a, n, x, dy, out, part, st);
 }
 
 // dy NULL: forward, x -> out = y; else backward, (x, dy) -> out = dx and part.
 template <typename T>
-cudaError_t norm_launch_act(const NormArgs& a, const NormCut& n, const void* x, const void* dy,
+cudaError_t norm_launch_act(const NormArgs& a, NormCut* n, const void* x, const void* dy,
                             void* out, float2* part, cudaStream_t st) {
   switch (a.act) {
     case RNNT_ACT_SILU: return norm_launch_cut<T, RNNT_ACT_SILU>(a, n, x, dy, out, part, st);
@@ -1394,9 +1498,9 @@ rnnt_status rnnt_norm_fwd(const rnnt_norm_dims* dims, const void* x, const float
   cudaStream_t st = (cudaStream_t)stream;
   ProfScope ps("norm_fwd", st);
   const int e = op_size(dims->dtype);
-  const NormCut n = norm_cut(a, e, 1, norm_aligned(a, e, x, y, nullptr));
-  OPS_CHECK(e == 4 ? norm_launch_act<float>(a, n, x, nullptr, y, nullptr, st)
-                   : norm_launch_act<__nv_bfloat16>(a, n, x, nullptr, y, nullptr, st));
+  NormCut n = norm_cut(a, e, 1, norm_aligned(a, e, x, y, nullptr));
+  OPS_CHECK(e == 4 ? norm_launch_act<float>(a, &n, x, nullptr, y, nullptr, st)
+                   : norm_launch_act<__nv_bfloat16>(a, &n, x, nullptr, y, nullptr, st));
   return RNNT_OK;
 }
 
@@ -1414,11 +1518,11 @@ rnnt_status rnnt_norm_bwd(const rnnt_norm_dims* dims, const void* x, const void*
   cudaStream_t st = (cudaStream_t)stream;
   float2* part = (float2*)ws;
   const int e = op_size(dims->dtype);
-  const NormCut n = norm_cut(a, e, 2, norm_aligned(a, e, x, dy, dx));
+  NormCut n = norm_cut(a, e, 2, norm_aligned(a, e, x, dy, dx));
   if (a.B > 0) {
     ProfScope ps("norm_bwd", st);
-    OPS_CHECK(e == 4 ? norm_launch_act<float>(a, n, x, dy, dx, part, st)
-                     : norm_launch_act<__nv_bfloat16>(a, n, x, dy, dx, part, st));
+    OPS_CHECK(e == 4 ? norm_launch_act<float>(a, &n, x, dy, dx, part, st)
+                     : norm_launch_act<__nv_bfloat16>(a, &n, x, dy, dx, part, st));
   }
   if (!dgamma && !dbeta) return RNNT_OK;
   const int rows = n.rows, S = rows > 256 ? 8 : 1;
