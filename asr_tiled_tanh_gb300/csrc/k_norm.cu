@@ -172,12 +172,14 @@ __device__ __forceinline__ void load_param(float2 (&v)[kPairs(VEC)], const float
 // owns it, a contiguous share of its frames each.  The resident kernels
 // (k_norm_*_res) copy their share into shared memory once and make every pass
 // over it there, so that x (and dy) are read once from DRAM and y (dx) written
-// once, which is the kernels' bound; slabs that eight blocks cannot hold, and
+// once, which is the kernels' bound; slabs that a cluster cannot hold, and
 // rows that are not 16-byte aligned, are read from global memory in every pass
 // (k_norm_*_stream).
 constexpr int NT = 128, NWARPS = NT / 32;
 constexpr int MAX_KK = 128;
-constexpr int SHARE = 64 * 1024, SHARE_MAX = 200 * 1024;
+constexpr int MAX_S = 16;  // blocks in a cluster (8 where shares stay in global memory)
+constexpr int SHARE = 64 * 1024;
+constexpr int SMEM_MAX = SHARE + 32 * 1024;  // with room for sums (dynamic)
 
 struct Slab {
   int kk, W, S;      // groups and channels per slab, blocks per slab
@@ -188,9 +190,9 @@ struct Slab {
   int nslabs;
   int uni;           // a thread's channels are of one group (and pow2): GroupSum applies
   int lanes;         // lane bits that share a group (uni)
+  int two;           // a thread's channels are of two groups at most (not uni): TwoGroups
   int lg;            // log2 of the lanes that gather a group's sum (not uni)
   int keep;          // a block's slabs have the same channels
-  int scratch;       // scratch bytes per reduced quantity
   int S_log, step_log;  // S; NT / cbv where cbv is a power of two
   FastDiv per_sample_div, cbv_div;
 };
@@ -223,12 +225,11 @@ __device__ __forceinline__ void to_peer_f32(float* p, int rank, float v) {
 }
 
 // Sums over the block's frames of NA quantities per channel, for the channels
-// of the current column block: afterwards res[q * n + c], n = cbv * VEC, where
-// res is returned (behind the NA * rows * n partial sums).
-template <int NA, int VEC>
-__device__ __forceinline__ const float* reduce_channels(const Slab& sl,
-                                                        float2 (&acc)[NA][kPairs(VEC)],
-                                                        float* scr, int col, int rg, bool active) {
+// of the current column block: out(q, c, sum), c < n = cbv * VEC.  scr: NA * rows * n
+// partial sums, rows the row groups of frames (warps, where columns meet by shuffles).
+template <int NA, int VEC, typename F>
+__device__ __forceinline__ void sum_channels(const Slab& sl, float2 (&acc)[NA][kPairs(VEC)],
+                                             float* scr, int col, int rg, bool active, F out) {
   const int n = sl.cbv * VEC, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = sl.pow2 ? NWARPS : NT / sl.cbv_div;
   if (sl.pow2) {
@@ -256,16 +257,25 @@ __device__ __forceinline__ const float* reduce_channels(const Slab& sl,
     }
   }
   __syncthreads();
-  float* res = scr + NA * rows * n;
   for (int c = threadIdx.x; c < NA * n; c += NT) {
     const int q = NA > 1 && c >= n;
     const float* d = scr + q * (rows - 1) * n + c;
     float t = 0.f;
 #pragma unroll 8
     for (int r = 0; r < rows; ++r) t += d[r * n];
-    res[c] = t;
+    out(q, c - q * n, t);
   }
   __syncthreads();
+}
+// The same into res[q * n + c], returned, behind the partial sums.
+template <int NA, int VEC>
+__device__ __forceinline__ const float* reduce_channels(const Slab& sl,
+                                                        float2 (&acc)[NA][kPairs(VEC)],
+                                                        float* scr, int col, int rg, bool active) {
+  const int n = sl.cbv * VEC;
+  float* res = scr + NA * n * (sl.pow2 ? NWARPS : NT / sl.cbv_div);
+  sum_channels<NA, VEC>(sl, acc, scr, col, rg, active,
+                        [&](int q, int c, float t) { res[q * n + c] = t; });
   return res;
 }
 
@@ -319,6 +329,75 @@ __device__ __forceinline__ void gather_groups(const Slab& sl, int rows, int cg,
   }
   __syncthreads();
 }
+
+// A thread's channels in two groups at most: those before `split` are of group
+// g0, the others of g1.  A thread adds up its channels of either, and a group's
+// lanes gather one value a thread and row of frames where gather_groups takes one
+// for each channel.
+template <int VEC>
+struct TwoGroups {
+  int g0, g1, split;
+  __device__ __forceinline__ TwoGroups(const Slab& sl, int c, int cg, int g)
+      : g0(g), g1(min(g + 1, sl.kk - 1)), split((g + 1) * cg - c) {}
+  __device__ __forceinline__ float2 pick(int i, float lo, float hi) const {
+    return make_float2(2 * i < split ? lo : hi, 2 * i + 1 < split ? lo : hi);
+  }
+  // (sum over g0's channels, sum over g1's)
+  __device__ __forceinline__ float2 sums(const float2 (&v)[kPairs(VEC)]) const {
+    float2 t = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kPairs(VEC); ++i) {
+      t = __fadd2_rn(t, 2 * i < split ? make_float2(v[i].x, 0.f) : make_float2(0.f, v[i].x));
+      t = __fadd2_rn(t, 2 * i + 1 < split ? make_float2(v[i].y, 0.f) : make_float2(0.f, v[i].y));
+    }
+    return t;
+  }
+};
+// gs[q][g] = the sum over the block of v[q]'s parts of group g.
+template <int VEC, int NQ>
+__device__ __forceinline__ void gather_two(const Slab& sl, int rows, int cg,
+                                           const float2 (&v)[NQ], float* scr,
+                                           float* const (&gs)[NQ]) {
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+    scr[2 * q * NT + threadIdx.x] = v[q].x;
+    scr[(2 * q + 1) * NT + threadIdx.x] = v[q].y;
+  }
+  __syncthreads();
+  const int sub = threadIdx.x >> sl.lg, at = threadIdx.x & ((1 << sl.lg) - 1);
+  const int nr = min(rows, NT / sl.cbv_div);  // (row groups that hold frames)
+  for (int g0 = 0; g0 < sl.kk; g0 += NT >> sl.lg) {  // (the same rounds for every thread)
+    const int g = g0 + sub;
+    float s[NQ] = {};
+    if (g < sl.kk) {
+      // columns v0 ... of the group; the first may be its owner's second group
+      const int v0 = g * cg / VEC, nv = ((g + 1) * cg - 1) / VEC - v0 + 1;
+      const int second = v0 * VEC < g * cg ? NT : 0;
+      const uint32_t inv = 65536u / nv + 1;  // k / nv for k <= 2 NT
+      for (int k = at; k < nr * nv; k += 1 << sl.lg) {
+        const int r = (int)(k * inv >> 16), j = k - r * nv;
+        const float* d = scr + r * sl.cbv + v0 + j + (j == 0 ? second : 0);
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) s[q] += d[2 * q * NT];
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      for (int o = 1 << sl.lg >> 1; o; o >>= 1) s[q] += __shfl_xor_sync(0xffffffffu, s[q], o);
+      if (at == 0 && g < sl.kk) gs[q][g] = s[q];
+    }
+  }
+  __syncthreads();
+}
+
+// Frames in flight per thread of the stream kernels, forward and backward: loads
+// this narrow are bound by how many are under way (32 x 2000 x 1024 in one group:
+// 141 us forward and 157 backward, with 4 and 2 frames 164 and 208; 333 channels,
+// an element a thread: 286 and 351, with 4 and 2 frames 350 and 665).
+template <int VEC>
+constexpr int kFlyFwd = VEC == 1 ? 16 : 8;
+template <int VEC>
+constexpr int kFlyBwd = VEC == 1 ? 8 : 4;
 
 // The block's slab, frames and column.
 template <int VEC>
@@ -430,6 +509,20 @@ struct Partial {
       s[i] = __fadd2_rn(mk, make_float2(-first[i].x, -first[i].y));
     }
   }
+  // the same for a thread of two groups at most, of means (lo, hi)
+  __device__ __forceinline__ float2 out(const TwoGroups<VEC>& tw, int half, int cnt, float lo,
+                                        float hi) const {
+    const float k = (float)cnt;
+    float2 v[kPairs(VEC)];
+#pragma unroll
+    for (int i = 0; i < kPairs(VEC); ++i) {
+      const float2 mean = tw.pick(i, lo, hi);
+      const float2 d = __fadd2_rn(s[i], make_float2(-mean.x, -mean.y));
+      v[i] = half == 0 ? __fmul2_rn(make_float2(k, k), s[i])
+                       : __ffma2_rn(__fmul2_rn(d, d), make_float2(k, k), q[i]);
+    }
+    return tw.sums(v);
+  }
   // half 0: the sum; half 1: the squares about the groups' means
   __device__ __forceinline__ void out(float2 (&acc)[1][kPairs(VEC)], int half, int cnt, int c,
                                       const float* mean_s, const FastDiv& cg) const {
@@ -478,7 +571,7 @@ k_norm_fwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ 
         if (half == 0 || nb < sl.W) {  // (one column block keeps its sums; more read again)
           const T* p = src + w.rg * ld + c;
           st.begin(load_ch<VEC, T>(p));
-#pragma unroll 4
+#pragma unroll (kFlyFwd<VEC>)
           for (int k = 0; k < cnt; ++k, p += inc) st.add(load_ch<VEC, T>(p));
           st.end(cnt);
         }
@@ -519,7 +612,7 @@ k_norm_fwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ 
     const T* p = src + w.rg * ld + c;
     T* o = yt + w.rg * a.yf + c;
     const long long oinc = w.step * a.yf;
-#pragma unroll 4
+#pragma unroll (kFlyFwd<VEC>)
     for (int k = 0; k < cnt; ++k, p += inc, o += oinc) {
       Ch<VEC> q = load_ch<VEC, T>(p);
 #pragma unroll
@@ -634,15 +727,16 @@ __device__ __forceinline__ void means_of(const float* m1_t, const float* m2_t, i
   }
 }
 
-// m1, m2 of the slab's groups from the blocks' sums gs[2][MAX_KK], in order.
+// m1, m2 of the slab's groups from the blocks' sums gs2 and gs1, in order.
 __device__ __forceinline__ void join_means(const NormArgs& a, const Slab& sl, int tb,
-                                           const float (*gs)[MAX_KK], float* m1_t, float* m2_t) {
+                                           const float* gs2, const float* gs1, float* m1_t,
+                                           float* m2_t) {
   const float n = (float)tb * a.cg;
   for (int g = threadIdx.x; g < sl.kk; g += NT) {
     float s2 = 0.f, s1 = 0.f;
     for (int k = 0; k < sl.S; ++k) {
-      s2 += sl.S > 1 ? peer_f32(&gs[0][g], k) : gs[0][g];
-      s1 += sl.S > 1 ? peer_f32(&gs[1][g], k) : gs[1][g];
+      s2 += sl.S > 1 ? peer_f32(gs2 + g, k) : gs2[g];
+      s1 += sl.S > 1 ? peer_f32(gs1 + g, k) : gs1[g];
     }
     m1_t[g] = n > 0.f ? s1 / n : 0.f;
     m2_t[g] = n > 0.f ? s2 / n : 0.f;
@@ -688,7 +782,7 @@ k_norm_bwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restr
         float2 acc[2][kPairs(VEC)] = {};
         if (in) {
           const auto sums = bk.sums();
-#pragma unroll 2
+#pragma unroll (kFlyBwd<VEC>)
           for (int k = 0; k < cnt; ++k, px += xinc, pd += dinc)
             sums.add(load_ch<VEC, T>(px), load_ch<VEC, T>(pd), acc);
           bk.scale(acc[0]);
@@ -705,7 +799,7 @@ k_norm_bwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restr
         means_of<VEC>(m1_t, m2_t, c, a.cg_div, k1, k2);
         const auto last = bk.dx(k1, k2);
         T* po = os + w.rg * a.xf + c;
-#pragma unroll 2
+#pragma unroll (kFlyBwd<VEC>)
         for (int k = 0; k < cnt; ++k, px += xinc, pd += dinc, po += xinc)
           store_ch<VEC, T>(po, last.of(load_ch<VEC, T>(px), load_ch<VEC, T>(pd)));
       }
@@ -716,7 +810,7 @@ k_norm_bwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restr
       cluster_arrive();
       cluster_wait();
     }
-    join_means(a, sl, w.tb, gs, m1_t, m2_t);
+    join_means(a, sl, w.tb, gs[0], gs[1], m1_t, m2_t);
     __syncthreads();
     if (sl.S > 1) cluster_arrive();  // (waited for at the end: peers may still read)
   }
@@ -822,8 +916,9 @@ k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) 
   __shared__ float mean_s[2][GK], m2_s[2][GK], n_s[2];
   __shared__ float mean_t[GK], rstd_t[GK];
   __shared__ __align__(16) float buf[2][UK][NWARPS];
-  __shared__ float from[2][8][2][UK];  // (mean, M2) of every block of the cluster
-  float* scr = (float*)(smem + (size_t)sl.slots * SLOT);
+  // (mean, M2) of every block of the cluster (UNI): [parity][block][2][group]
+  float* from = (float*)(smem + (size_t)sl.slots * SLOT);
+  float* scr = from;
   const unsigned char* mine = smem + threadIdx.x * 16;
   const uint32_t mine_a = ptx::smem_u32(mine);
   const int first = (int)blockIdx.x >> sl.S_log, rank = blockIdx.x - first * sl.S;
@@ -832,6 +927,7 @@ k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) 
   Where<VEC> w = where<VEC>(a, sl, first, rank, length_of(a, first / sl.per_sample_div));
   int ahead = length_ahead(a, sl, first + stride);
   const int c = w.v * VEC, myg = c / a.cg_div;
+  const TwoGroups<VEC> tw(sl, c, a.cg, myg);
   int cnt = rows_of(w, sl);
   const long long xinc = a.xf * w.step, yinc = a.yf * w.step;
   {
@@ -908,8 +1004,8 @@ k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) 
       if (sl.S > 1) {
         if (leader && warp == 0)
           for (int k = 0; k < sl.S; ++k) {
-            to_peer_f32(&from[par][rank][0][myg], k, mean);
-            to_peer_f32(&from[par][rank][1][myg], k, m2);
+            to_peer_f32(from + (par * sl.S + rank) * 2 * sl.kk + myg, k, mean);
+            to_peer_f32(from + ((par * sl.S + rank) * 2 + 1) * sl.kk + myg, k, m2);
           }
         __syncwarp();
         cluster_arrive();
@@ -919,7 +1015,8 @@ k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) 
         all = 0.f;
         for (int k = 0; k < sl.S; ++k) {
           const float nk = (float)(min(w.tb, (k + 1) * per) - min(w.tb, k * per)) * a.cg;
-          const float mk = from[par][k][0][myg], sk = from[par][k][1][myg];
+          const float* fk = from + (par * sl.S + k) * 2 * sl.kk + myg;
+          const float mk = fk[0], sk = fk[sl.kk];
           if (nk == 0.f) break;
           const float dk = mk - mt, f = __fdividef(nk, all + nk);
           mt = fmaf(dk, f, mt);
@@ -941,9 +1038,18 @@ k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) 
     } else {
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
-        float2 acc[1][NP] = {};
-        if (cnt > 0) st.out(acc, half, cnt, c, mean_s[par], a.cg_div);
-        gather_groups<VEC>(sl, w.rows, a.cg, a.cg_div, acc[0], scr, half ? m2_s[par] : mean_s[par]);
+        float* to = half ? m2_s[par] : mean_s[par];
+        if (sl.two) {
+          float2 v[1] = {make_float2(0.f, 0.f)};
+          if (cnt > 0)
+            v[0] = st.out(tw, half, cnt, half ? mean_s[par][tw.g0] : 0.f,
+                          half ? mean_s[par][tw.g1] : 0.f);
+          gather_two<VEC, 1>(sl, w.rows, a.cg, v, scr, {to});
+        } else {
+          float2 acc[1][NP] = {};
+          if (cnt > 0) st.out(acc, half, cnt, c, mean_s[par], a.cg_div);
+          gather_groups<VEC>(sl, w.rows, a.cg, a.cg_div, acc[0], scr, to);
+        }
         if (half == 0) {
           for (int g = threadIdx.x; g < sl.kk; g += NT)
             mean_s[par][g] = w.rows ? mean_s[par][g] / n : 0.f;
@@ -957,7 +1063,15 @@ k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) 
       }
       join_stats(a, sl, w.b, w.c0, rank, mean_s[par], m2_s[par], &n_s[par], mean_t, rstd_t);
       __syncthreads();
-      if (w.active) {
+      if (w.active && sl.two) {
+        const float ml = mean_t[tw.g0], mh = mean_t[tw.g1];
+        const float rl = rstd_t[tw.g0], rh = rstd_t[tw.g1];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          m[i] = tw.pick(i, -ml, -mh);
+          s[i] = __fmul2_rn(tw.pick(i, rl, rh), ga[i]);
+        }
+      } else if (w.active) {
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           const int ca = c + 2 * i, gx = ca / a.cg_div, gz = (ca + 1) / a.cg_div;
@@ -1006,12 +1120,13 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
   constexpr int VEC = kVec16<T>, NP = kPairs(VEC);
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int GK = UNI ? 1 : MAX_KK, UK = UNI ? 32 : 1;
-  __shared__ float gs[2][2][MAX_KK];  // by parity; read by the cluster's other blocks
+  __shared__ float gs[2][2][UNI ? 1 : MAX_KK];  // by parity; read by the cluster's other blocks
   __shared__ float m1_t[GK], m2_t[GK];
   __shared__ __align__(16) float buf[2][2][UK][NWARPS];
-  __shared__ float from[2][8][2][UK];  // sums of every block of the cluster
   const int half_bytes = sl.slots * SLOT;
-  float* scr = (float*)(smem + 2 * (size_t)half_bytes);
+  // sums of every block of the cluster (UNI): [parity][block][2][group]
+  float* from = (float*)(smem + 2 * (size_t)half_bytes);
+  float* scr = from + (UNI ? 4 * sl.S * sl.kk : 0);
   const unsigned char* mine = smem + threadIdx.x * 16;
   const uint32_t mine_a = ptx::smem_u32(mine);
   const int first = (int)blockIdx.x >> sl.S_log, rank = blockIdx.x - first * sl.S;
@@ -1020,6 +1135,7 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
   Where<VEC> w = where<VEC>(a, sl, first, rank, length_of(a, first / sl.per_sample_div));
   int ahead = length_ahead(a, sl, first + stride);
   const int c = w.v * VEC, myg = c / a.cg_div;
+  const TwoGroups<VEC> tw(sl, c, a.cg, myg);
   int cnt = rows_of(w, sl);
   const long long xinc = a.xf * w.step, dinc = a.yf * w.step;
   {
@@ -1051,7 +1167,17 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
         bk.rs[i] = make_float2(stat.y, stat.y);
       }
     } else if (w.active) {
-      bk.stats(a.stats + (long long)w.b * a.G + w.c0 / a.cg_div, c, a.cg_div);
+      const float2* st = a.stats + (long long)w.b * a.G + w.c0 / a.cg_div;
+      if (sl.two) {
+        const float2 lo = st[tw.g0], hi = st[tw.g1];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          bk.m[i] = tw.pick(i, -lo.x, -hi.x);
+          bk.rs[i] = tw.pick(i, lo.y, hi.y);
+        }
+      } else {
+        bk.stats(st, c, a.cg_div);
+      }
     }
     if (w.active && (!sl.keep || slab == first)) {
       load_param<VEC>(bk.ga, a.gamma ? a.gamma + w.c0 + c : nullptr, 1.f, al16);
@@ -1108,8 +1234,8 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
       if (sl.S > 1) {
         if (leader && warp == 0)
           for (int k = 0; k < sl.S; ++k) {
-            to_peer_f32(&from[par][rank][0][myg], k, g2);
-            to_peer_f32(&from[par][rank][1][myg], k, g1);
+            to_peer_f32(from + (par * sl.S + rank) * 2 * sl.kk + myg, k, g2);
+            to_peer_f32(from + ((par * sl.S + rank) * 2 + 1) * sl.kk + myg, k, g1);
           }
         __syncwarp();
         cluster_arrive();
@@ -1118,8 +1244,9 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
         cluster_wait();
         g2 = g1 = 0.f;
         for (int k = 0; k < sl.S; ++k) {
-          g2 += from[par][k][0][myg];
-          g1 += from[par][k][1][myg];
+          const float* fk = from + (par * sl.S + k) * 2 * sl.kk + myg;
+          g2 += fk[0];
+          g1 += fk[sl.kk];
         }
       } else {
         meanwhile();
@@ -1131,6 +1258,7 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
         k2[i] = make_float2(-g2 * rn, -g2 * rn);
       }
     } else {
+      float2 both[2];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         float2 v[NP];
@@ -1139,22 +1267,34 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
           v[i] = make_float2(0.f, 0.f);
           if (w.active) v[i] = __fmul2_rn(bk.ga[i], acc[q][i]);
         }
-        gather_groups<VEC>(sl, w.rows, a.cg, a.cg_div, v, scr, gs[par][q]);
+        if (sl.two)
+          both[q] = tw.sums(v);
+        else
+          gather_groups<VEC>(sl, w.rows, a.cg, a.cg_div, v, scr, gs[par][q]);
       }
+      if (sl.two) gather_two<VEC, 2>(sl, w.rows, a.cg, both, scr, {gs[par][0], gs[par][1]});
       if (sl.S > 1) {
         cluster_arrive();
         cluster_wait();
       }
-      join_means(a, sl, w.tb, gs[par], m1_t, m2_t);
+      join_means(a, sl, w.tb, gs[par][0], gs[par][1], m1_t, m2_t);
       __syncthreads();
-      if (w.active) means_of<VEC>(m1_t, m2_t, c, a.cg_div, k1, k2);
+      if (w.active && sl.two) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          k1[i] = tw.pick(i, -m1_t[tw.g0], -m1_t[tw.g1]);
+          k2[i] = tw.pick(i, -m2_t[tw.g0], -m2_t[tw.g1]);
+        }
+      } else if (w.active) {
+        means_of<VEC>(m1_t, m2_t, c, a.cg_div, k1, k2);
+      }
       meanwhile();
     }
     if (!sl.keep || !more) {  // these channels' sums leave the block
-      const float* res = reduce_channels<2, VEC>(sl, tot, scr, w.v, w.rg, w.active);
       const int row = sl.keep ? first / sl.per_sample_div : w.b;
-      for (int k = threadIdx.x; k < sl.W; k += NT)
-        part[((long long)row * sl.S + rank) * a.C + w.c0 + k] = make_float2(res[k], res[sl.W + k]);
+      float* to = (float*)(part + ((long long)row * sl.S + rank) * a.C + w.c0);
+      sum_channels<2, VEC>(sl, tot, scr, w.v, w.rg, w.active,
+                           [&](int q, int k, float t) { to[2 * k + q] = t; });
 #pragma unroll
       for (int i = 0; i < NP; ++i) tot[0][i] = tot[1][i] = make_float2(0.f, 0.f);
     }
@@ -1304,38 +1444,46 @@ NormCut norm_cut(const NormArgs& a, int e, int tiles, bool aligned) {
   s.nslabs = a.B * (a.G / kk);
   const long long frame = (long long)s.W * e * tiles;
   s.S = 1;
-  while (s.S < 8 && cdiv(a.T, s.S) * frame > SHARE) s.S *= 2;
+  // resident: a thread per 16-byte column, slots within the block's share.  64 KB
+  // a block keeps three blocks on an SM, and clusters go up to 16 for that: one
+  // group of 512 channels, 1000 frames, 173 us forward (8 blocks of 128 KB 223,
+  // from global memory 194); two groups, backward, 238 (338 from global memory).
+  const int cols16 = s.W * e / 16;
+  const bool slots = n.vec == 4 && cols16 <= NT;
+  auto share = [&](int S) {
+    const long long per = cdiv(a.T, S);
+    return slots ? cdiv(per, NT / cols16) * SLOT * tiles : per * frame;
+  };
+  n.res = slots && share(MAX_S) <= SHARE;
+  while (s.S < (n.res ? MAX_S : 8) && share(s.S) > SHARE) s.S *= 2;
   // few slabs: shares of at least 2048 values, until there are two blocks an SM
-  while (s.S < 8 && (long long)s.nslabs * s.S < 2 * 152 &&
+  while (s.S < (n.res ? 8 : MAX_S) && (long long)s.nslabs * s.S < 2 * 152 &&
          (long long)a.T / (2 * s.S) * s.W >= 2048 && a.T >= 4 * s.S)
     s.S *= 2;
   s.per_max = (int)cdiv(a.T, s.S);
-  // resident: a thread per 16-byte column, slots within the block's share
-  const int cols16 = s.W * e / 16;
-  if (n.vec == 4 && cols16 <= NT) {
-    s.slots = (int)cdiv(s.per_max, NT / cols16);
-    n.res = (size_t)s.slots * SLOT * tiles <= SHARE_MAX;
-  }
+  if (n.res) s.slots = (int)cdiv(s.per_max, NT / cols16);
   if (n.res) n.vec = 16 / e;
   const int vr = s.W / n.vec;
   s.cbv = vr < NT ? vr : NT;
   s.pow2 = s.cbv <= 32 && (s.cbv & (s.cbv - 1)) == 0;
-  const int rows = s.pow2 ? NWARPS : NT / s.cbv;
-  s.scratch = 4 * (rows + 1) * s.cbv * n.vec;
   for (s.lg = 0; s.lg < 5 && (kk << (s.lg + 1)) <= NT;) ++s.lg;
-  // (gather_groups takes a value per thread and channel)
-  if (n.res) s.scratch = std::max(s.scratch, (int)cdiv(4 * NT * n.vec, tiles));
   s.per_sample_div = fast_div(a.G / kk);
   for (s.S_log = 0; (1 << s.S_log) < s.S;) ++s.S_log;
   for (s.step_log = 0; (2 << s.step_log) <= NT / s.cbv;) ++s.step_log;
   s.cbv_div = fast_div(s.cbv);
-  n.smem = (n.res ? (size_t)s.slots * SLOT * tiles : 0) + (size_t)s.scratch * tiles;
   n.grid = s.nslabs * s.S;
   n.rows = a.B * s.S;
-  if (n.res) {
-    s.uni = s.pow2 && a.cg % n.vec == 0;
-    s.lanes = s.uni ? 31 & ~(s.cbv - a.cg / n.vec) : 0;
-  }
+  s.uni = n.res && s.pow2 && a.cg % n.vec == 0;
+  s.lanes = s.uni ? 31 & ~(s.cbv - a.cg / n.vec) : 0;
+  s.two = !s.uni && (a.cg >= n.vec - 1 || 2 * a.cg == n.vec);
+  // shared memory: the slots, and room for the channels' and the groups' sums
+  const int rows = s.pow2 ? NWARPS : NT / s.cbv;
+  const size_t channels = 4 * rows * s.cbv * n.vec * tiles;
+  const size_t groups = s.uni ? 0 : s.two ? 8 * NT * tiles : 4 * NT * n.vec;
+  const size_t blocks = s.uni ? 16 * s.S * s.kk : 0;
+  n.smem = n.res ? (size_t)s.slots * SLOT * tiles + blocks +
+                       std::max(tiles > 1 ? channels : 0, groups)
+                 : channels + 4 * s.cbv * n.vec * tiles;
   return n;
 }
 
@@ -1381,10 +1529,10 @@ cudaError_t launch_cluster(void (*k)(KA...), unsigned grid, int S, size_t smem, 
 }
 
 // Clusters of S blocks that the card holds at a time, asked once for each kernel,
-// device, cluster size and 4 KB of shared memory.
+// device, cluster size and 2 KB of shared memory.
 struct Resident {
-  static constexpr int kStep = 4096, kSteps = (SHARE_MAX + 20 * 1024) / kStep;
-  std::atomic<uint16_t> most[kDeviceSlots][4][kSteps + 1];
+  static constexpr int kStep = 2048, kSteps = (SMEM_MAX) / kStep;
+  std::atomic<uint16_t> most[kDeviceSlots][5][kSteps + 1];
 };
 template <typename K>
 cudaError_t most_clusters(K k, Resident* known, const NormCut& n, int* most) {
@@ -1410,8 +1558,10 @@ template <typename K>
 cudaError_t opt_in(K k, std::atomic<bool>* done) {
   std::atomic<bool>& d = done[device_slot()];
   if (d.load()) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             SHARE_MAX + 20 * 1024);
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       SMEM_MAX);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) d.store(true);
   return e;
 }
@@ -1484,7 +1634,7 @@ size_t rnnt_norm_saved_bytes(const rnnt_norm_dims* dims) {
 
 size_t rnnt_norm_workspace_bytes(const rnnt_norm_dims* dims) {
   NormArgs a;
-  return norm_args(dims, &a) ? align_up(8 * 8 * (size_t)a.B * a.C + 8) : 0;  // up to 8 blocks a slab
+  return norm_args(dims, &a) ? align_up(8 * MAX_S * (size_t)a.B * a.C + 8) : 0;  // a row for every block of a slab
 }
 
 rnnt_status rnnt_norm_fwd(const rnnt_norm_dims* dims, const void* x, const float* gamma,
