@@ -99,7 +99,7 @@ __device__ __forceinline__ float2 dact2(float2 dy, float2 u) {
 }
 
 // ---- vectors ------------------------------------------------------------------
-// A thread's VEC (8, 4 or 1) consecutive channels of a frame, as pairs of fp32.
+// A thread's VEC (8, 4, 2 or 1) consecutive channels of a frame, as pairs of fp32.
 constexpr int kPairs(int vec) { return vec == 1 ? 1 : vec / 2; }
 template <int VEC>
 struct Ch {
@@ -111,6 +111,11 @@ __device__ __forceinline__ Ch<VEC> load_ch(const T* p) {
   Ch<VEC> c;
   if constexpr (VEC == 1) {
     c.v[0] = make_float2(to_f<T>(*p), 0.f);
+  } else if constexpr (VEC == 2 && sizeof(T) == 4) {
+    c.v[0] = *(const float2*)p;
+  } else if constexpr (VEC == 2) {
+    const uint32_t q = *(const uint32_t*)p;
+    c.v[0] = make_float2(ptx::bf16lo(q), ptx::bf16hi(q));
   } else if constexpr (sizeof(T) == 4) {
     const float4 q = *(const float4*)p;
     c.v[0] = make_float2(q.x, q.y);
@@ -132,6 +137,10 @@ template <int VEC, typename T>
 __device__ __forceinline__ void store_ch(T* p, const Ch<VEC>& c) {
   if constexpr (VEC == 1) {
     *p = from_f<T>(c.v[0].x);
+  } else if constexpr (VEC == 2 && sizeof(T) == 4) {
+    *(float2*)p = c.v[0];
+  } else if constexpr (VEC == 2) {
+    *(uint32_t*)p = ptx::pack_bf16x2(c.v[0].x, c.v[0].y);
   } else if constexpr (sizeof(T) == 4) {
     *(float4*)p = make_float4(c.v[0].x, c.v[0].y, c.v[1].x, c.v[1].y);
   } else if constexpr (VEC == 4) {
@@ -152,7 +161,7 @@ __device__ __forceinline__ void load_param(float2 (&v)[kPairs(VEC)], const float
   if (!p) {
 #pragma unroll
     for (int i = 0; i < kPairs(VEC); ++i) v[i] = make_float2(other, other);
-  } else if (VEC > 1 && al16) {
+  } else if (VEC >= 4 && al16) {
 #pragma unroll
     for (int i = 0; i < VEC / 4; ++i) {
       const float4 q = __ldg((const float4*)p + i);
@@ -395,9 +404,9 @@ __device__ __forceinline__ void gather_two(const Slab& sl, int rows, int cg,
 // 141 us forward and 157 backward, with 4 and 2 frames 164 and 208; 333 channels,
 // an element a thread: 286 and 351, with 4 and 2 frames 350 and 665).
 template <int VEC>
-constexpr int kFlyFwd = VEC == 1 ? 16 : 8;
+constexpr int kFlyFwd = VEC <= 2 ? 16 : 8;
 template <int VEC>
-constexpr int kFlyBwd = VEC == 1 ? 8 : 4;
+constexpr int kFlyBwd = VEC <= 2 ? 8 : 4;
 
 // The block's slab, frames and column.
 template <int VEC>
@@ -544,8 +553,8 @@ template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(NT, 5)
 k_norm_fwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) {
   extern __shared__ __align__(16) unsigned char smem[];
-  // (gs[1], mean_s and n_s are read by the cluster's other blocks)
-  __shared__ float gs[2][MAX_KK], mean_s[MAX_KK], n_s;
+  // (mean_s, m2_s and n_s are read by the cluster's other blocks)
+  __shared__ float gs[2][MAX_KK], mean_cb[MAX_KK], mean_s[MAX_KK], m2_s[MAX_KK], n_s;
   __shared__ float mean_t[MAX_KK], rstd_t[MAX_KK];
   float* scr = (float*)smem;
   const int slab = (int)blockIdx.x >> sl.S_log;
@@ -556,34 +565,44 @@ k_norm_fwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ 
   zero_tail<VEC, T>(a, sl, w, ys, a.yf);
   const long long ld = a.xf, inc = ld * w.step;
   const int nb = sl.cbv * VEC, cnt = rows_of(w, sl);
-  const float n = (float)w.rows * a.cg;
-  for (int g = threadIdx.x; g < sl.kk; g += NT) gs[0][g] = gs[1][g] = 0.f;
+  for (int g = threadIdx.x; g < sl.kk; g += NT) gs[0][g] = gs[1][g] = mean_s[g] = m2_s[g] = 0.f;
+  if (threadIdx.x == 0) n_s = (float)w.rows * a.cg;
   __syncthreads();
-  Partial<VEC> st;
 #pragma unroll 1
-  for (int half = 0; half < 2; ++half) {
-#pragma unroll 1
-    for (int cb = 0; cb < sl.W; cb += nb) {
-      const int c = cb + w.v * VEC;
-      const bool in = w.active && c < sl.W;
-      float2 acc[1][kPairs(VEC)] = {};
-      if (in && cnt > 0) {
-        if (half == 0 || nb < sl.W) {  // (one column block keeps its sums; more read again)
-          const T* p = src + w.rg * ld + c;
-          st.begin(load_ch<VEC, T>(p));
+  for (int cb = 0; cb < sl.W; cb += nb) {
+    const int c = cb + w.v * VEC;
+    const bool in = w.active && c < sl.W;
+    Partial<VEC> st;
+    if (in && cnt > 0) {
+      const T* p = src + w.rg * ld + c;
+      st.begin(load_ch<VEC, T>(p));
 #pragma unroll (kFlyFwd<VEC>)
-          for (int k = 0; k < cnt; ++k, p += inc) st.add(load_ch<VEC, T>(p));
-          st.end(cnt);
-        }
-        st.out(acc, half, cnt, c, mean_s, a.cg_div);
-      }
+      for (int k = 0; k < cnt; ++k, p += inc) st.add(load_ch<VEC, T>(p));
+      st.end(cnt);
+    }
+    // the column block's sums, then its squares about its own means
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      float2 acc[1][kPairs(VEC)] = {};
+      if (in && cnt > 0) st.out(acc, half, cnt, c, mean_cb, a.cg_div);
       const float* res = reduce_channels<1, VEC>(sl, acc, scr, w.v, w.rg, in);
       reduce_groups<1, VEC>(sl, a.cg, cb, res, gs + half, [](int) { return 1.f; });
-    }
-    __syncthreads();
-    if (half == 0) {
-      for (int g = threadIdx.x; g < sl.kk; g += NT) mean_s[g] = w.rows ? gs[0][g] / n : 0.f;
-      if (threadIdx.x == 0) n_s = n;
+      __syncthreads();
+      for (int g = threadIdx.x; g < sl.kk; g += NT) {
+        // the group's channels in this column block, and in those before
+        const int g0 = g * a.cg, now = min(g0 + a.cg, min(cb + nb, sl.W)) - max(g0, cb);
+        if (now <= 0 || w.rows == 0) continue;
+        const float n1 = (float)w.rows * now, n0 = (float)w.rows * max(0, cb - g0);
+        if (half == 0) {
+          mean_cb[g] = gs[0][g] / n1;
+          gs[0][g] = 0.f;
+        } else {
+          const float d = mean_cb[g] - mean_s[g], f = n1 / (n0 + n1);
+          mean_s[g] += d * f;
+          m2_s[g] += gs[1][g] + d * d * (n0 * f);
+          gs[1][g] = 0.f;
+        }
+      }
       __syncthreads();
     }
   }
@@ -591,7 +610,7 @@ k_norm_fwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ 
     cluster_arrive();
     cluster_wait();
   }
-  join_stats(a, sl, w.b, w.c0, w.rank, mean_s, gs[1], &n_s, mean_t, rstd_t);
+  join_stats(a, sl, w.b, w.c0, w.rank, mean_s, m2_s, &n_s, mean_t, rstd_t);
   __syncthreads();
   if (sl.S > 1) cluster_arrive();  // (waited for at the end: peers may still read)
   T* yt = ys + (long long)w.t0 * a.yf;
@@ -1411,19 +1430,19 @@ struct NormCut {
   size_t smem;
 };
 
-NormCut norm_cut(const NormArgs& a, int e, int tiles, bool aligned) {
+NormCut norm_cut(const NormArgs& a, int e, int tiles, int align) {
   NormCut n{};
   // the fewest whole groups that make 64-byte pieces of a frame (16-byte
   // aligned ones) and, while there are more slabs than the SMs take twice, 16 KB:
   // a slab costs its reductions, whatever its length (250 frames of 512 channels,
   // 4096 samples: 337 us forward and 546 backward, against 433 and 780 with slabs
-  // of 8 KB upward; from 32 KB upward 352 and 669).  Short of alignment, 32 channels.
+  // of 8 KB upward; from 32 KB upward 352 and 669).  Short of alignment, 64 channels in pairs or 32.
   auto enough = [&](int k) {
     return (long long)a.T * k * a.cg * e >= 16384 || (long long)a.B * (a.G / k) <= 2 * 3 * 152;
   };
   int kk = 0;
   n.vec = 1;
-  if (aligned)
+  if (align == 16)
     for (int k = 1; k <= a.G && k <= MAX_KK; ++k)
       if (a.G % k == 0 && (long long)k * a.cg * e % 16 == 0) {
         // (groups as long as a thread may hold a 16-byte column of them)
@@ -1431,6 +1450,13 @@ NormCut norm_cut(const NormArgs& a, int e, int tiles, bool aligned) {
         kk = k;
         n.vec = 4;
         if (k * a.cg * e >= 64 && enough(k)) break;
+      }
+  if (!kk && align >= 2 * e)
+    for (int k = 1; k <= a.G && k <= MAX_KK; ++k)
+      if (a.G % k == 0 && k * a.cg % 2 == 0) {
+        kk = k;
+        n.vec = 2;
+        if (k * a.cg >= 64) break;
       }
   if (!kk)
     for (int k = 1; k <= a.G && k <= MAX_KK; ++k)
@@ -1587,7 +1613,7 @@ cudaError_t norm_launch(KF kf, KB kb, std::atomic<bool>* fdone, std::atomic<bool
 template <typename T, int ACT>
 cudaError_t norm_launch_cut(const NormArgs& a, NormCut* n, const void* x, const void* dy,
                             void* out, float2* part, cudaStream_t st) {
-  static std::atomic<bool> done[8][kDeviceSlots];
+  static std::atomic<bool> done[10][kDeviceSlots];
   static Resident known[4];
   if (n->res && n->sl.uni)
     return norm_launch<T>(k_norm_fwd_res<T, ACT, 1>, k_norm_bwd_res<T, ACT, 1>, done[6], done[7],
@@ -1598,6 +1624,9 @@ cudaError_t norm_launch_cut(const NormArgs& a, NormCut* n, const void* x, const 
   if (n->vec == 4)
     return norm_launch<T>(k_norm_fwd_stream<T, 4, ACT>, k_norm_bwd_stream<T, 4, ACT>, done[2],
                           done[3], nullptr, a, n, x, dy, out, part, st);
+  if (n->vec == 2)
+    return norm_launch<T>(k_norm_fwd_stream<T, 2, ACT>, k_norm_bwd_stream<T, 2, ACT>, done[8],
+                          done[9], nullptr, a, n, x, dy, out, part, st);
   return norm_launch<T>(k_norm_fwd_stream<T, 1, ACT>, k_norm_bwd_stream<T, 1, ACT>, done[4],
                         done[5], nullptr, a, n, x, dy, out, part, st);
 }
@@ -1613,11 +1642,14 @@ cudaError_t norm_launch_act(const NormArgs& a, NormCut* n, const void* x, const 
   }
 }
 
-// Rows that 16-byte copies and 4-element stores may take: x and dx, y and dy.
-bool norm_aligned(const NormArgs& a, int e, const void* x, const void* y, const void* dx) {
-  const int v = 16 / e;
-  return aligned_to(x, 16) && aligned_to(y, 16) && aligned_to(dx, 16) && a.xf % v == 0 &&
-         a.xb % v == 0 && a.yf % v == 0 && a.yb % v == 0;
+// Alignment of every row of x and dx, y and dy: 16 bytes, or two elements, or one.
+int norm_align(const NormArgs& a, int e, const void* x, const void* y, const void* dx) {
+  auto all = [&](int bytes) {
+    const int v = bytes / e;
+    return aligned_to(x, bytes) && aligned_to(y, bytes) && aligned_to(dx, bytes) &&
+           a.xf % v == 0 && a.xb % v == 0 && a.yf % v == 0 && a.yb % v == 0;
+  };
+  return all(16) ? 16 : all(2 * e) ? 2 * e : e;
 }
 
 }  // namespace
@@ -1648,7 +1680,7 @@ rnnt_status rnnt_norm_fwd(const rnnt_norm_dims* dims, const void* x, const float
   cudaStream_t st = (cudaStream_t)stream;
   ProfScope ps("norm_fwd", st);
   const int e = op_size(dims->dtype);
-  NormCut n = norm_cut(a, e, 1, norm_aligned(a, e, x, y, nullptr));
+  NormCut n = norm_cut(a, e, 1, norm_align(a, e, x, y, nullptr));
   OPS_CHECK(e == 4 ? norm_launch_act<float>(a, &n, x, nullptr, y, nullptr, st)
                    : norm_launch_act<__nv_bfloat16>(a, &n, x, nullptr, y, nullptr, st));
   return RNNT_OK;
@@ -1668,7 +1700,7 @@ rnnt_status rnnt_norm_bwd(const rnnt_norm_dims* dims, const void* x, const void*
   cudaStream_t st = (cudaStream_t)stream;
   float2* part = (float2*)ws;
   const int e = op_size(dims->dtype);
-  NormCut n = norm_cut(a, e, 2, norm_aligned(a, e, x, dy, dx));
+  NormCut n = norm_cut(a, e, 2, norm_align(a, e, x, dy, dx));
   if (a.B > 0) {
     ProfScope ps("norm_bwd", st);
     OPS_CHECK(e == 4 ? norm_launch_act<float>(a, &n, x, dy, dx, part, st)

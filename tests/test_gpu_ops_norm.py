@@ -263,3 +263,16 @@ def test_another_stream_and_a_graph():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(got, ref))
+
+
+# Rows of every alignment (16 bytes, two elements, one), threads of one, two and more groups,
+# one group over many blocks, and more slabs than the card holds at a time.
+CUTS = [(3, 70, 330, 2), (2, 65, 22, 1), (4, 40, 333, 1), (1, 1100, 1022, 1), (3, 90, 56, 8),
+        (3, 90, 72, 8), (2, 120, 96, 24), (3, 1000, 512, 1), (2, 9000, 64, 4), (2, 700, 768, 2),
+        (1500, 9, 512, 1), (700, 33, 120, 8)]
+
+
+@pytest.mark.parametrize("B,T,C,G", CUTS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_cuts(B, T, C, G, dtype):
+    test_forward_and_gradients(B, T, C, G, dtype, "silu")
