@@ -67,6 +67,7 @@ struct OrthArgs {
   int m, n, tall, batch, steps;
   int exact;            // three terms in gram and update too
   int rows, cols;       // of G, and of X
+  FastDiv chunks;       // of eight columns in a row
   long long ldx, ldm;   // row strides of X; of S and P
   __half* X[2][2];
   __half* S[2];
@@ -79,6 +80,7 @@ struct OrthArgs {
   int splits, kb_split; // gram: K ranges and their length in K blocks
   int bn[3];            // tile width of each product
   int ut_m, ut_n;       // update: tiles
+  int ut_whole;         // the tiles after these go out as two halves each
   const void* G;
   int in_f32;
   long long in_ld, in_batch;
@@ -130,16 +132,17 @@ k_orth_sumsq(OrthArgs a, double* sums) {
     if (blockIdx.y == 0) *a.abort = 0;
   }
   const T* g = (const T*)a.G + blockIdx.y * a.in_batch;
-  const int chunks = (a.cols + 7) / 8;  // of eight columns
+  const int chunks = a.chunks.d;
   const bool vec = a.in_ld % 8 == 0 && a.in_batch % 8 == 0 && ((uintptr_t)a.G & 15) == 0;
   double s = 0;
-  const long long total = (long long)a.rows * chunks, stride = gridDim.x * 256LL;
-  for (long long i0 = blockIdx.x * 256LL + threadIdx.x; i0 < total; i0 += 4 * stride) {
+  // (unsigned: the last step may pass 2^31)
+  const unsigned total = (unsigned)a.rows * chunks, stride = gridDim.x * 256;
+  for (unsigned i0 = blockIdx.x * 256 + threadIdx.x; i0 < total; i0 += 4 * stride) {
     float v[4][8];  // four chunks' loads in flight
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const long long i = i0 + u * stride;
-      const int r = (int)(i / chunks), c = (int)(i - (long long)r * chunks) * 8;
+      const unsigned i = i0 + u * stride;
+      const int r = (int)i / a.chunks, c = ((int)i - r * chunks) * 8;
       if (i < total) {
         load8<T>(g + r * a.in_ld + c, a.cols - c, vec, v[u]);
       } else {
@@ -231,7 +234,7 @@ struct Work {
   int stage_bytes, stages;
 };
 struct Unit {
-  int b, m0, n0, kb0, kb1, diag;
+  int b, m0, n0, kb0, kb1, diag, bn;
 };
 
 template <int EXACT>
@@ -257,7 +260,7 @@ __device__ __forceinline__ Work work_of(const OrthArgs& a, int kind, int cur) {
     w.a_buf = a.tall ? cur : BUF_P;
     w.b_buf = a.tall ? BUF_P : cur;
     w.b_mn = !a.tall;
-    w.units = a.batch * a.ut_m * a.ut_n;
+    w.units = 2 * a.batch * a.ut_m * a.ut_n - a.ut_whole;
   }
   w.kbs = (w.K + BK - 1) / BK;
   w.stage_bytes = (BM + w.bn) * BK * 2 << w.fat;
@@ -271,11 +274,18 @@ __device__ __forceinline__ Unit unit_of(const OrthArgs& a, const Work& w, int u)
   q.kb0 = 0;
   q.kb1 = w.kbs;
   q.diag = 0;
+  q.bn = w.bn;
   if (w.kind == UPDATE) {
-    const int n = u % a.ut_n, rest = u / a.ut_n;
+    int t = u, right = 0;
+    if (u >= a.ut_whole) {
+      t = a.ut_whole + (u - a.ut_whole) / 2;
+      right = (u - a.ut_whole) & 1;
+      q.bn = w.bn / 2;
+    }
+    const int n = t % a.ut_n, rest = t / a.ut_n;
     q.b = rest / a.ut_m;
     q.m0 = (rest - q.b * a.ut_m) * BM;
-    q.n0 = n * w.bn;
+    q.n0 = n * w.bn + right * q.bn;
     return q;
   }
   const int per_block = BM / w.bn, per = a.blocks * per_block;
@@ -553,8 +563,8 @@ __device__ __forceinline__ void finish(const OrthArgs& a, const Work& w, const U
 }
 
 // Blocks of 64 columns of a fast update's tile.
-__device__ __forceinline__ int boxes_of(const OrthArgs& a, const Work& w, const Unit& q) {
-  return min(w.bn / 64, (a.cols - q.n0 + 63) / 64);
+__device__ __forceinline__ int boxes_of(const OrthArgs& a, const Unit& q) {
+  return min(q.bn / 64, (a.cols - q.n0 + 63) / 64);
 }
 
 // Fast update of 32 columns of the thread's row of an X block in shared memory
@@ -635,25 +645,25 @@ __device__ __forceinline__ float inverse_norm(const OrthArgs& a, int b) {
 // chunks of eight in flight.
 template <typename T>
 __device__ __forceinline__ void convert(const OrthArgs& a, int tid, int nthreads) {
-  const int chunks = (a.cols + 7) / 8;
+  const int chunks = a.chunks.d;
+  const unsigned per = (unsigned)a.rows * chunks;
   const bool vec = a.in_ld % 8 == 0 && a.in_batch % 8 == 0 && ((uintptr_t)a.G & 15) == 0;
-  const long long per = (long long)a.rows * chunks;
   for (int b = 0; b < a.batch; ++b) {
     const float f = inverse_norm(a, b) * (1 << XE);
-    for (long long i0 = tid; i0 < per; i0 += 4LL * nthreads) {
+    for (unsigned i0 = tid; i0 < per; i0 += 4 * nthreads) {
       float v[4][8];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const long long i = i0 + (long long)u * nthreads;
-        const int r = (int)(i / chunks), c = (int)(i - (long long)r * chunks) * 8;
+        const unsigned i = i0 + u * nthreads;
+        const int r = (int)i / a.chunks, c = ((int)i - r * chunks) * 8;
         if (i < per)
           load8<T>((const T*)a.G + b * a.in_batch + r * a.in_ld + c, a.cols - c, vec, v[u]);
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const long long i = i0 + (long long)u * nthreads;
+        const unsigned i = i0 + u * nthreads;
         if (i >= per) break;
-        const int r = (int)(i / chunks), c = (int)(i - (long long)r * chunks) * 8;
+        const int r = (int)i / a.chunks, c = ((int)i - r * chunks) * 8;
         uint4 h, l;
         split2(v[u][0] * f, v[u][1] * f, h.x, l.x);
         split2(v[u][2] * f, v[u][3] * f, h.y, l.y);
@@ -797,7 +807,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
             }
             // (a block on the diagonal multiplies its rows by themselves: one load)
             ptx::mbar_arrive_expect_tx(&full[stage],
-                                       q.diag ? BM * BK * 2 << w.fat : w.stage_bytes);
+                                       (BM + (q.diag ? 0 : q.bn)) * BK * 2 << w.fat);
             unsigned char* d = smem + stage * w.stage_bytes;
             // boxes of 64 x 64: K-major rows (k, row), MN-major rows (row, k)
             const int k0 = kb * BK;
@@ -811,7 +821,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
               const CUtensorMap* m = &maps.m[w.b_buf][pl];
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                if (64 * j >= w.bn) break;
+                if (64 * j >= q.bn) break;
                 const int r = q.n0 + 64 * j;
                 tma_load_3d(d, m, &full[stage], w.b_mn ? r : k0, w.b_mn ? k0 : r, q.b);
                 d += BOX;
@@ -836,10 +846,9 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
       for (int g = 0; g < 3 * a.steps && !*abort_flag; ++g) {
         const int step = g / 3, kind = g - 3 * step;
         const Work w = work_of<EXACT>(a, kind, step & 1);
-        const uint32_t idesc = idesc_f16(w.bn, w.a_mn, w.b_mn);
         // 16-byte units: planes, one K step of 16 in each layout, and the
         // descriptors without their address
-        const uint32_t plane_a = BM * BK * 2 / 16, plane_b = w.bn * BK * 2 / 16;
+        const uint32_t plane_a = BM * BK * 2 / 16;
         const uint32_t step_a = w.a_mn ? 128 : 2, step_b = w.b_mn ? 128 : 2;
         const uint64_t desc_a = ptx::sdesc_sw128(0, w.a_mn ? 8192 : 16, 1024);
         const uint64_t desc_b = ptx::sdesc_sw128(0, w.b_mn ? 8192 : 16, 1024);
@@ -853,7 +862,8 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t d = tmem + acc * 256;
+          const uint32_t d = tmem + acc * 256, idesc = idesc_f16(q.bn, w.a_mn, w.b_mn);
+          const uint32_t plane_b = q.bn * BK * 2 / 16;
           bool ok = true;
           for (int kb = q.kb0; kb < q.kb1; ++kb) {
             if (!ptx::mbar_wait(&full[stage], par >> stage & 1, 4 * WAIT_NS)) {
@@ -932,7 +942,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
               tma_load_3d(d + j * BOX, &maps.m[cur][j >> 1], bar, q.n0 + 64 * lc,
                           q.m0 + 64 * (j & 1), q.b);
             ++n_load;
-            if (++lc == boxes_of(a, w, q)) { lc = 0; lu += ctas; }
+            if (++lc == boxes_of(a, q)) { lc = 0; lu += ctas; }
           }
           const Unit q = unit_of(a, w, su);
           if (!ptx::mbar_wait(&x_done[n_done & 1], n_done >> 1 & 1, 4 * WAIT_NS)) {
@@ -951,7 +961,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
             ptx::bulk_wait_read();
           }
           ++n_done;
-          if (++sc == boxes_of(a, w, q)) { sc = 0; su += ctas; }
+          if (++sc == boxes_of(a, q)) { sc = 0; su += ctas; }
         }
         ptx::bulk_wait_all();
         ptx::mbar_arrive(x_stored);
@@ -1004,7 +1014,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
         ptx::tc_fence_after();
         const uint32_t t0 = tmem + acc * 256 + ((uint32_t)(sub * 32) << 16);
         if (!EXACT && w.boxed) {
-          const int boxes = boxes_of(a, w, q);
+          const int boxes = boxes_of(a, q);
 #pragma unroll 1
           for (int c = 0; c < boxes; ++c, ++n_box) {
             float v[32];
@@ -1030,7 +1040,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
           continue;
         }
 #pragma unroll 1
-        for (int c = half; c < w.bn / 32; c += 2) {
+        for (int c = half; c < q.bn / 32; c += 2) {
           float v[32];
           ptx::tmem_ld32(t0 + c * 32, v);
           if (EXACT || w.fat) {
@@ -1047,7 +1057,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
           }
           const Ahead now = ahead;
           const Block kn = k;
-          if (c + 2 < w.bn / 32) {
+          if (c + 2 < q.bn / 32) {
             k = block_of(a, w, q, sub * 32, (c + 2) * 32);
             look_ahead(a, w, q, step & 1, k, ahead);
           }
@@ -1429,6 +1439,7 @@ bool orth_plan(const rnnt_orth_dims* d, OrthPlan* p) {
       (a.in_batch < 0 || a.out_batch < (long long)(a.rows - 1) * a.out_ld + a.cols))
     return false;
   a.ldx = cdiv(a.cols, 8) * 8;
+  a.chunks = fast_div((uint32_t)cdiv(a.cols, 8));
   a.ldm = cdiv(a.m, 8) * 8;
   const long long nt = cdiv(a.m, BM);
   a.blocks = (int)(nt * (nt + 1) / 2);
@@ -1452,11 +1463,21 @@ bool orth_plan(const rnnt_orth_dims* d, OrthPlan* p) {
   const int un = a.tall ? a.m : a.n, um = a.tall ? a.n : a.m;
   a.ut_m = (int)cdiv(um, BM);
   auto tiles = [&](int bn) { return (long long)a.batch * a.ut_m * cdiv(un, bn); };
-  auto rows = [&](int bn) { return cdiv(tiles(bn), kSms) * (BM + bn); };
+  // the tiles of the last round go out as two halves each where the SMs take them
+  // at once (16384 x 1024, 512 tiles of 256: 420 us, in four whole rounds 440)
+  auto halved = [&](int bn) {
+    const long long rest = tiles(bn) % kSms;
+    return tiles(bn) > kSms && bn >= 128 && 2 * rest <= kSms &&
+                   (un - 1) % bn >= bn / 2 ? rest : 0;
+  };
+  auto rows = [&](int bn) {
+    return cdiv(tiles(bn), kSms) * (BM + bn) - (halved(bn) ? bn / 2 : 0);
+  };
   a.bn[UPDATE] = 64;
   for (int bn = 128; bn <= (a.exact ? 128 : 256); bn *= 2)
     if (rows(bn) < rows(a.bn[UPDATE])) a.bn[UPDATE] = bn;
   a.ut_n = (int)cdiv(un, a.bn[UPDATE]);
+  a.ut_whole = (int)(tiles(a.bn[UPDATE]) - halved(a.bn[UPDATE]));
   const long long gram_units = gu * (BM / a.bn[GRAM]) * a.splits;
   const long long units = std::max(
       {gram_units, gu * (BM / a.bn[POLY]), (long long)a.batch * a.ut_m * a.ut_n});
