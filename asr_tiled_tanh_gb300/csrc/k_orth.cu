@@ -73,6 +73,7 @@ struct OrthArgs {
   __half* S[2];
   __half* P[2];
   int thin;             // blocks per matrix of k_orth_thin (0: k_orth)
+  int cluster;          // they are a cluster
   float* part;          // gram partial tiles [splits][batch][tiles][128][bn];
                         // k_orth_thin: [batch][thin][128][128]
   float* sum;           // k_orth_thin: their sum [batch][128][128]
@@ -1094,11 +1095,16 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
 // S and as the MN-major operand of its share of P X; S, then P over it, have the
 // same layout.  So a product is three MMA chains and a pass of the 128 x 128
 // accumulator through registers, about 0.7 us, against 4.4 us through global
-// memory and a grid barrier; only the blocks' shares of S meet there, once per
-// step.  All products exact.
+// memory and a grid barrier; only the blocks' shares of S meet, once per step:
+// over the shared memory of a cluster for up to 16 blocks (128 x 2048: 95 us,
+// 126 x 142: 75), else through global memory (132 and 107).  All products exact.
 constexpr int THIN_THREADS = 256;
 constexpr int IMG = 128 * 128 * 2;           // bytes of a 128 x 128 plane: two 64-column blocks
 constexpr int THIN_SMEM = 1024 + 4 * IMG + 256;
+// A cluster's blocks take their pieces of S here: 8 rows x 64 columns in fp32, 32
+// at most, dealt out evenly, each from every block (at most 45 for 2 to 16 blocks).
+constexpr int MAX_THIN_CLUSTER = 16, PIECE = 8 * 64 * 4;
+constexpr int THIN_CLUSTER_SMEM = THIN_SMEM + 45 * PIECE;
 
 // byte of (row, col) in a plane, col a multiple of 8
 __device__ __forceinline__ uint32_t img_at(int row, int col) {
@@ -1226,6 +1232,71 @@ __device__ __forceinline__ void thin_reduce(const float* part, float* sum, int c
   }
 }
 
+__device__ __forceinline__ void cluster_meet() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the same shared address in block `rank` of the cluster, and a store to it
+__device__ __forceinline__ uint32_t peer_of(uint32_t a, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void peer_store(uint32_t a, const uint4& v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+// byte of columns 4 q .. of row r in a piece (swizzled: a warp writes by rows)
+__device__ __forceinline__ uint32_t piece_at(int r, int q) { return r * 256 + ((q ^ r) << 4); }
+
+// The blocks' shares of S meet in their cluster.  Every block's share stands in
+// its planes of S, as pieces; each goes to the block that owns it, which adds it up
+// over the blocks in order and stores it, as hi and lo, into every block's planes.
+// Both ways a warp's stores are contiguous, or the network between the SMs takes
+// them one by one.
+__device__ __forceinline__ void thin_share(const OrthArgs& a, int c, int pieces, float f,
+                                           const unsigned char* S, uint32_t ss) {
+  const int own = (pieces + a.thin - 1) / a.thin;
+  const unsigned char* in = S + 2 * IMG;
+  __syncthreads();
+  for (int it = threadIdx.x; it < pieces * (PIECE / 16); it += THIN_THREADS) {
+    const int u = it / (PIECE / 16), to = u / own;
+    peer_store(peer_of(ss + 2 * IMG + (c * own + u - to * own) * PIECE + it % (PIECE / 16) * 16, to),
+               *(const uint4*)(S + it * 16));
+  }
+  cluster_meet();
+  const int mine = min(own, pieces - c * own);
+  for (int it = threadIdx.x; it < mine * 64; it += THIN_THREADS) {
+    const int ul = it >> 6, r = it >> 3 & 7, q = it & 7;
+    float v[8] = {};
+#pragma unroll 4
+    for (int k = 0; k < a.thin; ++k) {
+      const unsigned char* p = in + (k * own + ul) * PIECE;
+      const float4 x = *(const float4*)(p + piece_at(r, 2 * q));
+      const float4 y = *(const float4*)(p + piece_at(r, 2 * q + 1));
+      v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+      v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    }
+    uint4 h, l;
+    split2(v[0] * f, v[1] * f, h.x, l.x);
+    split2(v[2] * f, v[3] * f, h.y, l.y);
+    split2(v[4] * f, v[5] * f, h.z, l.z);
+    split2(v[6] * f, v[7] * f, h.w, l.w);
+    const int u = c * own + ul;
+    const uint32_t at = ss + img_at((u & 15) * 8 + r, (u >> 4) * 64 + q * 8);
+    for (int k = 0; k < a.thin; ++k) {
+      const uint32_t to = peer_of(at, k);
+      peer_store(to, h);
+      peer_store(to + IMG, l);
+    }
+  }
+  fence_proxy_async();  // (the tensor cores of every block read the planes)
+  cluster_meet();
+}
+
 __global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ float4 tmp[8][32];
@@ -1252,6 +1323,7 @@ __global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a)
   else thin_load<__nv_bfloat16>(a, b, j0, X);
   ptx::tc_fence_before();
   __syncthreads();
+  if (a.cluster) cluster_meet();  // (the others run: their shared memory may be written)
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const uint32_t xs = ptx::smem_u32(X), ss = ptx::smem_u32(S);
@@ -1303,7 +1375,20 @@ __global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a)
     // S
     product(xs, xs, 0, mk * 16, nk);
     const float fs = 1.f / (1 << (2 * XE - SE));
-    if (a.thin > 1) {  // (stored by columns: lanes are rows)
+    if (a.cluster) {
+#pragma unroll 1
+      for (int c0 = cbase; c0 < mk * 16; c0 += 64) {
+        float v[32];
+        acc32(c0, v);
+        // piece (64 columns) * 16 + (8 rows)
+        unsigned char* p = S + ((c0 >> 6) * 16 + (row >> 3)) * PIECE;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *(float4*)(p + piece_at(row & 7, (c0 & 63) / 4 + i)) =
+              make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      }
+      thin_share(a, c, (mk * 16 + 63) / 64 * 16, fs, S, ss);
+    } else if (a.thin > 1) {  // (stored by columns: lanes are rows)
 #pragma unroll 1
       for (int c0 = cbase; c0 < a.m; c0 += 64) {
         float v[32];
@@ -1317,7 +1402,7 @@ __global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a)
       meet();
     }
 #pragma unroll 1
-    for (int c0 = cbase; c0 < mk * 16; c0 += 64) {
+    for (int c0 = cbase; c0 < mk * 16 && !a.cluster; c0 += 64) {
       float v[32];
       if (a.thin > 1) {
 #pragma unroll
@@ -1511,12 +1596,12 @@ bool orth_plan(const rnnt_orth_dims* d, OrthPlan* p) {
 // Blocks that wait for one another are all resident at once: a cooperative launch.
 template <int WHICH, typename... KA, typename... A>
 cudaError_t launch_resident(void (*k)(KA...), bool together, int grid, int threads, size_t smem,
-                            cudaStream_t st, const A&... args) {
+                            size_t smem_max, cudaStream_t st, const A&... args) {
   static std::atomic<bool> opted_in[kDeviceSlots];  // per kernel (WHICH) and device
   std::atomic<bool>& opted = opted_in[device_slot()];
   if (!opted.load()) {
     const cudaError_t e =
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_max);
     if (e != cudaSuccess) return e;
     opted.store(true);
   }
@@ -1533,17 +1618,55 @@ cudaError_t launch_resident(void (*k)(KA...), bool together, int grid, int threa
   return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
+// The blocks of a thin matrix as a cluster, where the card can hold one (*done).
+cudaError_t launch_thin_cluster(OrthArgs& a, cudaStream_t st, bool* done) {
+  static std::atomic<int> fits[kDeviceSlots][MAX_THIN_CLUSTER + 1];  // 0: not asked, 1: no, 2: yes
+  *done = false;
+  if (a.thin < 2 || a.thin > MAX_THIN_CLUSTER) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = a.thin;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(a.thin * a.batch);
+  cfg.blockDim = dim3(THIN_THREADS);
+  cfg.dynamicSmemBytes = THIN_CLUSTER_SMEM;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  std::atomic<int>& f = fits[device_slot()][a.thin];
+  if (!f.load()) {
+    cudaError_t e = cudaFuncSetAttribute(k_orth_thin, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         THIN_CLUSTER_SMEM);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k_orth_thin, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, k_orth_thin, &cfg) != cudaSuccess) {
+      cudaGetLastError();  // (no cluster of this size: not an error of the call)
+      n = 0;
+    }
+    f.store(n > 0 ? 2 : 1);
+  }
+  if (f.load() != 2) return cudaSuccess;
+  *done = true;
+  a.cluster = 1;
+  return cudaLaunchKernelEx(&cfg, k_orth_thin, (const OrthArgs)a);
+}
+
 cudaError_t orth_launch(OrthPlan& p, cudaStream_t st) {
   OrthArgs& a = p.a;
   double* sums = const_cast<double*>(a.sums);
   const dim3 grid(a.nb, a.batch);
   if (a.in_f32) k_orth_sumsq<float><<<grid, 256, 0, st>>>(a, sums);
   else k_orth_sumsq<__nv_bfloat16><<<grid, 256, 0, st>>>(a, sums);
-  const cudaError_t e = cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  bool done = false;
+  if ((e = launch_thin_cluster(a, st, &done)) != cudaSuccess || done) return e;
   if (a.thin)
-    return launch_resident<2>(k_orth_thin, a.thin > 1, a.thin * a.batch, THIN_THREADS, THIN_SMEM, st,
-                           a);
+    return launch_resident<2>(k_orth_thin, a.thin > 1, a.thin * a.batch, THIN_THREADS, THIN_SMEM,
+                              THIN_CLUSTER_SMEM, st, a);
   OrthMaps maps;
   for (int j = 0; j < 2; ++j) {
     for (int i = 0; i < 2; ++i)
@@ -1554,8 +1677,8 @@ cudaError_t orth_launch(OrthPlan& p, cudaStream_t st) {
       return cudaErrorInvalidValue;
   }
   const int blocks = std::min(p.ctas, num_sms());
-  return a.exact ? launch_resident<1>(k_orth<1>, true, blocks, THREADS, SMEM, st, maps, a)
-                 : launch_resident<0>(k_orth<0>, true, blocks, THREADS, SMEM, st, maps, a);
+  return a.exact ? launch_resident<1>(k_orth<1>, true, blocks, THREADS, SMEM, SMEM, st, maps, a)
+                 : launch_resident<0>(k_orth<0>, true, blocks, THREADS, SMEM, SMEM, st, maps, a);
 }
 
 }  // namespace

@@ -148,3 +148,18 @@ def test_same_bits_another_stream_and_a_graph():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, ref)
+
+
+# Thin matrices on one block, on clusters of 2 to 16, and on more blocks than a cluster takes.
+@pytest.mark.parametrize("R,K", [(100, 128), (126, 142), (384, 128), (17, 500), (90, 700),
+                                 (1100, 128), (33, 1408), (120, 1860), (2048, 128), (2049, 70)])
+@pytest.mark.parametrize("N,odt", [(1, "f32"), (3, "bf16")])
+def test_thin(R, K, N, odt):
+    G = torch.stack([_grad(R, K, 7 * R + K + i, "strong") for i in range(N)])
+    o = rn.Orthogonalizer(R, K, batch=N, out_dtype=odt)
+    got = o.run(G.cuda()).double().cpu()
+    again = o.run(G.cuda()).double().cpu()
+    assert o.status() == (0, 0) and torch.equal(got, again)
+    for i in range(N):
+        ref = _ref(G[i], 5)
+        assert (got[i] - ref).norm() <= TOL[odt] * ref.norm()
