@@ -73,7 +73,6 @@ struct OrthArgs {
   __half* S[2];
   __half* P[2];
   int thin;             // blocks per matrix of k_orth_thin (0: k_orth)
-  int cluster;          // they are a cluster
   float* part;          // gram partial tiles [splits][batch][tiles][128][bn];
                         // k_orth_thin: [batch][thin][128][128]
   float* sum;           // k_orth_thin: their sum [batch][128][128]
@@ -980,13 +979,12 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
     uint32_t acc_phase = 0;
     unsigned ph = 0;
     // One arrival for the block, after all of its writes of this phase (the
-    // barrier orders the other threads' writes before thread 0's release).
+    // barrier orders the other threads' writes before thread 0's release, which
+    // is fence enough: one more made a phase 0.4 us longer).
     auto arrive = [&]() {
       ptx::named_barrier(1, 32 * EPI_WARPS);
-      if (et == 0) {
-        __threadfence();
+      if (et == 0)
         asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.counter) : "memory");
-      }
       ++ph;
     };
     auto wait = [&]() {
@@ -1096,8 +1094,8 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
 // same layout.  So a product is three MMA chains and a pass of the 128 x 128
 // accumulator through registers, about 0.7 us, against 4.4 us through global
 // memory and a grid barrier; only the blocks' shares of S meet, once per step:
-// over the shared memory of a cluster for up to 16 blocks (128 x 2048: 95 us,
-// 126 x 142: 75), else through global memory (132 and 107).  All products exact.
+// over the shared memory of a cluster for up to 16 blocks (128 x 2048: 91 us,
+// 126 x 142: 72), else through global memory (132 and 107).  All products exact.
 constexpr int THIN_THREADS = 256;
 constexpr int IMG = 128 * 128 * 2;           // bytes of a 128 x 128 plane: two 64-column blocks
 constexpr int THIN_SMEM = 1024 + 4 * IMG + 256;
@@ -1297,6 +1295,10 @@ __device__ __forceinline__ void thin_share(const OrthArgs& a, int c, int pieces,
   cluster_meet();
 }
 
+// How a matrix's blocks meet: there is one, or they are a cluster, or through
+// global memory.
+enum { ALONE, CLUSTER, GLOBAL };
+template <int MEET>
 __global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ float4 tmp[8][32];
@@ -1306,7 +1308,8 @@ __global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a)
   unsigned char* X = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   unsigned char* S = X + 2 * IMG;  // S, then P
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / a.thin, c = blockIdx.x - b * a.thin;
+  const int b = MEET == ALONE ? blockIdx.x : blockIdx.x / a.thin;
+  const int c = MEET == ALONE ? 0 : blockIdx.x - b * a.thin;
   const int j0 = c * 128, nc = min(128, a.n - j0);
   // a warp's lanes are 32 rows; it takes every other 32 columns
   const int row = (warp & 3) * 32 + lane, cbase = (warp >> 2) * 32;
@@ -1323,7 +1326,7 @@ __global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a)
   else thin_load<__nv_bfloat16>(a, b, j0, X);
   ptx::tc_fence_before();
   __syncthreads();
-  if (a.cluster) cluster_meet();  // (the others run: their shared memory may be written)
+  if (MEET == CLUSTER) cluster_meet();  // (the others run: their shared memory may be written)
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const uint32_t xs = ptx::smem_u32(X), ss = ptx::smem_u32(S);
@@ -1362,7 +1365,6 @@ __global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a)
     __syncthreads();
     arrivals += a.thin;
     if (tid == 0) {
-      __threadfence();
       asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.counter + b) : "memory");
       if (!abort_s && !grid_wait(a, arrivals, &abort_s, b)) give_up(a, &abort_s);
     }
@@ -1375,7 +1377,7 @@ __global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a)
     // S
     product(xs, xs, 0, mk * 16, nk);
     const float fs = 1.f / (1 << (2 * XE - SE));
-    if (a.cluster) {
+    if constexpr (MEET == CLUSTER) {
 #pragma unroll 1
       for (int c0 = cbase; c0 < mk * 16; c0 += 64) {
         float v[32];
@@ -1388,7 +1390,7 @@ __global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a)
               make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
       }
       thin_share(a, c, (mk * 16 + 63) / 64 * 16, fs, S, ss);
-    } else if (a.thin > 1) {  // (stored by columns: lanes are rows)
+    } else if constexpr (MEET == GLOBAL) {  // (stored by columns: lanes are rows)
 #pragma unroll 1
       for (int c0 = cbase; c0 < a.m; c0 += 64) {
         float v[32];
@@ -1402,9 +1404,9 @@ __global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a)
       meet();
     }
 #pragma unroll 1
-    for (int c0 = cbase; c0 < mk * 16 && !a.cluster; c0 += 64) {
+    for (int c0 = cbase; c0 < mk * 16 && MEET != CLUSTER; c0 += 64) {
       float v[32];
-      if (a.thin > 1) {
+      if constexpr (MEET == GLOBAL) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = c0 + j < a.m ? __ldcg(sum + (c0 + j) * 128 + row) : 0.f;
       } else {
@@ -1549,7 +1551,7 @@ bool orth_plan(const rnnt_orth_dims* d, OrthPlan* p) {
   a.ut_m = (int)cdiv(um, BM);
   auto tiles = [&](int bn) { return (long long)a.batch * a.ut_m * cdiv(un, bn); };
   // the tiles of the last round go out as two halves each where the SMs take them
-  // at once (16384 x 1024, 512 tiles of 256: 420 us, in four whole rounds 440)
+  // at once (16384 x 1024, 512 tiles of 256: 420 us, in whole rounds 440)
   auto halved = [&](int bn) {
     const long long rest = tiles(bn) % kSms;
     return tiles(bn) > kSms && bn >= 128 && 2 * rest <= kSms &&
@@ -1596,12 +1598,12 @@ bool orth_plan(const rnnt_orth_dims* d, OrthPlan* p) {
 // Blocks that wait for one another are all resident at once: a cooperative launch.
 template <int WHICH, typename... KA, typename... A>
 cudaError_t launch_resident(void (*k)(KA...), bool together, int grid, int threads, size_t smem,
-                            size_t smem_max, cudaStream_t st, const A&... args) {
+                            cudaStream_t st, const A&... args) {
   static std::atomic<bool> opted_in[kDeviceSlots];  // per kernel (WHICH) and device
   std::atomic<bool>& opted = opted_in[device_slot()];
   if (!opted.load()) {
     const cudaError_t e =
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_max);
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     opted.store(true);
   }
@@ -1619,7 +1621,7 @@ cudaError_t launch_resident(void (*k)(KA...), bool together, int grid, int threa
 }
 
 // The blocks of a thin matrix as a cluster, where the card can hold one (*done).
-cudaError_t launch_thin_cluster(OrthArgs& a, cudaStream_t st, bool* done) {
+cudaError_t launch_thin_cluster(const OrthArgs& a, cudaStream_t st, bool* done) {
   static std::atomic<int> fits[kDeviceSlots][MAX_THIN_CLUSTER + 1];  // 0: not asked, 1: no, 2: yes
   *done = false;
   if (a.thin < 2 || a.thin > MAX_THIN_CLUSTER) return cudaSuccess;
@@ -1636,13 +1638,14 @@ cudaError_t launch_thin_cluster(OrthArgs& a, cudaStream_t st, bool* done) {
   cfg.numAttrs = 1;
   std::atomic<int>& f = fits[device_slot()][a.thin];
   if (!f.load()) {
-    cudaError_t e = cudaFuncSetAttribute(k_orth_thin, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    auto k = k_orth_thin<CLUSTER>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          THIN_CLUSTER_SMEM);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k_orth_thin, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, k_orth_thin, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, k_orth_thin<CLUSTER>, &cfg) != cudaSuccess) {
       cudaGetLastError();  // (no cluster of this size: not an error of the call)
       n = 0;
     }
@@ -1650,8 +1653,7 @@ cudaError_t launch_thin_cluster(OrthArgs& a, cudaStream_t st, bool* done) {
   }
   if (f.load() != 2) return cudaSuccess;
   *done = true;
-  a.cluster = 1;
-  return cudaLaunchKernelEx(&cfg, k_orth_thin, (const OrthArgs)a);
+  return cudaLaunchKernelEx(&cfg, k_orth_thin<CLUSTER>, a);
 }
 
 cudaError_t orth_launch(OrthPlan& p, cudaStream_t st) {
@@ -1665,8 +1667,11 @@ cudaError_t orth_launch(OrthPlan& p, cudaStream_t st) {
   bool done = false;
   if ((e = launch_thin_cluster(a, st, &done)) != cudaSuccess || done) return e;
   if (a.thin)
-    return launch_resident<2>(k_orth_thin, a.thin > 1, a.thin * a.batch, THIN_THREADS, THIN_SMEM,
-                              THIN_CLUSTER_SMEM, st, a);
+    return a.thin > 1
+               ? launch_resident<3>(k_orth_thin<GLOBAL>, true, a.thin * a.batch, THIN_THREADS,
+                                    THIN_SMEM, st, a)
+               : launch_resident<2>(k_orth_thin<ALONE>, false, a.batch, THIN_THREADS, THIN_SMEM,
+                                    st, a);
   OrthMaps maps;
   for (int j = 0; j < 2; ++j) {
     for (int i = 0; i < 2; ++i)
@@ -1677,8 +1682,8 @@ cudaError_t orth_launch(OrthPlan& p, cudaStream_t st) {
       return cudaErrorInvalidValue;
   }
   const int blocks = std::min(p.ctas, num_sms());
-  return a.exact ? launch_resident<1>(k_orth<1>, true, blocks, THREADS, SMEM, SMEM, st, maps, a)
-                 : launch_resident<0>(k_orth<0>, true, blocks, THREADS, SMEM, SMEM, st, maps, a);
+  return a.exact ? launch_resident<1>(k_orth<1>, true, blocks, THREADS, SMEM, st, maps, a)
+                 : launch_resident<0>(k_orth<0>, true, blocks, THREADS, SMEM, st, maps, a);
 }
 
 }  // namespace
