@@ -1570,7 +1570,10 @@ bool orth_plan(const rnnt_orth_dims* d, OrthPlan* p) {
       {gram_units, gu * (BM / a.bn[POLY]), (long long)a.batch * a.ut_m * a.ut_n});
   if (tiles(64) > 2147483647LL || gram_units * 64 > 2147483647LL) return false;
   p->ctas = (int)std::min<long long>(kSms, units);
-  a.nb = (int)std::min<long long>(std::max<long long>(1, (long long)a.rows * a.cols / 8192), 1216);
+  // (two blocks an SM at most: every warp that scales X adds up these sums; 1216
+  // of them, 412 us for 16384 x 1024, were slower than 304, 405)
+  a.nb = (int)std::min<long long>(std::max<long long>(1, (long long)a.rows * a.cols / 8192),
+                                  2 * kSms);
   // thin: a block per 128 columns; more than one per matrix wait for one another
   // and have to be resident together
   const long long thin = cdiv(a.n, 128);
