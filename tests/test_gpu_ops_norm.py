@@ -276,3 +276,10 @@ CUTS = [(3, 70, 330, 2), (2, 65, 22, 1), (4, 40, 333, 1), (1, 1100, 1022, 1), (3
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_cuts(B, T, C, G, dtype):
     test_forward_and_gradients(B, T, C, G, dtype, "silu")
+
+
+# A whole number of samples' slabs would leave an eighth of the clusters idle: blocks change
+# channels from slab to slab.
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_blocks_change_channels(dtype):
+    test_forward_and_gradients(12, 2000, 512, 32, dtype, "silu")
