@@ -202,6 +202,21 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// A block's shared memory may be written by its cluster once it runs.  A kernel that
+// writes to its peers says that it has started while its first loads are on their
+// way, and waits for the others' word before its first write (the reading kernels
+// meet a barrier ahead of their first read as it is).
+template <int WRITES>
+__device__ __forceinline__ void say_started(const Slab& sl) {
+  if (WRITES && sl.S > 1) {
+    __syncwarp();
+    cluster_arrive();
+  }
+}
+__device__ __forceinline__ void wait_started() {
+  __syncwarp();
+  cluster_wait();
+}
 // value at the same shared address of another block of the cluster
 __device__ __forceinline__ float peer_f32(const float* p, int rank) {
   uint32_t a;
@@ -940,6 +955,7 @@ k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) 
     copy_commit();
     copy_commit();
   }
+  say_started<UNI>(sl);
   int ready = cnt;  // slots of the first of the two copy groups
   int par = 0;
   float2 ga[NP], be[NP];
@@ -1006,6 +1022,7 @@ k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) 
       __syncthreads();
       float m2 = group_warps(buf[1], myg), all = n;
       if (sl.S > 1) {
+        if (slab == first) wait_started();
         if (leader && warp == 0)
           for (int k = 0; k < sl.S; ++k) {
             to_peer_f32(from + (par * sl.S + rank) * 2 * sl.kk + myg, k, mean);
@@ -1152,6 +1169,7 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
     copy_commit();
     copy_commit();
   }
+  say_started<UNI>(sl);
   int ready = cnt, par = 0;
   Back<T, VEC, ACT> bk;
   // (a slab's statistics are asked for one slab ahead)
@@ -1236,6 +1254,7 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
       __syncthreads();
       float g2 = group_warps(buf[par][0], myg), g1 = group_warps(buf[par][1], myg);
       if (sl.S > 1) {
+        if (slab == first) wait_started();
         if (leader && warp == 0)
           for (int k = 0; k < sl.S; ++k) {
             to_peer_f32(from + (par * sl.S + rank) * 2 * sl.kk + myg, k, g2);

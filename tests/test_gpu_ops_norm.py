@@ -283,3 +283,31 @@ def test_cuts(B, T, C, G, dtype):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_blocks_change_channels(dtype):
     test_forward_and_gradients(12, 2000, 512, 32, dtype, "silu")
+
+
+# A cluster's blocks write their sums into one another's shared memory: blocks whose first slab
+# has no frames, or one, get there before the others have begun.
+@pytest.mark.parametrize("B,T,C,G", [(40, 2000, 512, 32), (3, 2600, 64, 8), (64, 500, 128, 1)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_clusters_whose_first_samples_are_empty(B, T, C, G, dtype):
+    x, dy, gamma, beta, _ = _inputs(B, T, C, dtype, 11)
+    T_len = torch.zeros(B, dtype=torch.int32)
+    T_len[B // 2:] = 1
+    T_len[-1] = T
+    n = rn.FrameNorm(B, T, C, G, dtype=dtype)
+    f = lambda t: t.double().numpy()
+    ry, r, rdx, rdg, rdb, tg, tb, *_ = _ref(f(x), f(gamma), f(beta), T_len.numpy(), G, "silu",
+                                            1e-5, f(dy))
+    t32 = 64 * U32 * (1 + r)
+    tol = t32 if dtype == "f32" else 2.0 ** -8 + t32
+    first = None
+    for _ in range(3):
+        y, dx, dg, db = _run(n, x, dy, gamma, beta, T_len)
+        assert _rel(y, ry) <= tol
+        assert np.linalg.norm(dx.double().cpu().numpy() - rdx) <= 4 * tol * np.linalg.norm(rdx)
+        cnt = np.sqrt(float(T_len.sum()))
+        assert np.all(np.abs(dg.double().cpu().numpy() - rdg) <= 1e-30 + t32 * tg * cnt)
+        assert np.all(np.abs(db.double().cpu().numpy() - rdb) <= 1e-30 + t32 * tb * cnt)
+        first = first or (y, dx, dg, db)
+        assert all(torch.equal(p, q) for p, q in zip(first, (y, dx, dg, db)))
+    assert n.status() == (0, 0)
