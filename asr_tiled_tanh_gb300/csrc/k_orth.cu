@@ -1031,6 +1031,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&x_done[n_box & 1]);
+            __syncwarp();
           }
           if (!ok) break;
           ptx::tc_fence_before();
@@ -1080,6 +1081,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
       }
     }
   }
+  __syncwarp();  // (of the first warps one lane alone worked)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -1352,6 +1354,7 @@ __global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a)
   };
   auto acc32 = [&](int col0, float (&v)[32]) {
     float x[32];
+    __syncwarp();  // (a warp reads tensor memory together: its rows past m stored nothing before)
     ptx::tmem_ld32(lanes + col0, v);
     ptx::tmem_ld32(lanes + 128 + col0, x);
     ptx::tmem_ld_wait();
@@ -1449,15 +1452,16 @@ __global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a)
         img_store(X, row, c0, v);
         continue;
       }
-      if (row >= a.m) continue;
-      const long long o = b * a.out_batch;
+      if (row < a.m) {
+        const long long o = b * a.out_batch;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        if (c0 + j >= nc) continue;
-        const long long at = o + (a.tall ? (j0 + c0 + j) * a.out_ld + row
-                                         : row * a.out_ld + j0 + c0 + j);
-        if (a.out_f32) ((float*)a.O)[at] = v[j] * (1.f / (1 << XE));
-        else ((__nv_bfloat16*)a.O)[at] = __float2bfloat16_rn(v[j] * (1.f / (1 << XE)));
+        for (int j = 0; j < 32; ++j) {
+          if (c0 + j >= nc) continue;
+          const long long at = o + (a.tall ? (j0 + c0 + j) * a.out_ld + row
+                                           : row * a.out_ld + j0 + c0 + j);
+          if (a.out_f32) ((float*)a.O)[at] = v[j] * (1.f / (1 << XE));
+          else ((__nv_bfloat16*)a.O)[at] = __float2bfloat16_rn(v[j] * (1.f / (1 << XE)));
+        }
       }
     }
   }

@@ -163,3 +163,21 @@ def test_thin(R, K, N, odt):
     for i in range(N):
         ref = _ref(G[i], 5)
         assert (got[i] - ref).norm() <= TOL[odt] * ref.norm()
+
+
+# Rows that end inside a warp: some of its lanes store nothing, in blocks of more than 64 columns
+# between one read of tensor memory and the next.
+@pytest.mark.parametrize("R,K", [(1, 128), (31, 96), (33, 65), (97, 127), (128, 40), (127, 100),
+                                 (90, 17), (65, 230), (300, 97), (47, 2560)])
+@pytest.mark.parametrize("odt", ["f32", "bf16"])
+def test_thin_rows_inside_a_warp(R, K, odt):
+    G = _grad(R, K, R * K, "noise")
+    ld = K + 3
+    buf = torch.full((R * ld,), 9.0, dtype=DT[odt], device="cuda")
+    o = rn.Orthogonalizer(R, K, out_dtype=odt, out_strides=(R * ld, ld))
+    out = buf.as_strided((R, K), (ld, 1))
+    o.run(G.cuda(), out=out)
+    ref = _ref(G, 5)
+    assert (out.double().cpu() - ref).norm() <= TOL[odt] * ref.norm()
+    out.fill_(9.0)
+    assert torch.all(buf == 9.0) and o.status() == (0, 0)
