@@ -63,6 +63,12 @@ struct Raw {
 #pragma unroll
     for (int i = 0; i < WORDS; ++i) w[i] = __ldg((const W*)p + i);
   }
+  // data that an earlier kernel may still write when this one starts: not by the
+  // read-only path, which holds for what stays unchanged while a kernel runs
+  __device__ __forceinline__ void load_late(const T* p) {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = __ldcg((const W*)p + i);
+  }
   __device__ __forceinline__ void widen(float (&v)[VEC]) const {
     if constexpr (sizeof(T) == 4) {
       const uint32_t* u = (const uint32_t*)w;
@@ -688,7 +694,7 @@ __global__ void __launch_bounds__(SUM_WARPS * 32) k_embed_join(SumArgs a) {
 #pragma unroll 4
     for (int p = p0; p < p1; ++p) {  // piece 0 is chunk c's tail, the others are heads
       Raw<VEC, float> raw;
-      raw.load(a.part + (2LL * (c + p) + (p == 0)) * a.ldp + col);
+      raw.load_late(a.part + (2LL * (c + p) + (p == 0)) * a.ldp + col);
       float x[VEC];
       raw.widen(x);
       add_vec<VEC>(acc, x);

@@ -203,3 +203,17 @@ def test_another_stream_and_a_graph():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, ref) and torch.equal(dt, dref)
+
+
+@pytest.mark.parametrize("D", [64, 50, 33])
+def test_runs_over_many_chunks_are_this_calls(D):
+    # one label in every row: its sum is joined from the partial rows of all chunks, which lie
+    # at the same addresses in call after call
+    B, U1, V = 64, 101, 5
+    _, i, _ = _inputs(B, U1, V, 1, "f32", 1, "same")
+    i, e = i.cuda(), rn.LabelEmbedding(B, U1, V, D, out_dtype="f32", sos=False)
+    lab, here = _rows(i.cpu(), torch.full((B,), U1 - 1), V, False, 0)
+    ds = [torch.randn(B, U1, D, device="cuda") * 4.0 ** k for k in range(6)]
+    got = [e.bwd(d, i) for d in ds]  # back to back
+    for d, g in zip(ds, got):
+        _check_grad(g, d, lab, here, V, 1.0)
