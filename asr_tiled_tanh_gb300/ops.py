@@ -72,6 +72,13 @@ def _ptr(t, name, dtype, shape, strides):
     return t.data_ptr()
 
 
+def _strides(given, rows, width):
+    """(batch, row) strides of rows of `width` elements; None or 0: dense, as in C."""
+    batch, row = given or (0, 0)
+    row = row or width
+    return batch or rows * row, row
+
+
 class _Op:
     """Status word and workspace of one problem size."""
 
@@ -153,7 +160,7 @@ class FrameNorm(_Op):
     """y = act(gamma * xh + beta), xh the group norm of x [B,T,C] over the frames t < T_len[b].
 
     x_strides, y_strides: (batch, frame) strides in elements of x and dx, and of y and dy
-    (None: dense).  fwd keeps the statistics that bwd reads.
+    (None, or 0 for either: dense).  fwd keeps the statistics that bwd reads.
     """
 
     def __init__(self, B, T, C, G, act="silu", dtype="bf16", eps=1e-5, x_strides=None,
@@ -161,7 +168,7 @@ class FrameNorm(_Op):
         code, self._t = _dtype(dtype)
         if act not in _ACTS:
             raise ValueError(f"act {act!r}: one of {sorted(_ACTS)}")
-        xs, ys = x_strides or (T * C, C), y_strides or (T * C, C)
+        xs, ys = _strides(x_strides, T, C), _strides(y_strides, T, C)
         self.dims = RnntNormDims(B, T, C, G, _ACTS[act], code, eps, xs[1], xs[0], ys[1], ys[0])
         self._d = ctypes.byref(self.dims)
         lib = load()
@@ -212,14 +219,14 @@ class Orthogonalizer(_Op):
     """O = the Newton-Schulz iterate of G / |G|_F after `steps` steps (see include/rnnt_ops.h).
 
     G [batch,rows,cols], or [rows,cols] with batch = 1.  in_strides, out_strides: (batch, row)
-    strides in elements (None: dense).
+    strides in elements (None, or 0 for either: dense).
     """
 
     def __init__(self, rows, cols, batch=1, dtype="f32", out_dtype="bf16", steps=5, eps=1e-7,
                  in_strides=None, out_strides=None, device="cuda"):
         icode, self._it = _dtype(dtype)
         ocode, self._ot = _dtype(out_dtype)
-        i, o = in_strides or (rows * cols, cols), out_strides or (rows * cols, cols)
+        i, o = _strides(in_strides, rows, cols), _strides(out_strides, rows, cols)
         self.dims = RnntOrthDims(rows, cols, batch, icode, ocode, steps, eps, i[1], i[0], o[1],
                                  o[0])
         self._d = ctypes.byref(self.dims)

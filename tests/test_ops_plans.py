@@ -1,0 +1,88 @@
+"""What the Python plans of the operators around the loss take and refuse (CPU, nothing launched).
+
+Tensors are stand-ins with a type, a shape, strides and a device; a call that passes the checks
+ends in a recorder in place of the library's function.
+"""
+import pytest
+import torch
+
+import asr_tiled_tanh_gb300 as rn
+from asr_tiled_tanh_gb300 import build, ops
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build_library()
+    rn.load()
+
+
+class Tensor:
+    """A CUDA tensor as far as the checks look at it."""
+
+    def __init__(self, dtype, shape, strides=None, index=0):
+        self.dtype, self.shape = dtype, torch.Size(shape)
+        self._strides, self._index = strides or torch.empty(shape, device="meta").stride(), index
+        self.device, self.is_cuda = torch.device("cuda", index), True
+
+    def dim(self):
+        return len(self.shape)
+
+    def get_device(self):
+        return self._index
+
+    def stride(self):
+        return self._strides
+
+    def data_ptr(self):
+        return 1 << 20
+
+    def __getitem__(self, key):
+        assert key is None
+        return Tensor(self.dtype, (1, *self.shape), (1 << 40, *self._strides), self._index)
+
+
+def _on(plan, names, monkeypatch, index=0, current=0):
+    """The plan as one of GPU `index`, its calls recorded."""
+    calls = []
+    for name in names:
+        setattr(plan, name, lambda *a: calls.append(a) or 0)
+    plan._index = index
+    monkeypatch.setattr(ops, "_raw_stream", lambda i: 0)
+    monkeypatch.setattr(ops, "_current_device", lambda: current, raising=False)
+    return calls
+
+
+F, H, I = torch.float32, torch.bfloat16, torch.int32
+
+
+# The C side takes a stride of 0 for the dense one: a tensor that is expanded, and so holds less
+# than dense rows, must not pass as one of stride 0.
+@pytest.mark.parametrize("zero", [(0, 0), (0, 8), (None, 0)])
+def test_frames_of_stride_zero_are_refused(zero, monkeypatch):
+    B, T, C = 3, 5, 8
+    zero = tuple(40 if z is None else z for z in zero)
+    n = rn.FrameNorm(B, T, C, 2, x_strides=zero, y_strides=zero, device="cpu")
+    calls = _on(n, ("_fwd", "_bwd"), monkeypatch)
+    dense, flat = Tensor(H, (B, T, C)), Tensor(H, (B, T, C), (*zero, 1))
+    for x, y in ((flat, dense), (dense, flat)):
+        with pytest.raises(ValueError):
+            n.fwd(x, y=y)
+        with pytest.raises(ValueError):
+            n.bwd(x, y, dx=dense, dgamma=Tensor(F, (C,)), dbeta=Tensor(F, (C,)))
+    assert not calls
+    n.fwd(dense, y=dense)
+    assert len(calls) == 1
+
+
+@pytest.mark.parametrize("zero", [(0, 6), (0, 0), (24, 0)])
+def test_matrices_of_stride_zero_are_refused(zero, monkeypatch):
+    N, R, K = 3, 4, 6
+    o = rn.Orthogonalizer(R, K, batch=N, in_strides=zero, out_strides=zero, device="cpu")
+    calls = _on(o, ("_run",), monkeypatch)
+    for g, out in ((Tensor(F, (N, R, K), (*zero, 1)), Tensor(H, (N, R, K))),
+                   (Tensor(F, (N, R, K)), Tensor(H, (N, R, K), (*zero, 1)))):
+        with pytest.raises(ValueError):
+            o.run(g, out=out)
+    assert not calls
+    o.run(Tensor(F, (N, R, K)), out=Tensor(H, (N, R, K)))
+    assert len(calls) == 1
