@@ -9,7 +9,8 @@ Argument checks and marshalling only; each class owns the workspace, saved state
 word of one problem size, as ``Rnnt`` does for the loss.  A call works on the current stream
 unless one is given, writes into the tensor it is handed or into a new one, and returns it.
 Calls of one object share its buffers and must not overlap on the GPU: use one object per
-stream.
+stream.  An object belongs to one GPU: its tensors live there, and it is the current device
+when a call is made.
 """
 from __future__ import annotations
 
@@ -53,23 +54,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = torch.cuda.current_device
+
+
 def _dtype(name):
     try:
         return _DTYPES[name]
     except KeyError:
         raise ValueError(f"dtype {name!r}: one of {sorted(_DTYPES)}") from None
-
-
-def _ptr(t, name, dtype, shape, strides):
-    """Data pointer of a CUDA tensor that has exactly this type and layout."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
-        raise ValueError(f"{name}: a CUDA tensor of {dtype} {tuple(shape)} is needed, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    if t.stride() != strides:
-        # (the stride of a dimension of length 1 is never used)
-        if any(n > 1 and a != b for n, a, b in zip(shape, t.stride(), strides)):
-            raise ValueError(f"{name}: strides {strides} are needed, got {t.stride()}")
-    return t.data_ptr()
 
 
 def _strides(given, rows, width):
@@ -92,8 +84,24 @@ class _Op:
         self._args = (self.ws.data_ptr(), ws_bytes, self.status_word.data_ptr())
         self._index = self.ws.device.index
 
+    def _ptr(self, t, name, dtype, layout):
+        """Data pointer of a tensor of the plan's GPU that has exactly this type and layout."""
+        shape, strides = layout
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != self._index:
+            raise ValueError(f"{name}: a tensor of {dtype} {tuple(shape)} on {self.ws.device} is "
+                             f"needed, got {t.dtype} {tuple(t.shape)} on {t.device}")
+        if t.stride() != strides:
+            # (the stride of a dimension of length 1 is never used)
+            if any(n > 1 and a != b for n, a, b in zip(shape, t.stride(), strides)):
+                raise ValueError(f"{name}: strides {strides} are needed, got {t.stride()}")
+        return t.data_ptr()
+
     def _stream(self, stream):
         """Handle of the stream to work on: the one given, else the device's current one."""
+        # (a launch goes to the current device, wherever its pointers and stream belong)
+        if _current_device() != self._index:
+            raise ValueError(f"the plan is of {self.ws.device}, the current device is "
+                             f"cuda:{_current_device()}")
         if stream is None:
             return _raw_stream(self._index)
         return stream if isinstance(stream, int) else stream.cuda_stream
@@ -130,8 +138,8 @@ class LabelEmbedding(_Op):
         self._rows = ((B, U1, D), (U1 * lr, lr, 1))
 
     def _in(self, ids, U_len):
-        return (_ptr(ids, "ids", torch.int32, *self._ids),
-                None if U_len is None else _ptr(U_len, "U_len", torch.int32, *self._len))
+        return (self._ptr(ids, "ids", torch.int32, self._ids),
+                None if U_len is None else self._ptr(U_len, "U_len", torch.int32, self._len))
 
     def fwd(self, table, ids, U_len=None, out=None, stream=None):
         """The rows [B,U1,D] of ids [B,U1] int32; U_len [B] int32 or None (every row)."""
@@ -139,8 +147,8 @@ class LabelEmbedding(_Op):
             shape, strides = self._rows
             out = torch.empty_strided(shape, strides, dtype=self._rt, device=self.device)
         i, u = self._in(ids, U_len)
-        _check(self._fwd(self._d, i, u, _ptr(table, "table", self._tt, *self._table),
-                         _ptr(out, "out", self._rt, *self._rows), self._args[2],
+        _check(self._fwd(self._d, i, u, self._ptr(table, "table", self._tt, self._table),
+                         self._ptr(out, "out", self._rt, self._rows), self._args[2],
                          self._stream(stream)), "rnnt_embed_fwd")
         return out
 
@@ -150,8 +158,8 @@ class LabelEmbedding(_Op):
             shape, strides = self._table
             dtable = torch.empty_strided(shape, strides, dtype=torch.float32, device=self.device)
         i, u = self._in(ids, U_len)
-        _check(self._bwd(self._d, i, u, _ptr(dout, "dout", self._rt, *self._rows),
-                         _ptr(dtable, "dtable", torch.float32, *self._table), *self._args,
+        _check(self._bwd(self._d, i, u, self._ptr(dout, "dout", self._rt, self._rows),
+                         self._ptr(dtable, "dtable", torch.float32, self._table), *self._args,
                          self._stream(stream)), "rnnt_embed_bwd")
         return dtable
 
@@ -184,16 +192,16 @@ class FrameNorm(_Op):
 
     def _params(self, gamma, beta, T_len):
         f = torch.float32
-        return (None if gamma is None else _ptr(gamma, "gamma", f, *self._c),
-                None if beta is None else _ptr(beta, "beta", f, *self._c),
-                None if T_len is None else _ptr(T_len, "T_len", torch.int32, *self._len))
+        return (None if gamma is None else self._ptr(gamma, "gamma", f, self._c),
+                None if beta is None else self._ptr(beta, "beta", f, self._c),
+                None if T_len is None else self._ptr(T_len, "T_len", torch.int32, self._len))
 
     def fwd(self, x, gamma=None, beta=None, T_len=None, y=None, stream=None):
         """y [B,T,C]; gamma, beta [C] fp32 or None; T_len [B] int32 or None (every frame)."""
         if y is None:
             y = torch.empty_strided(*self._y, dtype=self._t, device=self.device)
-        _check(self._fwd(self._d, _ptr(x, "x", self._t, *self._x),
-                         *self._params(gamma, beta, T_len), _ptr(y, "y", self._t, *self._y),
+        _check(self._fwd(self._d, self._ptr(x, "x", self._t, self._x),
+                         *self._params(gamma, beta, T_len), self._ptr(y, "y", self._t, self._y),
                          self._saved, *self._args, self._stream(stream)), "rnnt_norm_fwd")
         return y
 
@@ -207,10 +215,10 @@ class FrameNorm(_Op):
             dgamma = torch.empty(self.dims.C, dtype=f, device=self.device)
         if dbeta is None:
             dbeta = torch.empty(self.dims.C, dtype=f, device=self.device)
-        pg, pb = (_ptr(dgamma, "dgamma", f, *self._c), _ptr(dbeta, "dbeta", f, *self._c))
-        _check(self._bwd(self._d, _ptr(x, "x", self._t, *self._x),
-                         _ptr(dy, "dy", self._t, *self._y), *self._params(gamma, beta, T_len),
-                         self._saved, _ptr(dx, "dx", self._t, *self._x), pg, pb, *self._args,
+        pg, pb = (self._ptr(dgamma, "dgamma", f, self._c), self._ptr(dbeta, "dbeta", f, self._c))
+        _check(self._bwd(self._d, self._ptr(x, "x", self._t, self._x),
+                         self._ptr(dy, "dy", self._t, self._y), *self._params(gamma, beta, T_len),
+                         self._saved, self._ptr(dx, "dx", self._t, self._x), pg, pb, *self._args,
                          self._stream(stream)), "rnnt_norm_bwd")
         return dx, dgamma, dbeta
 
@@ -241,7 +249,7 @@ class Orthogonalizer(_Op):
         if out is None:
             out = torch.empty_strided(*self._out, dtype=self._ot, device=self.device)
             out = out[0] if flat and self.dims.batch == 1 else out
-        _check(self._run(self._d, _ptr(G[None] if flat else G, "G", self._it, *self._in),
-                         _ptr(out[None] if out.dim() == 2 else out, "out", self._ot, *self._out),
+        _check(self._run(self._d, self._ptr(G[None] if flat else G, "G", self._it, self._in),
+                         self._ptr(out[None] if out.dim() == 2 else out, "out", self._ot, self._out),
                          *self._args, self._stream(stream)), "rnnt_orth")
         return out

@@ -86,3 +86,48 @@ def test_matrices_of_stride_zero_are_refused(zero, monkeypatch):
     assert not calls
     o.run(Tensor(F, (N, R, K)), out=Tensor(H, (N, R, K)))
     assert len(calls) == 1
+
+
+def _calls(index, monkeypatch, plan_index, current):
+    """Every call of every plan, with tensors of GPU `index`: (plan's recorder, call) pairs."""
+    e = rn.LabelEmbedding(2, 3, 7, 16, device="cpu")
+    n = rn.FrameNorm(2, 5, 16, 4, device="cpu")
+    o = rn.Orthogonalizer(4, 6, device="cpu")
+    t = lambda dt, *shape: Tensor(dt, shape, None, index)
+    ids, ul, c = t(I, 2, 3), t(I, 2), t(F, 16)
+    at = dict(index=plan_index, current=current)
+    re = _on(e, ("_fwd", "_bwd"), monkeypatch, **at)
+    rnorm = _on(n, ("_fwd", "_bwd"), monkeypatch, **at)
+    ro = _on(o, ("_run",), monkeypatch, **at)
+    x = t(H, 2, 5, 16)
+    return [(re, lambda: e.fwd(t(H, 7, 16), ids, ul, out=t(H, 2, 3, 16))),
+            (re, lambda: e.bwd(t(H, 2, 3, 16), ids, ul, dtable=t(F, 7, 16))),
+            (rnorm, lambda: n.fwd(x, c, c, ul, y=x)),
+            (rnorm, lambda: n.bwd(x, x, c, c, ul, dx=x, dgamma=c, dbeta=c)),
+            (ro, lambda: o.run(t(F, 4, 6), out=t(H, 4, 6)))]
+
+
+@pytest.mark.parametrize("plan,tensors,current", [(0, 1, 0), (1, 0, 1), (1, 1, 0), (0, 0, 1),
+                                                  (None, 0, 0)])
+def test_another_gpu_is_refused(plan, tensors, current, monkeypatch):
+    for record, call in _calls(tensors, monkeypatch, plan, current):
+        with pytest.raises(ValueError):
+            call()
+        assert not record
+
+
+@pytest.mark.parametrize("index", [0, 1])
+def test_the_plans_own_gpu_is_taken(index, monkeypatch):
+    for record, call in _calls(index, monkeypatch, index, index):
+        call()
+        assert len(record) == 1
+        record.clear()
+
+
+def test_a_given_stream_does_not_lift_the_check(monkeypatch):
+    o = rn.Orthogonalizer(4, 6, device="cpu")
+    calls = _on(o, ("_run",), monkeypatch, index=1, current=0)
+    g, out = Tensor(F, (4, 6), None, 1), Tensor(H, (4, 6), None, 1)
+    with pytest.raises(ValueError):
+        o.run(g, out=out, stream=77)
+    assert not calls
