@@ -7,7 +7,8 @@
 
 Argument checks and marshalling only; each class owns the workspace, saved state and status
 word of one problem size, as ``Rnnt`` does for the loss.  A call works on the current stream
-unless one is given, writes into the tensor it is handed or into a new one, and returns it.
+unless one is given, writes into the tensor it is handed or into a new one (of that stream's
+memory), and returns it.  An object's own buffers are made on the stream that is current then.
 Calls of one object share its buffers and must not overlap on the GPU: use one object per
 stream.  An object belongs to one GPU: its tensors live there, and it is the current device
 when a call is made.
@@ -106,6 +107,18 @@ class _Op:
             return _raw_stream(self._index)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
+    def _empty(self, layout, dtype, stream):
+        """A new tensor for a call on `stream` to write."""
+        shape, strides = layout
+        if stream is None:
+            return torch.empty_strided(shape, strides, dtype=dtype, device=self.device)
+        # (memory is ordered on the stream it was asked for: from the current one's it could
+        # be a block that the current stream still uses)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.ws.device)
+        with torch.cuda.stream(stream):
+            return torch.empty_strided(shape, strides, dtype=dtype, device=self.device)
+
     def status(self, stream=None):
         """(status code, raw word) of every call so far; synchronizes the stream."""
         w = ctypes.c_int32(0)
@@ -144,8 +157,7 @@ class LabelEmbedding(_Op):
     def fwd(self, table, ids, U_len=None, out=None, stream=None):
         """The rows [B,U1,D] of ids [B,U1] int32; U_len [B] int32 or None (every row)."""
         if out is None:
-            shape, strides = self._rows
-            out = torch.empty_strided(shape, strides, dtype=self._rt, device=self.device)
+            out = self._empty(self._rows, self._rt, stream)
         i, u = self._in(ids, U_len)
         _check(self._fwd(self._d, i, u, self._ptr(table, "table", self._tt, self._table),
                          self._ptr(out, "out", self._rt, self._rows), self._args[2],
@@ -155,8 +167,7 @@ class LabelEmbedding(_Op):
     def bwd(self, dout, ids, U_len=None, dtable=None, stream=None):
         """The table's gradient [V,D] fp32 from the rows' gradient."""
         if dtable is None:
-            shape, strides = self._table
-            dtable = torch.empty_strided(shape, strides, dtype=torch.float32, device=self.device)
+            dtable = self._empty(self._table, torch.float32, stream)
         i, u = self._in(ids, U_len)
         _check(self._bwd(self._d, i, u, self._ptr(dout, "dout", self._rt, self._rows),
                          self._ptr(dtable, "dtable", torch.float32, self._table), *self._args,
@@ -199,7 +210,7 @@ class FrameNorm(_Op):
     def fwd(self, x, gamma=None, beta=None, T_len=None, y=None, stream=None):
         """y [B,T,C]; gamma, beta [C] fp32 or None; T_len [B] int32 or None (every frame)."""
         if y is None:
-            y = torch.empty_strided(*self._y, dtype=self._t, device=self.device)
+            y = self._empty(self._y, self._t, stream)
         _check(self._fwd(self._d, self._ptr(x, "x", self._t, self._x),
                          *self._params(gamma, beta, T_len), self._ptr(y, "y", self._t, self._y),
                          self._saved, *self._args, self._stream(stream)), "rnnt_norm_fwd")
@@ -209,12 +220,12 @@ class FrameNorm(_Op):
             stream=None):
         """(dx, dgamma, dbeta) for the x and T_len of the last fwd."""
         if dx is None:
-            dx = torch.empty_strided(*self._x, dtype=self._t, device=self.device)
+            dx = self._empty(self._x, self._t, stream)
         f = torch.float32
         if dgamma is None:
-            dgamma = torch.empty(self.dims.C, dtype=f, device=self.device)
+            dgamma = self._empty(self._c, f, stream)
         if dbeta is None:
-            dbeta = torch.empty(self.dims.C, dtype=f, device=self.device)
+            dbeta = self._empty(self._c, f, stream)
         pg, pb = (self._ptr(dgamma, "dgamma", f, self._c), self._ptr(dbeta, "dbeta", f, self._c))
         _check(self._bwd(self._d, self._ptr(x, "x", self._t, self._x),
                          self._ptr(dy, "dy", self._t, self._y), *self._params(gamma, beta, T_len),
@@ -247,7 +258,7 @@ class Orthogonalizer(_Op):
     def run(self, G, out=None, stream=None):
         flat = G.dim() == 2
         if out is None:
-            out = torch.empty_strided(*self._out, dtype=self._ot, device=self.device)
+            out = self._empty(self._out, self._ot, stream)
             out = out[0] if flat and self.dims.batch == 1 else out
         _check(self._run(self._d, self._ptr(G[None] if flat else G, "G", self._it, self._in),
                          self._ptr(out[None] if out.dim() == 2 else out, "out", self._ot, self._out),
