@@ -1394,7 +1394,8 @@ k_norm_params(const float2* __restrict__ part, int rows, int C, int S, float* __
 
 bool norm_args(const rnnt_norm_dims* d, NormArgs* a) {
   if (!d || d->B < 0 || d->T < 1 || d->C < 1 || d->G < 1 || d->C % d->G) return false;
-  if (d->T > (1 << 20) || (long long)d->B * d->G > (1LL << 27)) return false;
+  // (a frame's bytes and a column past its end stay within 31 bits)
+  if (d->T > (1 << 20) || d->C > (1 << 28) || (long long)d->B * d->G > (1LL << 27)) return false;
   if (d->act < RNNT_ACT_NONE || d->act > RNNT_ACT_RELU || !op_dtype(d->dtype)) return false;
   if (!(d->eps >= 0.f)) return false;
   a->B = d->B; a->T = d->T; a->C = d->C; a->G = d->G; a->cg = d->C / d->G;

@@ -86,7 +86,7 @@ rnnt_status rnnt_embed_bwd(const rnnt_embed_dims* dims, const int32_t* ids, cons
  * act' of relu at 0 is 0.  Frames t >= T_len[b] are never read; their y and dx
  * are 0.  T_len NULL: every frame exists; T_len[b] = 0 is an empty sample; one
  * outside [0,T] sets RNNT_ERR_LENGTH_RANGE and counts as 0.
- * C divisible by G; T <= 2^20, B*G <= 2^27.
+ * C divisible by G; T <= 2^20, C <= 2^28, B*G <= 2^27.
  */
 typedef enum { RNNT_ACT_NONE = 0, RNNT_ACT_SILU = 1, RNNT_ACT_RELU = 2 } rnnt_act;
 

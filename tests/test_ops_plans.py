@@ -3,6 +3,8 @@
 Tensors are stand-ins with a type, a shape, strides and a device; a call that passes the checks
 ends in a recorder in place of the library's function.
 """
+import ctypes
+
 import pytest
 import torch
 
@@ -131,3 +133,15 @@ def test_a_given_stream_does_not_lift_the_check(monkeypatch):
     with pytest.raises(ValueError):
         o.run(g, out=out, stream=77)
     assert not calls
+
+
+# Sizes at a limit: the largest is planned, the next is refused before anything is worked out of
+# it (a frame of 2^30 floats divided by zero).
+@pytest.mark.parametrize("C,dtype", [((1 << 28) + 1, 1), (1 << 29, 1), (1 << 30, 0), (1 << 30, 1)])
+def test_frames_past_the_width_limit(C, dtype):
+    lib, d = rn.load(), lambda c: ctypes.byref(ops.RnntNormDims(B=1, T=1, C=c, G=1, act=1,
+                                                                dtype=dtype, eps=1e-5))
+    assert lib.rnnt_norm_workspace_bytes(d(1 << 28)) > 0
+    assert lib.rnnt_norm_workspace_bytes(d(C)) == lib.rnnt_norm_saved_bytes(d(C)) == 0
+    assert lib.rnnt_norm_fwd(d(C), *[4096] * 7, 1 << 50, None, None) == 1
+    assert lib.rnnt_norm_bwd(d(C), *[4096] * 10, 1 << 50, None, None) == 1
