@@ -716,7 +716,8 @@ __global__ void __launch_bounds__(SUM_WARPS * 32) k_embed_join(SumArgs a) {
 
 bool embed_args(const rnnt_embed_dims* d, EmbedArgs* a) {
   if (!d || d->B < 0 || d->U1 < 1 || d->V < 1 || d->D < 1) return false;
-  if ((long long)d->B * d->U1 > (1LL << 30)) return false;
+  // (the sums take their columns in at most 65535 blocks of 32)
+  if ((long long)d->B * d->U1 > (1LL << 30) || d->D > (1 << 20)) return false;
   if (d->sos && (d->blank < 0 || d->blank >= d->V)) return false;
   if (!op_dtype(d->table_dtype) || !op_dtype(d->row_dtype) || !isfinite(d->scale)) return false;
   if ((d->ld_table && d->ld_table < d->D) || (d->ld_rows && d->ld_rows < d->D)) return false;

@@ -51,7 +51,7 @@ rnnt_status rnnt_ops_status(const int32_t* status, rnnt_stream stream, int32_t* 
  * hL is zero and it has no gradient; a U_len outside [0,U1-1] sets
  * RNNT_ERR_LENGTH_RANGE and its sample has no rows.  Rows that do not exist
  * are never read (their ids and their dhL may hold anything).
- * B*U1 <= 2^30; scale finite.
+ * B*U1 <= 2^30, D <= 2^20; scale finite.
  */
 typedef struct {
   int B, U1, V, D;

@@ -145,3 +145,14 @@ def test_frames_past_the_width_limit(C, dtype):
     assert lib.rnnt_norm_workspace_bytes(d(C)) == lib.rnnt_norm_saved_bytes(d(C)) == 0
     assert lib.rnnt_norm_fwd(d(C), *[4096] * 7, 1 << 50, None, None) == 1
     assert lib.rnnt_norm_bwd(d(C), *[4096] * 10, 1 << 50, None, None) == 1
+
+
+# 65,535 blocks of 32 columns are the most that one launch of the sums takes.
+@pytest.mark.parametrize("D", [(1 << 20) + 1, 3_000_001, (1 << 31) - 1])
+def test_rows_past_the_width_limit(D):
+    lib, d = rn.load(), lambda n: ctypes.byref(ops.RnntEmbedDims(B=1, U1=1, V=2, D=n, table_dtype=0,
+                                                                 row_dtype=0, scale=1.0))
+    assert lib.rnnt_embed_workspace_bytes(d(1 << 20)) > 0
+    assert lib.rnnt_embed_workspace_bytes(d(D)) == 0
+    assert lib.rnnt_embed_fwd(d(D), *[4096] * 4, None, None) == 1
+    assert lib.rnnt_embed_bwd(d(D), *[4096] * 5, 1 << 50, None, None) == 1
