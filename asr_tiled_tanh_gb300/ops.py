@@ -65,6 +65,15 @@ def _dtype(name):
         raise ValueError(f"dtype {name!r}: one of {sorted(_DTYPES)}") from None
 
 
+def _dims(struct, *values):
+    """The C struct of these values; whole numbers that its fields cannot hold are refused."""
+    d = struct(*values)
+    for (name, _), v in zip(struct._fields_, values):
+        if isinstance(v, int) and getattr(d, name) != v and not isinstance(getattr(d, name), float):
+            raise ValueError(f"{name} = {v}: out of range")
+    return d
+
+
 def _strides(given, rows, width):
     """(batch, row) strides of rows of `width` elements; None or 0: dense, as in C."""
     batch, row = given or (0, 0)
@@ -138,8 +147,8 @@ class LabelEmbedding(_Op):
                  ld_table=0, ld_rows=0, device="cuda"):
         tcode, self._tt = _dtype(dtype)
         rcode, self._rt = _dtype(out_dtype)
-        self.dims = RnntEmbedDims(B, U1, V, D, blank, int(sos), tcode, rcode, scale, ld_table,
-                                  ld_rows)
+        self.dims = _dims(RnntEmbedDims, B, U1, V, D, blank, int(sos), tcode, rcode, scale,
+                          ld_table, ld_rows)
         self._d = ctypes.byref(self.dims)
         lib = load()
         super().__init__(lib.rnnt_embed_workspace_bytes(self._d), "LabelEmbedding(dims)", device)
@@ -188,7 +197,8 @@ class FrameNorm(_Op):
         if act not in _ACTS:
             raise ValueError(f"act {act!r}: one of {sorted(_ACTS)}")
         xs, ys = _strides(x_strides, T, C), _strides(y_strides, T, C)
-        self.dims = RnntNormDims(B, T, C, G, _ACTS[act], code, eps, xs[1], xs[0], ys[1], ys[0])
+        self.dims = _dims(RnntNormDims, B, T, C, G, _ACTS[act], code, eps, xs[1], xs[0], ys[1],
+                          ys[0])
         self._d = ctypes.byref(self.dims)
         lib = load()
         super().__init__(lib.rnnt_norm_workspace_bytes(self._d), "FrameNorm(dims)", device)
@@ -246,8 +256,8 @@ class Orthogonalizer(_Op):
         icode, self._it = _dtype(dtype)
         ocode, self._ot = _dtype(out_dtype)
         i, o = _strides(in_strides, rows, cols), _strides(out_strides, rows, cols)
-        self.dims = RnntOrthDims(rows, cols, batch, icode, ocode, steps, eps, i[1], i[0], o[1],
-                                 o[0])
+        self.dims = _dims(RnntOrthDims, rows, cols, batch, icode, ocode, steps, eps, i[1], i[0],
+                          o[1], o[0])
         self._d = ctypes.byref(self.dims)
         lib = load()
         super().__init__(lib.rnnt_orth_workspace_bytes(self._d), "Orthogonalizer(dims)", device)
@@ -260,7 +270,8 @@ class Orthogonalizer(_Op):
         if out is None:
             out = self._empty(self._out, self._ot, stream)
             out = out[0] if flat and self.dims.batch == 1 else out
+        o = out[None] if out.dim() == 2 else out
         _check(self._run(self._d, self._ptr(G[None] if flat else G, "G", self._it, self._in),
-                         self._ptr(out[None] if out.dim() == 2 else out, "out", self._ot, self._out),
-                         *self._args, self._stream(stream)), "rnnt_orth")
+                         self._ptr(o, "out", self._ot, self._out), *self._args,
+                         self._stream(stream)), "rnnt_orth")
         return out

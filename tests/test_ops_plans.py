@@ -156,3 +156,22 @@ def test_rows_past_the_width_limit(D):
     assert lib.rnnt_embed_workspace_bytes(d(D)) == 0
     assert lib.rnnt_embed_fwd(d(D), *[4096] * 4, None, None) == 1
     assert lib.rnnt_embed_bwd(d(D), *[4096] * 5, 1 << 50, None, None) == 1
+
+
+# A size past 32 bits would reach the C side as another one, and plan and tensors differ.
+@pytest.mark.parametrize("make", [
+    lambda: rn.LabelEmbedding((1 << 32) + 2, 3, 7, 16, device="cpu"),
+    lambda: rn.LabelEmbedding(2, 3, (1 << 32) + 7, 16, device="cpu"),
+    lambda: rn.FrameNorm(2, (1 << 32) + 5, 16, 4, device="cpu"),
+    lambda: rn.FrameNorm(2, 5, (1 << 33) + 16, 4, device="cpu"),
+    lambda: rn.FrameNorm(2, 5, 16, 4, x_strides=((1 << 64) + 80, 16), device="cpu"),
+    lambda: rn.Orthogonalizer(4, (1 << 32) + 6, device="cpu"),
+    lambda: rn.Orthogonalizer(4, 6, steps=(1 << 32) + 5, device="cpu")])
+def test_sizes_past_the_fields_are_refused(make):
+    with pytest.raises(ValueError):
+        make()
+
+
+def test_whole_numbers_for_real_fields():
+    assert rn.LabelEmbedding(2, 3, 7, 16, scale=(1 << 24) + 1, device="cpu").dims.scale == 1 << 24
+    assert rn.Orthogonalizer(4, 6, eps=0, device="cpu").dims.eps == 0
