@@ -647,13 +647,12 @@ k_norm_fwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ 
 // The backward's two uses of a frame, in d = x - mean and s = rstd gamma:
 //   u = s d + beta,  g = dy act'(u),  sums of g d and g (rstd goes onto the sums),
 //   dx = s g + (k1 + k2 d),  k1 = -rstd m1,  k2 = -rstd^2 m2.
-// The sums become fp32 gradients and take sigmoid2.  dx in bf16 takes the unit's
-// tanh, one operation where sigmoid2 has two: its relative error of 2^-11 moves
-// act' by at most 2^-12 (1 + |u| / 2), where the rounding of dx moves it by 2^-9
-// (1024 x 1000 x 512: 485 us against 509).
+// Both uses take sigmoid2 in bf16 too: the unit's tanh, one operation where that has
+// two, is 5% faster (1024 x 1000 x 512: 485 us against 509), but its error of 2^-11 of
+// tanh(u / 2) moves act' by up to 2^-12 |t| |1 - u t|, whatever act' itself is: at u = -8
+// 1.7e-3 of an act' of -2.3e-3.
 template <typename T, int VEC, int ACT>
 struct Back {
-  static constexpr bool kHalf = ACT == RNNT_ACT_SILU && sizeof(T) == 2;
   float2 m[kPairs(VEC)], rs[kPairs(VEC)], ga[kPairs(VEC)], be[kPairs(VEC)];
   __device__ __forceinline__ void stats(const float2* st, int c, const FastDiv& cg) {
 #pragma unroll
@@ -685,18 +684,7 @@ struct Back {
       for (int i = 0; i < kPairs(VEC); ++i) {
         const float2 d = __fadd2_rn(x.v[i], m[i]), u = __ffma2_rn(d, s[i], be[i]);
         const float2 k = __ffma2_rn(d, k2[i], k1[i]);
-        if constexpr (kHalf) {
-          // s and be are halved: u is h = u / 2, and with t = tanh h
-          // act'(u) = (1 + t + h (1 - t^2)) / 2
-          float2 t;
-          asm("tanh.approx.f32 %0, %1;" : "=f"(t.x) : "f"(u.x));
-          asm("tanh.approx.f32 %0, %1;" : "=f"(t.y) : "f"(u.y));
-          const float2 w = __fmul2_rn(dy.v[i], s[i]);
-          const float2 q = __ffma2_rn(make_float2(-t.x, -t.y), t, make_float2(1.f, 1.f));
-          o.v[i] = __ffma2_rn(w, __ffma2_rn(u, q, t), __fadd2_rn(w, k));
-        } else {
-          o.v[i] = __ffma2_rn(dact2<ACT, T>(dy.v[i], u), s[i], k);
-        }
+        o.v[i] = __ffma2_rn(dact2<ACT, T>(dy.v[i], u), s[i], k);
       }
       return o;
     }
@@ -720,12 +708,11 @@ struct Back {
   __device__ __forceinline__ Dx dx(const float2 (&k1)[kPairs(VEC)],
                                    const float2 (&k2)[kPairs(VEC)]) const {
     Dx q;
-    const float2 f = kHalf ? make_float2(0.5f, 0.5f) : make_float2(1.f, 1.f);
 #pragma unroll
     for (int i = 0; i < kPairs(VEC); ++i) {
       q.m[i] = m[i];
-      q.s[i] = __fmul2_rn(f, __fmul2_rn(rs[i], ga[i]));
-      q.be[i] = __fmul2_rn(f, be[i]);
+      q.s[i] = __fmul2_rn(rs[i], ga[i]);
+      q.be[i] = be[i];
       q.k1[i] = __fmul2_rn(rs[i], k1[i]);
       q.k2[i] = __fmul2_rn(__fmul2_rn(rs[i], rs[i]), k2[i]);
     }

@@ -311,3 +311,35 @@ def test_clusters_whose_first_samples_are_empty(B, T, C, G, dtype):
         first = first or (y, dx, dg, db)
         assert all(torch.equal(p, q) for p, q in zip(first, (y, dx, dg, db)))
     assert n.status() == (0, 0)
+
+
+# Where silu's derivative is small, each element of dx for itself: half a unit of its own last
+# place, twice, and 64 2^-24 (1 + r) of every term it is made of, where u's error (that, of 1 + |u|)
+# reaches act' through act''.
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,C,G", [(3, 130, 64, 4), (2, 70, 66, 2), (1, 3000, 512, 1)])
+def test_each_element_on_the_negative_tail(B, T, C, G, dtype):
+    x, dy, _, _, T_len = _inputs(B, T, C, dtype, 13, full=True, offset=0.3)
+    g = torch.Generator().manual_seed(5)
+    gamma, beta = torch.full((C,), 0.2), -3.6 - 5.8 * torch.rand(C, generator=g)
+    n = rn.FrameNorm(B, T, C, G, dtype=dtype)
+    _, dx, _, _ = _run(n, x, dy, gamma, beta, T_len)
+    f = lambda t: t.double().numpy().reshape(B, T, G, C // G)
+    v, d = f(x), f(dy)
+    ga, be = (t.double().numpy().reshape(1, 1, G, C // G) for t in (gamma, beta))
+    mean, rstd = v.mean((1, 3), keepdims=True), 1 / np.sqrt(v.var((1, 3), keepdims=True) + 1e-5)
+    xh = (v - mean) * rstd
+    u = xh * ga + be
+    assert u.min() > -12 and u.max() < -2
+    s = 1 / (1 + np.exp(-u))
+    a1, a2 = s * (1 + u * (1 - s)), s * (1 - s) * (2 + u * (1 - 2 * s))
+    gg = ga * d * a1
+    m1, m2 = gg.mean((1, 3), keepdims=True), (gg * xh).mean((1, 3), keepdims=True)
+    ref = rstd * (gg - m1 - xh * m2)
+    size = ga * np.abs(d) * (np.abs(a1) + np.abs(a2) * (1 + np.abs(u)))
+    size = size + size.mean((1, 3), keepdims=True) + np.abs(xh) * (size * np.abs(xh)).mean(
+        (1, 3), keepdims=True)
+    tol = 64 * U32 * (1 + (np.abs(mean) * rstd).max()) * rstd * size
+    if dtype == "bf16":
+        tol = tol + 2.0 ** -8 * np.abs(ref)
+    assert np.all(np.abs(f(dx.cpu()) - ref) <= tol)
