@@ -181,3 +181,36 @@ def test_thin_rows_inside_a_warp(R, K, odt):
     assert (out.double().cpu() - ref).norm() <= TOL[odt] * ref.norm()
     out.fill_(9.0)
     assert torch.all(buf == 9.0) and o.status() == (0, 0)
+
+
+# Entries over the whole of fp32's range, on every kernel: the squares of all but the middle ones
+# leave it, and so does the norm of the largest.
+@pytest.mark.parametrize("scale", [1e37, 1e25, 2e18, 1e-12, 1e-18, 3e-30])
+@pytest.mark.parametrize("R,K", [(40, 70), (90, 700), (2049, 70), (300, 260)])
+def test_entries_of_any_size(R, K, scale):
+    G = _grad(R, K, R + K)  # (noise: 5 at most)
+    G[3, 5] = 30.0  # the largest scale's largest entry: 3e38
+    if scale < 1e-20:
+        G[1:] *= 0.01
+    G = G * scale
+    for odt in ("f32", "bf16"):
+        got = rn.Orthogonalizer(R, K, out_dtype=odt, eps=0.0).run(G.cuda()).double().cpu()
+        ref = _ref(G, 5, eps=0.0)
+        assert (got - ref).norm() <= TOL[odt] * ref.norm()
+
+
+@pytest.mark.parametrize("R,K", [(40, 70), (300, 260)])
+def test_zeros_whatever_eps(R, K):
+    for eps in (0.0, 1e-45, 1e-7, 1.0):
+        out = rn.Orthogonalizer(R, K, out_dtype="f32", eps=eps).run(torch.zeros(R, K).cuda())
+        assert torch.all(out == 0)
+
+
+def test_eps_counts_beside_the_norm():
+    # |G| far below eps: X = G / eps at first, 485 times that in the end
+    G = _grad(60, 90, 4) * 1e-9
+    for eps in (1e-7, 1e-3):
+        got = rn.Orthogonalizer(60, 90, out_dtype="f32", eps=eps).run(G.cuda()).double().cpu()
+        ref = _ref(G, 5, eps=eps)
+        # (22 bits at a fixed scale: 2^-38 of 1 is the least that X holds)
+        assert (got - ref).norm() <= TOL["f32"] * ref.norm() + 485 * 2.0 ** -38 * 73.5
