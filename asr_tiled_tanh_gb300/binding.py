@@ -140,6 +140,8 @@ def load(build_if_missing: bool = False):
                  "rnnt_norm_workspace_bytes", "rnnt_orth_workspace_bytes"):
         getattr(lib, name).restype = S
         getattr(lib, name).argtypes = [P]
+    lib.rnnt_testing_orth_plan.restype = ctypes.c_int
+    lib.rnnt_testing_orth_plan.argtypes = [P, P]
     _lib = lib
     return lib
 

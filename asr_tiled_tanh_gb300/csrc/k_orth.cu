@@ -35,6 +35,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "../../include/rnnt_testing.h"
 #include "ops.h"
 #include "ptx.cuh"
 
@@ -1764,6 +1765,24 @@ rnnt_status rnnt_orth(const rnnt_orth_dims* dims, const void* G, void* O, void* 
   ProfScope ps("orth", st);
   ps.set_kernels(2);
   OPS_CHECK(orth_launch(p, st));
+  return RNNT_OK;
+}
+
+rnnt_status rnnt_testing_orth_plan(const rnnt_orth_dims* dims, rnnt_testing_orth* out) {
+  OrthPlan p;
+  if (!out || !orth_plan(dims, &p)) return RNNT_ERR_INVALID_ARG;
+  const OrthArgs& a = p.a;
+  *out = {};
+  out->thin = a.thin;
+  out->exact = a.exact;
+  out->splits = a.splits;
+  const int sym = a.batch * a.blocks, tiles = a.batch * a.ut_m * a.ut_n;
+  for (int k = 0; k < 3; ++k) out->bn[k] = a.bn[k];
+  out->units[GRAM] = sym * (BM / a.bn[GRAM]) * a.splits;
+  out->units[POLY] = sym * (BM / a.bn[POLY]);
+  out->units[UPDATE] = 2 * tiles - a.ut_whole;
+  out->halved = tiles - a.ut_whole;
+  out->blocks = a.thin ? a.thin * a.batch : p.ctas;
   return RNNT_OK;
 }
 

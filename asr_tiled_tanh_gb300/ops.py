@@ -275,3 +275,17 @@ class Orthogonalizer(_Op):
                          self._ptr(o, "out", self._ot, self._out), *self._args,
                          self._stream(stream)), "rnnt_orth")
         return out
+
+
+class RnntTestingOrth(ctypes.Structure):
+    """What rnnt_orth runs for a size (include/rnnt_testing.h)."""
+    _fields_ = [("thin", ctypes.c_int), ("exact", ctypes.c_int), ("splits", ctypes.c_int),
+                ("bn", ctypes.c_int * 3), ("units", ctypes.c_int * 3), ("halved", ctypes.c_int),
+                ("blocks", ctypes.c_int)]
+
+
+def rnnt_testing_orth_plan(dims) -> RnntTestingOrth:
+    out = RnntTestingOrth()
+    _check(load().rnnt_testing_orth_plan(ctypes.byref(dims), ctypes.byref(out)),
+           "rnnt_testing_orth_plan")
+    return out

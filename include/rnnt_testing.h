@@ -1,13 +1,15 @@
 /*
- * rnnt_testing.h -- test hook of librnnt_gb300 (not part of the method).
+ * rnnt_testing.h -- test hooks of librnnt_gb300 (not part of the method).
  *
  * Exposes the library's bf16 tcgen05 GEMM kernel on its own so that its
- * operand layouts can be checked against a host matrix product.
+ * operand layouts can be checked against a host matrix product, and what
+ * rnnt_orth decides for a size, so that tests can name the paths they take.
  */
 #ifndef RNNT_GB300_TESTING_H
 #define RNNT_GB300_TESTING_H
 
 #include "rnnt.h"
+#include "rnnt_ops.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -43,6 +45,19 @@ rnnt_status rnnt_testing_gemm_timeout(int M, int N, int K, const void* A, const 
  * Asynchronous on `stream`. */
 rnnt_status rnnt_testing_quantize_wo(int V, int H, const void* WO, void* Q, void* Wdq,
                                      float* nscale, void* stream);
+
+/* What rnnt_orth runs for `dims` (host only, nothing is launched):
+ * RNNT_ERR_INVALID_ARG for dims it refuses. */
+typedef struct {
+  int thin;        /* blocks per matrix of the on-chip kernel; 0: the others */
+  int exact;       /* three terms in every product */
+  int splits;      /* K ranges of the Gram matrix */
+  int bn[3];       /* tile width of gram, poly and update */
+  int units[3];    /* their tiles, halves of the update's counted */
+  int halved;      /* update tiles that go out as two halves */
+  int blocks;      /* blocks of the launch on a card that has SMs for them */
+} rnnt_testing_orth;
+rnnt_status rnnt_testing_orth_plan(const rnnt_orth_dims* dims, rnnt_testing_orth* out);
 
 #ifdef __cplusplus
 }
