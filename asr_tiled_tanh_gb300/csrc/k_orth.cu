@@ -27,7 +27,10 @@
 //     through (a + d) X.  The shift enters as the steps converge (it would cost
 //     small singular values digits in the first ones).  In 64-bit emulation over
 //     flat, 1/i^p and low-rank-plus-noise spectra the fast result is 0.3 to
-//     1.6e-3 off, next to 1.7e-3 for its own rounding to bf16.
+//     1.6e-3 off, next to 1.7e-3 for its own rounding to bf16.  Up to five steps,
+//     that is: small singular values grow by a a step, and their errors with them
+//     (640 x 640, 1/i^2: 2.1e-3 off after five steps, 6.7e-3 after seven, 4.8e-2
+//     after ten; exact 1.7, 1.7 and 1.9e-3).
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
@@ -1564,8 +1567,9 @@ bool orth_plan(const rnnt_orth_dims* d, OrthPlan* p) {
   const long long nt = cdiv(a.m, BM);
   a.blocks = (int)(nt * (nt + 1) / 2);
   // exact products where the result is fp32; for small matrices they cost
-  // little (a product's time is its latency)
-  a.exact = a.out_f32 || a.m <= 256;
+  // little (a product's time is its latency); and past five steps, for which the
+  // fast ones are made (see the head of this file)
+  a.exact = a.out_f32 || a.m <= 256 || a.steps > 5;
   // gram: K in as many ranges as there are SMs for its blocks, eight K blocks
   // at least (a range's partial tile costs as much as four); without ranges,
   // and for poly, 64-wide tiles while they fit the SMs once: a product's time

@@ -138,3 +138,28 @@ def test_one_term_products_over_spectra(R, K, kind):
     assert not ops.rnnt_testing_orth_plan(o.dims).exact
     ref = _ref(G, 5)
     assert (o.run(G.cuda()).double().cpu() - ref).norm() <= TOL["bf16"] * ref.norm()
+
+
+# (past five steps the products take three terms: small singular values, and their errors, go on
+# growing by 3.4445 a step)
+@pytest.mark.gpu
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 6, 8, 12, 32])
+@pytest.mark.parametrize("kind", ["noise", "strong"])
+def test_bf16_results_over_steps(steps, kind):
+    R, K = 320, 500
+    G = _grad(R, K, steps, kind)
+    o = rn.Orthogonalizer(R, K, out_dtype="bf16", steps=steps)
+    assert bool(ops.rnnt_testing_orth_plan(o.dims).exact) == (steps > 5)
+    ref = _ref(G, steps)
+    assert (o.run(G.cuda()).double().cpu() - ref).norm() <= TOL["bf16"] * ref.norm()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("steps", [6, 7, 8, 10])
+@pytest.mark.parametrize("kind", ["flat", "decay", "steep"])
+def test_bf16_results_of_more_steps_over_spectra(steps, kind):
+    R, K = 640, 640
+    G = _spectrum(R, K, kind)
+    ref = _ref(G, steps)
+    got = rn.Orthogonalizer(R, K, out_dtype="bf16", steps=steps).run(G.cuda()).double().cpu()
+    assert (got - ref).norm() <= TOL["bf16"] * ref.norm()
