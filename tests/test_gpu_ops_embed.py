@@ -217,3 +217,29 @@ def test_runs_over_many_chunks_are_this_calls(D):
     got = [e.bwd(d, i) for d in ds]  # back to back
     for d, g in zip(ds, got):
         _check_grad(g, d, lab, here, V, 1.0)
+
+
+# Four rows in flight a lane: from 64 rows per SM on and warp's rows at a time (1, 2 or 4 of them), in
+# vectors of 8, 2 and 1 elements; the last warp's rows are fewer than it takes.
+@pytest.mark.parametrize("D", [160, 96, 40, 42, 26, 10, 33, 11, 5])
+@pytest.mark.parametrize("tdt,rdt", [("f32", "f32"), ("f32", "bf16"), ("bf16", "f32"),
+                                     ("bf16", "bf16")])
+def test_many_rows(D, tdt, rdt):
+    B, U1, V, scale = 397, 101, 700, 1.7
+    vec = next(v for v in (8, 2, 1) if D % v == 0)
+    per = 1 if D // vec > 16 else 2 if D // vec > 8 else 4
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert B * U1 >= 64 * sms * per and B * U1 % (4 * per)
+    table, i, U_len = (t.cuda() for t in _inputs(B, U1, V, D, tdt, D))
+    e = rn.LabelEmbedding(B, U1, V, D, dtype=tdt, out_dtype=rdt, scale=scale, sos=True, blank=3)
+    dev = i.clone()
+    dev[:, 0] = -5  # never read
+    gone = torch.arange(U1, device="cuda")[None] > U_len[:, None]
+    dev[gone] = 1 << 30
+    buf = torch.full((B * U1 * D + 64,), 9.0, dtype=DT[rdt], device="cuda")
+    out = e.fwd(table, dev, U_len, out=buf[:-64].view(B, U1, D))
+    i[:, 0] = 3
+    s32 = torch.tensor(scale, dtype=torch.float32, device="cuda")  # exact in 64 bits, one rounding
+    ref = (table.double()[i.long()] * s32.double()).float().to(DT[rdt]) * ~gone[..., None]
+    assert torch.equal(out, ref) and torch.all(buf[-64:] == 9.0)
+    assert e.status() == (0, 0)
