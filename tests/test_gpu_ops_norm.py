@@ -343,3 +343,13 @@ def test_each_element_on_the_negative_tail(B, T, C, G, dtype):
     if dtype == "bf16":
         tol = tol + 2.0 ** -8 * np.abs(ref)
     assert np.all(np.abs(f(dx.cpu()) - ref) <= tol)
+
+
+# Groups of so few channels that a thread holds three or more, over a cluster's blocks; groups that
+# end inside a block's columns and go on in the next; as many groups as a slab takes.
+@pytest.mark.parametrize("B,T,C,G", [(2, 3000, 24, 8), (2, 3000, 16, 16), (2, 9000, 48, 16),
+                                     (2, 40, 8200, 8), (1, 5000, 3084, 12), (3, 500, 4104, 12),
+                                     (2, 64, 130, 130), (1, 3000, 254, 127)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_narrow_and_straddling_groups(B, T, C, G, dtype):
+    test_forward_and_gradients(B, T, C, G, dtype, "silu")
