@@ -142,6 +142,8 @@ def load(build_if_missing: bool = False):
         getattr(lib, name).argtypes = [P]
     lib.rnnt_testing_orth_plan.restype = ctypes.c_int
     lib.rnnt_testing_orth_plan.argtypes = [P, P]
+    lib.rnnt_testing_orth_timeout.restype = ctypes.c_int
+    lib.rnnt_testing_orth_timeout.argtypes = [P, P, P, P, S, P, ctypes.c_ulonglong, P]
     _lib = lib
     return lib
 

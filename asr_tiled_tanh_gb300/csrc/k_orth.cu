@@ -57,7 +57,7 @@ constexpr int SMEM = 1024 + RING + EPI_WARPS * STG + 256;
 // fast update: the ring ends here, and two 128 x 64 blocks of X (hi and lo) follow
 constexpr int XBUF_AT = 144 * 1024, XPLANE = 128 * 128, XBUF = 2 * XPLANE;
 static_assert(XBUF_AT + 2 * XBUF <= RING + EPI_WARPS * STG, "blocks of X lie in the ring and staging");
-constexpr uint64_t WAIT_NS = 2000000000ull;  // 2 s per wait, then give up
+constexpr uint64_t WAIT_NS = 2000000000ull;  // per wait, then give up (2 s)
 constexpr int XE = 14, SE = 14, PE = 13;     // scale exponents of X, S and P
 
 enum { GRAM, POLY, UPDATE };
@@ -98,6 +98,8 @@ struct OrthArgs {
   unsigned* counter;    // grid barriers: arrivals so far (one per matrix; k_orth has one)
   int* abort;
   int32_t* status;
+  uint64_t wait_ns;
+  int lost;             // 1: the first block never arrives at its first barrier (a test's)
 };
 
 // Eight consecutive elements of a row of G, those past nv 0.
@@ -339,7 +341,7 @@ __device__ __forceinline__ bool grid_wait(const OrthArgs& a, unsigned target,
       if (*abort_flag || *(volatile int*)a.abort) return false;
       const uint64_t t = ptx::globaltimer();
       if (!t0) t0 = t;
-      if (t - t0 > WAIT_NS) return false;
+      if (t - t0 > a.wait_ns) return false;
     }
   }
 }
@@ -830,7 +832,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
         for (int u = cta; u < w.units && !*abort_flag; u += ctas) {
           const Unit q = unit_of(a, w, u);
           for (int kb = q.kb0; kb < q.kb1; ++kb) {
-            if (!ptx::mbar_wait(&empty[stage], (par >> stage & 1) ^ 1, WAIT_NS)) {
+            if (!ptx::mbar_wait(&empty[stage], (par >> stage & 1) ^ 1, a.wait_ns)) {
               give_up(a, abort_flag);
               break;
             }
@@ -864,7 +866,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
       }
       // every load issued has landed before the block may end
       for (int s = 0; s < MAX_STAGES; ++s)
-        if (used >> s & 1 && !ptx::mbar_wait(&full[s], (par >> s & 1) ^ 1, WAIT_NS))
+        if (used >> s & 1 && !ptx::mbar_wait(&full[s], (par >> s & 1) ^ 1, a.wait_ns))
           give_up(a, abort_flag);
     }
   } else if (warp == 1) {
@@ -886,7 +888,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
         for (int u = cta; u < w.units && !*abort_flag; u += ctas) {
           const Unit q = unit_of(a, w, u);
           // (these waits allow for the other blocks' products before as well)
-          if (!ptx::mbar_wait(&acc_empty[acc], acc_phase ^ 1, 4 * WAIT_NS)) {
+          if (!ptx::mbar_wait(&acc_empty[acc], acc_phase ^ 1, 4 * a.wait_ns)) {
             give_up(a, abort_flag);
             break;
           }
@@ -895,7 +897,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
           const uint32_t plane_b = q.bn * BK * 2 / 16;
           bool ok = true;
           for (int kb = q.kb0; kb < q.kb1; ++kb) {
-            if (!ptx::mbar_wait(&full[stage], par >> stage & 1, 4 * WAIT_NS)) {
+            if (!ptx::mbar_wait(&full[stage], par >> stage & 1, 4 * a.wait_ns)) {
               give_up(a, abort_flag);
               ok = false;
               break;
@@ -938,7 +940,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
       }
       // all issued MMAs complete before TMEM is released
       ptx::mma_commit(done_bar);
-      if (!ptx::mbar_wait(done_bar, 0, WAIT_NS)) give_up(a, abort_flag);
+      if (!ptx::mbar_wait(done_bar, 0, a.wait_ns)) give_up(a, abort_flag);
     }
   } else if (warp == 2 + EPI_WARPS) {
     // ---------------------------------------------------------------- X blocks
@@ -974,7 +976,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
             if (++lc == boxes_of(a, q)) { lc = 0; lu += ctas; }
           }
           const Unit q = unit_of(a, w, su);
-          if (!ptx::mbar_wait(&x_done[n_done & 1], n_done >> 1 & 1, 4 * WAIT_NS)) {
+          if (!ptx::mbar_wait(&x_done[n_done & 1], n_done >> 1 & 1, 4 * a.wait_ns)) {
             give_up(a, abort_flag);
             ok = false;
             break;
@@ -997,7 +999,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
       }
       // every load issued has landed before the block may end
       for (int i = n_done; i < n_load; ++i)
-        if (!ptx::mbar_wait(&x_full[i & 1], i >> 1 & 1, WAIT_NS)) give_up(a, abort_flag);
+        if (!ptx::mbar_wait(&x_full[i & 1], i >> 1 & 1, a.wait_ns)) give_up(a, abort_flag);
     }
   } else {
     // ---------------------------------------------------------------- epilogue
@@ -1012,7 +1014,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
     // is fence enough: one more made a phase 0.4 us longer).
     auto arrive = [&]() {
       ptx::named_barrier(1, 32 * EPI_WARPS);
-      if (et == 0)
+      if (et == 0 && !(a.lost && cta == 0 && ph == 0))
         asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.counter) : "memory");
       ++ph;
     };
@@ -1034,7 +1036,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
         Ahead ahead;
         Block k = block_of(a, w, q, sub * 32, half * 32);
         if (!w.boxed) look_ahead(a, w, q, step & 1, k, ahead);
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&acc_full[acc], acc_phase, 4 * WAIT_NS));
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&acc_full[acc], acc_phase, 4 * a.wait_ns));
         if (!ok) {
           give_up(a, abort_flag);
           break;
@@ -1048,7 +1050,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
             float v[32];
             ptx::tmem_ld32(t0 + c * 64 + half * 32, v);
             ok = __all_sync(0xffffffffu, ptx::mbar_wait(&x_full[n_box & 1], n_box >> 1 & 1,
-                                                        4 * WAIT_NS));
+                                                        4 * a.wait_ns));
             ptx::tmem_ld_wait();
             ptx::reg_fence32(v);
             if (!ok) {
@@ -1099,7 +1101,7 @@ k_orth(const __grid_constant__ OrthMaps maps, const OrthArgs a) {
       }
       // (the X blocks are stored by another warp)
       if (!EXACT && w.boxed && cta < w.units && ok && et == 0)
-        ok = ptx::mbar_wait(x_stored, step & 1, 4 * WAIT_NS);
+        ok = ptx::mbar_wait(x_stored, step & 1, 4 * a.wait_ns);
       ok = !epi_any(!ok);
       if (!ok) break;
       arrive();
@@ -1379,7 +1381,7 @@ __global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a)
       ptx::mma_commit(bar);
     }
     __syncwarp();
-    if (!ptx::mbar_wait(bar, parity, WAIT_NS)) report(a.status, RNNT_ERR_TIMEOUT);
+    if (!ptx::mbar_wait(bar, parity, a.wait_ns)) report(a.status, RNNT_ERR_TIMEOUT);
     __syncwarp();
     parity ^= 1;
     ptx::tc_fence_after();
@@ -1400,7 +1402,8 @@ __global__ void __launch_bounds__(THIN_THREADS, 1) k_orth_thin(const OrthArgs a)
     __syncthreads();
     arrivals += a.thin;
     if (tid == 0) {
-      asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.counter + b) : "memory");
+      if (!(a.lost && blockIdx.x == 0 && arrivals == a.thin))
+        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.counter + b) : "memory");
       if (!abort_s && !grid_wait(a, arrivals, &abort_s, b)) give_up(a, &abort_s);
     }
     __syncthreads();
@@ -1551,6 +1554,7 @@ bool orth_plan(const rnnt_orth_dims* d, OrthPlan* p) {
   a.tall = a.rows > a.cols;
   a.m = a.tall ? a.cols : a.rows;
   a.n = a.tall ? a.rows : a.cols;
+  a.wait_ns = WAIT_NS;
   a.in_f32 = d->in_dtype == RNNT_F32;
   a.out_f32 = d->out_dtype == RNNT_F32;
   a.in_ld = d->in_ld ? d->in_ld : a.cols;
@@ -1726,22 +1730,8 @@ cudaError_t orth_launch(OrthPlan& p, cudaStream_t st) {
                  : launch_resident<0>(k_orth<0>, true, blocks, THREADS, SMEM, st, maps, a);
 }
 
-}  // namespace
-}  // namespace rnnt
-
-using namespace rnnt;
-
-extern "C" {
-
-size_t rnnt_orth_workspace_bytes(const rnnt_orth_dims* dims) {
-  OrthPlan p;
-  return orth_plan(dims, &p) ? p.total : 0;
-}
-
-rnnt_status rnnt_orth(const rnnt_orth_dims* dims, const void* G, void* O, void* ws,
+rnnt_status orth_call(const rnnt_orth_dims* dims, OrthPlan& p, const void* G, void* O, void* ws,
                       size_t ws_bytes, int32_t* status, rnnt_stream stream) {
-  OrthPlan p;
-  if (!orth_plan(dims, &p)) return RNNT_ERR_INVALID_ARG;
   OrthArgs& a = p.a;
   if (a.batch == 0) return RNNT_OK;
   if (!G || !O || !ws) return RNNT_ERR_INVALID_ARG;
@@ -1770,6 +1760,37 @@ rnnt_status rnnt_orth(const rnnt_orth_dims* dims, const void* G, void* O, void* 
   ps.set_kernels(2);
   OPS_CHECK(orth_launch(p, st));
   return RNNT_OK;
+}
+
+}  // namespace
+}  // namespace rnnt
+
+using namespace rnnt;
+
+extern "C" {
+
+size_t rnnt_orth_workspace_bytes(const rnnt_orth_dims* dims) {
+  OrthPlan p;
+  return orth_plan(dims, &p) ? p.total : 0;
+}
+
+rnnt_status rnnt_orth(const rnnt_orth_dims* dims, const void* G, void* O, void* ws,
+                      size_t ws_bytes, int32_t* status, rnnt_stream stream) {
+  OrthPlan p;
+  if (!orth_plan(dims, &p)) return RNNT_ERR_INVALID_ARG;
+  return orth_call(dims, p, G, O, ws, ws_bytes, status, stream);
+}
+
+rnnt_status rnnt_testing_orth_timeout(const rnnt_orth_dims* dims, const void* G, void* O, void* ws,
+                                      size_t ws_bytes, int32_t* status,
+                                      unsigned long long wait_ns, rnnt_stream stream) {
+  OrthPlan p;
+  // (the blocks of a cluster, or one alone, meet at no barrier that gives up)
+  if (!orth_plan(dims, &p) || p.a.thin == 1 || (p.a.thin && p.a.thin <= MAX_THIN_CLUSTER))
+    return RNNT_ERR_INVALID_ARG;
+  p.a.wait_ns = wait_ns;
+  p.a.lost = 1;
+  return orth_call(dims, p, G, O, ws, ws_bytes, status, stream);
 }
 
 rnnt_status rnnt_testing_orth_plan(const rnnt_orth_dims* dims, rnnt_testing_orth* out) {

@@ -59,6 +59,15 @@ typedef struct {
 } rnnt_testing_orth;
 rnnt_status rnnt_testing_orth_plan(const rnnt_orth_dims* dims, rnnt_testing_orth* out);
 
+/* Failure-detection hook: rnnt_orth with the first block's first arrival at the
+ * grid barrier left out, so that the bounded waits run out after `wait_ns`
+ * nanoseconds (four times that where a wait spans another).  The kernel sets bit
+ * RNNT_ERR_TIMEOUT in `*status`, issues no more work and returns; O is undefined.
+ * RNNT_ERR_INVALID_ARG where no two blocks meet at such a barrier. */
+rnnt_status rnnt_testing_orth_timeout(const rnnt_orth_dims* dims, const void* G, void* O, void* ws,
+                                      size_t ws_bytes, int32_t* status,
+                                      unsigned long long wait_ns, rnnt_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
