@@ -221,10 +221,10 @@ constexpr int SORT_THREADS = 1024, SORT_WARPS = SORT_THREADS / 32;
 // The list of few rows, by label ranges: block c owns labels [c r, (c+1) r) and
 // reads every row's label.  First it counts its own labels per warp segment and
 // the rows of smaller labels, which gives every label's place; then each warp
-// walks its segment in order and lists the rows.  One launch, about 4 us, where
-// the radix sort below takes three (13 us); every block reads all labels, so
-// beyond GROUP_MAX_ROWS the radix sort is the shorter (at 103,424 rows 16 us
-// against 23).
+// walks its segment in order and lists the rows.  One launch, 6.5 us for 1296
+// rows and 9 for 4096 (V 16384, little to clear), where the radix sort below takes
+// three, 15 us for 4097; every block reads all labels, so far beyond GROUP_MAX_ROWS
+// the radix sort is the shorter (at 103,424 rows 16 us against 23).
 //
 // Table rows that no label names are cleared here and in the two kernels of
 // the sums, a share each (ClearShare): the stores of a large table take longer
@@ -272,7 +272,7 @@ k_embed_group(EmbedArgs a, ClearShare cs, int32_t* __restrict__ lkey, int32_t* _
   }
   __syncthreads();
   // The blocks of the sums are not let in early: waiting on the SMs they take the
-  // room of the clearing blocks (27.3 us against 22.7 for 1296 rows, V 4096).
+  // room of the clearing blocks (27.3 us against 22.7 for 1296 rows, V 16384).
   const int seg = (int)cdiv(NP / 128, SORT_WARPS) * 128;
   const int n0 = min(NP, warp * seg), n1 = min(NP, n0 + seg);
   int32_t* mycnt = cnt + warp * range;

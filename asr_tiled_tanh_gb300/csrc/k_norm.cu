@@ -1026,6 +1026,7 @@ k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) 
           const float* fk = from + (par * sl.S + k) * 2 * sl.kk + myg;
           const float mk = fk[0], sk = fk[sl.kk];
           if (nk == 0.f) break;
+          // (an approximate quotient and root, 2 units in the last place, once a group)
           const float dk = mk - mt, f = __fdividef(nk, all + nk);
           mt = fmaf(dk, f, mt);
           sq += fmaf(dk * dk, all * f, sk);
@@ -1037,7 +1038,8 @@ k_norm_fwd_res(NormArgs a, Slab sl, const T* __restrict__ x, T* __restrict__ y) 
       const float rstd =
           all > 0.f ? rsqrtf(fmaf(m2, __frcp_rn(fmaxf(all, 1.f)), a.eps)) : 0.f;
       if (rank == 0 && warp == 0 && leader)
-        a.stats[(long long)w.b * a.G + w.c0 / a.cg_div + myg] = make_float2(all > 0.f ? mean : 0.f, rstd);
+        a.stats[(long long)w.b * a.G + w.c0 / a.cg_div + myg] =
+            make_float2(all > 0.f ? mean : 0.f, rstd);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         m[i] = make_float2(-mean, -mean);
@@ -1428,7 +1430,8 @@ NormCut norm_cut(const NormArgs& a, int e, int tiles, int align) {
   // aligned ones) and, while there are more slabs than the SMs take twice, 16 KB:
   // a slab costs its reductions, whatever its length (250 frames of 512 channels,
   // 4096 samples: 337 us forward and 546 backward, against 433 and 780 with slabs
-  // of 8 KB upward; from 32 KB upward 352 and 669).  Short of alignment, 64 channels in pairs or 32.
+  // of 8 KB upward; from 32 KB upward 352 and 669).  Short of alignment, 64 channels
+  // in pairs or 32.
   auto enough = [&](int k) {
     return (long long)a.T * k * a.cg * e >= 16384 || (long long)a.B * (a.G / k) <= 2 * 3 * 152;
   };
@@ -1466,6 +1469,8 @@ NormCut norm_cut(const NormArgs& a, int e, int tiles, int align) {
   // a block keeps three blocks on an SM, and clusters go up to 16 for that: one
   // group of 512 channels, 1000 frames, 173 us forward (8 blocks of 128 KB 223,
   // from global memory 194); two groups, backward, 238 (338 from global memory).
+  // (It is the slower in fp32 with one group of 384: 256 x 1000 frames, backward,
+  // 381 us, 353 with 8 larger blocks.)
   const int cols16 = s.W * e / 16;
   const bool slots = n.vec == 4 && cols16 <= NT;
   auto share = [&](int S) {
@@ -1658,7 +1663,8 @@ size_t rnnt_norm_saved_bytes(const rnnt_norm_dims* dims) {
 
 size_t rnnt_norm_workspace_bytes(const rnnt_norm_dims* dims) {
   NormArgs a;
-  return norm_args(dims, &a) ? align_up(8 * MAX_S * (size_t)a.B * a.C + 8) : 0;  // a row for every block of a slab
+  // a row of sums for every block of a slab
+  return norm_args(dims, &a) ? align_up(8 * MAX_S * (size_t)a.B * a.C + 8) : 0;
 }
 
 rnnt_status rnnt_norm_fwd(const rnnt_norm_dims* dims, const void* x, const float* gamma,

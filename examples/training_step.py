@@ -7,8 +7,10 @@
     dhA --FrameNorm.bwd--> d frames, d gamma, d beta     dhL --LabelEmbedding.bwd--> d table
     dW^A, dW^L, dW^O --Orthogonalizer--> weight updates (momentum, then Newton-Schulz products)
 
-The encoder that would make the frames and take their gradient is left out: the frames are a
-fixed synthetic batch whose features carry the labels, so the loss falls as the step repeats.
+Every matrix takes the orthogonalised update here, the output layer's as well (Muon as published
+leaves that one to another method).  The encoder that would make the frames and take their
+gradient is left out: the frames are a fixed synthetic batch whose features carry the labels, so
+the loss falls as the step repeats.
 Run:  python examples/training_step.py [steps]
 """
 import math

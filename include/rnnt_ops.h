@@ -9,7 +9,9 @@
  *                 channels last, ragged lengths: the rows hA, and the frames'
  *                 gradient from dhA;
  *   rnnt_orth     the orthogonalised update of a weight matrix (Newton-Schulz
- *                 products, as the Muon optimiser takes of dW^A, dW^L, dW^O).
+ *                 products, as the Muon optimiser takes of hidden matrices such
+ *                 as W^A and W^L; it leaves input and output layers, and so W^O,
+ *                 to another method).
  *
  * Conventions are those of rnnt.h: tensor pointers are device pointers, the
  * dims structs host memory; calls are asynchronous on `stream`, never
@@ -24,8 +26,12 @@
  * cleared; the kernels OR bit k into it when a problem with rnnt_status code
  * k is found, and nothing clears it.  Read it with rnnt_ops_status.
  *
- * All sums run in fp32 in an order that depends on the sizes alone: the same
- * inputs give the same bits.
+ * Outputs must not overlap inputs or one another.
+ *
+ * Sums run in fp32 (rnnt_orth's products as described there, its norm in fp64)
+ * without atomics on values: the same inputs, sizes, strides, alignment of the
+ * pointers and device give the same bits.  The last three can choose another
+ * kernel or grid, and with it another order of a sum.
  */
 #ifndef RNNT_GB300_OPS_H
 #define RNNT_GB300_OPS_H
@@ -87,6 +93,10 @@ rnnt_status rnnt_embed_bwd(const rnnt_embed_dims* dims, const int32_t* ids, cons
  * are 0.  T_len NULL: every frame exists; T_len[b] = 0 is an empty sample; one
  * outside [0,T] sets RNNT_ERR_LENGTH_RANGE and counts as 0.
  * C divisible by G; T <= 2^20, C <= 2^28, B*G <= 2^27.
+ * Statistics, sums and the activation's sigmoid (relative error about 2^-21) are
+ * fp32; only y and dx are rounded to dtype.  A group's statistics run over all
+ * frames of its sample: frames handed over one at a time are normalised each by
+ * itself.
  */
 typedef enum { RNNT_ACT_NONE = 0, RNNT_ACT_SILU = 1, RNNT_ACT_RELU = 2 } rnnt_act;
 
@@ -123,7 +133,19 @@ rnnt_status rnnt_norm_bwd(const rnnt_norm_dims* dims, const void* x, const void*
  * with (a, b, c) = (3.4445, -4.7750, 2.0315), the quintic of the Muon
  * optimiser; O = X.  The singular values move towards 1 and the singular
  * vectors stay: O is near the closest (semi-)orthogonal matrix to G.  A matrix
- * of zeros gives zeros; a NaN or an infinity gives NaN throughout its matrix.
+ * of zeros gives zeros; a NaN or an infinity gives NaN throughout its matrix, and
+ * finite entries of any size are fine.
+ * Numbers: X and S are held in 22 bits at a fixed scale, so an entry of G below
+ * about 2^-39 |G|_F counts as 0, and rows far smaller than the rest keep fewer
+ * digits of their own.  A product is three of fp16 halves (22 bits), added in
+ * fp32, when O is fp32, when rows or cols is at most 256, or when steps > 5; a
+ * bf16 O of larger matrices takes one term (11 bits) where the rounding averages
+ * out, which leaves it 1.7 to 2.9e-3 off in all over a range of spectra (relative
+ * 2-norm), of which the rounding to bf16 alone is 1.7e-3.  For bf16 storage of an
+ * exact result, ask for fp32 and round.  An error of the first step grows by up
+ * to 3.4445 a step, and after about eight steps singular values no longer settle
+ * but cycle between 0.68 and 1.13: more steps than that are bound to amplify
+ * rounding, here as in fp32.
  * rows * cols <= 2^31 - 1 per matrix, batch <= 65535.  O must not overlap G.
  * A wait inside the kernel that gives up sets RNNT_ERR_TIMEOUT; O is then
  * undefined.
