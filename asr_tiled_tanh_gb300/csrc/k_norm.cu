@@ -704,17 +704,19 @@ struct Back {
 #pragma unroll
     for (int i = 0; i < kPairs(VEC); ++i) acc[i] = __fmul2_rn(acc[i], rs[i]);
   }
-  // k1, k2: minus the means of gamma g and gamma g xh
+  // k1, k2: minus the means of gamma g and gamma g xh.  A group of one value (one)
+  // passes no gradient on, where the three terms would cancel but for their rounding.
   __device__ __forceinline__ Dx dx(const float2 (&k1)[kPairs(VEC)],
-                                   const float2 (&k2)[kPairs(VEC)]) const {
+                                   const float2 (&k2)[kPairs(VEC)], bool one) const {
     Dx q;
 #pragma unroll
     for (int i = 0; i < kPairs(VEC); ++i) {
       q.m[i] = m[i];
-      q.s[i] = __fmul2_rn(rs[i], ga[i]);
+      const float2 r = one ? make_float2(0.f, 0.f) : rs[i];
+      q.s[i] = __fmul2_rn(r, ga[i]);
       q.be[i] = be[i];
-      q.k1[i] = __fmul2_rn(rs[i], k1[i]);
-      q.k2[i] = __fmul2_rn(__fmul2_rn(rs[i], rs[i]), k2[i]);
+      q.k1[i] = __fmul2_rn(r, k1[i]);
+      q.k2[i] = __fmul2_rn(__fmul2_rn(r, r), k2[i]);
     }
     return q;
   }
@@ -803,7 +805,7 @@ k_norm_bwd_stream(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restr
       } else if (in) {
         float2 k1[kPairs(VEC)], k2[kPairs(VEC)];
         means_of<VEC>(m1_t, m2_t, c, a.cg_div, k1, k2);
-        const auto last = bk.dx(k1, k2);
+        const auto last = bk.dx(k1, k2, w.tb == 1 && a.cg == 1);
         T* po = os + w.rg * a.xf + c;
 #pragma unroll (kFlyBwd<VEC>)
         for (int k = 0; k < cnt; ++k, px += xinc, pd += dinc, po += xinc)
@@ -1310,7 +1312,7 @@ k_norm_bwd_res(NormArgs a, Slab sl, const T* __restrict__ x, const T* __restrict
 #pragma unroll
       for (int i = 0; i < NP; ++i) tot[0][i] = tot[1][i] = make_float2(0.f, 0.f);
     }
-    const auto last = bk.dx(k1, k2);
+    const auto last = bk.dx(k1, k2, w.tb == 1 && a.cg == 1);
     T* o = os + (long long)(w.t0 + w.rg) * a.xf + c;
     const T* p = x + nx.b * a.xb + nx.c0 + (long long)(nx.t0 + nx.rg) * a.xf + c;
     const T* d = dy + nx.b * a.yb + nx.c0 + (long long)(nx.t0 + nx.rg) * a.yf + c;

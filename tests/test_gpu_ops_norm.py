@@ -353,3 +353,20 @@ def test_each_element_on_the_negative_tail(B, T, C, G, dtype):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_narrow_and_straddling_groups(B, T, C, G, dtype):
     test_forward_and_gradients(B, T, C, G, dtype, "silu")
+
+
+# The gradient of a group of one value is 0, not what rounding leaves of terms that cancel.
+@pytest.mark.parametrize("B,T,C", [(8, 1, 32), (5, 1, 8), (3, 1, 33), (4, 1, 22), (500, 1, 512),
+                                   (6, 3000, 16), (6, 40, 33)])
+@pytest.mark.parametrize("dtype,act", [("f32", "silu"), ("bf16", "none"), ("bf16", "silu")])
+def test_groups_of_one_value_pass_nothing_on(B, T, C, dtype, act):
+    x, dy, gamma, beta, T_len = _inputs(B, T, C, dtype, 17)
+    T_len[1:] = 1  # (the first sample has every frame)
+    n = rn.FrameNorm(B, T, C, C, act=act, dtype=dtype)
+    y, dx, dg, _ = _run(n, x, dy, gamma, beta, T_len)
+    assert torch.all(dx[1:, 0] == 0) and (T == 1 or torch.all(dx[0].float().norm(dim=0) > 0))
+    ry, *_ = _ref(x[1:, :1].double().numpy(), gamma.double().numpy(), beta.double().numpy(),
+                  np.ones(B - 1), C, act, 1e-5)
+    tol = 64 * U32 if dtype == "f32" else 2.0 ** -8
+    assert _rel(y[1:, :1], ry) <= tol
+    assert T > 1 or torch.all(dg == 0)
