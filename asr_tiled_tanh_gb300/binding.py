@@ -34,7 +34,9 @@ EXPORTS = ("rnnt_saved_bytes", "rnnt_saved_layout", "rnnt_workspace_bytes",
            "rnnt_status_string", "rnnt_profile_start", "rnnt_profile_stop", "rnnt_profile_entry",
            "rnnt_ops_status", "rnnt_embed_workspace_bytes", "rnnt_embed_fwd", "rnnt_embed_bwd",
            "rnnt_norm_saved_bytes", "rnnt_norm_workspace_bytes", "rnnt_norm_fwd",
-           "rnnt_norm_bwd", "rnnt_orth_workspace_bytes", "rnnt_orth")
+           "rnnt_norm_bwd", "rnnt_orth_workspace_bytes", "rnnt_orth", "rnnt_ln_saved_bytes",
+           "rnnt_ln_workspace_bytes", "rnnt_ln_fwd", "rnnt_ln_bwd", "rnnt_clip_workspace_bytes",
+           "rnnt_clip", "rnnt_adamw")
 
 
 class RnntError(RuntimeError):
@@ -133,11 +135,15 @@ def load(build_if_missing: bool = False):
     for name, args in (("rnnt_embed_fwd", [P] * 7), ("rnnt_embed_bwd", [P] * 6 + [S, P, P]),
                        ("rnnt_norm_fwd", [P] * 8 + [S, P, P]),
                        ("rnnt_norm_bwd", [P] * 11 + [S, P, P]), ("rnnt_orth", [P] * 4 + [S, P, P]),
+                       ("rnnt_ln_fwd", [P] * 9), ("rnnt_ln_bwd", [P] * 10 + [S, P, P]),
+                       ("rnnt_clip", [P] * 3 + [ctypes.c_float] * 2 + [P, P, S, P]),
+                       ("rnnt_adamw", [P] * 11),
                        ("rnnt_ops_status", [P, P, ctypes.POINTER(ctypes.c_int32)])):
         getattr(lib, name).restype = ctypes.c_int
         getattr(lib, name).argtypes = args
     for name in ("rnnt_embed_workspace_bytes", "rnnt_norm_saved_bytes",
-                 "rnnt_norm_workspace_bytes", "rnnt_orth_workspace_bytes"):
+                 "rnnt_norm_workspace_bytes", "rnnt_orth_workspace_bytes", "rnnt_ln_saved_bytes",
+                 "rnnt_ln_workspace_bytes", "rnnt_clip_workspace_bytes"):
         getattr(lib, name).restype = S
         getattr(lib, name).argtypes = [P]
     lib.rnnt_testing_orth_plan.restype = ctypes.c_int

@@ -3,7 +3,10 @@
     LabelEmbedding   hL from the labels, and the table's gradient from dhL
     FrameNorm        hA from the encoder's frames (group norm + activation, channels last,
                      ragged lengths), and the frames' gradient from dhA
+    LayerNorm        layer norm of frames or label rows, each by itself, and its gradients
     Orthogonalizer   the orthogonalised update of a weight matrix (Newton-Schulz products)
+    GradClip         the norm of all gradients together, and their clipping
+    AdamW            the AdamW update of many tensors, with the clipping's scale
 
 Argument checks and marshalling only; each class owns the workspace, saved state and status
 word of one problem size, as ``Rnnt`` does for the loss.  A call works on the current stream
@@ -49,6 +52,25 @@ class RnntOrthDims(ctypes.Structure):
                 ("out_batch", ctypes.c_longlong)]
 
 
+class RnntLnDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("C", ctypes.c_int),
+                ("label_rows", ctypes.c_int), ("x_dtype", ctypes.c_int),
+                ("y_dtype", ctypes.c_int), ("eps", ctypes.c_float),
+                ("x_frame", ctypes.c_longlong), ("x_batch", ctypes.c_longlong),
+                ("y_frame", ctypes.c_longlong), ("y_batch", ctypes.c_longlong)]
+
+
+class RnntGradList(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int), ("count", ctypes.POINTER(ctypes.c_longlong)),
+                ("dtype", ctypes.POINTER(ctypes.c_int))]
+
+
+class RnntAdamwOpts(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_float),
+                ("lr", ctypes.c_float), ("decay", ctypes.c_float),
+                ("decays", ctypes.POINTER(ctypes.c_float))]
+
+
 # Handle of a device's current stream.  (torch.cuda.current_stream builds a Stream object, 3.8 us
 # of a 10 us call; this is what its own compiled code takes.)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -79,6 +101,11 @@ def _strides(given, rows, width):
     batch, row = given or (0, 0)
     row = row or width
     return batch or rows * row, row
+
+
+def _dense(shape):
+    """Strides of a dense tensor."""
+    return torch.empty(shape, device="meta").stride()
 
 
 class _Op:
@@ -244,6 +271,69 @@ class FrameNorm(_Op):
         return dx, dgamma, dbeta
 
 
+class LayerNorm(_Op):
+    """y = gamma * xh + beta, xh each row of x [B,T,C] that exists less its mean, over its deviation.
+
+    Rows t < lengths[b] exist, or with label_rows (the rows of LabelEmbedding) rows
+    u <= lengths[b]; the others' y and dx are 0.  dtype: of x and dx; out_dtype: of y and dy
+    (None: dtype).  x_strides, y_strides: (batch, frame) strides in elements of x and dx, and of
+    y and dy (None, or 0 for either: dense).  fwd keeps the statistics that bwd reads.
+    """
+
+    def __init__(self, B, T, C, dtype="bf16", out_dtype=None, eps=1e-5, label_rows=False,
+                 x_strides=None, y_strides=None, device="cuda"):
+        xcode, self._xt = _dtype(dtype)
+        ycode, self._yt = _dtype(dtype if out_dtype is None else out_dtype)
+        xs, ys = _strides(x_strides, T, C), _strides(y_strides, T, C)
+        self.dims = _dims(RnntLnDims, B, T, C, int(label_rows), xcode, ycode, eps, xs[1], xs[0],
+                          ys[1], ys[0])
+        self._d = ctypes.byref(self.dims)
+        lib = load()
+        super().__init__(lib.rnnt_ln_workspace_bytes(self._d), "LayerNorm(dims)", device)
+        self.saved = torch.empty(lib.rnnt_ln_saved_bytes(self._d), dtype=torch.uint8,
+                                 device=device)
+        self._saved = self.saved.data_ptr()
+        self._fwd, self._bwd = lib.rnnt_ln_fwd, lib.rnnt_ln_bwd
+        self._x = ((B, T, C), (xs[0], xs[1], 1))
+        self._y = ((B, T, C), (ys[0], ys[1], 1))
+        self._c = ((C,), (1,))
+        self._len = ((B,), (1,))
+
+    def _opt(self, t, name, dtype, layout):
+        return None if t is None else self._ptr(t, name, dtype, layout)
+
+    def fwd(self, x, gamma=None, beta=None, lengths=None, y=None, stream=None):
+        """y [B,T,C]; gamma, beta [C] fp32 or None; lengths [B] int32 or None (every row)."""
+        if y is None:
+            y = self._empty(self._y, self._yt, stream)
+        f = torch.float32
+        _check(self._fwd(self._d, self._ptr(x, "x", self._xt, self._x),
+                         self._opt(gamma, "gamma", f, self._c), self._opt(beta, "beta", f, self._c),
+                         self._opt(lengths, "lengths", torch.int32, self._len),
+                         self._ptr(y, "y", self._yt, self._y), self._saved, self._args[2],
+                         self._stream(stream)), "rnnt_ln_fwd")
+        return y
+
+    def bwd(self, x, dy, gamma=None, lengths=None, dx=None, dgamma=None, dbeta=None, stream=None):
+        """(dx, dgamma, dbeta) for the x and lengths of the last fwd."""
+        f = torch.float32
+        if dx is None:
+            dx = self._empty(self._x, self._xt, stream)
+        if dgamma is None:
+            dgamma = self._empty(self._c, f, stream)
+        if dbeta is None:
+            dbeta = self._empty(self._c, f, stream)
+        _check(self._bwd(self._d, self._ptr(x, "x", self._xt, self._x),
+                         self._ptr(dy, "dy", self._yt, self._y),
+                         self._opt(gamma, "gamma", f, self._c),
+                         self._opt(lengths, "lengths", torch.int32, self._len), self._saved,
+                         self._ptr(dx, "dx", self._xt, self._x),
+                         self._ptr(dgamma, "dgamma", f, self._c),
+                         self._ptr(dbeta, "dbeta", f, self._c), *self._args,
+                         self._stream(stream)), "rnnt_ln_bwd")
+        return dx, dgamma, dbeta
+
+
 class Orthogonalizer(_Op):
     """O = the Newton-Schulz iterate of G / |G|_F after `steps` steps (see include/rnnt_ops.h).
 
@@ -275,6 +365,136 @@ class Orthogonalizer(_Op):
                          self._ptr(o, "out", self._ot, self._out), *self._args,
                          self._stream(stream)), "rnnt_orth")
         return out
+
+
+class _ListOp(_Op):
+    """An operator on a list of dense tensors of fixed shapes."""
+
+    def __init__(self, shapes, dtype, ws_bytes, what, device):
+        self._shapes = [torch.Size(k) for k in shapes]
+        n = len(self._shapes)
+        names = [dtype] * n if isinstance(dtype, str) else list(dtype)
+        if len(names) != n:
+            raise ValueError(f"{len(names)} dtypes for {n} tensors")
+        codes = [_dtype(k) for k in names]
+        self._types = [t for _, t in codes]
+        self._count = (ctypes.c_longlong * n)(*[k.numel() for k in self._shapes])
+        self._codes = (ctypes.c_int * n)(*[c for c, _ in codes])
+        self.list = RnntGradList(n, self._count, self._codes)
+        self._l = ctypes.byref(self.list)
+        self._array = ctypes.c_void_p * n
+        super().__init__(ws_bytes(self._l), what, device)
+
+    def _ptrs(self, ts, name, types):
+        """Their data pointers, as the C side takes them."""
+        if [t.shape for t in ts] != self._shapes:
+            raise ValueError(f"{name}: {len(self._shapes)} tensors of the plan's shapes are needed")
+        index = self._index
+        for i, t in enumerate(ts):
+            if t.dtype is not types[i] or t.get_device() != index or not t.is_contiguous():
+                raise ValueError(f"{name}[{i}]: a dense tensor of {types[i]} on {self.ws.device} "
+                                 f"is needed, got {t.dtype} of strides {t.stride()} on {t.device}")
+        return self._array(*[t.data_ptr() for t in ts])
+
+    def _vector(self, n, stream):
+        return self._empty(((n,), (1,)), torch.float32, stream)
+
+
+class GradClip(_ListOp):
+    """norm = the 2-norm of all gradients together; scale = min(1, max_norm / (norm + eps)).
+
+    shapes: of the tensors, in the order of every call's list.  dtype: the gradients' ("f32" or
+    "bf16"), one for all or a list.  Results are fp32 [2] tensors (norm, scale).
+    """
+
+    def __init__(self, shapes, max_norm=1.0, dtype="f32", eps=1e-6, device="cuda"):
+        lib = load()
+        super().__init__(shapes, dtype, lib.rnnt_clip_workspace_bytes, "GradClip(shapes)", device)
+        self.max_norm, self.eps = float(max_norm), float(eps)
+        if not self.max_norm >= 0 or not 0 <= self.eps < float("inf") or not (
+                self.max_norm or self.eps):
+            raise ValueError(f"max_norm {max_norm}, eps {eps}: not negative, not both 0")
+        self._clip = lib.rnnt_clip
+
+    def _call(self, grads, into, out, stream):
+        if out is None:
+            out = self._vector(2, stream)
+        g = self._ptrs(grads, "grads", self._types)
+        w = g if into is grads else None if into is None else self._ptrs(into, "into", self._types)
+        _check(self._clip(self._l, g, w, self.max_norm, self.eps,
+                          self._ptr(out, "out", torch.float32, ((2,), (1,))), self._args[0],
+                          self.ws_bytes, self._stream(stream)), "rnnt_clip")
+        return out
+
+    def norm(self, grads, out=None, stream=None):
+        """(norm, scale) alone, as AdamW.step takes it; the gradients stay as they are."""
+        return self._call(grads, None, out, stream)
+
+    def clip(self, grads, into=None, out=None, stream=None):
+        """The same, and the gradients times the scale, in place or into other tensors."""
+        return self._call(grads, grads if into is None else into, out, stream)
+
+
+class AdamW(_ListOp):
+    """The AdamW update of a list of fp32 tensors (see include/rnnt_ops.h).
+
+    shapes: of the tensors, in the order of every call's lists.  grad_dtype: "f32" or "bf16", one
+    for all or a list.  weight_decay: one number for all or a list.  m, v: lists of fp32 tensors
+    to keep the moments in (None: new ones, zeros); steps: updates they have taken.
+    """
+
+    def __init__(self, shapes, grad_dtype="f32", betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
+                 m=None, v=None, steps=0, device="cuda"):
+        lib = load()
+        super().__init__(shapes, grad_dtype, lib.rnnt_clip_workspace_bytes, "AdamW(shapes)", device)
+        n = len(self._shapes)
+        if not (0 <= betas[0] < 1 and 0 <= betas[1] < 1 and 0 <= eps < float("inf")):
+            raise ValueError(f"betas {betas}, eps {eps}: out of range")
+        if not 0 <= steps < 1 << 31:
+            raise ValueError(f"steps = {steps}: out of range")
+        one = isinstance(weight_decay, (int, float))
+        if not one and len(weight_decay) != n:
+            raise ValueError(f"{len(weight_decay)} weight decays for {n} tensors")
+        self._decays = None if one else (ctypes.c_float * n)(*weight_decay)
+        self.opts = RnntAdamwOpts(betas[0], betas[1], eps, 0.0, weight_decay if one else 0.0,
+                                  self._decays)
+        self._o = ctypes.byref(self.opts)
+        self._f32, self._bf16 = [torch.float32] * n, [torch.bfloat16] * n
+        new = lambda: [torch.zeros(k, device=device) for k in self._shapes]  # noqa: E731
+        self.m, self.v = (tuple(new() if k is None else k) for k in (m, v))
+        self._mv = None
+        self.steps = torch.tensor([int(steps), 0], dtype=torch.int32, device=device)
+        self._steps = self.steps.data_ptr()
+        self._run = lib.rnnt_adamw
+
+    def step(self, params, grads, lr, clip=None, low=None, stream=None):
+        """One update of params in place.
+
+        lr: a number, or a device fp32 tensor of one element (a captured call reads it again at
+        every replay); clip: GradClip's (norm, scale); low: tensors for the bf16 copies of params,
+        an entry or all of them None.
+        """
+        if self._mv is None:
+            self._mv = self._ptrs(self.m, "m", self._f32), self._ptrs(self.v, "v", self._f32)
+        if isinstance(lr, torch.Tensor):
+            lr = self._ptr(lr.reshape(1), "lr", torch.float32, ((1,), (1,)))
+        else:
+            self.opts.lr, lr = lr, None
+        if low is not None:
+            low = self._low(low)
+        c = None if clip is None else self._ptr(clip, "clip", torch.float32, ((2,), (1,)))
+        _check(self._run(self._l, self._o, self._ptrs(params, "params", self._f32),
+                         self._ptrs(grads, "grads", self._types), *self._mv, low, lr, c,
+                         self._steps, self._stream(stream)), "rnnt_adamw")
+
+    def _low(self, low):
+        if all(t is not None for t in low):
+            return self._ptrs(low, "low", self._bf16)
+        if len(low) != len(self._shapes):
+            raise ValueError(f"low: {len(low)} entries for {len(self._shapes)} tensors")
+        return self._array(*[None if t is None else self._ptr(
+            t, f"low[{i}]", torch.bfloat16, (k, _dense(k))) for i, (t, k) in
+            enumerate(zip(low, self._shapes))])
 
 
 class RnntTestingOrth(ctypes.Structure):

@@ -8,10 +8,14 @@
  *   rnnt_norm_*   group norm with an activation over the encoder's frames,
  *                 channels last, ragged lengths: the rows hA, and the frames'
  *                 gradient from dhA;
+ *   rnnt_ln_*     layer norm of rows (frames or label rows), and its gradients;
  *   rnnt_orth     the orthogonalised update of a weight matrix (Newton-Schulz
  *                 products, as the Muon optimiser takes of hidden matrices such
  *                 as W^A and W^L; it leaves input and output layers, and so W^O,
- *                 to another method).
+ *                 to another method);
+ *   rnnt_clip     the norm of all gradients together, and their clipping;
+ *   rnnt_adamw    the AdamW update of many tensors (W^O, the label table, biases
+ *                 and norms, or everything), with the clipping's scale.
  *
  * Conventions are those of rnnt.h: tensor pointers are device pointers, the
  * dims structs host memory; calls are asynchronous on `stream`, never
@@ -22,11 +26,12 @@
  * nothing between calls.  Tensors need only their element's alignment (16
  * bytes and sizes that keep rows 16-byte aligned run faster).
  *
- * `status` (every call; may be NULL): one device int32 that the caller
+ * `status` (every call but rnnt_clip and rnnt_adamw; may be NULL): one device int32 that the caller
  * cleared; the kernels OR bit k into it when a problem with rnnt_status code
  * k is found, and nothing clears it.  Read it with rnnt_ops_status.
  *
- * Outputs must not overlap inputs or one another.
+ * Outputs must not overlap inputs or one another (but as rnnt_clip and rnnt_adamw
+ * say).
  *
  * Sums run in fp32 (rnnt_orth's products as described there, its norm in fp64)
  * without atomics on values: the same inputs, sizes, strides, alignment of the
@@ -126,6 +131,50 @@ rnnt_status rnnt_norm_bwd(const rnnt_norm_dims* dims, const void* x, const void*
                           const void* saved, void* dx, float* dgamma, float* dbeta, void* ws,
                           size_t ws_bytes, int32_t* status, rnnt_stream stream);
 
+/* ---- layer norm of rows ------------------------------------------------------
+ * x [B,T,C]; each row (b,t) that exists is normalised by itself:
+ *   xh = (x - mean) * rstd, rstd = 1 / sqrt(var + eps) (var over C, not C-1)
+ *   y = gamma_c xh + beta_c
+ * Backward, a = gamma dy:
+ *   dgamma_c = sum_{b,t} dy xh,  dbeta_c = sum_{b,t} dy
+ *   dx = rstd (a - mean(a) - xh mean(a xh))
+ * Rows that exist: t < lengths[b] for frames (label_rows = 0, lengths in [0,T]),
+ * t <= lengths[b] for label rows as rnnt_embed_fwd makes them (label_rows = 1,
+ * lengths in [0,T-1]).  The others are never read; their y and dx are 0.  lengths
+ * NULL: every row exists; a length out of its range sets RNNT_ERR_LENGTH_RANGE and
+ * its sample has no rows.  One streamed frame or one decoding step: T = 1.
+ * Statistics and sums are fp32, the variance taken about the mean; only y and dx
+ * are rounded to their types.  B*T <= 2^30, C <= 2^20.  Strides may put samples
+ * after one another or frames after one another (time-major), without overlap.
+ */
+typedef struct {
+  int B, T, C;
+  int label_rows;
+  int x_dtype;                 /* x and dx: RNNT_F32 or RNNT_BF16 */
+  int y_dtype;                 /* y and dy: RNNT_F32 or RNNT_BF16 */
+  float eps;                   /* >= 0; a constant row with eps = 0 gives NaN */
+  long long x_frame, x_batch;  /* strides of x and dx, elements (0: C, T * x_frame) */
+  long long y_frame, y_batch;  /* strides of y and dy, elements (0: C, T * y_frame) */
+} rnnt_ln_dims;
+
+/* Bytes of `saved` (fp32 mean and rstd of every row) and of the workspace of
+ * rnnt_ln_bwd (rnnt_ln_fwd needs none); 0: invalid dims. */
+size_t rnnt_ln_saved_bytes(const rnnt_ln_dims* dims);
+size_t rnnt_ln_workspace_bytes(const rnnt_ln_dims* dims);
+
+/* gamma, beta: fp32 [C], either may be NULL (1 and 0).  saved may be NULL when no
+ * gradient will be asked for. */
+rnnt_status rnnt_ln_fwd(const rnnt_ln_dims* dims, const void* x, const float* gamma,
+                        const float* beta, const int32_t* lengths, void* y, void* saved,
+                        int32_t* status, rnnt_stream stream);
+
+/* saved: as rnnt_ln_fwd wrote it for the same x and lengths.  dgamma, dbeta: fp32
+ * [C], overwritten; either may be NULL. */
+rnnt_status rnnt_ln_bwd(const rnnt_ln_dims* dims, const void* x, const void* dy,
+                        const float* gamma, const int32_t* lengths, const void* saved, void* dx,
+                        float* dgamma, float* dbeta, void* ws, size_t ws_bytes, int32_t* status,
+                        rnnt_stream stream);
+
 /* ---- orthogonalised update -------------------------------------------------
  * For each of `batch` matrices G [rows,cols]:
  *   X = G / (|G|_F + eps), then `steps` times
@@ -163,6 +212,61 @@ size_t rnnt_orth_workspace_bytes(const rnnt_orth_dims* dims); /* 0: invalid dims
 
 rnnt_status rnnt_orth(const rnnt_orth_dims* dims, const void* G, void* O, void* ws,
                       size_t ws_bytes, int32_t* status, rnnt_stream stream);
+
+/* ---- gradient clipping ---------------------------------------------------------
+ * Over all elements of n tensors together:
+ *   norm = sqrt(sum g^2),  scale = min(1, max_norm / (norm + eps)),  into = scale g
+ * Squares are added in fp64 (fp32 in groups of 32 or fewer, fp64 where that would
+ * leave the range), in an order that follows from the list and the device, so
+ * finite entries of any size are fine.  A norm that is not finite: an infinite one
+ * gives scale 0, NaN gives NaN, and `into` is the product all the same; rnnt_adamw
+ * leaves such an update out.
+ */
+typedef struct {
+  int n;                   /* tensors, 0 to 2^16 */
+  const long long* count;  /* host [n]: elements of each, dense, 0 allowed */
+  const int* dtype;        /* host [n]: RNNT_F32 or RNNT_BF16 each; NULL: fp32 */
+} rnnt_grad_list;          /* read before a call returns */
+
+size_t rnnt_clip_workspace_bytes(const rnnt_grad_list* list); /* 0: invalid list */
+
+/* grads, into: host [n] of device pointers (a tensor of 0 elements: anything), read
+ * before the call returns.  into NULL: the norm alone; into[i] = grads[i]: in place
+ * (nothing is written there when scale is 1); otherwise `into` overlaps nothing.
+ * clip: fp32 [2] on the device, (norm, scale).  max_norm >= 0 (infinity: scale 1
+ * while the norm is finite), eps >= 0. */
+rnnt_status rnnt_clip(const rnnt_grad_list* list, const void* const* grads, void* const* into,
+                      float max_norm, float eps, float* clip, void* ws, size_t ws_bytes,
+                      rnnt_stream stream);
+
+/* ---- AdamW update ---------------------------------------------------------------
+ * For every element of n tensors, t the number of this update (from 1), s = clip's
+ * scale (1 without clip):
+ *   m <- beta1 m + (1 - beta1) s g,   v <- beta2 v + (1 - beta2) (s g)^2
+ *   p <- p - lr (decay p + (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps))
+ *   low <- p in bf16, where a copy is wanted
+ * p, m, v are fp32, updated in place; g is read only, fp32 or bf16 by the list.
+ * With clip, an update whose norm is not finite changes nothing and is not counted.
+ */
+typedef struct {
+  double beta1, beta2;  /* [0,1) */
+  float eps;            /* >= 0 (0: an element whose v is 0 gives NaN) */
+  float lr;             /* used when the call's lr is NULL */
+  float decay;          /* used when decays is NULL */
+  const float* decays;  /* host [n], read before a call returns, or NULL */
+} rnnt_adamw_opts;
+
+/* params, grads, m, v, low: host [n] of device pointers, read before the call
+ * returns (a tensor of 0 elements: anything).  low NULL, or an entry NULL: no bf16
+ * copy.  The 5 n tensors do not overlap, but for gradients among themselves (the
+ * same parameter twice is refused).  lr: one device fp32 or NULL; clip: rnnt_clip's
+ * (norm, scale) or NULL.  steps: device int32 [2]: the updates taken so far, which
+ * the call reads and adds 1 to, and a word that is 0 between calls; the caller
+ * clears both once.  So a captured call counts its replays. */
+rnnt_status rnnt_adamw(const rnnt_grad_list* list, const rnnt_adamw_opts* opts,
+                       float* const* params, const void* const* grads, float* const* m,
+                       float* const* v, void* const* low, const float* lr, const float* clip,
+                       int32_t* steps, rnnt_stream stream);
 
 #ifdef __cplusplus
 }
