@@ -1,69 +1,95 @@
-// k_ln.cu -- layer norm of rows, channels last (include/rnnt_ops.h).
-#include <algorithm>
-
-#include "ops.h"
-#include "ptx.cuh"
+// k_ln.cu -- layer norm of rows, channels last (include/rnnt_ops.h): the forward
+// pass, and the checks of both.
+#include "ln.cuh"
 
 namespace rnnt {
 namespace {
+using namespace ln;
 
-struct LnArgs {
-  int B, T, C, extra;  // extra: rows past lengths[b] that exist (1 for label rows)
-  int rows;            // B * T
-  float eps, rC;
-  FastDiv t_div;
-  long long xf, xb, yf, yb;
-  const float* gamma;
-  const float* beta;
-  const int32_t* lengths;
-  int32_t* status;
-  float2* stats;  // mean and rstd of every row
-};
-
-// Row r of the batch.
-struct Row {
-  bool live;
-  long long x, y;  // offsets of its first element
-};
-__device__ __forceinline__ Row row_of(const LnArgs& a, int r) {
-  const int b = r / a.t_div, t = r - b * a.T;
-  Row w;
-  w.x = b * a.xb + t * a.xf;
-  w.y = b * a.yb + t * a.yf;
-  w.live = true;
-  if (a.lengths) {
-    const int n = __ldg(a.lengths + b);
-    if (n < 0 || n > a.T - a.extra) {
-      report(a.status, RNNT_ERR_LENGTH_RANGE);
-      w.live = false;
-    } else {
-      w.live = t < n + a.extra;
+template <typename TX, typename TY, int VEC, int NV>
+__global__ void __launch_bounds__(MAX_THREADS)
+k_ln_fwd(LnArgs a, Team t, const TX* __restrict__ x, TY* __restrict__ y) {
+  using R = Ring<VEC, NV, TX>;
+  constexpr int NP = kPairs(VEC);
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float scr[2][MAX_THREADS / 32][1];
+  const Place p = place_of(t);
+  const bool al16 = (((uintptr_t)a.gamma | (uintptr_t)a.beta) & 15) == 0;
+  R ring;
+  ring.init(smem);
+  unsigned lives = 0;  // bit s: the row of stage s exists
+  int length = ask_length(a, p.first);
+  auto ahead = [&](int r, int stage) {
+    const bool live = exists(a, r, length, p.lane == 0);
+    length = ask_length(a, r + p.step);
+    if (live) ring.fetch(stage, x + offset(r, a, a.xf, a.xb), t, p);
+    copy_commit();
+    lives = (lives & ~(1u << stage)) | ((unsigned)live << stage);
+  };
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s) ahead(p.first + s * p.step, s);
+  int stage = 0;
+#pragma unroll 1
+  for (int r = p.first, w = p.warp0; w < a.rows; r += p.step, w += p.step) {
+    const bool live = (lives >> stage) & 1;
+    TY* yr = y + offset(r, a, a.yf, a.yb);
+    typename R::U u[NV];
+    copy_wait<STAGES - 1>();
+    ring.read(u, stage, x + (R::kAhead ? 0 : offset(r, a, a.xf, a.xb)), live, t, p);
+    ahead(r + STAGES * p.step, stage);
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
+    if (t.lanes < 32 ? !__any_sync(0xffffffffu, live) : !live) {
+      Vals<VEC> z;
+      z.fill(0.f);
+      if (r < a.rows)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int k = p.lane + j * t.lanes;
+          if (k < t.nvec) store<VEC, TY>(yr + k * VEC, z);
+        }
+      continue;
     }
-  }
-  return w;
-}
-
-// ---- a block a row ------------------------------------------------------------
-// Any width and alignment: the row is read again for each of its sums (from L2).
-constexpr int WT = 256, WWARPS = WT / 32;
-
-// Sums of two values over the block, for all threads; scr: 2 WWARPS + 2 floats.
-__device__ __forceinline__ float2 block_sum(float2 v, float2* scr) {
+    // the mean, then the squares about it
+    Vals<VEC> v[NV];
+    float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, d);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, d);
-  }
-  __syncthreads();  // (scr may still be read)
-  if ((threadIdx.x & 31) == 0) scr[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = scr[0];
+    for (int j = 0; j < NV; ++j) {
+      v[j] = widen<VEC, TX>(u[j]);
 #pragma unroll
-  for (int k = 1; k < WWARPS; ++k) {
-    v.x += scr[k].x;
-    v.y += scr[k].y;
+      for (int i = 0; i < NP; ++i) s2 = __fadd2_rn(s2, v[j].p[i]);
+    }
+    float s[1] = {s2.x + s2.y};
+    team_sum(s, t, p, scr[0]);
+    const float mean = s[0] / (float)a.C;  // (exact for rows of one value)
+    s2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        v[j].p[i] = __fadd2_rn(v[j].p[i], make_float2(-mean, -mean));
+        if (p.lane + j * t.lanes < t.nvec) s2 = __ffma2_rn(v[j].p[i], v[j].p[i], s2);
+      }
+    }
+    s[0] = VEC == 1 ? s2.x : s2.x + s2.y;
+    team_sum(s, t, p, scr[1]);
+    const float rstd = 1.f / sqrtf(s[0] * a.rC + a.eps);
+    if (a.stats && live && p.lane == 0) a.stats[r] = make_float2(mean, rstd);
+    if (r < a.rows)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int k = p.lane + j * t.lanes;
+        if (k >= t.nvec) continue;
+        const Vals<VEC> g = param<VEC>(a.gamma, k * VEC, 1.f, al16);
+        Vals<VEC> o = param<VEC>(a.beta, k * VEC, 0.f, al16);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const float2 h = __fmul2_rn(v[j].p[i], make_float2(rstd, rstd));
+          o.p[i] = live ? __ffma2_rn(g.p[i], h, o.p[i]) : make_float2(0.f, 0.f);
+        }
+        store<VEC, TY>(yr + k * VEC, o);
+      }
   }
-  return v;
+  copy_wait<0>();
 }
 
 template <typename TX, typename TY>
@@ -96,93 +122,6 @@ k_ln_fwd_wide(LnArgs a, const TX* __restrict__ x, TY* __restrict__ y) {
   }
 }
 
-template <typename TX, typename TY>
-__global__ void __launch_bounds__(WT)
-k_ln_bwd_wide(LnArgs a, const TX* __restrict__ x, const TY* __restrict__ dy,
-              TX* __restrict__ dx) {
-  __shared__ float2 scr[WWARPS];
-  for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    const Row w = row_of(a, r);
-    TX* dr = dx + w.x;
-    if (!w.live) {
-      for (int c = threadIdx.x; c < a.C; c += WT) dr[c] = from_f<TX>(0.f);
-      continue;
-    }
-    const TX* xr = x + w.x;
-    const TY* gr = dy + w.y;
-    const float2 st = a.stats[r];
-    float2 s = make_float2(0.f, 0.f);
-    for (int c = threadIdx.x; c < a.C; c += WT) {
-      const float g = to_f<TY>(gr[c]) * (a.gamma ? __ldg(a.gamma + c) : 1.f);
-      s.x += g;
-      s.y = fmaf(g, (to_f<TX>(xr[c]) - st.x) * st.y, s.y);
-    }
-    s = block_sum(s, scr);
-    const float m1 = s.x * a.rC, m2 = s.y * a.rC;
-    for (int c = threadIdx.x; c < a.C; c += WT) {
-      const float g = to_f<TY>(gr[c]) * (a.gamma ? __ldg(a.gamma + c) : 1.f);
-      const float xh = (to_f<TX>(xr[c]) - st.x) * st.y;
-      dr[c] = from_f<TX>(st.y * (g - m1 - xh * m2));
-    }
-  }
-}
-
-// part[slice][c] = (sum dy xh, sum dy) over the slice's rows: 32 channels and a
-// slice of the rows a block.
-template <typename TX, typename TY>
-__global__ void __launch_bounds__(WT)
-k_ln_cols(LnArgs a, const TX* __restrict__ x, const TY* __restrict__ dy,
-          float2* __restrict__ part, int per) {
-  __shared__ float2 scr[WWARPS][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  const long long r0 = (long long)blockIdx.y * per, r1 = min((long long)a.rows, r0 + per);
-  float2 s = make_float2(0.f, 0.f);
-  if (c < a.C)
-    for (long long r = r0 + warp; r < r1; r += WWARPS) {
-      const Row w = row_of(a, (int)r);
-      if (!w.live) continue;
-      const float2 st = a.stats[r];
-      const float g = to_f<TY>(dy[w.y + c]);
-      s.x = fmaf(g, (to_f<TX>(x[w.x + c]) - st.x) * st.y, s.x);
-      s.y += g;
-    }
-  scr[warp][lane] = s;
-  __syncthreads();
-  if (warp || c >= a.C) return;
-  for (int k = 1; k < WWARPS; ++k) {
-    s.x += scr[k][lane].x;
-    s.y += scr[k][lane].y;
-  }
-  part[(long long)blockIdx.y * a.C + c] = s;
-}
-
-// dgamma, dbeta: the column sums of part [n][C], 32 channels a block.
-__global__ void __launch_bounds__(WT)
-k_ln_params(const float2* __restrict__ part, int n, int C, float* __restrict__ dgamma,
-            float* __restrict__ dbeta) {
-  __shared__ float2 scr[WWARPS][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  float2 s = make_float2(0.f, 0.f);
-  if (c < C)
-#pragma unroll 4
-    for (int r = warp; r < n; r += WWARPS) {
-      const float2 p = __ldcg(part + (long long)r * C + c);
-      s.x += p.x;
-      s.y += p.y;
-    }
-  scr[warp][lane] = s;
-  __syncthreads();
-  if (warp || c >= C) return;
-  for (int k = 1; k < WWARPS; ++k) {
-    s.x += scr[k][lane].x;
-    s.y += scr[k][lane].y;
-  }
-  if (dgamma) dgamma[c] = s.x;
-  if (dbeta) dbeta[c] = s.y;
-}
-
 // Rows of `n` by strides: samples after one another, or frames after one another.
 // (A tensor spans at most 2^47 elements, so that offsets stay within 64 bits.)
 bool ln_strides(long long B, long long T, long long C, long long f, long long b) {
@@ -213,11 +152,6 @@ bool ln_args(const rnnt_ln_dims* d, LnArgs* a) {
   return ln_strides(d->B, d->T, d->C, a->xf, a->xb) && ln_strides(d->B, d->T, d->C, a->yf, a->yb);
 }
 
-// Slices of the rows whose sums the workspace holds.
-int ln_slices(const LnArgs& a) {
-  return (int)std::min<long long>(64, std::max(1, a.rows));
-}
-
 rnnt_status ln_check(const rnnt_ln_dims* d, LnArgs* a, const void* x, const void* y,
                      const float* gamma, const float* beta, const int32_t* lengths,
                      const void* saved, int32_t* status) {
@@ -232,23 +166,45 @@ rnnt_status ln_check(const rnnt_ln_dims* d, LnArgs* a, const void* x, const void
   return RNNT_OK;
 }
 
-template <typename TX, typename TY>
-cudaError_t ln_fwd(const LnArgs& a, const void* x, void* y, cudaStream_t st) {
-  const int grid = std::min(a.rows, 8 * num_sms());
-  k_ln_fwd_wide<TX, TY><<<grid, WT, 0, st>>>(a, (const TX*)x, (TY*)y);
+template <typename TX, typename TY, int VEC, int NV>
+cudaError_t fwd_team(const LnArgs& a, const Team& t, const void* x, void* y, cudaStream_t st) {
+  static Known known;
+  const int threads = t.lanes * t.teams;
+  const size_t smem = Ring<VEC, NV, TX>::bytes(threads);
+  int per = 0;
+  const cudaError_t e = blocks_per_sm(k_ln_fwd<TX, TY, VEC, NV>, &known, threads, smem, &per);
+  if (e != cudaSuccess) return e;
+  const int grid = (int)std::min<long long>(cdiv(a.rows, t.teams), (long long)per * num_sms());
+  k_ln_fwd<TX, TY, VEC, NV><<<grid, threads, smem, st>>>(a, t, (const TX*)x, (TY*)y);
   return cudaGetLastError();
 }
 
 template <typename TX, typename TY>
-cudaError_t ln_bwd(const LnArgs& a, const void* x, const void* dy, void* dx, float2* part,
-                   bool params, cudaStream_t st) {
+cudaError_t ln_fwd(const LnArgs& a, const void* x, void* y, cudaStream_t st) {
+  constexpr int V16 = 16 / (int)std::max(sizeof(TX), sizeof(TY));
+  const int vec = vec_of(a, sizeof(TX), x, nullptr, sizeof(TY), y);
+  int nv = 0;
+  const Team t = team_for((int)cdiv(a.C, vec), vec == V16 ? 4 : 8, vec == V16, &nv);
+  if (t.lanes) {
+    if (vec == V16) switch (nv) {
+      case 1: return fwd_team<TX, TY, V16, 1>(a, t, x, y, st);
+      case 2: return fwd_team<TX, TY, V16, 2>(a, t, x, y, st);
+      case 3: return fwd_team<TX, TY, V16, 3>(a, t, x, y, st);
+      default: return fwd_team<TX, TY, V16, 4>(a, t, x, y, st);
+    }
+    if (vec == 2) switch (nv) {
+      case 2: return fwd_team<TX, TY, 2, 2>(a, t, x, y, st);
+      case 4: return fwd_team<TX, TY, 2, 4>(a, t, x, y, st);
+      default: return fwd_team<TX, TY, 2, 8>(a, t, x, y, st);
+    }
+    switch (nv) {
+      case 2: return fwd_team<TX, TY, 1, 2>(a, t, x, y, st);
+      case 4: return fwd_team<TX, TY, 1, 4>(a, t, x, y, st);
+      default: return fwd_team<TX, TY, 1, 8>(a, t, x, y, st);
+    }
+  }
   const int grid = std::min(a.rows, 8 * num_sms());
-  k_ln_bwd_wide<TX, TY><<<grid, WT, 0, st>>>(a, (const TX*)x, (const TY*)dy, (TX*)dx);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !params) return e;
-  const int n = ln_slices(a);
-  k_ln_cols<TX, TY><<<dim3((unsigned)cdiv(a.C, 32), n), WT, 0, st>>>(
-      a, (const TX*)x, (const TY*)dy, part, (int)cdiv(a.rows, n));
+  k_ln_fwd_wide<TX, TY><<<grid, WT, 0, st>>>(a, (const TX*)x, (TY*)y);
   return cudaGetLastError();
 }
 
@@ -266,7 +222,7 @@ size_t rnnt_ln_saved_bytes(const rnnt_ln_dims* dims) {
 
 size_t rnnt_ln_workspace_bytes(const rnnt_ln_dims* dims) {
   LnArgs a;
-  return ln_args(dims, &a) ? align_up(8 * (size_t)ln_slices(a) * a.C) : 0;
+  return ln_args(dims, &a) ? align_up(8 * (size_t)part_rows_max(a) * a.C) : 0;
 }
 
 rnnt_status rnnt_ln_fwd(const rnnt_ln_dims* dims, const void* x, const float* gamma,
@@ -299,23 +255,13 @@ rnnt_status rnnt_ln_bwd(const rnnt_ln_dims* dims, const void* x, const void* dy,
     return RNNT_ERR_INVALID_ARG;
   if (ws_bytes < rnnt_ln_workspace_bytes(dims)) return RNNT_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t st = (cudaStream_t)stream;
-  using bf = __nv_bfloat16;
-  const bool yf = dims->y_dtype == RNNT_F32, params = dgamma || dbeta;
-  float2* part = (float2*)ws;
-  if (a.rows > 0) {
-    ProfScope ps("ln_bwd", st);
-    if (dims->x_dtype == RNNT_F32)
-      OPS_CHECK((yf ? ln_bwd<float, float>(a, x, dy, dx, part, params, st)
-                    : ln_bwd<float, bf>(a, x, dy, dx, part, params, st)));
-    else
-      OPS_CHECK((yf ? ln_bwd<bf, float>(a, x, dy, dx, part, params, st)
-                    : ln_bwd<bf, bf>(a, x, dy, dx, part, params, st)));
-  }
-  if (!params) return RNNT_OK;
-  ProfScope ps("ln_params", st);
-  k_ln_params<<<(unsigned)cdiv(a.C, 32), WT, 0, st>>>(part, a.rows ? ln_slices(a) : 0, a.C, dgamma,
-                                                     dbeta);
-  OPS_CHECK(cudaGetLastError());
+  const bool params = dgamma || dbeta;
+  int rows = 0;
+  if (a.rows > 0)
+    OPS_LAUNCH("ln_bwd", launch_bwd(a, dims->x_dtype, dims->y_dtype, x, dy, dx, (float2*)ws, &rows,
+                                    params, st));
+  if (params)
+    OPS_LAUNCH("ln_params", launch_params((const float2*)ws, rows, a.C, dgamma, dbeta, st));
   return RNNT_OK;
 }
 

@@ -1,0 +1,362 @@
+// ln.cuh -- layer norm of rows: what its forward (k_ln.cu) and backward
+// (k_ln_bwd.cu) kernels share (internal).
+//
+// A team of lanes (8 to 512 threads) takes a row at a time: each lane holds NV
+// vectors of VEC consecutive channels in registers from the load to the store,
+// so that a row is read once, whatever its sums need.  Rows are copied to shared
+// memory STAGES ahead: a lane copies the vectors that it will read itself, so
+// nothing but its own copies is waited for, and the loads in flight (three rows a
+// team) take no registers.  Both directions are bound by DRAM.
+#pragma once
+#include <algorithm>
+#include <atomic>
+
+#include "ops.h"
+#include "ptx.cuh"
+
+namespace rnnt {
+namespace ln {
+
+struct LnArgs {
+  int B, T, C, extra;  // extra: rows past lengths[b] that exist (1 for label rows)
+  int rows;            // B * T
+  float eps, rC;
+  FastDiv t_div;
+  long long xf, xb, yf, yb;
+  const float* gamma;
+  const float* beta;
+  const int32_t* lengths;
+  int32_t* status;
+  float2* stats;  // mean and rstd of every row
+};
+
+// Row r of the batch (where it is taken by a block).
+struct Row {
+  bool live;
+  long long x, y;  // offsets of its first element
+};
+__device__ __forceinline__ Row row_of(const LnArgs& a, int r) {
+  const int b = r / a.t_div, t = r - b * a.T;
+  Row w;
+  w.x = b * a.xb + t * a.xf;
+  w.y = b * a.yb + t * a.yf;
+  w.live = true;
+  if (a.lengths) {
+    const int n = __ldg(a.lengths + b);
+    if (n < 0 || n > a.T - a.extra) {
+      report(a.status, RNNT_ERR_LENGTH_RANGE);
+      w.live = false;
+    } else {
+      w.live = t < n + a.extra;
+    }
+  }
+  return w;
+}
+
+
+// ---- vectors ------------------------------------------------------------------
+// VEC (8, 4, 2 or 1) channels as pairs of fp32 (of one: the pair's first).
+constexpr int kPairs(int vec) { return vec == 1 ? 1 : vec / 2; }
+template <int VEC>
+struct Vals {
+  float2 p[kPairs(VEC)];
+  __device__ __forceinline__ void fill(float v) {
+#pragma unroll
+    for (int i = 0; i < kPairs(VEC); ++i) p[i] = make_float2(v, VEC == 1 ? 0.f : v);
+  }
+};
+
+template <int BYTES> struct UnitOf;
+template <> struct UnitOf<2> { using type = unsigned short; };
+template <> struct UnitOf<4> { using type = uint32_t; };
+template <> struct UnitOf<8> { using type = uint2; };
+template <> struct UnitOf<16> { using type = uint4; };
+// VEC values of T as they are stored
+template <int VEC, typename T>
+using Unit = typename UnitOf<VEC * (int)sizeof(T)>::type;
+
+template <int VEC, typename T>
+__device__ __forceinline__ Vals<VEC> widen(const Unit<VEC, T>& u) {
+  Vals<VEC> v;
+  if constexpr (sizeof(T) == 4) {
+    const float* f = (const float*)&u;
+    if constexpr (VEC == 1) {
+      v.p[0] = make_float2(f[0], 0.f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC / 2; ++i) v.p[i] = make_float2(f[2 * i], f[2 * i + 1]);
+    }
+  } else if constexpr (VEC == 1) {
+    v.p[0] = make_float2(__uint_as_float((uint32_t)u << 16), 0.f);
+  } else {
+    const uint32_t* w = (const uint32_t*)&u;
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) v.p[i] = make_float2(ptx::bf16lo(w[i]), ptx::bf16hi(w[i]));
+  }
+  return v;
+}
+
+template <int VEC, typename T>
+__device__ __forceinline__ void store(T* at, const Vals<VEC>& v) {
+  Unit<VEC, T> u;
+  if constexpr (sizeof(T) == 4) {
+    float* f = (float*)&u;
+    if constexpr (VEC == 1) {
+      f[0] = v.p[0].x;
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC / 2; ++i) {
+        f[2 * i] = v.p[i].x;
+        f[2 * i + 1] = v.p[i].y;
+      }
+    }
+  } else if constexpr (VEC == 1) {
+    u = __bfloat16_as_ushort(__float2bfloat16_rn(v.p[0].x));
+  } else {
+    uint32_t* w = (uint32_t*)&u;
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) w[i] = ptx::pack_bf16x2(v.p[i].x, v.p[i].y);
+  }
+  *(Unit<VEC, T>*)at = u;
+}
+
+// fp32 parameters of channels c to c + VEC - 1 (NULL: all `other`).
+template <int VEC>
+__device__ __forceinline__ Vals<VEC> param(const float* p, int c, float other, bool al16) {
+  Vals<VEC> v;
+  if (!p) {
+    v.fill(other);
+  } else if (VEC >= 4 && al16) {
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) {
+      const float4 q = __ldg((const float4*)(p + c) + i);
+      v.p[2 * i] = make_float2(q.x, q.y);
+      v.p[2 * i + 1] = make_float2(q.z, q.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPairs(VEC); ++i)
+      v.p[i] = make_float2(__ldg(p + c + 2 * i), VEC == 1 ? 0.f : __ldg(p + c + 2 * i + 1));
+  }
+  return v;
+}
+
+// ---- a block a row ------------------------------------------------------------
+// Rows too wide for a team: read again for each of their sums (from L2).
+constexpr int WT = 256, WWARPS = WT / 32;
+
+// Sums of two values over the block, for all threads; scr: 2 WWARPS + 2 floats.
+__device__ __forceinline__ float2 block_sum(float2 v, float2* scr) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, d);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, d);
+  }
+  __syncthreads();  // (scr may still be read)
+  if ((threadIdx.x & 31) == 0) scr[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = scr[0];
+#pragma unroll
+  for (int k = 1; k < WWARPS; ++k) {
+    v.x += scr[k].x;
+    v.y += scr[k].y;
+  }
+  return v;
+}
+
+
+// ---- teams ----------------------------------------------------------------------
+constexpr int MAX_THREADS = 512;
+constexpr int STAGES = 3;
+
+struct Team {
+  int lanes;    // threads a row: 8, 16, or whole warps
+  int teams;    // a block's
+  int nvec;     // vectors of a row
+  FastDiv div;  // by lanes
+};
+
+// The calling thread's place.
+struct Place {
+  int team, lane;  // in the block, in the team
+  int first, step; // rows first, first + step, ... are the team's
+  int warp0;       // the first row of the warp's first team (a warp's teams turn together)
+};
+__device__ __forceinline__ Place place_of(const Team& t) {
+  Place p;
+  p.team = (int)threadIdx.x / t.div;
+  p.lane = threadIdx.x - p.team * t.lanes;
+  p.first = blockIdx.x * t.teams + p.team;
+  p.step = gridDim.x * t.teams;
+  p.warp0 = t.lanes < 32 ? (int)blockIdx.x * t.teams + (int)(threadIdx.x & ~31) / t.div : p.first;
+  return p;
+}
+
+// Sums of NQ values over the team, for all its lanes, in a fixed order.  scr: one
+// of two buffers in turn, so that one barrier a sum keeps writers off readers.
+template <int NQ>
+__device__ __forceinline__ void team_sum(float (&v)[NQ], const Team& t, const Place& p,
+                                         float (*scr)[NQ]) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1)
+    if (d < t.lanes)
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) v[q] += __shfl_xor_sync(0xffffffffu, v[q], d);
+  if (t.lanes <= 32) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = t.lanes >> 5;
+  const int w0 = p.team * warps;
+  if (lane == 0)
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) scr[warp][q] = v[q];
+  ptx::named_barrier(1 + p.team, t.lanes);
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) v[q] = lane < warps ? scr[w0 + lane][q] : 0.f;
+#pragma unroll
+  for (int d = 8; d; d >>= 1)
+    if (d < warps)
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) v[q] += __shfl_xor_sync(0xffffffffu, v[q], d);
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) v[q] = __shfl_sync(0xffffffffu, v[q], 0);
+}
+
+// ---- rows ahead -------------------------------------------------------------------
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A lane's vectors of one tensor's rows ahead: [STAGES][NV][threads] units.  Units
+// of two bytes (bf16 rows of odd width or place) are too small for the copies and
+// are loaded when they are used.
+template <int VEC, int NV, typename T>
+struct Ring {
+  static constexpr int BYTES = VEC * (int)sizeof(T);
+  static constexpr bool kAhead = BYTES >= 4;
+  using U = Unit<VEC, T>;
+  uint32_t base;
+  const unsigned char* mine;
+  __device__ __forceinline__ void init(unsigned char* smem) {
+    mine = smem + threadIdx.x * BYTES;
+    base = ptx::smem_u32(mine);
+  }
+  static __host__ __device__ size_t bytes(int threads) {
+    return kAhead ? (size_t)STAGES * NV * threads * BYTES : 0;
+  }
+  __device__ __forceinline__ void fetch(int stage, const T* row, const Team& t, const Place& p) {
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int k = p.lane + j * t.lanes;
+        if (k < t.nvec)
+          copy_async<BYTES>(base + (stage * NV + j) * blockDim.x * BYTES, row + k * VEC);
+      }
+    }
+  }
+  // (a row that does not exist, or a vector past its end: zeros)
+  __device__ __forceinline__ void read(U (&u)[NV], int stage, const T* row, bool live,
+                                       const Team& t, const Place& p) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int k = p.lane + j * t.lanes;
+      u[j] = U{};
+      if (live && k < t.nvec) {
+        if constexpr (kAhead) u[j] = *(const U*)(mine + (stage * NV + j) * blockDim.x * BYTES);
+        else u[j] = *(const U*)(row + k * VEC);
+      }
+    }
+  }
+};
+
+// Length of row r's sample, asked for ahead of its use.
+__device__ __forceinline__ int ask_length(const LnArgs& a, int r) {
+  return a.lengths && r < a.rows ? __ldg(a.lengths + r / a.t_div) : a.T - a.extra;
+}
+// Row r by that length.
+__device__ __forceinline__ bool exists(const LnArgs& a, int r, int length, bool says) {
+  if (r >= a.rows) return false;
+  if (length < 0 || length > a.T - a.extra) {
+    if (says) report(a.status, RNNT_ERR_LENGTH_RANGE);
+    return false;
+  }
+  return r - r / a.t_div * a.T < length + a.extra;
+}
+__device__ __forceinline__ long long offset(int r, const LnArgs& a, long long f, long long b) {
+  const int s = r / a.t_div;
+  return s * b + (r - s * a.T) * f;
+}
+
+// ---- host -------------------------------------------------------------------------
+// Vectors a lane and lanes a row, for rows of nvec vectors: the fewest lanes whose
+// NV (among the sizes compiled, at most `most`) hold them; 0 lanes: too wide.
+inline Team team_for(int nvec, int most, bool wide_units, int* nv) {
+  Team t{};
+  t.nvec = nvec;
+  auto fit = [&](int per) {
+    if (wide_units) return per;                      // 1, 2, 3, 4
+    return per <= 2 ? 2 : per <= 4 ? 4 : 8;          // of narrow units
+  };
+  const int warps = (int)cdiv(nvec, 32LL * most);
+  *nv = fit((int)cdiv(nvec, 32LL * warps));
+  t.lanes = 32 * warps;
+  if (warps == 1)
+    while (t.lanes > 8 && nvec <= (t.lanes / 2) * *nv) t.lanes /= 2;
+  if (t.lanes > MAX_THREADS) {
+    t.lanes = 0;
+    return t;
+  }
+  t.teams = t.lanes > 256 ? 1 : 256 / t.lanes;
+  t.div = fast_div(t.lanes);
+  return t;
+}
+
+// Vector width that every row of these tensors allows: 16 bytes of the larger
+// type, two elements, or one.
+inline int vec_of(const LnArgs& a, int ex, const void* x, const void* dx, int ey, const void* y) {
+  auto all = [&](int v) {
+    return a.C % v == 0 && a.xf % v == 0 && a.yf % v == 0 && (a.B <= 1 || (a.xb % v == 0 && a.yb % v == 0)) &&
+           aligned_to(x, v * ex) && aligned_to(dx, v * ex) && aligned_to(y, v * ey);
+  };
+  const int v16 = 16 / std::max(ex, ey);
+  return all(v16) ? v16 : all(2) ? 2 : 1;
+}
+
+// Most of a kernel's blocks that an SM holds: asked once per kernel, device and
+// number of warps (a kernel's shared memory follows from its threads).
+struct Known {
+  std::atomic<uint8_t> blocks[kDeviceSlots][MAX_THREADS / 32 + 1];
+};
+constexpr int SMEM_MAX = 200 * 1024;
+template <typename K>
+cudaError_t blocks_per_sm(K k, Known* known, int threads, size_t smem, int* out) {
+  std::atomic<uint8_t>& m = known->blocks[device_slot()][threads / 32];
+  *out = m.load();
+  if (*out) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(out, k, threads, smem);
+  if (e != cudaSuccess) return e;
+  *out = std::max(1, *out);
+  m.store((uint8_t)*out);
+  return e;
+}
+
+// launchers (k_ln.cu, k_ln_bwd.cu); part_rows: rows of part that were written
+int part_rows_max(const LnArgs& a);
+cudaError_t launch_bwd(const LnArgs& a, int x_dtype, int y_dtype, const void* x, const void* dy,
+                       void* dx, float2* part, int* part_rows, bool params, cudaStream_t st);
+cudaError_t launch_params(const float2* part, int rows, int C, float* dgamma, float* dbeta,
+                          cudaStream_t st);
+
+}  // namespace ln
+}  // namespace rnnt
