@@ -5,48 +5,78 @@
 namespace rnnt {
 namespace {
 using namespace ln;
+#ifndef FWD_CH
+#define FWD_CH 16
+#endif
+#ifndef FWD_B
+#define FWD_B 2
+#endif
 
-template <typename TX, typename TY, int VEC, int NV>
-__global__ void __launch_bounds__(MAX_THREADS)
+template <typename TX, typename TY, int VEC, int NV, int MODE>
+__global__ void __launch_bounds__(MODE == WARPS ? MAX_THREADS : 256, MODE == WARPS ? 1 : FWD_B)
 k_ln_fwd(LnArgs a, Team t, const TX* __restrict__ x, TY* __restrict__ y) {
   using R = Ring<VEC, NV, TX>;
   constexpr int NP = kPairs(VEC);
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float scr[2][MAX_THREADS / 32][1];
-  const Place p = place_of(t);
+  const Place p = place_of<MODE>(t);
   const bool al16 = (((uintptr_t)a.gamma | (uintptr_t)a.beta) & 15) == 0;
+  const Stride by(a, p.step);
+  // the row to copy next, and the row at hand
+  Walk next(a, p.first), row = next;
+  Offset xo(a, next, by, a.xf, a.xb), yo(a, row, by, a.yf, a.yb);
+  Offset xr = xo;  // (of rows that are not copied ahead)
   R ring;
   ring.init(smem);
-  unsigned lives = 0;  // bit s: the row of stage s exists
-  int length = ask_length(a, p.first);
-  auto ahead = [&](int r, int stage) {
-    const bool live = exists(a, r, length, p.lane == 0);
-    length = ask_length(a, r + p.step);
-    if (live) ring.fetch(stage, x + offset(r, a, a.xf, a.xb), t, p);
+  unsigned lives = 0;  // bit s: the row s turns from now exists
+  int length = ask_length(a, next);
+  auto ahead = [&](int stage) {
+    const bool live = exists(a, next, length, p.lane == 0);
+    if (live) ring.fetch(stage, x + xo.at, t, p);
     copy_commit();
-    lives = (lives & ~(1u << stage)) | ((unsigned)live << stage);
+    lives |= (unsigned)live << (STAGES - 1);
+    advance(a, by, next, xo);
+    length = ask_length(a, next);
   };
 #pragma unroll
-  for (int s = 0; s < STAGES; ++s) ahead(p.first + s * p.step, s);
+  for (int s = 0; s < STAGES; ++s) {
+    lives >>= 1;
+    ahead(s);
+  }
+  Vals<VEC> gamma[NV], beta[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int k = p.lane + j * t.lanes;
+    gamma[j].fill(0.f);
+    beta[j].fill(0.f);
+    if (k < t.nvec) {
+      gamma[j] = param<VEC>(a.gamma, k * VEC, 1.f, al16);
+      beta[j] = param<VEC>(a.beta, k * VEC, 0.f, al16);
+    }
+  }
+  const float C = (float)a.C;
   int stage = 0;
 #pragma unroll 1
-  for (int r = p.first, w = p.warp0; w < a.rows; r += p.step, w += p.step) {
-    const bool live = (lives >> stage) & 1;
-    TY* yr = y + offset(r, a, a.yf, a.yb);
+  while (MODE == PART ? __any_sync(0xffffffffu, row.b < a.B) : row.b < a.B) {
+    const bool live = lives & 1, here = MODE != PART || row.b < a.B;
+    const int r = row.b * a.T + row.t;
+    TY* to = y + yo.at;
     typename R::U u[NV];
     copy_wait<STAGES - 1>();
-    ring.read(u, stage, x + (R::kAhead ? 0 : offset(r, a, a.xf, a.xb)), live, t, p);
-    ahead(r + STAGES * p.step, stage);
+    ring.read(u, stage, x + xr.at, live, t, p);
+    lives >>= 1;
+    ahead(stage);
     stage = stage + 1 == STAGES ? 0 : stage + 1;
-    if (t.lanes < 32 ? !__any_sync(0xffffffffu, live) : !live) {
+    if constexpr (R::kAhead) advance(a, by, row, yo);
+    else advance(a, by, row, yo, xr);
+    if (MODE == PART ? !__any_sync(0xffffffffu, live) : !live) {
       Vals<VEC> z;
       z.fill(0.f);
-      if (r < a.rows)
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int k = p.lane + j * t.lanes;
-          if (k < t.nvec) store<VEC, TY>(yr + k * VEC, z);
-        }
+      for (int j = 0; j < NV; ++j) {
+        const int k = p.lane + j * t.lanes;
+        if (here && k < t.nvec) store<VEC, TY>(to + k * VEC, z);
+      }
       continue;
     }
     // the mean, then the squares about it
@@ -59,8 +89,9 @@ k_ln_fwd(LnArgs a, Team t, const TX* __restrict__ x, TY* __restrict__ y) {
       for (int i = 0; i < NP; ++i) s2 = __fadd2_rn(s2, v[j].p[i]);
     }
     float s[1] = {s2.x + s2.y};
-    team_sum(s, t, p, scr[0]);
-    const float mean = s[0] / (float)a.C;  // (exact for rows of one value)
+    team_sum<MODE>(s, t, p, scr[0]);
+    float mean = s[0] * a.rC;
+    mean = fmaf(fmaf(-mean, C, s[0]), a.rC, mean);  // (exact for rows of one value)
     s2 = make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -71,23 +102,21 @@ k_ln_fwd(LnArgs a, Team t, const TX* __restrict__ x, TY* __restrict__ y) {
       }
     }
     s[0] = VEC == 1 ? s2.x : s2.x + s2.y;
-    team_sum(s, t, p, scr[1]);
-    const float rstd = 1.f / sqrtf(s[0] * a.rC + a.eps);
+    team_sum<MODE>(s, t, p, scr[1]);
+    const float rstd = rsqrtf(fmaf(s[0], a.rC, a.eps));
     if (a.stats && live && p.lane == 0) a.stats[r] = make_float2(mean, rstd);
-    if (r < a.rows)
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int k = p.lane + j * t.lanes;
-        if (k >= t.nvec) continue;
-        const Vals<VEC> g = param<VEC>(a.gamma, k * VEC, 1.f, al16);
-        Vals<VEC> o = param<VEC>(a.beta, k * VEC, 0.f, al16);
+    for (int j = 0; j < NV; ++j) {
+      const int k = p.lane + j * t.lanes;
+      Vals<VEC> o;
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const float2 h = __fmul2_rn(v[j].p[i], make_float2(rstd, rstd));
-          o.p[i] = live ? __ffma2_rn(g.p[i], h, o.p[i]) : make_float2(0.f, 0.f);
-        }
-        store<VEC, TY>(yr + k * VEC, o);
+      for (int i = 0; i < NP; ++i) {
+        o.p[i] = __ffma2_rn(gamma[j].p[i], __fmul2_rn(v[j].p[i], make_float2(rstd, rstd)),
+                            beta[j].p[i]);
+        if (MODE == PART && !live) o.p[i] = make_float2(0.f, 0.f);
       }
+      if (here && k < t.nvec) store<VEC, TY>(to + k * VEC, o);
+    }
   }
   copy_wait<0>();
 }
@@ -166,43 +195,33 @@ rnnt_status ln_check(const rnnt_ln_dims* d, LnArgs* a, const void* x, const void
   return RNNT_OK;
 }
 
-template <typename TX, typename TY, int VEC, int NV>
-cudaError_t fwd_team(const LnArgs& a, const Team& t, const void* x, void* y, cudaStream_t st) {
-  static Known known;
-  const int threads = t.lanes * t.teams;
-  const size_t smem = Ring<VEC, NV, TX>::bytes(threads);
-  int per = 0;
-  const cudaError_t e = blocks_per_sm(k_ln_fwd<TX, TY, VEC, NV>, &known, threads, smem, &per);
-  if (e != cudaSuccess) return e;
-  const int grid = (int)std::min<long long>(cdiv(a.rows, t.teams), (long long)per * num_sms());
-  k_ln_fwd<TX, TY, VEC, NV><<<grid, threads, smem, st>>>(a, t, (const TX*)x, (TY*)y);
-  return cudaGetLastError();
-}
+template <typename TX, typename TY>
+struct Fwd {
+  const LnArgs& a;
+  const void* x;
+  void* y;
+  cudaStream_t st;
+  template <int VEC, int NV, int MODE>
+  cudaError_t run(const Team& t) const {
+    static Known known;
+    const auto k = k_ln_fwd<TX, TY, VEC, NV, MODE>;
+    const int threads = t.lanes * t.teams;
+    const size_t smem = Ring<VEC, NV, TX>::bytes(threads);
+    int per = 0;
+    const cudaError_t e = blocks_per_sm(k, &known, threads, smem, &per);
+    if (e != cudaSuccess) return e;
+    const int grid = (int)std::min<long long>(cdiv(a.rows, t.teams), (long long)per * num_sms());
+    k<<<grid, threads, smem, st>>>(a, t, (const TX*)x, (TY*)y);
+    return cudaGetLastError();
+  }
+};
 
 template <typename TX, typename TY>
 cudaError_t ln_fwd(const LnArgs& a, const void* x, void* y, cudaStream_t st) {
   constexpr int V16 = 16 / (int)std::max(sizeof(TX), sizeof(TY));
   const int vec = vec_of(a, sizeof(TX), x, nullptr, sizeof(TY), y);
-  int nv = 0;
-  const Team t = team_for((int)cdiv(a.C, vec), vec == V16 ? 4 : 8, vec == V16, &nv);
-  if (t.lanes) {
-    if (vec == V16) switch (nv) {
-      case 1: return fwd_team<TX, TY, V16, 1>(a, t, x, y, st);
-      case 2: return fwd_team<TX, TY, V16, 2>(a, t, x, y, st);
-      case 3: return fwd_team<TX, TY, V16, 3>(a, t, x, y, st);
-      default: return fwd_team<TX, TY, V16, 4>(a, t, x, y, st);
-    }
-    if (vec == 2) switch (nv) {
-      case 2: return fwd_team<TX, TY, 2, 2>(a, t, x, y, st);
-      case 4: return fwd_team<TX, TY, 2, 4>(a, t, x, y, st);
-      default: return fwd_team<TX, TY, 2, 8>(a, t, x, y, st);
-    }
-    switch (nv) {
-      case 2: return fwd_team<TX, TY, 1, 2>(a, t, x, y, st);
-      case 4: return fwd_team<TX, TY, 1, 4>(a, t, x, y, st);
-      default: return fwd_team<TX, TY, 1, 8>(a, t, x, y, st);
-    }
-  }
+  cudaError_t e;
+  if (by_team<V16, (V16 == 8 ? FWD_CH : 16)>(a.C, vec, Fwd<TX, TY>{a, x, y, st}, &e)) return e;
   const int grid = std::min(a.rows, 8 * num_sms());
   k_ln_fwd_wide<TX, TY><<<grid, WT, 0, st>>>(a, (const TX*)x, (TY*)y);
   return cudaGetLastError();

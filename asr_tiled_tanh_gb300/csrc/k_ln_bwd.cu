@@ -4,10 +4,13 @@
 namespace rnnt {
 namespace {
 using namespace ln;
+#ifndef BWD_B
+#define BWD_B 2
+#endif
 
 // dx of the team's rows, and part[block][c] = (sum dy xh, sum dy) over the block's.
-template <typename TX, typename TY, int VEC, int NV>
-__global__ void __launch_bounds__(MAX_THREADS)
+template <typename TX, typename TY, int VEC, int NV, int MODE>
+__global__ void __launch_bounds__(MODE == WARPS ? MAX_THREADS : 256, MODE == WARPS ? 1 : BWD_B)
 k_ln_bwd(LnArgs a, Team t, const TX* __restrict__ x, const TY* __restrict__ dy,
          TX* __restrict__ dx, float2* __restrict__ part) {
   using RX = Ring<VEC, NV, TX>;
@@ -15,66 +18,75 @@ k_ln_bwd(LnArgs a, Team t, const TX* __restrict__ x, const TY* __restrict__ dy,
   constexpr int NP = kPairs(VEC);
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float scr[2][MAX_THREADS / 32][2];
-  const Place p = place_of(t);
+  ptx::griddep_launch();
+  const Place p = place_of<MODE>(t);
   const bool al16 = ((uintptr_t)a.gamma & 15) == 0;
+  const Stride by(a, p.step);
+  Walk next(a, p.first), row = next;
+  Offset xo(a, next, by, a.xf, a.xb), yo(a, next, by, a.yf, a.yb), xr = xo, yr = yo;
   RX rx;
   RY ry;
   rx.init(smem);
   ry.init(smem + RX::bytes(blockDim.x));
-  unsigned lives = 0;
-  int length = ask_length(a, p.first);
-  auto ahead = [&](int r, int stage) {
-    const bool live = exists(a, r, length, p.lane == 0);
-    length = ask_length(a, r + p.step);
+  unsigned lives = 0;  // bit s: the row s turns from now exists
+  int length = ask_length(a, next);
+  auto ahead = [&](int stage) {
+    const bool live = exists(a, next, length, p.lane == 0);
     if (live) {
-      rx.fetch(stage, x + offset(r, a, a.xf, a.xb), t, p);
-      ry.fetch(stage, dy + offset(r, a, a.yf, a.yb), t, p);
+      rx.fetch(stage, x + xo.at, t, p);
+      ry.fetch(stage, dy + yo.at, t, p);
     }
     copy_commit();
-    lives = (lives & ~(1u << stage)) | ((unsigned)live << stage);
+    lives |= (unsigned)live << (STAGES - 1);
+    advance(a, by, next, xo, yo);
+    length = ask_length(a, next);
   };
 #pragma unroll
-  for (int s = 0; s < STAGES; ++s) ahead(p.first + s * p.step, s);
-  auto ask_stats = [&](int r, bool live) {
-    return live ? __ldg(a.stats + r) : make_float2(0.f, 0.f);
+  for (int s = 0; s < STAGES; ++s) {
+    lives >>= 1;
+    ahead(s);
+  }
+  auto ask_stats = [&]() {
+    return lives & 1 ? __ldg(a.stats + row.b * a.T + row.t) : make_float2(0.f, 0.f);
   };
-  float2 next = ask_stats(p.first, lives & 1);
+  float2 coming = ask_stats();
   Vals<VEC> gamma[NV], dg[NV], db[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int k = p.lane + j * t.lanes;
+    gamma[j].fill(0.f);
     if (k < t.nvec) gamma[j] = param<VEC>(a.gamma, k * VEC, 1.f, al16);
-    else gamma[j].fill(0.f);
     dg[j].fill(0.f);
     db[j].fill(0.f);
   }
   int stage = 0, par = 0;
 #pragma unroll 1
-  for (int r = p.first, w = p.warp0; w < a.rows; r += p.step, w += p.step) {
-    const bool live = (lives >> stage) & 1;
-    const long long at = offset(r, a, a.xf, a.xb);
-    TX* dr = dx + at;
+  while (MODE == PART ? __any_sync(0xffffffffu, row.b < a.B) : row.b < a.B) {
+    const bool live = lives & 1, here = MODE != PART || row.b < a.B;
+    TX* to = dx + xr.at;
     typename RX::U ux[NV];
     typename RY::U uy[NV];
     copy_wait<STAGES - 1>();
-    rx.read(ux, stage, x + (RX::kAhead ? 0 : at), live, t, p);
-    ry.read(uy, stage, dy + (RY::kAhead ? 0 : offset(r, a, a.yf, a.yb)), live, t, p);
-    ahead(r + STAGES * p.step, stage);
+    rx.read(ux, stage, x + xr.at, live, t, p);
+    ry.read(uy, stage, dy + yr.at, live, t, p);
+    lives >>= 1;
+    ahead(stage);
     stage = stage + 1 == STAGES ? 0 : stage + 1;
-    const float2 st = next;
-    next = ask_stats(r + p.step, (lives >> stage) & 1);
-    if (t.lanes < 32 ? !__any_sync(0xffffffffu, live) : !live) {
+    if constexpr (RY::kAhead) advance(a, by, row, xr);
+    else advance(a, by, row, xr, yr);
+    const float2 st = coming;
+    coming = ask_stats();
+    if (MODE == PART ? !__any_sync(0xffffffffu, live) : !live) {
       Vals<VEC> z;
       z.fill(0.f);
-      if (r < a.rows)
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int k = p.lane + j * t.lanes;
-          if (k < t.nvec) store<VEC, TX>(dr + k * VEC, z);
-        }
+      for (int j = 0; j < NV; ++j) {
+        const int k = p.lane + j * t.lanes;
+        if (here && k < t.nvec) store<VEC, TX>(to + k * VEC, z);
+      }
       continue;
     }
-    // (rows and vectors that do not exist: dy is 0)
+    // (of vectors past the row's end dy is 0)
     Vals<VEC> xh[NV], g[NV];
     float2 s1 = make_float2(0.f, 0.f), s2 = s1;
 #pragma unroll
@@ -85,6 +97,7 @@ k_ln_bwd(LnArgs a, Team t, const TX* __restrict__ x, const TY* __restrict__ dy,
       for (int i = 0; i < NP; ++i) {
         xh[j].p[i] = __fmul2_rn(__fadd2_rn(xh[j].p[i], make_float2(-st.x, -st.x)),
                                 make_float2(st.y, st.y));
+        if (MODE == PART && !live) xh[j].p[i] = g[j].p[i] = make_float2(0.f, 0.f);
         dg[j].p[i] = __ffma2_rn(g[j].p[i], xh[j].p[i], dg[j].p[i]);
         db[j].p[i] = __fadd2_rn(g[j].p[i], db[j].p[i]);
         g[j].p[i] = __fmul2_rn(g[j].p[i], gamma[j].p[i]);
@@ -93,30 +106,28 @@ k_ln_bwd(LnArgs a, Team t, const TX* __restrict__ x, const TY* __restrict__ dy,
       }
     }
     float s[2] = {s1.x + s1.y, s2.x + s2.y};
-    team_sum(s, t, p, scr[par]);
+    team_sum<MODE>(s, t, p, scr[par]);
     par ^= 1;
-    const float m1 = -s[0] * a.rC, m2 = -s[1] * a.rC;
-    if (r < a.rows)
+    // dx = rstd a + (k1 + k2 xh)
+    const float k1 = -s[0] * a.rC * st.y, k2 = -s[1] * a.rC * st.y;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int k = p.lane + j * t.lanes;
-        if (k >= t.nvec) continue;
-        Vals<VEC> o;
+    for (int j = 0; j < NV; ++j) {
+      const int k = p.lane + j * t.lanes;
+      Vals<VEC> o;
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
-          o.p[i] = __fmul2_rn(__ffma2_rn(xh[j].p[i], make_float2(m2, m2),
-                                         __fadd2_rn(g[j].p[i], make_float2(m1, m1))),
-                              make_float2(st.y, st.y));
-        store<VEC, TX>(dr + k * VEC, o);
-      }
+      for (int i = 0; i < NP; ++i)
+        o.p[i] = __ffma2_rn(g[j].p[i], make_float2(st.y, st.y),
+                            __ffma2_rn(xh[j].p[i], make_float2(k2, k2), make_float2(k1, k1)));
+      if (here && k < t.nvec) store<VEC, TX>(to + k * VEC, o);
+    }
   }
   copy_wait<0>();
   if (!part) return;
   // the block's sums: the teams' in order (of a warp's narrow teams by shuffles first)
-  const int groups = t.lanes < 32 ? (int)blockDim.x >> 5 : t.teams;
-  const int cols = t.lanes * VEC, group = t.lanes < 32 ? (int)threadIdx.x >> 5 : p.team;
+  const int groups = MODE == WARPS ? t.teams : (int)blockDim.x >> 5;
+  const int cols = t.lanes * VEC, group = MODE == WARPS ? p.team : (int)threadIdx.x >> 5;
   float2* sums = (float2*)smem;  // [group][cols]
-  float2* row = part + (long long)blockIdx.x * a.C;
+  float2* out = part + (long long)blockIdx.x * a.C;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     __syncthreads();
@@ -124,7 +135,7 @@ k_ln_bwd(LnArgs a, Team t, const TX* __restrict__ x, const TY* __restrict__ dy,
     for (int i = 0; i < VEC; ++i) {
       float2 v = make_float2(i & 1 ? dg[j].p[i / 2].y : dg[j].p[i / 2].x,
                              i & 1 ? db[j].p[i / 2].y : db[j].p[i / 2].x);
-      for (int d = 16; d >= t.lanes; d >>= 1) {
+      for (int d = 16; MODE == PART && d >= t.lanes; d >>= 1) {
         v.x += __shfl_xor_sync(0xffffffffu, v.x, d);
         v.y += __shfl_xor_sync(0xffffffffu, v.y, d);
       }
@@ -138,7 +149,7 @@ k_ln_bwd(LnArgs a, Team t, const TX* __restrict__ x, const TY* __restrict__ dy,
       if (col >= a.C) continue;
       float2 v = sums[at];
       for (int k = 1; k < groups; ++k) v = __fadd2_rn(v, sums[k * cols + at]);
-      row[col] = v;
+      out[col] = v;
     }
   }
 }
@@ -204,85 +215,70 @@ k_ln_cols(LnArgs a, const TX* __restrict__ x, const TY* __restrict__ dy,
   part[(long long)blockIdx.y * a.C + c] = s;
 }
 
-// dgamma, dbeta: the column sums of part [n][C], 32 channels a block.
+// dgamma, dbeta: the column sums of part [n][C], 8 channels a block, its 32 groups
+// of threads a row each at a time.
+constexpr int PCOLS = 8, PGROUPS = WT / PCOLS;
 __global__ void __launch_bounds__(WT)
 k_ln_params(const float2* __restrict__ part, int n, int C, float* __restrict__ dgamma,
             float* __restrict__ dbeta) {
-  __shared__ float2 scr[WWARPS][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+  __shared__ float2 scr[PGROUPS][PCOLS];
+  const int col = threadIdx.x % PCOLS, group = threadIdx.x / PCOLS;
+  const int c = blockIdx.x * PCOLS + col;
+  ptx::griddep_wait();
   float2 s = make_float2(0.f, 0.f);
   if (c < C)
-#pragma unroll 4
-    for (int r = warp; r < n; r += WWARPS) {
-      const float2 p = __ldcg(part + (long long)r * C + c);
-      s.x += p.x;
-      s.y += p.y;
-    }
-  scr[warp][lane] = s;
+#pragma unroll 8
+    for (int r = group; r < n; r += PGROUPS)
+      s = __fadd2_rn(s, __ldcg(part + (long long)r * C + c));
+  scr[group][col] = s;
   __syncthreads();
-  if (warp || c >= C) return;
-  for (int k = 1; k < WWARPS; ++k) {
-    s.x += scr[k][lane].x;
-    s.y += scr[k][lane].y;
-  }
+  if (group || c >= C) return;
+#pragma unroll
+  for (int k = 1; k < PGROUPS; ++k) s = __fadd2_rn(s, scr[k][col]);
   if (dgamma) dgamma[c] = s.x;
   if (dbeta) dbeta[c] = s.y;
 }
 
 constexpr int PART_ROWS = 608;  // (the workspace may not depend on the device)
 
-template <typename TX, typename TY, int VEC, int NV>
-cudaError_t bwd_team(const LnArgs& a, const Team& t, const void* x, const void* dy, void* dx,
-                     float2* part, int* part_rows, cudaStream_t st) {
-  static Known known;
-  const int threads = t.lanes * t.teams;
-  const size_t sums = sizeof(float2) * VEC * threads;
-  const size_t smem =
-      std::max(sums, Ring<VEC, NV, TX>::bytes(threads) + Ring<VEC, NV, TY>::bytes(threads));
-  int per = 0;
-  const cudaError_t e = blocks_per_sm(k_ln_bwd<TX, TY, VEC, NV>, &known, threads, smem, &per);
-  if (e != cudaSuccess) return e;
-  const int grid = (int)std::min<long long>(
-      std::min<long long>(cdiv(a.rows, t.teams), part_rows_max(a)), (long long)per * num_sms());
-  k_ln_bwd<TX, TY, VEC, NV><<<grid, threads, smem, st>>>(a, t, (const TX*)x, (const TY*)dy, (TX*)dx,
-                                                         part);
-  *part_rows = grid;
-  return cudaGetLastError();
-}
+template <typename TX, typename TY>
+struct Bwd {
+  const LnArgs& a;
+  const void *x, *dy;
+  void* dx;
+  float2* part;
+  int* part_rows;
+  cudaStream_t st;
+  template <int VEC, int NV, int MODE>
+  cudaError_t run(const Team& t) const {
+    static Known known;
+    const auto k = k_ln_bwd<TX, TY, VEC, NV, MODE>;
+    const int threads = t.lanes * t.teams;
+    const size_t sums = sizeof(float2) * VEC * threads;
+    const size_t smem =
+        std::max(sums, Ring<VEC, NV, TX>::bytes(threads) + Ring<VEC, NV, TY>::bytes(threads));
+    int per = 0;
+    const cudaError_t e = blocks_per_sm(k, &known, threads, smem, &per);
+    if (e != cudaSuccess) return e;
+    const int grid = (int)std::min<long long>(
+        std::min<long long>(cdiv(a.rows, t.teams), part_rows_max(a)), (long long)per * num_sms());
+    k<<<grid, threads, smem, st>>>(a, t, (const TX*)x, (const TY*)dy, (TX*)dx, part);
+    *part_rows = grid;
+    return cudaGetLastError();
+  }
+};
 
 template <typename TX, typename TY>
 cudaError_t ln_bwd(const LnArgs& a, const void* x, const void* dy, void* dx, float2* part,
                    int* part_rows, cudaStream_t st) {
   constexpr int V16 = 16 / (int)std::max(sizeof(TX), sizeof(TY));
   const int vec = vec_of(a, sizeof(TX), x, dx, sizeof(TY), dy);
-  int nv = 0;
+  cudaError_t e;
   // (16 channels a lane: their sums stay in registers)
-  const Team t = team_for((int)cdiv(a.C, vec), vec == V16 ? 16 / V16 : 8, vec == V16, &nv);
-  if (t.lanes) {
-    if (vec == V16) switch (nv) {
-      case 1: return bwd_team<TX, TY, V16, 1>(a, t, x, dy, dx, part, part_rows, st);
-      case 2: return bwd_team<TX, TY, V16, 2>(a, t, x, dy, dx, part, part_rows, st);
-      default:
-        if constexpr (V16 == 4) {
-          if (nv == 3) return bwd_team<TX, TY, V16, 3>(a, t, x, dy, dx, part, part_rows, st);
-          return bwd_team<TX, TY, V16, 4>(a, t, x, dy, dx, part, part_rows, st);
-        }
-    }
-    if (vec == 2) switch (nv) {
-      case 2: return bwd_team<TX, TY, 2, 2>(a, t, x, dy, dx, part, part_rows, st);
-      case 4: return bwd_team<TX, TY, 2, 4>(a, t, x, dy, dx, part, part_rows, st);
-      default: return bwd_team<TX, TY, 2, 8>(a, t, x, dy, dx, part, part_rows, st);
-    }
-    switch (nv) {
-      case 2: return bwd_team<TX, TY, 1, 2>(a, t, x, dy, dx, part, part_rows, st);
-      case 4: return bwd_team<TX, TY, 1, 4>(a, t, x, dy, dx, part, part_rows, st);
-      default: return bwd_team<TX, TY, 1, 8>(a, t, x, dy, dx, part, part_rows, st);
-    }
-  }
+  if (by_team<V16, 16>(a.C, vec, Bwd<TX, TY>{a, x, dy, dx, part, part_rows, st}, &e)) return e;
   const int grid = std::min(a.rows, 8 * num_sms());
   k_ln_bwd_wide<TX, TY><<<grid, WT, 0, st>>>(a, (const TX*)x, (const TY*)dy, (TX*)dx);
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess || !part) return e;
   const int n = std::min(64, part_rows_max(a));
   k_ln_cols<TX, TY><<<dim3((unsigned)cdiv(a.C, 32), n), WT, 0, st>>>(
@@ -310,8 +306,17 @@ cudaError_t launch_bwd(const LnArgs& a, int x_dtype, int y_dtype, const void* x,
 
 cudaError_t launch_params(const float2* part, int rows, int C, float* dgamma, float* dbeta,
                           cudaStream_t st) {
-  k_ln_params<<<(unsigned)cdiv(C, 32), WT, 0, st>>>(part, rows, C, dgamma, dbeta);
-  return cudaGetLastError();
+  // (its blocks come in under the sums' tail and wait for them)
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)cdiv(C, PCOLS));
+  cfg.blockDim = dim3(WT);
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_ln_params, part, rows, C, dgamma, dbeta);
 }
 
 }  // namespace ln

@@ -167,10 +167,16 @@ __device__ __forceinline__ float2 block_sum(float2 v, float2* scr) {
 
 // ---- teams ----------------------------------------------------------------------
 constexpr int MAX_THREADS = 512;
-constexpr int STAGES = 3;
+#ifndef STG
+#define STG 3
+#endif
+constexpr int STAGES = STG;
+
+// A row is taken by part of a warp (8 or 16 lanes), a warp, or several.
+enum { PART = 0, WARP = 1, WARPS = 2 };
 
 struct Team {
-  int lanes;    // threads a row: 8, 16, or whole warps
+  int lanes;    // threads a row
   int teams;    // a block's
   int nvec;     // vectors of a row
   FastDiv div;  // by lanes
@@ -178,46 +184,96 @@ struct Team {
 
 // The calling thread's place.
 struct Place {
-  int team, lane;  // in the block, in the team
-  int first, step; // rows first, first + step, ... are the team's
-  int warp0;       // the first row of the warp's first team (a warp's teams turn together)
+  int team, lane;   // in the block, in the team
+  int first, step;  // rows first, first + step, ... are the team's
 };
+template <int MODE>
 __device__ __forceinline__ Place place_of(const Team& t) {
   Place p;
-  p.team = (int)threadIdx.x / t.div;
-  p.lane = threadIdx.x - p.team * t.lanes;
+  p.team = MODE == WARP ? threadIdx.x >> 5 : (int)threadIdx.x / t.div;
+  p.lane = MODE == WARP ? threadIdx.x & 31 : threadIdx.x - p.team * t.lanes;
   p.first = blockIdx.x * t.teams + p.team;
   p.step = gridDim.x * t.teams;
-  p.warp0 = t.lanes < 32 ? (int)blockIdx.x * t.teams + (int)(threadIdx.x & ~31) / t.div : p.first;
   return p;
 }
 
 // Sums of NQ values over the team, for all its lanes, in a fixed order.  scr: one
 // of two buffers in turn, so that one barrier a sum keeps writers off readers.
-template <int NQ>
+template <int MODE, int NQ>
 __device__ __forceinline__ void team_sum(float (&v)[NQ], const Team& t, const Place& p,
                                          float (*scr)[NQ]) {
 #pragma unroll
   for (int d = 16; d; d >>= 1)
-    if (d < t.lanes)
+    if (MODE != PART || d < t.lanes)
 #pragma unroll
       for (int q = 0; q < NQ; ++q) v[q] += __shfl_xor_sync(0xffffffffu, v[q], d);
-  if (t.lanes <= 32) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = t.lanes >> 5;
-  const int w0 = p.team * warps;
-  if (lane == 0)
+  if constexpr (MODE == WARPS) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = t.lanes >> 5;
+    if (lane == 0)
 #pragma unroll
-    for (int q = 0; q < NQ; ++q) scr[warp][q] = v[q];
-  ptx::named_barrier(1 + p.team, t.lanes);
+      for (int q = 0; q < NQ; ++q) scr[warp][q] = v[q];
+    ptx::named_barrier(1 + p.team, t.lanes);
 #pragma unroll
-  for (int q = 0; q < NQ; ++q) v[q] = lane < warps ? scr[w0 + lane][q] : 0.f;
+    for (int q = 0; q < NQ; ++q) v[q] = lane < warps ? scr[p.team * warps + lane][q] : 0.f;
 #pragma unroll
-  for (int d = 8; d; d >>= 1)
-    if (d < warps)
+    for (int d = 8; d; d >>= 1)
+      if (d < warps)
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) v[q] += __shfl_xor_sync(0xffffffffu, v[q], d);
+        for (int q = 0; q < NQ; ++q) v[q] += __shfl_xor_sync(0xffffffffu, v[q], d);
 #pragma unroll
-  for (int q = 0; q < NQ; ++q) v[q] = __shfl_sync(0xffffffffu, v[q], 0);
+    for (int q = 0; q < NQ; ++q) v[q] = __shfl_sync(0xffffffffu, v[q], 0);
+  }
+}
+
+// ---- a team's rows, one after another --------------------------------------------
+// Steps of the walk, by additions alone.
+struct Stride {
+  int db, dt;
+  __device__ __forceinline__ Stride(const LnArgs& a, int step) {
+    db = step / a.t_div;
+    dt = step - db * a.T;
+  }
+};
+struct Walk {
+  int b, t;
+  __device__ __forceinline__ Walk(const LnArgs& a, int r) {
+    b = r / a.t_div;
+    t = r - b * a.T;
+  }
+};
+// An offset that goes with a walk: by `step` a row, and by `wrap` where a sample ends.
+struct Offset {
+  long long at, step, wrap;
+  __device__ __forceinline__ Offset(const LnArgs& a, const Walk& w, const Stride& s, long long f,
+                                    long long b) {
+    at = w.b * b + w.t * f;
+    step = s.db * b + s.dt * f;
+    wrap = b - a.T * f;
+  }
+};
+template <typename... O>
+__device__ __forceinline__ void advance(const LnArgs& a, const Stride& s, Walk& w, O&... o) {
+  w.b += s.db;
+  w.t += s.dt;
+  ((o.at += o.step), ...);
+  if (w.t >= a.T) {
+    w.t -= a.T;
+    ++w.b;
+    ((o.at += o.wrap), ...);
+  }
+}
+// Length of the walk's sample, asked for ahead of its use.
+__device__ __forceinline__ int ask_length(const LnArgs& a, const Walk& w) {
+  return a.lengths && w.b < a.B ? __ldg(a.lengths + w.b) : a.T - a.extra;
+}
+// Whether the walk's row exists by that length.
+__device__ __forceinline__ bool exists(const LnArgs& a, const Walk& w, int length, bool says) {
+  if (w.b >= a.B) return false;
+  if ((unsigned)length > (unsigned)(a.T - a.extra)) {
+    if (says) report(a.status, RNNT_ERR_LENGTH_RANGE);
+    return false;
+  }
+  return w.t < length + a.extra;
 }
 
 // ---- rows ahead -------------------------------------------------------------------
@@ -237,78 +293,60 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A lane's vectors of one tensor's rows ahead: [STAGES][NV][threads] units.  Units
-// of two bytes (bf16 rows of odd width or place) are too small for the copies and
-// are loaded when they are used.
+// A lane's vectors of one tensor's rows ahead: [STAGES][NV][threads] units, those of
+// vectors past the row's end zero.  A stage is read and then filled again.  Units of
+// two bytes (bf16 rows of odd width or place) are too small for the copies and are
+// loaded when they are used.
 template <int VEC, int NV, typename T>
 struct Ring {
   static constexpr int BYTES = VEC * (int)sizeof(T);
   static constexpr bool kAhead = BYTES >= 4;
   using U = Unit<VEC, T>;
-  uint32_t base;
-  const unsigned char* mine;
-  __device__ __forceinline__ void init(unsigned char* smem) {
-    mine = smem + threadIdx.x * BYTES;
-    base = ptx::smem_u32(mine);
-  }
+  unsigned char* mine;
+  int pitch;  // bytes from one of a lane's units to its next
   static __host__ __device__ size_t bytes(int threads) {
     return kAhead ? (size_t)STAGES * NV * threads * BYTES : 0;
   }
+  __device__ __forceinline__ void init(unsigned char* smem) {
+    mine = smem + threadIdx.x * BYTES;
+    pitch = blockDim.x * BYTES;
+    if constexpr (kAhead)
+#pragma unroll
+      for (int k = 0; k < STAGES * NV; ++k) *(U*)(mine + k * pitch) = U{};
+  }
   __device__ __forceinline__ void fetch(int stage, const T* row, const Team& t, const Place& p) {
     if constexpr (kAhead) {
+      const uint32_t to = ptx::smem_u32(mine) + stage * (NV * pitch);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (p.lane + j * t.lanes < t.nvec)
+          copy_async<BYTES>(to + j * pitch, row + (p.lane + j * t.lanes) * VEC);
+    }
+  }
+  __device__ __forceinline__ void read(U (&u)[NV], int stage, const T* row, bool live,
+                                       const Team& t, const Place& p) {
+    if constexpr (kAhead) {
+      const unsigned char* from = mine + stage * (NV * pitch);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) u[j] = *(const U*)(from + j * pitch);
+    } else {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int k = p.lane + j * t.lanes;
-        if (k < t.nvec)
-          copy_async<BYTES>(base + (stage * NV + j) * blockDim.x * BYTES, row + k * VEC);
-      }
-    }
-  }
-  // (a row that does not exist, or a vector past its end: zeros)
-  __device__ __forceinline__ void read(U (&u)[NV], int stage, const T* row, bool live,
-                                       const Team& t, const Place& p) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int k = p.lane + j * t.lanes;
-      u[j] = U{};
-      if (live && k < t.nvec) {
-        if constexpr (kAhead) u[j] = *(const U*)(mine + (stage * NV + j) * blockDim.x * BYTES);
-        else u[j] = *(const U*)(row + k * VEC);
+        u[j] = live && k < t.nvec ? *(const U*)(row + k * VEC) : U{};
       }
     }
   }
 };
 
-// Length of row r's sample, asked for ahead of its use.
-__device__ __forceinline__ int ask_length(const LnArgs& a, int r) {
-  return a.lengths && r < a.rows ? __ldg(a.lengths + r / a.t_div) : a.T - a.extra;
-}
-// Row r by that length.
-__device__ __forceinline__ bool exists(const LnArgs& a, int r, int length, bool says) {
-  if (r >= a.rows) return false;
-  if (length < 0 || length > a.T - a.extra) {
-    if (says) report(a.status, RNNT_ERR_LENGTH_RANGE);
-    return false;
-  }
-  return r - r / a.t_div * a.T < length + a.extra;
-}
-__device__ __forceinline__ long long offset(int r, const LnArgs& a, long long f, long long b) {
-  const int s = r / a.t_div;
-  return s * b + (r - s * a.T) * f;
-}
-
 // ---- host -------------------------------------------------------------------------
-// Vectors a lane and lanes a row, for rows of nvec vectors: the fewest lanes whose
-// NV (among the sizes compiled, at most `most`) hold them; 0 lanes: too wide.
+// Rows of nvec vectors: the fewest lanes whose vectors, at most `most` each, hold
+// them; nv: vectors a lane among the sizes that are compiled; 0 lanes: too wide.
 inline Team team_for(int nvec, int most, bool wide_units, int* nv) {
   Team t{};
   t.nvec = nvec;
-  auto fit = [&](int per) {
-    if (wide_units) return per;                      // 1, 2, 3, 4
-    return per <= 2 ? 2 : per <= 4 ? 4 : 8;          // of narrow units
-  };
-  const int warps = (int)cdiv(nvec, 32LL * most);
-  *nv = fit((int)cdiv(nvec, 32LL * warps));
+  const int warps = (int)cdiv(nvec, 32LL * most), per = (int)cdiv(nvec, 32LL * warps);
+  *nv = wide_units ? per : per <= 2 ? 2 : per <= 4 ? 4 : 8;
   t.lanes = 32 * warps;
   if (warps == 1)
     while (t.lanes > 8 && nvec <= (t.lanes / 2) * *nv) t.lanes /= 2;
@@ -319,6 +357,38 @@ inline Team team_for(int nvec, int most, bool wide_units, int* nv) {
   t.teams = t.lanes > 256 ? 1 : 256 / t.lanes;
   t.div = fast_div(t.lanes);
   return t;
+}
+
+// f.run<VEC, NV, MODE>(team) for rows of C channels in vectors of vec (V16: those of
+// 16 bytes) and at most CH channels a lane; false: no team holds such a row.
+template <int VEC, int NV, bool NARROW, typename F>
+cudaError_t by_mode(const Team& t, const F& f) {
+  if (NARROW && t.lanes < 32) return f.template run<VEC, NV, NARROW ? PART : WARP>(t);
+  if (t.lanes == 32) return f.template run<VEC, NV, WARP>(t);
+  return f.template run<VEC, NV, WARPS>(t);
+}
+template <int V16, int CH, typename F>
+bool by_team(int C, int vec, const F& f, cudaError_t* e) {
+  constexpr int MOST = CH / V16;  // 2 or 4
+  const bool wide = vec == V16;
+  int nv = 0;
+  const Team t = team_for(C / vec, wide ? MOST : 8, wide, &nv);
+  if (!t.lanes) return false;
+  if (wide) {
+    if (nv == 1) *e = by_mode<V16, 1, true>(t, f);
+    else if (nv == 2) *e = by_mode<V16, 2, false>(t, f);
+    else if constexpr (MOST > 2)
+      *e = nv == 3 ? by_mode<V16, 3, false>(t, f) : by_mode<V16, 4, false>(t, f);
+  } else if (vec == 2) {
+    *e = nv == 2   ? by_mode<2, 2, true>(t, f)
+         : nv == 4 ? by_mode<2, 4, false>(t, f)
+                   : by_mode<2, 8, false>(t, f);
+  } else {
+    *e = nv == 2   ? by_mode<1, 2, true>(t, f)
+         : nv == 4 ? by_mode<1, 4, false>(t, f)
+                   : by_mode<1, 8, false>(t, f);
+  }
+  return true;
 }
 
 // Vector width that every row of these tensors allows: 16 bytes of the larger

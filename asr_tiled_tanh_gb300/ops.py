@@ -19,6 +19,7 @@ when a call is made.
 from __future__ import annotations
 
 import ctypes
+import operator
 
 import torch
 
@@ -367,6 +368,12 @@ class Orthogonalizer(_Op):
         return out
 
 
+# (a list of hundreds of tensors is checked and taken apart for every call: by maps of these)
+_shape_of, _dtype_of = operator.attrgetter("shape"), operator.attrgetter("dtype")
+_is_dense, _index_of, _data_of = map(operator.methodcaller,
+                                     ("is_contiguous", "get_device", "data_ptr"))
+
+
 class _ListOp(_Op):
     """An operator on a list of dense tensors of fixed shapes."""
 
@@ -387,14 +394,17 @@ class _ListOp(_Op):
 
     def _ptrs(self, ts, name, types):
         """Their data pointers, as the C side takes them."""
-        if [t.shape for t in ts] != self._shapes:
+        if list(map(_shape_of, ts)) != self._shapes:
             raise ValueError(f"{name}: {len(self._shapes)} tensors of the plan's shapes are needed")
         index = self._index
-        for i, t in enumerate(ts):
-            if t.dtype is not types[i] or t.get_device() != index or not t.is_contiguous():
-                raise ValueError(f"{name}[{i}]: a dense tensor of {types[i]} on {self.ws.device} "
-                                 f"is needed, got {t.dtype} of strides {t.stride()} on {t.device}")
-        return self._array(*[t.data_ptr() for t in ts])
+        if (list(map(_dtype_of, ts)) != types or not all(map(_is_dense, ts))
+                or any(k != index for k in map(_index_of, ts))):
+            for i, t in enumerate(ts):
+                if t.dtype is not types[i] or t.get_device() != index or not t.is_contiguous():
+                    raise ValueError(f"{name}[{i}]: a dense tensor of {types[i]} on "
+                                     f"{self.ws.device} is needed, got {t.dtype} of strides "
+                                     f"{t.stride()} on {t.device}")
+        return self._array(*map(_data_of, ts))
 
     def _vector(self, n, stream):
         return self._empty(((n,), (1,)), torch.float32, stream)
