@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <atomic>
 #include <new>
+#include <type_traits>
 
 #include "ops.h"
 #include "ptx.cuh"
@@ -10,8 +11,14 @@
 namespace rnnt {
 namespace {
 
-constexpr int UT = 256;       // threads
-constexpr int CHUNK = 8192;   // elements of one tensor that a block takes at a time
+#ifndef UTN
+#define UTN 256
+#endif
+constexpr int UT = UTN;       // threads
+#ifndef CK
+#define CK 8192
+#endif
+constexpr int CHUNK = CK;   // elements of one tensor that a block takes at a time
 constexpr int PARTS = 1024;   // sums of squares that the workspace holds
 // Tensors a launch: its tables are kernel parameters, of which there are 32 KB.
 constexpr int FEW = 32, MANY = 512;
@@ -26,36 +33,58 @@ struct Chunks {
   uint8_t vec[N];    // every tensor of the place is aligned to four elements
 };
 
-// Tensor of chunk k < first[n] (the last one that begins at or before it), and the
-// chunk's elements.
-struct Piece {
-  int i, n;
-  long long at;
-};
+// A block's chunks, every gridDim.x-th, upwards or downwards, and the one at hand.
 template <int N>
-__device__ __forceinline__ Piece piece_of(const Chunks<N>& c, int k) {
-  int lo = 0, hi = c.n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (c.first[mid] <= k) lo = mid;
-    else hi = mid - 1;
+struct Walk {
+  int k, i;      // the chunk, its tensor
+  long long at;  // its first element, and their number
+  int n;
+  __device__ __forceinline__ Walk(const Chunks<N>& c, bool down) {
+    const int all = c.first[c.n];
+    k = down ? all - 1 - (int)blockIdx.x : (int)blockIdx.x;
+    i = down ? c.n - 1 : 0;
+    if (on(c)) find(c);
   }
-  Piece p;
-  p.i = lo;
-  p.at = (long long)(k - c.first[lo]) * CHUNK;
-  p.n = (int)min((long long)CHUNK, c.count[lo] - p.at);
-  return p;
-}
+  __device__ __forceinline__ bool on(const Chunks<N>& c) const {
+    return k >= 0 && k < c.first[c.n];
+  }
+  __device__ __forceinline__ void find(const Chunks<N>& c) {
+    while (k >= c.first[i + 1]) ++i;
+    while (k < c.first[i]) --i;
+    at = (long long)(k - c.first[i]) * CHUNK;
+    n = (int)min((long long)CHUNK, c.count[i] - at);
+  }
+  __device__ __forceinline__ void up(const Chunks<N>& c) {
+    k += gridDim.x;
+    if (on(c)) find(c);
+  }
+  __device__ __forceinline__ void down(const Chunks<N>& c) {
+    k -= gridDim.x;
+    if (on(c)) find(c);
+  }
+};
 
-// Four elements, or one, as they are stored and widened.
-__device__ __forceinline__ float4 widen4(uint2 u) {
-  return make_float4(ptx::bf16lo(u.x), ptx::bf16hi(u.x), ptx::bf16lo(u.y), ptx::bf16hi(u.y));
+// Four elements of a gradient as they are stored.
+template <bool BF16>
+struct Quad {
+  using U = std::conditional_t<BF16, uint2, float4>;
+  static __device__ __forceinline__ U load(const void* g, long long i) {
+    return BF16 ? *(const U*)((const __nv_bfloat16*)g + i) : *(const U*)((const float*)g + i);
+  }
+  static __device__ __forceinline__ float4 widen(const U& u) {
+    if constexpr (BF16)
+      return make_float4(ptx::bf16lo(u.x), ptx::bf16hi(u.x), ptx::bf16lo(u.y), ptx::bf16hi(u.y));
+    else
+      return u;
+  }
+};
+__device__ __forceinline__ uint2 pack4(const float4& q) {
+  return make_uint2(ptx::pack_bf16x2(q.x, q.y), ptx::pack_bf16x2(q.z, q.w));
 }
-__device__ __forceinline__ float4 grad4(const void* g, bool bf16, long long i) {
-  return bf16 ? widen4(*(const uint2*)((const __nv_bfloat16*)g + i)) : *(const float4*)((const float*)g + i);
-}
-__device__ __forceinline__ float grad1(const void* g, bool bf16, long long i) {
-  return bf16 ? __bfloat162float(((const __nv_bfloat16*)g)[i]) : ((const float*)g)[i];
+// One element.
+template <bool BF16>
+__device__ __forceinline__ float grad1(const void* g, long long i) {
+  return BF16 ? __bfloat162float(((const __nv_bfloat16*)g)[i]) : ((const float*)g)[i];
 }
 
 // Sum of v over the block's threads in a fixed order, for thread 0.
@@ -93,6 +122,44 @@ __device__ __forceinline__ double squares(const float (&g)[EACH]) {
   return d;
 }
 
+// The squares of a chunk's n elements from `at` on: a thread's loads all under way
+// before the first is used.
+template <bool BF16>
+__device__ __forceinline__ double chunk_squares(const void* g, long long at, int n, bool vec) {
+  using Q = Quad<BF16>;
+  float v[EACH];
+  if (vec) {
+    typename Q::U u[EACH / 4];
+    const int whole = n & ~3;
+#pragma unroll
+    for (int j = 0; j < EACH / 4; ++j) {
+      const int e = (j * UT + threadIdx.x) * 4;
+      u[j] = typename Q::U{};
+      if (e < whole) u[j] = Q::load(g, at + e);
+    }
+#pragma unroll
+    for (int j = 0; j < EACH / 4; ++j) {
+      const float4 q = Q::widen(u[j]);
+      v[4 * j] = q.x;
+      v[4 * j + 1] = q.y;
+      v[4 * j + 2] = q.z;
+      v[4 * j + 3] = q.w;
+    }
+    double d = squares(v);
+    if (whole + threadIdx.x < n) {  // the tensor's last one to three
+      const double q = grad1<BF16>(g, at + whole + threadIdx.x);
+      d += q * q;
+    }
+    return d;
+  }
+#pragma unroll
+  for (int j = 0; j < EACH; ++j) {
+    const int e = j * UT + threadIdx.x;
+    v[j] = e < n ? grad1<BF16>(g, at + e) : 0.f;
+  }
+  return squares(v);
+}
+
 template <int N>
 struct NormTable {
   Chunks<N> c;
@@ -108,37 +175,11 @@ k_clip_squares(const __grid_constant__ NormTable<N> t, double* __restrict__ part
   ptx::griddep_launch();
   double sum = 0;
 #pragma unroll 1
-  for (int k = blockIdx.x; k < t.c.first[t.c.n]; k += gridDim.x) {
-    const Piece p = piece_of(t.c, k);
-    const bool bf16 = t.c.bf16[p.i];
-    const void* g = t.g[p.i];
-    float v[EACH];
-    if (t.c.vec[p.i]) {
-      const int whole = p.n & ~3;
-#pragma unroll
-      for (int j = 0; j < EACH / 4; ++j) {
-        const int e = (j * UT + threadIdx.x) * 4;
-        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (e < whole) {
-          q = grad4(g, bf16, p.at + e);
-        } else if (e < p.n) {  // the tensor's last one to three
-          q.x = grad1(g, bf16, p.at + e);
-          if (e + 1 < p.n) q.y = grad1(g, bf16, p.at + e + 1);
-          if (e + 2 < p.n) q.z = grad1(g, bf16, p.at + e + 2);
-        }
-        v[4 * j] = q.x;
-        v[4 * j + 1] = q.y;
-        v[4 * j + 2] = q.z;
-        v[4 * j + 3] = q.w;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < EACH; ++j) {
-        const int e = j * UT + threadIdx.x;
-        v[j] = e < p.n ? grad1(g, bf16, p.at + e) : 0.f;
-      }
-    }
-    sum += squares(v);
+  for (Walk<N> w(t.c, false); w.on(t.c); w.up(t.c)) {
+    const void* g = t.g[w.i];
+    const bool vec = t.c.vec[w.i];
+    sum += t.c.bf16[w.i] ? chunk_squares<true>(g, w.at, w.n, vec)
+                         : chunk_squares<false>(g, w.at, w.n, vec);
   }
   sum = block_sum(sum, scr);
   if (threadIdx.x == 0) part[blockIdx.x] = add ? part[blockIdx.x] + sum : sum;
@@ -170,6 +211,37 @@ struct ScaleTable {
   void* into[N];
 };
 
+template <bool BF16>
+__device__ __forceinline__ void scale_chunk(const void* g, void* into, long long at, int n,
+                                            bool vec, float s) {
+  using Q = Quad<BF16>;
+  int done = 0;
+  if (vec) {
+    done = n & ~3;
+    typename Q::U u[EACH / 4];
+#pragma unroll
+    for (int j = 0; j < EACH / 4; ++j) {
+      const int e = (j * UT + threadIdx.x) * 4;
+      if (e < done) u[j] = Q::load(g, at + e);
+    }
+#pragma unroll
+    for (int j = 0; j < EACH / 4; ++j) {
+      const int e = (j * UT + threadIdx.x) * 4;
+      if (e >= done) continue;
+      float4 q = Q::widen(u[j]);
+      q = make_float4(s * q.x, s * q.y, s * q.z, s * q.w);
+      if constexpr (BF16) *(uint2*)((__nv_bfloat16*)into + at + e) = pack4(q);
+      else *(float4*)((float*)into + at + e) = q;
+    }
+  }
+#pragma unroll 8
+  for (int e = done + threadIdx.x; e < n; e += UT) {
+    const float v = s * grad1<BF16>(g, at + e);
+    if constexpr (BF16) ((__nv_bfloat16*)into)[at + e] = __float2bfloat16_rn(v);
+    else ((float*)into)[at + e] = v;
+  }
+}
+
 // (Chunks are taken from the end: the norm's pass left those in L2.)
 template <int N>
 __global__ void __launch_bounds__(UT)
@@ -177,36 +249,29 @@ k_clip_scale(const __grid_constant__ ScaleTable<N> t, const float* clip) {
   ptx::griddep_wait();
   const float s = __ldcg(clip + 1);
 #pragma unroll 1
-  for (int k = t.c.first[t.c.n] - 1 - blockIdx.x; k >= 0; k -= gridDim.x) {
-    const Piece p = piece_of(t.c, k);
-    const bool bf16 = t.c.bf16[p.i];
-    const void* g = t.g[p.i];
-    void* into = t.into[p.i];
+  for (Walk<N> w(t.c, true); w.on(t.c); w.down(t.c)) {
+    const void* g = t.g[w.i];
+    void* into = t.into[w.i];
+    const bool vec = t.c.vec[w.i];
     if (s == 1.f && g == into) continue;
-    int done = 0;
-    if (t.c.vec[p.i]) {
-      done = p.n & ~3;
-#pragma unroll
-      for (int j = 0; j < EACH / 4; ++j) {
-        const int e = (j * UT + threadIdx.x) * 4;
-        if (e >= done) continue;
-        const float4 q = grad4(g, bf16, p.at + e);
-        if (bf16)
-          *(uint2*)((__nv_bfloat16*)into + p.at + e) =
-              make_uint2(ptx::pack_bf16x2(s * q.x, s * q.y), ptx::pack_bf16x2(s * q.z, s * q.w));
-        else
-          *(float4*)((float*)into + p.at + e) = make_float4(s * q.x, s * q.y, s * q.z, s * q.w);
-      }
-    }
-#pragma unroll 8
-    for (int e = done + threadIdx.x; e < p.n; e += UT) {
-      const float v = s * grad1(g, bf16, p.at + e);
-      if (bf16) ((__nv_bfloat16*)into)[p.at + e] = __float2bfloat16_rn(v);
-      else ((float*)into)[p.at + e] = v;
-    }
+    if (t.c.bf16[w.i]) scale_chunk<true>(g, into, w.at, w.n, vec, s);
+    else scale_chunk<false>(g, into, w.at, w.n, vec, s);
   }
 }
 
+#ifndef AD_LD
+#define AD_LD(p) *(p)
+#endif
+#ifndef AD_ST
+#define AD_ST(p,v) *(p) = (v)
+#endif
+#ifndef ADU
+#define ADU 2
+#endif
+constexpr int kAdU = ADU;
+#ifndef AD_B
+#define AD_B 1
+#endif
 // ---- AdamW ------------------------------------------------------------------------
 template <int N>
 struct AdamTable {
@@ -244,9 +309,57 @@ struct AdamStep {
   }
 };
 
+// A chunk's parts of p, m, v and low (or NULL).
+struct Tensors {
+  float *p, *m, *v;
+  __nv_bfloat16* low;
+};
+template <bool BF16>
+__device__ __forceinline__ void adam_chunk(const Tensors& x, const void* g, long long at, int n,
+                                           bool vec, const AdamStep& f) {
+  using Q = Quad<BF16>;
+  int done = 0;
+  if (vec) {
+    done = n & ~3;
+#pragma unroll 1
+    for (int e0 = threadIdx.x * 4; e0 < done; e0 += kAdU * UT * 4) {
+      float4 p[kAdU], m[kAdU], v[kAdU];
+      typename Q::U u[kAdU];
+#pragma unroll
+      for (int j = 0; j < kAdU; ++j) {
+        const int e = e0 + j * UT * 4;
+        if (e >= done) continue;
+        p[j] = AD_LD((const float4*)(x.p + e));
+        m[j] = AD_LD((const float4*)(x.m + e));
+        v[j] = AD_LD((const float4*)(x.v + e));
+        u[j] = Q::load(g, at + e);
+      }
+#pragma unroll
+      for (int j = 0; j < kAdU; ++j) {
+        const int e = e0 + j * UT * 4;
+        if (e >= done) continue;
+        f(p[j], m[j], v[j], Q::widen(u[j]));
+        AD_ST((float4*)(x.p + e), p[j]);
+        AD_ST((float4*)(x.m + e), m[j]);
+        AD_ST((float4*)(x.v + e), v[j]);
+        if (x.low) *(uint2*)(x.low + e) = pack4(p[j]);
+      }
+    }
+  }
+#pragma unroll 4
+  for (int e = done + threadIdx.x; e < n; e += UT) {
+    float p = x.p[e], m = x.m[e], v = x.v[e];
+    f(p, m, v, grad1<BF16>(g, at + e));
+    x.p[e] = p;
+    x.m[e] = m;
+    x.v[e] = v;
+    if (x.low) x.low[e] = __float2bfloat16_rn(p);
+  }
+}
+
 // Bound by DRAM: 28 to 30 bytes an element in 8 streams.
 template <int N>
-__global__ void __launch_bounds__(UT)
+__global__ void __launch_bounds__(UT, AD_B)
 k_adamw(const __grid_constant__ AdamTable<N> t, AdamArgs a) {
   ptx::griddep_wait();
   const int done = __ldcg(a.steps);
@@ -260,40 +373,12 @@ k_adamw(const __grid_constant__ AdamTable<N> t, AdamArgs a) {
     f.r1 = 1.f / -expm1f((float)(done + 1) * a.log1);
     f.r2 = 1.f / -expm1f((float)(done + 1) * a.log2);
 #pragma unroll 1
-    for (int k = t.c.first[t.c.n] - 1 - blockIdx.x; k >= 0; k -= gridDim.x) {
-      const Piece c = piece_of(t.c, k);
-      const bool bf16 = t.c.bf16[c.i];
-      const void* g = t.g[c.i];
-      float *p = t.p[c.i] + c.at, *m = t.m[c.i] + c.at, *v = t.v[c.i] + c.at;
-      __nv_bfloat16* low = t.low[c.i];
-      if (low) low += c.at;
-      f.decay = t.decay[c.i];
-      int vec = 0;
-      if (t.c.vec[c.i]) {
-        vec = c.n & ~3;
-#pragma unroll 2
-        for (int e = threadIdx.x * 4; e < vec; e += UT * 4) {
-          const float4 gq = grad4(g, bf16, c.at + e);
-          float4 pq = *(const float4*)(p + e), mq = *(const float4*)(m + e),
-                 vq = *(const float4*)(v + e);
-          f(pq, mq, vq, gq);
-          *(float4*)(p + e) = pq;
-          *(float4*)(m + e) = mq;
-          *(float4*)(v + e) = vq;
-          if (low)
-            *(uint2*)(low + e) =
-                make_uint2(ptx::pack_bf16x2(pq.x, pq.y), ptx::pack_bf16x2(pq.z, pq.w));
-        }
-      }
-#pragma unroll 2
-      for (int e = vec + threadIdx.x; e < c.n; e += UT) {
-        float pe = p[e], me = m[e], ve = v[e];
-        f(pe, me, ve, grad1(g, bf16, c.at + e));
-        p[e] = pe;
-        m[e] = me;
-        v[e] = ve;
-        if (low) low[e] = __float2bfloat16_rn(pe);
-      }
+    for (Walk<N> w(t.c, true); w.on(t.c); w.down(t.c)) {
+      const Tensors x{t.p[w.i] + w.at, t.m[w.i] + w.at, t.v[w.i] + w.at,
+                      t.low[w.i] ? t.low[w.i] + w.at : nullptr};
+      f.decay = t.decay[w.i];
+      if (t.c.bf16[w.i]) adam_chunk<true>(x, t.g[w.i], w.at, w.n, t.c.vec[w.i], f);
+      else adam_chunk<false>(x, t.g[w.i], w.at, w.n, t.c.vec[w.i], f);
     }
   }
   // The last block to come here counts the update, when every block has read the

@@ -3,6 +3,7 @@
 Addresses are fake and never dereferenced.
 """
 import ctypes
+import operator
 
 import pytest
 import torch
@@ -208,6 +209,9 @@ def _plans(monkeypatch, current=0):
         setattr(plan, name, lambda *a: calls.append(a) or 0)
     monkeypatch.setattr(ops, "_raw_stream", lambda i: 0)
     monkeypatch.setattr(ops, "_current_device", lambda: current)
+    for name, method in (("_is_dense", "is_contiguous"), ("_index_of", "get_device"),
+                         ("_data_of", "data_ptr")):
+        monkeypatch.setattr(ops, name, operator.methodcaller(method))
     return c, o, calls
 
 
