@@ -1,4 +1,5 @@
-"""Build librnnt_gb300.so in-tree for sm_103a (nvcc, one -gencode, parallel TUs)."""
+"""Build librnnt_gb300.so in-tree for sm_103a (nvcc, one -gencode, parallel TUs), and beside it
+the binding's helper for lists of tensors (g++, torch's headers)."""
 from __future__ import annotations
 
 import glob
@@ -6,12 +7,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(BUILD, "librnnt_gb300.so")
+LISTS = os.path.join(BUILD, "rnnt_lists.so")
+LISTS_SRC = os.path.join(CSRC, "lists.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I", INCLUDE]
@@ -40,8 +44,54 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+_lists_tried = False
+
+
+def _start_lists(force: bool):
+    """The compiler of the helper at work on it; None where it is up to date, or cannot be built
+    (ops.py then takes lists apart in Python)."""
+    global _lists_tried
+    fresh = os.path.exists(LISTS) and os.path.getmtime(LISTS) >= os.path.getmtime(LISTS_SRC)
+    if (fresh or _lists_tried) and not force:
+        return None
+    _lists_tried = True
+    import torch
+    t = os.path.dirname(torch.__file__)
+    lib = os.path.join(t, "lib")
+    tmp = LISTS + f".{os.getpid()}.tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(t, "include"),
+           "-I", os.path.join(t, "include", "torch", "csrc", "api", "include"), LISTS_SRC, "-o",
+           tmp, "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+    os.makedirs(BUILD, exist_ok=True)
+    try:
+        return tmp, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    except OSError as e:
+        print(f"{LISTS_SRC}: not built ({e})", file=sys.stderr)
+        return None
+
+
+def _finish_lists(job):
+    if job is None:
+        return
+    tmp, p = job
+    out, _ = p.communicate()
+    if p.returncode == 0:
+        os.replace(tmp, LISTS)
+    else:
+        print(f"{LISTS_SRC}: not built\n{out.decode(errors='replace')}", file=sys.stderr)
+
+
 def build_library(force: bool = False, verbose: bool = False) -> str:
     """Compile every csrc/*.cu for sm_103a and link the shared library."""
+    lists = _start_lists(force)
+    try:
+        return _build_library(force, verbose)
+    finally:
+        _finish_lists(lists)
+
+
+def _build_library(force, verbose):
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -5,9 +5,6 @@
 namespace rnnt {
 namespace {
 using namespace ln;
-#ifndef FWD_CH
-#define FWD_CH 16
-#endif
 #ifndef FWD_B
 #define FWD_B 2
 #endif
@@ -15,44 +12,39 @@ using namespace ln;
 template <typename TX, typename TY, int VEC, int NV, int MODE>
 __global__ void __launch_bounds__(MODE == WARPS ? MAX_THREADS : 256, MODE == WARPS ? 1 : FWD_B)
 k_ln_fwd(LnArgs a, Team t, const TX* __restrict__ x, TY* __restrict__ y) {
-  using R = Ring<VEC, NV, TX>;
-  constexpr int NP = kPairs(VEC);
+  constexpr int NP = kPairs(VEC), S = kCopied<VEC, TX> ? STAGES : 1;
+  using R = Ring<VEC, NV, S, TX>;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float scr[2][MAX_THREADS / 32][1];
   const Place p = place_of<MODE>(t);
   const bool al16 = (((uintptr_t)a.gamma | (uintptr_t)a.beta) & 15) == 0;
+  const Cols<VEC> cols{p.lane, t.lanes, a.C};
   const Stride by(a, p.step);
   // the row to copy next, and the row at hand
   Walk next(a, p.first), row = next;
   Offset xo(a, next, by, a.xf, a.xb), yo(a, row, by, a.yf, a.yb);
-  Offset xr = xo;  // (of rows that are not copied ahead)
   R ring;
   ring.init(smem);
   unsigned lives = 0;  // bit s: the row s turns from now exists
   int length = ask_length(a, next);
   auto ahead = [&](int stage) {
     const bool live = exists(a, next, length, p.lane == 0);
-    if (live) ring.fetch(stage, x + xo.at, t, p);
+    if (live) ring.fetch(stage, x + xo.at, cols);
     copy_commit();
-    lives |= (unsigned)live << (STAGES - 1);
+    lives |= (unsigned)live << (S - 1);
     advance(a, by, next, xo);
     length = ask_length(a, next);
   };
 #pragma unroll
-  for (int s = 0; s < STAGES; ++s) {
+  for (int s = 0; s < S; ++s) {
     lives >>= 1;
     ahead(s);
   }
   Vals<VEC> gamma[NV], beta[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int k = p.lane + j * t.lanes;
-    gamma[j].fill(0.f);
-    beta[j].fill(0.f);
-    if (k < t.nvec) {
-      gamma[j] = param<VEC>(a.gamma, k * VEC, 1.f, al16);
-      beta[j] = param<VEC>(a.beta, k * VEC, 0.f, al16);
-    }
+    gamma[j] = cols.param(a.gamma, j, 1.f, al16);
+    beta[j] = cols.param(a.beta, j, 0.f, al16);
   }
   const float C = (float)a.C;
   int stage = 0;
@@ -62,21 +54,18 @@ k_ln_fwd(LnArgs a, Team t, const TX* __restrict__ x, TY* __restrict__ y) {
     const int r = row.b * a.T + row.t;
     TY* to = y + yo.at;
     typename R::U u[NV];
-    copy_wait<STAGES - 1>();
-    ring.read(u, stage, x + xr.at, live, t, p);
+    copy_wait<S - 1>();
+    ring.read(u, stage);
     lives >>= 1;
     ahead(stage);
-    stage = stage + 1 == STAGES ? 0 : stage + 1;
-    if constexpr (R::kAhead) advance(a, by, row, yo);
-    else advance(a, by, row, yo, xr);
+    stage = stage + 1 == S ? 0 : stage + 1;
+    advance(a, by, row, yo);
     if (MODE == PART ? !__any_sync(0xffffffffu, live) : !live) {
       Vals<VEC> z;
       z.fill(0.f);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int k = p.lane + j * t.lanes;
-        if (here && k < t.nvec) store<VEC, TY>(to + k * VEC, z);
-      }
+      for (int j = 0; j < NV; ++j)
+        if (here) cols.store(to, j, z);
       continue;
     }
     // the mean, then the squares about it
@@ -98,16 +87,16 @@ k_ln_fwd(LnArgs a, Team t, const TX* __restrict__ x, TY* __restrict__ y) {
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         v[j].p[i] = __fadd2_rn(v[j].p[i], make_float2(-mean, -mean));
-        if (p.lane + j * t.lanes < t.nvec) s2 = __ffma2_rn(v[j].p[i], v[j].p[i], s2);
+        if (VEC == 1 && !cols.both(j)) v[j].p[i].y = 0.f;
+        if (cols.has(j)) s2 = __ffma2_rn(v[j].p[i], v[j].p[i], s2);
       }
     }
-    s[0] = VEC == 1 ? s2.x : s2.x + s2.y;
+    s[0] = s2.x + s2.y;
     team_sum<MODE>(s, t, p, scr[1]);
     const float rstd = rsqrtf(fmaf(s[0], a.rC, a.eps));
     if (a.stats && live && p.lane == 0) a.stats[r] = make_float2(mean, rstd);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int k = p.lane + j * t.lanes;
       Vals<VEC> o;
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
@@ -115,7 +104,7 @@ k_ln_fwd(LnArgs a, Team t, const TX* __restrict__ x, TY* __restrict__ y) {
                             beta[j].p[i]);
         if (MODE == PART && !live) o.p[i] = make_float2(0.f, 0.f);
       }
-      if (here && k < t.nvec) store<VEC, TY>(to + k * VEC, o);
+      if (here) cols.store(to, j, o);
     }
   }
   copy_wait<0>();
@@ -206,7 +195,7 @@ struct Fwd {
     static Known known;
     const auto k = k_ln_fwd<TX, TY, VEC, NV, MODE>;
     const int threads = t.lanes * t.teams;
-    const size_t smem = Ring<VEC, NV, TX>::bytes(threads);
+    const size_t smem = Ring<VEC, NV, STAGES, TX>::bytes(threads);
     int per = 0;
     const cudaError_t e = blocks_per_sm(k, &known, threads, smem, &per);
     if (e != cudaSuccess) return e;
@@ -221,7 +210,7 @@ cudaError_t ln_fwd(const LnArgs& a, const void* x, void* y, cudaStream_t st) {
   constexpr int V16 = 16 / (int)std::max(sizeof(TX), sizeof(TY));
   const int vec = vec_of(a, sizeof(TX), x, nullptr, sizeof(TY), y);
   cudaError_t e;
-  if (by_team<V16, (V16 == 8 ? FWD_CH : 16)>(a.C, vec, Fwd<TX, TY>{a, x, y, st}, &e)) return e;
+  if (by_team<V16, 16, 8>(a.C, vec, Fwd<TX, TY>{a, x, y, st}, &e)) return e;
   const int grid = std::min(a.rows, 8 * num_sms());
   k_ln_fwd_wide<TX, TY><<<grid, WT, 0, st>>>(a, (const TX*)x, (TY*)y);
   return cudaGetLastError();

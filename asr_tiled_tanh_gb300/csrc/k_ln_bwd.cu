@@ -13,17 +13,18 @@ template <typename TX, typename TY, int VEC, int NV, int MODE>
 __global__ void __launch_bounds__(MODE == WARPS ? MAX_THREADS : 256, MODE == WARPS ? 1 : BWD_B)
 k_ln_bwd(LnArgs a, Team t, const TX* __restrict__ x, const TY* __restrict__ dy,
          TX* __restrict__ dx, float2* __restrict__ part) {
-  using RX = Ring<VEC, NV, TX>;
-  using RY = Ring<VEC, NV, TY>;
-  constexpr int NP = kPairs(VEC);
+  constexpr int NP = kPairs(VEC), S = kCopied<VEC, TX> && kCopied<VEC, TY> ? STAGES : 1;
+  using RX = Ring<VEC, NV, S, TX>;
+  using RY = Ring<VEC, NV, S, TY>;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float scr[2][MAX_THREADS / 32][2];
   ptx::griddep_launch();
   const Place p = place_of<MODE>(t);
   const bool al16 = ((uintptr_t)a.gamma & 15) == 0;
+  const Cols<VEC> cols{p.lane, t.lanes, a.C};
   const Stride by(a, p.step);
   Walk next(a, p.first), row = next;
-  Offset xo(a, next, by, a.xf, a.xb), yo(a, next, by, a.yf, a.yb), xr = xo, yr = yo;
+  Offset xo(a, next, by, a.xf, a.xb), yo(a, next, by, a.yf, a.yb), xr = xo;
   RX rx;
   RY ry;
   rx.init(smem);
@@ -33,16 +34,16 @@ k_ln_bwd(LnArgs a, Team t, const TX* __restrict__ x, const TY* __restrict__ dy,
   auto ahead = [&](int stage) {
     const bool live = exists(a, next, length, p.lane == 0);
     if (live) {
-      rx.fetch(stage, x + xo.at, t, p);
-      ry.fetch(stage, dy + yo.at, t, p);
+      rx.fetch(stage, x + xo.at, cols);
+      ry.fetch(stage, dy + yo.at, cols);
     }
     copy_commit();
-    lives |= (unsigned)live << (STAGES - 1);
+    lives |= (unsigned)live << (S - 1);
     advance(a, by, next, xo, yo);
     length = ask_length(a, next);
   };
 #pragma unroll
-  for (int s = 0; s < STAGES; ++s) {
+  for (int s = 0; s < S; ++s) {
     lives >>= 1;
     ahead(s);
   }
@@ -53,9 +54,7 @@ k_ln_bwd(LnArgs a, Team t, const TX* __restrict__ x, const TY* __restrict__ dy,
   Vals<VEC> gamma[NV], dg[NV], db[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int k = p.lane + j * t.lanes;
-    gamma[j].fill(0.f);
-    if (k < t.nvec) gamma[j] = param<VEC>(a.gamma, k * VEC, 1.f, al16);
+    gamma[j] = cols.param(a.gamma, j, 1.f, al16);
     dg[j].fill(0.f);
     db[j].fill(0.f);
   }
@@ -66,24 +65,21 @@ k_ln_bwd(LnArgs a, Team t, const TX* __restrict__ x, const TY* __restrict__ dy,
     TX* to = dx + xr.at;
     typename RX::U ux[NV];
     typename RY::U uy[NV];
-    copy_wait<STAGES - 1>();
-    rx.read(ux, stage, x + xr.at, live, t, p);
-    ry.read(uy, stage, dy + yr.at, live, t, p);
+    copy_wait<S - 1>();
+    rx.read(ux, stage);
+    ry.read(uy, stage);
     lives >>= 1;
     ahead(stage);
-    stage = stage + 1 == STAGES ? 0 : stage + 1;
-    if constexpr (RY::kAhead) advance(a, by, row, xr);
-    else advance(a, by, row, xr, yr);
+    stage = stage + 1 == S ? 0 : stage + 1;
+    advance(a, by, row, xr);
     const float2 st = coming;
     coming = ask_stats();
     if (MODE == PART ? !__any_sync(0xffffffffu, live) : !live) {
       Vals<VEC> z;
       z.fill(0.f);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int k = p.lane + j * t.lanes;
-        if (here && k < t.nvec) store<VEC, TX>(to + k * VEC, z);
-      }
+      for (int j = 0; j < NV; ++j)
+        if (here) cols.store(to, j, z);
       continue;
     }
     // (of vectors past the row's end dy is 0)
@@ -112,44 +108,43 @@ k_ln_bwd(LnArgs a, Team t, const TX* __restrict__ x, const TY* __restrict__ dy,
     const float k1 = -s[0] * a.rC * st.y, k2 = -s[1] * a.rC * st.y;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int k = p.lane + j * t.lanes;
       Vals<VEC> o;
 #pragma unroll
       for (int i = 0; i < NP; ++i)
         o.p[i] = __ffma2_rn(g[j].p[i], make_float2(st.y, st.y),
                             __ffma2_rn(xh[j].p[i], make_float2(k2, k2), make_float2(k1, k1)));
-      if (here && k < t.nvec) store<VEC, TX>(to + k * VEC, o);
+      if (here) cols.store(to, j, o);
     }
   }
   copy_wait<0>();
   if (!part) return;
   // the block's sums: the teams' in order (of a warp's narrow teams by shuffles first)
+  constexpr int CH = 2 * NP;  // channels of a unit
   const int groups = MODE == WARPS ? t.teams : (int)blockDim.x >> 5;
-  const int cols = t.lanes * VEC, group = MODE == WARPS ? p.team : (int)threadIdx.x >> 5;
-  float2* sums = (float2*)smem;  // [group][cols]
+  const int n = t.lanes * CH, group = MODE == WARPS ? p.team : (int)threadIdx.x >> 5;
+  float2* sums = (float2*)smem;  // [group][channel of the lanes' units][lane]
   float2* out = part + (long long)blockIdx.x * a.C;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
+    for (int i = 0; i < CH; ++i) {
       float2 v = make_float2(i & 1 ? dg[j].p[i / 2].y : dg[j].p[i / 2].x,
                              i & 1 ? db[j].p[i / 2].y : db[j].p[i / 2].x);
       for (int d = 16; MODE == PART && d >= t.lanes; d >>= 1) {
         v.x += __shfl_xor_sync(0xffffffffu, v.x, d);
         v.y += __shfl_xor_sync(0xffffffffu, v.y, d);
       }
-      // (lanes next to each other, so that their stores do not meet in a bank)
-      sums[group * cols + i * t.lanes + p.lane] = v;
+      sums[group * n + i * t.lanes + p.lane] = v;
     }
     __syncthreads();
-    for (int c = threadIdx.x; c < cols; c += blockDim.x) {
-      const int lane = c / VEC, at = (c - lane * VEC) * t.lanes + lane;
-      const int col = j * cols + c;
-      if (col >= a.C) continue;
+    for (int c = threadIdx.x; c < n; c += blockDim.x) {
+      // (channels that are apart lie here as in the row)
+      const int lane = VEC == 1 ? 0 : c / CH, at = VEC == 1 ? c : (c - lane * CH) * t.lanes + lane;
+      if (j * n + c >= a.C) continue;
       float2 v = sums[at];
-      for (int k = 1; k < groups; ++k) v = __fadd2_rn(v, sums[k * cols + at]);
-      out[col] = v;
+      for (int k = 1; k < groups; ++k) v = __fadd2_rn(v, sums[k * n + at]);
+      out[j * n + c] = v;
     }
   }
 }
@@ -254,9 +249,9 @@ struct Bwd {
     static Known known;
     const auto k = k_ln_bwd<TX, TY, VEC, NV, MODE>;
     const int threads = t.lanes * t.teams;
-    const size_t sums = sizeof(float2) * VEC * threads;
-    const size_t smem =
-        std::max(sums, Ring<VEC, NV, TX>::bytes(threads) + Ring<VEC, NV, TY>::bytes(threads));
+    const size_t sums = sizeof(float2) * 2 * kPairs(VEC) * threads;
+    const size_t smem = std::max(sums, Ring<VEC, NV, STAGES, TX>::bytes(threads) +
+                                           Ring<VEC, NV, STAGES, TY>::bytes(threads));
     int per = 0;
     const cudaError_t e = blocks_per_sm(k, &known, threads, smem, &per);
     if (e != cudaSuccess) return e;
@@ -275,7 +270,7 @@ cudaError_t ln_bwd(const LnArgs& a, const void* x, const void* dy, void* dx, flo
   const int vec = vec_of(a, sizeof(TX), x, dx, sizeof(TY), dy);
   cudaError_t e;
   // (16 channels a lane: their sums stay in registers)
-  if (by_team<V16, 16>(a.C, vec, Bwd<TX, TY>{a, x, dy, dx, part, part_rows, st}, &e)) return e;
+  if (by_team<V16, 16, 6>(a.C, vec, Bwd<TX, TY>{a, x, dy, dx, part, part_rows, st}, &e)) return e;
   const int grid = std::min(a.rows, 8 * num_sms());
   k_ln_bwd_wide<TX, TY><<<grid, WT, 0, st>>>(a, (const TX*)x, (const TY*)dy, (TX*)dx);
   e = cudaGetLastError();

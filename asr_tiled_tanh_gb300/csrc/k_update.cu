@@ -11,14 +11,8 @@
 namespace rnnt {
 namespace {
 
-#ifndef UTN
-#define UTN 256
-#endif
-constexpr int UT = UTN;       // threads
-#ifndef CK
-#define CK 8192
-#endif
-constexpr int CHUNK = CK;   // elements of one tensor that a block takes at a time
+constexpr int UT = 256;       // threads
+constexpr int CHUNK = 8192;   // elements of one tensor that a block takes at a time
 constexpr int PARTS = 1024;   // sums of squares that the workspace holds
 // Tensors a launch: its tables are kernel parameters, of which there are 32 KB.
 constexpr int FEW = 32, MANY = 512;
@@ -33,16 +27,14 @@ struct Chunks {
   uint8_t vec[N];    // every tensor of the place is aligned to four elements
 };
 
-// A block's chunks, every gridDim.x-th, upwards or downwards, and the one at hand.
+// Chunks first, first + step, ... (step < 0: downwards) and the one at hand.
 template <int N>
 struct Walk {
-  int k, i;      // the chunk, its tensor
-  long long at;  // its first element, and their number
+  int k, step, i;  // the chunk, its tensor
+  long long at;    // its first element, and their number
   int n;
-  __device__ __forceinline__ Walk(const Chunks<N>& c, bool down) {
-    const int all = c.first[c.n];
-    k = down ? all - 1 - (int)blockIdx.x : (int)blockIdx.x;
-    i = down ? c.n - 1 : 0;
+  __device__ __forceinline__ Walk(const Chunks<N>& c, int first, int step_)
+      : k(first), step(step_), i(step_ < 0 ? c.n - 1 : 0) {
     if (on(c)) find(c);
   }
   __device__ __forceinline__ bool on(const Chunks<N>& c) const {
@@ -54,15 +46,16 @@ struct Walk {
     at = (long long)(k - c.first[i]) * CHUNK;
     n = (int)min((long long)CHUNK, c.count[i] - at);
   }
-  __device__ __forceinline__ void up(const Chunks<N>& c) {
-    k += gridDim.x;
-    if (on(c)) find(c);
-  }
-  __device__ __forceinline__ void down(const Chunks<N>& c) {
-    k -= gridDim.x;
+  __device__ __forceinline__ void next(const Chunks<N>& c) {
+    k += step;
     if (on(c)) find(c);
   }
 };
+// The block's, from the last on: an earlier pass left those in L2.
+template <int N>
+__device__ __forceinline__ Walk<N> backwards(const Chunks<N>& c) {
+  return Walk<N>(c, c.first[c.n] - 1 - (int)blockIdx.x, -(int)gridDim.x);
+}
 
 // Four elements of a gradient as they are stored.
 template <bool BF16>
@@ -87,14 +80,18 @@ __device__ __forceinline__ float grad1(const void* g, long long i) {
   return BF16 ? __bfloat162float(((const __nv_bfloat16*)g)[i]) : ((const float*)g)[i];
 }
 
-// Sum of v over the block's threads in a fixed order, for thread 0.
+// Sum of v over the block's threads in a fixed order, for the first warp's.
+template <int THREADS>
 __device__ __forceinline__ double block_sum(double v, double* scr) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
   if ((threadIdx.x & 31) == 0) scr[threadIdx.x >> 5] = v;
   __syncthreads();
-  if (threadIdx.x == 0)
-    for (int k = 1; k < UT / 32; ++k) v += scr[k];
+  if (threadIdx.x < 32) {
+    v = threadIdx.x < THREADS / 32 ? scr[threadIdx.x] : 0.;
+#pragma unroll
+    for (int d = THREADS / 64; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  }
   return v;
 }
 
@@ -125,7 +122,8 @@ __device__ __forceinline__ double squares(const float (&g)[EACH]) {
 // The squares of a chunk's n elements from `at` on: a thread's loads all under way
 // before the first is used.
 template <bool BF16>
-__device__ __forceinline__ double chunk_squares(const void* g, long long at, int n, bool vec) {
+__device__ __forceinline__ double chunk_squares(const void* g, long long at, int n, bool vec,
+                                                int tid) {
   using Q = Quad<BF16>;
   float v[EACH];
   if (vec) {
@@ -133,7 +131,7 @@ __device__ __forceinline__ double chunk_squares(const void* g, long long at, int
     const int whole = n & ~3;
 #pragma unroll
     for (int j = 0; j < EACH / 4; ++j) {
-      const int e = (j * UT + threadIdx.x) * 4;
+      const int e = (j * UT + tid) * 4;
       u[j] = typename Q::U{};
       if (e < whole) u[j] = Q::load(g, at + e);
     }
@@ -146,18 +144,28 @@ __device__ __forceinline__ double chunk_squares(const void* g, long long at, int
       v[4 * j + 3] = q.w;
     }
     double d = squares(v);
-    if (whole + threadIdx.x < n) {  // the tensor's last one to three
-      const double q = grad1<BF16>(g, at + whole + threadIdx.x);
+    if (whole + tid < n) {  // the tensor's last one to three
+      const double q = grad1<BF16>(g, at + whole + tid);
       d += q * q;
     }
     return d;
   }
 #pragma unroll
   for (int j = 0; j < EACH; ++j) {
-    const int e = j * UT + threadIdx.x;
+    const int e = j * UT + tid;
     v[j] = e < n ? grad1<BF16>(g, at + e) : 0.f;
   }
   return squares(v);
+}
+
+__device__ __forceinline__ float2 norm_and_scale(double sum, float max_norm, float eps) {
+  // (a root and a quotient in fp64 cost 0.7 us where a thread waits for them alone)
+  if (sum >= 0x1p-100 && sum <= 0x1p100) {
+    const float norm = sqrtf((float)sum), q = max_norm / (norm + eps);
+    return make_float2(norm, q >= 1.f ? 1.f : q);
+  }
+  const double norm = sqrt(sum), q = (double)max_norm / (norm + (double)eps);
+  return make_float2((float)norm, q >= 1 ? 1.f : (float)q);  // (NaN stays)
 }
 
 template <int N>
@@ -175,13 +183,13 @@ k_clip_squares(const __grid_constant__ NormTable<N> t, double* __restrict__ part
   ptx::griddep_launch();
   double sum = 0;
 #pragma unroll 1
-  for (Walk<N> w(t.c, false); w.on(t.c); w.up(t.c)) {
+  for (Walk<N> w(t.c, blockIdx.x, gridDim.x); w.on(t.c); w.next(t.c)) {
     const void* g = t.g[w.i];
     const bool vec = t.c.vec[w.i];
-    sum += t.c.bf16[w.i] ? chunk_squares<true>(g, w.at, w.n, vec)
-                         : chunk_squares<false>(g, w.at, w.n, vec);
+    sum += t.c.bf16[w.i] ? chunk_squares<true>(g, w.at, w.n, vec, threadIdx.x)
+                         : chunk_squares<false>(g, w.at, w.n, vec, threadIdx.x);
   }
-  sum = block_sum(sum, scr);
+  sum = block_sum<UT>(sum, scr);
   if (threadIdx.x == 0) part[blockIdx.x] = add ? part[blockIdx.x] + sum : sum;
 }
 
@@ -195,11 +203,11 @@ k_clip_norm(const double* __restrict__ part, int n, float max_norm, float eps,
 #pragma unroll
   for (int k = 0; k < PARTS / UT; ++k)
     if (threadIdx.x + k * UT < n) sum += __ldcg(part + threadIdx.x + k * UT);
-  sum = block_sum(sum, scr);
+  sum = block_sum<UT>(sum, scr);
   if (threadIdx.x == 0) {
-    const double norm = sqrt(sum), q = (double)max_norm / (norm + (double)eps);
-    clip[0] = (float)norm;
-    clip[1] = q >= 1 ? 1.f : (float)q;  // (NaN stays)
+    const float2 c = norm_and_scale(sum, max_norm, eps);
+    clip[0] = c.x;
+    clip[1] = c.y;
   }
 }
 
@@ -213,7 +221,7 @@ struct ScaleTable {
 
 template <bool BF16>
 __device__ __forceinline__ void scale_chunk(const void* g, void* into, long long at, int n,
-                                            bool vec, float s) {
+                                            bool vec, float s, int tid) {
   using Q = Quad<BF16>;
   int done = 0;
   if (vec) {
@@ -221,12 +229,12 @@ __device__ __forceinline__ void scale_chunk(const void* g, void* into, long long
     typename Q::U u[EACH / 4];
 #pragma unroll
     for (int j = 0; j < EACH / 4; ++j) {
-      const int e = (j * UT + threadIdx.x) * 4;
+      const int e = (j * UT + tid) * 4;
       if (e < done) u[j] = Q::load(g, at + e);
     }
 #pragma unroll
     for (int j = 0; j < EACH / 4; ++j) {
-      const int e = (j * UT + threadIdx.x) * 4;
+      const int e = (j * UT + tid) * 4;
       if (e >= done) continue;
       float4 q = Q::widen(u[j]);
       q = make_float4(s * q.x, s * q.y, s * q.z, s * q.w);
@@ -235,43 +243,98 @@ __device__ __forceinline__ void scale_chunk(const void* g, void* into, long long
     }
   }
 #pragma unroll 8
-  for (int e = done + threadIdx.x; e < n; e += UT) {
+  for (int e = done + tid; e < n; e += UT) {
     const float v = s * grad1<BF16>(g, at + e);
     if constexpr (BF16) ((__nv_bfloat16*)into)[at + e] = __float2bfloat16_rn(v);
     else ((float*)into)[at + e] = v;
   }
 }
 
-// (Chunks are taken from the end: the norm's pass left those in L2.)
 template <int N>
 __global__ void __launch_bounds__(UT)
 k_clip_scale(const __grid_constant__ ScaleTable<N> t, const float* clip) {
   ptx::griddep_wait();
   const float s = __ldcg(clip + 1);
 #pragma unroll 1
-  for (Walk<N> w(t.c, true); w.on(t.c); w.down(t.c)) {
+  for (Walk<N> w = backwards(t.c); w.on(t.c); w.next(t.c)) {
     const void* g = t.g[w.i];
     void* into = t.into[w.i];
     const bool vec = t.c.vec[w.i];
     if (s == 1.f && g == into) continue;
-    if (t.c.bf16[w.i]) scale_chunk<true>(g, into, w.at, w.n, vec, s);
-    else scale_chunk<false>(g, into, w.at, w.n, vec, s);
+    if (t.c.bf16[w.i]) scale_chunk<true>(g, into, w.at, w.n, vec, s, threadIdx.x);
+    else scale_chunk<false>(g, into, w.at, w.n, vec, s, threadIdx.x);
   }
 }
 
-#ifndef AD_LD
-#define AD_LD(p) *(p)
-#endif
-#ifndef AD_ST
-#define AD_ST(p,v) *(p) = (v)
-#endif
-#ifndef ADU
-#define ADU 2
-#endif
-constexpr int kAdU = ADU;
-#ifndef AD_B
-#define AD_B 1
-#endif
+// ---- short lists --------------------------------------------------------------------
+// Norm and scaling in one launch of one cluster: its blocks add up each other's sums
+// in shared memory.  A launch costs the host 2.4 us and the GPU about 2, which is
+// most of what few elements cost.
+constexpr int CBLOCKS = 16, CGROUPS = 2;  // blocks at most, and their groups of UT threads
+
+// value at the same shared address of another block of the cluster
+__device__ __forceinline__ double peer_f64(const double* mine, int rank) {
+  uint32_t at;
+  double v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(at) : "r"(ptx::smem_u32(mine)), "r"(rank));
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+
+// (into[0] NULL: the norm alone)
+template <int N>
+__global__ void __launch_bounds__(UT * CGROUPS)
+k_clip_short(const __grid_constant__ ScaleTable<N> t, float max_norm, float eps,
+             float* __restrict__ clip) {
+  __shared__ double scr[UT * CGROUPS / 32], mine;
+  __shared__ float scale_s;
+  ptx::griddep_launch();
+  const int tid = threadIdx.x & (UT - 1), group = threadIdx.x / UT;
+  const int first = blockIdx.x * CGROUPS + group, step = gridDim.x * CGROUPS;
+  double sum = 0;
+#pragma unroll 1
+  for (Walk<N> w(t.c, first, step); w.on(t.c); w.next(t.c)) {
+    const void* g = t.g[w.i];
+    const bool vec = t.c.vec[w.i];
+    sum += t.c.bf16[w.i] ? chunk_squares<true>(g, w.at, w.n, vec, tid)
+                         : chunk_squares<false>(g, w.at, w.n, vec, tid);
+  }
+  sum = block_sum<UT * CGROUPS>(sum, scr);
+  if (threadIdx.x == 0) mine = sum;
+  cluster_sync();
+  if (threadIdx.x < 32) {
+    sum = threadIdx.x < gridDim.x ? peer_f64(&mine, threadIdx.x) : 0.;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (threadIdx.x == 0) {
+      const float2 c = norm_and_scale(sum, max_norm, eps);
+      scale_s = c.y;
+      if (blockIdx.x == 0) {
+        clip[0] = c.x;
+        clip[1] = c.y;
+      }
+    }
+  }
+  cluster_sync();  // (and no block leaves while its sum is read)
+  if (!t.into[0]) return;
+  const float s = scale_s;
+#pragma unroll 1
+  for (Walk<N> w(t.c, first, step); w.on(t.c); w.next(t.c)) {
+    const void* g = t.g[w.i];
+    void* into = t.into[w.i];
+    const bool vec = t.c.vec[w.i];
+    if (s == 1.f && g == into) continue;
+    if (t.c.bf16[w.i]) scale_chunk<true>(g, into, w.at, w.n, vec, s, tid);
+    else scale_chunk<false>(g, into, w.at, w.n, vec, s, tid);
+  }
+}
+
 // ---- AdamW ------------------------------------------------------------------------
 template <int N>
 struct AdamTable {
@@ -309,6 +372,10 @@ struct AdamStep {
   }
 };
 
+// Quads of each tensor that a thread has under way (336M elements: 1,764 us with the
+// norm for one, 1,715 for two, 1,895 for four, which leave one block an SM less).
+constexpr int AHEAD = 2;
+
 // A chunk's parts of p, m, v and low (or NULL).
 struct Tensors {
   float *p, *m, *v;
@@ -322,26 +389,26 @@ __device__ __forceinline__ void adam_chunk(const Tensors& x, const void* g, long
   if (vec) {
     done = n & ~3;
 #pragma unroll 1
-    for (int e0 = threadIdx.x * 4; e0 < done; e0 += kAdU * UT * 4) {
-      float4 p[kAdU], m[kAdU], v[kAdU];
-      typename Q::U u[kAdU];
+    for (int e0 = threadIdx.x * 4; e0 < done; e0 += AHEAD * UT * 4) {
+      float4 p[AHEAD], m[AHEAD], v[AHEAD];
+      typename Q::U u[AHEAD];
 #pragma unroll
-      for (int j = 0; j < kAdU; ++j) {
+      for (int j = 0; j < AHEAD; ++j) {
         const int e = e0 + j * UT * 4;
         if (e >= done) continue;
-        p[j] = AD_LD((const float4*)(x.p + e));
-        m[j] = AD_LD((const float4*)(x.m + e));
-        v[j] = AD_LD((const float4*)(x.v + e));
+        p[j] = *(const float4*)(x.p + e);
+        m[j] = *(const float4*)(x.m + e);
+        v[j] = *(const float4*)(x.v + e);
         u[j] = Q::load(g, at + e);
       }
 #pragma unroll
-      for (int j = 0; j < kAdU; ++j) {
+      for (int j = 0; j < AHEAD; ++j) {
         const int e = e0 + j * UT * 4;
         if (e >= done) continue;
         f(p[j], m[j], v[j], Q::widen(u[j]));
-        AD_ST((float4*)(x.p + e), p[j]);
-        AD_ST((float4*)(x.m + e), m[j]);
-        AD_ST((float4*)(x.v + e), v[j]);
+        *(float4*)(x.p + e) = p[j];
+        *(float4*)(x.m + e) = m[j];
+        *(float4*)(x.v + e) = v[j];
         if (x.low) *(uint2*)(x.low + e) = pack4(p[j]);
       }
     }
@@ -359,7 +426,7 @@ __device__ __forceinline__ void adam_chunk(const Tensors& x, const void* g, long
 
 // Bound by DRAM: 28 to 30 bytes an element in 8 streams.
 template <int N>
-__global__ void __launch_bounds__(UT, AD_B)
+__global__ void __launch_bounds__(UT)
 k_adamw(const __grid_constant__ AdamTable<N> t, AdamArgs a) {
   ptx::griddep_wait();
   const int done = __ldcg(a.steps);
@@ -373,7 +440,7 @@ k_adamw(const __grid_constant__ AdamTable<N> t, AdamArgs a) {
     f.r1 = 1.f / -expm1f((float)(done + 1) * a.log1);
     f.r2 = 1.f / -expm1f((float)(done + 1) * a.log2);
 #pragma unroll 1
-    for (Walk<N> w(t.c, true); w.on(t.c); w.down(t.c)) {
+    for (Walk<N> w = backwards(t.c); w.on(t.c); w.next(t.c)) {
       const Tensors x{t.p[w.i] + w.at, t.m[w.i] + w.at, t.v[w.i] + w.at,
                       t.low[w.i] ? t.low[w.i] + w.at : nullptr};
       f.decay = t.decay[w.i];
@@ -541,6 +608,44 @@ cudaError_t launch_scale(const rnnt_grad_list* l, const void* const* grads, void
   return e;
 }
 
+// What one cluster takes in one launch: up to as many chunks (262,144 elements) as
+// its groups of threads take once.
+constexpr int SHORT = CBLOCKS * CGROUPS;
+
+// The whole call.
+template <int N>
+cudaError_t launch_short(const rnnt_grad_list* l, const void* const* grads, void* const* into,
+                         float max_norm, float eps, float* clip, cudaStream_t st) {
+  static std::atomic<bool> known[kDeviceSlots];
+  ScaleTable<N> t;
+  t.into[0] = nullptr;
+  next_chunks(l, 0, &t.c, [&](int k, int j) {
+    t.g[k] = grads[j];
+    t.into[k] = into ? into[j] : nullptr;
+    return quads(grads[j], t.c.bf16[k]) && quads(t.into[k], t.c.bf16[k]);
+  });
+  std::atomic<bool>& d = known[device_slot()];
+  if (!d.load()) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        k_clip_short<N>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    d.store(true);
+  }
+  int blocks = 1;
+  while (blocks * CGROUPS < t.c.first[t.c.n]) blocks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = blocks;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(UT * CGROUPS);
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_clip_short<N>, t, max_norm, eps, clip);
+}
+
 struct AdamLists {
   float* const* p;
   const void* const* g;
@@ -611,6 +716,14 @@ rnnt_status rnnt_clip(const rnnt_grad_list* list, const void* const* grads, void
   cudaStream_t st = (cudaStream_t)stream;
   double* part = (double*)ws;
   const bool few = list->n <= FEW;
+  long long chunks = 0;
+  for (int i = 0; i < list->n; ++i) chunks += cdiv(list->count[i], CHUNK);
+  if (list->n <= MANY && chunks <= SHORT) {
+    OPS_LAUNCH("clip_norm",
+               (few ? launch_short<FEW>(list, grads, into, max_norm, eps, clip, st)
+                    : launch_short<MANY>(list, grads, into, max_norm, eps, clip, st)));
+    return RNNT_OK;
+  }
   {
     ProfScope ps("clip_norm", st);
     int blocks = 0, launches = 0;

@@ -1,0 +1,62 @@
+// lists.cpp -- the data pointers of lists of tensors, for the Python binding.
+//
+// A call on hundreds of tensors looks at each one's type, place, shape and pointer.
+// Through Python attributes that takes 0.35 us a tensor, more than the GPU takes for
+// the lists of a small model; here it takes about 0.01 us.
+#include <Python.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <cstdint>
+
+namespace {
+
+// take(tensors, n, layout, device, out): the pointers of a list of dense CUDA tensors into
+// the memory at `out`.  layout: the address of int64 words, for each tensor its type (0
+// fp32, 1 bf16), dimensions and sizes.  Returns -1, or the place of the first that is
+// not as the layout says (their number, where that differs).
+PyObject* take(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  if (nargs != 5 || !PyList_Check(args[0])) {
+    PyErr_SetString(PyExc_TypeError, "take(list, n, layout, device, out)");
+    return nullptr;
+  }
+  const Py_ssize_t n = PyLong_AsSsize_t(args[1]);
+  const int64_t* want = (const int64_t*)PyLong_AsVoidPtr(args[2]);
+  const long device = PyLong_AsLong(args[3]);
+  uint64_t* out = (uint64_t*)PyLong_AsVoidPtr(args[4]);
+  if (PyErr_Occurred()) return nullptr;
+  const Py_ssize_t have = PyList_GET_SIZE(args[0]);
+  if (have != n) return PyLong_FromSsize_t(have < n ? have : n);
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    PyObject* o = PyList_GET_ITEM(args[0], i);
+    if (!THPVariable_Check(o)) return PyLong_FromSsize_t(i);
+    const at::Tensor& t = THPVariable_Unpack(o);
+    const int64_t type = *want++, dims = *want++;
+    const at::ScalarType s = type ? at::kBFloat16 : at::kFloat;
+    bool ok = t.defined() && t.layout() == at::kStrided && t.scalar_type() == s &&
+              t.is_cuda() && t.get_device() == device && t.dim() == dims && t.is_contiguous();
+    for (int64_t d = 0; ok && d < dims; ++d) ok = t.size(d) == want[d];
+    if (!ok) return PyLong_FromSsize_t(i);
+    want += dims;
+    out[i] = (uint64_t)(uintptr_t)t.data_ptr();
+  }
+  return PyLong_FromLong(-1);
+}
+
+// The same, with a C++ exception (a tensor without storage) as a Python one.
+PyObject* take_guarded(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  try {
+    return take(self, args, nargs);
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_ValueError, e.what());
+    return nullptr;
+  }
+}
+
+PyMethodDef methods[] = {{"take", (PyCFunction)(void (*)())take_guarded, METH_FASTCALL, nullptr},
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "rnnt_lists", nullptr, -1, methods,
+                      nullptr,               nullptr,      nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit_rnnt_lists() { return PyModule_Create(&module); }

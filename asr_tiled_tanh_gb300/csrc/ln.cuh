@@ -55,39 +55,42 @@ __device__ __forceinline__ Row row_of(const LnArgs& a, int r) {
 
 
 // ---- vectors ------------------------------------------------------------------
-// VEC (8, 4, 2 or 1) channels as pairs of fp32 (of one: the pair's first).
+// VEC (8, 4 or 2) channels next to each other, or two that are as many channels apart
+// as the team has lanes (VEC = 1: rows of odd width or place), as pairs of fp32.
 constexpr int kPairs(int vec) { return vec == 1 ? 1 : vec / 2; }
 template <int VEC>
 struct Vals {
   float2 p[kPairs(VEC)];
   __device__ __forceinline__ void fill(float v) {
 #pragma unroll
-    for (int i = 0; i < kPairs(VEC); ++i) p[i] = make_float2(v, VEC == 1 ? 0.f : v);
+    for (int i = 0; i < kPairs(VEC); ++i) p[i] = make_float2(v, v);
   }
 };
 
-template <int BYTES> struct UnitOf;
-template <> struct UnitOf<2> { using type = unsigned short; };
-template <> struct UnitOf<4> { using type = uint32_t; };
-template <> struct UnitOf<8> { using type = uint2; };
-template <> struct UnitOf<16> { using type = uint4; };
-// VEC values of T as they are stored
+template <typename W> struct Two { W a, b; };
+template <int VEC, int SIZE> struct UnitOf;
+template <> struct UnitOf<1, 2> { using type = Two<unsigned short>; };
+template <> struct UnitOf<1, 4> { using type = Two<uint32_t>; };
+template <> struct UnitOf<2, 2> { using type = uint32_t; };
+template <> struct UnitOf<2, 4> { using type = uint2; };
+template <> struct UnitOf<4, 2> { using type = uint2; };
+template <> struct UnitOf<4, 4> { using type = uint4; };
+template <> struct UnitOf<8, 2> { using type = uint4; };
+// as they are stored
 template <int VEC, typename T>
-using Unit = typename UnitOf<VEC * (int)sizeof(T)>::type;
+using Unit = typename UnitOf<VEC, (int)sizeof(T)>::type;
 
 template <int VEC, typename T>
 __device__ __forceinline__ Vals<VEC> widen(const Unit<VEC, T>& u) {
   Vals<VEC> v;
-  if constexpr (sizeof(T) == 4) {
-    const float* f = (const float*)&u;
-    if constexpr (VEC == 1) {
-      v.p[0] = make_float2(f[0], 0.f);
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC / 2; ++i) v.p[i] = make_float2(f[2 * i], f[2 * i + 1]);
-    }
+  if constexpr (VEC == 1 && sizeof(T) == 2) {
+    v.p[0] = make_float2(__uint_as_float((uint32_t)u.a << 16), __uint_as_float((uint32_t)u.b << 16));
   } else if constexpr (VEC == 1) {
-    v.p[0] = make_float2(__uint_as_float((uint32_t)u << 16), 0.f);
+    v.p[0] = make_float2(__uint_as_float(u.a), __uint_as_float(u.b));
+  } else if constexpr (sizeof(T) == 4) {
+    const float* f = (const float*)&u;
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) v.p[i] = make_float2(f[2 * i], f[2 * i + 1]);
   } else {
     const uint32_t* w = (const uint32_t*)&u;
 #pragma unroll
@@ -96,50 +99,66 @@ __device__ __forceinline__ Vals<VEC> widen(const Unit<VEC, T>& u) {
   return v;
 }
 
-template <int VEC, typename T>
-__device__ __forceinline__ void store(T* at, const Vals<VEC>& v) {
-  Unit<VEC, T> u;
-  if constexpr (sizeof(T) == 4) {
-    float* f = (float*)&u;
+// A lane's units of a row: unit j begins at channel at(j).
+template <int VEC>
+struct Cols {
+  int lane, lanes, C;
+  __device__ __forceinline__ int at(int j) const {
+    return VEC == 1 ? lane + 2 * j * lanes : (lane + j * lanes) * VEC;
+  }
+  __device__ __forceinline__ bool has(int j) const { return at(j) < C; }
+  // (the second of two that are apart)
+  __device__ __forceinline__ bool both(int j) const {
+    return VEC == 1 ? at(j) + lanes < C : has(j);
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* row, int j, const Vals<VEC>& v) const {
+    if (!has(j)) return;
+    T* to = row + at(j);
     if constexpr (VEC == 1) {
-      f[0] = v.p[0].x;
+      to[0] = from_f<T>(v.p[0].x);
+      if (both(j)) to[lanes] = from_f<T>(v.p[0].y);
+    } else {
+      Unit<VEC, T> u;
+      if constexpr (sizeof(T) == 4) {
+        float* f = (float*)&u;
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+          f[2 * i] = v.p[i].x;
+          f[2 * i + 1] = v.p[i].y;
+        }
+      } else {
+        uint32_t* w = (uint32_t*)&u;
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) w[i] = ptx::pack_bf16x2(v.p[i].x, v.p[i].y);
+      }
+      *(Unit<VEC, T>*)to = u;
+    }
+  }
+  // fp32 parameters of unit j (NULL: all `other`; 0 past the row's end)
+  __device__ __forceinline__ Vals<VEC> param(const float* p, int j, float other, bool al16) const {
+    Vals<VEC> v;
+    v.fill(0.f);
+    if (!has(j)) return v;
+    if (!p) {
+      v.fill(other);
+    } else if constexpr (VEC == 1) {
+      v.p[0] = make_float2(__ldg(p + at(j)), both(j) ? __ldg(p + at(j) + lanes) : 0.f);
+    } else if (VEC >= 4 && al16) {
+#pragma unroll
+      for (int i = 0; i < VEC / 4; ++i) {
+        const float4 q = __ldg((const float4*)(p + at(j)) + i);
+        v.p[2 * i] = make_float2(q.x, q.y);
+        v.p[2 * i + 1] = make_float2(q.z, q.w);
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < VEC / 2; ++i) {
-        f[2 * i] = v.p[i].x;
-        f[2 * i + 1] = v.p[i].y;
-      }
+      for (int i = 0; i < kPairs(VEC); ++i)
+        v.p[i] = make_float2(__ldg(p + at(j) + 2 * i), __ldg(p + at(j) + 2 * i + 1));
     }
-  } else if constexpr (VEC == 1) {
-    u = __bfloat16_as_ushort(__float2bfloat16_rn(v.p[0].x));
-  } else {
-    uint32_t* w = (uint32_t*)&u;
-#pragma unroll
-    for (int i = 0; i < VEC / 2; ++i) w[i] = ptx::pack_bf16x2(v.p[i].x, v.p[i].y);
+    return v;
   }
-  *(Unit<VEC, T>*)at = u;
-}
-
-// fp32 parameters of channels c to c + VEC - 1 (NULL: all `other`).
-template <int VEC>
-__device__ __forceinline__ Vals<VEC> param(const float* p, int c, float other, bool al16) {
-  Vals<VEC> v;
-  if (!p) {
-    v.fill(other);
-  } else if (VEC >= 4 && al16) {
-#pragma unroll
-    for (int i = 0; i < VEC / 4; ++i) {
-      const float4 q = __ldg((const float4*)(p + c) + i);
-      v.p[2 * i] = make_float2(q.x, q.y);
-      v.p[2 * i + 1] = make_float2(q.z, q.w);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kPairs(VEC); ++i)
-      v.p[i] = make_float2(__ldg(p + c + 2 * i), VEC == 1 ? 0.f : __ldg(p + c + 2 * i + 1));
-  }
-  return v;
-}
+};
 
 // ---- a block a row ------------------------------------------------------------
 // Rows too wide for a team: read again for each of their sums (from L2).
@@ -167,10 +186,7 @@ __device__ __forceinline__ float2 block_sum(float2 v, float2* scr) {
 
 // ---- teams ----------------------------------------------------------------------
 constexpr int MAX_THREADS = 512;
-#ifndef STG
-#define STG 3
-#endif
-constexpr int STAGES = STG;
+constexpr int STAGES = 3;
 
 // A row is taken by part of a warp (8 or 16 lanes), a warp, or several.
 enum { PART = 0, WARP = 1, WARPS = 2 };
@@ -178,7 +194,6 @@ enum { PART = 0, WARP = 1, WARPS = 2 };
 struct Team {
   int lanes;    // threads a row
   int teams;    // a block's
-  int nvec;     // vectors of a row
   FastDiv div;  // by lanes
 };
 
@@ -293,63 +308,68 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A lane's vectors of one tensor's rows ahead: [STAGES][NV][threads] units, those of
-// vectors past the row's end zero.  A stage is read and then filled again.  Units of
-// two bytes (bf16 rows of odd width or place) are too small for the copies and are
-// loaded when they are used.
-template <int VEC, int NV, typename T>
+// A lane's units of one tensor's rows ahead: [S stages][NV][threads], those past the
+// row's end zero.  A stage is read and then filled again.  Elements of two bytes are
+// too small for the copies: units of two such are loaded to registers instead, one
+// row ahead.
+template <int VEC, typename T>
+constexpr bool kCopied = VEC * sizeof(T) >= 4;
+template <int VEC, int NV, int S, typename T>
 struct Ring {
-  static constexpr int BYTES = VEC * (int)sizeof(T);
-  static constexpr bool kAhead = BYTES >= 4;
   using U = Unit<VEC, T>;
+  static constexpr int BYTES = sizeof(U);
   unsigned char* mine;
   int pitch;  // bytes from one of a lane's units to its next
+  U held[kCopied<VEC, T> ? 1 : NV];
   static __host__ __device__ size_t bytes(int threads) {
-    return kAhead ? (size_t)STAGES * NV * threads * BYTES : 0;
+    return kCopied<VEC, T> ? (size_t)S * NV * threads * BYTES : 0;
   }
   __device__ __forceinline__ void init(unsigned char* smem) {
-    mine = smem + threadIdx.x * BYTES;
-    pitch = blockDim.x * BYTES;
-    if constexpr (kAhead)
+    if constexpr (kCopied<VEC, T>) {
+      mine = smem + threadIdx.x * BYTES;
+      pitch = blockDim.x * BYTES;
 #pragma unroll
-      for (int k = 0; k < STAGES * NV; ++k) *(U*)(mine + k * pitch) = U{};
-  }
-  __device__ __forceinline__ void fetch(int stage, const T* row, const Team& t, const Place& p) {
-    if constexpr (kAhead) {
-      const uint32_t to = ptx::smem_u32(mine) + stage * (NV * pitch);
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (p.lane + j * t.lanes < t.nvec)
-          copy_async<BYTES>(to + j * pitch, row + (p.lane + j * t.lanes) * VEC);
-    }
-  }
-  __device__ __forceinline__ void read(U (&u)[NV], int stage, const T* row, bool live,
-                                       const Team& t, const Place& p) {
-    if constexpr (kAhead) {
-      const unsigned char* from = mine + stage * (NV * pitch);
-#pragma unroll
-      for (int j = 0; j < NV; ++j) u[j] = *(const U*)(from + j * pitch);
+      for (int k = 0; k < S * NV; ++k) *(U*)(mine + k * pitch) = U{};
     } else {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int k = p.lane + j * t.lanes;
-        u[j] = live && k < t.nvec ? *(const U*)(row + k * VEC) : U{};
+      for (int j = 0; j < NV; ++j) held[j] = U{};
+    }
+  }
+  __device__ __forceinline__ void fetch(int stage, const T* row, const Cols<VEC>& c) {
+    const uint32_t to = kCopied<VEC, T> ? ptx::smem_u32(mine) + stage * (NV * pitch) : 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const T* from = row + c.at(j);
+      if constexpr (!kCopied<VEC, T>) {
+        if (c.has(j)) held[j].a = *(const unsigned short*)from;
+        if (c.both(j)) held[j].b = *(const unsigned short*)(from + c.lanes);
+      } else if constexpr (VEC == 1) {
+        if (c.has(j)) copy_async<4>(to + j * pitch, from);
+        if (c.both(j)) copy_async<4>(to + j * pitch + 4, from + c.lanes);
+      } else {
+        if (c.has(j)) copy_async<BYTES>(to + j * pitch, from);
       }
+    }
+  }
+  __device__ __forceinline__ void read(U (&u)[NV], int stage) const {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if constexpr (kCopied<VEC, T>) u[j] = *(const U*)(mine + (stage * NV + j) * pitch);
+      else u[j] = held[j];
     }
   }
 };
 
 // ---- host -------------------------------------------------------------------------
-// Rows of nvec vectors: the fewest lanes whose vectors, at most `most` each, hold
-// them; nv: vectors a lane among the sizes that are compiled; 0 lanes: too wide.
-inline Team team_for(int nvec, int most, bool wide_units, int* nv) {
+// Rows of n units: the fewest lanes that hold them, at most `most` each; nv: units a
+// lane among the numbers that are compiled; 0 lanes: too wide.
+inline Team team_for(int n, int most, bool wide_units, int* nv) {
   Team t{};
-  t.nvec = nvec;
-  const int warps = (int)cdiv(nvec, 32LL * most), per = (int)cdiv(nvec, 32LL * warps);
-  *nv = wide_units ? per : per <= 2 ? 2 : per <= 4 ? 4 : 8;
+  const int warps = (int)cdiv(n, 32LL * most), per = (int)cdiv(n, 32LL * warps);
+  *nv = wide_units ? per : (per + 1) / 2 * 2;
   t.lanes = 32 * warps;
   if (warps == 1)
-    while (t.lanes > 8 && nvec <= (t.lanes / 2) * *nv) t.lanes /= 2;
+    while (t.lanes > 8 && n <= (t.lanes / 2) * *nv) t.lanes /= 2;
   if (t.lanes > MAX_THREADS) {
     t.lanes = 0;
     return t;
@@ -359,34 +379,38 @@ inline Team team_for(int nvec, int most, bool wide_units, int* nv) {
   return t;
 }
 
-// f.run<VEC, NV, MODE>(team) for rows of C channels in vectors of vec (V16: those of
-// 16 bytes) and at most CH channels a lane; false: no team holds such a row.
+// f.run<VEC, NV, MODE>(team) for rows of C channels in units of vec (V16: those of 16
+// bytes) and at most CH channels a lane, ONE pairs of those apart; false: no team holds
+// such a row.
 template <int VEC, int NV, bool NARROW, typename F>
 cudaError_t by_mode(const Team& t, const F& f) {
   if (NARROW && t.lanes < 32) return f.template run<VEC, NV, NARROW ? PART : WARP>(t);
   if (t.lanes == 32) return f.template run<VEC, NV, WARP>(t);
   return f.template run<VEC, NV, WARPS>(t);
 }
-template <int V16, int CH, typename F>
+template <int VEC, int MOST, typename F>
+cudaError_t by_pairs(const Team& t, int nv, const F& f) {
+  if (nv == 2) return by_mode<VEC, 2, true>(t, f);
+  if (nv == 4) return by_mode<VEC, 4, false>(t, f);
+  if (MOST == 6 || nv == 6) return by_mode<VEC, 6, false>(t, f);
+  return by_mode<VEC, MOST, false>(t, f);
+}
+template <int V16, int CH, int ONE, typename F>
 bool by_team(int C, int vec, const F& f, cudaError_t* e) {
   constexpr int MOST = CH / V16;  // 2 or 4
   const bool wide = vec == V16;
   int nv = 0;
-  const Team t = team_for(C / vec, wide ? MOST : 8, wide, &nv);
+  const Team t = team_for((int)cdiv(C, vec == 1 ? 2 : vec), wide ? MOST : vec == 2 ? 8 : ONE, wide,
+                          &nv);
   if (!t.lanes) return false;
-  if (wide) {
-    if (nv == 1) *e = by_mode<V16, 1, true>(t, f);
-    else if (nv == 2) *e = by_mode<V16, 2, false>(t, f);
-    else if constexpr (MOST > 2)
-      *e = nv == 3 ? by_mode<V16, 3, false>(t, f) : by_mode<V16, 4, false>(t, f);
-  } else if (vec == 2) {
-    *e = nv == 2   ? by_mode<2, 2, true>(t, f)
-         : nv == 4 ? by_mode<2, 4, false>(t, f)
-                   : by_mode<2, 8, false>(t, f);
-  } else {
-    *e = nv == 2   ? by_mode<1, 2, true>(t, f)
-         : nv == 4 ? by_mode<1, 4, false>(t, f)
-                   : by_mode<1, 8, false>(t, f);
+  if (!wide) {
+    *e = vec == 2 ? by_pairs<2, 8>(t, nv, f) : by_pairs<1, ONE>(t, nv, f);
+  } else if (nv == 1) {
+    *e = by_mode<V16, 1, true>(t, f);
+  } else if (nv == 2) {
+    *e = by_mode<V16, 2, false>(t, f);
+  } else if constexpr (MOST > 2) {
+    *e = nv == 3 ? by_mode<V16, 3, false>(t, f) : by_mode<V16, 4, false>(t, f);
   }
   return true;
 }

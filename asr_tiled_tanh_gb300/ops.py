@@ -20,11 +20,14 @@ from __future__ import annotations
 
 import array
 import ctypes
+import importlib.util
 import itertools
 import operator
+import os
 
 import torch
 
+from . import build as _build
 from .binding import RNNT_BF16, RNNT_F32, RnntError, _check, load
 
 _DTYPES = {"f32": (RNNT_F32, torch.float32), "bf16": (RNNT_BF16, torch.bfloat16)}
@@ -380,9 +383,26 @@ _data_of = torch.Tensor.data_ptr
 _PAIR = ((2,), (1,))
 
 
-def _address(pointers):
-    """Where an array of pointers lies (None: nowhere)."""
-    return None if pointers is None else pointers.buffer_info()[0]
+def _load_lists():
+    """take() of csrc/lists.cpp, or None where it was not built."""
+    if not os.path.exists(_build.LISTS):
+        return None
+    spec = importlib.util.spec_from_file_location("rnnt_lists", _build.LISTS)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module.take
+
+
+class _Kind:
+    """What a list's tensors have to be: their types and shapes."""
+
+    def __init__(self, name, types, shapes):
+        self.name, self.types = name, types
+        words = []
+        for t, k in zip(types, shapes):
+            words += [int(t is torch.bfloat16), len(k), *k]
+        self._words = array.array("q", words)
+        self.at = self._words.buffer_info()[0]
 
 
 class _ListOp(_Op):
@@ -390,31 +410,51 @@ class _ListOp(_Op):
 
     def __init__(self, shapes, dtype, ws_bytes, what, device):
         self._shapes = [torch.Size(k) for k in shapes]
-        n = len(self._shapes)
+        self._n = n = len(self._shapes)
         names = [dtype] * n if isinstance(dtype, str) else list(dtype)
         if len(names) != n:
             raise ValueError(f"{len(names)} dtypes for {n} tensors")
         codes = [_dtype(k) for k in names]
-        self._types = [t for _, t in codes]
         self._count = (ctypes.c_longlong * n)(*[k.numel() for k in self._shapes])
         self._codes = (ctypes.c_int * n)(*[c for c, _ in codes])
         self.list = RnntGradList(n, self._count, self._codes)
         self._l = ctypes.byref(self.list)
+        self._grads = self._kind("grads", [t for _, t in codes])
+        self._take_list = _load_lists()
         super().__init__(ws_bytes(self._l), what, device)
 
-    def _ptrs(self, ts, name, types):
-        """Their data pointers, an array as the C side takes it."""
-        if list(map(_shape_of, ts)) != self._shapes:
-            raise ValueError(f"{name}: {len(self._shapes)} tensors of the plan's shapes are needed")
-        index = self._index
-        if (list(map(_dtype_of, ts)) != types or not all(map(_is_dense, ts))
-                or list(map(_index_of, ts)).count(index) != len(types)):
-            for i, t in enumerate(ts):
-                if t.dtype is not types[i] or t.get_device() != index or not t.is_contiguous():
-                    raise ValueError(f"{name}[{i}]: a dense tensor of {types[i]} on "
-                                     f"{self.ws.device} is needed, got {t.dtype} of strides "
-                                     f"{t.stride()} on {t.device}")
-        return array.array("Q", map(_data_of, ts))
+    def _kind(self, name, types):
+        return _Kind(name, types, self._shapes)
+
+    def _take(self, ts, kind):
+        """The data pointers of a list: an array, and its address for the C side."""
+        n = self._n
+        a = array.array("Q", bytes(8 * n))
+        at = a.buffer_info()[0]
+        ts = ts if type(ts) is list else list(ts)
+        if self._take_list is None:
+            if not self._fits(ts, kind):
+                self._refuse(ts, kind)
+            a[:] = array.array("Q", [t.data_ptr() for t in ts])
+        elif self._take_list(ts, n, kind.at, self._index, at) >= 0:
+            self._refuse(ts, kind)
+        return a, at
+
+    def _fits(self, ts, kind):
+        return len(ts) == self._n and all(
+            t.shape == k and t.dtype is d and t.get_device() == self._index and t.is_contiguous()
+            for t, k, d in zip(ts, self._shapes, kind.types))
+
+    def _refuse(self, ts, kind):
+        if len(ts) != self._n:
+            raise ValueError(f"{kind.name}: {len(ts)} tensors, the plan has {self._n}")
+        for i, (t, k, d) in enumerate(zip(ts, self._shapes, kind.types)):
+            if not (t.shape == k and t.dtype is d and t.get_device() == self._index
+                    and t.is_contiguous()):
+                raise ValueError(f"{kind.name}[{i}]: a dense tensor of {d} {tuple(k)} on "
+                                 f"{self.ws.device} is needed, got {t.dtype} {tuple(t.shape)} of "
+                                 f"strides {t.stride()} on {t.device}")
+        raise ValueError(f"{kind.name}: dense CUDA tensors are needed")
 
 
 class GradClip(_ListOp):
@@ -431,14 +471,17 @@ class GradClip(_ListOp):
         if not self.max_norm >= 0 or not 0 <= self.eps < float("inf") or not (
                 self.max_norm or self.eps):
             raise ValueError(f"max_norm {max_norm}, eps {eps}: not negative, not both 0")
+        self._into = self._kind("into", self._grads.types)
         self._clip = lib.rnnt_clip
 
     def _call(self, grads, into, out, stream):
         if out is None:
             out = self._empty(_PAIR, torch.float32, stream)
-        g = self._ptrs(grads, "grads", self._types)
-        w = g if into is grads else None if into is None else self._ptrs(into, "into", self._types)
-        _check(self._clip(self._l, _address(g), _address(w), self.max_norm, self.eps,
+        held, g = self._take(grads, self._grads)
+        w = None
+        if into is not None:
+            held_w, w = (held, g) if into is grads else self._take(into, self._into)
+        _check(self._clip(self._l, g, w, self.max_norm, self.eps,
                           self._ptr(out, "out", torch.float32, _PAIR), self._args[0],
                           self.ws_bytes, self._stream(stream)), "rnnt_clip")
         return out
@@ -476,7 +519,9 @@ class AdamW(_ListOp):
         self.opts = RnntAdamwOpts(betas[0], betas[1], eps, 0.0, weight_decay if one else 0.0,
                                   self._decays)
         self._o = ctypes.byref(self.opts)
-        self._f32, self._bf16 = [torch.float32] * n, [torch.bfloat16] * n
+        self._params, self._m, self._v = (self._kind(k, [torch.float32] * n)
+                                          for k in ("params", "m", "v"))
+        self._copies = self._kind("low", [torch.bfloat16] * n)
         new = lambda: [torch.zeros(k, device=device) for k in self._shapes]  # noqa: E731
         self.m, self.v = (tuple(new() if k is None else k) for k in (m, v))
         self._mv = None
@@ -492,26 +537,29 @@ class AdamW(_ListOp):
         an entry or all of them None.
         """
         if self._mv is None:
-            self._mv = self._ptrs(self.m, "m", self._f32), self._ptrs(self.v, "v", self._f32)
+            self._mv = self._take(self.m, self._m), self._take(self.v, self._v)
         if isinstance(lr, torch.Tensor):
             lr = self._ptr(lr.reshape(1), "lr", torch.float32, ((1,), (1,)))
         else:
             self.opts.lr, lr = lr, None
+        held_p, p = self._take(params, self._params)
+        held_g, g = self._take(grads, self._grads)
+        held_l, w = None, None
         if low is not None:
-            low = self._low(low)
+            some = any(map(operator.is_, low, itertools.repeat(None)))
+            held_l, w = self._some(low) if some else self._take(low, self._copies)
         c = None if clip is None else self._ptr(clip, "clip", torch.float32, _PAIR)
-        p, g = self._ptrs(params, "params", self._f32), self._ptrs(grads, "grads", self._types)
-        _check(self._run(self._l, self._o, _address(p), _address(g), *map(_address, self._mv),
-                         _address(low), lr, c, self._steps, self._stream(stream)), "rnnt_adamw")
+        _check(self._run(self._l, self._o, p, g, self._mv[0][1], self._mv[1][1], w, lr, c,
+                         self._steps, self._stream(stream)), "rnnt_adamw")
 
-    def _low(self, low):
-        if not any(map(operator.is_, low, itertools.repeat(None))):
-            return self._ptrs(low, "low", self._bf16)
-        if len(low) != len(self._shapes):
-            raise ValueError(f"low: {len(low)} entries for {len(self._shapes)} tensors")
-        return array.array("Q", [0 if t is None else self._ptr(
+    def _some(self, low):
+        """The pointers of copies that only some tensors have."""
+        if len(low) != self._n:
+            raise ValueError(f"low: {len(low)} tensors, the plan has {self._n}")
+        a = array.array("Q", [0 if t is None else self._ptr(
             t, f"low[{i}]", torch.bfloat16, (k, _dense(k))) for i, (t, k) in
             enumerate(zip(low, self._shapes))])
+        return a, a.buffer_info()[0]
 
 
 class RnntTestingOrth(ctypes.Structure):

@@ -3,7 +3,6 @@
 Addresses are fake and never dereferenced.
 """
 import ctypes
-import operator
 
 import pytest
 import torch
@@ -209,9 +208,8 @@ def _plans(monkeypatch, current=0):
         setattr(plan, name, lambda *a: calls.append(a) or 0)
     monkeypatch.setattr(ops, "_raw_stream", lambda i: 0)
     monkeypatch.setattr(ops, "_current_device", lambda: current)
-    for name, method in (("_is_dense", "is_contiguous"), ("_index_of", "get_device"),
-                         ("_data_of", "data_ptr")):
-        monkeypatch.setattr(ops, name, operator.methodcaller(method))
+    for plan in (c, o):  # (the helper of lists takes no stand-ins)
+        plan._take_list = None
     return c, o, calls
 
 
@@ -258,3 +256,13 @@ def test_another_current_gpu_is_refused(monkeypatch):
     with pytest.raises(ValueError):
         o.step(p, g, 0.1)
     assert not calls
+
+
+def test_lists_are_refused_by_the_helper_too():
+    c = rn.GradClip([(2, 3), (4,)], dtype=["f32", "bf16"], device="cpu")
+    a, b = torch.zeros(2, 3), torch.zeros(4, dtype=torch.bfloat16)
+    assert c._take_list is not None  # it was built
+    c._index = 0
+    for g in ([a, b], [a], [a, b, b], [b, a], [a, None], (a, b), [1, 2]):
+        with pytest.raises((ValueError, AttributeError)):  # (no CUDA tensors, at best)
+            c.norm(g, out=torch.zeros(2))
