@@ -5,14 +5,24 @@
 namespace rnnt {
 namespace {
 using namespace ln;
-#ifndef FWD_B
-#define FWD_B 2
-#endif
+
+// Rows ahead.  What is read ahead competes with what is written: 1024 x 1000 x 256 and
+// 64 x 1000 x 4096, all fp32, 321 and 328 us with one stage, 344 and 347 with two, 341
+// and 361 with three; fp32 to bf16 260 and 261, 250 and 227, 263 and 244; bf16 to fp32
+// 274 and 273, 242 and 253, 264 and 254; 512 x 1000 x 1024 in bf16 387, 332 and 324.
+// (Parts of a warp, 512 x 2000 x 64 in fp32: 97, 85 and 85.)
+template <typename TX, typename TY, int VEC, int MODE>
+constexpr int stages() {
+  if (!kCopied<VEC, TX>) return 1;
+  if (sizeof(TX) != sizeof(TY)) return 2;
+  return sizeof(TX) == 4 && VEC == 4 && MODE != PART ? 1 : STAGES;
+}
 
 template <typename TX, typename TY, int VEC, int NV, int MODE>
-__global__ void __launch_bounds__(MODE == WARPS ? MAX_THREADS : 256, MODE == WARPS ? 1 : FWD_B)
+__global__ void
+__launch_bounds__(MODE == WARPS ? MAX_THREADS : 256, MODE == WARPS ? 1 : 2)
 k_ln_fwd(LnArgs a, Team t, const TX* __restrict__ x, TY* __restrict__ y) {
-  constexpr int NP = kPairs(VEC), S = kCopied<VEC, TX> ? STAGES : 1;
+  constexpr int NP = kPairs(VEC), S = stages<TX, TY, VEC, MODE>();
   using R = Ring<VEC, NV, S, TX>;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float scr[2][MAX_THREADS / 32][1];
@@ -195,7 +205,7 @@ struct Fwd {
     static Known known;
     const auto k = k_ln_fwd<TX, TY, VEC, NV, MODE>;
     const int threads = t.lanes * t.teams;
-    const size_t smem = Ring<VEC, NV, STAGES, TX>::bytes(threads);
+    const size_t smem = Ring<VEC, NV, stages<TX, TY, VEC, MODE>(), TX>::bytes(threads);
     int per = 0;
     const cudaError_t e = blocks_per_sm(k, &known, threads, smem, &per);
     if (e != cudaSuccess) return e;

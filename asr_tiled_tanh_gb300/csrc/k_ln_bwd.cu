@@ -4,13 +4,11 @@
 namespace rnnt {
 namespace {
 using namespace ln;
-#ifndef BWD_B
-#define BWD_B 2
-#endif
 
 // dx of the team's rows, and part[block][c] = (sum dy xh, sum dy) over the block's.
 template <typename TX, typename TY, int VEC, int NV, int MODE>
-__global__ void __launch_bounds__(MODE == WARPS ? MAX_THREADS : 256, MODE == WARPS ? 1 : BWD_B)
+__global__ void
+__launch_bounds__(MODE == WARPS ? MAX_THREADS : 256, MODE == WARPS ? 1 : 2)
 k_ln_bwd(LnArgs a, Team t, const TX* __restrict__ x, const TY* __restrict__ dy,
          TX* __restrict__ dx, float2* __restrict__ part) {
   constexpr int NP = kPairs(VEC), S = kCopied<VEC, TX> && kCopied<VEC, TY> ? STAGES : 1;

@@ -186,9 +186,9 @@ __device__ __forceinline__ float2 block_sum(float2 v, float2* scr) {
 
 // ---- teams ----------------------------------------------------------------------
 constexpr int MAX_THREADS = 512;
-constexpr int STAGES = 3;
+constexpr int STAGES = 3;  // at most
 
-// A row is taken by part of a warp (8 or 16 lanes), a warp, or several.
+// A row is taken by part of a warp (4, 8 or 16 lanes), a warp, or several.
 enum { PART = 0, WARP = 1, WARPS = 2 };
 
 struct Team {
@@ -361,15 +361,19 @@ struct Ring {
 };
 
 // ---- host -------------------------------------------------------------------------
-// Rows of n units: the fewest lanes that hold them, at most `most` each; nv: units a
-// lane among the numbers that are compiled; 0 lanes: too wide.
+// Rows of n units, at most `most` a lane; nv: units a lane among the numbers that are
+// compiled; 0 lanes: too wide.  Up to 32 units (of 16 bytes; of narrower ones 64) go to
+// part of a warp, two a lane where one would leave it a warp: a warp's steps between
+// rows then serve several (512 x 2000 rows of 256 in bf16, one a lane: 181 us forward
+// and 324 backward).
 inline Team team_for(int n, int most, bool wide_units, int* nv) {
   Team t{};
-  const int warps = (int)cdiv(n, 32LL * most), per = (int)cdiv(n, 32LL * warps);
-  *nv = wide_units ? per : (per + 1) / 2 * 2;
+  const int warps = (int)cdiv(n, 32LL * most);
   t.lanes = 32 * warps;
   if (warps == 1)
-    while (t.lanes > 8 && n <= (t.lanes / 2) * *nv) t.lanes /= 2;
+    while (t.lanes > 4 && n <= (t.lanes / 2) * 2) t.lanes /= 2;
+  const int per = (int)cdiv(n, t.lanes);
+  *nv = wide_units ? per : (per + 1) / 2 * 2;
   if (t.lanes > MAX_THREADS) {
     t.lanes = 0;
     return t;
@@ -382,18 +386,18 @@ inline Team team_for(int n, int most, bool wide_units, int* nv) {
 // f.run<VEC, NV, MODE>(team) for rows of C channels in units of vec (V16: those of 16
 // bytes) and at most CH channels a lane, ONE pairs of those apart; false: no team holds
 // such a row.
-template <int VEC, int NV, bool NARROW, typename F>
+template <int VEC, int NV, typename F>
 cudaError_t by_mode(const Team& t, const F& f) {
-  if (NARROW && t.lanes < 32) return f.template run<VEC, NV, NARROW ? PART : WARP>(t);
+  if (NV <= 2 && t.lanes < 32) return f.template run<VEC, NV, NV <= 2 ? PART : WARP>(t);
   if (t.lanes == 32) return f.template run<VEC, NV, WARP>(t);
   return f.template run<VEC, NV, WARPS>(t);
 }
 template <int VEC, int MOST, typename F>
 cudaError_t by_pairs(const Team& t, int nv, const F& f) {
-  if (nv == 2) return by_mode<VEC, 2, true>(t, f);
-  if (nv == 4) return by_mode<VEC, 4, false>(t, f);
-  if (MOST == 6 || nv == 6) return by_mode<VEC, 6, false>(t, f);
-  return by_mode<VEC, MOST, false>(t, f);
+  if (nv == 2) return by_mode<VEC, 2>(t, f);
+  if (nv == 4) return by_mode<VEC, 4>(t, f);
+  if (MOST == 6 || nv == 6) return by_mode<VEC, 6>(t, f);
+  return by_mode<VEC, MOST>(t, f);
 }
 template <int V16, int CH, int ONE, typename F>
 bool by_team(int C, int vec, const F& f, cudaError_t* e) {
@@ -406,11 +410,11 @@ bool by_team(int C, int vec, const F& f, cudaError_t* e) {
   if (!wide) {
     *e = vec == 2 ? by_pairs<2, 8>(t, nv, f) : by_pairs<1, ONE>(t, nv, f);
   } else if (nv == 1) {
-    *e = by_mode<V16, 1, true>(t, f);
+    *e = f.template run<V16, 1, PART>(t);
   } else if (nv == 2) {
-    *e = by_mode<V16, 2, false>(t, f);
+    *e = by_mode<V16, 2>(t, f);
   } else if constexpr (MOST > 2) {
-    *e = nv == 3 ? by_mode<V16, 3, false>(t, f) : by_mode<V16, 4, false>(t, f);
+    *e = nv == 3 ? by_mode<V16, 3>(t, f) : by_mode<V16, 4>(t, f);
   }
   return true;
 }
