@@ -150,6 +150,8 @@ def load(build_if_missing: bool = False):
     lib.rnnt_testing_orth_plan.argtypes = [P, P]
     lib.rnnt_testing_orth_timeout.restype = ctypes.c_int
     lib.rnnt_testing_orth_timeout.argtypes = [P, P, P, P, S, P, ctypes.c_ulonglong, P]
+    lib.rnnt_testing_overlap.restype = ctypes.c_int
+    lib.rnnt_testing_overlap.argtypes = [ctypes.c_int, P, P, P]
     _lib = lib
     return lib
 

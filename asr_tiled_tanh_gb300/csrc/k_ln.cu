@@ -103,7 +103,7 @@ k_ln_fwd(LnArgs a, Team t, const TX* __restrict__ x, TY* __restrict__ y) {
     }
     s[0] = s2.x + s2.y;
     team_sum<MODE>(s, t, p, scr[1]);
-    const float rstd = rsqrtf(fmaf(s[0], a.rC, a.eps));
+    const float rstd = __frsqrt_rn(fmaf(s[0], a.rC, a.eps));
     if (a.stats && live && p.lane == 0) a.stats[r] = make_float2(mean, rstd);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {

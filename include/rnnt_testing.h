@@ -2,8 +2,9 @@
  * rnnt_testing.h -- test hooks of librnnt_gb300 (not part of the method).
  *
  * Exposes the library's bf16 tcgen05 GEMM kernel on its own so that its
- * operand layouts can be checked against a host matrix product, and what
- * rnnt_orth decides for a size, so that tests can name the paths they take.
+ * operand layouts can be checked against a host matrix product, what rnnt_orth
+ * decides for a size, so that tests can name the paths they take, and the host's
+ * check of overlapping lists.
  */
 #ifndef RNNT_GB300_TESTING_H
 #define RNNT_GB300_TESTING_H
@@ -67,6 +68,10 @@ rnnt_status rnnt_testing_orth_plan(const rnnt_orth_dims* dims, rnnt_testing_orth
 rnnt_status rnnt_testing_orth_timeout(const rnnt_orth_dims* dims, const void* G, void* O, void* ws,
                                       size_t ws_bytes, int32_t* status,
                                       unsigned long long wait_ns, rnnt_stream stream);
+
+/* Whether, of n pieces of memory (host only, nothing is read), one that is
+ * written meets another: what rnnt_clip and rnnt_adamw refuse.  -1: no memory. */
+int rnnt_testing_overlap(int n, const void* const* p, const size_t* bytes, const int* written);
 
 #ifdef __cplusplus
 }

@@ -23,9 +23,11 @@ def _lib():
     rn.load(build_if_missing=True)
 
 
+# (lists of one launch for everything, of several, of more tensors than a launch's tables hold)
 LISTS = [[(1,)], [(3,), (), (0,), (5, 7)], [(64, 64), (64,), (32, 64), (33,)],
          [(2048,), (2049,), (2047,), (4096, 3)], [(513, 1025)], [(17,)] * 70,
-         [(1000 + 37 * i,) for i in range(140)], [(1 << 21,), (7,), (1 << 20, 3)]]
+         [(1000 + 37 * i,) for i in range(140)], [(1 << 21,), (7,), (1 << 20, 3)],
+         [(1 + i % 37,) for i in range(530)], [(8192 * 31 - 5,)], [(8192 * 33,)]]
 
 
 def _dtypes(shapes, kind):

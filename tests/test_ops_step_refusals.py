@@ -169,6 +169,31 @@ def test_names_and_numbers(lib):
         rn.GradClip([((1 << 36) + 1,)], device="cpu")
 
 
+@pytest.mark.parametrize("seed", range(60))
+def test_overlap_against_every_pair(lib, seed):
+    import random
+    r = random.Random(seed)
+    spans, at = [], 4096
+    for _ in range(r.choice([0, 1, 2, 5])):  # lists that lie one after another, or anywhere
+        one = []
+        for _ in range(r.randint(0, 12)):
+            one.append((at, r.choice([0, 4, 64, 100]), r.random() < 0.6))
+            at += r.choice([64, 100, 128])
+        spans += r.choice([one, one[::-1], r.sample(one, len(one))])
+    if seed % 2 and spans:  # one more that may meet others
+        spans.insert(r.randint(0, len(spans)), (r.choice(spans)[0] + r.choice([-40, 0, 3, 63]),
+                                                r.choice([1, 41, 5000]), r.random() < 0.5))
+    if seed % 3 == 0:
+        spans = sorted(spans, key=lambda s: s[0] % 1000)
+    n = len(spans)
+    expect = any(a[1] and b[1] and (a[2] or b[2]) and a[0] < b[0] + b[1] and b[0] < a[0] + a[1]
+                 for i, a in enumerate(spans) for b in spans[:i])
+    got = lib.rnnt_testing_overlap(n, _ptrs(*[s[0] for s in spans]),
+                                   (ctypes.c_size_t * n)(*[s[1] for s in spans]),
+                                   (ctypes.c_int * n)(*[int(s[2]) for s in spans]))
+    assert got == int(expect)
+
+
 class Tensor:
     """A CUDA tensor as far as the checks look at it."""
 
