@@ -254,8 +254,10 @@ __device__ __forceinline__ void scale_chunk(const void* g, void* into, long long
   }
 }
 
+// (Three blocks an SM: 336M elements in bf16 312 us with the norm, 340 with two, 314 with
+// four, 323 with five; 4.7M in fp32 14.0, 13.4, 15.1 and 17.6.)
 template <int N>
-__global__ void __launch_bounds__(UT)
+__global__ void __launch_bounds__(UT, 3)
 k_clip_scale(const __grid_constant__ ScaleTable<N> t, const float* clip) {
   ptx::griddep_wait();
   const float s = __ldcg(clip + 1);
