@@ -103,7 +103,9 @@ k_ln_fwd(LnArgs a, Team t, const TX* __restrict__ x, TY* __restrict__ y) {
     }
     s[0] = s2.x + s2.y;
     team_sum<MODE>(s, t, p, scr[1]);
-    const float rstd = __frsqrt_rn(fmaf(s[0], a.rC, a.eps));
+    const float var = fmaf(s[0], a.rC, a.eps);
+    float rstd = rsqrtf(var);  // (2 ulp; the step leaves it within one)
+    rstd = fmaf(0.5f * rstd, fmaf(-var * rstd, rstd, 1.f), rstd);
     if (a.stats && live && p.lane == 0) a.stats[r] = make_float2(mean, rstd);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -220,7 +222,7 @@ cudaError_t ln_fwd(const LnArgs& a, const void* x, void* y, cudaStream_t st) {
   constexpr int V16 = 16 / (int)std::max(sizeof(TX), sizeof(TY));
   const int vec = vec_of(a, sizeof(TX), x, nullptr, sizeof(TY), y);
   cudaError_t e;
-  if (by_team<V16, 16, 8>(a.C, vec, Fwd<TX, TY>{a, x, y, st}, &e)) return e;
+  if (by_team<V16, 24, (V16 == 8 ? 24 : 16), 8>(a.C, vec, Fwd<TX, TY>{a, x, y, st}, &e)) return e;
   const int grid = std::min(a.rows, 8 * num_sms());
   k_ln_fwd_wide<TX, TY><<<grid, WT, 0, st>>>(a, (const TX*)x, (TY*)y);
   return cudaGetLastError();

@@ -5,10 +5,16 @@ namespace rnnt {
 namespace {
 using namespace ln;
 
+// Threads of a block at most.  Up to 16 channels a lane fit in 128 registers, two blocks
+// of 256 threads an SM; 24 take 168, and three blocks of 128 (512 x 1000 rows of 640 in
+// bf16: 322 us; with one block of 256 377, by two warps a row of 16 channels a lane 427).
+template <int VEC, int NV, int MODE>
+constexpr int kBound = MODE == WARPS ? MAX_THREADS : VEC >= 4 && VEC * NV > 16 ? 128 : 256;
+
 // dx of the team's rows, and part[block][c] = (sum dy xh, sum dy) over the block's.
 template <typename TX, typename TY, int VEC, int NV, int MODE>
 __global__ void
-__launch_bounds__(MODE == WARPS ? MAX_THREADS : 256, MODE == WARPS ? 1 : 2)
+__launch_bounds__(kBound<VEC, NV, MODE>, MODE == WARPS ? 1 : kBound<VEC, NV, MODE> == 128 ? 3 : 2)
 k_ln_bwd(LnArgs a, Team t, const TX* __restrict__ x, const TY* __restrict__ dy,
          TX* __restrict__ dx, float2* __restrict__ part) {
   constexpr int NP = kPairs(VEC), S = kCopied<VEC, TX> && kCopied<VEC, TY> ? STAGES : 1;
@@ -243,9 +249,10 @@ struct Bwd {
   int* part_rows;
   cudaStream_t st;
   template <int VEC, int NV, int MODE>
-  cudaError_t run(const Team& t) const {
+  cudaError_t run(Team t) const {
     static Known known;
     const auto k = k_ln_bwd<TX, TY, VEC, NV, MODE>;
+    if (MODE != WARPS) t.teams = kBound<VEC, NV, MODE> / t.lanes;
     const int threads = t.lanes * t.teams;
     const size_t sums = sizeof(float2) * 2 * kPairs(VEC) * threads;
     const size_t smem = std::max(sums, Ring<VEC, NV, STAGES, TX>::bytes(threads) +
@@ -269,8 +276,8 @@ cudaError_t ln_bwd(const LnArgs& a, const void* x, const void* dy, void* dx, flo
   constexpr int V16 = 16 / (int)std::max(sizeof(TX), sizeof(TY));
   const int vec = vec_of(a, sizeof(TX), x, dx, sizeof(TY), dy);
   cudaError_t e;
-  // (16 channels a lane: their sums stay in registers)
-  if (by_team<V16, 16, 6>(a.C, vec, Bwd<TX, TY>{a, x, dy, dx, part, part_rows, st}, &e)) return e;
+  // (their sums stay in registers)
+  if (by_team<V16, (V16 == 8 ? 24 : 16), 16, 6>(a.C, vec, Bwd<TX, TY>{a, x, dy, dx, part, part_rows, st}, &e)) return e;
   const int grid = std::min(a.rows, 8 * num_sms());
   k_ln_bwd_wide<TX, TY><<<grid, WT, 0, st>>>(a, (const TX*)x, (const TY*)dy, (TX*)dx);
   e = cudaGetLastError();

@@ -361,36 +361,69 @@ struct Ring {
 };
 
 // ---- host -------------------------------------------------------------------------
-// Rows of n units, at most `most` a lane; nv: units a lane among the numbers that are
-// compiled; 0 lanes: too wide.  Up to 32 units (of 16 bytes; of narrower ones 64) go to
-// part of a warp, two a lane where one would leave it a warp: a warp's steps between
-// rows then serve several (512 x 2000 rows of 256 in bf16, one a lane: 181 us forward
-// and 324 backward).
-inline Team team_for(int n, int most, bool wide_units, int* nv) {
+// Lanes for rows of n units, and nv units a lane among the numbers that are compiled: at
+// most `one` of a warp that holds a row, `most` of several; 0 lanes: too wide.  Of units
+// of 16 bytes those that cost least: a lane's steps for a row count as 2.2 times those
+// for a unit, and what a block of 256 threads has left over is lost.  So a warp's steps
+// between rows serve several where it can hold them, and few lanes idle (bf16, us: 512 x
+// 2000 rows of 256 in 16 lanes of two units 159 forward and 253 backward, in 32 of one
+// 181 and 324; 256 x 1000 rows of 1280 in two warps of 3 units 216 forward, in three of 2
+// 313; 2000 in four of 2 367, in three of 3 395).
+constexpr int PART_UNITS = 3;  // of part of a warp
+inline Team team_for(int n, int one, int most, bool wide_units, int* nv) {
   Team t{};
-  const int warps = (int)cdiv(n, 32LL * most);
-  t.lanes = 32 * warps;
-  if (warps == 1)
-    while (t.lanes > 4 && n <= (t.lanes / 2) * 2) t.lanes /= 2;
-  const int per = (int)cdiv(n, t.lanes);
-  *nv = wide_units ? per : (per + 1) / 2 * 2;
-  if (t.lanes > MAX_THREADS) {
-    t.lanes = 0;
-    return t;
+  if (wide_units) {
+    long long least = 0;
+    auto offer = [&](long long lanes, long long threads, int per) {
+      const long long cost = threads * (11 + 5 * per);
+      if (lanes * per < n || (least && cost >= least)) return;
+      least = cost;
+      t.lanes = (int)lanes;
+      *nv = per;
+    };
+    for (int lanes = 4; lanes <= 16; lanes *= 2)
+      for (int per = 1; per <= std::min(one, PART_UNITS); ++per) offer(lanes, lanes, per);
+    for (int per = 2; per <= one; ++per) offer(32, 32, per);
+    for (int per = 2; per <= most; ++per) {
+      const long long w = std::max(2LL, cdiv(n, 32LL * per));
+      if (32 * w <= MAX_THREADS) offer(32 * w, w > 8 ? 32 * w : 256 / (8 / w), per);
+    }
+  } else {
+    const long long w = cdiv(n, 32LL * most);
+    if (32 * w <= MAX_THREADS) t.lanes = (int)(32 * w);
+    if (w == 1)
+      while (t.lanes > 4 && n <= t.lanes / 2 * 2) t.lanes /= 2;
+    if (t.lanes) *nv = ((int)cdiv(n, t.lanes) + 1) / 2 * 2;
   }
+  if (!t.lanes) return t;
   t.teams = t.lanes > 256 ? 1 : 256 / t.lanes;
   t.div = fast_div(t.lanes);
   return t;
 }
 
 // f.run<VEC, NV, MODE>(team) for rows of C channels in units of vec (V16: those of 16
-// bytes) and at most CH channels a lane, ONE pairs of those apart; false: no team holds
-// such a row.
+// bytes): at most CH channels a lane, CH1 of a warp that holds a row, ONE pairs of
+// those apart; false: no team holds such a row.
 template <int VEC, int NV, typename F>
 cudaError_t by_mode(const Team& t, const F& f) {
-  if (NV <= 2 && t.lanes < 32) return f.template run<VEC, NV, NV <= 2 ? PART : WARP>(t);
+  constexpr bool PARTS = NV <= (VEC >= 4 ? PART_UNITS : 2);
+  if (PARTS && t.lanes < 32) return f.template run<VEC, NV, PARTS ? PART : WARP>(t);
   if (t.lanes == 32) return f.template run<VEC, NV, WARP>(t);
   return f.template run<VEC, NV, WARPS>(t);
+}
+template <int VEC, int NV, int MOST1, int MOST, typename F>
+cudaError_t by_units(const Team& t, int nv, const F& f) {
+  if constexpr (NV == 1) {
+    if (nv == 1) return f.template run<VEC, 1, PART>(t);
+  } else if constexpr (NV <= MOST) {
+    if (nv == NV) return by_mode<VEC, NV>(t, f);
+  } else if (nv == NV) {
+    if (NV <= PART_UNITS && t.lanes < 32)
+      return f.template run<VEC, NV, NV <= PART_UNITS ? PART : WARP>(t);
+    return f.template run<VEC, NV, WARP>(t);
+  }
+  if constexpr (NV < MOST1) return by_units<VEC, NV + 1, MOST1, MOST>(t, nv, f);
+  return cudaErrorInvalidValue;
 }
 template <int VEC, int MOST, typename F>
 cudaError_t by_pairs(const Team& t, int nv, const F& f) {
@@ -399,23 +432,17 @@ cudaError_t by_pairs(const Team& t, int nv, const F& f) {
   if (MOST == 6 || nv == 6) return by_mode<VEC, 6>(t, f);
   return by_mode<VEC, MOST>(t, f);
 }
-template <int V16, int CH, int ONE, typename F>
+template <int V16, int CH1, int CH, int ONE, typename F>
 bool by_team(int C, int vec, const F& f, cudaError_t* e) {
-  constexpr int MOST = CH / V16;  // 2 or 4
+  constexpr int MOST1 = CH1 / V16, MOST = CH / V16;
   const bool wide = vec == V16;
   int nv = 0;
-  const Team t = team_for((int)cdiv(C, vec == 1 ? 2 : vec), wide ? MOST : vec == 2 ? 8 : ONE, wide,
-                          &nv);
+  const int narrow = vec == 2 ? 8 : ONE;
+  const Team t = team_for((int)cdiv(C, vec == 1 ? 2 : vec), wide ? MOST1 : narrow,
+                          wide ? MOST : narrow, wide, &nv);
   if (!t.lanes) return false;
-  if (!wide) {
-    *e = vec == 2 ? by_pairs<2, 8>(t, nv, f) : by_pairs<1, ONE>(t, nv, f);
-  } else if (nv == 1) {
-    *e = f.template run<V16, 1, PART>(t);
-  } else if (nv == 2) {
-    *e = by_mode<V16, 2>(t, f);
-  } else if constexpr (MOST > 2) {
-    *e = nv == 3 ? by_mode<V16, 3>(t, f) : by_mode<V16, 4>(t, f);
-  }
+  if (wide) *e = by_units<V16, 1, MOST1, MOST>(t, nv, f);
+  else *e = vec == 2 ? by_pairs<2, 8>(t, nv, f) : by_pairs<1, ONE>(t, nv, f);
   return true;
 }
 
