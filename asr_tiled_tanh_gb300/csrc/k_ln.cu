@@ -34,7 +34,7 @@ k_ln_fwd(LnArgs a, Team t, const TX* __restrict__ x, TY* __restrict__ y) {
   Walk next(a, p.first), row = next;
   Offset xo(a, next, by, a.xf, a.xb), yo(a, row, by, a.yf, a.yb);
   R ring;
-  ring.init(smem);
+  ring.init(smem, cols);
   unsigned lives = 0;  // bit s: the row s turns from now exists
   int length = ask_length(a, next);
   auto ahead = [&](int stage) {
@@ -122,32 +122,54 @@ k_ln_fwd(LnArgs a, Team t, const TX* __restrict__ x, TY* __restrict__ y) {
   copy_wait<0>();
 }
 
-template <typename TX, typename TY>
+template <typename TX, typename TY, int VEC>
 __global__ void __launch_bounds__(WT)
 k_ln_fwd_wide(LnArgs a, const TX* __restrict__ x, TY* __restrict__ y) {
+  constexpr int NP = kPairs(VEC);
   __shared__ float2 scr[WWARPS];
+  const Cols<VEC> cols{(int)threadIdx.x, WT, a.C};
+  const bool al16 = (((uintptr_t)a.gamma | (uintptr_t)a.beta) & 15) == 0;
   for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const Row w = row_of(a, r);
     TY* yr = y + w.y;
     if (!w.live) {
-      for (int c = threadIdx.x; c < a.C; c += WT) yr[c] = from_f<TY>(0.f);
+      Vals<VEC> z;
+      z.fill(0.f);
+      for (int j = 0; cols.has(j); ++j) cols.store(yr, j, z);
       continue;
     }
     const TX* xr = x + w.x;
     float2 s = make_float2(0.f, 0.f);
-    for (int c = threadIdx.x; c < a.C; c += WT) s.x += to_f<TX>(xr[c]);
-    const float mean = block_sum(s, scr).x / (float)a.C;  // (exact for rows of one value)
-    s.x = 0.f;
-    for (int c = threadIdx.x; c < a.C; c += WT) {
-      const float d = to_f<TX>(xr[c]) - mean;
-      s.x = fmaf(d, d, s.x);
+#pragma unroll 2
+    for (int j = 0; cols.has(j); ++j) {
+      const Vals<VEC> v = cols.load(xr, j);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) s = __fadd2_rn(s, v.p[i]);
     }
-    const float rstd = 1.f / sqrtf(block_sum(s, scr).x * a.rC + a.eps);
+    const float mean = block_sum(make_float2(s.x + s.y, 0.f), scr).x / (float)a.C;
+    s = make_float2(0.f, 0.f);
+#pragma unroll 2
+    for (int j = 0; cols.has(j); ++j) {
+      const Vals<VEC> v = cols.load(xr, j);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        float2 d = __fadd2_rn(v.p[i], make_float2(-mean, -mean));
+        if (VEC == 1 && !cols.both(j)) d.y = 0.f;
+        s = __ffma2_rn(d, d, s);
+      }
+    }
+    const float rstd =
+        1.f / sqrtf(block_sum(make_float2(s.x + s.y, 0.f), scr).x * a.rC + a.eps);
     if (a.stats && threadIdx.x == 0) a.stats[r] = make_float2(mean, rstd);
-    for (int c = threadIdx.x; c < a.C; c += WT) {
-      const float xh = (to_f<TX>(xr[c]) - mean) * rstd;
-      yr[c] = from_f<TY>(fmaf(a.gamma ? __ldg(a.gamma + c) : 1.f, xh,
-                              a.beta ? __ldg(a.beta + c) : 0.f));
+#pragma unroll 2
+    for (int j = 0; cols.has(j); ++j) {
+      const Vals<VEC> v = cols.load(xr, j), g = cols.param(a.gamma, j, 1.f, al16);
+      Vals<VEC> o = cols.param(a.beta, j, 0.f, al16);
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        o.p[i] = __ffma2_rn(g.p[i], __fmul2_rn(__fadd2_rn(v.p[i], make_float2(-mean, -mean)),
+                                               make_float2(rstd, rstd)), o.p[i]);
+      cols.store(yr, j, o);
     }
   }
 }
@@ -223,8 +245,8 @@ cudaError_t ln_fwd(const LnArgs& a, const void* x, void* y, cudaStream_t st) {
   const int vec = vec_of(a, sizeof(TX), x, nullptr, sizeof(TY), y);
   cudaError_t e;
   if (by_team<V16, 24, (V16 == 8 ? 24 : 16), 8>(a.C, vec, Fwd<TX, TY>{a, x, y, st}, &e)) return e;
-  const int grid = std::min(a.rows, 8 * num_sms());
-  k_ln_fwd_wide<TX, TY><<<grid, WT, 0, st>>>(a, (const TX*)x, (TY*)y);
+  const auto k = vec == V16 ? k_ln_fwd_wide<TX, TY, V16> : k_ln_fwd_wide<TX, TY, 1>;
+  k<<<std::min(a.rows, 4 * num_sms()), WT, 0, st>>>(a, (const TX*)x, (TY*)y);
   return cudaGetLastError();
 }
 

@@ -31,8 +31,8 @@ k_ln_bwd(LnArgs a, Team t, const TX* __restrict__ x, const TY* __restrict__ dy,
   Offset xo(a, next, by, a.xf, a.xb), yo(a, next, by, a.yf, a.yb), xr = xo;
   RX rx;
   RY ry;
-  rx.init(smem);
-  ry.init(smem + RX::bytes(blockDim.x));
+  rx.init(smem, cols);
+  ry.init(smem + RX::bytes(blockDim.x), cols);
   unsigned lives = 0;  // bit s: the row s turns from now exists
   int length = ask_length(a, next);
   auto ahead = [&](int stage) {
@@ -153,71 +153,113 @@ k_ln_bwd(LnArgs a, Team t, const TX* __restrict__ x, const TY* __restrict__ dy,
   }
 }
 
-template <typename TX, typename TY>
+template <typename TX, typename TY, int VEC>
 __global__ void __launch_bounds__(WT)
 k_ln_bwd_wide(LnArgs a, const TX* __restrict__ x, const TY* __restrict__ dy,
               TX* __restrict__ dx) {
+  constexpr int NP = kPairs(VEC);
   __shared__ float2 scr[WWARPS];
+  const Cols<VEC> cols{(int)threadIdx.x, WT, a.C};
+  const bool al16 = ((uintptr_t)a.gamma & 15) == 0;
   for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const Row w = row_of(a, r);
     TX* dr = dx + w.x;
     if (!w.live) {
-      for (int c = threadIdx.x; c < a.C; c += WT) dr[c] = from_f<TX>(0.f);
+      Vals<VEC> z;
+      z.fill(0.f);
+      for (int j = 0; cols.has(j); ++j) cols.store(dr, j, z);
       continue;
     }
+    const float2 st = a.stats[r];
     const TX* xr = x + w.x;
     const TY* gr = dy + w.y;
-    const float2 st = a.stats[r];
-    float2 s = make_float2(0.f, 0.f);
-    for (int c = threadIdx.x; c < a.C; c += WT) {
-      const float g = to_f<TY>(gr[c]) * (a.gamma ? __ldg(a.gamma + c) : 1.f);
-      s.x += g;
-      s.y = fmaf(g, (to_f<TX>(xr[c]) - st.x) * st.y, s.y);
+    // gamma dy and xh of unit j (past the row's end gamma is 0)
+    auto terms = [&](int j, Vals<VEC>& g, Vals<VEC>& xh) {
+      g = cols.load(gr, j);
+      xh = cols.load(xr, j);
+      const Vals<VEC> gamma = cols.param(a.gamma, j, 1.f, al16);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        g.p[i] = __fmul2_rn(g.p[i], gamma.p[i]);
+        xh.p[i] = __fmul2_rn(__fadd2_rn(xh.p[i], make_float2(-st.x, -st.x)),
+                             make_float2(st.y, st.y));
+      }
+    };
+    float2 s1 = make_float2(0.f, 0.f), s2 = s1;
+#pragma unroll 2
+    for (int j = 0; cols.has(j); ++j) {
+      Vals<VEC> g, xh;
+      terms(j, g, xh);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        s1 = __fadd2_rn(g.p[i], s1);
+        s2 = __ffma2_rn(g.p[i], xh.p[i], s2);
+      }
     }
-    s = block_sum(s, scr);
-    const float m1 = s.x * a.rC, m2 = s.y * a.rC;
-    for (int c = threadIdx.x; c < a.C; c += WT) {
-      const float g = to_f<TY>(gr[c]) * (a.gamma ? __ldg(a.gamma + c) : 1.f);
-      const float xh = (to_f<TX>(xr[c]) - st.x) * st.y;
-      dr[c] = from_f<TX>(st.y * (g - m1 - xh * m2));
+    const float2 s = block_sum(make_float2(s1.x + s1.y, s2.x + s2.y), scr);
+    const float k1 = -s.x * a.rC * st.y, k2 = -s.y * a.rC * st.y;
+#pragma unroll 2
+    for (int j = 0; cols.has(j); ++j) {
+      Vals<VEC> g, xh;
+      terms(j, g, xh);
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        g.p[i] = __ffma2_rn(g.p[i], make_float2(st.y, st.y),
+                            __ffma2_rn(xh.p[i], make_float2(k2, k2), make_float2(k1, k1)));
+      cols.store(dr, j, g);
     }
   }
 }
 
-// part[slice][c] = (sum dy xh, sum dy) over the slice's rows: 32 channels and a
-// slice of the rows a block.
-template <typename TX, typename TY>
-__global__ void __launch_bounds__(WT)
+// part[slice][c] = (sum dy xh, sum dy) over the slice's rows: a unit a lane, and a slice
+// of the rows a block, a warp a row of it.
+constexpr int CT = 256, CWARPS = CT / 32;
+template <typename TX, typename TY, int VEC>
+__global__ void __launch_bounds__(CT)
 k_ln_cols(LnArgs a, const TX* __restrict__ x, const TY* __restrict__ dy,
           float2* __restrict__ part, int per) {
-  __shared__ float2 scr[WWARPS][32];
+  constexpr int NP = kPairs(VEC), CH = 2 * NP;
+  __shared__ float2 scr[CWARPS][CH][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+  const Cols<VEC> cols{(int)(blockIdx.x * 32) + lane, (int)gridDim.x * 32, a.C};
   const long long r0 = (long long)blockIdx.y * per, r1 = min((long long)a.rows, r0 + per);
-  float2 s = make_float2(0.f, 0.f);
-  if (c < a.C)
-    for (long long r = r0 + warp; r < r1; r += WWARPS) {
+  Vals<VEC> dg, db;
+  dg.fill(0.f);
+  db.fill(0.f);
+  if (cols.has(0)) {
+#pragma unroll 4
+    for (long long r = r0 + warp; r < r1; r += CWARPS) {
       const Row w = row_of(a, (int)r);
       if (!w.live) continue;
       const float2 st = a.stats[r];
-      const float g = to_f<TY>(dy[w.y + c]);
-      s.x = fmaf(g, (to_f<TX>(x[w.x + c]) - st.x) * st.y, s.x);
-      s.y += g;
+      const Vals<VEC> g = cols.load(dy + w.y, 0), v = cols.load(x + w.x, 0);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const float2 xh = __fmul2_rn(__fadd2_rn(v.p[i], make_float2(-st.x, -st.x)),
+                                     make_float2(st.y, st.y));
+        dg.p[i] = __ffma2_rn(g.p[i], xh, dg.p[i]);
+        db.p[i] = __fadd2_rn(g.p[i], db.p[i]);
+      }
     }
-  scr[warp][lane] = s;
-  __syncthreads();
-  if (warp || c >= a.C) return;
-  for (int k = 1; k < WWARPS; ++k) {
-    s.x += scr[k][lane].x;
-    s.y += scr[k][lane].y;
   }
-  part[(long long)blockIdx.y * a.C + c] = s;
+#pragma unroll
+  for (int i = 0; i < CH; ++i)
+    scr[warp][i][lane] = make_float2(i & 1 ? dg.p[i / 2].y : dg.p[i / 2].x,
+                                     i & 1 ? db.p[i / 2].y : db.p[i / 2].x);
+  __syncthreads();
+  // a warp a channel of the units
+  for (int i = warp; i < CH; i += CWARPS) {
+    if (!(VEC == 1 && i ? cols.both(0) : cols.has(0))) continue;
+    float2 s = scr[0][i][lane];
+    for (int k = 1; k < CWARPS; ++k) s = __fadd2_rn(s, scr[k][i][lane]);
+    part[(long long)blockIdx.y * a.C + cols.at(0) + (VEC == 1 ? i * cols.lanes : i)] = s;
+  }
 }
 
 // dgamma, dbeta: the column sums of part [n][C], 8 channels a block, its 32 groups
 // of threads a row each at a time.
-constexpr int PCOLS = 8, PGROUPS = WT / PCOLS;
-__global__ void __launch_bounds__(WT)
+constexpr int PT = 256, PCOLS = 8, PGROUPS = PT / PCOLS;
+__global__ void __launch_bounds__(PT)
 k_ln_params(const float2* __restrict__ part, int n, int C, float* __restrict__ dgamma,
             float* __restrict__ dbeta) {
   __shared__ float2 scr[PGROUPS][PCOLS];
@@ -278,12 +320,14 @@ cudaError_t ln_bwd(const LnArgs& a, const void* x, const void* dy, void* dx, flo
   cudaError_t e;
   // (their sums stay in registers)
   if (by_team<V16, (V16 == 8 ? 24 : 16), 16, 6>(a.C, vec, Bwd<TX, TY>{a, x, dy, dx, part, part_rows, st}, &e)) return e;
-  const int grid = std::min(a.rows, 8 * num_sms());
-  k_ln_bwd_wide<TX, TY><<<grid, WT, 0, st>>>(a, (const TX*)x, (const TY*)dy, (TX*)dx);
+  const bool wide = vec == V16;
+  const auto k = wide ? k_ln_bwd_wide<TX, TY, V16> : k_ln_bwd_wide<TX, TY, 1>;
+  k<<<std::min(a.rows, 4 * num_sms()), WT, 0, st>>>(a, (const TX*)x, (const TY*)dy, (TX*)dx);
   e = cudaGetLastError();
   if (e != cudaSuccess || !part) return e;
   const int n = std::min(64, part_rows_max(a));
-  k_ln_cols<TX, TY><<<dim3((unsigned)cdiv(a.C, 32), n), WT, 0, st>>>(
+  const auto c = wide ? k_ln_cols<TX, TY, V16> : k_ln_cols<TX, TY, 1>;
+  c<<<dim3((unsigned)cdiv(a.C, 32 * (wide ? V16 : 2)), n), CT, 0, st>>>(
       a, (const TX*)x, (const TY*)dy, part, (int)cdiv(a.rows, n));
   *part_rows = n;
   return cudaGetLastError();
@@ -314,7 +358,7 @@ cudaError_t launch_params(const float2* part, int rows, int C, float* dgamma, fl
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)cdiv(C, PCOLS));
-  cfg.blockDim = dim3(WT);
+  cfg.blockDim = dim3(PT);
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;

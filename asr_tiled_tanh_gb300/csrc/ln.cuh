@@ -112,6 +112,17 @@ struct Cols {
     return VEC == 1 ? at(j) + lanes < C : has(j);
   }
   template <typename T>
+  __device__ __forceinline__ Vals<VEC> load(const T* row, int j) const {
+    const T* from = row + at(j);
+    if constexpr (VEC == 1) {
+      Vals<1> v;
+      v.p[0] = make_float2(to_f<T>(from[0]), both(j) ? to_f<T>(from[lanes]) : 0.f);
+      return v;
+    } else {
+      return widen<VEC, T>(*(const Unit<VEC, T>*)from);
+    }
+  }
+  template <typename T>
   __device__ __forceinline__ void store(T* row, int j, const Vals<VEC>& v) const {
     if (!has(j)) return;
     T* to = row + at(j);
@@ -162,9 +173,9 @@ struct Cols {
 
 // ---- a block a row ------------------------------------------------------------
 // Rows too wide for a team: read again for each of their sums (from L2).
-constexpr int WT = 256, WWARPS = WT / 32;
+constexpr int WT = 512, WWARPS = WT / 32;
 
-// Sums of two values over the block, for all threads; scr: 2 WWARPS + 2 floats.
+// Sums of two values over the block, for all threads.
 __device__ __forceinline__ float2 block_sum(float2 v, float2* scr) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) {
@@ -324,12 +335,21 @@ struct Ring {
   static __host__ __device__ size_t bytes(int threads) {
     return kCopied<VEC, T> ? (size_t)S * NV * threads * BYTES : 0;
   }
-  __device__ __forceinline__ void init(unsigned char* smem) {
+  __device__ __forceinline__ void init(unsigned char* smem, const Cols<VEC>& c) {
     if constexpr (kCopied<VEC, T>) {
       mine = smem + threadIdx.x * BYTES;
       pitch = blockDim.x * BYTES;
+      // (only what no copy will write)
 #pragma unroll
-      for (int k = 0; k < S * NV; ++k) *(U*)(mine + k * pitch) = U{};
+      for (int k = 0; k < S * NV; ++k) {
+        U* u = (U*)(mine + k * pitch);
+        if constexpr (VEC == 1) {
+          if (!c.has(k % NV)) u->a = 0;
+          if (!c.both(k % NV)) u->b = 0;
+        } else {
+          if (!c.has(k % NV)) *u = U{};
+        }
+      }
     } else {
 #pragma unroll
       for (int j = 0; j < NV; ++j) held[j] = U{};

@@ -2,15 +2,18 @@
 
     frames [B,T,C] --FrameNorm--> hA --+
                                        +--> joint network, output layer, loss (Rnnt) and gradients
-    labels [B,U+1] --LabelEmbedding--> hL --+
+    labels [B,U+1] --LabelEmbedding, LayerNorm--> hL --+
 
-    dhA --FrameNorm.bwd--> d frames, d gamma, d beta     dhL --LabelEmbedding.bwd--> d table
-    dW^A, dW^L, dW^O --Orthogonalizer--> weight updates (momentum, then Newton-Schulz products)
+    dhA --FrameNorm.bwd--> d frames, d gamma, d beta
+    dhL --LayerNorm.bwd, LabelEmbedding.bwd--> d scale, d shift, d table
+    all gradients --GradClip--> their norm and the scale that limits it
+    dW^A, dW^L --Orthogonalizer--> weight updates (momentum, then Newton-Schulz products)
+    the others --AdamW--> weights and their bf16 copies
 
-Every matrix takes the orthogonalised update here, the output layer's as well (Muon as published
-leaves that one to another method).  The encoder that would make the frames and take their
-gradient is left out: the frames are a fixed synthetic batch whose features carry the labels, so
-the loss falls as the step repeats.
+The hidden matrices take the orthogonalised update, the output layer, the label table, biases
+and norms AdamW.  The encoder that would make the frames and take their gradient is left out: the
+frames are a fixed synthetic batch whose features carry the labels, so the loss falls as the step
+repeats.
 Run:  python examples/training_step.py [steps]
 """
 import math
@@ -26,50 +29,60 @@ import asr_tiled_tanh_gb300 as rn  # noqa: E402
 class Transducer:
     """fp32 master weights, bf16 activations; plans and buffers are made once."""
 
-    def __init__(self, B, T, U1, C, H, V, groups=32, lr=0.02, momentum=0.9, seed=0):
+    def __init__(self, B, T, U1, C, H, V, groups=32, lr=0.02, momentum=0.9, max_norm=5.0, seed=0):
         g = torch.Generator(device="cuda").manual_seed(seed)
         r = lambda *s, std: std * torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+        one, zero = (lambda n: torch.ones(n, device="cuda")), (lambda n: torch.zeros(n, device="cuda"))
         self.lr, self.mu = lr, momentum
-        self.matrices = {"WA": r(H, C, std=C ** -0.5), "WL": r(H, H, std=H ** -0.5),
-                         "WO": r(V, H, std=H ** -0.5)}
-        self.vectors = {"bZ": torch.zeros(H, device="cuda"), "bO": torch.zeros(V, device="cuda"),
-                        "gamma": torch.ones(C, device="cuda"), "beta": torch.zeros(C, device="cuda"),
-                        "table": r(V, H, std=H ** -0.5)}
-        self.velocity = {k: torch.zeros_like(v) for k, v in {**self.matrices, **self.vectors}.items()}
+        self.matrices = {"WA": r(H, C, std=C ** -0.5), "WL": r(H, H, std=H ** -0.5)}
+        self.others = {"WO": r(V, H, std=H ** -0.5), "table": r(V, H, std=H ** -0.5),
+                       "bZ": zero(H), "bO": zero(V), "gamma": one(C), "beta": zero(C),
+                       "scale": one(H), "shift": zero(H)}
+        self.velocity = {k: torch.zeros_like(v) for k, v in self.matrices.items()}
+        # what the loss reads: AdamW keeps the copies of its own weights
+        self.low = {k: v.bfloat16() for k, v in {**self.matrices, **self.others}.items()
+                    if k in ("WA", "WL", "WO", "bZ", "bO")}
         self.norm = rn.FrameNorm(B, T, C, groups, act="silu", dtype="bf16")
         self.embed = rn.LabelEmbedding(B, U1, V, H, dtype="f32", out_dtype="bf16",
                                        scale=math.sqrt(H))
+        self.rows = rn.LayerNorm(B, U1, H, dtype="bf16", label_rows=True)
         self.rnnt = rn.Rnnt(B, T, U1, C, H, H, V, dtype="bf16")
         self.orth = {k: rn.Orthogonalizer(*w.shape, out_dtype="f32")
                      for k, w in self.matrices.items()}
+        weights = [*self.matrices.values(), *self.others.values()]
+        self.clip = rn.GradClip([w.shape for w in weights], max_norm=max_norm)
+        self.adamw = rn.AdamW([w.shape for w in self.others.values()],
+                              weight_decay=[0.01 if k == "WO" else 0.0 for k in self.others])
 
     def step(self, frames, labels, T_len, U_len):
         """One update; returns (loss per sample, d frames)."""
-        m, v = self.matrices, self.vectors
+        m, v = self.matrices, self.others
         hA = self.norm.fwd(frames, v["gamma"], v["beta"], T_len)
-        hL = self.embed.fwd(v["table"], labels, U_len)
-        low = {k: p.bfloat16() for k, p in {**m, "bZ": v["bZ"], "bO": v["bO"]}.items()}
-        params = rn.make_params(low["WA"], low["WL"], low["bZ"], low["WO"], low["bO"])
+        e = self.embed.fwd(v["table"], labels, U_len)
+        hL = self.rows.fwd(e, v["scale"], v["shift"], U_len)
+        params = rn.make_params(*(self.low[k] for k in ("WA", "WL", "bZ", "WO", "bO")))
         args = (hA, hL, params, labels, T_len, U_len)
+        count = frames.shape[0]
         loss = self.rnnt.fwd(*args)
-        d = self.rnnt.bwd_ex(*args, enc_dtype="bf16")
+        d = self.rnnt.bwd_ex(*args, grad_loss=torch.full_like(loss, 1 / count), enc_dtype="bf16")
         dframes, dgamma, dbeta = self.norm.bwd(frames, d["dhA"], v["gamma"], v["beta"], T_len)
-        dtable = self.embed.bwd(d["dhL"], labels, U_len)
-        grads = {"WA": d["dWA"], "WL": d["dWL"], "WO": d["dWO"], "bZ": d["dbZ"], "bO": d["dbO"],
-                 "gamma": dgamma, "beta": dbeta, "table": dtable}
-        count = float(frames.shape[0])
-        for k, grad in grads.items():
-            vel = self.velocity[k].mul_(self.mu).add_(grad, alpha=1 / count)
-            if k in m:  # an update of singular values near 1, whatever the gradient's
-                scale = self.lr * math.sqrt(max(1.0, m[k].shape[0] / m[k].shape[1]))
-                m[k].sub_(self.orth[k].run(vel), alpha=scale)
-            else:
-                v[k].sub_(vel, alpha=0.1 * self.lr)
-        return loss, dframes
+        de, dscale, dshift = self.rows.bwd(e, d["dhL"], v["scale"], U_len)
+        grads = {"WA": d["dWA"], "WL": d["dWL"], "WO": d["dWO"],
+                 "table": self.embed.bwd(de, labels, U_len), "bZ": d["dbZ"], "bO": d["dbO"],
+                 "gamma": dgamma, "beta": dbeta, "scale": dscale, "shift": dshift}
+        clip = self.clip.norm([grads[k] for k in (*m, *v)])
+        for k, w in m.items():  # an update of singular values near 1, whatever the gradient's
+            vel = self.velocity[k].mul_(self.mu).add_(grads[k] * clip[1])
+            w.sub_(self.orth[k].run(vel),
+                   alpha=self.lr * math.sqrt(max(1.0, w.shape[0] / w.shape[1])))
+            self.low[k].copy_(w)
+        self.adamw.step(list(v.values()), [grads[k] for k in v], 0.5 * self.lr, clip=clip,
+                        low=[self.low.get(k) for k in v])
+        return loss, dframes * count
 
     def status(self):
         """0 when no call found a problem on the device."""
-        ops = [self.norm, self.embed, *self.orth.values()]
+        ops = [self.norm, self.embed, self.rows, *self.orth.values()]
         return max([self.rnnt.status()[0], *(o.status()[0] for o in ops)])
 
 

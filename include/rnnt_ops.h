@@ -143,8 +143,8 @@ rnnt_status rnnt_norm_bwd(const rnnt_norm_dims* dims, const void* x, const void*
  * lengths in [0,T-1]).  The others are never read; their y and dx are 0.  lengths
  * NULL: every row exists; a length out of its range sets RNNT_ERR_LENGTH_RANGE and
  * its sample has no rows.  One streamed frame or one decoding step: T = 1.
- * Statistics and sums are fp32, the variance taken about the mean; only y and dx
- * are rounded to their types.  B*T <= 2^30, C <= 2^20.  Strides may put samples
+ * Statistics and sums are fp32, the variance taken about the mean (a row whose
+ * squares leave fp32's range gives NaN); only y and dx are rounded to their types.  B*T <= 2^30, C <= 2^20.  Strides may put samples
  * after one another or frames after one another (time-major), without overlap.
  */
 typedef struct {
@@ -216,7 +216,7 @@ rnnt_status rnnt_orth(const rnnt_orth_dims* dims, const void* G, void* O, void* 
 /* ---- gradient clipping ---------------------------------------------------------
  * Over all elements of n tensors together:
  *   norm = sqrt(sum g^2),  scale = min(1, max_norm / (norm + eps)),  into = scale g
- * Squares are added in fp64 (fp32 in groups of 32 or fewer, fp64 where that would
+ * Squares are added in fp64 (fp32 in groups of 33 or fewer, fp64 where that would
  * leave the range), in an order that follows from the list and the device, so
  * finite entries of any size are fine.  A norm that is not finite: an infinite one
  * gives scale 0, NaN gives NaN, and `into` is the product all the same; rnnt_adamw
@@ -246,7 +246,8 @@ rnnt_status rnnt_clip(const rnnt_grad_list* list, const void* const* grads, void
  *   p <- p - lr (decay p + (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps))
  *   low <- p in bf16, where a copy is wanted
  * p, m, v are fp32, updated in place; g is read only, fp32 or bf16 by the list.
- * With clip, an update whose norm is not finite changes nothing and is not counted.
+ * With clip, an update whose norm is not finite changes nothing and is not counted;
+ * neither is one of a list without elements.
  */
 typedef struct {
   double beta1, beta2;  /* [0,1) */
