@@ -34,7 +34,8 @@ k_ln_fwd(LnArgs a, Team t, const TX* __restrict__ x, TY* __restrict__ y) {
   Walk next(a, p.first), row = next;
   Offset xo(a, next, by, a.xf, a.xb), yo(a, row, by, a.yf, a.yb);
   R ring;
-  ring.init(smem, cols);
+  ring.init(smem);
+  __syncthreads();
   unsigned lives = 0;  // bit s: the row s turns from now exists
   int length = ask_length(a, next);
   auto ahead = [&](int stage) {

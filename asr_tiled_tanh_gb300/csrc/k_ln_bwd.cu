@@ -31,8 +31,9 @@ k_ln_bwd(LnArgs a, Team t, const TX* __restrict__ x, const TY* __restrict__ dy,
   Offset xo(a, next, by, a.xf, a.xb), yo(a, next, by, a.yf, a.yb), xr = xo;
   RX rx;
   RY ry;
-  rx.init(smem, cols);
-  ry.init(smem + RX::bytes(blockDim.x), cols);
+  rx.init(smem);
+  ry.init(smem + RX::bytes(blockDim.x));
+  __syncthreads();
   unsigned lives = 0;  // bit s: the row s turns from now exists
   int length = ask_length(a, next);
   auto ahead = [&](int stage) {

@@ -335,21 +335,13 @@ struct Ring {
   static __host__ __device__ size_t bytes(int threads) {
     return kCopied<VEC, T> ? (size_t)S * NV * threads * BYTES : 0;
   }
-  __device__ __forceinline__ void init(unsigned char* smem, const Cols<VEC>& c) {
+  // (a barrier between this and the first copies)
+  __device__ __forceinline__ void init(unsigned char* smem) {
     if constexpr (kCopied<VEC, T>) {
       mine = smem + threadIdx.x * BYTES;
       pitch = blockDim.x * BYTES;
-      // (only what no copy will write)
 #pragma unroll
-      for (int k = 0; k < S * NV; ++k) {
-        U* u = (U*)(mine + k * pitch);
-        if constexpr (VEC == 1) {
-          if (!c.has(k % NV)) u->a = 0;
-          if (!c.both(k % NV)) u->b = 0;
-        } else {
-          if (!c.has(k % NV)) *u = U{};
-        }
-      }
+      for (int k = 0; k < S * NV; ++k) *(U*)(mine + k * pitch) = U{};
     } else {
 #pragma unroll
       for (int j = 0; j < NV; ++j) held[j] = U{};
