@@ -6,15 +6,16 @@ namespace rnnt {
 namespace {
 using namespace ln;
 
-// Rows ahead.  What is read ahead competes with what is written: 1024 x 1000 x 256 and
-// 64 x 1000 x 4096, all fp32, 321 and 328 us with one stage, 344 and 347 with two, 341
-// and 361 with three; fp32 to bf16 260 and 261, 250 and 227, 263 and 244; bf16 to fp32
-// 274 and 273, 242 and 253, 264 and 254; 512 x 1000 x 1024 in bf16 387, 332 and 324.
-// (Parts of a warp, 512 x 2000 x 64 in fp32: 97, 85 and 85.)
-template <typename TX, typename TY, int VEC, int MODE>
+// Rows ahead.  What is read ahead competes with what is written (us with one, two and
+// three stages): 1024 x 1000 x 256 and 64 x 1000 x 4096, all fp32, 321, 344, 341 and 328,
+// 347, 361; fp32 to bf16 260, 250, 263 and 261, 227, 244; bf16 to fp32 274, 242, 264 and
+// 273, 253, 254; bf16 in two units a lane, 512 x 1000 x 1024, 387, 332, 324; in three,
+// 512 x 1000 x 640, 704 and 768, 231, 199, 198 and 248, 233, 250 and 258, 268, 275; parts
+// of a warp, 512 x 2000 x 64 in fp32, 97, 85, 85.
+template <typename TX, typename TY, int VEC, int NV, int MODE>
 constexpr int stages() {
   if (!kCopied<VEC, TX>) return 1;
-  if (sizeof(TX) != sizeof(TY)) return 2;
+  if (sizeof(TX) != sizeof(TY) || (VEC == 8 && NV == 3)) return 2;
   return sizeof(TX) == 4 && VEC == 4 && MODE != PART ? 1 : STAGES;
 }
 
@@ -22,7 +23,7 @@ template <typename TX, typename TY, int VEC, int NV, int MODE>
 __global__ void
 __launch_bounds__(MODE == WARPS ? MAX_THREADS : 256, MODE == WARPS ? 1 : 2)
 k_ln_fwd(LnArgs a, Team t, const TX* __restrict__ x, TY* __restrict__ y) {
-  constexpr int NP = kPairs(VEC), S = stages<TX, TY, VEC, MODE>();
+  constexpr int NP = kPairs(VEC), S = stages<TX, TY, VEC, NV, MODE>();
   using R = Ring<VEC, NV, S, TX>;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float scr[2][MAX_THREADS / 32][1];
@@ -230,7 +231,7 @@ struct Fwd {
     static Known known;
     const auto k = k_ln_fwd<TX, TY, VEC, NV, MODE>;
     const int threads = t.lanes * t.teams;
-    const size_t smem = Ring<VEC, NV, stages<TX, TY, VEC, MODE>(), TX>::bytes(threads);
+    const size_t smem = Ring<VEC, NV, stages<TX, TY, VEC, NV, MODE>(), TX>::bytes(threads);
     int per = 0;
     const cudaError_t e = blocks_per_sm(k, &known, threads, smem, &per);
     if (e != cudaSuccess) return e;

@@ -1,12 +1,15 @@
 // ln.cuh -- layer norm of rows: what its forward (k_ln.cu) and backward
 // (k_ln_bwd.cu) kernels share (internal).
 //
-// A team of lanes (8 to 512 threads) takes a row at a time: each lane holds NV
-// vectors of VEC consecutive channels in registers from the load to the store,
-// so that a row is read once, whatever its sums need.  Rows are copied to shared
-// memory STAGES ahead: a lane copies the vectors that it will read itself, so
-// nothing but its own copies is waited for, and the loads in flight (three rows a
-// team) take no registers.  Both directions are bound by DRAM.
+// A team of lanes (part of a warp, a warp or several) takes a row at a time: each lane
+// holds NV units of VEC channels in registers from the load to the store, so that a row
+// is read once, whatever its sums need.  Rows are copied to shared memory one to three
+// ahead: a lane copies the units that it will read itself, so nothing but its own copies
+// is waited for, and the loads in flight take no registers.  Blocks stay and walk the
+// rows.  Both directions are bound by DRAM where a row is many units, by the steps
+// between rows where it is few: 1024 x 1000 rows of 512 in bf16, ragged, 274 us forward
+// and 380 backward (0.93 and 0.94 of a plain copy's rate), 512 x 2000 rows of 24 28 and
+// 53 (0.51 and 0.41).
 #pragma once
 #include <algorithm>
 #include <atomic>

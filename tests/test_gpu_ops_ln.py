@@ -109,6 +109,27 @@ def test_matches_64_bits(B, T, C, dtype, out):
     assert n.status() == (0, 0)
 
 
+# Widths for every number of lanes and units: parts of a warp, a warp, several; 16-byte units,
+# pairs, channels apart; a block a row.
+WIDTHS = [3, 4, 5, 6, 8, 10, 16, 18, 24, 32, 36, 48, 50, 72, 96, 100, 127, 144, 192, 250, 256, 264,
+          320, 321, 384, 400, 480, 600, 640, 704, 767, 768, 770, 776, 1002, 1280, 1281, 1536, 2002,
+          2047, 2560, 3000, 4094, 6144, 8190, 8192, 12288, 16386]
+
+
+@pytest.mark.parametrize("C", WIDTHS)
+@pytest.mark.parametrize("dtype,out", [("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16"),
+                                       ("bf16", "f32")])
+def test_every_width(C, dtype, out):
+    B, T = 3, 5
+    case = (B, T, C, dtype, out, False)
+    x, dy, gamma, beta, lengths = _inputs(*case, seed=C)
+    n = rn.LayerNorm(B, T, C, dtype=dtype, out_dtype=out)
+    xg, dyg = _poison(x, lengths, False, float("nan")), _poison(dy, lengths, False, float("inf"))
+    y = n.fwd(xg, gamma.cuda(), beta.cuda(), lengths.cuda())
+    _compare(case, x, dy, gamma, beta, lengths.numpy(), 1e-5, y,
+             *n.bwd(xg, dyg, gamma.cuda(), lengths.cuda()))
+
+
 @pytest.mark.parametrize("B,T,C", [(1, 1, 16), (4, 9, 512), (5, 1, 64), (3, 12, 77), (64, 101, 128)])
 @pytest.mark.parametrize("given", [True, False])
 def test_label_rows_and_parameters_left_out(B, T, C, given):
@@ -279,16 +300,47 @@ def test_the_same_bits_again_in_a_graph_and_on_another_stream():
         assert all(torch.equal(a, b) for a, b in zip(out, ref))
 
 
-def test_more_rows_than_the_grid():
-    # rows that walk, ragged: each row against its neighbours' order
-    B, T, C = 700, 90, 40
-    x, dy, gamma, beta, lengths = _inputs(B, T, C, "f32", "f32", seed=6)
-    n = rn.LayerNorm(B, T, C, dtype="f32")
+@pytest.mark.parametrize("B,T,C,dtype", [(700, 90, 40, "f32"), (300, 60, 512, "bf16"),
+                                         (150, 40, 1280, "bf16"), (200, 70, 333, "bf16"),
+                                         (200, 70, 330, "f32"), (90, 60, 1500, "f32")])
+def test_more_rows_than_the_grid(B, T, C, dtype):
+    # teams that walk over many ragged samples
+    x, dy, gamma, beta, lengths = _inputs(B, T, C, dtype, dtype, seed=6)
+    n = rn.LayerNorm(B, T, C, dtype=dtype)
     xg = _poison(x, lengths, False, float("nan"))
     y = n.fwd(xg, gamma.cuda(), beta.cuda(), lengths.cuda())
     dx, dg, db = n.bwd(xg, _poison(dy, lengths, False, float("nan")), gamma.cuda(), lengths.cuda())
-    _compare((B, T, C, "f32", "f32", False), x, dy, gamma, beta, lengths.numpy(), 1e-5, y, dx, dg,
+    _compare((B, T, C, dtype, dtype, False), x, dy, gamma, beta, lengths.numpy(), 1e-5, y, dx, dg,
              db)
+
+
+@pytest.mark.parametrize("C,dtype", [(56, "f32"), (720, "bf16"), (1544, "bf16"), (131, "bf16")])
+def test_a_first_call_may_be_captured(C, dtype):
+    x, dy, gamma, beta, lengths = (t.cuda() for t in _inputs(4, 6, C, dtype, dtype, seed=2))
+    n = rn.LayerNorm(4, 6, C, dtype=dtype)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = [n.fwd(x, gamma, beta, lengths), *n.bwd(x, dy, gamma, lengths)]
+    g.replay()
+    torch.cuda.synchronize()
+    ref = [n.fwd(x, gamma, beta, lengths), *n.bwd(x, dy, gamma, lengths)]
+    assert all(torch.equal(a, b) for a, b in zip(out, ref))
+
+
+def test_rows_of_infinities_and_nan_stay_by_themselves():
+    # (rows that share a warp)
+    for C, dtype in ((16, "f32"), (64, "bf16"), (130, "bf16"), (512, "bf16")):
+        x, dy, gamma, beta, lengths = (t.cuda() for t in _inputs(2, 40, C, dtype, dtype, full=True))
+        n = rn.LayerNorm(2, 40, C, dtype=dtype)
+        ref = n.fwd(x, gamma, beta), n.bwd(x, dy, gamma)[0]
+        bad = x.clone()
+        bad[0, 3, 1], bad[0, 7, 0], bad[1, 39, C - 1] = float("inf"), float("nan"), -float("inf")
+        got = n.fwd(bad, gamma, beta), n.bwd(bad, dy, gamma)[0]
+        hit = torch.zeros(2, 40, dtype=torch.bool, device="cuda")
+        hit[0, 3] = hit[0, 7] = hit[1, 39] = True
+        for a, b in zip(got, ref):
+            assert torch.equal(a[~hit], b[~hit])
+            assert torch.isnan(a[hit].float()).any(1).all()
 
 
 def test_offsets_past_32_bits():
