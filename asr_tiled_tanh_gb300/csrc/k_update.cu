@@ -197,21 +197,33 @@ k_clip_squares(const __grid_constant__ NormTable<N> t, double* __restrict__ part
   if (threadIdx.x == 0) part[blockIdx.x] = add ? part[blockIdx.x] + sum : sum;
 }
 
-__global__ void __launch_bounds__(UT)
-k_clip_norm(const double* __restrict__ part, int n, float max_norm, float eps,
-            float* __restrict__ clip) {
-  __shared__ double scr[UT / 32];
-  ptx::griddep_launch();
-  ptx::griddep_wait();
+// What the sums of squares and the limit make of it, for the block's first thread.
+struct NormArgs {
+  const double* part;
+  int n;  // sums; 0: an earlier launch has left (norm, scale) in clip
+  float max_norm, eps;
+  float* clip;
+};
+__device__ __forceinline__ float2 clip_of(const NormArgs& a, double* scr) {
   double sum = 0;
 #pragma unroll
   for (int k = 0; k < PARTS / UT; ++k)
-    if (threadIdx.x + k * UT < n) sum += __ldcg(part + threadIdx.x + k * UT);
+    if (threadIdx.x + k * UT < a.n) sum += __ldcg(a.part + threadIdx.x + k * UT);
   sum = block_sum<UT>(sum, scr);
+  float2 c = make_float2(0.f, 0.f);
+  if (threadIdx.x == 0) c = norm_and_scale(sum, a.max_norm, a.eps);
+  return c;
+}
+
+__global__ void __launch_bounds__(UT)
+k_clip_norm(NormArgs a) {
+  __shared__ double scr[UT / 32];
+  ptx::griddep_launch();
+  ptx::griddep_wait();
+  const float2 c = clip_of(a, scr);
   if (threadIdx.x == 0) {
-    const float2 c = norm_and_scale(sum, max_norm, eps);
-    clip[0] = c.x;
-    clip[1] = c.y;
+    a.clip[0] = c.x;
+    a.clip[1] = c.y;
   }
 }
 
@@ -254,13 +266,27 @@ __device__ __forceinline__ void scale_chunk(const void* g, void* into, long long
   }
 }
 
-// (Three blocks an SM: 336M elements in bf16 312 us with the norm, 340 with two, 314 with
-// four, 323 with five; 4.7M in fp32 14.0, 13.4, 15.1 and 17.6.)
+// Every block adds up the sums of squares for itself: 8 KB from L2, where another launch
+// between them takes 2 us.  (Three blocks an SM: 336M elements in bf16 312 us with the
+// norm, 340 with two, 314 with four, 323 with five; 4.7M in fp32 14.0, 13.4, 15.1, 17.6.)
 template <int N>
 __global__ void __launch_bounds__(UT, 3)
-k_clip_scale(const __grid_constant__ ScaleTable<N> t, const float* clip) {
+k_clip_scale(const __grid_constant__ ScaleTable<N> t, NormArgs a) {
+  __shared__ double scr[UT / 32];
+  __shared__ float scale_s;
   ptx::griddep_wait();
-  const float s = __ldcg(clip + 1);
+  if (a.n) {
+    const float2 c = clip_of(a, scr);
+    if (threadIdx.x == 0) {
+      scale_s = c.y;
+      if (blockIdx.x == 0) {
+        a.clip[0] = c.x;
+        a.clip[1] = c.y;
+      }
+    }
+    __syncthreads();
+  }
+  const float s = a.n ? scale_s : __ldcg(a.clip + 1);
 #pragma unroll 1
   for (Walk<N> w = backwards(t.c); w.on(t.c); w.next(t.c)) {
     const void* g = t.g[w.i];
@@ -274,9 +300,13 @@ k_clip_scale(const __grid_constant__ ScaleTable<N> t, const float* clip) {
 
 // ---- short lists --------------------------------------------------------------------
 // Norm and scaling in one launch of one cluster: its blocks add up each other's sums
-// in shared memory.  A launch costs the host 2.4 us and the GPU about 2, which is
-// most of what few elements cost.
+// in shared memory.  A program that calls for few elements waits for its host, which a
+// launch costs 2.4 us (eight tensors of 14 thousand elements 12.2 us as called from
+// Python, 16.0 in two launches; on the GPU alone 6.9 and 5.6, 200 thousand 7.2 and 5.2).
 constexpr int CBLOCKS = 16, CGROUPS = 2;  // blocks at most, and their groups of UT threads
+// What one cluster takes in one launch: up to as many chunks (262,144 elements) as its
+// groups of threads take once.
+constexpr int SHORT = CBLOCKS * CGROUPS;
 
 // value at the same shared address of another block of the cluster
 __device__ __forceinline__ double peer_f64(const double* mine, int rank) {
@@ -294,9 +324,8 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // (into[0] NULL: the norm alone)
-template <int N>
 __global__ void __launch_bounds__(UT * CGROUPS)
-k_clip_short(const __grid_constant__ ScaleTable<N> t, float max_norm, float eps,
+k_clip_short(const __grid_constant__ ScaleTable<SHORT> t, float max_norm, float eps,
              float* __restrict__ clip) {
   __shared__ double scr[UT * CGROUPS / 32], mine;
   __shared__ float scale_s;
@@ -305,7 +334,7 @@ k_clip_short(const __grid_constant__ ScaleTable<N> t, float max_norm, float eps,
   const int first = blockIdx.x * CGROUPS + group, step = gridDim.x * CGROUPS;
   double sum = 0;
 #pragma unroll 1
-  for (Walk<N> w(t.c, first, step); w.on(t.c); w.next(t.c)) {
+  for (Walk<SHORT> w(t.c, first, step); w.on(t.c); w.next(t.c)) {
     const void* g = t.g[w.i];
     const bool vec = t.c.vec[w.i];
     sum += t.c.bf16[w.i] ? chunk_squares<true>(g, w.at, w.n, vec, tid)
@@ -331,7 +360,7 @@ k_clip_short(const __grid_constant__ ScaleTable<N> t, float max_norm, float eps,
   if (!t.into[0]) return;
   const float s = scale_s;
 #pragma unroll 1
-  for (Walk<N> w(t.c, first, step); w.on(t.c); w.next(t.c)) {
+  for (Walk<SHORT> w(t.c, first, step); w.on(t.c); w.next(t.c)) {
     const void* g = t.g[w.i];
     void* into = t.into[w.i];
     const bool vec = t.c.vec[w.i];
@@ -642,7 +671,7 @@ cudaError_t launch_squares(const rnnt_grad_list* l, const void* const* grads, do
 
 template <int N>
 cudaError_t launch_scale(const rnnt_grad_list* l, const void* const* grads, void* const* into,
-                         const float* clip, int* launches, cudaStream_t st) {
+                         NormArgs a, int* launches, cudaStream_t st) {
   static std::atomic<int> known[kDeviceSlots];
   int most = 0;
   cudaError_t e = resident(k_clip_scale<N>, known, &most);
@@ -654,23 +683,19 @@ cudaError_t launch_scale(const rnnt_grad_list* l, const void* const* grads, void
       return quads(grads[j], t.c.bf16[k]) && quads(into[j], t.c.bf16[k]);
     });
     if (!t.c.n) break;
-    // (only the first may start under the norm: a later one's tail says nothing of it)
-    e = launch(k_clip_scale<N>, std::min(most, t.c.first[t.c.n]), *launches == 0, st, t, clip);
+    // (only the first may start under the squares: a later one's tail says nothing of them)
+    e = launch(k_clip_scale<N>, std::min(most, t.c.first[t.c.n]), *launches == 0, st, t, a);
+    a.n = 0;
     ++*launches;
   }
   return e;
 }
 
-// What one cluster takes in one launch: up to as many chunks (262,144 elements) as
-// its groups of threads take once.
-constexpr int SHORT = CBLOCKS * CGROUPS;
-
-// The whole call.
-template <int N>
+// The whole call.  (So few chunks are of as few tensors, and all of them have one.)
 cudaError_t launch_short(const rnnt_grad_list* l, const void* const* grads, void* const* into,
                          float max_norm, float eps, float* clip, cudaStream_t st) {
   static std::atomic<bool> known[kDeviceSlots];
-  ScaleTable<N> t;
+  ScaleTable<SHORT> t;
   t.into[0] = nullptr;
   next_chunks(l, 0, &t.c, [&](int k, int j) {
     t.g[k] = grads[j];
@@ -680,7 +705,7 @@ cudaError_t launch_short(const rnnt_grad_list* l, const void* const* grads, void
   std::atomic<bool>& d = known[device_slot()];
   if (!d.load()) {
     const cudaError_t e = cudaFuncSetAttribute(
-        k_clip_short<N>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        k_clip_short, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     d.store(true);
   }
@@ -696,7 +721,7 @@ cudaError_t launch_short(const rnnt_grad_list* l, const void* const* grads, void
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_clip_short<N>, t, max_norm, eps, clip);
+  return cudaLaunchKernelEx(&cfg, k_clip_short, t, max_norm, eps, clip);
 }
 
 struct AdamLists {
@@ -766,25 +791,27 @@ rnnt_status rnnt_clip(const rnnt_grad_list* list, const void* const* grads, void
   const bool few = list->n <= FEW;
   long long chunks = 0;
   for (int i = 0; i < list->n; ++i) chunks += cdiv(list->count[i], CHUNK);
-  if (list->n <= MANY && chunks <= SHORT) {
-    OPS_LAUNCH("clip_norm",
-               (few ? launch_short<FEW>(list, grads, into, max_norm, eps, clip, st)
-                    : launch_short<MANY>(list, grads, into, max_norm, eps, clip, st)));
+  if (chunks <= SHORT) {
+    OPS_LAUNCH("clip_norm", launch_short(list, grads, into, max_norm, eps, clip, st));
     return RNNT_OK;
   }
+  NormArgs a{part, 0, max_norm, eps, clip};
   {
     ProfScope ps("clip_norm", st);
-    int blocks = 0, launches = 0;
-    OPS_CHECK((few ? launch_squares<FEW>(list, grads, part, &blocks, &launches, st)
-                   : launch_squares<MANY>(list, grads, part, &blocks, &launches, st)));
-    OPS_CHECK(launch(k_clip_norm, 1, true, st, part, blocks, max_norm, eps, clip));
-    ps.set_kernels(launches + 1);
+    int launches = 0;
+    OPS_CHECK((few ? launch_squares<FEW>(list, grads, part, &a.n, &launches, st)
+                   : launch_squares<MANY>(list, grads, part, &a.n, &launches, st)));
+    if (!into) {
+      OPS_CHECK(launch(k_clip_norm, 1, true, st, a));
+      ++launches;
+    }
+    ps.set_kernels(launches);
   }
   if (!into) return RNNT_OK;
   ProfScope ps("clip_scale", st);
   int launches = 0;
-  OPS_CHECK((few ? launch_scale<FEW>(list, grads, into, clip, &launches, st)
-                 : launch_scale<MANY>(list, grads, into, clip, &launches, st)));
+  OPS_CHECK((few ? launch_scale<FEW>(list, grads, into, a, &launches, st)
+                 : launch_scale<MANY>(list, grads, into, a, &launches, st)));
   ps.set_kernels(launches);
   return RNNT_OK;
 }

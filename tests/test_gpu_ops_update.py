@@ -113,9 +113,19 @@ def test_small_entries_beside_large_ones():
 
 
 def test_no_elements_and_zeros():
-    for shapes in ([], [(0,), (4, 0)]):
+    for shapes in ([], [(0,), (4, 0)], [(0,)] * 600, [(2, 0)] * 600 + [(0, 3)]):
         c = rn.GradClip(shapes, max_norm=2.0)
         assert c.clip([torch.empty(k, device="cuda") for k in shapes]).tolist() == [0.0, 1.0]
+    shapes = [(0,)] * 600 + [(7,)]  # one tensor with elements behind many without
+    grads = [torch.full(k, 2.0, device="cuda") for k in shapes]
+    c = rn.GradClip(shapes, max_norm=1.0)
+    _check_clip(c.clip(grads), [torch.full((7,), 2.0, device="cuda")], 1.0, 1e-6)
+    o = rn.AdamW(shapes)
+    o.step([torch.zeros(k, device="cuda") for k in shapes], grads, 0.1)
+    assert o.steps.tolist() == [1, 0]
+    o = rn.AdamW([(0,)] * 600)
+    o.step(grads[:600], grads[:600], 0.1)
+    assert o.steps.tolist() == [0, 0]  # nothing to update
     z = [torch.zeros(100, 30, device="cuda")]
     assert rn.GradClip([(100, 30)], max_norm=2.0).clip(z).tolist() == [0.0, 1.0]
 
