@@ -14,7 +14,6 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(BUILD, "librnnt_gb300.so")
-LISTS = os.path.join(BUILD, "rnnt_lists.so")
 LISTS_SRC = os.path.join(CSRC, "lists.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -47,18 +46,26 @@ def up_to_date() -> bool:
 _lists_tried = False
 
 
+def lists_path() -> str:
+    """The helper for lists of tensors: built for one version of Python and of torch."""
+    import torch
+    return os.path.join(BUILD, f"rnnt_lists-{sys.version_info[0]}.{sys.version_info[1]}"
+                               f"-{torch.__version__}.so")
+
+
 def _start_lists(force: bool):
     """The compiler of the helper at work on it; None where it is up to date, or cannot be built
     (ops.py then takes lists apart in Python)."""
     global _lists_tried
-    fresh = os.path.exists(LISTS) and os.path.getmtime(LISTS) >= os.path.getmtime(LISTS_SRC)
+    path = lists_path()
+    fresh = os.path.exists(path) and os.path.getmtime(path) >= os.path.getmtime(LISTS_SRC)
     if (fresh or _lists_tried) and not force:
         return None
     _lists_tried = True
     import torch
     t = os.path.dirname(torch.__file__)
     lib = os.path.join(t, "lib")
-    tmp = LISTS + f".{os.getpid()}.tmp"
+    tmp = path + f".{os.getpid()}.tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
            "-I", os.path.join(t, "include"),
            "-I", os.path.join(t, "include", "torch", "csrc", "api", "include"), LISTS_SRC, "-o",
@@ -77,7 +84,7 @@ def _finish_lists(job):
     tmp, p = job
     out, _ = p.communicate()
     if p.returncode == 0:
-        os.replace(tmp, LISTS)
+        os.replace(tmp, lists_path())
     else:
         print(f"{LISTS_SRC}: not built\n{out.decode(errors='replace')}", file=sys.stderr)
 

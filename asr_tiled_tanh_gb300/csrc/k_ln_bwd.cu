@@ -281,7 +281,9 @@ k_ln_params(const float2* __restrict__ part, int n, int C, float* __restrict__ d
   if (dbeta) dbeta[c] = s.y;
 }
 
-constexpr int PART_ROWS = 608;  // (the workspace may not depend on the device)
+// Rows of sums that the workspace holds (it may not depend on the device), for rows that
+// a team may take and for those that none does.
+constexpr int PART_ROWS = 608, WIDE_ROWS = 64, WIDE = 24 * MAX_THREADS;
 
 template <typename TX, typename TY>
 struct Bwd {
@@ -326,7 +328,7 @@ cudaError_t ln_bwd(const LnArgs& a, const void* x, const void* dy, void* dx, flo
   k<<<std::min(a.rows, 4 * num_sms()), WT, 0, st>>>(a, (const TX*)x, (const TY*)dy, (TX*)dx);
   e = cudaGetLastError();
   if (e != cudaSuccess || !part) return e;
-  const int n = std::min(64, part_rows_max(a));
+  const int n = std::min(WIDE_ROWS, part_rows_max(a));
   const auto c = wide ? k_ln_cols<TX, TY, V16> : k_ln_cols<TX, TY, 1>;
   c<<<dim3((unsigned)cdiv(a.C, 32 * (wide ? V16 : 2)), n), CT, 0, st>>>(
       a, (const TX*)x, (const TY*)dy, part, (int)cdiv(a.rows, n));
@@ -338,7 +340,9 @@ cudaError_t ln_bwd(const LnArgs& a, const void* x, const void* dy, void* dx, flo
 
 namespace ln {
 
-int part_rows_max(const LnArgs& a) { return std::min(PART_ROWS, std::max(1, a.rows)); }
+int part_rows_max(const LnArgs& a) {
+  return std::min(a.C > WIDE ? WIDE_ROWS : PART_ROWS, std::max(1, a.rows));
+}
 
 cudaError_t launch_bwd(const LnArgs& a, int x_dtype, int y_dtype, const void* x, const void* dy,
                        void* dx, float2* part, int* part_rows, bool params, cudaStream_t st) {

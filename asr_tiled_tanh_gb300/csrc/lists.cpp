@@ -33,7 +33,8 @@ PyObject* take(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     const int64_t type = *want++, dims = *want++;
     const at::ScalarType s = type ? at::kBFloat16 : at::kFloat;
     bool ok = t.defined() && t.layout() == at::kStrided && t.scalar_type() == s &&
-              t.is_cuda() && t.get_device() == device && t.dim() == dims && t.is_contiguous();
+              t.is_cuda() && t.get_device() == device && t.dim() == dims && t.is_contiguous() &&
+              !t.is_neg();
     for (int64_t d = 0; ok && d < dims; ++d) ok = t.size(d) == want[d];
     if (!ok) return PyLong_FromSsize_t(i);
     want += dims;

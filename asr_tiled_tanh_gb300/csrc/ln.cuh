@@ -197,7 +197,6 @@ __device__ __forceinline__ float2 block_sum(float2 v, float2* scr) {
   return v;
 }
 
-
 // ---- teams ----------------------------------------------------------------------
 constexpr int MAX_THREADS = 512;
 constexpr int STAGES = 3;  // at most
@@ -465,8 +464,9 @@ bool by_team(int C, int vec, const F& f, cudaError_t* e) {
 // type, two elements, or one.
 inline int vec_of(const LnArgs& a, int ex, const void* x, const void* dx, int ey, const void* y) {
   auto all = [&](int v) {
-    return a.C % v == 0 && a.xf % v == 0 && a.yf % v == 0 && (a.B <= 1 || (a.xb % v == 0 && a.yb % v == 0)) &&
-           aligned_to(x, v * ex) && aligned_to(dx, v * ex) && aligned_to(y, v * ey);
+    return a.C % v == 0 && a.xf % v == 0 && a.yf % v == 0 &&
+           (a.B <= 1 || (a.xb % v == 0 && a.yb % v == 0)) && aligned_to(x, v * ex) &&
+           aligned_to(dx, v * ex) && aligned_to(y, v * ey);
   };
   const int v16 = 16 / std::max(ex, ey);
   return all(v16) ? v16 : all(2) ? 2 : 1;

@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import functools
 import importlib.util
 import itertools
 import operator
@@ -383,13 +384,18 @@ _data_of = torch.Tensor.data_ptr
 _PAIR = ((2,), (1,))
 
 
+@functools.lru_cache(None)
 def _load_lists():
     """take() of csrc/lists.cpp, or None where it was not built."""
-    if not os.path.exists(_build.LISTS):
+    path = _build.lists_path()
+    if not os.path.exists(path):
         return None
-    spec = importlib.util.spec_from_file_location("rnnt_lists", _build.LISTS)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
+    spec = importlib.util.spec_from_file_location("rnnt_lists", path)
+    try:
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError:  # (another build of torch under the same version)
+        return None
     return module.take
 
 

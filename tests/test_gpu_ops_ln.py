@@ -221,6 +221,28 @@ def test_gamma_off_16_bytes():
     _compare(case, x, dy, gamma, beta, lengths.numpy(), 1e-5, y, dx, dg, db)
 
 
+@pytest.mark.parametrize("C", [512, 77, 9000])
+def test_what_the_c_side_may_leave_out(C):
+    # no statistics kept, and either or both of the parameters' gradients not wanted
+    B, T = 3, 4
+    x, dy, gamma, beta, lengths = (t.cuda() for t in _inputs(B, T, C, "f32", "f32", seed=1))
+    n = rn.LayerNorm(B, T, C, dtype="f32")
+    y, ref = n.fwd(x, gamma, beta, lengths), n.bwd(x, dy, gamma, lengths)
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    out = torch.full_like(y, 5.0)
+    assert n._fwd(n._d, p(x), p(gamma), p(beta), p(lengths), p(out), None, None,
+                  n._stream(None)) == 0
+    assert torch.equal(out, y)
+    for want in ((0, 0), (1, 0), (0, 1)):
+        dx, dg, db = torch.full_like(x, 5.0), *torch.full((2, C), 5.0, device="cuda")
+        assert n._bwd(n._d, p(x), p(dy), p(gamma), p(lengths), n._saved, p(dx),
+                      p(dg) if want[0] else None, p(db) if want[1] else None, *n._args,
+                      n._stream(None)) == 0
+        assert torch.equal(dx, ref[0])
+        assert torch.equal(dg, ref[1]) if want[0] else torch.all(dg == 5.0)
+        assert torch.equal(db, ref[2]) if want[1] else torch.all(db == 5.0)
+
+
 def test_no_rows_at_all():
     B, T, C = 4, 5, 40
     n = rn.LayerNorm(B, T, C)
