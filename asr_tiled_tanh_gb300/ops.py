@@ -19,6 +19,7 @@ when a call is made.
 from __future__ import annotations
 
 import array
+import copy
 import ctypes
 import functools
 import importlib.util
@@ -410,6 +411,12 @@ class _Kind:
         self._words = array.array("q", words)
         self.at = self._words.buffer_info()[0]
 
+    def called(self, name):
+        """The same of another list."""
+        other = copy.copy(self)
+        other.name = name
+        return other
+
 
 class _ListOp(_Op):
     """An operator on a list of dense tensors of fixed shapes."""
@@ -477,7 +484,7 @@ class GradClip(_ListOp):
         if not self.max_norm >= 0 or not 0 <= self.eps < float("inf") or not (
                 self.max_norm or self.eps):
             raise ValueError(f"max_norm {max_norm}, eps {eps}: not negative, not both 0")
-        self._into = self._kind("into", self._grads.types)
+        self._into = self._grads.called("into")
         self._clip = lib.rnnt_clip
 
     def _call(self, grads, into, out, stream):
@@ -525,8 +532,8 @@ class AdamW(_ListOp):
         self.opts = RnntAdamwOpts(betas[0], betas[1], eps, 0.0, weight_decay if one else 0.0,
                                   self._decays)
         self._o = ctypes.byref(self.opts)
-        self._params, self._m, self._v = (self._kind(k, [torch.float32] * n)
-                                          for k in ("params", "m", "v"))
+        self._params = self._kind("params", [torch.float32] * n)
+        self._m, self._v = self._params.called("m"), self._params.called("v")
         self._copies = self._kind("low", [torch.bfloat16] * n)
         new = lambda: [torch.zeros(k, device=device) for k in self._shapes]  # noqa: E731
         self.m, self.v = (tuple(new() if k is None else k) for k in (m, v))
