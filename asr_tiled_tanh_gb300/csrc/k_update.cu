@@ -28,7 +28,9 @@ struct Chunks {
   int first[N + 1];  // chunks before each tensor
   long long count[N];
   uint8_t bf16[N];   // the gradient's type
-  uint8_t vec[N];    // every tensor of the place is aligned to four elements
+  // elements before the first four that lie on 16 bytes (8 of bf16) in every tensor of
+  // the place (views of buffers that are laid out alike); -1: they differ
+  int8_t head[N];
 };
 
 // Chunks first, first + step, ... (step < 0: downwards) and the one at hand.
@@ -123,21 +125,33 @@ __device__ __forceinline__ double squares(const float (&g)[EACH]) {
   return d;
 }
 
+// A chunk's n elements, by fours from `head` on (head < 0: none) and the others, at most
+// six: other(i) for i below `others`.
+struct Cut {
+  int head, whole, others;
+  __device__ __forceinline__ Cut(int n, int h) {
+    head = min(max(h, 0), n);
+    whole = h < 0 ? 0 : (n - head) & ~3;
+    others = n - whole;
+  }
+  __device__ __forceinline__ int other(int i) const { return i < head ? i : whole + i; }
+};
+
 // The squares of a chunk's n elements from `at` on: a thread's loads all under way
 // before the first is used.
 template <bool BF16>
-__device__ __forceinline__ double chunk_squares(const void* g, long long at, int n, bool vec,
+__device__ __forceinline__ double chunk_squares(const void* g, long long at, int n, int head,
                                                 int tid) {
   using Q = Quad<BF16>;
   float v[EACH];
-  if (vec) {
+  if (head >= 0) {
+    const Cut c(n, head);
     typename Q::U u[EACH / 4];
-    const int whole = n & ~3;
 #pragma unroll
     for (int j = 0; j < EACH / 4; ++j) {
       const int e = (j * UT + tid) * 4;
       u[j] = typename Q::U{};
-      if (e < whole) u[j] = Q::load(g, at + e);
+      if (e < c.whole) u[j] = Q::load(g, at + c.head + e);
     }
 #pragma unroll
     for (int j = 0; j < EACH / 4; ++j) {
@@ -148,8 +162,8 @@ __device__ __forceinline__ double chunk_squares(const void* g, long long at, int
       v[4 * j + 3] = q.w;
     }
     double d = squares(v);
-    if (whole + tid < n) {  // the tensor's last one to three
-      const double q = grad1<BF16>(g, at + whole + tid);
+    if (tid < c.others) {
+      const double q = grad1<BF16>(g, at + c.other(tid));
       d += q * q;
     }
     return d;
@@ -189,9 +203,9 @@ k_clip_squares(const __grid_constant__ NormTable<N> t, double* __restrict__ part
 #pragma unroll 1
   for (Walk<N> w(t.c, blockIdx.x, gridDim.x); w.on(t.c); w.next(t.c)) {
     const void* g = t.g[w.i];
-    const bool vec = t.c.vec[w.i];
-    sum += t.c.bf16[w.i] ? chunk_squares<true>(g, w.at, w.n, vec, threadIdx.x)
-                         : chunk_squares<false>(g, w.at, w.n, vec, threadIdx.x);
+    const int head = t.c.head[w.i];
+    sum += t.c.bf16[w.i] ? chunk_squares<true>(g, w.at, w.n, head, threadIdx.x)
+                         : chunk_squares<false>(g, w.at, w.n, head, threadIdx.x);
   }
   sum = block_sum<UT>(sum, scr);
   if (threadIdx.x == 0) part[blockIdx.x] = add ? part[blockIdx.x] + sum : sum;
@@ -237,32 +251,33 @@ struct ScaleTable {
 
 template <bool BF16>
 __device__ __forceinline__ void scale_chunk(const void* g, void* into, long long at, int n,
-                                            bool vec, float s, int tid) {
+                                            int head, float s, int tid) {
   using Q = Quad<BF16>;
-  int done = 0;
-  if (vec) {
-    done = n & ~3;
+  const Cut c(n, head);
+  if (c.whole) {
     typename Q::U u[EACH / 4];
 #pragma unroll
     for (int j = 0; j < EACH / 4; ++j) {
       const int e = (j * UT + tid) * 4;
-      if (e < done) u[j] = Q::load(g, at + e);
+      if (e < c.whole) u[j] = Q::load(g, at + c.head + e);
     }
 #pragma unroll
     for (int j = 0; j < EACH / 4; ++j) {
       const int e = (j * UT + tid) * 4;
-      if (e >= done) continue;
+      if (e >= c.whole) continue;
+      const long long to = at + c.head + e;
       float4 q = Q::widen(u[j]);
       q = make_float4(s * q.x, s * q.y, s * q.z, s * q.w);
-      if constexpr (BF16) *(uint2*)((__nv_bfloat16*)into + at + e) = pack4(q);
-      else *(float4*)((float*)into + at + e) = q;
+      if constexpr (BF16) *(uint2*)((__nv_bfloat16*)into + to) = pack4(q);
+      else *(float4*)((float*)into + to) = q;
     }
   }
 #pragma unroll 8
-  for (int e = done + tid; e < n; e += UT) {
-    const float v = s * grad1<BF16>(g, at + e);
-    if constexpr (BF16) ((__nv_bfloat16*)into)[at + e] = __float2bfloat16_rn(v);
-    else ((float*)into)[at + e] = v;
+  for (int i = tid; i < c.others; i += UT) {
+    const long long e = at + c.other(i);
+    const float v = s * grad1<BF16>(g, e);
+    if constexpr (BF16) ((__nv_bfloat16*)into)[e] = __float2bfloat16_rn(v);
+    else ((float*)into)[e] = v;
   }
 }
 
@@ -291,10 +306,10 @@ k_clip_scale(const __grid_constant__ ScaleTable<N> t, NormArgs a) {
   for (Walk<N> w = backwards(t.c); w.on(t.c); w.next(t.c)) {
     const void* g = t.g[w.i];
     void* into = t.into[w.i];
-    const bool vec = t.c.vec[w.i];
+    const int head = t.c.head[w.i];
     if (s == 1.f && g == into) continue;
-    if (t.c.bf16[w.i]) scale_chunk<true>(g, into, w.at, w.n, vec, s, threadIdx.x);
-    else scale_chunk<false>(g, into, w.at, w.n, vec, s, threadIdx.x);
+    if (t.c.bf16[w.i]) scale_chunk<true>(g, into, w.at, w.n, head, s, threadIdx.x);
+    else scale_chunk<false>(g, into, w.at, w.n, head, s, threadIdx.x);
   }
 }
 
@@ -336,9 +351,9 @@ k_clip_short(const __grid_constant__ ScaleTable<SHORT> t, float max_norm, float 
 #pragma unroll 1
   for (Walk<SHORT> w(t.c, first, step); w.on(t.c); w.next(t.c)) {
     const void* g = t.g[w.i];
-    const bool vec = t.c.vec[w.i];
-    sum += t.c.bf16[w.i] ? chunk_squares<true>(g, w.at, w.n, vec, tid)
-                         : chunk_squares<false>(g, w.at, w.n, vec, tid);
+    const int head = t.c.head[w.i];
+    sum += t.c.bf16[w.i] ? chunk_squares<true>(g, w.at, w.n, head, tid)
+                         : chunk_squares<false>(g, w.at, w.n, head, tid);
   }
   sum = block_sum<UT * CGROUPS>(sum, scr);
   if (threadIdx.x == 0) mine = sum;
@@ -363,10 +378,10 @@ k_clip_short(const __grid_constant__ ScaleTable<SHORT> t, float max_norm, float 
   for (Walk<SHORT> w(t.c, first, step); w.on(t.c); w.next(t.c)) {
     const void* g = t.g[w.i];
     void* into = t.into[w.i];
-    const bool vec = t.c.vec[w.i];
+    const int head = t.c.head[w.i];
     if (s == 1.f && g == into) continue;
-    if (t.c.bf16[w.i]) scale_chunk<true>(g, into, w.at, w.n, vec, s, tid);
-    else scale_chunk<false>(g, into, w.at, w.n, vec, s, tid);
+    if (t.c.bf16[w.i]) scale_chunk<true>(g, into, w.at, w.n, head, s, tid);
+    else scale_chunk<false>(g, into, w.at, w.n, head, s, tid);
   }
 }
 
@@ -418,38 +433,36 @@ struct Tensors {
 };
 template <bool BF16>
 __device__ __forceinline__ void adam_chunk(const Tensors& x, const void* g, long long at, int n,
-                                           bool vec, const AdamStep& f) {
+                                           int head, const AdamStep& f) {
   using Q = Quad<BF16>;
-  int done = 0;
-  if (vec) {
-    done = n & ~3;
+  const Cut c(n, head);
 #pragma unroll 1
-    for (int e0 = threadIdx.x * 4; e0 < done; e0 += AHEAD * UT * 4) {
-      float4 p[AHEAD], m[AHEAD], v[AHEAD];
-      typename Q::U u[AHEAD];
+  for (int e0 = threadIdx.x * 4; e0 < c.whole; e0 += AHEAD * UT * 4) {
+    float4 p[AHEAD], m[AHEAD], v[AHEAD];
+    typename Q::U u[AHEAD];
 #pragma unroll
-      for (int j = 0; j < AHEAD; ++j) {
-        const int e = e0 + j * UT * 4;
-        if (e >= done) continue;
-        p[j] = *(const float4*)(x.p + e);
-        m[j] = *(const float4*)(x.m + e);
-        v[j] = *(const float4*)(x.v + e);
-        u[j] = Q::load(g, at + e);
-      }
+    for (int j = 0; j < AHEAD; ++j) {
+      const int e = c.head + e0 + j * UT * 4;
+      if (e0 + j * UT * 4 >= c.whole) continue;
+      p[j] = *(const float4*)(x.p + e);
+      m[j] = *(const float4*)(x.m + e);
+      v[j] = *(const float4*)(x.v + e);
+      u[j] = Q::load(g, at + e);
+    }
 #pragma unroll
-      for (int j = 0; j < AHEAD; ++j) {
-        const int e = e0 + j * UT * 4;
-        if (e >= done) continue;
-        f(p[j], m[j], v[j], Q::widen(u[j]));
-        *(float4*)(x.p + e) = p[j];
-        *(float4*)(x.m + e) = m[j];
-        *(float4*)(x.v + e) = v[j];
-        if (x.low) *(uint2*)(x.low + e) = pack4(p[j]);
-      }
+    for (int j = 0; j < AHEAD; ++j) {
+      const int e = c.head + e0 + j * UT * 4;
+      if (e0 + j * UT * 4 >= c.whole) continue;
+      f(p[j], m[j], v[j], Q::widen(u[j]));
+      *(float4*)(x.p + e) = p[j];
+      *(float4*)(x.m + e) = m[j];
+      *(float4*)(x.v + e) = v[j];
+      if (x.low) *(uint2*)(x.low + e) = pack4(p[j]);
     }
   }
 #pragma unroll 4
-  for (int e = done + threadIdx.x; e < n; e += UT) {
+  for (int i = threadIdx.x; i < c.others; i += UT) {
+    const int e = c.other(i);
     float p = x.p[e], m = x.m[e], v = x.v[e];
     f(p, m, v, grad1<BF16>(g, at + e));
     x.p[e] = p;
@@ -481,8 +494,8 @@ k_adamw(const __grid_constant__ AdamTable<N> t, AdamArgs a) {
       const Tensors x{t.p[w.i] + w.at, t.m[w.i] + w.at, t.v[w.i] + w.at,
                       t.low[w.i] ? t.low[w.i] + w.at : nullptr};
       f.decay = t.decay[w.i];
-      if (t.c.bf16[w.i]) adam_chunk<true>(x, t.g[w.i], w.at, w.n, t.c.vec[w.i], f);
-      else adam_chunk<false>(x, t.g[w.i], w.at, w.n, t.c.vec[w.i], f);
+      if (t.c.bf16[w.i]) adam_chunk<true>(x, t.g[w.i], w.at, w.n, t.c.head[w.i], f);
+      else adam_chunk<false>(x, t.g[w.i], w.at, w.n, t.c.head[w.i], f);
     }
   }
   // The last block to come here counts the update, when every block has read the
@@ -592,9 +605,11 @@ class Spans {
   }
 };
 
-// The next launch's tensors, from i on, into c; fill(k, j): tensor j is its k-th,
-// and returns whether its places are aligned to four elements.  Returns the tensor
-// after them.
+// Elements before the first four that lie together in p (0 to 3).
+int head_of(const void* p, bool bf16) { return (int)(-(intptr_t)((uintptr_t)p / (bf16 ? 2 : 4)) & 3); }
+
+// The next launch's tensors, from i on, into c; fill(k, j): tensor j is its k-th, and
+// returns its head.  Returns the tensor after them.
 template <int N, typename F>
 int next_chunks(const rnnt_grad_list* l, int i, Chunks<N>* c, F fill) {
   c->n = 0;
@@ -607,13 +622,10 @@ int next_chunks(const rnnt_grad_list* l, int i, Chunks<N>* c, F fill) {
     c->count[k] = l->count[i];
     c->bf16[k] = is_bf16(l, i);
     c->first[k + 1] = c->first[k] + (int)chunks;
-    c->vec[k] = fill(k, i);
+    c->head[k] = (int8_t)fill(k, i);
   }
   return i;
 }
-
-// Aligned to four elements of fp32, or of bf16.
-bool quads(const void* p, bool bf16) { return aligned_to(p, bf16 ? 8 : 16); }
 
 // Blocks of a kernel that the card holds at a time, asked once per kernel and device.
 template <typename K>
@@ -657,7 +669,7 @@ cudaError_t launch_squares(const rnnt_grad_list* l, const void* const* grads, do
     NormTable<N> t;
     i = next_chunks(l, i, &t.c, [&](int k, int j) {
       t.g[k] = grads[j];
-      return quads(grads[j], t.c.bf16[k]);
+      return head_of(grads[j], t.c.bf16[k]);
     });
     // (every launch of a call fills the same sums)
     if (!*launches)
@@ -680,7 +692,8 @@ cudaError_t launch_scale(const rnnt_grad_list* l, const void* const* grads, void
     i = next_chunks(l, i, &t.c, [&](int k, int j) {
       t.g[k] = grads[j];
       t.into[k] = into[j];
-      return quads(grads[j], t.c.bf16[k]) && quads(into[j], t.c.bf16[k]);
+      const int h = head_of(grads[j], t.c.bf16[k]);
+      return h == head_of(into[j], t.c.bf16[k]) ? h : -1;
     });
     if (!t.c.n) break;
     // (only the first may start under the squares: a later one's tail says nothing of them)
@@ -700,7 +713,8 @@ cudaError_t launch_short(const rnnt_grad_list* l, const void* const* grads, void
   next_chunks(l, 0, &t.c, [&](int k, int j) {
     t.g[k] = grads[j];
     t.into[k] = into ? into[j] : nullptr;
-    return quads(grads[j], t.c.bf16[k]) && quads(t.into[k], t.c.bf16[k]);
+    const int h = head_of(grads[j], t.c.bf16[k]);
+    return !into || h == head_of(into[j], t.c.bf16[k]) ? h : -1;
   });
   std::atomic<bool>& d = known[device_slot()];
   if (!d.load()) {
@@ -748,8 +762,10 @@ cudaError_t launch_adamw(const rnnt_grad_list* l, const rnnt_adamw_opts* o, cons
     t.v[k] = x.v[j];
     t.low[k] = x.low ? (__nv_bfloat16*)x.low[j] : nullptr;
     t.decay[k] = o->decays ? o->decays[j] : o->decay;
-    return quads(x.g[j], t.c.bf16[k]) && quads(x.p[j], false) && quads(x.m[j], false) &&
-           quads(x.v[j], false) && quads(t.low[k], true);
+    const int h = head_of(x.g[j], t.c.bf16[k]);
+    const bool alike = h == head_of(x.p[j], false) && h == head_of(x.m[j], false) &&
+                       h == head_of(x.v[j], false) && (!t.low[k] || h == head_of(t.low[k], true));
+    return alike ? h : -1;
   });
   *left -= t.c.n;
   a.last = *left == 0;

@@ -164,6 +164,23 @@ def test_tensors_off_16_bytes(kind, shift):
         assert torch.all(b == 9.0)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_views_of_one_buffer_without_gaps(kind):
+    # tensors that begin anywhere, alike in both lists
+    n = [1, 5001, 3, 8191, 8192, 2, 20001]
+    flat, out = (torch.zeros(sum(n) + 9, dtype=DT[kind], device="cuda") for _ in range(2))
+    flat.copy_(_grads([(sum(n) + 9,)], [kind], seed=3)[0])
+    at = np.cumsum([0, *n])
+    for move in (0, 1):
+        grads = [flat[a:a + k] for a, k in zip(at, n)]
+        into = [out[a + move:a + move + k] for a, k in zip(at, n)]
+        out.fill_(9.0)
+        scale = _check_clip(rn.GradClip([(k,) for k in n], dtype=kind).clip(grads, into=into),
+                            grads, 1.0, 1e-6)
+        _check_scaled(into, grads, scale)
+        assert torch.all(out[:move] == 9.0) and torch.all(out[sum(n) + move:] == 9.0)
+
+
 # ---- AdamW
 
 OPT = dict(betas=(0.9, 0.999), eps=1e-8)
@@ -300,6 +317,22 @@ def test_adamw_off_16_bytes(shift, which):
         assert torch.equal(L[i], P[i].bfloat16())
     for buf, at, k, name in bufs:
         assert torch.all(buf[:at] == 9.0) and torch.all(buf[at + k:] == 9.0), name
+
+
+def test_adamw_on_views_of_buffers_without_gaps():
+    n = [1, 5001, 3, 8191, 8192, 2, 20001]
+    total, at = sum(n), np.cumsum([0, *n])
+    cut = lambda t: [t[a:a + k] for a, k in zip(at, n)]  # noqa: E731
+    (p,), (m,), (v,) = _state([(total + 5,)], seed=2)
+    g = _grads([(total + 5,)], ["bf16"], seed=9)[0]
+    low = torch.full((total + 5,), 9.0, dtype=torch.bfloat16, device="cuda")
+    keep = [x.clone() for x in (p, m, v, g)]
+    o = rn.AdamW([(k,) for k in n], grad_dtype="bf16", m=cut(m), v=cut(v))
+    o.step(cut(p), cut(g), 0.01, low=cut(low))
+    ref, bound = _adam64(*[x[:total] for x in keep], 1, 0.01, 0.01)
+    _within((p[:total], m[:total], v[:total]), ref, bound, "views")
+    assert torch.equal(low[:total], p[:total].bfloat16()) and torch.all(low[total:] == 9.0)
+    assert all(torch.equal(a[total:], b[total:]) for a, b in zip((p, m, v), keep))
 
 
 def test_zero_gradients_only_decay():
