@@ -249,6 +249,9 @@ struct ScaleTable {
   void* into[N];
 };
 
+// Single elements under way, where the places differ (68M in bf16 with the norm, 281 us
+// one by one, 189 two together, 141 four, 145 eight, which spill).
+constexpr int SINGLES = 4;
 template <bool BF16>
 __device__ __forceinline__ void scale_chunk(const void* g, void* into, long long at, int n,
                                             int head, float s, int tid) {
@@ -272,12 +275,19 @@ __device__ __forceinline__ void scale_chunk(const void* g, void* into, long long
       else *(float4*)((float*)into + to) = q;
     }
   }
-#pragma unroll 8
-  for (int i = tid; i < c.others; i += UT) {
-    const long long e = at + c.other(i);
-    const float v = s * grad1<BF16>(g, e);
-    if constexpr (BF16) ((__nv_bfloat16*)into)[e] = __float2bfloat16_rn(v);
-    else ((float*)into)[e] = v;
+#pragma unroll 1
+  for (int i0 = tid; i0 < c.others; i0 += SINGLES * UT) {
+    float v[SINGLES];
+#pragma unroll
+    for (int j = 0; j < SINGLES; ++j)
+      if (i0 + j * UT < c.others) v[j] = s * grad1<BF16>(g, at + c.other(i0 + j * UT));
+#pragma unroll
+    for (int j = 0; j < SINGLES; ++j) {
+      if (i0 + j * UT >= c.others) continue;
+      const long long e = at + c.other(i0 + j * UT);
+      if constexpr (BF16) ((__nv_bfloat16*)into)[e] = __float2bfloat16_rn(v[j]);
+      else ((float*)into)[e] = v[j];
+    }
   }
 }
 
@@ -425,6 +435,9 @@ struct AdamStep {
 // Quads of each tensor that a thread has under way (336M elements: 1,764 us with the
 // norm for one, 1,715 for two, 1,895 for four, which leave one block an SM less).
 constexpr int AHEAD = 2;
+// (and single elements, where the tensors' places differ: 68M, 712 us one by one, 511 two
+// together, 561 three, 574 four)
+constexpr int ONES = 2;
 
 // A chunk's parts of p, m, v and low (or NULL).
 struct Tensors {
@@ -460,15 +473,28 @@ __device__ __forceinline__ void adam_chunk(const Tensors& x, const void* g, long
       if (x.low) *(uint2*)(x.low + e) = pack4(p[j]);
     }
   }
-#pragma unroll 4
-  for (int i = threadIdx.x; i < c.others; i += UT) {
-    const int e = c.other(i);
-    float p = x.p[e], m = x.m[e], v = x.v[e];
-    f(p, m, v, grad1<BF16>(g, at + e));
-    x.p[e] = p;
-    x.m[e] = m;
-    x.v[e] = v;
-    if (x.low) x.low[e] = __float2bfloat16_rn(p);
+#pragma unroll 1
+  for (int i0 = threadIdx.x; i0 < c.others; i0 += ONES * UT) {
+    float p[ONES], m[ONES], v[ONES], u[ONES];
+#pragma unroll
+    for (int j = 0; j < ONES; ++j) {
+      const int e = c.other(i0 + j * UT);
+      if (i0 + j * UT >= c.others) continue;
+      p[j] = x.p[e];
+      m[j] = x.m[e];
+      v[j] = x.v[e];
+      u[j] = grad1<BF16>(g, at + e);
+    }
+#pragma unroll
+    for (int j = 0; j < ONES; ++j) {
+      const int e = c.other(i0 + j * UT);
+      if (i0 + j * UT >= c.others) continue;
+      f(p[j], m[j], v[j], u[j]);
+      x.p[e] = p[j];
+      x.m[e] = m[j];
+      x.v[e] = v[j];
+      if (x.low) x.low[e] = __float2bfloat16_rn(p[j]);
+    }
   }
 }
 
