@@ -111,6 +111,31 @@ def _strides(given, rows, width):
     return batch or rows * row, row
 
 
+@functools.lru_cache(None)
+def _helper():
+    """The functions of csrc/lists.cpp, or None where it was not built."""
+    path = _build.lists_path()
+    if not os.path.exists(path):
+        return None
+    spec = importlib.util.spec_from_file_location("rnnt_lists", path)
+    try:
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError:  # (another build of torch under the same version)
+        return None
+    return module
+
+
+class _Want:
+    """What a tensor has to be: type, shape and strides (words: for csrc/lists.cpp)."""
+    _CODES = {torch.float32: 0, torch.bfloat16: 1, torch.int32: 2}
+
+    def __init__(self, dtype, shape, strides):
+        self.dtype, self.layout = dtype, (shape, strides)
+        self._words = array.array("q", [self._CODES[dtype], len(shape), *shape, *strides])
+        self.at = self._words.buffer_info()[0]
+
+
 def _dense(shape):
     """Strides of a dense tensor."""
     return torch.empty(shape, device="meta").stride()
@@ -128,6 +153,21 @@ class _Op:
         self.status_word = torch.zeros(1, dtype=torch.int32, device=device)
         self._args = (self.ws.data_ptr(), ws_bytes, self.status_word.data_ptr())
         self._index = self.ws.device.index
+        self._fast = _helper() if self.ws.is_cuda else None
+
+    def _pointer(self, t, name, want):
+        """_ptr of what is wanted (0.1 us where it is that, 0.5 by _ptr)."""
+        if self._fast is not None:
+            p = self._fast.pointer(t, want.at, self._index)
+            if p is not None:
+                return p
+        return self._ptr(t, name, want.dtype, want.layout)
+
+    def _new(self, want, stream):
+        """_empty of what is wanted."""
+        if stream is None and self._fast is not None:
+            return self._fast.empty(want.at, self._index)
+        return self._empty(want.layout, want.dtype, stream)
 
     def _ptr(self, t, name, dtype, layout):
         """Data pointer of a tensor of the plan's GPU that has exactly this type and layout."""
@@ -290,8 +330,8 @@ class LayerNorm(_Op):
 
     def __init__(self, B, T, C, dtype="bf16", out_dtype=None, eps=1e-5, label_rows=False,
                  x_strides=None, y_strides=None, device="cuda"):
-        xcode, self._xt = _dtype(dtype)
-        ycode, self._yt = _dtype(dtype if out_dtype is None else out_dtype)
+        xcode, xt = _dtype(dtype)
+        ycode, yt = _dtype(dtype if out_dtype is None else out_dtype)
         xs, ys = _strides(x_strides, T, C), _strides(y_strides, T, C)
         self.dims = _dims(RnntLnDims, B, T, C, int(label_rows), xcode, ycode, eps, xs[1], xs[0],
                           ys[1], ys[0])
@@ -302,42 +342,37 @@ class LayerNorm(_Op):
                                  device=device)
         self._saved = self.saved.data_ptr()
         self._fwd, self._bwd = lib.rnnt_ln_fwd, lib.rnnt_ln_bwd
-        self._x = ((B, T, C), (xs[0], xs[1], 1))
-        self._y = ((B, T, C), (ys[0], ys[1], 1))
-        self._c = ((C,), (1,))
-        self._len = ((B,), (1,))
+        self._x = _Want(xt, (B, T, C), (xs[0], xs[1], 1))
+        self._y = _Want(yt, (B, T, C), (ys[0], ys[1], 1))
+        self._c = _Want(torch.float32, (C,), (1,))
+        self._len = _Want(torch.int32, (B,), (1,))
 
-    def _opt(self, t, name, dtype, layout):
-        return None if t is None else self._ptr(t, name, dtype, layout)
+    def _opt(self, t, name, want):
+        return None if t is None else self._pointer(t, name, want)
 
     def fwd(self, x, gamma=None, beta=None, lengths=None, y=None, stream=None):
         """y [B,T,C]; gamma, beta [C] fp32 or None; lengths [B] int32 or None (every row)."""
         if y is None:
-            y = self._empty(self._y, self._yt, stream)
-        f = torch.float32
-        _check(self._fwd(self._d, self._ptr(x, "x", self._xt, self._x),
-                         self._opt(gamma, "gamma", f, self._c), self._opt(beta, "beta", f, self._c),
-                         self._opt(lengths, "lengths", torch.int32, self._len),
-                         self._ptr(y, "y", self._yt, self._y), self._saved, self._args[2],
-                         self._stream(stream)), "rnnt_ln_fwd")
+            y = self._new(self._y, stream)
+        _check(self._fwd(self._d, self._pointer(x, "x", self._x),
+                         self._opt(gamma, "gamma", self._c), self._opt(beta, "beta", self._c),
+                         self._opt(lengths, "lengths", self._len), self._pointer(y, "y", self._y),
+                         self._saved, self._args[2], self._stream(stream)), "rnnt_ln_fwd")
         return y
 
     def bwd(self, x, dy, gamma=None, lengths=None, dx=None, dgamma=None, dbeta=None, stream=None):
         """(dx, dgamma, dbeta) for the x and lengths of the last fwd."""
-        f = torch.float32
         if dx is None:
-            dx = self._empty(self._x, self._xt, stream)
+            dx = self._new(self._x, stream)
         if dgamma is None:
-            dgamma = self._empty(self._c, f, stream)
+            dgamma = self._new(self._c, stream)
         if dbeta is None:
-            dbeta = self._empty(self._c, f, stream)
-        _check(self._bwd(self._d, self._ptr(x, "x", self._xt, self._x),
-                         self._ptr(dy, "dy", self._yt, self._y),
-                         self._opt(gamma, "gamma", f, self._c),
-                         self._opt(lengths, "lengths", torch.int32, self._len), self._saved,
-                         self._ptr(dx, "dx", self._xt, self._x),
-                         self._ptr(dgamma, "dgamma", f, self._c),
-                         self._ptr(dbeta, "dbeta", f, self._c), *self._args,
+            dbeta = self._new(self._c, stream)
+        _check(self._bwd(self._d, self._pointer(x, "x", self._x), self._pointer(dy, "dy", self._y),
+                         self._opt(gamma, "gamma", self._c),
+                         self._opt(lengths, "lengths", self._len), self._saved,
+                         self._pointer(dx, "dx", self._x), self._pointer(dgamma, "dgamma", self._c),
+                         self._pointer(dbeta, "dbeta", self._c), *self._args,
                          self._stream(stream)), "rnnt_ln_bwd")
         return dx, dgamma, dbeta
 
@@ -382,22 +417,8 @@ _is_dense, _index_of = torch.Tensor.is_contiguous, torch.Tensor.get_device
 _data_of = torch.Tensor.data_ptr
 
 
-_PAIR = ((2,), (1,))
-
-
-@functools.lru_cache(None)
-def _load_lists():
-    """take() of csrc/lists.cpp, or None where it was not built."""
-    path = _build.lists_path()
-    if not os.path.exists(path):
-        return None
-    spec = importlib.util.spec_from_file_location("rnnt_lists", path)
-    try:
-        module = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(module)
-    except ImportError:  # (another build of torch under the same version)
-        return None
-    return module.take
+_PAIR = _Want(torch.float32, (2,), (1,))
+_ONE = _Want(torch.float32, (1,), (1,))
 
 
 class _Kind:
@@ -433,7 +454,7 @@ class _ListOp(_Op):
         self.list = RnntGradList(n, self._count, self._codes)
         self._l = ctypes.byref(self.list)
         self._grads = self._kind("grads", [t for _, t in codes])
-        self._take_list = _load_lists()
+        self._take_list = _helper() and _helper().take
         super().__init__(ws_bytes(self._l), what, device)
 
     def _kind(self, name, types):
@@ -489,13 +510,13 @@ class GradClip(_ListOp):
 
     def _call(self, grads, into, out, stream):
         if out is None:
-            out = self._empty(_PAIR, torch.float32, stream)
+            out = self._new(_PAIR, stream)
         held, g = self._take(grads, self._grads)
         w = None
         if into is not None:
             held_w, w = (held, g) if into is grads else self._take(into, self._into)
         _check(self._clip(self._l, g, w, self.max_norm, self.eps,
-                          self._ptr(out, "out", torch.float32, _PAIR), self._args[0],
+                          self._pointer(out, "out", _PAIR), self._args[0],
                           self.ws_bytes, self._stream(stream)), "rnnt_clip")
         return out
 
@@ -552,7 +573,7 @@ class AdamW(_ListOp):
         if self._mv is None:
             self._mv = self._take(self.m, self._m), self._take(self.v, self._v)
         if isinstance(lr, torch.Tensor):
-            lr = self._ptr(lr.reshape(1), "lr", torch.float32, ((1,), (1,)))
+            lr = self._pointer(lr.reshape(1), "lr", _ONE)
         else:
             self.opts.lr, lr = lr, None
         held_p, p = self._take(params, self._params)
@@ -561,7 +582,7 @@ class AdamW(_ListOp):
         if low is not None:
             some = any(map(operator.is_, low, itertools.repeat(None)))
             held_l, w = self._some(low) if some else self._take(low, self._copies)
-        c = None if clip is None else self._ptr(clip, "clip", torch.float32, _PAIR)
+        c = None if clip is None else self._pointer(clip, "clip", _PAIR)
         _check(self._run(self._l, self._o, p, g, self._mv[0][1], self._mv[1][1], w, lr, c,
                          self._steps, self._stream(stream)), "rnnt_adamw")
 

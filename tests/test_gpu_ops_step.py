@@ -11,6 +11,7 @@ import pytest
 import torch
 
 import asr_tiled_tanh_gb300 as rn
+from tests.test_gpu_ops_streams import _stream_of
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +97,49 @@ def test_embedding_norm_clip_and_update(graph):
         assert torch.equal(low[1], dev[1].bfloat16())
     assert adamw.steps.tolist() == [t0 + 3, 0]
     assert embed.status() == rows.status() == (0, 0)
+
+
+@pytest.mark.parametrize("how", ["stream", "handle", "current"])
+def test_results_belong_to_the_calls_stream(how):
+    x, dy = torch.randn(4, 9, 64, device="cuda"), torch.randn(4, 9, 64, device="cuda")
+    g = [torch.randn(300, 7, device="cuda"), torch.randn(5, device="cuda")]
+    n, c = rn.LayerNorm(4, 9, 64, dtype="f32"), rn.GradClip([(300, 7), (5,)])
+
+    def run(**k):
+        return [n.fwd(x, **k), *n.bwd(x, dy, **k), c.norm(g, **k)]
+
+    ref = [t.clone() for t in run()]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    if how == "current":
+        with torch.cuda.stream(s):
+            got = run()
+    else:
+        got = run(stream=s if how == "stream" else s.cuda_stream)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    assert [_stream_of(t) for t in got] == [s.cuda_stream] * len(got)
+
+
+def test_the_helper_and_python_say_the_same():
+    # (what is refused, and the same results where csrc/lists.cpp was not built)
+    x = torch.randn(3, 5, 40, device="cuda")
+    g = [torch.randn(30, device="cuda"), torch.randn(4, 4, device="cuda").bfloat16()]
+    n = rn.LayerNorm(3, 5, 40, dtype="f32")
+    c = rn.GradClip([(30,), (4, 4)], dtype=["f32", "bf16"])
+    assert n._fast is not None and c._take_list is not None
+    out = []
+    for fast in (True, False):
+        if not fast:
+            n._fast = c._fast = c._take_list = None
+        out.append([n.fwd(x), *n.bwd(x, x), c.norm(g)])
+        for bad in (x.bfloat16(), x[:2], x.cpu(), x.transpose(0, 1), x[:, :, ::2], x.expand(3, 5, 40)
+                    .transpose(1, 2), torch.zeros(5, 3, 40, device="cuda"), None):
+            with pytest.raises((ValueError, AttributeError)):
+                n.fwd(bad)
+        for bad in ([g[0]], g[::-1], [g[0], g[1].float()], [g[0], g[1].t()[:2]], [g[0][::2], g[1]],
+                    [g[0].cpu(), g[1]], [g[0].double(), g[1]], [g[0].view(5, 6), g[1]]):
+            with pytest.raises(ValueError):
+                c.norm(bad)
+    assert all(torch.equal(a, b) for a, b in zip(*out))
