@@ -28,8 +28,8 @@ struct Chunks {
   int first[N + 1];  // chunks before each tensor
   long long count[N];
   uint8_t bf16[N];   // the gradient's type
-  // elements before the first four that lie on 16 bytes (8 of bf16) in every tensor of
-  // the place (views of buffers that are laid out alike); -1: they differ
+  // elements before the first four that lie on 16 bytes (8 of bf16) in the tensors of the
+  // place (views of buffers that are laid out alike); -1: they differ
   int8_t head[N];
 };
 
@@ -244,9 +244,11 @@ k_clip_norm(NormArgs a) {
 // ---- scaling ----------------------------------------------------------------------
 template <int N>
 struct ScaleTable {
-  Chunks<N> c;
+  Chunks<N> c;  // (heads of the gradients alone: the squares are added in their order)
   const void* g[N];
   void* into[N];
+  uint8_t alike[N];  // the other tensor lies as the gradient does
+  __device__ __forceinline__ int head(int i) const { return alike[i] ? c.head[i] : -1; }
 };
 
 // Single elements under way, where the places differ (68M in bf16 with the norm, 281 us
@@ -316,7 +318,7 @@ k_clip_scale(const __grid_constant__ ScaleTable<N> t, NormArgs a) {
   for (Walk<N> w = backwards(t.c); w.on(t.c); w.next(t.c)) {
     const void* g = t.g[w.i];
     void* into = t.into[w.i];
-    const int head = t.c.head[w.i];
+    const int head = t.head(w.i);
     if (s == 1.f && g == into) continue;
     if (t.c.bf16[w.i]) scale_chunk<true>(g, into, w.at, w.n, head, s, threadIdx.x);
     else scale_chunk<false>(g, into, w.at, w.n, head, s, threadIdx.x);
@@ -388,7 +390,7 @@ k_clip_short(const __grid_constant__ ScaleTable<SHORT> t, float max_norm, float 
   for (Walk<SHORT> w(t.c, first, step); w.on(t.c); w.next(t.c)) {
     const void* g = t.g[w.i];
     void* into = t.into[w.i];
-    const int head = t.c.head[w.i];
+    const int head = t.head(w.i);
     if (s == 1.f && g == into) continue;
     if (t.c.bf16[w.i]) scale_chunk<true>(g, into, w.at, w.n, head, s, tid);
     else scale_chunk<false>(g, into, w.at, w.n, head, s, tid);
@@ -719,7 +721,8 @@ cudaError_t launch_scale(const rnnt_grad_list* l, const void* const* grads, void
       t.g[k] = grads[j];
       t.into[k] = into[j];
       const int h = head_of(grads[j], t.c.bf16[k]);
-      return h == head_of(into[j], t.c.bf16[k]) ? h : -1;
+      t.alike[k] = h == head_of(into[j], t.c.bf16[k]);
+      return h;
     });
     if (!t.c.n) break;
     // (only the first may start under the squares: a later one's tail says nothing of them)
@@ -740,7 +743,8 @@ cudaError_t launch_short(const rnnt_grad_list* l, const void* const* grads, void
     t.g[k] = grads[j];
     t.into[k] = into ? into[j] : nullptr;
     const int h = head_of(grads[j], t.c.bf16[k]);
-    return !into || h == head_of(into[j], t.c.bf16[k]) ? h : -1;
+    t.alike[k] = into && h == head_of(into[j], t.c.bf16[k]);
+    return h;
   });
   std::atomic<bool>& d = known[device_slot()];
   if (!d.load()) {

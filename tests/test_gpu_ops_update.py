@@ -164,21 +164,25 @@ def test_tensors_off_16_bytes(kind, shift):
         assert torch.all(b == 9.0)
 
 
+@pytest.mark.parametrize("times", [1, 9])  # one launch, and two
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
-def test_views_of_one_buffer_without_gaps(kind):
+def test_views_of_one_buffer_without_gaps(kind, times):
     # tensors that begin anywhere, alike in both lists
-    n = [1, 5001, 3, 8191, 8192, 2, 20001]
+    n = [1, 5001, 3, 8191, 8192, 2, 20001] * times
     flat, out = (torch.zeros(sum(n) + 9, dtype=DT[kind], device="cuda") for _ in range(2))
     flat.copy_(_grads([(sum(n) + 9,)], [kind], seed=3)[0])
     at = np.cumsum([0, *n])
+    norms = []
     for move in (0, 1):
         grads = [flat[a:a + k] for a, k in zip(at, n)]
         into = [out[a + move:a + move + k] for a, k in zip(at, n)]
         out.fill_(9.0)
-        scale = _check_clip(rn.GradClip([(k,) for k in n], dtype=kind).clip(grads, into=into),
-                            grads, 1.0, 1e-6)
+        c = rn.GradClip([(k,) for k in n], dtype=kind)
+        norms += [c.norm(grads), c.clip(grads, into=into)]
+        scale = _check_clip(norms[-1], grads, 1.0, 1e-6)
         _check_scaled(into, grads, scale)
         assert torch.all(out[:move] == 9.0) and torch.all(out[sum(n) + move:] == 9.0)
+    assert all(torch.equal(a, norms[0]) for a in norms)  # wherever the products go
 
 
 # ---- AdamW
