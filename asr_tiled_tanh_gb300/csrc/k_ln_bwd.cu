@@ -9,12 +9,13 @@ using namespace ln;
 // of 256 threads an SM; 24 take 168, and three blocks of 128 (512 x 1000 rows of 640 in
 // bf16: 322 us; with one block of 256 377, by two warps a row of 16 channels a lane 427).
 template <int VEC, int NV, int MODE>
-constexpr int kBound = MODE == WARPS ? MAX_THREADS : VEC >= 4 && VEC * NV > 16 ? 128 : 256;
+constexpr int kBound = VEC >= 4 && VEC * NV > 16 ? 128 : MODE == WARPS ? MAX_THREADS : 256;
 
 // dx of the team's rows, and part[block][c] = (sum dy xh, sum dy) over the block's.
 template <typename TX, typename TY, int VEC, int NV, int MODE>
 __global__ void
-__launch_bounds__(kBound<VEC, NV, MODE>, MODE == WARPS ? 1 : kBound<VEC, NV, MODE> == 128 ? 3 : 2)
+__launch_bounds__(kBound<VEC, NV, MODE>,
+                  kBound<VEC, NV, MODE> == 128 ? 3 : MODE == WARPS ? 1 : 2)
 k_ln_bwd(LnArgs a, Team t, const TX* __restrict__ x, const TY* __restrict__ dy,
          TX* __restrict__ dx, float2* __restrict__ part) {
   constexpr int NP = kPairs(VEC), S = kCopied<VEC, TX> && kCopied<VEC, TY> ? STAGES : 1;
@@ -297,7 +298,7 @@ struct Bwd {
   cudaError_t run(Team t) const {
     static Known known;
     const auto k = k_ln_bwd<TX, TY, VEC, NV, MODE>;
-    if (MODE != WARPS) t.teams = kBound<VEC, NV, MODE> / t.lanes;
+    if (kBound<VEC, NV, MODE> <= 256) t.teams = kBound<VEC, NV, MODE> / t.lanes;
     const int threads = t.lanes * t.teams;
     const size_t sums = sizeof(float2) * 2 * kPairs(VEC) * threads;
     const size_t smem = std::max(sums, Ring<VEC, NV, STAGES, TX>::bytes(threads) +
@@ -322,7 +323,7 @@ cudaError_t ln_bwd(const LnArgs& a, const void* x, const void* dy, void* dx, flo
   const int vec = vec_of(a, sizeof(TX), x, dx, sizeof(TY), dy);
   cudaError_t e;
   // (their sums stay in registers)
-  if (by_team<V16, (V16 == 8 ? 24 : 16), 16, 6>(a.C, vec, Bwd<TX, TY>{a, x, dy, dx, part, part_rows, st}, &e)) return e;
+  if (by_team<V16, (V16 == 8 ? 24 : 16), 16, 16, 6>(a.C, vec, Bwd<TX, TY>{a, x, dy, dx, part, part_rows, st}, &e)) return e;
   const bool wide = vec == V16;
   const auto k = wide ? k_ln_bwd_wide<TX, TY, V16> : k_ln_bwd_wide<TX, TY, 1>;
   k<<<std::min(a.rows, 4 * num_sms()), WT, 0, st>>>(a, (const TX*)x, (const TY*)dy, (TX*)dx);

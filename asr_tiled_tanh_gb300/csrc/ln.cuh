@@ -376,7 +376,7 @@ struct Ring {
 
 // ---- host -------------------------------------------------------------------------
 // Lanes for rows of n units, and nv units a lane among the numbers that are compiled: at
-// most `one` of a warp that holds a row, `most` of several; 0 lanes: too wide.  Of units
+// most `one` of a warp that holds a row, `two` of two, `most` of more; 0 lanes: too wide.  Of units
 // of 16 bytes those that cost least: a lane's steps for a row count as 2.2 times those
 // for a unit, and what a block of 256 threads has left over is lost.  So a warp's steps
 // between rows serve several where it can hold them, and few lanes idle (bf16, us: 512 x
@@ -384,7 +384,7 @@ struct Ring {
 // 181 and 324; 256 x 1000 rows of 1280 in two warps of 3 units 216 forward, in three of 2
 // 313; 2000 in four of 2 367, in three of 3 395).
 constexpr int PART_UNITS = 3;  // of part of a warp
-inline Team team_for(int n, int one, int most, bool wide_units, int* nv) {
+inline Team team_for(int n, int one, int two, int most, bool wide_units, int* nv) {
   Team t{};
   if (wide_units) {
     long long least = 0;
@@ -402,6 +402,7 @@ inline Team team_for(int n, int one, int most, bool wide_units, int* nv) {
       const long long w = std::max(2LL, cdiv(n, 32LL * per));
       if (32 * w <= MAX_THREADS) offer(32 * w, w > 8 ? 32 * w : 256 / (8 / w), per);
     }
+    for (int per = most + 1; per <= two; ++per) offer(64, 64, per);
   } else {
     const long long w = cdiv(n, 32LL * most);
     if (32 * w <= MAX_THREADS) t.lanes = (int)(32 * w);
@@ -416,8 +417,8 @@ inline Team team_for(int n, int one, int most, bool wide_units, int* nv) {
 }
 
 // f.run<VEC, NV, MODE>(team) for rows of C channels in units of vec (V16: those of 16
-// bytes): at most CH channels a lane, CH1 of a warp that holds a row, ONE pairs of
-// those apart; false: no team holds such a row.
+// bytes): at most CH channels a lane, CH1 of a warp that holds a row, CH2 of two, ONE
+// pairs of those apart; false: no team holds such a row.
 template <int VEC, int NV, typename F>
 cudaError_t by_mode(const Team& t, const F& f) {
   constexpr bool PARTS = NV <= (VEC >= 4 ? PART_UNITS : 2);
@@ -425,7 +426,7 @@ cudaError_t by_mode(const Team& t, const F& f) {
   if (t.lanes == 32) return f.template run<VEC, NV, WARP>(t);
   return f.template run<VEC, NV, WARPS>(t);
 }
-template <int VEC, int NV, int MOST1, int MOST, typename F>
+template <int VEC, int NV, int MOST1, int MOST2, int MOST, typename F>
 cudaError_t by_units(const Team& t, int nv, const F& f) {
   if constexpr (NV == 1) {
     if (nv == 1) return f.template run<VEC, 1, PART>(t);
@@ -434,9 +435,10 @@ cudaError_t by_units(const Team& t, int nv, const F& f) {
   } else if (nv == NV) {
     if (NV <= PART_UNITS && t.lanes < 32)
       return f.template run<VEC, NV, NV <= PART_UNITS ? PART : WARP>(t);
+    if (NV <= MOST2 && t.lanes > 32) return f.template run<VEC, NV, NV <= MOST2 ? WARPS : WARP>(t);
     return f.template run<VEC, NV, WARP>(t);
   }
-  if constexpr (NV < MOST1) return by_units<VEC, NV + 1, MOST1, MOST>(t, nv, f);
+  if constexpr (NV < MOST1) return by_units<VEC, NV + 1, MOST1, MOST2, MOST>(t, nv, f);
   return cudaErrorInvalidValue;
 }
 template <int VEC, int MOST, typename F>
@@ -446,16 +448,16 @@ cudaError_t by_pairs(const Team& t, int nv, const F& f) {
   if (MOST == 6 || nv == 6) return by_mode<VEC, 6>(t, f);
   return by_mode<VEC, MOST>(t, f);
 }
-template <int V16, int CH1, int CH, int ONE, typename F>
+template <int V16, int CH1, int CH2, int CH, int ONE, typename F>
 bool by_team(int C, int vec, const F& f, cudaError_t* e) {
-  constexpr int MOST1 = CH1 / V16, MOST = CH / V16;
+  constexpr int MOST1 = CH1 / V16, MOST2 = CH2 / V16, MOST = CH / V16;
   const bool wide = vec == V16;
   int nv = 0;
   const int narrow = vec == 2 ? 8 : ONE;
   const Team t = team_for((int)cdiv(C, vec == 1 ? 2 : vec), wide ? MOST1 : narrow,
-                          wide ? MOST : narrow, wide, &nv);
+                          wide ? MOST2 : narrow, wide ? MOST : narrow, wide, &nv);
   if (!t.lanes) return false;
-  if (wide) *e = by_units<V16, 1, MOST1, MOST>(t, nv, f);
+  if (wide) *e = by_units<V16, 1, MOST1, MOST2, MOST>(t, nv, f);
   else *e = vec == 2 ? by_pairs<2, 8>(t, nv, f) : by_pairs<1, ONE>(t, nv, f);
   return true;
 }
