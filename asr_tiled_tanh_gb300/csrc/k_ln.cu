@@ -246,7 +246,8 @@ cudaError_t ln_fwd(const LnArgs& a, const void* x, void* y, cudaStream_t st) {
   constexpr int V16 = 16 / (int)std::max(sizeof(TX), sizeof(TY));
   const int vec = vec_of(a, sizeof(TX), x, nullptr, sizeof(TY), y);
   cudaError_t e;
-  if (by_team<V16, 24, 24, (V16 == 8 ? 24 : 16), 8>(a.C, vec, Fwd<TX, TY>{a, x, y, st}, &e)) return e;
+  const Fwd<TX, TY> f{a, x, y, st};
+  if (by_team<V16, 24, 24, (V16 == 8 ? 24 : 16), 8>(a.C, vec, f, &e)) return e;
   const auto k = vec == V16 ? k_ln_fwd_wide<TX, TY, V16> : k_ln_fwd_wide<TX, TY, 1>;
   k<<<std::min(a.rows, 4 * num_sms()), WT, 0, st>>>(a, (const TX*)x, (TY*)y);
   return cudaGetLastError();

@@ -309,7 +309,8 @@ struct Bwd {
     // (two rows a team before there are more blocks, each of which leaves a row of sums: 8
     // x 200 rows of 512 7.1 us, with one 8.8; 4 x 60 of 256 5.8 and 5.3)
     const int grid = (int)std::min<long long>(
-        std::min<long long>(cdiv(a.rows, 2 * t.teams), part_rows_max(a)), (long long)per * num_sms());
+        std::min<long long>(cdiv(a.rows, 2 * t.teams), part_rows_max(a)),
+        (long long)per * num_sms());
     k<<<grid, threads, smem, st>>>(a, t, (const TX*)x, (const TY*)dy, (TX*)dx, part);
     *part_rows = grid;
     return cudaGetLastError();
@@ -323,7 +324,8 @@ cudaError_t ln_bwd(const LnArgs& a, const void* x, const void* dy, void* dx, flo
   const int vec = vec_of(a, sizeof(TX), x, dx, sizeof(TY), dy);
   cudaError_t e;
   // (their sums stay in registers)
-  if (by_team<V16, (V16 == 8 ? 24 : 16), 16, 16, 6>(a.C, vec, Bwd<TX, TY>{a, x, dy, dx, part, part_rows, st}, &e)) return e;
+  const Bwd<TX, TY> f{a, x, dy, dx, part, part_rows, st};
+  if (by_team<V16, (V16 == 8 ? 24 : 16), 16, 16, 6>(a.C, vec, f, &e)) return e;
   const bool wide = vec == V16;
   const auto k = wide ? k_ln_bwd_wide<TX, TY, V16> : k_ln_bwd_wide<TX, TY, 1>;
   k<<<std::min(a.rows, 4 * num_sms()), WT, 0, st>>>(a, (const TX*)x, (const TY*)dy, (TX*)dx);

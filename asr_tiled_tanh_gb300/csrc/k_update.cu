@@ -634,7 +634,9 @@ class Spans {
 };
 
 // Elements before the first four that lie together in p (0 to 3).
-int head_of(const void* p, bool bf16) { return (int)(-(intptr_t)((uintptr_t)p / (bf16 ? 2 : 4)) & 3); }
+int head_of(const void* p, bool bf16) {
+  return (int)((4 - (uintptr_t)p / (bf16 ? 2 : 4) % 4) % 4);
+}
 
 // The next launch's tensors, from i on, into c; fill(k, j): tensor j is its k-th, and
 // returns its head.  Returns the tensor after them.
@@ -886,7 +888,8 @@ rnnt_status rnnt_adamw(const rnnt_grad_list* list, const rnnt_adamw_opts* o,
     auto fp32 = [&](int i) { return (size_t)list->count[i] * 4; };
     for (float* const* x : {params, m, v})
       s.add(list->n, true, [&](int i) { return x[i]; }, fp32);
-    if (low) s.add(list->n, true, [&](int i) { return low[i]; }, [&](int i) { return fp32(i) / 2; });
+    if (low)
+      s.add(list->n, true, [&](int i) { return low[i]; }, [&](int i) { return fp32(i) / 2; });
     s.add(list->n, false, [&](int i) { return grads[i]; },
           [&](int i) { return fp32(i) / (is_bf16(list, i) ? 2 : 1); });
     if (s.overlap()) return RNNT_ERR_INVALID_ARG;

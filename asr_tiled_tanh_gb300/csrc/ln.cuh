@@ -87,7 +87,8 @@ template <int VEC, typename T>
 __device__ __forceinline__ Vals<VEC> widen(const Unit<VEC, T>& u) {
   Vals<VEC> v;
   if constexpr (VEC == 1 && sizeof(T) == 2) {
-    v.p[0] = make_float2(__uint_as_float((uint32_t)u.a << 16), __uint_as_float((uint32_t)u.b << 16));
+    v.p[0] = make_float2(__uint_as_float((uint32_t)u.a << 16),
+                         __uint_as_float((uint32_t)u.b << 16));
   } else if constexpr (VEC == 1) {
     v.p[0] = make_float2(__uint_as_float(u.a), __uint_as_float(u.b));
   } else if constexpr (sizeof(T) == 4) {

@@ -320,7 +320,7 @@ class FrameNorm(_Op):
 
 
 class LayerNorm(_Op):
-    """y = gamma * xh + beta, xh each row of x [B,T,C] that exists less its mean, over its deviation.
+    """y = gamma * xh + beta, xh a row of x [B,T,C] less its mean, over its deviation.
 
     Rows t < lengths[b] exist, or with label_rows (the rows of LabelEmbedding) rows
     u <= lengths[b]; the others' y and dx are 0.  dtype: of x and dx; out_dtype: of y and dy
@@ -557,11 +557,26 @@ class AdamW(_ListOp):
         self._m, self._v = self._params.called("m"), self._params.called("v")
         self._copies = self._kind("low", [torch.bfloat16] * n)
         new = lambda: [torch.zeros(k, device=device) for k in self._shapes]  # noqa: E731
-        self.m, self.v = (tuple(new() if k is None else k) for k in (m, v))
+        self._moments = tuple(tuple(new() if k is None else k) for k in (m, v))
         self._mv = None
-        self.steps = torch.tensor([int(steps), 0], dtype=torch.int32, device=device)
-        self._steps = self.steps.data_ptr()
+        self._counts = torch.tensor([int(steps), 0], dtype=torch.int32, device=device)
+        self._steps = self._counts.data_ptr()
         self._run = lib.rnnt_adamw
+
+    @property
+    def m(self):
+        """The first moments (to resume: copy into them)."""
+        return self._moments[0]
+
+    @property
+    def v(self):
+        """The second moments."""
+        return self._moments[1]
+
+    @property
+    def steps(self):
+        """int32 [2] on the device: the updates taken so far, and a word of the library's."""
+        return self._counts
 
     def step(self, params, grads, lr, clip=None, low=None, stream=None):
         """One update of params in place.
@@ -575,7 +590,7 @@ class AdamW(_ListOp):
         if isinstance(lr, torch.Tensor):
             lr = self._pointer(lr.reshape(1), "lr", _ONE)
         else:
-            self.opts.lr, lr = lr, None
+            self.opts.lr, lr = float(lr), None
         held_p, p = self._take(params, self._params)
         held_g, g = self._take(grads, self._grads)
         held_l, w = None, None

@@ -130,7 +130,8 @@ def test_every_width(C, dtype, out):
              *n.bwd(xg, dyg, gamma.cuda(), lengths.cuda()))
 
 
-@pytest.mark.parametrize("B,T,C", [(1, 1, 16), (4, 9, 512), (5, 1, 64), (3, 12, 77), (64, 101, 128)])
+@pytest.mark.parametrize("B,T,C", [(1, 1, 16), (4, 9, 512), (5, 1, 64), (3, 12, 77),
+                                   (64, 101, 128)])
 @pytest.mark.parametrize("given", [True, False])
 def test_label_rows_and_parameters_left_out(B, T, C, given):
     case = (B, T, C, "bf16", "bf16", True)
@@ -258,7 +259,8 @@ def test_an_empty_batch():
     n = rn.LayerNorm(0, 5, 40, dtype="f32")
     x = torch.empty(0, 5, 40, device="cuda")
     assert n.fwd(x).shape == (0, 5, 40)
-    _, dg, db = n.bwd(x, x, dgamma=torch.ones(40, device="cuda"), dbeta=torch.ones(40, device="cuda"))
+    one = lambda: torch.ones(40, device="cuda")  # noqa: E731
+    _, dg, db = n.bwd(x, x, dgamma=one(), dbeta=one())
     assert torch.all(dg == 0) and torch.all(db == 0)
 
 

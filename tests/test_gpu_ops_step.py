@@ -143,3 +143,41 @@ def test_the_helper_and_python_say_the_same():
             with pytest.raises(ValueError):
                 c.norm(bad)
     assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+def test_plans_of_several_host_threads():
+    # each thread with plans, tensors and a stream of its own
+    import threading
+    wrong = []
+
+    def work(seed, stream):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        r = lambda *k: torch.randn(*k, device="cuda", generator=gen)  # noqa: E731
+        with torch.cuda.stream(stream):
+            C = (512, 333, 64, 1280)[seed % 4]
+            x, dy, scale = r(9, 50, C), r(9, 50, C), r(C)
+            shapes = [(1000 * (i + 1) + seed,) for i in range(4 + 12 * seed)]
+            grads, p = [r(*k) for k in shapes], [r(*k) for k in shapes]
+            q = [t.clone() for t in p]
+            n, c = rn.LayerNorm(9, 50, C, dtype="f32"), rn.GradClip(shapes)
+            a, b = rn.AdamW(shapes), rn.AdamW(shapes)
+            ref = None
+            for _ in range(25):
+                out = [n.fwd(x, scale, scale), *n.bwd(x, dy, scale), c.norm(grads)]
+                a.step(p, grads, 1e-3, clip=out[-1])
+                stream.synchronize()
+                ref = ref or [t.clone() for t in out]
+                if not all(torch.equal(u, w) for u, w in zip(out, ref)):
+                    wrong.append(("results", seed))
+            for _ in range(25):
+                b.step(q, grads, 1e-3, clip=ref[-1])
+            stream.synchronize()
+            if not all(torch.equal(u, w) for u, w in zip(p, q)) or a.steps.tolist() != [25, 0]:
+                wrong.append(("update", seed))
+
+    threads = [threading.Thread(target=work, args=(k, torch.cuda.Stream())) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
