@@ -78,6 +78,19 @@ def test_norm_and_clip(shapes, kind):
     assert all(torch.equal(a, b) for a, b in zip(grads, into))
 
 
+@pytest.mark.parametrize("sizes", [(300, 41, 5000), (200000, 33, 90001)])
+def test_some_in_place_some_elsewhere(sizes):
+    shapes = [(k,) for k in sizes]
+    grads = tuple(_grads(shapes, ["f32", "bf16", "f32"], seed=4))
+    keep = [g.clone() for g in grads]
+    into = [grads[0], torch.zeros_like(grads[1]), grads[2]]
+    c = rn.GradClip(shapes, max_norm=0.5, dtype=["f32", "bf16", "f32"])
+    out = torch.zeros(2, device="cuda")
+    assert c.clip(grads, into=into, out=out) is out
+    _check_scaled(into, keep, _check_clip(out, keep, 0.5, 1e-6))
+    assert torch.equal(grads[1], keep[1])
+
+
 def test_a_norm_below_the_limit_leaves_the_gradients():
     shapes = [(100, 33), (5,)]
     grads = _grads(shapes, ["f32"] * 2)
