@@ -558,7 +558,6 @@ class AdamW(_ListOp):
         self._copies = self._kind("low", [torch.bfloat16] * n)
         new = lambda: [torch.zeros(k, device=device) for k in self._shapes]  # noqa: E731
         self._moments = tuple(tuple(new() if k is None else k) for k in (m, v))
-        self._mv = None
         self._counts = torch.tensor([int(steps), 0], dtype=torch.int32, device=device)
         self._steps = self._counts.data_ptr()
         self._run = lib.rnnt_adamw
@@ -585,21 +584,21 @@ class AdamW(_ListOp):
         every replay); clip: GradClip's (norm, scale); low: tensors for the bf16 copies of params,
         an entry or all of them None.
         """
-        if self._mv is None:
-            self._mv = self._take(self.m, self._m), self._take(self.v, self._v)
         if isinstance(lr, torch.Tensor):
             lr = self._pointer(lr.reshape(1), "lr", _ONE)
         else:
             self.opts.lr, lr = float(lr), None
         held_p, p = self._take(params, self._params)
         held_g, g = self._take(grads, self._grads)
+        held_m, m = self._take(self.m, self._m)
+        held_v, v = self._take(self.v, self._v)
         held_l, w = None, None
         if low is not None:
             some = any(map(operator.is_, low, itertools.repeat(None)))
             held_l, w = self._some(low) if some else self._take(low, self._copies)
         c = None if clip is None else self._pointer(clip, "clip", _PAIR)
-        _check(self._run(self._l, self._o, p, g, self._mv[0][1], self._mv[1][1], w, lr, c,
-                         self._steps, self._stream(stream)), "rnnt_adamw")
+        _check(self._run(self._l, self._o, p, g, m, v, w, lr, c, self._steps,
+                         self._stream(stream)), "rnnt_adamw")
 
     def _some(self, low):
         """The pointers of copies that only some tensors have."""

@@ -1,0 +1,32 @@
+"""Clipping and the AdamW update at the ends of their ranges (GPU)."""
+import numpy as np
+import pytest
+import torch
+
+import asr_tiled_tanh_gb300 as rn
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    rn.load(build_if_missing=True)
+
+
+def test_moments_whose_memory_moved():
+    shapes = [(700,), (30, 5)]
+    r = lambda: [torch.randn(k, device="cuda") for k in shapes]  # noqa: E731
+    p, g = r(), r()
+    q = [t.clone() for t in p]
+    a, b = rn.AdamW(shapes), rn.AdamW(shapes)
+    old = []
+    for i in range(3):
+        a.step(p, g, 0.1)
+        b.step(q, g, 0.1)
+        for t in (b.m[0], b.v[1]):  # (as a program that moved them to the host and back)
+            old.append((t.data, t.data.clone()))
+            t.data = t.data.clone()
+    for x, y in ((p, q), (a.m, b.m), (a.v, b.v)):
+        assert all(torch.equal(s, t) for s, t in zip(x, y))
+    assert all(torch.equal(s, t) for s, t in old)  # nothing went to where they were
