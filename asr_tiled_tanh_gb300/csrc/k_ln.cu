@@ -105,9 +105,7 @@ k_ln_fwd(LnArgs a, Team t, const TX* __restrict__ x, TY* __restrict__ y) {
     }
     s[0] = s2.x + s2.y;
     team_sum<MODE>(s, t, p, scr[1]);
-    const float var = fmaf(s[0], a.rC, a.eps);
-    float rstd = rsqrtf(var);  // (2 ulp; the step leaves it within one)
-    rstd = fmaf(0.5f * rstd, fmaf(-var * rstd, rstd, 1.f), rstd);
+    const float rstd = root_of(fmaf(s[0], a.rC, a.eps));
     if (a.stats && live && p.lane == 0) a.stats[r] = make_float2(mean, rstd);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -161,7 +159,7 @@ k_ln_fwd_wide(LnArgs a, const TX* __restrict__ x, TY* __restrict__ y) {
       }
     }
     const float rstd =
-        1.f / sqrtf(block_sum(make_float2(s.x + s.y, 0.f), scr).x * a.rC + a.eps);
+        root_of(fmaf(block_sum(make_float2(s.x + s.y, 0.f), scr).x, a.rC, a.eps));
     if (a.stats && threadIdx.x == 0) a.stats[r] = make_float2(mean, rstd);
 #pragma unroll 2
     for (int j = 0; cols.has(j); ++j) {

@@ -56,6 +56,12 @@ __device__ __forceinline__ Row row_of(const LnArgs& a, int r) {
   return w;
 }
 
+// 1 / sqrt(var): rsqrtf is 2 ulp off, the step leaves it within one.  NaN for 0 and for
+// infinity (a row of one value without eps, squares past the range), by 0 * inf in the step.
+__device__ __forceinline__ float root_of(float var) {
+  const float r = rsqrtf(var);
+  return fmaf(0.5f * r, fmaf(-var * r, r, 1.f), r);
+}
 
 // ---- vectors ------------------------------------------------------------------
 // VEC (8, 4 or 2) channels next to each other, or two that are as many channels apart
