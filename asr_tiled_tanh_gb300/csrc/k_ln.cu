@@ -92,7 +92,7 @@ k_ln_fwd(LnArgs a, Team t, const TX* __restrict__ x, TY* __restrict__ y) {
     float s[1] = {s2.x + s2.y};
     team_sum<MODE>(s, t, p, scr[0]);
     float mean = s[0] * a.rC;
-    mean = fmaf(fmaf(-mean, C, s[0]), a.rC, mean);  // (exact for rows of one value)
+    mean = fmaf(fmaf(-mean, C, s[0]), a.rC, mean);  // (the sum's quotient, rounded once)
     s2 = make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -105,6 +105,33 @@ k_ln_fwd(LnArgs a, Team t, const TX* __restrict__ x, TY* __restrict__ y) {
     }
     s[0] = s2.x + s2.y;
     team_sum<MODE>(s, t, p, scr[1]);
+    // (what a sum of equal bf16 values needs, 8 bits and those of C, it has)
+    const bool flat = sizeof(TX) == 4 && may_be_flat(s[0], a.rC, mean);
+    if (MODE == PART ? sizeof(TX) == 4 && __any_sync(0xffffffffu, flat) : flat) {
+      // (a warp's other teams only keep the flat ones company: by 0)
+      s2 = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+          if (cols.has(j)) s2 = __fadd2_rn(s2, v[j].p[i]);
+      float rest[1] = {s2.x + s2.y};
+      team_sum<MODE>(rest, t, p, scr[0]);
+      const float better = flat ? fmaf(rest[0], a.rC, mean) : mean, off = better - mean;
+      mean = better;
+      s2 = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          v[j].p[i] = __fadd2_rn(v[j].p[i], make_float2(-off, -off));
+          if (VEC == 1 && !cols.both(j)) v[j].p[i].y = 0.f;
+          if (cols.has(j)) s2 = __ffma2_rn(v[j].p[i], v[j].p[i], s2);
+        }
+      }
+      s[0] = s2.x + s2.y;
+      team_sum<MODE>(s, t, p, scr[1]);
+    }
     const float rstd = root_of(fmaf(s[0], a.rC, a.eps));
     if (a.stats && live && p.lane == 0) a.stats[r] = make_float2(mean, rstd);
 #pragma unroll
@@ -146,20 +173,28 @@ k_ln_fwd_wide(LnArgs a, const TX* __restrict__ x, TY* __restrict__ y) {
 #pragma unroll
       for (int i = 0; i < NP; ++i) s = __fadd2_rn(s, v.p[i]);
     }
-    const float mean = block_sum(make_float2(s.x + s.y, 0.f), scr).x / (float)a.C;
-    s = make_float2(0.f, 0.f);
+    float mean = block_sum(make_float2(s.x + s.y, 0.f), scr).x / (float)a.C;
+    // sums about the mean: of the squares, or of what is left
+    auto about = [&](bool squares) {
+      float2 q = make_float2(0.f, 0.f);
 #pragma unroll 2
-    for (int j = 0; cols.has(j); ++j) {
-      const Vals<VEC> v = cols.load(xr, j);
+      for (int j = 0; cols.has(j); ++j) {
+        const Vals<VEC> v = cols.load(xr, j);
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        float2 d = __fadd2_rn(v.p[i], make_float2(-mean, -mean));
-        if (VEC == 1 && !cols.both(j)) d.y = 0.f;
-        s = __ffma2_rn(d, d, s);
+        for (int i = 0; i < NP; ++i) {
+          float2 d = __fadd2_rn(v.p[i], make_float2(-mean, -mean));
+          if (VEC == 1 && !cols.both(j)) d.y = 0.f;
+          q = __ffma2_rn(d, squares ? d : make_float2(1.f, 1.f), q);
+        }
       }
+      return block_sum(make_float2(q.x + q.y, 0.f), scr).x;
+    };
+    float var = about(true);
+    if (may_be_flat(var, a.rC, mean)) {
+      mean = fmaf(about(false), a.rC, mean);
+      var = about(true);
     }
-    const float rstd =
-        root_of(fmaf(block_sum(make_float2(s.x + s.y, 0.f), scr).x, a.rC, a.eps));
+    const float rstd = root_of(fmaf(var, a.rC, a.eps));
     if (a.stats && threadIdx.x == 0) a.stats[r] = make_float2(mean, rstd);
 #pragma unroll 2
     for (int j = 0; cols.has(j); ++j) {

@@ -42,3 +42,73 @@ def test_rows_whose_squares_leave_the_range_are_nan(C, dtype):
         assert torch.isnan(a[hit].float()).all()
     assert torch.isnan(got[2]).all()
     assert torch.equal(got[3], ref[3])  # (the sum of dy alone)
+
+
+# Their sums of equal terms are rounded, unlike those of 7.0 or of any value in bf16.
+VALUES = [0.1, -1e4 / 3, 7.7e-3, 123456.789, 1.0 + 2.0 ** -23, 1e-12, 1e15]
+
+
+@pytest.mark.parametrize("C", WIDTHS)
+def test_rows_of_one_value(C):
+    B, T = 2, len(VALUES)
+    x, dy, gamma, beta = _inputs(B, 2 * T, C, "f32")
+    mixed = x.clone()  # rows of one value beside others
+    for i, v in enumerate(VALUES):
+        mixed[:, 2 * i] = v
+    n = rn.LayerNorm(B, 2 * T, C, dtype="f32")
+    ref, ref_dx = n.fwd(x, gamma, beta), n.bwd(x, dy, gamma)[0]
+    y = n.fwd(mixed, gamma, beta)
+    dx, dg, db = n.bwd(mixed, dy, gamma)
+    assert torch.equal(y[:, ::2], beta.expand(B, T, C))  # no deviation: the offset alone
+    assert torch.equal(y[:, 1::2], ref[:, 1::2]) and torch.equal(dx[:, 1::2], ref_dx[:, 1::2])
+    # dx = rstd (a - mean(a)), xh being 0: within (64 + C / 256) u of the terms' sizes
+    a = (gamma * dy[:, ::2]).double()
+    rstd = 1e-5 ** -0.5
+    size = rstd * (a.abs() + a.abs().mean(2, keepdim=True))
+    err = (dx[:, ::2].double() - rstd * (a - a.mean(2, keepdim=True))).abs()
+    assert torch.all(err <= (64 + C / 256) * 2.0 ** -24 * size)
+    alone = rn.LayerNorm(B, T, C, dtype="f32")
+    only = mixed[:, ::2].contiguous()
+    assert torch.equal(alone.fwd(only, gamma, beta), beta.expand(B, T, C))
+    assert not alone.bwd(only, torch.ones_like(only), gamma)[1].any()  # dgamma = sum dy xh
+
+
+@pytest.mark.parametrize("C", WIDTHS)
+def test_rows_of_one_value_without_eps_are_nan(C):
+    T = len(VALUES)
+    x = torch.tensor(VALUES, device="cuda")[None, :, None].expand(1, T, C).contiguous()
+    n = rn.LayerNorm(1, T, C, dtype="f32", eps=0.0)
+    assert torch.isnan(n.fwd(x)).all()
+    assert torch.isnan(n.bwd(x, torch.ones_like(x))[0]).all()
+
+
+@pytest.mark.parametrize("C", WIDTHS)
+def test_rows_far_from_zero(C):
+    # |mean| of 2^12 to 2^20 deviations (r).  The mean is held in fp32, half a step of itself off:
+    # r u of the deviation, twice that with the step of its sum; a sum about it is k u of the
+    # deviations off.  The deviation is as far off as the mean squared, and by its own sum.
+    B, T, u = 1, 9, 2.0 ** -24
+    g = torch.Generator().manual_seed(C)
+    base = torch.randn(B, T, C, generator=g)
+    shift = 2.0 ** torch.arange(12, 21).float()
+    x = base + shift[None, :, None] * 1.1
+    n = rn.LayerNorm(B, T, C, dtype="f32", eps=0.0)
+    y = n.fwd(x.cuda()).double().cpu()
+    xd = x.double()
+    mean, dev = xd.mean(2, keepdim=True), xd.std(2, correction=0, keepdim=True)
+    xh, r = (xd - mean) / dev, mean.abs() / dev
+    k = 64 + C / 256
+    bound = 2 * r * u + k * u + xh.abs() * ((2 * r * u) ** 2 + k * u + 2 * u)
+    err = (y - xh).abs()
+    assert torch.all(err <= bound), float((err / bound).max())
+
+
+@pytest.mark.parametrize("C", WIDTHS + [12288, 100000])
+def test_rows_of_one_bf16_value(C):
+    T = len(VALUES)
+    x = torch.tensor(VALUES, device="cuda").bfloat16()[None, :, None].expand(2, T, C).contiguous()
+    beta = torch.randn(C, device="cuda")
+    n = rn.LayerNorm(2, T, C, out_dtype="f32")
+    assert torch.equal(n.fwd(x, None, beta), beta.expand(2, T, C))
+    assert not n.bwd(x, torch.ones(2, T, C, device="cuda"))[1].any()
+    assert torch.isnan(rn.LayerNorm(2, T, C, out_dtype="f32", eps=0.0).fwd(x)).all()
