@@ -2,6 +2,7 @@
 // (include/rnnt_ops.h).
 #include <algorithm>
 #include <atomic>
+#include <climits>
 #include <memory>
 #include <new>
 #include <type_traits>
@@ -507,7 +508,8 @@ template <int N>
 __global__ void __launch_bounds__(UT, 2)
 k_adamw(const __grid_constant__ AdamTable<N> t, AdamArgs a) {
   ptx::griddep_wait();
-  const int done = __ldcg(a.steps);
+  // (a count at its end stays there)
+  const int now = min(__ldcg(a.steps), INT_MAX - 1) + 1;
   const bool take = !a.clip || isfinite(__ldcg(a.clip));
   if (take) {
     AdamStep f;
@@ -515,8 +517,8 @@ k_adamw(const __grid_constant__ AdamTable<N> t, AdamArgs a) {
     f.scale = a.clip ? __ldcg(a.clip + 1) : 1.f;
     f.lr = a.lr_dev ? __ldcg(a.lr_dev) : a.lr;
     // 1 - beta^t without the cancellation
-    f.r1 = 1.f / -expm1f((float)(done + 1) * a.log1);
-    f.r2 = 1.f / -expm1f((float)(done + 1) * a.log2);
+    f.r1 = 1.f / -expm1f((float)now * a.log1);
+    f.r2 = 1.f / -expm1f((float)now * a.log2);
 #pragma unroll 1
     for (Walk<N> w = backwards(t.c); w.on(t.c); w.next(t.c)) {
       const Tensors x{t.p[w.i] + w.at, t.m[w.i] + w.at, t.v[w.i] + w.at,
@@ -532,7 +534,7 @@ k_adamw(const __grid_constant__ AdamTable<N> t, AdamArgs a) {
   if (threadIdx.x) return;
   __threadfence();
   if (atomicInc((unsigned*)a.steps + 1, gridDim.x - 1) == gridDim.x - 1 && a.last && take)
-    a.steps[0] = done + 1;
+    a.steps[0] = now;
 }
 
 // ---- host ----------------------------------------------------------------------

@@ -544,7 +544,7 @@ class AdamW(_ListOp):
         n = len(self._shapes)
         if not (0 <= betas[0] < 1 and 0 <= betas[1] < 1 and 0 <= eps < float("inf")):
             raise ValueError(f"betas {betas}, eps {eps}: out of range")
-        if not 0 <= steps < 1 << 31:
+        if not 0 <= steps < (1 << 31) - 1:
             raise ValueError(f"steps = {steps}: out of range")
         one = isinstance(weight_decay, (int, float))
         if not one and len(weight_decay) != n:

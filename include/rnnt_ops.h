@@ -262,8 +262,9 @@ typedef struct {
  * copy.  The 5 n tensors do not overlap, but for gradients among themselves (the
  * same parameter twice is refused).  lr: one device fp32 or NULL; clip: rnnt_clip's
  * (norm, scale) or NULL.  steps: device int32 [2]: the updates taken so far, which
- * the call reads and adds 1 to, and a word that is 0 between calls; the caller
- * clears both once.  So a captured call counts its replays. */
+ * the call reads and adds 1 to (up to 2^31 - 1, where the count stays), and a word
+ * that is 0 between calls; the caller clears both once.  So a captured call counts
+ * its replays. */
 rnnt_status rnnt_adamw(const rnnt_grad_list* list, const rnnt_adamw_opts* opts,
                        float* const* params, const void* const* grads, float* const* m,
                        float* const* v, void* const* low, const float* lr, const float* clip,

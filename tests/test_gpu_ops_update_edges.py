@@ -30,3 +30,21 @@ def test_moments_whose_memory_moved():
     for x, y in ((p, q), (a.m, b.m), (a.v, b.v)):
         assert all(torch.equal(s, t) for s, t in zip(x, y))
     assert all(torch.equal(s, t) for s, t in old)  # nothing went to where they were
+
+
+def test_the_count_stays_at_its_end():
+    # (the corrections of these betas are 1 there)
+    most = (1 << 31) - 1
+    with pytest.raises(ValueError):
+        rn.AdamW([(3,)], steps=most)
+    g = torch.randn(300, device="cuda")
+    p = torch.randn(300, device="cuda")
+    m, v = 0.1 * torch.randn(300, device="cuda"), 0.1 + torch.rand(300, device="cuda")
+    o = rn.AdamW([(300,)], weight_decay=0.0, m=[m], v=[v], steps=most - 1)
+    for _ in range(3):
+        q = p.double()
+        o.step([p], [g], 0.125)
+        step = m.double() / (v.double().sqrt() + 1e-8)  # (of the moments as they now are)
+        bound = U * p.double().abs() + 0.125 * 32 * U * step.abs()
+        assert torch.all((p.double() - (q - 0.125 * step)).abs() <= bound)
+        assert o.steps.tolist() == [most, 0]
