@@ -103,8 +103,8 @@ __device__ __forceinline__ double block_sum(double v, double* scr) {
 }
 
 // ---- norm -------------------------------------------------------------------------
-// A thread's 32 elements of a chunk: squares added in fp32 (33 roundings of terms of
-// one sign), in fp64 where that left the range or came near its bottom.  fp64 for
+// A thread's 32 elements of a chunk: squares added in fp32 (two chains of 16 terms of one
+// sign, and their sum), in fp64 where that left the range or came near its bottom.  fp64 for
 // every element would cost three times what DRAM does.
 constexpr int EACH = CHUNK / UT;
 __device__ __forceinline__ double squares(const float (&g)[EACH]) {
@@ -183,7 +183,9 @@ __device__ __forceinline__ float2 norm_and_scale(double sum, float max_norm, flo
     const float norm = sqrtf((float)sum), q = max_norm / (norm + eps);
     return make_float2(norm, q >= 1.f ? 1.f : q);
   }
+  // (a norm that fp32 does not hold is infinite, and the scale goes with it)
   const double norm = sqrt(sum), q = (double)max_norm / (norm + (double)eps);
+  if (isinf((float)norm)) return make_float2(INFINITY, 0.f);
   return make_float2((float)norm, q >= 1 ? 1.f : (float)q);  // (NaN stays)
 }
 

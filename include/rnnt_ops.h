@@ -216,11 +216,12 @@ rnnt_status rnnt_orth(const rnnt_orth_dims* dims, const void* G, void* O, void* 
 /* ---- gradient clipping ---------------------------------------------------------
  * Over all elements of n tensors together:
  *   norm = sqrt(sum g^2),  scale = min(1, max_norm / (norm + eps)),  into = scale g
- * Squares are added in fp64 (fp32 in groups of 33 or fewer, fp64 where that would
- * leave the range), in an order that follows from the list and the device, so
- * finite entries of any size are fine.  A norm that is not finite: an infinite one
- * gives scale 0, NaN gives NaN, and `into` is the product all the same; rnnt_adamw
- * leaves such an update out.
+ * Squares are added in fp64 (fp32 in groups of 32, fp64 where that would leave the
+ * range), in an order that follows from the list, the gradients' places modulo 16
+ * bytes and the device; entries of any size add up.  The norm is given in fp32: one
+ * past its range is infinite, as one of an infinite entry.  An infinite norm gives
+ * scale 0, whatever the limit, NaN gives NaN, and `into` is the product (0 times an
+ * infinite entry: NaN) all the same; rnnt_adamw leaves such an update out.
  */
 typedef struct {
   int n;                   /* tensors, 0 to 2^16 */

@@ -48,3 +48,39 @@ def test_the_count_stays_at_its_end():
         bound = U * p.double().abs() + 0.125 * 32 * U * step.abs()
         assert torch.all((p.double() - (q - 0.125 * step)).abs() <= bound)
         assert o.steps.tolist() == [most, 0]
+
+
+@pytest.mark.parametrize("n", [8, 400000])  # one launch, and several
+def test_a_norm_past_the_range_is_infinite(n):
+    shapes = [(n,), (3,)]
+    g = [torch.full(k, 1e-3, device="cuda") for k in shapes]
+    g[0][1] = g[1][2] = 3e38  # the norm: 4.2e38
+    keep = [t.clone() for t in g]
+    into = [torch.full_like(t, 5.0) for t in g]
+    c, o = rn.GradClip(shapes), rn.AdamW(shapes)
+    out = c.clip(g, into=into)
+    assert out.tolist() == [float("inf"), 0.0] == c.norm(g).tolist()
+    assert not any(t.any() for t in into)
+    p = [torch.ones(k, device="cuda") for k in shapes]
+    o.step(p, g, 0.1, clip=out)
+    assert o.steps.tolist() == [0, 0] and all(torch.all(t == 1) for t in p)
+    g[1][2] = 1e38  # 3.2e38
+    out = c.norm(g)
+    norm = np.sqrt(sum(float((t.double() ** 2).sum()) for t in g))
+    assert abs(float(out[0]) - norm) <= 20 * U * norm
+    assert abs(float(out[1]) - 1 / norm) <= 22 * U / norm + 2.0 ** -149
+    assert torch.equal(g[0], keep[0])
+
+
+@pytest.mark.parametrize("n", [8, 400000])
+def test_an_unlimited_norm(n):
+    # scale 1 while the norm is finite, 0 where it is not, NaN where it is none
+    g = torch.ones(n, device="cuda")
+    c = rn.GradClip([(n,)], max_norm=float("inf"))
+    assert float(c.norm([g])[1]) == 1.0
+    g[3] = 1e30
+    assert float(c.norm([g])[1]) == 1.0
+    g[3] = -float("inf")
+    assert c.norm([g]).tolist() == [float("inf"), 0.0]
+    g[3] = float("nan")
+    assert torch.isnan(c.norm([g])).all()
