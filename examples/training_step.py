@@ -11,9 +11,9 @@
     the others --AdamW--> weights and their bf16 copies
 
 The hidden matrices take the orthogonalised update, the output layer, the label table, biases
-and norms AdamW.  The encoder that would make the frames and take their gradient is left out: the
-frames are a fixed synthetic batch whose features carry the labels, so the loss falls as the step
-repeats.
+and norms AdamW; a step whose gradients are not finite changes none of them.  The encoder that
+would make the frames and take their gradient is left out: the frames are a fixed synthetic batch
+whose features carry the labels, so the loss falls as the step repeats.
 Run:  python examples/training_step.py [steps]
 """
 import math
@@ -71,10 +71,15 @@ class Transducer:
                  "table": self.embed.bwd(de, labels, U_len), "bZ": d["dbZ"], "bO": d["dbO"],
                  "gamma": dgamma, "beta": dbeta, "scale": dscale, "shift": dshift}
         clip = self.clip.norm([grads[k] for k in (*m, *v)])
+        # (AdamW leaves an update out whose norm is not finite; so do these: a product with 0
+        # would keep a NaN)
+        ok = torch.isfinite(clip[0])
         for k, w in m.items():  # an update of singular values near 1, whatever the gradient's
-            vel = self.velocity[k].mul_(self.mu).add_(grads[k] * clip[1])
-            w.sub_(self.orth[k].run(vel),
-                   alpha=self.lr * math.sqrt(max(1.0, w.shape[0] / w.shape[1])))
+            old = self.velocity[k]
+            vel = torch.where(ok, self.mu * old + grads[k] * clip[1], old)
+            rate = self.lr * math.sqrt(max(1.0, w.shape[0] / w.shape[1]))
+            w.copy_(torch.where(ok, w - rate * self.orth[k].run(vel), w))
+            old.copy_(vel)
             self.low[k].copy_(w)
         self.adamw.step(list(v.values()), [grads[k] for k in v], 0.5 * self.lr, clip=clip,
                         low=[self.low.get(k) for k in v])
