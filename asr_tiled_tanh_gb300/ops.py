@@ -594,6 +594,7 @@ class AdamW(_ListOp):
         held_v, v = self._take(self.v, self._v)
         held_l, w = None, None
         if low is not None:
+            low = low if type(low) is list else list(low)
             some = any(map(operator.is_, low, itertools.repeat(None)))
             held_l, w = self._some(low) if some else self._take(low, self._copies)
         c = None if clip is None else self._pointer(clip, "clip", _PAIR)

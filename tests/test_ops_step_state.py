@@ -26,3 +26,16 @@ def test_moments_are_looked_at_in_every_step(monkeypatch):
     with pytest.raises(ValueError):
         o.step(p, g, 0.1)
     assert len(seen) == 3
+
+
+def test_copies_may_be_an_iterator(monkeypatch):
+    # as the other lists
+    _, o, calls = _plans(monkeypatch)
+    seen = []
+    o._run = lambda *a: seen.append(_addresses(a[6])) or 0
+    g, p = [Tensor(F, (4, 6)), Tensor(H, (7,))], [Tensor(F, (4, 6)), Tensor(F, (7,))]
+    low = [Tensor(H, (4, 6), at=1 << 21), Tensor(H, (7,), at=1 << 22)]
+    for some in (low, [None, low[1]], [low[0], None], [None, None]):
+        for kind in (list, tuple, iter):
+            o.step(iter(p), iter(g), 0.1, low=kind(some))
+            assert seen[-1] == [t._at if t else 0 for t in some]
