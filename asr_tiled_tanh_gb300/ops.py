@@ -14,7 +14,9 @@ unless one is given, writes into the tensor it is handed or into a new one (of t
 memory), and returns it.  An object's own buffers are made on the stream that is current then.
 Calls of one object share its buffers and must not overlap on the GPU: use one object per
 stream.  An object belongs to one GPU: its tensors live there, and it is the current device
-when a call is made.
+when a call is made.  What a call writes of the tensors that it is handed counts as written for
+autograd: a graph that still holds their old values refuses its backward pass, as it does after an
+in-place operation of torch.
 """
 from __future__ import annotations
 
@@ -203,6 +205,13 @@ class _Op:
         with torch.cuda.stream(stream):
             return torch.empty_strided(shape, strides, dtype=dtype, device=self.device)
 
+    def _wrote(self, *ts):
+        """Count these tensors, or lists of them, as written (0.15 us with csrc/lists.cpp)."""
+        if self._fast is not None:
+            return self._fast.wrote(*ts)
+        flat = itertools.chain.from_iterable(t if type(t) is list else (t,) for t in ts)
+        torch.autograd.graph.increment_version([t for t in flat if isinstance(t, torch.Tensor)])
+
     def status(self, stream=None):
         """(status code, raw word) of every call so far; synchronizes the stream."""
         w = ctypes.c_int32(0)
@@ -240,22 +249,26 @@ class LabelEmbedding(_Op):
 
     def fwd(self, table, ids, U_len=None, out=None, stream=None):
         """The rows [B,U1,D] of ids [B,U1] int32; U_len [B] int32 or None (every row)."""
+        given = out
         if out is None:
             out = self._empty(self._rows, self._rt, stream)
         i, u = self._in(ids, U_len)
         _check(self._fwd(self._d, i, u, self._ptr(table, "table", self._tt, self._table),
                          self._ptr(out, "out", self._rt, self._rows), self._args[2],
                          self._stream(stream)), "rnnt_embed_fwd")
+        self._wrote(given)
         return out
 
     def bwd(self, dout, ids, U_len=None, dtable=None, stream=None):
         """The table's gradient [V,D] fp32 from the rows' gradient."""
+        given = dtable
         if dtable is None:
             dtable = self._empty(self._table, torch.float32, stream)
         i, u = self._in(ids, U_len)
         _check(self._bwd(self._d, i, u, self._ptr(dout, "dout", self._rt, self._rows),
                          self._ptr(dtable, "dtable", torch.float32, self._table), *self._args,
                          self._stream(stream)), "rnnt_embed_bwd")
+        self._wrote(given)
         return dtable
 
 
@@ -294,16 +307,19 @@ class FrameNorm(_Op):
 
     def fwd(self, x, gamma=None, beta=None, T_len=None, y=None, stream=None):
         """y [B,T,C]; gamma, beta [C] fp32 or None; T_len [B] int32 or None (every frame)."""
+        given = y
         if y is None:
             y = self._empty(self._y, self._t, stream)
         _check(self._fwd(self._d, self._ptr(x, "x", self._t, self._x),
                          *self._params(gamma, beta, T_len), self._ptr(y, "y", self._t, self._y),
                          self._saved, *self._args, self._stream(stream)), "rnnt_norm_fwd")
+        self._wrote(given)
         return y
 
     def bwd(self, x, dy, gamma=None, beta=None, T_len=None, dx=None, dgamma=None, dbeta=None,
             stream=None):
         """(dx, dgamma, dbeta) for the x and T_len of the last fwd."""
+        given = dx, dgamma, dbeta
         if dx is None:
             dx = self._empty(self._x, self._t, stream)
         f = torch.float32
@@ -316,6 +332,7 @@ class FrameNorm(_Op):
                          self._ptr(dy, "dy", self._t, self._y), *self._params(gamma, beta, T_len),
                          self._saved, self._ptr(dx, "dx", self._t, self._x), pg, pb, *self._args,
                          self._stream(stream)), "rnnt_norm_bwd")
+        self._wrote(*given)
         return dx, dgamma, dbeta
 
 
@@ -352,16 +369,19 @@ class LayerNorm(_Op):
 
     def fwd(self, x, gamma=None, beta=None, lengths=None, y=None, stream=None):
         """y [B,T,C]; gamma, beta [C] fp32 or None; lengths [B] int32 or None (every row)."""
+        given = y
         if y is None:
             y = self._new(self._y, stream)
         _check(self._fwd(self._d, self._pointer(x, "x", self._x),
                          self._opt(gamma, "gamma", self._c), self._opt(beta, "beta", self._c),
                          self._opt(lengths, "lengths", self._len), self._pointer(y, "y", self._y),
                          self._saved, self._args[2], self._stream(stream)), "rnnt_ln_fwd")
+        self._wrote(given)
         return y
 
     def bwd(self, x, dy, gamma=None, lengths=None, dx=None, dgamma=None, dbeta=None, stream=None):
         """(dx, dgamma, dbeta) for the x and lengths of the last fwd."""
+        given = dx, dgamma, dbeta
         if dx is None:
             dx = self._new(self._x, stream)
         if dgamma is None:
@@ -374,6 +394,7 @@ class LayerNorm(_Op):
                          self._pointer(dx, "dx", self._x), self._pointer(dgamma, "dgamma", self._c),
                          self._pointer(dbeta, "dbeta", self._c), *self._args,
                          self._stream(stream)), "rnnt_ln_bwd")
+        self._wrote(*given)
         return dx, dgamma, dbeta
 
 
@@ -400,6 +421,7 @@ class Orthogonalizer(_Op):
 
     def run(self, G, out=None, stream=None):
         flat = G.dim() == 2
+        given = out
         if out is None:
             out = self._empty(self._out, self._ot, stream)
             out = out[0] if flat and self.dims.batch == 1 else out
@@ -407,6 +429,7 @@ class Orthogonalizer(_Op):
         _check(self._run(self._d, self._ptr(G[None] if flat else G, "G", self._it, self._in),
                          self._ptr(o, "out", self._ot, self._out), *self._args,
                          self._stream(stream)), "rnnt_orth")
+        self._wrote(given)
         return out
 
 
@@ -415,6 +438,10 @@ class Orthogonalizer(_Op):
 _shape_of, _dtype_of = operator.attrgetter("shape"), operator.attrgetter("dtype")
 _is_dense, _index_of = torch.Tensor.is_contiguous, torch.Tensor.get_device
 _data_of = torch.Tensor.data_ptr
+
+
+def _listed(ts):
+    return ts if type(ts) is list else list(ts)
 
 
 _PAIR = _Want(torch.float32, (2,), (1,))
@@ -460,18 +487,21 @@ class _ListOp(_Op):
     def _kind(self, name, types):
         return _Kind(name, types, self._shapes)
 
-    def _take(self, ts, kind):
-        """The data pointers of a list: an array, and its address for the C side."""
+    def _take(self, lists, kinds, layouts):
+        """The data pointers of lists (a tuple), one list after another: an array, and its address
+        for the C side.  layouts: the kinds' addresses."""
         n = self._n
-        a = array.array("Q", bytes(8 * n))
+        a = array.array("Q", bytes(8 * n * len(lists)))
         at = a.buffer_info()[0]
-        ts = ts if type(ts) is list else list(ts)
         if self._take_list is None:
-            if not self._fits(ts, kind):
-                self._refuse(ts, kind)
-            a[:] = array.array("Q", [t.data_ptr() for t in ts])
-        elif self._take_list(ts, n, kind.at, self._index, at) >= 0:
-            self._refuse(ts, kind)
+            for k, (ts, kind) in enumerate(zip(lists, kinds)):
+                if not self._fits(ts, kind):
+                    self._refuse(ts, kind)
+                a[k * n:(k + 1) * n] = array.array("Q", [t.data_ptr() for t in ts])
+        else:
+            bad = self._take_list(lists, layouts, n, self._index, at)
+            if bad >= 0:
+                self._refuse(lists[bad], kinds[bad])
         return a, at
 
     def _fits(self, ts, kind):
@@ -505,19 +535,23 @@ class GradClip(_ListOp):
         if not self.max_norm >= 0 or not 0 <= self.eps < float("inf") or not (
                 self.max_norm or self.eps):
             raise ValueError(f"max_norm {max_norm}, eps {eps}: not negative, not both 0")
-        self._into = self._grads.called("into")
+        self._kinds = self._grads, self._grads.called("into")
+        self._layouts = tuple(k.at for k in self._kinds)
         self._clip = lib.rnnt_clip
 
     def _call(self, grads, into, out, stream):
+        given = out
         if out is None:
             out = self._new(_PAIR, stream)
-        held, g = self._take(grads, self._grads)
-        w = None
-        if into is not None:
-            held_w, w = (held, g) if into is grads else self._take(into, self._into)
+        lists = [_listed(grads)]
+        if into is not None and into is not grads:
+            lists.append(_listed(into))
+        held, g = self._take(tuple(lists), self._kinds, self._layouts)
+        w = None if into is None else g + 8 * self._n * (len(lists) - 1)
         _check(self._clip(self._l, g, w, self.max_norm, self.eps,
                           self._pointer(out, "out", _PAIR), self._args[0],
                           self.ws_bytes, self._stream(stream)), "rnnt_clip")
+        self._wrote(given, None if into is None else lists[-1])
         return out
 
     def norm(self, grads, out=None, stream=None):
@@ -553,11 +587,12 @@ class AdamW(_ListOp):
         self.opts = RnntAdamwOpts(betas[0], betas[1], eps, 0.0, weight_decay if one else 0.0,
                                   self._decays)
         self._o = ctypes.byref(self.opts)
-        self._params = self._kind("params", [torch.float32] * n)
-        self._m, self._v = self._params.called("m"), self._params.called("v")
-        self._copies = self._kind("low", [torch.bfloat16] * n)
+        params = self._kind("params", [torch.float32] * n)
+        self._kinds = (params, self._grads, params.called("m"), params.called("v"),
+                       self._kind("low", [torch.bfloat16] * n))
+        self._layouts = tuple(k.at for k in self._kinds)
         new = lambda: [torch.zeros(k, device=device) for k in self._shapes]  # noqa: E731
-        self._moments = tuple(tuple(new() if k is None else k) for k in (m, v))
+        self._moments = tuple(list(new() if k is None else k) for k in (m, v))
         self._counts = torch.tensor([int(steps), 0], dtype=torch.int32, device=device)
         self._steps = self._counts.data_ptr()
         self._run = lib.rnnt_adamw
@@ -565,12 +600,12 @@ class AdamW(_ListOp):
     @property
     def m(self):
         """The first moments (to resume: copy into them)."""
-        return self._moments[0]
+        return tuple(self._moments[0])
 
     @property
     def v(self):
         """The second moments."""
-        return self._moments[1]
+        return tuple(self._moments[1])
 
     @property
     def steps(self):
@@ -588,18 +623,22 @@ class AdamW(_ListOp):
             lr = self._pointer(lr.reshape(1), "lr", _ONE)
         else:
             self.opts.lr, lr = float(lr), None
-        held_p, p = self._take(params, self._params)
-        held_g, g = self._take(grads, self._grads)
-        held_m, m = self._take(self.m, self._m)
-        held_v, v = self._take(self.v, self._v)
-        held_l, w = None, None
+        params = _listed(params)
+        lists, held_l, w = (params, _listed(grads), *self._moments), None, None
         if low is not None:
-            low = low if type(low) is list else list(low)
-            some = any(map(operator.is_, low, itertools.repeat(None)))
-            held_l, w = self._some(low) if some else self._take(low, self._copies)
+            low = _listed(low)
+            if any(map(operator.is_, low, itertools.repeat(None))):
+                held_l, w = self._some(low)
+            else:
+                lists = *lists, low
+        held, p = self._take(lists, self._kinds, self._layouts)
+        size = 8 * self._n
+        if len(lists) == 5:
+            w = p + 4 * size
         c = None if clip is None else self._pointer(clip, "clip", _PAIR)
-        _check(self._run(self._l, self._o, p, g, m, v, w, lr, c, self._steps,
-                         self._stream(stream)), "rnnt_adamw")
+        _check(self._run(self._l, self._o, p, p + size, p + 2 * size, p + 3 * size, w, lr, c,
+                         self._steps, self._stream(stream)), "rnnt_adamw")
+        self._wrote(params, *self._moments, low)
 
     def _some(self, low):
         """The pointers of copies that only some tensors have."""

@@ -84,3 +84,24 @@ def test_an_unlimited_norm(n):
     assert c.norm([g]).tolist() == [float("inf"), 0.0]
     g[3] = float("nan")
     assert torch.isnan(c.norm([g])).all()
+
+
+@pytest.mark.parametrize("helper", [True, False])
+def test_a_graph_that_holds_old_values_is_refused(helper):
+    w, g = torch.ones(40, 3, device="cuda"), torch.ones(40, 3, device="cuda")
+    low, x = w.bfloat16(), torch.ones(40, 3, device="cuda", requires_grad=True)
+    c, o = rn.GradClip([(40, 3)], max_norm=2.0), rn.AdamW([(40, 3)])
+    if not helper:
+        c._fast = o._fast = None
+    for held, call in ((w, lambda: o.step([w], [g], 0.1)),
+                       (low, lambda: o.step([w], [g], 0.1, low=[low])),
+                       (g, lambda: c.clip([g]))):
+        loss = (x * held).sum()
+        call()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    with torch.inference_mode():  # (has no count)
+        p = torch.ones(40, 3, device="cuda")
+    o.step([p], [g], 0.1)
+    (x * g).sum().backward()  # what is only read stays
+    assert torch.equal(x.grad, g)
