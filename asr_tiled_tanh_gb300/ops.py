@@ -138,6 +138,11 @@ class _Want:
         self.at = self._words.buffer_info()[0]
 
 
+def _signed(t):
+    """Whether the tensor's memory has the other sign (a view that torch negates at its use)."""
+    return isinstance(t, torch.Tensor) and t.is_neg()
+
+
 def _dense(shape):
     """Strides of a dense tensor."""
     return torch.empty(shape, device="meta").stride()
@@ -174,9 +179,11 @@ class _Op:
     def _ptr(self, t, name, dtype, layout):
         """Data pointer of a tensor of the plan's GPU that has exactly this type and layout."""
         shape, strides = layout
-        if t.dtype is not dtype or t.shape != shape or t.get_device() != self._index:
+        if (t.dtype is not dtype or t.shape != shape or t.get_device() != self._index
+                or _signed(t)):
             raise ValueError(f"{name}: a tensor of {dtype} {tuple(shape)} on {self.ws.device} is "
-                             f"needed, got {t.dtype} {tuple(t.shape)} on {t.device}")
+                             f"needed, got {t.dtype} {tuple(t.shape)} on {t.device}"
+                             + " with its sign left to do" * _signed(t))
         if t.stride() != strides:
             # (the stride of a dimension of length 1 is never used)
             if any(n > 1 and a != b for n, a, b in zip(shape, t.stride(), strides)):
@@ -507,7 +514,7 @@ class _ListOp(_Op):
     def _fits(self, ts, kind):
         return len(ts) == self._n and all(
             t.shape == k and t.dtype is d and t.get_device() == self._index and t.is_contiguous()
-            for t, k, d in zip(ts, self._shapes, kind.types))
+            and not _signed(t) for t, k, d in zip(ts, self._shapes, kind.types))
 
     def _refuse(self, ts, kind):
         if len(ts) != self._n:
@@ -518,7 +525,7 @@ class _ListOp(_Op):
                 raise ValueError(f"{kind.name}[{i}]: a dense tensor of {d} {tuple(k)} on "
                                  f"{self.ws.device} is needed, got {t.dtype} {tuple(t.shape)} of "
                                  f"strides {t.stride()} on {t.device}")
-        raise ValueError(f"{kind.name}: dense CUDA tensors are needed")
+        raise ValueError(f"{kind.name}: dense CUDA tensors of resolved sign are needed")
 
 
 class GradClip(_ListOp):

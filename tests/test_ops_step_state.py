@@ -122,3 +122,19 @@ def test_a_graph_that_holds_old_weights_is_refused(monkeypatch):
     o.step([w], [torch.ones(3)], 0.1)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.backward()
+
+
+def test_views_with_the_sign_left_to_do_are_refused(monkeypatch):
+    # (the imaginary part of a conjugate is such a view: its memory has the other sign)
+    c = _on_the_cpu(monkeypatch, rn.GradClip([(1,)], device="cpu"), "_clip")
+    n = _on_the_cpu(monkeypatch, rn.LayerNorm(1, 1, 3, dtype="f32", device="cpu"), "_fwd")
+    e = _on_the_cpu(monkeypatch, rn.LabelEmbedding(1, 2, 5, 3, "f32", "f32", device="cpu"), "_fwd")
+    neg = torch.ones(1, dtype=torch.complex64).conj().imag
+    assert neg.is_neg() and neg.is_contiguous()
+    with pytest.raises(ValueError):
+        c.norm([neg])
+    with pytest.raises(ValueError):
+        n.fwd(torch._neg_view(torch.ones(1, 1, 3)))
+    with pytest.raises(ValueError):
+        e.fwd(torch._neg_view(torch.ones(5, 3)), torch.zeros(1, 2, dtype=torch.int32))
+    c.norm([neg.resolve_neg()])
