@@ -440,13 +440,6 @@ class Orthogonalizer(_Op):
         return out
 
 
-# (a list of hundreds of tensors is checked and taken apart for every call: by maps of these,
-# 0.35 us a tensor)
-_shape_of, _dtype_of = operator.attrgetter("shape"), operator.attrgetter("dtype")
-_is_dense, _index_of = torch.Tensor.is_contiguous, torch.Tensor.get_device
-_data_of = torch.Tensor.data_ptr
-
-
 def _listed(ts):
     return ts if type(ts) is list else list(ts)
 
