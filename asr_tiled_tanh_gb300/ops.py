@@ -151,11 +151,12 @@ def _dense(shape):
 class _Op:
     """Status word and workspace of one problem size."""
 
-    def __init__(self, ws_bytes, what, device):
+    def __init__(self, ws_bytes, what, device, works=True):
+        # (0 bytes: invalid; works: whether a call takes the workspace)
         if ws_bytes == 0:
             raise RnntError(1, what)
         self.device = device
-        self.ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+        self.ws = torch.empty(ws_bytes * works, dtype=torch.uint8, device=device)
         self.ws_bytes = ws_bytes
         self.status_word = torch.zeros(1, dtype=torch.int32, device=device)
         self._args = (self.ws.data_ptr(), ws_bytes, self.status_word.data_ptr())
@@ -469,7 +470,7 @@ class _Kind:
 class _ListOp(_Op):
     """An operator on a list of dense tensors of fixed shapes."""
 
-    def __init__(self, shapes, dtype, ws_bytes, what, device):
+    def __init__(self, shapes, dtype, what, device, works=True):
         self._shapes = [torch.Size(k) for k in shapes]
         self._n = n = len(self._shapes)
         names = [dtype] * n if isinstance(dtype, str) else list(dtype)
@@ -482,7 +483,7 @@ class _ListOp(_Op):
         self._l = ctypes.byref(self.list)
         self._grads = self._kind("grads", [t for _, t in codes])
         self._take_list = _helper() and _helper().take
-        super().__init__(ws_bytes(self._l), what, device)
+        super().__init__(load().rnnt_clip_workspace_bytes(self._l), what, device, works)
 
     def _kind(self, name, types):
         return _Kind(name, types, self._shapes)
@@ -529,15 +530,14 @@ class GradClip(_ListOp):
     """
 
     def __init__(self, shapes, max_norm=1.0, dtype="f32", eps=1e-6, device="cuda"):
-        lib = load()
-        super().__init__(shapes, dtype, lib.rnnt_clip_workspace_bytes, "GradClip(shapes)", device)
+        super().__init__(shapes, dtype, "GradClip(shapes)", device)
         self.max_norm, self.eps = float(max_norm), float(eps)
         if not self.max_norm >= 0 or not 0 <= self.eps < float("inf") or not (
                 self.max_norm or self.eps):
             raise ValueError(f"max_norm {max_norm}, eps {eps}: not negative, not both 0")
         self._kinds = self._grads, self._grads.called("into")
         self._layouts = tuple(k.at for k in self._kinds)
-        self._clip = lib.rnnt_clip
+        self._clip = load().rnnt_clip
 
     def _call(self, grads, into, out, stream):
         given = out
@@ -573,8 +573,7 @@ class AdamW(_ListOp):
 
     def __init__(self, shapes, grad_dtype="f32", betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
                  m=None, v=None, steps=0, device="cuda"):
-        lib = load()
-        super().__init__(shapes, grad_dtype, lib.rnnt_clip_workspace_bytes, "AdamW(shapes)", device)
+        super().__init__(shapes, grad_dtype, "AdamW(shapes)", device, works=False)
         n = len(self._shapes)
         if not (0 <= betas[0] < 1 and 0 <= betas[1] < 1 and 0 <= eps < float("inf")):
             raise ValueError(f"betas {betas}, eps {eps}: out of range")
@@ -595,7 +594,7 @@ class AdamW(_ListOp):
         self._moments = tuple(list(new() if k is None else k) for k in (m, v))
         self._counts = torch.tensor([int(steps), 0], dtype=torch.int32, device=device)
         self._steps = self._counts.data_ptr()
-        self._run = lib.rnnt_adamw
+        self._run = load().rnnt_adamw
 
     @property
     def m(self):

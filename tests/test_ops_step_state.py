@@ -138,3 +138,10 @@ def test_views_with_the_sign_left_to_do_are_refused(monkeypatch):
     with pytest.raises(ValueError):
         e.fwd(torch._neg_view(torch.ones(5, 3)), torch.zeros(1, 2, dtype=torch.int32))
     c.norm([neg.resolve_neg()])
+
+
+def test_a_plan_of_updates_has_no_workspace():
+    assert rn.AdamW([(300, 7)], device="cpu").ws.numel() == 0
+    assert rn.GradClip([(300, 7)], device="cpu").ws.numel() > 0
+    with pytest.raises(rn.RnntError):
+        rn.AdamW([((1 << 36) + 1,)], m=[torch.empty(0)], v=[torch.empty(0)], device="cpu")
