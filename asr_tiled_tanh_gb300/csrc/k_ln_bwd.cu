@@ -259,25 +259,47 @@ k_ln_cols(LnArgs a, const TX* __restrict__ x, const TY* __restrict__ dy,
 }
 
 // dgamma, dbeta: the column sums of part [n][C], 8 channels a block, its 32 groups
-// of threads a row each at a time.
-constexpr int PT = 256, PCOLS = 8, PGROUPS = PT / PCOLS;
+// of threads 8 rows each at a time.  The sums meet in trees: at most 11 roundings on a
+// row's way, up to 50 one after another (7 x 333 x 360 with the sums 6.4 us, was 6.9).
+constexpr int PT = 256, PCOLS = 8, PGROUPS = PT / PCOLS, PROWS = 8;
+template <int N>
+__device__ __forceinline__ float2 tree(float2 (&v)[N]) {
+#pragma unroll
+  for (int h = N / 2; h; h >>= 1)
+#pragma unroll
+    for (int k = 0; k < h; ++k) v[k] = __fadd2_rn(v[k], v[k + h]);
+  return v[0];
+}
 __global__ void __launch_bounds__(PT)
 k_ln_params(const float2* __restrict__ part, int n, int C, float* __restrict__ dgamma,
             float* __restrict__ dbeta) {
-  __shared__ float2 scr[PGROUPS][PCOLS];
+  constexpr int WARPS = PT / 32;
+  __shared__ float2 scr[WARPS][PCOLS];
   const int col = threadIdx.x % PCOLS, group = threadIdx.x / PCOLS;
   const int c = blockIdx.x * PCOLS + col;
   ptx::griddep_wait();
-  float2 s = make_float2(0.f, 0.f);
+  float2 s = make_float2(0.f, 0.f), v[PROWS];
   if (c < C)
-#pragma unroll 8
-    for (int r = group; r < n; r += PGROUPS)
-      s = __fadd2_rn(s, __ldcg(part + (long long)r * C + c));
-  scr[group][col] = s;
+    for (int r0 = group; r0 < n; r0 += PROWS * PGROUPS) {
+#pragma unroll
+      for (int k = 0; k < PROWS; ++k) {
+        const int r = r0 + k * PGROUPS;
+        v[k] = r < n ? __ldcg(part + (long long)r * C + c) : make_float2(0.f, 0.f);
+      }
+      s = __fadd2_rn(s, tree(v));
+    }
+#pragma unroll
+  for (int d = PCOLS; d < 32; d <<= 1) {
+    s.x += __shfl_xor_sync(0xffffffffu, s.x, d);
+    s.y += __shfl_xor_sync(0xffffffffu, s.y, d);
+  }
+  if ((threadIdx.x & 31) < PCOLS) scr[threadIdx.x >> 5][col] = s;
   __syncthreads();
   if (group || c >= C) return;
+  float2 w[WARPS];
 #pragma unroll
-  for (int k = 1; k < PGROUPS; ++k) s = __fadd2_rn(s, scr[k][col]);
+  for (int k = 0; k < WARPS; ++k) w[k] = scr[k][col];
+  s = tree(w);
   if (dgamma) dgamma[c] = s.x;
   if (dbeta) dbeta[c] = s.y;
 }

@@ -112,3 +112,22 @@ def test_rows_of_one_bf16_value(C):
     assert torch.equal(n.fwd(x, None, beta), beta.expand(2, T, C))
     assert not n.bwd(x, torch.ones(2, T, C, device="cuda"))[1].any()
     assert torch.isnan(rn.LayerNorm(2, T, C, out_dtype="f32", eps=0.0).fwd(x)).all()
+
+
+@pytest.mark.parametrize("C", [24, 333, 512, 2048, 9000])
+def test_infinities_in_parameter_gradients(C):
+    x, dy, gamma, _ = _inputs(2, 40, C, "f32")
+    n = rn.LayerNorm(2, 40, C, dtype="f32")
+    n.fwd(x, gamma)
+    ref = n.bwd(x, dy, gamma)
+    xh = (x.double() - x.double().mean(2, keepdim=True))[1, 7]
+    bad = dy.clone()
+    bad[1, 7, 3], bad[1, 7, 5] = float("inf"), -float("inf")
+    bad[0, 2, 9], bad[1, 7, 9] = float("inf"), -float("inf")
+    _, dg, db = n.bwd(x, bad, gamma)
+    inf = float("inf")
+    assert float(db[3]) == inf and float(db[5]) == -inf and torch.isnan(db[9])
+    assert float(dg[3]) == inf * float(xh[3].sign()) and float(dg[5]) == -inf * float(xh[5].sign())
+    other = torch.ones(C, dtype=torch.bool, device="cuda")
+    other[[3, 5, 9]] = False
+    assert torch.equal(db[other], ref[2][other]) and torch.equal(dg[other], ref[1][other])
