@@ -62,11 +62,20 @@ at::ScalarType type_of(int64_t code) {
   return code == 0 ? at::kFloat : code == 1 ? at::kBFloat16 : at::kInt;
 }
 
-// pointer(tensor, layout, device): its data pointer, or None where it is not a CUDA tensor
-// as the layout says (strides of dimensions of one element do not count).
+// Tells autograd that a kernel writes this tensor (None and tensors made under inference
+// mode, which have no count: nothing).
+void count_write(PyObject* o) {
+  if (!THPVariable_Check(o)) return;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
+// pointer(tensor, layout, device, written): its data pointer, or None where it is not a CUDA
+// tensor as the layout says (strides of dimensions of one element do not count); a tensor
+// that will be written is counted.
 PyObject* pointer(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
-  if (nargs != 3) {
-    PyErr_SetString(PyExc_TypeError, "pointer(tensor, layout, device)");
+  if (nargs != 4) {
+    PyErr_SetString(PyExc_TypeError, "pointer(tensor, layout, device, written)");
     return nullptr;
   }
   if (!THPVariable_Check(args[0])) Py_RETURN_NONE;
@@ -81,6 +90,7 @@ PyObject* pointer(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   for (int64_t d = 0; d < dims; ++d)
     if (t.size(d) != want[2 + d] || (t.size(d) > 1 && t.stride(d) != want[2 + dims + d]))
       Py_RETURN_NONE;
+  if (args[3] == Py_True) count_write(args[0]);
   return PyLong_FromVoidPtr(t.data_ptr());
 }
 
@@ -99,13 +109,7 @@ PyObject* empty(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
       at::TensorOptions().dtype(type_of(want[0])).device(at::kCUDA, (at::DeviceIndex)device)));
 }
 
-// wrote(...): tells autograd of tensors, or lists of them, that a kernel has written (None
-// and tensors made under inference mode, which have no count: nothing).
-void count_write(PyObject* o) {
-  if (!THPVariable_Check(o)) return;
-  const at::Tensor& t = THPVariable_Unpack(o);
-  if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
-}
+// wrote(...): counts these tensors, or lists of them.
 PyObject* wrote(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   for (Py_ssize_t k = 0; k < nargs; ++k) {
     if (!PyList_Check(args[k])) {

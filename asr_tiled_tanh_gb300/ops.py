@@ -163,13 +163,16 @@ class _Op:
         self._index = self.ws.device.index
         self._fast = _helper() if self.ws.is_cuda else None
 
-    def _pointer(self, t, name, want):
-        """_ptr of what is wanted (0.1 us where it is that, 0.5 by _ptr)."""
+    def _pointer(self, t, name, want, written=False):
+        """_ptr of what is wanted (0.1 us where it is that, 0.5 by _ptr); counts what is written."""
         if self._fast is not None:
-            p = self._fast.pointer(t, want.at, self._index)
+            p = self._fast.pointer(t, want.at, self._index, written)
             if p is not None:
                 return p
-        return self._ptr(t, name, want.dtype, want.layout)
+        p = self._ptr(t, name, want.dtype, want.layout)
+        if written:
+            self._wrote(t)
+        return p
 
     def _new(self, want, stream):
         """_empty of what is wanted."""
@@ -377,19 +380,17 @@ class LayerNorm(_Op):
 
     def fwd(self, x, gamma=None, beta=None, lengths=None, y=None, stream=None):
         """y [B,T,C]; gamma, beta [C] fp32 or None; lengths [B] int32 or None (every row)."""
-        given = y
         if y is None:
             y = self._new(self._y, stream)
         _check(self._fwd(self._d, self._pointer(x, "x", self._x),
                          self._opt(gamma, "gamma", self._c), self._opt(beta, "beta", self._c),
-                         self._opt(lengths, "lengths", self._len), self._pointer(y, "y", self._y),
-                         self._saved, self._args[2], self._stream(stream)), "rnnt_ln_fwd")
-        self._wrote(given)
+                         self._opt(lengths, "lengths", self._len),
+                         self._pointer(y, "y", self._y, True), self._saved, self._args[2],
+                         self._stream(stream)), "rnnt_ln_fwd")
         return y
 
     def bwd(self, x, dy, gamma=None, lengths=None, dx=None, dgamma=None, dbeta=None, stream=None):
         """(dx, dgamma, dbeta) for the x and lengths of the last fwd."""
-        given = dx, dgamma, dbeta
         if dx is None:
             dx = self._new(self._x, stream)
         if dgamma is None:
@@ -399,10 +400,10 @@ class LayerNorm(_Op):
         _check(self._bwd(self._d, self._pointer(x, "x", self._x), self._pointer(dy, "dy", self._y),
                          self._opt(gamma, "gamma", self._c),
                          self._opt(lengths, "lengths", self._len), self._saved,
-                         self._pointer(dx, "dx", self._x), self._pointer(dgamma, "dgamma", self._c),
-                         self._pointer(dbeta, "dbeta", self._c), *self._args,
+                         self._pointer(dx, "dx", self._x, True),
+                         self._pointer(dgamma, "dgamma", self._c, True),
+                         self._pointer(dbeta, "dbeta", self._c, True), *self._args,
                          self._stream(stream)), "rnnt_ln_bwd")
-        self._wrote(*given)
         return dx, dgamma, dbeta
 
 
@@ -540,7 +541,6 @@ class GradClip(_ListOp):
         self._clip = load().rnnt_clip
 
     def _call(self, grads, into, out, stream):
-        given = out
         if out is None:
             out = self._new(_PAIR, stream)
         lists = [_listed(grads)]
@@ -549,9 +549,10 @@ class GradClip(_ListOp):
         held, g = self._take(tuple(lists), self._kinds, self._layouts)
         w = None if into is None else g + 8 * self._n * (len(lists) - 1)
         _check(self._clip(self._l, g, w, self.max_norm, self.eps,
-                          self._pointer(out, "out", _PAIR), self._args[0],
+                          self._pointer(out, "out", _PAIR, True), self._args[0],
                           self.ws_bytes, self._stream(stream)), "rnnt_clip")
-        self._wrote(given, None if into is None else lists[-1])
+        if into is not None:
+            self._wrote(lists[-1])
         return out
 
     def norm(self, grads, out=None, stream=None):
