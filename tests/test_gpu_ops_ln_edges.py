@@ -131,3 +131,15 @@ def test_infinities_in_parameter_gradients(C):
     other = torch.ones(C, dtype=torch.bool, device="cuda")
     other[[3, 5, 9]] = False
     assert torch.equal(db[other], ref[2][other]) and torch.equal(dg[other], ref[1][other])
+
+
+@pytest.mark.parametrize("C", [1 << 20, (1 << 20) - 1])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_of_one_value_of_the_greatest_width(C, dtype):
+    # (bf16: with C past 2^16 a sum of equal values is rounded too)
+    values = [0.1, -1e4 / 3, 1.0 + 2.0 ** -7, 123.456]
+    x = torch.tensor(values, device="cuda").to(DT[dtype])[None, :, None].expand(1, 4, C)
+    beta = torch.randn(C, device="cuda")
+    n = rn.LayerNorm(1, 4, C, dtype=dtype, out_dtype="f32")
+    assert torch.equal(n.fwd(x.contiguous(), None, beta), beta.expand(1, 4, C))
+    assert not n.bwd(x.contiguous(), torch.ones(1, 4, C, device="cuda"))[1].any()
